@@ -278,7 +278,9 @@ def work(case):
     if case["op"].startswith("xent"):
         n, v, d = case["n"], case["v"], case["d"]
         train = case["op"] == "xent_train"
-        return dict(bytes=(2 if train else 1) * 2.0 * d * (n + v) + 12.0 * n, flops=(6.0 if train else 2.0) * n * v * d)
+        rows = n * (1.0 - case["ignored"])  # the rows that count
+        return dict(bytes=2.0 * d * (rows + v + (n + v if train else 0)) + 12.0 * n,
+                    flops=(6.0 if train else 2.0) * rows * v * d)
     tokens, heads, dim = case["batch"] * case["seq"], case["hq"] + case["hk"], case["dim"]
     size = 2 if case["dtype"] == BF16 else 4
     x = float(tokens) * heads * dim
