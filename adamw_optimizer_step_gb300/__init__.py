@@ -14,5 +14,9 @@ from ._binding import (  # noqa: F401
     gbo_muon_plan_info, gbo_muon_plan_phase_times, gbo_muon_plan_set_event, gbo_muon_plan_set_free_sms,
     gbo_muon_plan_set_stats, gbo_muon_plan_set_timing,
     gbo_muon_step,
-    gbo_muon_workspace_bytes, gbo_normuon_rownorm, gbo_struct_size, lib, library_path,
+    gbo_muon_workspace_bytes, gbo_normuon_rownorm,
+    gbo_rope_backward, gbo_rope_forward, gbo_rope_frequencies, gbo_rope_workspace_bytes,
+    gbo_struct_size,
+    gbo_xent_backward, gbo_xent_forward, gbo_xent_grad, gbo_xent_workspace_bytes,
+    lib, library_path,
 )

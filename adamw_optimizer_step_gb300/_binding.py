@@ -23,6 +23,17 @@ GBO_ROUTE_X = 1
 GBO_ROUTE_GRAM = 2
 GBO_STATUS_NONFINITE = 1
 GBO_STATUS_TIMEOUT = 2
+GBO_STATUS_BAD_LABEL = 4
+GBO_I32 = 16
+GBO_I64 = 17
+GBO_ROPE_HALF = 0
+GBO_ROPE_INTERLEAVED = 1
+GBO_ROPE_SCALE_NONE = 0
+GBO_ROPE_SCALE_LINEAR = 1
+GBO_ROPE_SCALE_NTK = 2
+GBO_ROPE_SCALE_YARN = 3
+GBO_ROPE_SCALE_WAVELENGTH = 4
+GBO_ROPE_MAX_TENSORS = 4
 GBO_MAX_VIEW_DIMS = 6
 GBO_N_PHASES = 6
 PHASE_NAMES = ("momentum", "gram", "product", "square", "rows", "final")
@@ -74,7 +85,41 @@ class PlanInfo(ctypes.Structure):
                 ("n_gram_route", c_int64), ("n_mom_fused", c_int64)]
 
 
-_STRUCTS = (MuonDesc, MuonOpts, Tensor, AdamWDesc, AdamWOpts, PlanInfo)
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", c_int32), ("reserved", c_int32), ("factor", ctypes.c_double),
+                ("trained", ctypes.c_double), ("fast", ctypes.c_double), ("slow", ctypes.c_double)]
+
+
+class RopeOpts(ctypes.Structure):
+    _fields_ = [("head_dim", c_int32), ("rot_dim", c_int32), ("offset", c_int32), ("layout", c_int32),
+                ("freq", ctypes.POINTER(ctypes.c_double)), ("magnitude", c_float), ("eps", c_float)]
+
+
+class RopeTensor(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("dy", c_void_p), ("y", c_void_p), ("gain", c_void_p), ("dgain", c_void_p),
+                ("x_stride", c_int64 * 3), ("dy_stride", c_int64 * 3), ("y_stride", c_int64 * 3),
+                ("heads", c_int32), ("dtype", c_int32), ("norm", c_int32), ("reserved", c_int32)]
+
+
+class RopePositions(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("stride_b", c_int64), ("stride_s", c_int64), ("start", c_int64),
+                ("dtype", c_int32), ("reserved", c_int32)]
+
+
+class XentArgs(ctypes.Structure):
+    _fields_ = [("h", c_void_p), ("w", c_void_p), ("labels", c_void_p), ("row_weight", c_void_p),
+                ("upstream", c_void_p), ("n", c_int64), ("v", c_int64), ("d", c_int64), ("h_stride", c_int64),
+                ("w_stride", c_int64), ("logit_scale", c_float), ("z_loss", c_float), ("label_dtype", c_int32),
+                ("mean", c_int32)]
+
+
+class XentGrads(ctypes.Structure):
+    _fields_ = [("dh", c_void_p), ("dw", c_void_p), ("dh_stride", c_int64), ("dw_stride", c_int64),
+                ("dh_dtype", c_int32), ("dw_dtype", c_int32), ("accumulate_dw", c_int32), ("reserved", c_int32)]
+
+
+_STRUCTS = (MuonDesc, MuonOpts, Tensor, AdamWDesc, AdamWOpts, PlanInfo, RopeScaling, RopeOpts, RopeTensor,
+            RopePositions, XentArgs, XentGrads)
 _lib = None
 
 
@@ -109,6 +154,20 @@ def lib():
                                             c_void_p, c_void_p]),
         "gbo_adamw_step": (c_int32, [ctypes.POINTER(AdamWDesc), c_int32, ctypes.POINTER(AdamWOpts), c_void_p,
                                      c_void_p, c_void_p]),
+        "gbo_rope_frequencies": (c_int32, [c_int32, ctypes.c_double, ctypes.POINTER(RopeScaling),
+                                           ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
+        "gbo_rope_workspace_bytes": (c_size_t, [ctypes.POINTER(RopeTensor), c_int32, ctypes.POINTER(RopeOpts)]),
+        "gbo_rope_forward": (c_int32, [ctypes.POINTER(RopeTensor), c_int32, ctypes.POINTER(RopeOpts), c_int64,
+                                       c_int64, ctypes.POINTER(RopePositions), c_void_p]),
+        "gbo_rope_backward": (c_int32, [ctypes.POINTER(RopeTensor), c_int32, ctypes.POINTER(RopeOpts), c_int64,
+                                        c_int64, ctypes.POINTER(RopePositions), c_void_p, c_size_t, c_void_p]),
+        "gbo_xent_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int64]),
+        "gbo_xent_forward": (c_int32, [ctypes.POINTER(XentArgs), c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                       c_void_p, c_void_p]),
+        "gbo_xent_backward": (c_int32, [ctypes.POINTER(XentArgs), c_void_p, ctypes.POINTER(XentGrads), c_void_p,
+                                        c_size_t, c_void_p, c_void_p]),
+        "gbo_xent_grad": (c_int32, [ctypes.POINTER(XentArgs), c_void_p, c_void_p, c_void_p, ctypes.POINTER(XentGrads),
+                                    c_void_p, c_size_t, c_void_p, c_void_p]),
         "gbo_testing_wait_timeout": (c_int32, [c_void_p, ctypes.c_uint32, c_void_p]),
         "gbo_testing_set_small_chain": (c_int32, [c_int32]),
         "gbo_testing_set_fused_gram": (c_int32, [c_int32]),
@@ -418,6 +477,195 @@ def gbo_adamw_step(params, *, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=
     opts = AdamWOpts(lr, beta1, beta2, eps, weight_decay, int(step), _dev_ptr(dev_step, "dev_step"))
     _check(lib().gbo_adamw_step(arr, len(params), ctypes.byref(opts), _dev_ptr(coef, "coef"),
                                 _dev_ptr(dev_status, "dev_status"), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# rotary positions and q/k norms, cross entropy of the tied classifier
+
+def gbo_rope_frequencies(rot_dim, base=10000.0, scaling=None):
+    """(frequencies, magnitude) of a rotation; ``scaling``: a RopeScaling or None."""
+    freq = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    magnitude = ctypes.c_double()
+    _check(lib().gbo_rope_frequencies(int(rot_dim), float(base), ctypes.byref(scaling) if scaling else None, freq,
+                                      ctypes.byref(magnitude)))
+    return freq, magnitude.value
+
+
+def _heads_of(t, what):
+    """Checks a (batch, seq, heads, dim) tensor whose head elements are consecutive."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if t.dim() != 4:
+        raise ValueError("%s must be (batch, seq, heads, dim)" % what)
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError("the elements of a head of %s must be consecutive" % what)
+    return t
+
+
+def _rope_table(tensors, opts, positions):
+    """Marshal a list of dicts with ``x``, ``y`` (and ``dy``, ``gain``, ``dgain``,
+    ``norm``) into a table; returns it with the batch and the length."""
+    arr = (RopeTensor * max(1, len(tensors)))()
+    batch = seq = None
+    for d, e in zip(arr, tensors):
+        shape = None
+        for name, ptr, stride in (("x", "x", d.x_stride), ("dy", "dy", d.dy_stride), ("y", "y", d.y_stride)):
+            t = e.get(name)
+            if t is None:
+                continue
+            _heads_of(t, name)
+            if shape is None:
+                shape, dtype = t.shape, t.dtype
+            elif t.shape != shape or t.dtype != dtype:
+                raise ValueError("x, dy and y differ in shape or dtype")
+            setattr(d, ptr, t.data_ptr())
+            stride[0], stride[1], stride[2] = t.stride()[:3]
+        if shape is None or shape[3] != opts.head_dim:
+            raise ValueError("a head has %d elements, the tensor %s" % (opts.head_dim, shape))
+        if batch is None:
+            batch, seq = shape[0], shape[1]
+        elif (batch, seq) != (shape[0], shape[1]):
+            raise ValueError("the tensors of one call have the same batch and length")
+        d.heads = shape[2]
+        d.dtype = _dtype(e["y"])
+        d.norm = int(bool(e.get("norm", False)))
+        for name in ("gain", "dgain"):
+            t = e.get(name)
+            if t is not None:
+                if t.dtype != torch.float32 or t.numel() != opts.head_dim:
+                    raise ValueError("%s must be %d float32 values" % (name, opts.head_dim))
+                setattr(d, name, _dev_ptr(t, name))
+    pos = RopePositions()
+    if isinstance(positions, int):
+        pos.start = positions
+    else:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError("positions must be int32 or int64")
+        if not positions.is_cuda:
+            raise ValueError("positions must be a CUDA tensor")
+        p = positions if positions.dim() == 2 else positions.unsqueeze(0)
+        if p.dim() != 2 or p.shape[1] != seq or p.shape[0] not in (1, batch):
+            raise ValueError("positions must be (seq,), (1, seq) or (batch, seq)")
+        pos.ptr = p.data_ptr()
+        pos.stride_b = p.stride(0) if p.shape[0] == batch else 0
+        pos.stride_s = p.stride(1)
+        pos.dtype = GBO_I64 if p.dtype == torch.int64 else GBO_I32
+    return arr, batch or 0, seq or 0, pos
+
+
+def gbo_rope_forward(tensors, opts, positions, stream=None):
+    """Rotate tensors (dicts with ``x``, ``y`` of (batch, seq, heads, dim), and
+    ``norm``, ``gain``) in one launch.  ``positions``: an integer tensor (seq,)
+    or (batch, seq), or the first position."""
+    arr, batch, seq, pos = _rope_table(tensors, opts, positions)
+    _check(lib().gbo_rope_forward(arr, len(tensors), ctypes.byref(opts), batch, seq, ctypes.byref(pos),
+                                  _stream(stream)))
+
+
+def gbo_rope_workspace_bytes(tensors, opts):
+    arr = (RopeTensor * max(1, len(tensors)))()
+    for d, e in zip(arr, tensors):
+        d.heads = e["dy"].shape[2]
+        d.dgain = None if e.get("dgain") is None else 4
+    return int(lib().gbo_rope_workspace_bytes(arr, len(tensors), ctypes.byref(opts)))
+
+
+def gbo_rope_backward(tensors, opts, positions, workspace=None, stream=None):
+    """Gradients: dicts with ``dy``, ``y`` (receives the input's gradient) and,
+    with a norm, ``x``, ``gain`` and ``dgain``."""
+    arr, batch, seq, pos = _rope_table(tensors, opts, positions)
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().gbo_rope_backward(arr, len(tensors), ctypes.byref(opts), batch, seq, ctypes.byref(pos),
+                                   _dev_ptr(workspace, "workspace"), nbytes, _stream(stream)))
+
+
+def gbo_xent_workspace_bytes(n, v, d, grad=False, cap=0):
+    return int(lib().gbo_xent_workspace_bytes(int(n), int(v), int(d), int(bool(grad)), int(cap)))
+
+
+def _rows_of(t, what):
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be two-dimensional with consecutive row elements" % what)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    return t
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean):
+    _rows_of(h, "h"), _rows_of(w, "w")
+    if h.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise TypeError("h and w must be bfloat16")
+    if h.shape[1] != w.shape[1]:
+        raise ValueError("h and w differ in width")
+    if labels.dtype not in (torch.int32, torch.int64):
+        raise TypeError("labels must be int32 or int64")
+    n = h.shape[0]
+    if labels.numel() != n:
+        raise ValueError("one label per row of h")
+    for t, count, what in ((row_weight, n, "row_weight"), (upstream, 1, "upstream")):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != count):
+            raise ValueError("%s must be %d float32 values" % (what, count))
+    return XentArgs(h.data_ptr(), w.data_ptr(), _dev_ptr(labels, "labels"), _dev_ptr(row_weight, "row_weight"),
+                    _dev_ptr(upstream, "upstream"), n, w.shape[0], h.shape[1], _row_stride(h), _row_stride(w),
+                    float(logit_scale), float(z_loss), GBO_I64 if labels.dtype == torch.int64 else GBO_I32,
+                    int(bool(mean)))
+
+
+def _xent_grads(dh, dw, h, w, accumulate_dw):
+    g = XentGrads()
+    if dh is not None:
+        if _rows_of(dh, "dh").shape != h.shape:
+            raise ValueError("dh must have the shape of h")
+        g.dh, g.dh_stride, g.dh_dtype = dh.data_ptr(), _row_stride(dh), _dtype(dh)
+    if dw is not None:
+        if _rows_of(dw, "dw").shape != w.shape:
+            raise ValueError("dw must have the shape of w")
+        g.dw, g.dw_stride, g.dw_dtype = dw.data_ptr(), _row_stride(dw), _dtype(dw)
+    g.accumulate_dw = int(bool(accumulate_dw))
+    return g
+
+
+def _out_f32(t, count, what):
+    if t is not None and (t.dtype != torch.float32 or t.numel() != count):
+        raise ValueError("%s must be %d float32 values" % (what, count))
+    return _dev_ptr(t, what)
+
+
+def gbo_xent_forward(h, w, labels, workspace, *, loss=None, lse=None, totals=None, row_weight=None, logit_scale=1.0,
+                     z_loss=0.0, dev_status=None, stream=None):
+    """Cross entropy of each row of ``h`` @ ``w``.T against ``labels`` into ``loss``,
+    ``lse`` (n) and ``totals`` (2), whichever are given."""
+    a = _xent_args(h, w, labels, row_weight, None, logit_scale, z_loss, True)
+    _check(lib().gbo_xent_forward(ctypes.byref(a), _out_f32(loss, a.n, "loss"), _out_f32(lse, a.n, "lse"),
+                                  _out_f32(totals, 2, "totals"), _dev_ptr(workspace, "workspace"),
+                                  workspace.numel() * workspace.element_size(), _dev_ptr(dev_status, "dev_status"),
+                                  _stream(stream)))
+
+
+def gbo_xent_backward(h, w, labels, lse, workspace, *, dh=None, dw=None, accumulate_dw=False, row_weight=None,
+                      upstream=None, mean=True, logit_scale=1.0, z_loss=0.0, dev_status=None, stream=None):
+    """Gradients into ``dh`` and ``dw`` from the forward's ``lse``."""
+    a = _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean)
+    g = _xent_grads(dh, dw, h, w, accumulate_dw)
+    _check(lib().gbo_xent_backward(ctypes.byref(a), _out_f32(lse, a.n, "lse"), ctypes.byref(g),
+                                   _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                   _dev_ptr(dev_status, "dev_status"), _stream(stream)))
+
+
+def gbo_xent_grad(h, w, labels, workspace, *, loss=None, lse=None, totals=None, dh=None, dw=None,
+                  accumulate_dw=False, row_weight=None, upstream=None, mean=True, logit_scale=1.0, z_loss=0.0,
+                  dev_status=None, stream=None):
+    """Losses and gradients in one call."""
+    a = _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean)
+    g = _xent_grads(dh, dw, h, w, accumulate_dw)
+    _check(lib().gbo_xent_grad(ctypes.byref(a), _out_f32(loss, a.n, "loss"), _out_f32(lse, a.n, "lse"),
+                               _out_f32(totals, 2, "totals"), ctypes.byref(g), _dev_ptr(workspace, "workspace"),
+                               workspace.numel() * workspace.element_size(), _dev_ptr(dev_status, "dev_status"),
+                               _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

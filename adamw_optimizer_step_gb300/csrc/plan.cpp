@@ -786,6 +786,12 @@ size_t gbo_struct_size(int32_t which) {
     case 3: return sizeof(gbo_adamw_desc);
     case 4: return sizeof(gbo_adamw_opts);
     case 5: return sizeof(gbo_plan_info);
+    case 6: return sizeof(gbo_rope_scaling);
+    case 7: return sizeof(gbo_rope_opts);
+    case 8: return sizeof(gbo_rope_tensor);
+    case 9: return sizeof(gbo_rope_positions);
+    case 10: return sizeof(gbo_xent_args);
+    case 11: return sizeof(gbo_xent_grads);
     default: return 0;
   }
 }

@@ -1,0 +1,1045 @@
+// Softmax cross entropy of a large-vocabulary classifier with its gradients
+// (gbo_xent_forward, gbo_xent_backward, gbo_xent_grad), without the n x v
+// logits in memory.
+//
+//   l = s H W^T;  lse_i = log sum_j exp l_ij;  loss_i = lse_i - l_iy + z lse_i^2
+//   P_ij = w_i s ((1 + 2 z lse_i) exp(l_ij - lse_i) - [j = y_i])
+//   dH = g P W,  dW = g P^T H
+//
+// Steps, all on one stream:
+//   rows    the rows that count (label >= 0, weight != 0) get consecutive
+//           places in their order, and H's rows are copied there: a batch
+//           whose prompts are left out costs what its answers cost, and what
+//           stands in a row that is left out (NaN, say) reaches nothing
+//   logits  tcgen05 GEMM over 256 x 256 tiles, whose epilogue leaves each
+//           row's maximum and sum of exponentials over the tile, and the
+//           label's logit (forward), or P in bf16 (backward)
+//   lse     joins the tiles' maxima and sums per row in a fixed order
+//   products dH += P W and dW = P^T H of one piece of the vocabulary in one
+//           launch, from the piece's P
+// The backward pass forms the logits again, piece by piece of the
+// vocabulary, so its scratch is one piece of P; P is rounded to bf16 once,
+// from the fp32 accumulator and the fp32 lse (the tensor cores take 16-bit
+// operands: the same rounding as a bf16 gradient of the logits), and sums
+// over tokens and vocabulary are fp32.
+//
+// Bound: tensor cores (2 n v d operations a product) from a few hundred rows
+// on, W's HBM traffic below.
+//
+// The GEMM kernel is warp-specialised and persistent like the Newton-Schulz
+// one: CTA pairs (cta_group::2), 256 x 256 tiles, TMA ring of three 64 KB
+// stages, two fp32 accumulators in TMEM, four epilogue warps per CTA; every
+// wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+#include <mutex>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "tc_common.cuh"
+
+namespace gbo {
+
+namespace {
+
+constexpr int kTile = 256;                     // rows and columns of a pair's tile
+constexpr int kBlockK = 64;                    // 64 bf16 = one 128-byte swizzle row
+constexpr int kStageK = 2 * kBlockK;           // K of a stage
+constexpr int kOpBytes = BM * kBlockK * 2;     // 16 KB: 128 rows of A, or of B, per CTA and K block
+constexpr int kSubBytes = 2 * kOpBytes;
+constexpr int kStageBytes = 2 * kSubBytes;
+constexpr int kStages = 3;
+constexpr int kEpiWarps = 4;
+constexpr int kWarpStage = 2 * kSlotBytes;     // two store slots a warp
+constexpr int kSmemUsed = kStages * kStageBytes + kEpiWarps * kWarpStage;
+constexpr int kXentSmem = 1024 + kSmemUsed + 256;
+constexpr int kXentThreads = 64 + 32 * kEpiWarps;
+static_assert(kXentSmem <= 232448, "shared memory per CTA");
+// Row tiles that sweep the vocabulary together: 8192 rows of H, which stay
+// in L2 (33 MB at d = 2048) while W streams past once per sweep.
+constexpr int kSweepTiles = 32;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+enum XentMode { kModeStats = 0, kModeP = 1, kModeProducts = 2 };
+
+// Per-call scalars in the workspace.
+struct XentHead {
+  int32_t rows;      // rows that count
+  float weight_sum;  // sum of their weights
+  float g;           // factor of the gradients
+  int32_t pad;
+};
+
+struct XentParams {
+  CUtensorMap mapA, mapB;    // logits: H, W (K-major); products: P K-major, W MN-major (dH)
+  CUtensorMap mapA2, mapB2;  // products: P MN-major, H MN-major (dW)
+  CUtensorMap mapO;          // P, 32 x 32 boxes
+  const XentHead *head;
+  const int32_t *idx, *lab;  // place -> row, label; padded to a whole tile
+  const float *wt, *lse2;    // weight (0: padding), lse in bits
+  float *ll2;                // forward: the label's logit in bits
+  float2 *part;              // forward: (maximum, sum) per vocabulary tile and place
+  float *dh_acc;             // fp32 sums over the pieces, places x d
+  void *dh, *dw;
+  int32_t *status;
+  int64_t part_ld;           // places per vocabulary tile in part
+  int64_t dh_stride, dw_stride, v0;
+  int32_t v_piece, d;        // columns of this piece
+  int32_t dh_f32, dw_f32, dh_vec, dw_vec, dw_add, first_piece, last_piece;
+  float scale2;              // logit scale in bits: s log2 e
+  float scale, z;
+};
+
+__device__ __forceinline__ uint32_t idesc_of(bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct XentItem {
+  int tm, tn, kit;
+  bool dw;
+};
+
+// What a launch has to do, from the number of rows that count.
+struct XentPlan {
+  int rows, m_tiles, n_tiles;       // logits: row tiles, vocabulary tiles
+  int dh_items, dw_items, d_tiles;  // products
+  int dh_kit, dw_kit;
+  int ncl, cid;
+  int extra, wide;                  // products: see item_at
+};
+
+template <int kMode>
+__device__ __forceinline__ XentPlan make_plan(const XentParams &P, int cid, int ncl) {
+  XentPlan q;
+  q.rows = P.head->rows;
+  q.m_tiles = (q.rows + kTile - 1) / kTile;
+  q.n_tiles = (P.v_piece + kTile - 1) / kTile;
+  q.d_tiles = (P.d + kTile - 1) / kTile;
+  q.dh_items = P.dh ? q.m_tiles * q.d_tiles : 0;
+  q.dw_items = P.dw ? q.n_tiles * q.d_tiles : 0;
+  q.dh_kit = (P.v_piece + kStageK - 1) / kStageK;
+  q.dw_kit = (q.rows + kStageK - 1) / kStageK;
+  q.ncl = ncl;
+  q.cid = cid;
+  q.wide = q.dh_items % ncl;
+  q.extra = q.wide ? (q.dh_kit + q.dw_kit / 2) / max(1, q.dw_kit) : 0;
+  return q;
+}
+
+// Item k of this pair; false: there is none.
+//   logits: round-robin over the pairs; a sweep of kSweepTiles row tiles
+//     takes the vocabulary tile by tile.
+//   products: dH items (K = the piece's width) first, round-robin; `wide`
+//     pairs get one more than the others, who therefore take `extra` dW items
+//     (K = rows) of the same total length first; the rest of dW is dealt to
+//     all.  Items are independent, so the split changes no result.
+template <int kMode>
+__device__ __forceinline__ bool item_at(const XentPlan &q, const XentParams &P, int64_t k, XentItem &it) {
+  if constexpr (kMode != kModeProducts) {
+    const int64_t t = q.cid + k * q.ncl;
+    if (t >= (int64_t)q.m_tiles * q.n_tiles) return false;
+    const int64_t sweep = (int64_t)kSweepTiles * q.n_tiles;
+    const int g = (int)(t / sweep);
+    const int r = (int)(t - g * sweep);
+    const int gm = min(kSweepTiles, q.m_tiles - g * kSweepTiles);
+    it.tn = r / gm;
+    it.tm = g * kSweepTiles + r % gm;
+    it.kit = (P.d + kStageK - 1) / kStageK;
+    it.dw = false;
+    return true;
+  } else {
+    const int mine = q.dh_items / q.ncl + (q.cid < q.wide ? 1 : 0);
+    if (k < mine) {
+      const int t = q.cid + (int)k * q.ncl;
+      it.tm = t / q.d_tiles;
+      it.tn = t % q.d_tiles;
+      it.kit = q.dh_kit;
+      it.dw = false;
+      return true;
+    }
+    k -= mine;
+    const int64_t narrow = q.ncl - q.wide, head = (int64_t)q.extra * narrow;
+    int64_t t;
+    if (q.cid >= q.wide && k < q.extra) {
+      t = (q.cid - q.wide) + k * narrow;
+    } else {
+      if (q.cid >= q.wide) k -= q.extra;
+      t = head + q.cid + k * q.ncl;
+    }
+    if (t >= q.dw_items) return false;
+    it.tm = (int)(t / q.d_tiles);
+    it.tn = (int)(t % q.d_tiles);
+    it.kit = q.dw_kit;
+    it.dw = true;
+    return true;
+  }
+}
+
+struct Ring {
+  int stage;
+  uint32_t phase;
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) stage = 0, phase ^= 1;
+  }
+};
+
+// Load one item's stages.  m0, n0: this CTA's first row of A and of B (their
+// columns when MN-major); k0: first row of B's K axis.  Only the leader arms
+// the barrier, for both CTAs' bytes.
+template <bool kAmn, bool kBmn>
+__device__ __forceinline__ bool produce(const CUtensorMap *ma, const CUtensorMap *mb, int m0, int n0, int kb0, int kit,
+                                        uint32_t smem, uint32_t full0, uint32_t empty0, uint32_t full_lead0,
+                                        bool leader, Ring &ring, uint32_t *armed_parity, uint32_t &armed,
+                                        volatile int32_t *abort_flag) {
+  for (int kb = 0; kb < kit; ++kb) {
+    if (!mbar_wait(empty0 + 8 * ring.stage, ring.phase ^ 1)) return false;
+    if (*abort_flag) return true;
+    if (leader) {
+      mbar_expect_tx(full0 + 8 * ring.stage, 2u * kStageBytes);
+      armed |= 1u << ring.stage;
+      armed_parity[ring.stage] = ring.phase;
+    }
+    const uint32_t fb = full_lead0 + 8 * ring.stage;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      const uint32_t sa = smem + ring.stage * kStageBytes + sub * kSubBytes, sb = sa + kOpBytes;
+      const int k = kb * kStageK + sub * kBlockK;
+      if constexpr (!kAmn) {
+        tma_load_3d_pair(sa, ma, fb, k, m0, 0);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tma_load_3d_pair(sa + h * 8192, ma, fb, m0 + h * 64, k, 0);
+      }
+      if constexpr (!kBmn) {
+        tma_load_3d_pair(sb, mb, fb, k, n0, 0);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tma_load_3d_pair(sb + h * 8192, mb, fb, n0 + h * 64, kb0 + k, 0);
+      }
+    }
+    ring.next();
+  }
+  return true;
+}
+
+template <bool kAmn, bool kBmn>
+__device__ __forceinline__ bool multiply(uint32_t smem, uint32_t full0, uint32_t empty0, uint32_t d_tmem, int kit,
+                                         Ring &ring, bool &issued) {
+  const uint32_t idesc = idesc_of(kAmn, kBmn);
+  const uint64_t a0 = smem_desc(smem, kAmn ? 8192 : 16, 1024);
+  const uint64_t b0 = smem_desc(smem + kOpBytes, kBmn ? 8192 : 16, 1024);
+  constexpr uint32_t astep = (kAmn ? 2048 : 32) >> 4, bstep = (kBmn ? 2048 : 32) >> 4;
+  for (int kb = 0; kb < kit; ++kb) {
+    if (!mbar_wait(full0 + 8 * ring.stage, ring.phase)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      const uint32_t off = (uint32_t)(ring.stage * kStageBytes + sub * kSubBytes) >> 4;
+#pragma unroll
+      for (int k = 0; k < kBlockK / 16; ++k)
+        mma_pair(d_tmem, a0 + off + k * astep, b0 + off + k * bstep, idesc, (kb | sub | k) != 0);
+    }
+    issued = true;
+    mma_commit_pair_mc(empty0 + 8 * ring.stage, 0x3);
+    ring.next();
+  }
+  return true;
+}
+
+// Running maximum and sum of one row over 32 more values (in bits).
+__device__ __forceinline__ void softmax_add(const float (&t)[32], float &m, float &s) {
+  float mx = t[0];
+#pragma unroll
+  for (int k = 1; k < 32; ++k) mx = fmaxf(mx, t[k]);
+  const float mn = fmaxf(m, mx);
+  const float at = mn == -INFINITY ? 0.f : mn;  // nothing but -inf so far: every term is 0
+  float a = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) a += exp2_fast(t[k] - at);
+  s = fmaf(s, exp2_fast(m - at), a);
+  m = mn;
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_constant__ XentParams P) {
+  pdl_launch();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kSmemUsed);
+  // bars: full[kStages], empty[kStages], accf[2], acce[2], drain, (TMEM address, abort flag)
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kStages + 5);
+  volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
+  const uint32_t accf0 = smem_u32(bars + 2 * kStages), acce0 = smem_u32(bars + 2 * kStages + 2);
+  const uint32_t drain = smem_u32(bars + 2 * kStages + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_rank();
+  const bool leader = crank == 0;
+  // Barriers as in the Newton-Schulz pair kernel: full on the leader (both
+  // CTAs' bytes), empty and accf in each CTA (multicast commits of the
+  // leader's MMAs), acce on the leader (one arrival per epilogue warp of both).
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(accf0 + 8 * a, 1);
+      mbar_init(acce0 + 8 * a, 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  const XentPlan q = make_plan<kMode>(P, blockIdx.x >> 1, gridDim.x >> 1);
+  const uint32_t full_lead0 = map_to_rank(full0, 0), acce_lead0 = map_to_rank(acce0, 0);
+  const uint32_t ring0 = smem_u32(smem);
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    flag_status(P.status, GBO_STATUS_TIMEOUT);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring ring = {0, 0};
+      uint32_t armed = 0, armed_parity[kStages] = {};
+      XentItem it;
+      for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
+        const int m0 = it.tm * kTile + (int)crank * BM, n0 = it.tn * kTile + (int)crank * BM;
+        bool ok;
+        if constexpr (kMode != kModeProducts)
+          ok = produce<false, false>(&P.mapA, &P.mapB, m0, (int)P.v0 + n0, 0, it.kit, ring0, full0, empty0, full_lead0,
+                                     leader, ring, armed_parity, armed, abort_flag);
+        else if (!it.dw)
+          ok = produce<false, true>(&P.mapA, &P.mapB, m0, n0, (int)P.v0, it.kit, ring0, full0, empty0, full_lead0,
+                                    leader, ring, armed_parity, armed, abort_flag);
+        else
+          ok = produce<true, true>(&P.mapA2, &P.mapB2, m0, n0, 0, it.kit, ring0, full0, empty0, full_lead0, leader,
+                                   ring, armed_parity, armed, abort_flag);
+        if (!ok) { give_up(); break; }
+      }
+      if (*abort_flag && leader) {  // copies armed here land before shared memory goes away
+        for (int s = 0; s < kStages; ++s)
+          if (armed >> s & 1u) (void)mbar_wait(full0 + 8 * s, armed_parity[s]);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      Ring ring = {0, 0};
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool issued = false;
+      XentItem it;
+      for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
+        if (!mbar_wait_cluster(acce0 + 8 * acc, acc_phase ^ 1)) { give_up(); break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
+        bool ok;
+        if constexpr (kMode != kModeProducts)
+          ok = multiply<false, false>(ring0, full0, empty0, d_tmem, it.kit, ring, issued);
+        else if (!it.dw)
+          ok = multiply<false, true>(ring0, full0, empty0, d_tmem, it.kit, ring, issued);
+        else
+          ok = multiply<true, true>(ring0, full0, empty0, d_tmem, it.kit, ring, issued);
+        if (!ok) { give_up(); break; }
+        mma_commit_pair_mc(accf0 + 8 * acc, 0x3);
+        if (++acc == 2) acc = 0, acc_phase ^= 1;
+      }
+      if (*abort_flag && issued) {
+        mma_commit_pair(drain);
+        (void)mbar_wait(drain, 0);
+      }
+    }
+  } else {
+    const int quarter = warp & 3;
+    const uint32_t stage = smem_u32(smem + kStages * kStageBytes + (warp - 2) * kWarpStage);
+    int slot = 0, acc = 0;
+    uint32_t acc_phase = 0;
+    XentItem it;
+    for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
+      const int i0 = it.tm * kTile + (int)crank * BM + quarter * 32, i = i0 + lane;
+      const int c0 = it.tn * kTile;
+      // per-row values of this tile, fetched while its products run
+      int lab = -1;
+      float wt = 0.f, lse2 = 0.f;
+      if constexpr (kMode != kModeProducts) {
+        if (i < q.rows) {
+          lab = P.lab[i] - (int)P.v0;
+          if constexpr (kMode == kModeP) wt = P.wt[i], lse2 = P.lse2[i];
+        }
+      }
+      if (!mbar_wait(accf0 + 8 * acc, acc_phase)) { give_up(); break; }
+      tc_fence_after();
+      const uint32_t trow = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile);
+      if constexpr (kMode == kModeStats) {
+        if (i0 < q.rows) {
+          float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+          for (int ch = 0; ch < kTile / 32; ++ch) {
+            const int col0 = c0 + 32 * ch;
+            if (col0 >= P.v_piece) break;
+            float v[32];
+            tmem_ld32(trow + ch * 32, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= P.scale2;
+            if (lab >= col0 && lab < col0 + 32) {
+              float l = 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) l = lab == col0 + j ? v[j] : l;
+              P.ll2[i] = l;
+            }
+            if (col0 + 32 > P.v_piece) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (col0 + j >= P.v_piece) v[j] = -INFINITY;
+            }
+            softmax_add(v, m, s);
+          }
+          if (i < q.rows) P.part[(int64_t)it.tn * P.part_ld + i] = make_float2(m, s);
+        }
+      } else if constexpr (kMode == kModeP) {
+        const float mult = wt * P.scale, peak = mult * fmaf(2.f * P.z, lse2 * kLn2, 1.f);
+#pragma unroll 1
+        for (int ch = 0; ch < kTile / 32; ++ch) {
+          const int col0 = c0 + 32 * ch;
+          if (col0 >= P.v_piece) break;
+          float v[32];
+          tmem_ld32(trow + ch * 32, v);
+          if (wt != 0.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = peak * exp2_fast(fmaf(v[j], P.scale2, -lse2));
+            if (lab >= col0 && lab < col0 + 32) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (lab == col0 + j) v[j] -= mult;
+            }
+          } else {  // places behind the last row: their P multiplies zero rows of H, and must be finite
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+          tma_store_block(&P.mapO, stage, slot, v, false, col0, i0, 0, lane);
+        }
+      } else if (it.dw) {
+        const float g = P.head->g;
+        const int64_t row = P.v0 + i;
+        const bool ok = i < P.v_piece;
+#pragma unroll 1
+        for (int ch = 0; ch < kTile / 32; ++ch) {
+          const int col0 = c0 + 32 * ch;
+          if (col0 >= P.d || i0 >= P.v_piece) break;
+          float v[32];
+          tmem_ld32(trow + ch * 32, v);
+          if (!ok) continue;
+          const uint32_t mask = prefix_mask(P.d - col0);
+          const bool vec = P.dw_vec && mask == 0xffffffffu;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = it.kit > 0 ? g * v[j] : 0.f;  // no rows: nothing was multiplied
+          const int64_t at = row * P.dw_stride + col0;
+          if (P.dw_f32) {
+            float *o = static_cast<float *>(P.dw) + at;
+            if (P.dw_add) {
+              float w[32];
+              load_row32(o, w, vec, mask);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += w[j];
+            }
+            store_row32(o, v, vec, mask);
+          } else {
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(P.dw) + at;
+            if (P.dw_add) {
+              float w[32];
+              load_row32(o, w, vec, mask);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += w[j];
+            }
+            store_row32(o, v, vec, mask);
+          }
+        }
+      } else {
+        const float g = P.head->g;
+        const bool ok = i < q.rows;
+        const int64_t row = ok ? P.idx[i] : 0;
+#pragma unroll 1
+        for (int ch = 0; ch < kTile / 32; ++ch) {
+          const int col0 = c0 + 32 * ch;
+          if (col0 >= P.d || i0 >= q.rows) break;
+          float v[32];
+          tmem_ld32(trow + ch * 32, v);
+          if (!ok) continue;
+          const uint32_t mask = prefix_mask(P.d - col0);
+          const bool whole = mask == 0xffffffffu;
+          float *sum = P.dh_acc + (int64_t)i * P.d + col0;  // d is a multiple of 8: 32-byte aligned
+          if (!P.first_piece) {
+            float w[32];
+            load_row32(sum, w, whole, mask);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += w[j];
+          }
+          if (!P.last_piece) {
+            store_row32(sum, v, whole, mask);
+            continue;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= g;
+          const int64_t at = row * P.dh_stride + col0;
+          const bool vec = P.dh_vec && whole;
+          if (P.dh_f32) store_row32(static_cast<float *>(P.dh) + at, v, vec, mask);
+          else store_row32(static_cast<__nv_bfloat16 *>(P.dh) + at, v, vec, mask);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acce_lead0 + 8 * acc);
+      if (++acc == 2) acc = 0, acc_phase ^= 1;
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// rows
+
+struct RowsParams {
+  const void *labels;
+  const float *row_weight, *upstream;
+  const float *lse_in;   // backward alone: the forward's lse per row
+  XentHead *head;
+  int32_t *place;        // row -> place, or -1
+  int32_t *idx, *lab;
+  float *wt, *lse2;
+  int32_t *status;
+  int64_t n, n_pad, v;
+  int32_t labels64, mean;
+};
+
+__device__ __forceinline__ int64_t label_at(const RowsParams &R, int64_t i) {
+  return R.labels64 ? reinterpret_cast<const int64_t *>(R.labels)[i] : reinterpret_cast<const int32_t *>(R.labels)[i];
+}
+
+// One block: places of the rows that count, in their order (a scan over
+// threads that each own a run of rows), the sum of their weights in a fixed
+// order, and the factor of the gradients.
+__global__ void __launch_bounds__(1024) xent_rows_kernel(const __grid_constant__ RowsParams R) {
+  pdl_launch();
+  __shared__ int32_t cnt[32];
+  __shared__ float red[32];
+  pdl_wait();
+  const int64_t run = (R.n + 1023) / 1024, i0 = threadIdx.x * run, i1 = min(i0 + run, R.n);
+  int mine = 0;
+  float wsum = 0.f;
+  bool bad = false;
+  for (int64_t i = i0; i < i1; ++i) {
+    const int64_t y = label_at(R, i);
+    const float w = R.row_weight ? R.row_weight[i] : 1.f;
+    bad |= y >= R.v;
+    if (y >= 0 && y < R.v && w != 0.f) ++mine, wsum += w;
+  }
+  if (bad) flag_status(R.status, GBO_STATUS_BAD_LABEL);
+  int at = mine;  // inclusive scan over the warp, then over the warps
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += u;
+  }
+  if (lane == 31) cnt[warp] = at;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) before += cnt[w];
+    total += cnt[w];
+  }
+  int place = before + at - mine;
+  for (int64_t i = i0; i < i1; ++i) {
+    const int64_t y = label_at(R, i);
+    const float w = R.row_weight ? R.row_weight[i] : 1.f;
+    const bool in = y >= 0 && y < R.v && w != 0.f;
+    R.place[i] = in ? place : -1;
+    if (!in) continue;
+    R.idx[place] = (int32_t)i;
+    R.lab[place] = (int32_t)y;
+    R.wt[place] = w;
+    if (R.lse_in) R.lse2[place] = R.lse_in[i] * kLog2e;
+    ++place;
+  }
+  const float ws = block_sum(wsum, red);
+  for (int64_t p = total + threadIdx.x; p < R.n_pad; p += 1024) R.idx[p] = 0, R.lab[p] = -1, R.wt[p] = 0.f, R.lse2[p] = 0.f;
+  if (threadIdx.x == 0) {
+    const float up = R.upstream ? *R.upstream : 1.f;
+    R.head->rows = total;
+    R.head->weight_sum = ws;
+    R.head->g = R.mean ? (total > 0 ? up / ws : 0.f) : up;
+  }
+}
+
+struct GatherParams {
+  const __nv_bfloat16 *h;
+  __nv_bfloat16 *hc;
+  const XentHead *head;
+  const int32_t *place;
+  float *loss, *lse;  // of rows left out: 0
+  void *dh;
+  int64_t n, n_pad, d, h_stride, dh_stride;
+  int32_t dh_f32, vec;
+};
+
+// One warp per row: its copy at its place; rows left out get zero losses and
+// gradients; the places behind the last row, up to a whole tile, zeros.
+__global__ void __launch_bounds__(256) xent_gather_kernel(const __grid_constant__ GatherParams G) {
+  pdl_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  pdl_wait();
+  if (i >= G.n) {  // the tail
+    const int64_t p = G.head->rows + (i - G.n);
+    const int64_t end = ((int64_t)G.head->rows + kTile - 1) / kTile * kTile;
+    if (p >= end) return;
+    for (int64_t c = lane; c < G.d / 8; c += 32) reinterpret_cast<uint4 *>(G.hc + p * G.d)[c] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int32_t p = G.place[i];
+  if (p >= 0) {
+    const __nv_bfloat16 *src = G.h + i * G.h_stride;
+    __nv_bfloat16 *dst = G.hc + p * G.d;
+    if (G.vec)
+      for (int64_t c = lane; c < G.d / 8; c += 32) reinterpret_cast<uint4 *>(dst)[c] = reinterpret_cast<const uint4 *>(src)[c];
+    else
+      for (int64_t c = lane; c < G.d; c += 32) dst[c] = src[c];
+    return;
+  }
+  if (lane == 0) {
+    if (G.loss) G.loss[i] = 0.f;
+    if (G.lse) G.lse[i] = 0.f;
+  }
+  if (G.dh)
+    for (int64_t c = lane; c < G.d; c += 32) st_elem(G.dh, G.dh_f32 ? GBO_F32 : GBO_BF16, i * G.dh_stride + c, 0.f);
+}
+
+struct LseParams {
+  const XentHead *head;
+  const float2 *part;
+  const float *ll2, *wt;
+  const int32_t *idx;
+  float *lse2, *loss, *lse, *sums;
+  int32_t *status;
+  int64_t part_ld;
+  int32_t tiles, rows_log2;
+  float z;
+};
+
+// Join the tiles' (maximum, sum) pairs of each row.  A block of 256 threads
+// takes 2^rows_log2 rows, consecutive threads consecutive rows, and 256 >>
+// rows_log2 strands of tiles; strands join in a fixed tree.
+__global__ void __launch_bounds__(256) xent_lse_kernel(const __grid_constant__ LseParams L) {
+  pdl_launch();
+  __shared__ float2 red[256];
+  __shared__ float wl[256];
+  pdl_wait();
+  const int nr = 1 << L.rows_log2, strands = 256 >> L.rows_log2;
+  const int r = threadIdx.x & (nr - 1), strand = threadIdx.x >> L.rows_log2;
+  const int rows = L.head->rows;
+  const int64_t i = (int64_t)blockIdx.x * nr + r;
+  float m = -INFINITY, s = 0.f;
+  auto join = [](float &m, float &s, float m2, float s2) {
+    const float mn = fmaxf(m, m2), at = mn == -INFINITY ? 0.f : mn;
+    s = s * exp2_fast(m - at) + s2 * exp2_fast(m2 - at);
+    m = mn;
+  };
+  if (i < rows) {
+    int t = strand;
+    for (; t + 3 * strands < L.tiles; t += 4 * strands) {
+      float2 p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) p[u] = L.part[(int64_t)(t + u * strands) * L.part_ld + i];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) join(m, s, p[u].x, p[u].y);
+    }
+    for (; t < L.tiles; t += strands) {
+      const float2 p = L.part[(int64_t)t * L.part_ld + i];
+      join(m, s, p.x, p.y);
+    }
+  }
+  red[threadIdx.x] = make_float2(m, s);
+  for (int h = strands >> 1; h > 0; h >>= 1) {
+    __syncthreads();
+    if (strand < h) {
+      const float2 o = red[threadIdx.x + (h << L.rows_log2)];
+      join(m, s, o.x, o.y);
+      red[threadIdx.x] = make_float2(m, s);
+    }
+  }
+  float weighted = 0.f;
+  if (strand == 0 && i < rows) {
+    const float lse2 = m + log2f(s), lse = lse2 * kLn2;
+    const float loss = (lse2 - L.ll2[i]) * kLn2 + L.z * lse * lse;
+    if (!isfinite(loss)) flag_status(L.status, GBO_STATUS_NONFINITE);
+    L.lse2[i] = lse2;
+    const int32_t row = L.idx[i];
+    if (L.loss) L.loss[row] = loss;
+    if (L.lse) L.lse[row] = lse;
+    weighted = L.wt[i] * loss;
+  }
+  if (!L.sums) return;
+  wl[threadIdx.x] = strand == 0 ? weighted : 0.f;
+  __syncthreads();
+  const float a = block_sum(wl[threadIdx.x], reinterpret_cast<float *>(red));
+  if (threadIdx.x == 0) L.sums[blockIdx.x] = a;
+}
+
+__global__ void __launch_bounds__(1024) xent_totals_kernel(const float *sums, int n, const XentHead *head,
+                                                           float *totals) {
+  pdl_launch();
+  __shared__ float red[32];
+  pdl_wait();
+  float a = 0.f;
+  for (int k = threadIdx.x; k < n; k += 1024) a += sums[k];
+  a = block_sum(a, red);
+  if (threadIdx.x == 0) totals[0] = a, totals[1] = head->weight_sum;
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Scratch of a call, in this order.  The tiles' statistics and P share their
+// room: the statistics are done with before P is written.
+struct XentSpace {
+  int64_t head, place, idx, lab, wt, lse2, ll2, sums, hc, acc, big;  // byte offsets
+  int64_t n_pad, bytes;
+  int64_t piece;  // columns of a piece of the vocabulary
+  int32_t pieces;
+};
+
+constexpr int64_t kPieceBytes = int64_t(2) << 30;  // P of one piece, unless the caller caps the workspace
+
+// grad: with the backward pass.  piece: columns per piece (0: as many as
+// kPieceBytes holds).
+XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, int64_t piece) {
+  XentSpace s = {};
+  s.n_pad = up_to(std::max<int64_t>(n, 1), kTile);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t r = at;
+    at += up_to(bytes, 1024);
+    return r;
+  };
+  s.head = take(sizeof(XentHead));
+  s.place = take(4 * s.n_pad);
+  s.idx = take(4 * s.n_pad);
+  s.lab = take(4 * s.n_pad);
+  s.wt = take(4 * s.n_pad);
+  s.lse2 = take(4 * s.n_pad);
+  s.ll2 = take(4 * s.n_pad);
+  s.sums = take(4 * s.n_pad);
+  s.hc = take(2 * s.n_pad * d);
+  int64_t big = forward ? 8 * s.n_pad * ((v + kTile - 1) / kTile) : 0;
+  if (grad) {
+    if (piece <= 0) piece = kPieceBytes / (2 * s.n_pad);
+    piece = std::max<int64_t>(kTile, piece / kTile * kTile);
+    s.pieces = (int32_t)((v + piece - 1) / piece);
+    s.piece = up_to((v + s.pieces - 1) / s.pieces, kTile);  // even pieces
+    s.pieces = (int32_t)((v + s.piece - 1) / s.piece);
+    s.acc = take(s.pieces > 1 ? 4 * s.n_pad * d : 0);
+    big = std::max(big, 2 * s.n_pad * s.piece);
+  }
+  s.big = take(big);
+  s.bytes = at;
+  return s;
+}
+
+// The widest pieces whose workspace fits `bytes` (false: not even one tile).
+bool fit_space(int64_t n, int64_t v, int64_t d, bool forward, int64_t bytes, XentSpace *out) {
+  XentSpace s = space_of(n, v, d, true, forward, 0);
+  if (s.bytes > bytes) {
+    int64_t lo = 1, hi = up_to(v, kTile) / kTile;  // pieces of lo tiles fit, of hi do not
+    if (space_of(n, v, d, true, forward, kTile).bytes > bytes) return false;
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) / 2;
+      (space_of(n, v, d, true, forward, mid * kTile).bytes <= bytes ? lo : hi) = mid;
+    }
+    s = space_of(n, v, d, true, forward, lo * kTile);
+  }
+  *out = s;
+  return true;
+}
+
+int xent_fail(int code, const char *msg) { return report_error(code, msg); }
+
+int check_args(const gbo_xent_args *a) {
+  if (!a) return xent_fail(GBO_ERR_INVALID_ARG, "args is NULL");
+  if (a->n < 0 || a->n > (int64_t(1) << 30)) return xent_fail(GBO_ERR_SHAPE, "n must be in 0..2^30");
+  if (a->v < 1 || a->v > (int64_t(1) << 30)) return xent_fail(GBO_ERR_SHAPE, "v must be in 1..2^30");
+  if (a->d < 8 || a->d % 8 || a->d > (1 << 20)) return xent_fail(GBO_ERR_SHAPE, "d must be a multiple of 8 in 8..2^20");
+  if (a->h_stride < a->d || a->w_stride < a->d) return xent_fail(GBO_ERR_SHAPE, "a row stride is smaller than d");
+  if (a->w_stride % 8) return xent_fail(GBO_ERR_SHAPE, "w_stride must be a multiple of 8 elements (16-byte rows)");
+  if (!a->w || (reinterpret_cast<uintptr_t>(a->w) & 15))
+    return xent_fail(GBO_ERR_INVALID_ARG, "w is NULL or not 16-byte aligned");
+  if (a->n > 0 && (!a->h || (reinterpret_cast<uintptr_t>(a->h) & 1) || !a->labels))
+    return xent_fail(GBO_ERR_INVALID_ARG, "h or labels NULL or misaligned");
+  if (a->label_dtype != GBO_I32 && a->label_dtype != GBO_I64)
+    return xent_fail(GBO_ERR_DTYPE, "labels must be GBO_I32 or GBO_I64");
+  if (reinterpret_cast<uintptr_t>(a->labels) % (a->label_dtype == GBO_I64 ? 8 : 4))
+    return xent_fail(GBO_ERR_INVALID_ARG, "labels misaligned");
+  if ((reinterpret_cast<uintptr_t>(a->row_weight) & 3) || (reinterpret_cast<uintptr_t>(a->upstream) & 3))
+    return xent_fail(GBO_ERR_INVALID_ARG, "row_weight or upstream misaligned");
+  if (!std::isfinite(a->logit_scale) || !std::isfinite(a->z_loss))
+    return xent_fail(GBO_ERR_INVALID_ARG, "non-finite logit_scale or z_loss");
+  if (a->mean != 0 && a->mean != 1) return xent_fail(GBO_ERR_INVALID_ARG, "mean must be 0 or 1");
+  return GBO_OK;
+}
+
+int check_grads(const gbo_xent_args *a, const gbo_xent_grads *g) {
+  if (!g || (!g->dh && !g->dw)) return xent_fail(GBO_ERR_INVALID_ARG, "no gradient is asked for");
+  const int32_t types[2] = {g->dh_dtype, g->dw_dtype};
+  const void *ptrs[2] = {g->dh, g->dw};
+  const int64_t strides[2] = {g->dh_stride, g->dw_stride};
+  for (int k = 0; k < 2; ++k) {
+    if (!ptrs[k]) continue;
+    if (types[k] != GBO_F32 && types[k] != GBO_BF16) return xent_fail(GBO_ERR_DTYPE, "gradients are GBO_F32 or GBO_BF16");
+    if (reinterpret_cast<uintptr_t>(ptrs[k]) % (types[k] == GBO_F32 ? 4 : 2))
+      return xent_fail(GBO_ERR_INVALID_ARG, "a gradient is misaligned");
+    if (strides[k] < a->d) return xent_fail(GBO_ERR_SHAPE, "a gradient's row stride is smaller than d");
+  }
+  if (g->accumulate_dw != 0 && g->accumulate_dw != 1) return xent_fail(GBO_ERR_INVALID_ARG, "accumulate_dw must be 0 or 1");
+  return GBO_OK;
+}
+
+template <int kMode>
+cudaError_t launch_xent(const XentParams &P, int64_t items, int sm, cudaStream_t stream) {
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  static int resident = 0;
+  std::call_once(once, [&] {
+    attr_err = cudaFuncSetAttribute(xent_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kXentSmem);
+    if (attr_err != cudaSuccess) return;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.blockDim = dim3(kXentThreads);
+    cfg.dynamicSmemBytes = kXentSmem;
+    cfg.gridDim = dim3(2 * std::max(1, sm / 2));
+    if (cudaOccupancyMaxActiveClusters(&resident, xent_kernel<kMode>, &cfg) != cudaSuccess) resident = 0;
+    (void)cudaGetLastError();
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  const int64_t fit = std::max(1, resident > 0 ? std::min(resident, sm / 2) : sm / 2);
+  const int clusters = (int)std::max<int64_t>(1, std::min(items, fit));
+  const cudaError_t e = launch_kernel(xent_kernel<kMode>, dim3(2 * clusters), dim3(kXentThreads), kXentSmem, stream, 2, P);
+  count_launches(1);
+  return e;
+}
+
+bool map_2d(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, int64_t ld, uint32_t bc, uint32_t br,
+            CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B) {
+  return encode_map(m, const_cast<void *>(p), cols, rows, 1, ld, bc, br, sw);
+}
+
+int cuda_err(cudaError_t e) {
+  char msg[200];
+  snprintf(msg, sizeof msg, "cross-entropy kernels: %s", cudaGetErrorString(e));
+  return xent_fail(GBO_ERR_CUDA, msg);
+}
+
+// forward: loss, lse, totals.  g: gradients too (lse_in: with the forward
+// pass skipped, its lse).
+int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, float *totals, const float *lse_in,
+             const gbo_xent_grads *g, void *workspace, size_t ws_bytes, int32_t *status, gbo_stream_t stream) {
+  int rc = check_args(a);
+  if (rc != GBO_OK) return rc;
+  if (g && (rc = check_grads(a, g)) != GBO_OK) return rc;
+  if (!forward && a->n > 0 && !lse_in) return xent_fail(GBO_ERR_INVALID_ARG, "lse is NULL");
+  if ((reinterpret_cast<uintptr_t>(loss) | reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(totals) |
+       reinterpret_cast<uintptr_t>(lse_in) | reinterpret_cast<uintptr_t>(status)) & 3)
+    return xent_fail(GBO_ERR_INVALID_ARG, "misaligned output, lse or status pointer");
+  int dev, sm = 0;
+  if ((rc = require_device(&dev, &sm)) != GBO_OK) return rc;
+  XentSpace S;
+  if (g) {
+    if (!fit_space(a->n, a->v, a->d, forward, (int64_t)ws_bytes, &S))
+      return xent_fail(GBO_ERR_WORKSPACE, "workspace too small for a piece of 256 columns");
+  } else {
+    S = space_of(a->n, a->v, a->d, false, true, 0);
+  }
+  if (!workspace || (int64_t)ws_bytes < S.bytes) return xent_fail(GBO_ERR_WORKSPACE, "workspace missing or too small");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255) return xent_fail(GBO_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  char *ws = static_cast<char *>(workspace);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+
+  RowsParams R = {};
+  R.labels = a->labels, R.row_weight = a->row_weight, R.upstream = a->upstream, R.lse_in = forward ? nullptr : lse_in;
+  R.head = reinterpret_cast<XentHead *>(ws + S.head);
+  R.place = reinterpret_cast<int32_t *>(ws + S.place);
+  R.idx = reinterpret_cast<int32_t *>(ws + S.idx);
+  R.lab = reinterpret_cast<int32_t *>(ws + S.lab);
+  R.wt = reinterpret_cast<float *>(ws + S.wt);
+  R.lse2 = reinterpret_cast<float *>(ws + S.lse2);
+  R.status = status;
+  R.n = a->n, R.n_pad = S.n_pad, R.v = a->v;
+  R.labels64 = a->label_dtype == GBO_I64, R.mean = a->mean;
+  if ((e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), 0, st, 1, R)) != cudaSuccess) return cuda_err(e);
+  count_launches(1);
+
+  GatherParams G = {};
+  G.h = static_cast<const __nv_bfloat16 *>(a->h);
+  G.hc = reinterpret_cast<__nv_bfloat16 *>(ws + S.hc);
+  G.head = R.head, G.place = R.place, G.loss = loss, G.lse = lse;
+  G.dh = g ? g->dh : nullptr;
+  G.n = a->n, G.n_pad = S.n_pad, G.d = a->d, G.h_stride = a->h_stride, G.dh_stride = g ? g->dh_stride : 0;
+  G.dh_f32 = g && g->dh_dtype == GBO_F32;
+  G.vec = a->h_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a->h) & 15) == 0;
+  if ((e = launch_kernel(xent_gather_kernel, dim3((unsigned)((a->n + kTile + 7) / 8)), dim3(256), 0, st, 1, G)) !=
+      cudaSuccess)
+    return cuda_err(e);
+  count_launches(1);
+
+  XentParams P;
+  memset(&P, 0, sizeof P);
+  P.head = R.head, P.idx = R.idx, P.lab = R.lab, P.wt = R.wt, P.lse2 = R.lse2;
+  P.ll2 = reinterpret_cast<float *>(ws + S.ll2);
+  P.status = status;
+  P.d = (int32_t)a->d;
+  P.scale = a->logit_scale, P.scale2 = a->logit_scale * kLog2e, P.z = a->z_loss;
+  const int64_t m_tiles = S.n_pad / kTile, d_tiles = (a->d + kTile - 1) / kTile;
+  bool maps = true;
+  if (a->n > 0) {
+    maps = map_2d(&P.mapA, G.hc, a->d, S.n_pad, a->d, kBlockK, BM) &&
+           map_2d(&P.mapB, a->w, a->d, a->v, a->w_stride, kBlockK, BM);
+    if (!maps) return xent_fail(GBO_ERR_CUDA, "tensor map of H or W");
+  }
+  if (forward && a->n > 0) {
+    P.part = reinterpret_cast<float2 *>(ws + S.big);
+    P.part_ld = S.n_pad;
+    P.v0 = 0, P.v_piece = (int32_t)a->v;
+    const int64_t n_tiles = (a->v + kTile - 1) / kTile;
+    if ((e = launch_xent<kModeStats>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) return cuda_err(e);
+    LseParams L = {};
+    L.head = R.head, L.part = P.part, L.ll2 = P.ll2, L.wt = R.wt, L.idx = R.idx;
+    L.lse2 = R.lse2, L.loss = loss, L.lse = lse;
+    L.sums = totals ? reinterpret_cast<float *>(ws + S.sums) : nullptr;
+    L.status = status;
+    L.part_ld = S.n_pad, L.tiles = (int32_t)n_tiles, L.z = a->z_loss;
+    while (L.rows_log2 < 5 && (1 << L.rows_log2) < a->n) ++L.rows_log2;
+    const int blocks = (int)((a->n + (1 << L.rows_log2) - 1) >> L.rows_log2);
+    if ((e = launch_kernel(xent_lse_kernel, dim3(blocks), dim3(256), 0, st, 1, L)) != cudaSuccess) return cuda_err(e);
+    count_launches(1);
+    if (totals) {
+      if ((e = launch_kernel(xent_totals_kernel, dim3(1), dim3(1024), 0, st, 1, (const float *)L.sums, blocks,
+                             (const XentHead *)R.head, totals)) != cudaSuccess)
+        return cuda_err(e);
+      count_launches(1);
+    }
+  } else if (forward && totals) {
+    if ((e = launch_kernel(xent_totals_kernel, dim3(1), dim3(1024), 0, st, 1, (const float *)nullptr, 0,
+                           (const XentHead *)R.head, totals)) != cudaSuccess)
+      return cuda_err(e);
+    count_launches(1);
+  }
+  if (g) {
+    P.dh = a->n > 0 ? g->dh : nullptr, P.dw = g->dw;
+    P.dh_stride = g->dh_stride, P.dw_stride = g->dw_stride;
+    P.dh_f32 = g->dh_dtype == GBO_F32, P.dw_f32 = g->dw_dtype == GBO_F32;
+    P.dh_vec = (reinterpret_cast<uintptr_t>(g->dh) & 15) == 0 && g->dh_stride % (P.dh_f32 ? 4 : 8) == 0;
+    P.dw_vec = (reinterpret_cast<uintptr_t>(g->dw) & 15) == 0 && g->dw_stride % (P.dw_f32 ? 4 : 8) == 0;
+    P.dw_add = g->accumulate_dw;
+    P.dh_acc = reinterpret_cast<float *>(ws + S.acc);
+    void *pbuf = ws + S.big;
+    for (int32_t c = 0; c < S.pieces; ++c) {
+      P.v0 = c * S.piece;
+      P.v_piece = (int32_t)std::min<int64_t>(S.piece, a->v - P.v0);
+      P.first_piece = c == 0, P.last_piece = c + 1 == S.pieces;
+      const int64_t n_tiles = (P.v_piece + kTile - 1) / kTile;
+      XentParams Q = P;
+      maps = map_2d(&P.mapO, pbuf, P.v_piece, S.n_pad, S.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
+             map_2d(&Q.mapA, pbuf, P.v_piece, S.n_pad, S.piece, kBlockK, BM) &&
+             map_2d(&Q.mapB, a->w, a->d, a->v, a->w_stride, 64, kBlockK) &&
+             map_2d(&Q.mapA2, pbuf, P.v_piece, S.n_pad, S.piece, 64, kBlockK) &&
+             map_2d(&Q.mapB2, G.hc, a->d, S.n_pad, a->d, 64, kBlockK);
+      if (!maps) return xent_fail(GBO_ERR_CUDA, "tensor map of P");
+      if (a->n > 0 && (e = launch_xent<kModeP>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) return cuda_err(e);
+      const int64_t items = (P.dh ? m_tiles * d_tiles : 0) + (P.dw ? n_tiles * d_tiles : 0);
+      if (items > 0 && (e = launch_xent<kModeProducts>(Q, items, sm, st)) != cudaSuccess) return cuda_err(e);
+    }
+  }
+  return report_ok();
+}
+
+}  // namespace
+}  // namespace gbo
+
+using namespace gbo;
+
+extern "C" size_t gbo_xent_workspace_bytes(int64_t n, int64_t v, int64_t d, int32_t grad, int64_t cap) {
+  if (n < 0 || v < 1 || d < 8 || d % 8 || n > (int64_t(1) << 30) || v > (int64_t(1) << 30) || d > (1 << 20)) return 0;
+  if (!grad) return (size_t)space_of(n, v, d, false, true, 0).bytes;
+  XentSpace s;
+  if (cap > 0) return fit_space(n, v, d, true, cap, &s) ? (size_t)s.bytes : 0;
+  return (size_t)space_of(n, v, d, true, true, 0).bytes;
+}
+
+extern "C" int gbo_xent_forward(const gbo_xent_args *args, float *loss, float *lse, float *totals, void *workspace,
+                                size_t ws_bytes, int32_t *dev_status, gbo_stream_t stream) {
+  return xent_run(args, true, loss, lse, totals, nullptr, nullptr, workspace, ws_bytes, dev_status, stream);
+}
+
+extern "C" int gbo_xent_backward(const gbo_xent_args *args, const float *lse, const gbo_xent_grads *grads,
+                                 void *workspace, size_t ws_bytes, int32_t *dev_status, gbo_stream_t stream) {
+  if (!grads) return xent_fail(GBO_ERR_INVALID_ARG, "grads is NULL");
+  return xent_run(args, false, nullptr, nullptr, nullptr, lse, grads, workspace, ws_bytes, dev_status, stream);
+}
+
+extern "C" int gbo_xent_grad(const gbo_xent_args *args, float *loss, float *lse, float *totals,
+                             const gbo_xent_grads *grads, void *workspace, size_t ws_bytes, int32_t *dev_status,
+                             gbo_stream_t stream) {
+  if (!grads) return xent_fail(GBO_ERR_INVALID_ARG, "grads is NULL");
+  return xent_run(args, true, loss, lse, totals, nullptr, grads, workspace, ws_bytes, dev_status, stream);
+}

@@ -1,0 +1,211 @@
+"""Torch-facing calls of the operators around the optimizer step: rotary
+positions, per-head q/k norms with rotation, and the tied classifier's cross
+entropy with its gradients.
+
+Each allocates its outputs and scratch with torch's allocator and makes one
+library call on the current stream.  ``rotary_autograd``, ``qk_norm_rotary_autograd``
+and ``linear_cross_entropy_loss`` are the same operators inside autograd, so
+that ``loss.backward()`` leaves the gradients that
+:class:`~.routing.HybridOptimizer` steps.
+
+Heads are (batch, seq, heads, dim) tensors whose last axis is contiguous; any
+other strides are taken as they are (slices of a fused projection, or a
+transposed (batch, heads, seq, dim) tensor).  Positions are an integer tensor
+(seq,) or (batch, seq), or an int, the first position.
+"""
+
+import ctypes
+
+import torch
+
+from . import _binding as B
+
+LAYOUTS = {"half": B.GBO_ROPE_HALF, "interleaved": B.GBO_ROPE_INTERLEAVED}
+SCALINGS = {"none": B.GBO_ROPE_SCALE_NONE, "linear": B.GBO_ROPE_SCALE_LINEAR, "ntk": B.GBO_ROPE_SCALE_NTK,
+            "yarn": B.GBO_ROPE_SCALE_YARN, "wavelength": B.GBO_ROPE_SCALE_WAVELENGTH}
+
+
+class RotarySpec:
+    """A rotation's layout and frequencies, built once and kept by the model.
+
+    ``rot_dim`` elements from ``offset`` on are rotated (default: the whole
+    head).  ``scaling``: None, or a dict with ``kind`` ("linear", "ntk", "yarn",
+    "wavelength") and its ``factor``, ``trained`` (length), ``fast``, ``slow``
+    (turns); see ``gbo_rope_scaling``.  ``frequencies``: radians per position,
+    instead of base and scaling.
+    """
+
+    def __init__(self, head_dim, rot_dim=None, offset=0, layout="half", base=10000.0, scaling=None, frequencies=None,
+                 magnitude=1.0):
+        self.head_dim = int(head_dim)
+        self.rot_dim = self.head_dim - int(offset) if rot_dim is None else int(rot_dim)
+        if layout not in LAYOUTS:
+            raise ValueError("layout must be one of %s" % ", ".join(sorted(LAYOUTS)))
+        if frequencies is not None:
+            if scaling is not None or len(frequencies) != self.rot_dim // 2:
+                raise ValueError("one frequency per pair, and no scaling beside them")
+            self._freq = (ctypes.c_double * max(1, len(frequencies)))(*[float(f) for f in frequencies])
+            self.magnitude = float(magnitude)
+        elif self.rot_dim == 0:
+            self._freq, self.magnitude = (ctypes.c_double * 1)(), 1.0
+        else:
+            s = None
+            if scaling is not None:
+                if scaling.get("kind") not in SCALINGS:
+                    raise ValueError("scaling kind must be one of %s" % ", ".join(sorted(SCALINGS)))
+                s = B.RopeScaling(SCALINGS[scaling["kind"]], 0, *(float(scaling.get(k, 0.0)) for k in
+                                                                  ("factor", "trained", "fast", "slow")))
+            self._freq, self.magnitude = B.gbo_rope_frequencies(self.rot_dim, base, s)
+        self.opts = B.RopeOpts(self.head_dim, self.rot_dim, int(offset), LAYOUTS[layout],
+                               ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double)), self.magnitude, 0.0)
+
+    @property
+    def frequencies(self):
+        return [self._freq[j] for j in range(self.rot_dim // 2)]
+
+    def with_eps(self, eps):
+        """The options with the norm's eps (the same frequencies)."""
+        o = self.opts
+        return B.RopeOpts(o.head_dim, o.rot_dim, o.offset, o.layout, o.freq, o.magnitude, float(eps))
+
+
+def _like(x):
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
+def rotary(x, positions, spec, *, inverse=False, out=None, stream=None):
+    """``x`` rotated (``inverse``: turned back, which is the rotation's gradient).
+    ``out`` may be ``x``."""
+    y = _like(x) if out is None else out
+    if inverse:
+        B.gbo_rope_backward([dict(dy=x, y=y)], spec.opts, positions, None, stream)
+    else:
+        B.gbo_rope_forward([dict(x=x, y=y)], spec.opts, positions, stream)
+    return y
+
+
+def qk_norm_rotary(q, k, q_gain, k_gain, positions, spec, *, eps=1e-6, stream=None):
+    """Queries and keys normed per head (root mean square, gain of head_dim float32
+    values or None) and rotated, in one launch."""
+    yq, yk = _like(q), _like(k)
+    B.gbo_rope_forward([dict(x=q, y=yq, gain=q_gain, norm=True), dict(x=k, y=yk, gain=k_gain, norm=True)],
+                       spec.with_eps(eps), positions, stream)
+    return yq, yk
+
+
+def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_gain, k_gain, positions, spec, *, eps=1e-6, stream=None):
+    """Gradients of :func:`qk_norm_rotary` by q, k and the gains (None where the gain is)."""
+    dq, dk = _like(q), _like(k)
+    dgq = torch.empty_like(q_gain) if q_gain is not None else None
+    dgk = torch.empty_like(k_gain) if k_gain is not None else None
+    table = [dict(x=q, dy=dq_out, y=dq, gain=q_gain, dgain=dgq, norm=True),
+             dict(x=k, dy=dk_out, y=dk, gain=k_gain, dgain=dgk, norm=True)]
+    opts = spec.with_eps(eps)
+    ws = torch.empty(max(16, B.gbo_rope_workspace_bytes(table, opts)), dtype=torch.uint8, device=q.device)
+    B.gbo_rope_backward(table, opts, positions, ws, stream)
+    return dq, dk, dgq, dgk
+
+
+def linear_cross_entropy(h, w, labels, *, z_loss=0.0, logit_scale=1.0, lse=None, totals=None, row_weight=None,
+                         dev_status=None, stream=None):
+    """Loss of each row of ``h`` (n x d, bf16) against ``labels`` under the classifier
+    ``w`` (v x d, bf16); rows with negative labels are left out (loss 0)."""
+    n, d = h.shape
+    loss = torch.empty(n, dtype=torch.float32, device=h.device)
+    ws = torch.empty(B.gbo_xent_workspace_bytes(n, w.shape[0], d), dtype=torch.uint8, device=h.device)
+    B.gbo_xent_forward(h, w, labels, ws, loss=loss, lse=lse, totals=totals, row_weight=row_weight,
+                       logit_scale=logit_scale, z_loss=z_loss, dev_status=dev_status, stream=stream)
+    return loss
+
+
+def linear_cross_entropy_grad(h, w, labels, *, z_loss=0.0, logit_scale=1.0, mean=True, row_weight=None, upstream=None,
+                              dh=None, dw=None, accumulate_dw=False, totals=None, workspace_cap=0, dev_status=None,
+                              stream=None):
+    """(losses, dh, dw): the losses of :func:`linear_cross_entropy` and the gradients
+    of their (weighted) mean, or sum with ``mean=False``, by ``h`` and ``w``, in one
+    call.  ``dh``, ``dw``: buffers to write (bf16 or float32; with ``accumulate_dw``
+    dw is added to).  ``workspace_cap``: bytes of scratch at most (more pieces of the
+    vocabulary)."""
+    n, d = h.shape
+    loss = torch.empty(n, dtype=torch.float32, device=h.device)
+    dh = _like(h) if dh is None else dh
+    dw = _like(w) if dw is None else dw
+    ws = torch.empty(B.gbo_xent_workspace_bytes(n, w.shape[0], d, True, workspace_cap), dtype=torch.uint8,
+                     device=h.device)
+    B.gbo_xent_grad(h, w, labels, ws, loss=loss, totals=totals, dh=dh, dw=dw, accumulate_dw=accumulate_dw,
+                    row_weight=row_weight, upstream=upstream, mean=mean, logit_scale=logit_scale, z_loss=z_loss,
+                    dev_status=dev_status, stream=stream)
+    return loss, dh, dw
+
+
+# ---------------------------------------------------------------------------
+# autograd
+
+def _rows(t):
+    """``t`` with consecutive last-axis elements (autograd hands over expanded gradients)."""
+    return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, positions, spec):
+        ctx.spec, ctx.positions = spec, positions
+        return rotary(x, positions, spec)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return rotary(_rows(dy), ctx.positions, ctx.spec, inverse=True), None, None
+
+
+class _QkNormRotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_gain, k_gain, positions, spec, eps):
+        ctx.save_for_backward(q, k, q_gain, k_gain)
+        ctx.rest = (positions, spec, eps)
+        return qk_norm_rotary(q, k, q_gain, k_gain, positions, spec, eps=eps)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        positions, spec, eps = ctx.rest
+        grads = qk_norm_rotary_backward(_rows(dq), _rows(dk), *ctx.saved_tensors, positions, spec, eps=eps)
+        return (*grads, None, None, None)
+
+
+class _LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, w, labels, row_weight, z_loss, logit_scale):
+        n, d = h.shape
+        lse = torch.empty(n, dtype=torch.float32, device=h.device)
+        totals = torch.empty(2, dtype=torch.float32, device=h.device)
+        linear_cross_entropy(h, w, labels, z_loss=z_loss, logit_scale=logit_scale, lse=lse, totals=totals,
+                             row_weight=row_weight)
+        ctx.save_for_backward(h, w, labels, row_weight, lse)
+        ctx.rest = (z_loss, logit_scale)
+        return torch.where(totals[1] != 0, totals[0] / totals[1], torch.zeros_like(totals[0]))
+
+    @staticmethod
+    def backward(ctx, up):
+        h, w, labels, row_weight, lse = ctx.saved_tensors
+        z_loss, logit_scale = ctx.rest
+        dh = _like(h) if ctx.needs_input_grad[0] else None
+        dw = _like(w) if ctx.needs_input_grad[1] else None
+        ws = torch.empty(B.gbo_xent_workspace_bytes(h.shape[0], w.shape[0], h.shape[1], True), dtype=torch.uint8,
+                         device=h.device)
+        B.gbo_xent_backward(h, w, labels, lse, ws, dh=dh, dw=dw, row_weight=row_weight,
+                            upstream=up.float().reshape(1), logit_scale=logit_scale, z_loss=z_loss)
+        return dh, dw, None, None, None, None
+
+
+def rotary_autograd(x, positions, spec):
+    """:func:`rotary` with its gradient."""
+    return _Rotary.apply(x, positions, spec)
+
+
+def qk_norm_rotary_autograd(q, k, q_gain, k_gain, positions, spec, eps=1e-6):
+    """:func:`qk_norm_rotary` with its gradients by q, k and the gains."""
+    return _QkNormRotary.apply(q, k, q_gain, k_gain, positions, spec, eps)
+
+
+def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_scale=1.0):
+    """Mean loss over the rows that count, with its gradients by ``h`` and ``w``."""
+    return _LinearCrossEntropy.apply(h, w, labels, row_weight, z_loss, logit_scale)

@@ -53,6 +53,7 @@ extern "C" {
 /* ---- device status bits (OR-ed into *dev_status) ---------------------- */
 #define GBO_STATUS_NONFINITE 1 /* a norm or a scale came out NaN or Inf             */
 #define GBO_STATUS_TIMEOUT 2   /* a bounded device-side wait gave up; outputs invalid */
+#define GBO_STATUS_BAD_LABEL 4 /* a label is not in the vocabulary (its row was left out) */
 
 /* ---- element types ------------------------------------------------------ */
 #define GBO_F32 0
@@ -332,6 +333,208 @@ typedef struct {
 int gbo_adamw_step(const gbo_adamw_desc *descs, int32_t n, const gbo_adamw_opts *opts,
                    const float *dev_coef, int32_t *dev_status, gbo_stream_t stream);
 
+/* ---- rotary positions and per-head q/k norms ------------------------------ */
+
+/*
+ * The gradients the AdamW path steps come from the model's forward and
+ * backward passes; the next two groups of entry points are the two places
+ * where the AdamW parameters of the OMN recipe other than the hidden norm
+ * gains enter them: the q/k norm gains of a block (with the rotation that
+ * follows them), and the tied embedding as the output classifier.  The
+ * source pages state the parameters (128 + 128 gains a block, one tied
+ * 128,256 x 2,048 table), not these passes; the formulas are the usual ones
+ * and are written out here.
+ *
+ * Rotation.  Of every head vector of head_dim elements, the rot_dim elements
+ * from `offset` on are rot_dim / 2 pairs; pair j at position t becomes
+ *   (a, b) -> magnitude * (a cos(t f_j) - b sin(t f_j), a sin(t f_j) + b cos(t f_j)),
+ * the other elements are copied.  Layouts: GBO_ROPE_HALF pairs elements j and
+ * j + rot_dim / 2 of the rotated part, GBO_ROPE_INTERLEAVED elements 2 j and
+ * 2 j + 1.
+ */
+#define GBO_ROPE_HALF 0
+#define GBO_ROPE_INTERLEAVED 1
+
+#define GBO_ROPE_MAX_HEAD_DIM 512
+#define GBO_ROPE_MAX_TENSORS 4
+
+/* element types of positions and labels */
+#define GBO_I32 16
+#define GBO_I64 17
+
+/* How frequencies are stretched for contexts longer than the trained one. */
+#define GBO_ROPE_SCALE_NONE 0       /* f_j = base^(-2 j / rot_dim)                                       */
+#define GBO_ROPE_SCALE_LINEAR 1     /* f_j / factor                                                       */
+#define GBO_ROPE_SCALE_NTK 2        /* the base becomes base * factor^(rot_dim / (rot_dim - 2))           */
+#define GBO_ROPE_SCALE_YARN 3       /* f_j below index low, f_j / factor above high, linear in j between,
+                                       where a frequency of index low (high) turns `fast` (`slow`) times
+                                       over the trained length (floor and ceiling, within 0 .. rot_dim - 1);
+                                       magnitude = 0.1 ln(factor) + 1                                     */
+#define GBO_ROPE_SCALE_WAVELENGTH 4 /* with n_j = trained f_j / 2 pi turns over the trained length: f_j
+                                       where n_j >= fast, f_j / factor where n_j <= slow, linear in n_j
+                                       between                                                            */
+typedef struct {
+  int32_t kind;     /* GBO_ROPE_SCALE_*                                            */
+  int32_t reserved; /* set to 0                                                    */
+  double factor;    /* > 0; the context's stretch (kinds other than NONE)          */
+  double trained;   /* > 0; trained length in positions (YARN, WAVELENGTH)         */
+  double fast;      /* turns, > slow (YARN, e.g. 32; WAVELENGTH, e.g. 4)           */
+  double slow;      /* turns, > 0 (YARN, e.g. 1; WAVELENGTH, e.g. 1)               */
+} gbo_rope_scaling;
+
+/*
+ * Frequencies of a rotation, in radians per position (host, no GPU).
+ *   scaling    NULL for GBO_ROPE_SCALE_NONE
+ *   freq       receives rot_dim / 2 values
+ *   magnitude  receives the factor on cosines and sines (1 except for YARN)
+ * Errors: INVALID_ARG, SHAPE (rot_dim odd, < 2 or > GBO_ROPE_MAX_HEAD_DIM).
+ */
+int gbo_rope_frequencies(int32_t rot_dim, double base, const gbo_rope_scaling *scaling, double *freq,
+                         double *magnitude);
+
+typedef struct {
+  int32_t head_dim;   /* 1 .. GBO_ROPE_MAX_HEAD_DIM                                    */
+  int32_t rot_dim;    /* even, 0 .. head_dim - offset (0: nothing is rotated)          */
+  int32_t offset;     /* first rotated element, >= 0                                   */
+  int32_t layout;     /* GBO_ROPE_HALF | GBO_ROPE_INTERLEAVED                          */
+  const double *freq; /* host: rot_dim / 2 finite frequencies in radians per position  */
+  float magnitude;    /* factor on cosines and sines                                   */
+  float eps;          /* of the norm, >= 0                                             */
+} gbo_rope_opts;
+
+/* One tensor of heads.  Strides are in elements, for the batch, the position
+ * and the head; the elements of a head are consecutive.  x, dy and y have the
+ * same dtype. */
+typedef struct {
+  const void *x;      /* forward: the input; backward: the forward's input (NULL without a norm) */
+  const void *dy;     /* backward: gradient of the forward's output; forward: NULL              */
+  void *y;            /* forward: the output; backward: the input's gradient.  May be x (forward)
+                         or dy (backward) with the same strides                                 */
+  const float *gain;  /* device, head_dim fp32: the norm's gain; NULL with norm = 1: ones       */
+  float *dgain;       /* backward: device, head_dim fp32, written; NULL: not wanted             */
+  int64_t x_stride[3];
+  int64_t dy_stride[3];
+  int64_t y_stride[3];
+  int32_t heads;      /* >= 0 */
+  int32_t dtype;      /* GBO_F32 | GBO_BF16 */
+  int32_t norm;       /* 1: x / sqrt(mean x^2 + eps) * gain before the rotation; 0: rotation alone */
+  int32_t reserved;   /* set to 0 */
+} gbo_rope_tensor;
+
+/* Positions of batch x seq tokens: entry (b, s) at element b * stride_b + s * stride_s. */
+typedef struct {
+  const void *ptr;   /* device, GBO_I32 or GBO_I64; NULL: position start + s        */
+  int64_t stride_b;  /* 0: the sequences share their positions                      */
+  int64_t stride_s;
+  int64_t start;     /* with ptr NULL                                               */
+  int32_t dtype;     /* GBO_I32 | GBO_I64                                           */
+  int32_t reserved;  /* set to 0                                                    */
+} gbo_rope_positions;
+
+/*
+ * Rotate up to GBO_ROPE_MAX_TENSORS tensors (queries and keys, say) of the
+ * same batch x seq tokens in one launch, each with its per-head norm before
+ * the rotation (norm = 1) or without:
+ *   y = R_t (x / sqrt(mean x^2 + eps) * gain).
+ * Arithmetic in fp32, rounded once.  The angle t f_j is reduced to a turn
+ * exactly for any 64-bit position (a fixed-point product modulo one turn),
+ * so long contexts lose no accuracy; negative positions turn backwards.
+ * Errors: INVALID_ARG, SHAPE, DTYPE, CUDA.
+ */
+int gbo_rope_forward(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *opts, int64_t batch,
+                     int64_t seq, const gbo_rope_positions *positions, gbo_stream_t stream);
+
+/*
+ * Gradients of gbo_rope_forward.  With e = R_t^T dy, r = sqrt(mean x^2 + eps):
+ *   norm = 0:  y = e
+ *   norm = 1:  y = (w - x mean(w x) / r^2) / r with w = gain e,
+ *              dgain_j = sum over tokens and heads of e_j x_j / r  (written, not added)
+ * The forward's input is read again; nothing else has to be kept.  dgain is
+ * summed in a fixed order in fp32.
+ *   workspace  device, >= gbo_rope_workspace_bytes(tensors, n, opts) bytes,
+ *              16-byte aligned; may be NULL when no dgain is wanted
+ * Errors: INVALID_ARG, SHAPE, DTYPE, WORKSPACE, CUDA.
+ */
+int gbo_rope_backward(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *opts, int64_t batch,
+                      int64_t seq, const gbo_rope_positions *positions, void *workspace, size_t ws_bytes,
+                      gbo_stream_t stream);
+size_t gbo_rope_workspace_bytes(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *opts);
+
+/* ---- softmax cross entropy of the tied classifier -------------------------- */
+
+/*
+ * Loss of a large-vocabulary classifier (the tied embedding as the output
+ * layer) and its gradients, without the n x v logits in memory.
+ *   l = logit_scale H W^T,  lse_i = log sum_j exp l_ij,
+ *   loss_i = lse_i - l_{i, y_i} + z_loss lse_i^2,
+ *   L = upstream * (sum_i w_i loss_i) / (mean ? sum_i w_i : 1).
+ * Row i is left out (loss and gradients 0, whatever stands in it) when its
+ * label is negative or its weight w_i is 0; a label >= v leaves the row out
+ * too and sets GBO_STATUS_BAD_LABEL.  With no row left, every output is 0.
+ * H, W are bf16 (an fp32 master table is cast by its owner, once per step);
+ * products accumulate in fp32, exponentials and sums are fp32.
+ */
+typedef struct {
+  const void *h;           /* device, bf16, n rows of d elements, h_stride apart               */
+  const void *w;           /* device, bf16, v rows of d elements, w_stride apart; 16-byte aligned */
+  const void *labels;      /* device, n, label_dtype                                           */
+  const float *row_weight; /* device, n, finite; NULL: 1                                       */
+  const float *upstream;   /* device scalar: gradient of the caller's objective by L; NULL: 1  */
+  int64_t n;               /* rows, >= 0                                                       */
+  int64_t v;               /* vocabulary, >= 1                                                 */
+  int64_t d;               /* a multiple of 8, >= 8                                            */
+  int64_t h_stride;        /* elements, >= d                                                   */
+  int64_t w_stride;        /* elements, >= d, a multiple of 8                                  */
+  float logit_scale;       /* 1 for plain logits                                               */
+  float z_loss;            /* 0 for none                                                       */
+  int32_t label_dtype;     /* GBO_I32 | GBO_I64                                                */
+  int32_t mean;            /* 1: divide by the sum of the weights of the rows that count       */
+} gbo_xent_args;
+
+typedef struct {
+  void *dh;              /* device, n x d gradient of L by H, or NULL                          */
+  void *dw;              /* device, v x d gradient of L by W, or NULL                          */
+  int64_t dh_stride;     /* elements, >= d                                                     */
+  int64_t dw_stride;     /* elements, >= d                                                     */
+  int32_t dh_dtype;      /* GBO_F32 | GBO_BF16                                                 */
+  int32_t dw_dtype;      /* GBO_F32 | GBO_BF16                                                 */
+  int32_t accumulate_dw; /* 1: add to dw (the table's other uses, or earlier micro-batches)    */
+  int32_t reserved;      /* set to 0                                                           */
+} gbo_xent_grads;
+
+/*
+ * Bytes of device workspace.  grad 0: gbo_xent_forward.  grad 1:
+ * gbo_xent_grad and gbo_xent_backward; these work through the vocabulary in
+ * pieces whose gradients of the logits (bf16) fit the workspace they are
+ * given: a larger workspace means fewer pieces.  cap > 0: the most that fits
+ * in `cap` bytes; 0: pieces of 2 GiB.  0 when the arguments are out of range
+ * or not even a piece of 256 columns fits the cap.
+ */
+size_t gbo_xent_workspace_bytes(int64_t n, int64_t v, int64_t d, int32_t grad, int64_t cap);
+
+/*
+ * Losses.
+ *   loss    device fp32, n, loss_i (not weighted), or NULL
+ *   lse     device fp32, n, or NULL (gbo_xent_backward reads it)
+ *   totals  device fp32, 2: sum of w_i loss_i and of w_i over the rows that
+ *           count, or NULL
+ *   workspace  device scratch, 256-byte aligned
+ * A loss that is not finite sets GBO_STATUS_NONFINITE.
+ * Errors: INVALID_ARG, SHAPE, DTYPE, WORKSPACE, CUDA.
+ */
+int gbo_xent_forward(const gbo_xent_args *args, float *loss, float *lse, float *totals, void *workspace,
+                     size_t ws_bytes, int32_t *dev_status, gbo_stream_t stream);
+
+/* Gradients of L from the forward's lse, written (dw: added with
+ * accumulate_dw), each rounded once to its dtype.  The gradient of the
+ * logits is rounded to bf16 between the products. */
+int gbo_xent_backward(const gbo_xent_args *args, const float *lse, const gbo_xent_grads *grads, void *workspace,
+                      size_t ws_bytes, int32_t *dev_status, gbo_stream_t stream);
+
+/* gbo_xent_forward and gbo_xent_backward in one call. */
+int gbo_xent_grad(const gbo_xent_args *args, float *loss, float *lse, float *totals, const gbo_xent_grads *grads,
+                  void *workspace, size_t ws_bytes, int32_t *dev_status, gbo_stream_t stream);
+
 /* ---- host-to-device transfer -------------------------------------------- */
 
 /*
@@ -372,7 +575,9 @@ int32_t gbo_abi_version(void);
 
 /* sizeof of an ABI struct, for binding checks: 0 gbo_muon_desc,
  * 1 gbo_muon_opts, 2 gbo_tensor, 3 gbo_adamw_desc, 4 gbo_adamw_opts,
- * 5 gbo_plan_info; 0 for other values. */
+ * 5 gbo_plan_info, 6 gbo_rope_scaling, 7 gbo_rope_opts, 8 gbo_rope_tensor,
+ * 9 gbo_rope_positions, 10 gbo_xent_args, 11 gbo_xent_grads; 0 for other
+ * values. */
 size_t gbo_struct_size(int32_t which);
 
 /* Number of kernels this library has launched in this process. */

@@ -1,0 +1,293 @@
+"""Cross entropy of the classifier and its gradients against the formulas in 64 bits.
+
+Tolerances.  A logit is a sum of d products of bf16 values (exact in fp32)
+accumulated in fp32: it is off by at most D = 2 d u sum_k |h_k w_k|, u =
+2^-24 (2: the tensor core's own order and rounding of partial sums).  Then
+lse is off by at most the largest D of its row plus the error of the
+exponentials and of their sum, at most 64 u (|lse| + 1), and so is the
+logit taken from it.  The gradient of a logit, P, is rounded to bf16, at most
+2^-8 of it, and inherits 2 (D + 64 u (|lse| + 1)) of its softmax part.
+The products accumulate K terms in fp32: 2 K u of the sum of the terms'
+sizes.  A bf16 output adds 2^-8 of its value, an fp32 one u."""
+
+import pytest
+import torch
+
+from adamw_optimizer_step_gb300 import _binding as B
+from adamw_optimizer_step_gb300 import layers
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from adamw_optimizer_step_gb300 import build
+    build.build()
+    B.lib()
+
+
+def inputs(n, v, d, seed, ignored=0.0, lean=6.0, dtype=torch.int64):
+    g = torch.Generator().manual_seed(seed)
+    W = torch.randn(v, d, generator=g) / d ** 0.5
+    y = torch.randint(0, v, (n,), generator=g)
+    H = torch.randn(n, d, generator=g) + lean * torch.rand(n, 1, generator=g) * W[y]
+    y = torch.where(torch.rand(n, generator=g) < ignored, torch.full_like(y, -100), y)
+    return H.to(torch.bfloat16).cuda(), W.to(torch.bfloat16).cuda(), y.to(dtype).cuda()
+
+
+class Want:
+    """Losses and gradients in 64 bits, with how far fp32 work may be off."""
+
+    def __init__(self, H, W, y, weight=None, z=0.0, scale=1.0, mean=True, upstream=1.0):
+        H, W, y = H.double().cpu(), W.double().cpu(), y.long().cpu()
+        n, d = H.shape
+        v = W.shape[0]
+        w = torch.ones(n, dtype=torch.float64) if weight is None else weight.double().cpu()
+        w = torch.where((y >= 0) & (y < v), w, torch.zeros_like(w))
+        use = w != 0
+        H = torch.where(use[:, None], H, torch.zeros_like(H))
+        at = y.clamp(0, v - 1)
+        L = scale * (H @ W.T)
+        D = 2 * d * U * abs(scale) * (H.abs() @ W.abs().T)
+        self.lse = torch.logsumexp(L, 1)
+        dl = D.max(1).values + 64 * U * (self.lse.abs() + 1)
+        rows = torch.arange(n)
+        self.loss = torch.where(use, self.lse - L[rows, at] + z * self.lse ** 2, torch.zeros(n).double())
+        self.loss_tol = dl + D[rows, at] + 64 * U * (self.lse.abs() + 1) + 2 * abs(z) * self.lse.abs() * dl
+        self.total, self.weight = (w * self.loss).sum(), w.sum()
+        self.total_tol = (w.abs() * (self.loss_tol + (n + 64) * U * self.loss.abs())).sum()
+        soft = torch.softmax(L, 1) * (1 + 2 * z * self.lse)[:, None]
+        hot = torch.zeros_like(L)
+        hot[rows, at] = 1.0
+        g = upstream / (self.weight if mean and use.any() else 1.0) * scale
+        P = w[:, None] * (soft - hot)
+        dP = 2.0 ** -8 * P.abs() + w.abs()[:, None] * soft.abs() * (2 * (D + dl[:, None]))
+        self.dh, self.dw = g * (P @ W), g * (P.T @ H)
+        self.dh_tol = abs(g) * (dP @ W.abs() + 2 * v * U * (P.abs() @ W.abs()))
+        self.dw_tol = abs(g) * (dP.T @ H.abs() + 2 * max(n, 1) * U * (P.abs().T @ H.abs()))
+        self.use = use
+
+
+def close(got, want, tol, dtype):
+    rounding = (2.0 ** -8 if dtype == torch.bfloat16 else 2 * U) * want.abs()
+    off = (got.double().cpu() - want).abs() - (tol * (1 + 2.0 ** -7) + rounding + 1e-30)
+    assert torch.isfinite(got).all() and off.max() <= 0, float(off.max())
+
+
+SHAPES = [(1, 1, 8), (1, 300, 64), (5, 257, 72), (130, 256, 128), (300, 1000, 64), (257, 2049, 136), (513, 130, 264),
+          (64, 5003, 512)]
+
+
+@pytest.mark.parametrize("n,v,d", SHAPES)
+def test_losses(n, v, d):
+    H, W, y = inputs(n, v, d, n + v, ignored=0.2 if n > 1 else 0.0)
+    lse, totals = torch.empty(n, device="cuda"), torch.empty(2, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss = layers.linear_cross_entropy(H, W, y, z_loss=1e-3, lse=lse, totals=totals, dev_status=status)
+    want = Want(H, W, y, z=1e-3)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(lse, torch.where(want.use, want.lse, torch.zeros_like(want.lse)), want.loss_tol, torch.float32)
+    close(totals[0], want.total, want.total_tol, torch.float32)
+    assert totals[1].item() == want.weight.item() and status.item() == 0
+
+
+@pytest.mark.parametrize("n,v,d", SHAPES)
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_gradients(n, v, d, out):
+    H, W, y = inputs(n, v, d, 3 * n + v, ignored=0.3 if n > 1 else 0.0, dtype=torch.int32)
+    dh, dw = (torch.full(t.shape, float("nan"), dtype=out, device="cuda") for t in (H, W))
+    loss, _, _ = layers.linear_cross_entropy_grad(H, W, y, z_loss=1e-3, dh=dh, dw=dw)
+    want = Want(H, W, y, z=1e-3)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(dh, want.dh, want.dh_tol, out)
+    close(dw, want.dw, want.dw_tol, out)
+
+
+def test_weights_scale_sum_and_upstream():
+    H, W, y = inputs(200, 700, 64, 11, ignored=0.1)
+    g = torch.Generator().manual_seed(1)
+    weight = torch.rand(200, generator=g).cuda() * 2
+    weight[::7] = 0  # left out, like a negative label
+    up = torch.tensor([0.37], device="cuda")
+    totals = torch.empty(2, device="cuda")
+    for mean in (True, False):
+        _, dh, dw = layers.linear_cross_entropy_grad(H, W, y, logit_scale=0.5, row_weight=weight, upstream=up,
+                                                     mean=mean, totals=totals)
+        want = Want(H, W, y, weight=weight, scale=0.5, mean=mean, upstream=0.37)
+        close(dh, want.dh, want.dh_tol, torch.bfloat16)
+        close(dw, want.dw, want.dw_tol, torch.bfloat16)
+        close(totals[0], want.total, want.total_tol, torch.float32)
+
+
+def test_pieces_of_the_vocabulary():
+    """Workspaces that hold 256 columns, some, and all of the vocabulary give the same
+    losses and dW bit for bit (each row of dW is one product), and dH within its tolerance."""
+    H, W, y = inputs(300, 3001, 128, 21)
+    want = Want(H, W, y)
+    full = layers.linear_cross_entropy_grad(H, W, y)
+    for tiles in (1, 3, 7):
+        cap = B.gbo_xent_workspace_bytes(300, 3001, 128, True) - 2 * 512 * (3072 - 256 * tiles)
+        loss, dh, dw = layers.linear_cross_entropy_grad(H, W, y, workspace_cap=cap + 4 * 512 * 128)
+        assert torch.equal(loss, full[0]) and torch.equal(dw, full[2])
+        close(dh, want.dh, want.dh_tol, torch.bfloat16)
+
+
+def test_accumulate_and_one_gradient_alone():
+    H, W, y = inputs(100, 600, 64, 31)
+    _, dh, dw = layers.linear_cross_entropy_grad(H, W, y, dw=torch.empty(600, 64, device="cuda"))
+    for dtype in (torch.float32, torch.bfloat16):
+        base = torch.randn(600, 64, device="cuda").to(dtype)
+        into = base.clone()
+        layers.linear_cross_entropy_grad(H, W, y, dw=into, accumulate_dw=True)
+        assert torch.equal(into, (base.float() + dw).to(dtype))
+    lse = torch.empty(100, device="cuda")
+    layers.linear_cross_entropy(H, W, y, lse=lse)
+    ws = torch.empty(B.gbo_xent_workspace_bytes(100, 600, 64, True), dtype=torch.uint8, device="cuda")
+    for which in ("dh", "dw"):
+        into = torch.empty_like(H if which == "dh" else W)
+        B.gbo_xent_backward(H, W, y, lse, ws, **{which: into})
+        # the row's lse in bits is rounded on its way through fp32: P may differ by a bf16 rounding
+        want = Want(H, W, y)
+        close(into, getattr(want, which), getattr(want, which + "_tol"), torch.bfloat16)
+
+
+def test_rows_left_out():
+    """Rows that are left out hold NaN and infinities: nothing of them reaches
+    a loss or a gradient.  A label outside the vocabulary is one of them, and is told."""
+    H, W, y = inputs(300, 500, 64, 41, ignored=0.4)
+    out = y < 0
+    H[out] = float("nan")
+    H[torch.nonzero(out)[0]] = float("inf")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss, dh, dw = layers.linear_cross_entropy_grad(H, W, y, dev_status=status)
+    want = Want(torch.where(out[:, None], torch.zeros_like(H), H), W, y)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(dh, want.dh, want.dh_tol, torch.bfloat16)
+    close(dw, want.dw, want.dw_tol, torch.bfloat16)
+    assert torch.all(loss[out] == 0) and torch.all(dh[out] == 0) and status.item() == 0
+    y2 = y.clone()
+    y2[out] = 500
+    loss2, dh2, dw2 = layers.linear_cross_entropy_grad(H, W, y2, dev_status=status)
+    assert torch.equal(loss2, loss) and torch.equal(dh2, dh) and torch.equal(dw2, dw)
+    assert status.item() == B.GBO_STATUS_BAD_LABEL
+
+
+def test_no_row_counts():
+    H, W, y = inputs(300, 500, 64, 43)
+    y.fill_(-1)
+    totals = torch.full((2,), 7.0, device="cuda")
+    loss, dh, dw = layers.linear_cross_entropy_grad(H, W, y, totals=totals)
+    assert torch.all(loss == 0) and torch.all(dh == 0) and torch.all(dw == 0) and torch.all(totals == 0)
+    base = torch.randn(500, 64, device="cuda")
+    into = base.clone()
+    layers.linear_cross_entropy_grad(H, W, y, dw=into, accumulate_dw=True)
+    assert torch.equal(into, base)
+    # no rows at all
+    loss, dh, dw = layers.linear_cross_entropy_grad(H[:0], W, y[:0])
+    assert loss.shape == (0,) and dh.shape == (0, 64) and torch.all(dw == 0)
+    assert layers.linear_cross_entropy(H[:0], W, y[:0]).shape == (0,)
+
+
+def test_large_logits():
+    """Logits in the hundreds: one softmax entry takes all, others vanish."""
+    H, W, y = inputs(64, 700, 64, 47, lean=0.0)
+    H, W = H * 30, W * 4
+    loss, dh, dw = layers.linear_cross_entropy_grad(H, W, y)
+    want = Want(H, W, y)
+    assert want.loss.max() > 200
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(dh, want.dh, want.dh_tol, torch.bfloat16)
+    close(dw, want.dw, want.dw_tol, torch.bfloat16)
+
+
+def test_not_finite_is_told():
+    H, W, y = inputs(40, 300, 64, 49)
+    H[3, 5] = float("nan")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss = layers.linear_cross_entropy(H, W, y, dev_status=status)
+    assert status.item() == B.GBO_STATUS_NONFINITE and torch.isnan(loss[3])
+    loss[3] = 0
+    assert torch.isfinite(loss).all()
+
+
+def test_strided_and_misaligned_rows():
+    """H and the gradients as slices of wider buffers, H off its 16-byte boundary: the same bits."""
+    H, W, y = inputs(130, 400, 72, 51)
+    loss, dh, dw = layers.linear_cross_entropy_grad(H, W, y)
+    wide = torch.zeros(130, 101, dtype=torch.bfloat16, device="cuda")
+    wide[:, 5:77] = H
+    Wide = torch.zeros(400, 88, dtype=torch.bfloat16, device="cuda")
+    Wide[:, 8:80] = W
+    oh = torch.zeros(130, 75, dtype=torch.bfloat16, device="cuda")
+    ow = torch.zeros(400, 99, dtype=torch.bfloat16, device="cuda")
+    got = layers.linear_cross_entropy_grad(wide[:, 5:77], Wide[:, 8:80], y, dh=oh[:, 3:75], dw=ow[:, 1:73])
+    assert torch.equal(got[0], loss) and torch.equal(oh[:, 3:75], dh) and torch.equal(ow[:, 1:73], dw)
+    assert torch.all(oh[:, :3] == 0) and torch.all(ow[:, 73:] == 0) and torch.all(ow[:, 0] == 0)
+
+
+def test_gradient_against_differences():
+    """Directional differences of the 64-bit loss match the gradients' inner products,
+    within the gradients' tolerance."""
+    H, W, y = inputs(24, 90, 32, 53)
+    want = Want(H, W, y, z=1e-3)
+    dh, dw = torch.empty(24, 32, device="cuda"), torch.empty(90, 32, device="cuda")
+    layers.linear_cross_entropy_grad(H, W, y, z_loss=1e-3, dh=dh, dw=dw)
+    g = torch.Generator().manual_seed(2)
+    a, b = torch.randn(24, 32, generator=g).double(), torch.randn(90, 32, generator=g).double()
+
+    def objective(t):
+        L = (H.double().cpu() + t * a) @ (W.double().cpu() + t * b).T
+        lse = torch.logsumexp(L, 1)
+        return (lse - L[torch.arange(24), y.cpu()] + 1e-3 * lse ** 2).mean()
+
+    h = 1e-5
+    num = (objective(h) - objective(-h)) / (2 * h)
+    got = (dh.double().cpu() * a).sum() + (dw.double().cpu() * b).sum()
+    tol = (want.dh_tol * a.abs()).sum() + (want.dw_tol * b.abs()).sum() + 1e-7
+    assert abs(num - got) <= tol
+
+
+def test_autograd_matches_the_call():
+    H, W, y = inputs(96, 333, 64, 57, ignored=0.1)
+    Hg, Wg = H.clone().requires_grad_(), W.clone().requires_grad_()
+    loss = layers.linear_cross_entropy_loss(Hg, Wg, y, z_loss=1e-3)
+    (3.0 * loss).backward()
+    want = Want(H, W, y, z=1e-3, upstream=3.0)
+    close(loss.detach(), want.total / want.weight, want.total_tol / want.weight, torch.float32)
+    close(Hg.grad, want.dh, want.dh_tol, torch.bfloat16)
+    close(Wg.grad, want.dw, want.dw_tol, torch.bfloat16)
+
+
+def test_repeatable_on_a_stream_and_in_a_graph():
+    H, W, y = inputs(700, 1500, 136, 59, ignored=0.2)
+    first = layers.linear_cross_entropy_grad(H, W, y)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        second = layers.linear_cross_entropy_grad(H, W, y)
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(first, second):
+        assert torch.equal(a, b)
+    loss, dh, dw = (torch.empty_like(t) for t in first)
+    ws = torch.empty(B.gbo_xent_workspace_bytes(700, 1500, 136, True), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.gbo_xent_grad(H, W, y, ws, loss=loss, dh=dh, dw=dw)
+    y[:100] = -1  # fewer rows count in the replay than in the capture
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip((loss, dh, dw), layers.linear_cross_entropy_grad(H, W, y)):
+        assert torch.equal(a, b)
+
+
+def test_large_tile_sweep():
+    """More than one sweep of 8192 rows, several pieces, against the 64-bit formula."""
+    H, W, y = inputs(8500, 1030, 72, 61, ignored=0.01)
+    want = Want(H, W, y)
+    loss, dh, dw = layers.linear_cross_entropy_grad(H, W, y)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(dh, want.dh, want.dh_tol, torch.bfloat16)
+    close(dw, want.dw, want.dw_tol, torch.bfloat16)
