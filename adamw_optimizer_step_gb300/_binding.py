@@ -7,7 +7,9 @@ All arithmetic runs in the library's CUDA kernels; there is no fallback.
 """
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -156,11 +158,11 @@ def lib():
                                      c_void_p, c_void_p]),
         "gbo_rope_frequencies": (c_int32, [c_int32, ctypes.c_double, ctypes.POINTER(RopeScaling),
                                            ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
-        "gbo_rope_workspace_bytes": (c_size_t, [ctypes.POINTER(RopeTensor), c_int32, ctypes.POINTER(RopeOpts)]),
-        "gbo_rope_forward": (c_int32, [ctypes.POINTER(RopeTensor), c_int32, ctypes.POINTER(RopeOpts), c_int64,
-                                       c_int64, ctypes.POINTER(RopePositions), c_void_p]),
-        "gbo_rope_backward": (c_int32, [ctypes.POINTER(RopeTensor), c_int32, ctypes.POINTER(RopeOpts), c_int64,
-                                        c_int64, ctypes.POINTER(RopePositions), c_void_p, c_size_t, c_void_p]),
+        "gbo_rope_workspace_bytes": (c_size_t, [c_void_p, c_int32, ctypes.POINTER(RopeOpts)]),
+        "gbo_rope_forward": (c_int32, [c_void_p, c_int32, ctypes.POINTER(RopeOpts), c_int64, c_int64, c_void_p,
+                                       c_void_p]),
+        "gbo_rope_backward": (c_int32, [c_void_p, c_int32, ctypes.POINTER(RopeOpts), c_int64, c_int64, c_void_p,
+                                        c_void_p, c_size_t, c_void_p]),
         "gbo_xent_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int64]),
         "gbo_xent_forward": (c_int32, [ctypes.POINTER(XentArgs), c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                        c_void_p, c_void_p]),
@@ -223,9 +225,20 @@ def _dev_ptr(t, what, allow_host=False):
     return t.data_ptr()
 
 
+def _current_stream():
+    """Torch's current stream on the current device, as a handle."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+if not (hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice")):
+    # without torch's direct accessors: through a Stream object, a few microseconds slower
+    def _current_stream():  # noqa: F811
+        return torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -491,94 +504,99 @@ def gbo_rope_frequencies(rot_dim, base=10000.0, scaling=None):
     return freq, magnitude.value
 
 
-def _heads_of(t, what):
-    """Checks a (batch, seq, heads, dim) tensor whose head elements are consecutive."""
+# The tables of the rotary calls are packed by struct (the layouts of RopeTensor
+# and RopePositions): a call while answering takes microseconds on the GPU,
+# and filling ctypes fields one by one takes longer than that.
+_PACK_ROPE_TENSOR = struct.Struct("@5P9q4i").pack
+_PACK_ROPE_POSITIONS = struct.Struct("@P3q2i").pack
+_ZERO3 = (0, 0, 0)
+_ELEMENT = {torch.float32: GBO_F32, torch.bfloat16: GBO_BF16}
+_INDEX = {torch.int32: GBO_I32, torch.int64: GBO_I64}
+
+
+def _heads_of(t, what, like):
+    """Strides of a (batch, seq, heads, dim) tensor whose head elements are consecutive."""
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % what)
-    if t.dim() != 4:
-        raise ValueError("%s must be (batch, seq, heads, dim)" % what)
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError("x, dy and y differ in shape or dtype")
+    s = t.stride()
+    if s[3] != 1 and t.shape[3] > 1:
         raise ValueError("the elements of a head of %s must be consecutive" % what)
-    return t
+    return s[:3]
+
+
+def _rope_gain(t, what, dim):
+    if t is None:
+        return 0
+    if t.dtype != torch.float32 or t.numel() != dim:
+        raise ValueError("%s must be %d float32 values" % (what, dim))
+    return _dev_ptr(t, what)
 
 
 def _rope_table(tensors, opts, positions):
     """Marshal a list of dicts with ``x``, ``y`` (and ``dy``, ``gain``, ``dgain``,
-    ``norm``) into a table; returns it with the batch and the length."""
-    arr = (RopeTensor * max(1, len(tensors)))()
-    batch = seq = None
-    for d, e in zip(arr, tensors):
-        shape = None
-        for name, ptr, stride in (("x", "x", d.x_stride), ("dy", "dy", d.dy_stride), ("y", "y", d.y_stride)):
-            t = e.get(name)
-            if t is None:
-                continue
-            _heads_of(t, name)
-            if shape is None:
-                shape, dtype = t.shape, t.dtype
-            elif t.shape != shape or t.dtype != dtype:
-                raise ValueError("x, dy and y differ in shape or dtype")
-            setattr(d, ptr, t.data_ptr())
-            stride[0], stride[1], stride[2] = t.stride()[:3]
-        if shape is None or shape[3] != opts.head_dim:
-            raise ValueError("a head has %d elements, the tensor %s" % (opts.head_dim, shape))
-        if batch is None:
+    ``norm``) into a table; returns it with the batch, the length and the positions."""
+    dim = opts.head_dim
+    batch = seq = 0
+    table = b""
+    for n, e in enumerate(tensors):
+        y, get = e["y"], e.get
+        x, dy = get("x"), get("dy")
+        shape = y.shape
+        if len(shape) != 4 or shape[3] != dim:
+            raise ValueError("(batch, seq, heads, %d) is wanted, got %s" % (dim, tuple(shape)))
+        if n == 0:
             batch, seq = shape[0], shape[1]
-        elif (batch, seq) != (shape[0], shape[1]):
+        elif batch != shape[0] or seq != shape[1]:
             raise ValueError("the tensors of one call have the same batch and length")
-        d.heads = shape[2]
-        d.dtype = _dtype(e["y"])
-        d.norm = int(bool(e.get("norm", False)))
-        for name in ("gain", "dgain"):
-            t = e.get(name)
-            if t is not None:
-                if t.dtype != torch.float32 or t.numel() != opts.head_dim:
-                    raise ValueError("%s must be %d float32 values" % (name, opts.head_dim))
-                setattr(d, name, _dev_ptr(t, name))
-    pos = RopePositions()
+        if y.dtype not in _ELEMENT:
+            raise TypeError("tensor dtype must be float32 or bfloat16, got %s" % y.dtype)
+        table += _PACK_ROPE_TENSOR(
+            0 if x is None else x.data_ptr(), 0 if dy is None else dy.data_ptr(), y.data_ptr(),
+            _rope_gain(get("gain"), "gain", dim), _rope_gain(get("dgain"), "dgain", dim),
+            *(_ZERO3 if x is None else _heads_of(x, "x", y)), *(_ZERO3 if dy is None else _heads_of(dy, "dy", y)),
+            *_heads_of(y, "y", y), shape[2], _ELEMENT[y.dtype], 1 if get("norm") else 0, 0)
     if isinstance(positions, int):
-        pos.start = positions
-    else:
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise TypeError("positions must be int32 or int64")
-        if not positions.is_cuda:
-            raise ValueError("positions must be a CUDA tensor")
-        p = positions if positions.dim() == 2 else positions.unsqueeze(0)
-        if p.dim() != 2 or p.shape[1] != seq or p.shape[0] not in (1, batch):
-            raise ValueError("positions must be (seq,), (1, seq) or (batch, seq)")
-        pos.ptr = p.data_ptr()
-        pos.stride_b = p.stride(0) if p.shape[0] == batch else 0
-        pos.stride_s = p.stride(1)
-        pos.dtype = GBO_I64 if p.dtype == torch.int64 else GBO_I32
-    return arr, batch or 0, seq or 0, pos
+        return table, batch, seq, _PACK_ROPE_POSITIONS(0, 0, 0, positions, GBO_I64, 0)
+    index = _INDEX.get(positions.dtype)
+    if index is None:
+        raise TypeError("positions must be int32 or int64")
+    if not positions.is_cuda:
+        raise ValueError("positions must be a CUDA tensor")
+    shape, stride = positions.shape, positions.stride()
+    if len(shape) == 1:
+        shape, stride = (1, shape[0]), (0, stride[0])
+    if len(shape) != 2 or shape[1] != seq or (shape[0] != 1 and shape[0] != batch):
+        raise ValueError("positions must be (seq,), (1, seq) or (batch, seq)")
+    return table, batch, seq, _PACK_ROPE_POSITIONS(positions.data_ptr(), stride[0] if shape[0] == batch else 0,
+                                                   stride[1], 0, index, 0)
 
 
 def gbo_rope_forward(tensors, opts, positions, stream=None):
     """Rotate tensors (dicts with ``x``, ``y`` of (batch, seq, heads, dim), and
     ``norm``, ``gain``) in one launch.  ``positions``: an integer tensor (seq,)
     or (batch, seq), or the first position."""
-    arr, batch, seq, pos = _rope_table(tensors, opts, positions)
-    _check(lib().gbo_rope_forward(arr, len(tensors), ctypes.byref(opts), batch, seq, ctypes.byref(pos),
-                                  _stream(stream)))
+    table, batch, seq, pos = _rope_table(tensors, opts, positions)
+    _check(lib().gbo_rope_forward(table, len(tensors), ctypes.byref(opts), batch, seq, pos, _stream(stream)))
 
 
 def gbo_rope_workspace_bytes(tensors, opts):
-    arr = (RopeTensor * max(1, len(tensors)))()
-    for d, e in zip(arr, tensors):
-        d.heads = e["dy"].shape[2]
-        d.dgain = None if e.get("dgain") is None else 4
-    return int(lib().gbo_rope_workspace_bytes(arr, len(tensors), ctypes.byref(opts)))
+    table = b"".join(_PACK_ROPE_TENSOR(0, 0, 0, 0, 0 if e.get("dgain") is None else 4, *_ZERO3, *_ZERO3, *_ZERO3,
+                                       e["dy"].shape[2], 0, 1, 0) for e in tensors)
+    return int(lib().gbo_rope_workspace_bytes(table, len(tensors), ctypes.byref(opts)))
 
 
 def gbo_rope_backward(tensors, opts, positions, workspace=None, stream=None):
     """Gradients: dicts with ``dy``, ``y`` (receives the input's gradient) and,
     with a norm, ``x``, ``gain`` and ``dgain``."""
-    arr, batch, seq, pos = _rope_table(tensors, opts, positions)
+    table, batch, seq, pos = _rope_table(tensors, opts, positions)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().gbo_rope_backward(arr, len(tensors), ctypes.byref(opts), batch, seq, ctypes.byref(pos),
+    _check(lib().gbo_rope_backward(table, len(tensors), ctypes.byref(opts), batch, seq, pos,
                                    _dev_ptr(workspace, "workspace"), nbytes, _stream(stream)))
 
 
+@functools.lru_cache(maxsize=256)
 def gbo_xent_workspace_bytes(n, v, d, grad=False, cap=0):
     return int(lib().gbo_xent_workspace_bytes(int(n), int(v), int(d), int(bool(grad)), int(cap)))
 

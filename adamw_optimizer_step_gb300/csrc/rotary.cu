@@ -7,12 +7,18 @@
 //             dgain_j = sum e_j u_j
 // Bound: HBM.  Each element is read once and written once (backward: x and
 // dy read, dx written); a head's norm stays in registers and warp shuffles.
+// Measured on 32768 tokens x 20 heads of 128 in bf16: forward 57 us, 5.9 TB/s
+// (87% of a copy); backward 96 us, 5.2 TB/s; 32768 x 32 heads of 192 with 64
+// rotated and no norm: 120 us, 6.7 TB/s.  What carried the forward there from
+// 88 us: the asynchronous ring (heads in flight without registers), two fp32
+// lanes per instruction, hardware sines for bf16, 32-bit index division.  The
+// backward's 111 registers leave 16 warps an SM; at 80 (24 warps) it spills
+// and measured 127 us.
 //
-// Work split.  A head is cut into units of two chunks: the two halves of a
-// run of pairs (GBO_ROPE_HALF: 16 bytes at j and 16 at j + rot / 2), two
-// consecutive chunks (GBO_ROPE_INTERLEAVED), or two chunks that are only
-// copied.  A unit's pairs are thus in one thread, and no rotation crosses
-// lanes.  A group of G lanes (a power of two) holds one head, one unit each
+// Work split.  A head is cut into units of two 16-byte chunks: the two halves
+// of a run of pairs (GBO_ROPE_HALF), two chunks of whole pairs
+// (GBO_ROPE_INTERLEAVED), or two chunks that are only copied.  A unit's pairs
+// are thus in one thread, and no rotation crosses lanes.  A group of G lanes (a power of two) holds one head, one unit each
 // (two for long fp32 heads); it walks over several heads of one token, so the
 // cosines and sines of the token are computed once for them.  Shapes whose
 // chunks are not 16-byte aligned take the same kernel with one-element
@@ -28,6 +34,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
 
 #include "device_common.cuh"
 #include "gbo.h"
@@ -38,7 +45,13 @@ namespace gbo {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBackBlocks = 4;  // backward: resident blocks per SM that share out the tokens
+// Backward: blocks per SM that share out the tokens (each leaves one row of
+// partial gain gradients).  2 are resident; 2 / 6 / 12 measured 96.8 / 95.8 /
+// 100.9 us on 32768 tokens x 20 heads of 128 in bf16.
+constexpr int kRopeBackBlocks = 6;
+// Heads a group walks over at most: 2 / 4 / 8 / 16 measured 111 / 67 / 57 / 58
+// us forward on the same tokens.
+constexpr int kMaxHeads = 8;
 
 struct RopeTensor {
   const void *x, *dy;
@@ -63,65 +76,107 @@ struct RopeParams {
   int32_t units, group;
 };
 
-template <typename T, int CH>
-struct Chunk;  // CH consecutive elements as fp32
+// Two fp32 values that are computed together (one instruction on sm_100 and up).
+__device__ __forceinline__ uint64_t bits2(float2 a) { return *reinterpret_cast<uint64_t *>(&a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 twice(float a) { return make_float2(a, a); }
 
+// A unit's two chunks of CH elements each, as CH pairs of fp32: the elements
+// in order (first chunk, then second).
+template <typename T, int CH>
+struct Chunks {  // CH = 1
+  static __device__ __forceinline__ void load(const T *a, const T *b, float2 *v) {
+    v[0] = make_float2(a ? (float)*a : 0.f, b ? (float)*b : 0.f);
+  }
+  static __device__ __forceinline__ void store(T *p, const float2 *v, int which) { *p = (T)(which ? v[0].y : v[0].x); }
+};
 template <>
-struct Chunk<__nv_bfloat16, 8> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *v) {
-    const uint4 raw = *reinterpret_cast<const uint4 *>(p);
+struct Chunks<__nv_bfloat16, 8> {
+  static __device__ __forceinline__ void unpack(uint4 raw, float2 *o) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
+    for (int h = 0; h < 4; ++h) o[h] = make_float2(__uint_as_float(w[h] << 16), __uint_as_float(w[h] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float2 *v, int which) {
+    uint32_t w[4];
+#pragma unroll
     for (int h = 0; h < 4; ++h) {
-      v[2 * h] = __uint_as_float(w[h] << 16);
-      v[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
+      const __nv_bfloat162 q = __float22bfloat162_rn(v[4 * which + h]);
+      w[h] = *reinterpret_cast<const uint32_t *>(&q);
     }
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) { store8(p, v, 8, true); }
-};
-template <>
-struct Chunk<float, 4> {
-  static __device__ __forceinline__ void load(const float *p, float *v) {
-    const float4 f = *reinterpret_cast<const float4 *>(p);
-    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-  }
-  static __device__ __forceinline__ void store(float *p, const float *v) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <>
-struct Chunk<__nv_bfloat16, 1> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *v) { v[0] = __bfloat162float(*p); }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) { *p = __float2bfloat16_rn(v[0]); }
-};
-template <>
-struct Chunk<float, 1> {
-  static __device__ __forceinline__ void load(const float *p, float *v) { v[0] = *p; }
-  static __device__ __forceinline__ void store(float *p, const float *v) { *p = v[0]; }
+struct Chunks<float, 4> {
+  static __device__ __forceinline__ void unpack(uint4 raw, float2 *o) {
+    o[0] = make_float2(__uint_as_float(raw.x), __uint_as_float(raw.y));
+    o[1] = make_float2(__uint_as_float(raw.z), __uint_as_float(raw.w));
+  }
+  static __device__ __forceinline__ void store(float *p, const float2 *v, int which) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[2 * which].x, v[2 * which].y, v[2 * which + 1].x, v[2 * which + 1].y);
+  }
 };
 
-// Element offsets of a unit's two chunks within the head (-1: no such chunk)
-// and its first pair (-1: copied, not rotated).
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Cosine and sine of a 32-bit fraction of a turn (signed).  For bf16 outputs
+// the hardware's approximation is enough: its error, 2^-21 for arguments
+// within half a turn, is 2^-12 of the output's rounding.
+template <typename T>
+__device__ __forceinline__ void turn_of(int32_t top, float &c, float &s) {
+  const float half_turns = (float)top * 4.656612873077393e-10f;  // 2^-31
+  if constexpr (sizeof(T) == 2) {
+    __sincosf(half_turns * 3.14159265358979f, &s, &c);
+  } else {
+    sincospif(half_turns, &s, &c);
+  }
+}
+
+// A unit: element offsets of its two chunks within the head (-1: no such
+// chunk), and the first pairs of its first and second CH / 2 pairs (-1:
+// copied, not rotated).  The second chunks lie half the rotated part (half
+// the copied chunks) behind the first, so that consecutive lanes read and
+// write consecutive chunks; interleaved pairs are whole within a chunk.
 struct Unit {
-  int a, b, pair0;
+  int a, b, pair0, pair1;
 };
 
 template <int CH>
 __device__ __forceinline__ Unit unit_of(const RopeParams &P, int u) {
-  Unit r = {-1, -1, -1};
+  Unit r = {-1, -1, -1, -1};
   const int rot_units = P.rot / (2 * CH);
   if (u >= P.units) return r;
   if (u < rot_units) {
-    r.pair0 = u * CH;
-    r.a = P.offset + (P.interleaved ? 2 * CH * u : CH * u);
-    r.b = P.interleaved ? r.a + CH : r.a + P.rot / 2;
+    if (CH == 1) {
+      r.pair0 = u;
+      r.a = P.offset + (P.interleaved ? 2 * u : u);
+      r.b = P.interleaved ? r.a + 1 : r.a + P.rot / 2;
+      return r;
+    }
+    r.a = P.offset + CH * u;
+    r.b = r.a + P.rot / 2;
+    r.pair0 = P.interleaved ? CH / 2 * u : CH * u;
+    r.pair1 = P.interleaved ? P.rot / 4 + CH / 2 * u : CH * u + CH / 2;
     return r;
   }
   // copied chunks in order: before the rotated part, then behind it
-  const int rest = (P.dim - P.rot) / CH, before = P.offset / CH;
-  const int c = 2 * (u - rot_units);
-  r.a = c < before ? c * CH : P.rot + c * CH;
-  if (c + 1 < rest) r.b = c + 1 < before ? (c + 1) * CH : P.rot + (c + 1) * CH;
+  const int rest = (P.dim - P.rot) / CH, before = P.offset / CH, half = (rest + 1) / 2;
+  auto at = [&](int c) { return c < before ? c * CH : P.rot + c * CH; };
+  const int c = u - rot_units;
+  r.a = at(c);
+  if (c + half < rest) r.b = at(c + half);
   return r;
 }
 
@@ -130,172 +185,287 @@ __device__ __forceinline__ float group_sum(float v, int group) {
   return v;
 }
 
-// Rotate the unit's pairs in place; sign = -1 turns backwards.
+// Rotate the unit's CH pairs in place (copied units have c = 1, s = 0).  c
+// and s are in the order of the pairs, two and two.  With one-element
+// chunks both layouts are one (a, b).
 template <int CH>
-__device__ __forceinline__ void rotate(float *v, const float *c, const float *s, bool interleaved, float sign) {
-  if (interleaved) {
+__device__ __forceinline__ void rotate(float2 *v, const float2 *c, const float2 *s, bool interleaved) {
+  if (CH == 1 || interleaved) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const float a = v[2 * i], b = v[2 * i + 1], si = sign * s[i];
-      v[2 * i] = a * c[i] - b * si;
-      v[2 * i + 1] = a * si + b * c[i];
+    for (int i = 0; i < CH; ++i) {  // (a, b) c + (b, a) (-s, s)
+      const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
+      v[i] = fma2(make_float2(v[i].y, v[i].x), make_float2(-si, si), mul2(v[i], twice(ci)));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const float a = v[i], b = v[CH + i], si = sign * s[i];
-      v[i] = a * c[i] - b * si;
-      v[CH + i] = a * si + b * c[i];
+    for (int i = 0; i < CH / 2; ++i) {
+      const float2 a = v[i], b = v[CH / 2 + i];
+      v[i] = fma2(make_float2(-b.x, -b.y), s[i], mul2(a, c[i]));
+      v[CH / 2 + i] = fma2(b, c[i], mul2(a, s[i]));
     }
   }
 }
 
-// UPL: units per lane.  kBack: gradients.
-template <typename T, int CH, int UPL, bool kBack>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams P) {
+constexpr int ring_depth(int ch, bool back) { return ch == 1 ? 0 : back ? 3 : 4; }
+// Bytes of a block's ring: per head in flight, x and / or dy, UPL units of two 16-byte chunks a thread.
+constexpr int ring_bytes(int ch, int upl, bool norm, bool back) {
+  return ring_depth(ch, back) * (norm && back ? 2 : 1) * upl * 2 * 16 * kRopeThreads;
+}
+
+// UPL: units per lane.  kNorm: with the per-head norm.  kBack: gradients.
+// kNorm wants the group to be a power of two (its sums are butterflies);
+// without it a group is exactly the head's units.
+//
+// Heads on their way in are 16-byte asynchronous copies into a ring of
+// shared memory in which every thread has slots of its own, so no thread
+// waits for another and the loads in flight take no registers: kDepth heads a
+// thread (three while gradients, which read two tensors).
+template <typename T, int CH, int UPL, bool kNorm, bool kBack>
+__global__ void __launch_bounds__(kRopeThreads, CH == 1 || UPL > 1 ? 1 : kNorm && kBack ? 2 : 4) rope_kernel(const __grid_constant__ RopeParams P) {
   pdl_launch();
-  constexpr int E = 2 * CH;  // elements of a unit
+  constexpr bool kGrad = kNorm && kBack;
+  constexpr bool kUseX = kNorm || !kBack;
+  constexpr int kDepth = ring_depth(CH, kBack);
+  constexpr int kIn = kGrad ? 2 : 1;           // tensors read
+  constexpr int H2 = (CH + 1) / 2;             // CH cosines, two and two
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ uint64_t turns[GBO_ROPE_MAX_HEAD_DIM / 2];
-  __shared__ float gain_s[GBO_ROPE_MAX_HEAD_DIM];
-  __shared__ float dg_s[kBack ? GBO_ROPE_MAX_HEAD_DIM : 1];
+  __shared__ __align__(16) float gain_s[kGrad ? GBO_ROPE_MAX_HEAD_DIM : 4];
+  __shared__ float dg_s[kGrad ? GBO_ROPE_MAX_HEAD_DIM : 1];
   int ti = 0;
   while (ti + 1 < P.n && (int)blockIdx.x >= P.t[ti + 1].block0) ++ti;
   const RopeTensor &X = P.t[ti];
   for (int i = threadIdx.x; i < P.rot / 2; i += kRopeThreads) turns[i] = P.turns[i];
-  pdl_wait();
-  if (X.norm)
-    for (int i = threadIdx.x; i < P.dim; i += kRopeThreads) gain_s[i] = X.gain ? X.gain[i] : 1.f;
-  __syncthreads();
-  const int G = P.group, lane_g = threadIdx.x & (G - 1);
-  const int groups = kRopeThreads / G, g = threadIdx.x / G;
+  const int G = P.group, g = threadIdx.x / G, lane_g = threadIdx.x - g * G;
+  const int groups = kRopeThreads / G;
   Unit unit[UPL];
 #pragma unroll
-  for (int k = 0; k < UPL; ++k) unit[k] = unit_of<CH>(P, lane_g + k * G);
-  float dg[kBack ? UPL : 1][kBack ? E : 1];
-  if constexpr (kBack) {
+  for (int k = 0; k < UPL; ++k) {
+    unit[k] = unit_of<CH>(P, lane_g + k * G);
+    if (!kNorm && g >= groups) unit[k] = {-1, -1, -1, -1};  // the block's last threads, too few for a group
+  }
+  const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+  constexpr uint32_t kPiece = kRopeThreads * 16;
+  auto slot = [&](int d, int in, int k, int which) { return slot0 + (uint32_t)(((d * kIn + in) * UPL + k) * 2 + which) * kPiece; };
+  if constexpr (kDepth > 0) {  // chunks that a unit lacks stay zero
+#pragma unroll
+    for (int p = 0; p < kDepth * kIn * UPL * 2; ++p)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot0 + p * kPiece), "r"(0) : "memory");
+  }
+  pdl_wait();
+  // the lane's gains: in registers, or, in the backward pass, which needs
+  // those for its sums, in shared memory
+  auto gain_at = [&](int k, int i) {  // element i of the unit's 2 CH
+    const int at = i < CH ? unit[k].a : unit[k].b;
+    return at >= 0 && X.gain ? X.gain[at + (i < CH ? i : i - CH)] : 1.f;
+  };
+  float2 gain_r[kNorm && !kBack ? UPL : 1][CH], dg[kGrad ? UPL : 1][CH];
+  if constexpr (kNorm && !kBack) {
 #pragma unroll
     for (int k = 0; k < UPL; ++k)
 #pragma unroll
-      for (int i = 0; i < E; ++i) dg[k][i] = 0.f;
+      for (int i = 0; i < CH; ++i) gain_r[k][i] = make_float2(gain_at(k, 2 * i), gain_at(k, 2 * i + 1));
   }
-  const float sign = kBack ? -1.f : 1.f;
+  if constexpr (kGrad) {
+    for (int i = threadIdx.x; i < P.dim; i += kRopeThreads) gain_s[i] = X.gain ? X.gain[i] : 1.f;
+#pragma unroll
+    for (int k = 0; k < UPL; ++k)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) dg[k][i] = make_float2(0.f, 0.f);
+  }
+  __syncthreads();
   const bool inter = P.interleaved != 0;
   // every group of a warp runs the same number of rounds (shuffles are warp-wide)
   const int64_t first = (int64_t)((int)blockIdx.x - X.block0) * groups;
   for (int64_t i0 = first; i0 < X.items; i0 += (int64_t)X.nblk * groups) {
-    const bool live = i0 + g < X.items;
+    const bool live = g < groups && i0 + g < X.items;
     const int64_t item = live ? i0 + g : X.items - 1;
-    const int64_t tok = item / X.head_blocks;
+    int64_t tok, b;
+    if (X.items <= 0x7fffffff) {  // 32-bit division: a third of the instructions
+      tok = (uint32_t)item / (uint32_t)X.head_blocks;
+      b = (uint32_t)tok / (uint32_t)min(P.seq, (int64_t)0x7fffffff);
+    } else {
+      tok = item / X.head_blocks;
+      b = tok / P.seq;
+    }
     const int h0 = (int)(item - tok * X.head_blocks) * X.per_item;
-    const int64_t b = tok / P.seq, s = tok - b * P.seq;
+    const int64_t s = tok - b * P.seq;
+    // heads of this item (0: the group has none); groups with fewer heads
+    // than the others go through the rounds all the same, and store nothing
+    const int nh = live ? min(X.per_item, X.heads - h0) : 0;
+    const T *x = reinterpret_cast<const T *>(X.x) + b * X.xs[0] + s * X.xs[1] + h0 * X.xs[2];
+    const T *dy = reinterpret_cast<const T *>(X.dy) + b * X.ds[0] + s * X.ds[1] + h0 * X.ds[2];
+    T *y = reinterpret_cast<T *>(X.y) + b * X.ys[0] + s * X.ys[1] + h0 * X.ys[2];
+    auto request = [&](int d, bool there) {  // the next head's copies, into slots d
+      if (there) {
+#pragma unroll
+        for (int k = 0; k < UPL; ++k) {
+          if constexpr (kUseX) {
+            if (unit[k].a >= 0) copy16_async(slot(d, 0, k, 0), x + unit[k].a);
+            if (unit[k].b >= 0) copy16_async(slot(d, 0, k, 1), x + unit[k].b);
+          }
+          if constexpr (kBack) {
+            if (unit[k].a >= 0) copy16_async(slot(d, kIn - 1, k, 0), dy + unit[k].a);
+            if (unit[k].b >= 0) copy16_async(slot(d, kIn - 1, k, 1), dy + unit[k].b);
+          }
+        }
+        if constexpr (kUseX) x += X.xs[2];
+        if constexpr (kBack) dy += X.ds[2];
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (kDepth > 0) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) request(d, d < nh);
+    }
     int64_t t;
     if (!P.pos) t = P.start + s;
     else if (P.pos64) t = reinterpret_cast<const int64_t *>(P.pos)[b * P.pos_b + s * P.pos_s];
     else t = reinterpret_cast<const int32_t *>(P.pos)[b * P.pos_b + s * P.pos_s];
-    float c[UPL][CH], sn[UPL][CH];
+    float2 c[UPL][H2], sn[UPL][H2];
 #pragma unroll
     for (int k = 0; k < UPL; ++k)
-      if (unit[k].pair0 >= 0) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int32_t top = (int32_t)((uint64_t)t * turns[unit[k].pair0 + i] >> 32);
-          sincospif((float)top * 4.656612873077393e-10f, &sn[k][i], &c[k][i]);  // 2^-31: in half turns
-          sn[k][i] *= P.magnitude;
-          c[k][i] *= P.magnitude;
+      for (int i = 0; i < CH; ++i) {
+        float ci = 1.f, si = 0.f;
+        if (unit[k].pair0 >= 0) {
+          turn_of<T>((int32_t)((uint64_t)t * turns[i < CH / 2 || CH == 1 ? unit[k].pair0 + i : unit[k].pair1 + i - CH / 2] >> 32), ci, si);
+          ci *= P.magnitude;
+          si *= kBack ? -P.magnitude : P.magnitude;
         }
+        if (i & 1) c[k][i / 2].y = ci, sn[k][i / 2].y = si;
+        else c[k][i / 2].x = ci, sn[k][i / 2].x = si;
       }
-    const T *x = reinterpret_cast<const T *>(X.x) + b * X.xs[0] + s * X.xs[1];
-    const T *dy = reinterpret_cast<const T *>(X.dy) + b * X.ds[0] + s * X.ds[1];
-    T *y = reinterpret_cast<T *>(X.y) + b * X.ys[0] + s * X.ys[1];
-    const bool need_x = !kBack || X.norm;
+    int d = 0;
     for (int hh = 0; hh < X.per_item; ++hh) {
-      const int h = min(h0 + hh, X.heads - 1);  // past the last head: compute it again, store nothing
-      const bool store = live && h0 + hh < X.heads;
-      float v[UPL][E], e[kBack ? UPL : 1][kBack ? E : 1];
+      const bool store = hh < nh;
+      float2 v[kUseX ? UPL : 1][CH], e[kBack ? UPL : 1][CH];
+      if constexpr (kDepth > 0) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+        auto take = [&](uint32_t from, float2 *o) {
+          uint4 raw;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w) : "r"(from) : "memory");
+          Chunks<T, CH>::unpack(raw, o);
+        };
 #pragma unroll
-      for (int k = 0; k < UPL; ++k) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) v[k][i] = 0.f;
-        if (need_x) {
-          if (unit[k].a >= 0) Chunk<T, CH>::load(x + h * X.xs[2] + unit[k].a, v[k]);
-          if (unit[k].b >= 0) Chunk<T, CH>::load(x + h * X.xs[2] + unit[k].b, v[k] + CH);
+        for (int k = 0; k < UPL; ++k) {
+          if constexpr (kUseX) take(slot(d, 0, k, 0), v[k]), take(slot(d, 0, k, 1), v[k] + CH / 2);
+          if constexpr (kBack) take(slot(d, kIn - 1, k, 0), e[k]), take(slot(d, kIn - 1, k, 1), e[k] + CH / 2);
         }
-        if constexpr (kBack) {
+      } else {
 #pragma unroll
-          for (int i = 0; i < E; ++i) e[k][i] = 0.f;
-          if (unit[k].a >= 0) Chunk<T, CH>::load(dy + h * X.ds[2] + unit[k].a, e[k]);
-          if (unit[k].b >= 0) Chunk<T, CH>::load(dy + h * X.ds[2] + unit[k].b, e[k] + CH);
-          if (unit[k].pair0 >= 0) rotate<CH>(e[k], c[k], sn[k], inter, sign);
+        for (int k = 0; k < UPL; ++k) {
+          const bool ha = unit[k].a >= 0 && store, hb = unit[k].b >= 0 && store;
+          if constexpr (kUseX) Chunks<T, CH>::load(ha ? x + unit[k].a : nullptr, hb ? x + unit[k].b : nullptr, v[k]);
+          if constexpr (kBack) Chunks<T, CH>::load(ha ? dy + unit[k].a : nullptr, hb ? dy + unit[k].b : nullptr, e[k]);
         }
+        if constexpr (kUseX) x += X.xs[2];
+        if constexpr (kBack) dy += X.ds[2];
       }
-      float rho = 1.f;
-      if (X.norm) {
-        float ss = 0.f;
+      if constexpr (kBack) {
+#pragma unroll
+        for (int k = 0; k < UPL; ++k) rotate<CH>(e[k], c[k], sn[k], inter);
+      }
+      if constexpr (kNorm && !kBack) {
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < UPL; ++k)
 #pragma unroll
-          for (int i = 0; i < E; ++i) ss = fmaf(v[k][i], v[k][i], ss);
-        rho = rsqrtf(group_sum(ss, G) * P.inv_dim + P.eps);
+          for (int i = 0; i < CH; ++i) ss = fma2(v[k][i], v[k][i], ss);
+        const float rho = rsqrtf(group_sum(ss.x + ss.y, G) * P.inv_dim + P.eps);
+#pragma unroll
+        for (int k = 0; k < UPL; ++k)
+#pragma unroll
+          for (int i = 0; i < CH; ++i) v[k][i] = mul2(v[k][i], mul2(gain_r[k][i], twice(rho)));
       }
       if constexpr (!kBack) {
 #pragma unroll
-        for (int k = 0; k < UPL; ++k) {
-          if (X.norm) {
+        for (int k = 0; k < UPL; ++k) rotate<CH>(v[k], c[k], sn[k], inter);
+      }
+      if constexpr (kGrad) {
+        // both sums in one butterfly: sum x^2 and sum gain e x; then
+        // dgain += rho e x and dx = rho (gain e - x rho^2 mean(gain e x))
+        auto gains = [&](int k, float2 *o) {
+          if constexpr (CH >= 4) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-              const int at = i < CH ? unit[k].a + i : unit[k].b + i - CH;
-              v[k][i] *= rho * gain_s[max(at, 0)];
+            for (int i = 0; i < CH; i += 2) {  // two pairs, 16 bytes
+              // a chunk that the unit lacks reads the first gains (16-byte aligned, and unused)
+              const int at = 2 * i < CH ? max(0, unit[k].a) + 2 * i : max(0, unit[k].b) + 2 * i - CH;
+              const float4 q = *reinterpret_cast<const float4 *>(gain_s + at);
+              o[i] = make_float2(q.x, q.y), o[i + 1] = make_float2(q.z, q.w);
             }
+          } else {
+            o[0] = make_float2(gain_s[max(0, unit[k].a)], gain_s[max(0, unit[k].b)]);
           }
-          if (unit[k].pair0 >= 0) rotate<CH>(v[k], c[k], sn[k], inter, sign);
+        };
+        float2 ss = make_float2(0.f, 0.f), wx2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < UPL; ++k) {
+          float2 gain[CH];
+          gains(k, gain);
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            ss = fma2(v[k][i], v[k][i], ss);
+            wx2 = fma2(mul2(gain[i], e[k][i]), v[k][i], wx2);
+          }
         }
-      } else {
-        if (X.norm) {
-          float wx = 0.f;
-#pragma unroll
-          for (int k = 0; k < UPL; ++k)
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-              const int at = i < CH ? unit[k].a + i : unit[k].b + i - CH;
-              v[k][i] *= rho;  // u
-              if (store) dg[k][i] = fmaf(e[k][i], v[k][i], dg[k][i]);
-              e[k][i] *= gain_s[max(at, 0)];  // w
-              wx = fmaf(e[k][i], v[k][i], wx);
-            }
-          wx = group_sum(wx, G) * P.inv_dim;
-#pragma unroll
-          for (int k = 0; k < UPL; ++k)
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[k][i] = rho * (e[k][i] - v[k][i] * wx);
-        } else {
-#pragma unroll
-          for (int k = 0; k < UPL; ++k)
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[k][i] = e[k][i];
+        float s1 = ss.x + ss.y, s2 = wx2.x + wx2.y;
+        for (int o = G >> 1; o > 0; o >>= 1) {
+          s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+          s2 += __shfl_xor_sync(0xffffffffu, s2, o);
         }
+        const float rho = rsqrtf(s1 * P.inv_dim + P.eps), back = -rho * (rho * (s2 * P.inv_dim));
+#pragma unroll
+        for (int k = 0; k < UPL; ++k) {
+          float2 gain[CH];
+          gains(k, gain);
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            if (store) dg[k][i] = fma2(mul2(twice(rho), e[k][i]), v[k][i], dg[k][i]);
+            e[k][i] = mul2(twice(rho), fma2(v[k][i], twice(back), mul2(gain[i], e[k][i])));
+          }
+        }
+      }
+      // the slots have been read (the values above are computed from them):
+      // the head kDepth further may come in
+      if constexpr (kDepth > 0) {
+        request(d, hh + kDepth < nh);
+        if (++d == kDepth) d = 0;
       }
       if (store) {
 #pragma unroll
         for (int k = 0; k < UPL; ++k) {
-          if (unit[k].a >= 0) Chunk<T, CH>::store(y + h * X.ys[2] + unit[k].a, v[k]);
-          if (unit[k].b >= 0) Chunk<T, CH>::store(y + h * X.ys[2] + unit[k].b, v[k] + CH);
+          const float2 *o = kBack ? e[kBack ? k : 0] : v[kUseX ? k : 0];
+          if (unit[k].a >= 0) Chunks<T, CH>::store(y + unit[k].a, o, 0);
+          if (unit[k].b >= 0) Chunks<T, CH>::store(y + unit[k].b, o, 1);
         }
+        y += X.ys[2];
       }
     }
   }
-  if constexpr (kBack) {
+  if constexpr (kDepth > 0) asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (kGrad) {
     if (!X.part) return;
-    // the block's groups one after another, so that the order is fixed
+    // the groups of a warp by a butterfly, the warps one after another: a fixed order
     for (int i = threadIdx.x; i < P.dim; i += kRopeThreads) dg_s[i] = 0.f;
-    for (int q = 0; q < groups; ++q) {
+#pragma unroll
+    for (int k = 0; k < UPL; ++k)
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        for (int o = G; o < 32; o <<= 1) {
+          dg[k][i].x += __shfl_xor_sync(0xffffffffu, dg[k][i].x, o);
+          dg[k][i].y += __shfl_xor_sync(0xffffffffu, dg[k][i].y, o);
+        }
+    for (int q = 0; q < kRopeThreads / 32; ++q) {
       __syncthreads();
-      if (g == q) {
+      if ((int)(threadIdx.x >> 5) == q && (int)(threadIdx.x & 31) < G) {
 #pragma unroll
         for (int k = 0; k < UPL; ++k)
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
+          for (int i = 0; i < 2 * CH; ++i) {
             const int at = i < CH ? unit[k].a : unit[k].b;
-            if (at >= 0) dg_s[at + (i < CH ? i : i - CH)] += dg[k][i];
+            if (at >= 0) dg_s[at + (i < CH ? i : i - CH)] += i & 1 ? dg[k][i / 2].y : dg[k][i / 2].x;
           }
       }
     }
@@ -365,18 +535,33 @@ void back_blocks(const gbo_rope_tensor *t, int32_t n, int sm_count, int32_t *nbl
                   : (int32_t)std::max<int64_t>(1, (int64_t)kRopeBackBlocks * sm_count * t[i].heads / heads);
 }
 
+template <typename T, int CH, int UPL, bool kNorm, bool kBack>
+cudaError_t launch_rope_n(const RopeParams &P, int blocks, cudaStream_t stream) {
+  constexpr int smem = ring_bytes(CH, UPL, kNorm, kBack);
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(rope_kernel<T, CH, UPL, kNorm, kBack>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    smem);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  return launch_kernel(rope_kernel<T, CH, UPL, kNorm, kBack>, dim3(blocks), dim3(kRopeThreads), smem, stream, 1, P);
+}
+
 template <typename T, int CH, int UPL, bool kBack>
-cudaError_t launch_rope(const RopeParams &P, int blocks, cudaStream_t stream) {
-  return launch_kernel(rope_kernel<T, CH, UPL, kBack>, dim3(blocks), dim3(kRopeThreads), 0, stream, 1, P);
+cudaError_t launch_rope(const RopeParams &P, bool norm, int blocks, cudaStream_t stream) {
+  return norm ? launch_rope_n<T, CH, UPL, true, kBack>(P, blocks, stream)
+              : launch_rope_n<T, CH, UPL, false, kBack>(P, blocks, stream);
 }
 
 template <typename T, bool kBack>
-cudaError_t dispatch_rope(const RopeParams &P, int chunk, int upl, int blocks, cudaStream_t stream) {
+cudaError_t dispatch_rope(const RopeParams &P, int chunk, int upl, bool norm, int blocks, cudaStream_t stream) {
   constexpr int V = 16 / (int)sizeof(T);
-  if (chunk == 1) {
-    return upl <= 2 ? launch_rope<T, 1, 2, kBack>(P, blocks, stream) : launch_rope<T, 1, 8, kBack>(P, blocks, stream);
-  }
-  return upl == 1 ? launch_rope<T, V, 1, kBack>(P, blocks, stream) : launch_rope<T, V, 2, kBack>(P, blocks, stream);
+  if (chunk == 1)
+    return upl <= 2 ? launch_rope<T, 1, 2, kBack>(P, norm, blocks, stream)
+                    : launch_rope<T, 1, 8, kBack>(P, norm, blocks, stream);
+  return upl == 1 ? launch_rope<T, V, 1, kBack>(P, norm, blocks, stream)
+                  : launch_rope<T, V, 2, kBack>(P, norm, blocks, stream);
 }
 
 int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, int64_t batch, int64_t seq,
@@ -393,7 +578,7 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
     if (reinterpret_cast<uintptr_t>(pos->ptr) % (pos->dtype == GBO_I64 ? 8 : 4))
       return rope_fail(GBO_ERR_INVALID_ARG, "positions misaligned");
   }
-  bool any_dgain = false, chunks16 = true;
+  bool any_dgain = false, chunks16 = true, in_place = true;
   int32_t dtype = n > 0 ? tensors[0].dtype : GBO_BF16;
   const bool none = n == 0 || batch == 0 || seq == 0;
   for (int32_t i = 0; i < n; ++i) {
@@ -402,6 +587,7 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
     if (t.dtype != dtype) return rope_fail(GBO_ERR_DTYPE, "the tensors of one call have one dtype");
     if (t.heads < 0) return rope_fail(GBO_ERR_SHAPE, "negative number of heads");
     if (t.norm != 0 && t.norm != 1) return rope_fail(GBO_ERR_INVALID_ARG, "norm must be 0 or 1");
+    if (t.norm != tensors[0].norm) return rope_fail(GBO_ERR_INVALID_ARG, "the tensors of one call have a norm, or none has");
     if (!t.norm && (t.gain || t.dgain)) return rope_fail(GBO_ERR_INVALID_ARG, "a gain without a norm");
     if (!back && (t.dgain || t.dy)) return rope_fail(GBO_ERR_INVALID_ARG, "dy and dgain belong to the backward pass");
     if (!ptr_ok(t.gain, GBO_F32) || !ptr_ok(t.dgain, GBO_F32))
@@ -412,6 +598,8 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
     if (!t.y || (need_x && !t.x) || (back && !t.dy)) return rope_fail(GBO_ERR_INVALID_ARG, "NULL tensor pointer");
     if (!ptr_ok(t.x, dtype) || !ptr_ok(t.dy, dtype) || !ptr_ok(t.y, dtype))
       return rope_fail(GBO_ERR_INVALID_ARG, "misaligned tensor pointer");
+    const int64_t *from = back ? t.dy_stride : t.x_stride;
+    in_place = in_place && t.y == (back ? t.dy : t.x) && memcmp(from, t.y_stride, sizeof t.y_stride) == 0;
     // 16-byte chunks need 16-byte aligned heads
     const int V = dtype == GBO_BF16 ? 8 : 4;
     const void *ptrs[3] = {need_x ? t.x : nullptr, back ? t.dy : nullptr, t.y};
@@ -437,9 +625,17 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
   // a unit is two chunks: pairs have to fill whole units
   const bool vec = chunks16 && o->head_dim % V == 0 && o->offset % V == 0 && o->rot_dim % (2 * V) == 0;
   const int CH = vec ? V : 1;
-  P.units = o->rot_dim / (2 * CH) + ((o->head_dim - o->rot_dim) / CH + 1) / 2;
+  const bool norm = n > 0 && tensors[0].norm;
+  // without a norm and in place, the elements that are not rotated stay as they are
+  P.units = o->rot_dim / (2 * CH) + (norm || !in_place ? ((o->head_dim - o->rot_dim) / CH + 1) / 2 : 0);
+  if (P.units == 0) return report_ok();
+  // with a norm, a power of two within a warp and several units a lane
+  // beyond; without one, lanes of a block as they come
   P.group = 1;
-  while (P.group < 32 && P.group < P.units) P.group *= 2;
+  if (norm)
+    while (P.group < 32 && P.group < P.units) P.group *= 2;
+  else
+    P.group = std::min(P.units, kRopeThreads);
   const int upl = (P.units + P.group - 1) / P.group;
   P.dim = o->head_dim, P.rot = o->rot_dim, P.offset = o->offset;
   P.interleaved = o->layout == GBO_ROPE_INTERLEAVED;
@@ -461,10 +657,10 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
   if (back) back_blocks(tensors, n, sm, nblk);
   int64_t all_heads = 0;
   for (int32_t i = 0; i < n; ++i) all_heads += tensors[i].heads;
-  // heads a group walks over: up to 8 while the groups still fill the device
-  // (four 256-thread blocks an SM), so that a token's cosines are shared
+  // heads a group walks over: up to kMaxHeads while the groups still fill the
+  // device (four 256-thread blocks an SM), so that a token's cosines are shared
   int32_t per_item = 1;
-  while (per_item < 8 && tokens * all_heads / (2 * per_item) >= (int64_t)sm * 4 * groups) per_item *= 2;
+  while (per_item < kMaxHeads && tokens * all_heads / (2 * per_item) >= (int64_t)sm * 4 * groups) per_item *= 2;
   float *part = static_cast<float *>(workspace);
   RopeSum S;
   memset(&S, 0, sizeof S);
@@ -501,11 +697,11 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
   cudaError_t err = cudaSuccess;
   if (blocks > 0) {
     if (dtype == GBO_BF16)
-      err = back ? dispatch_rope<__nv_bfloat16, true>(P, CH, upl, (int)blocks, st)
-                 : dispatch_rope<__nv_bfloat16, false>(P, CH, upl, (int)blocks, st);
+      err = back ? dispatch_rope<__nv_bfloat16, true>(P, CH, upl, norm, (int)blocks, st)
+                 : dispatch_rope<__nv_bfloat16, false>(P, CH, upl, norm, (int)blocks, st);
     else
-      err = back ? dispatch_rope<float, true>(P, CH, upl, (int)blocks, st)
-                 : dispatch_rope<float, false>(P, CH, upl, (int)blocks, st);
+      err = back ? dispatch_rope<float, true>(P, CH, upl, norm, (int)blocks, st)
+                 : dispatch_rope<float, false>(P, CH, upl, norm, (int)blocks, st);
     count_launches(1);
   }
   if (err == cudaSuccess && any_dgain) {

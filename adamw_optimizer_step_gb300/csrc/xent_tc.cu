@@ -10,10 +10,16 @@
 //   rows    the rows that count (label >= 0, weight != 0) get consecutive
 //           places in their order, and H's rows are copied there: a batch
 //           whose prompts are left out costs what its answers cost, and what
-//           stands in a row that is left out (NaN, say) reaches nothing
+//           stands in a row that is left out (NaN, say) reaches nothing; the
+//           label's logit is summed here, in fp32 in a warp
 //   logits  tcgen05 GEMM over 256 x 256 tiles, whose epilogue leaves each
-//           row's maximum and sum of exponentials over the tile, and the
-//           label's logit (forward), or P in bf16 (backward)
+//           row's maximum and sum of exponentials over the tile (forward), or
+//           P in bf16 (backward).  It puts the label's logit of the first
+//           step in the place of its own: the tensor core cuts off the
+//           partial sums that it adds up (K / 16 of them), which moved a
+//           logit of 5 by 3e-5 at K = 2048, and a loss is lse minus exactly
+//           that logit (relative error of the losses at 128256 x 2048: 1.7e-6
+//           with the tile's logit, see the tests' bound)
 //   lse     joins the tiles' maxima and sums per row in a fixed order
 //   products dH += P W and dW = P^T H of one piece of the vocabulary in one
 //           launch, from the piece's P
@@ -82,9 +88,9 @@ struct XentParams {
   CUtensorMap mapA2, mapB2;  // products: P MN-major, H MN-major (dW)
   CUtensorMap mapO;          // P, 32 x 32 boxes
   const XentHead *head;
-  const int32_t *idx, *lab;  // place -> row, label; padded to a whole tile
+  const int32_t *idx, *lab;  // place -> row, label; up to a whole tile
   const float *wt, *lse2;    // weight (0: padding), lse in bits
-  float *ll2;                // forward: the label's logit in bits
+  const float *ll2;          // the label's logit in bits
   float2 *part;              // forward: (maximum, sum) per vocabulary tile and place
   float *dh_acc;             // fp32 sums over the pieces, places x d
   void *dh, *dw;
@@ -397,10 +403,10 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       const int c0 = it.tn * kTile;
       // per-row values of this tile, fetched while its products run
       int lab = -1;
-      float wt = 0.f, lse2 = 0.f;
+      float wt = 0.f, lse2 = 0.f, ll2 = 0.f;
       if constexpr (kMode != kModeProducts) {
         if (i < q.rows) {
-          lab = P.lab[i] - (int)P.v0;
+          lab = P.lab[i] - (int)P.v0, ll2 = P.ll2[i];
           if constexpr (kMode == kModeP) wt = P.wt[i], lse2 = P.lse2[i];
         }
       }
@@ -419,10 +425,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= P.scale2;
             if (lab >= col0 && lab < col0 + 32) {
-              float l = 0.f;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) l = lab == col0 + j ? v[j] : l;
-              P.ll2[i] = l;
+              for (int j = 0; j < 32; ++j) v[j] = lab == col0 + j ? ll2 : v[j];
             }
             if (col0 + 32 > P.v_piece) {
 #pragma unroll
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             if (lab >= col0 && lab < col0 + 32) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (lab == col0 + j) v[j] -= mult;
+                if (lab == col0 + j) v[j] = fmaf(peak, exp2_fast(ll2 - lse2), -mult);
             }
           } else {  // places behind the last row: their P multiplies zero rows of H, and must be finite
 #pragma unroll
@@ -544,118 +548,119 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
 // rows
 
 struct RowsParams {
+  const __nv_bfloat16 *h, *w;
   const void *labels;
   const float *row_weight, *upstream;
   const float *lse_in;   // backward alone: the forward's lse per row
   XentHead *head;
-  int32_t *place;        // row -> place, or -1
-  int32_t *idx, *lab;
-  float *wt, *lse2;
+  int32_t *idx, *lab;    // place -> row, label
+  float *wt, *lse2, *ll2;
+  __nv_bfloat16 *hc;     // H by places
+  float *loss, *lse;     // of rows left out: 0
+  void *dh;
   int32_t *status;
-  int64_t n, n_pad, v;
-  int32_t labels64, mean;
+  int64_t n, v, d, h_stride, w_stride, dh_stride;
+  int64_t per_block;     // rows a block takes, a multiple of 8
+  float scale2;
+  int32_t labels64, mean, dh_f32, vec;
 };
 
-__device__ __forceinline__ int64_t label_at(const RowsParams &R, int64_t i) {
-  return R.labels64 ? reinterpret_cast<const int64_t *>(R.labels)[i] : reinterpret_cast<const int32_t *>(R.labels)[i];
+__device__ __forceinline__ bool row_counts(const RowsParams &R, int64_t i, int64_t &y, float &w) {
+  y = R.labels64 ? reinterpret_cast<const int64_t *>(R.labels)[i] : reinterpret_cast<const int32_t *>(R.labels)[i];
+  w = R.row_weight ? R.row_weight[i] : 1.f;
+  return y >= 0 && y < R.v && w != 0.f;
 }
 
-// One block: places of the rows that count, in their order (a scan over
-// threads that each own a run of rows), the sum of their weights in a fixed
-// order, and the factor of the gradients.
-__global__ void __launch_bounds__(1024) xent_rows_kernel(const __grid_constant__ RowsParams R) {
+// Every block counts the rows that count, all and those before its own (n
+// labels from L2; cheaper than a launch of its own for the scan: 9 us at
+// n = 4096), then takes its rows eight at a time, one warp each: the row's
+// copy at its place, and its product with the label's row of W (8 products a
+// lane and step, in fp32).  Rows left out get zero losses and gradients.  The
+// rows n .. n + 255 stand for the places behind the last row up to a whole
+// tile: they get zeros.  Sums are taken in the same order by every block.
+__global__ void __launch_bounds__(256) xent_rows_kernel(const __grid_constant__ RowsParams R) {
   pdl_launch();
-  __shared__ int32_t cnt[32];
+  __shared__ int32_t cnt[2][8];
   __shared__ float red[32];
   pdl_wait();
-  const int64_t run = (R.n + 1023) / 1024, i0 = threadIdx.x * run, i1 = min(i0 + run, R.n);
-  int mine = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row0 = blockIdx.x * R.per_block;
+  int all = 0, before = 0;
   float wsum = 0.f;
   bool bad = false;
-  for (int64_t i = i0; i < i1; ++i) {
-    const int64_t y = label_at(R, i);
-    const float w = R.row_weight ? R.row_weight[i] : 1.f;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < R.n; i += 256) {
+    int64_t y;
+    float w;
+    if (row_counts(R, i, y, w)) {
+      ++all;
+      if (i < row0) ++before;
+      wsum += w;
+    }
     bad |= y >= R.v;
-    if (y >= 0 && y < R.v && w != 0.f) ++mine, wsum += w;
   }
-  if (bad) flag_status(R.status, GBO_STATUS_BAD_LABEL);
-  int at = mine;  // inclusive scan over the warp, then over the warps
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, at, o);
-    if (lane >= o) at += u;
-  }
-  if (lane == 31) cnt[warp] = at;
-  __syncthreads();
-  int before = 0, total = 0;
-  for (int w = 0; w < 32; ++w) {
-    if (w < warp) before += cnt[w];
-    total += cnt[w];
-  }
-  int place = before + at - mine;
-  for (int64_t i = i0; i < i1; ++i) {
-    const int64_t y = label_at(R, i);
-    const float w = R.row_weight ? R.row_weight[i] : 1.f;
-    const bool in = y >= 0 && y < R.v && w != 0.f;
-    R.place[i] = in ? place : -1;
-    if (!in) continue;
-    R.idx[place] = (int32_t)i;
-    R.lab[place] = (int32_t)y;
-    R.wt[place] = w;
-    if (R.lse_in) R.lse2[place] = R.lse_in[i] * kLog2e;
-    ++place;
-  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) cnt[0][warp] = all, cnt[1][warp] = before;
   const float ws = block_sum(wsum, red);
-  for (int64_t p = total + threadIdx.x; p < R.n_pad; p += 1024) R.idx[p] = 0, R.lab[p] = -1, R.wt[p] = 0.f, R.lse2[p] = 0.f;
-  if (threadIdx.x == 0) {
-    const float up = R.upstream ? *R.upstream : 1.f;
-    R.head->rows = total;
-    R.head->weight_sum = ws;
-    R.head->g = R.mean ? (total > 0 ? up / ws : 0.f) : up;
+  all = before = 0;
+  for (int k = 0; k < 8; ++k) all += cnt[0][k], before += cnt[1][k];
+  if (blockIdx.x == 0) {
+    if (bad) flag_status(R.status, GBO_STATUS_BAD_LABEL);
+    if (threadIdx.x == 0) {
+      const float up = R.upstream ? *R.upstream : 1.f;
+      R.head->rows = all;
+      R.head->weight_sum = ws;
+      R.head->g = R.mean ? (all > 0 ? up / ws : 0.f) : up;
+    }
   }
-}
-
-struct GatherParams {
-  const __nv_bfloat16 *h;
-  __nv_bfloat16 *hc;
-  const XentHead *head;
-  const int32_t *place;
-  float *loss, *lse;  // of rows left out: 0
-  void *dh;
-  int64_t n, n_pad, d, h_stride, dh_stride;
-  int32_t dh_f32, vec;
-};
-
-// One warp per row: its copy at its place; rows left out get zero losses and
-// gradients; the places behind the last row, up to a whole tile, zeros.
-__global__ void __launch_bounds__(256) xent_gather_kernel(const __grid_constant__ GatherParams G) {
-  pdl_launch();
-  const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  pdl_wait();
-  if (i >= G.n) {  // the tail
-    const int64_t p = G.head->rows + (i - G.n);
-    const int64_t end = ((int64_t)G.head->rows + kTile - 1) / kTile * kTile;
-    if (p >= end) return;
-    for (int64_t c = lane; c < G.d / 8; c += 32) reinterpret_cast<uint4 *>(G.hc + p * G.d)[c] = make_uint4(0, 0, 0, 0);
-    return;
+  const int64_t end = ((int64_t)all + kTile - 1) / kTile * kTile;
+  for (int64_t base = row0; base < min(row0 + R.per_block, R.n + kTile); base += 8) {
+    int64_t y = -1;
+    float w = 0.f;
+    const bool in8 = lane < 8 && base + lane < R.n && row_counts(R, base + lane, y, w);
+    const uint32_t mask = __ballot_sync(0xffffffffu, in8);
+    y = __shfl_sync(0xffffffffu, y, warp);
+    w = __shfl_sync(0xffffffffu, w, warp);
+    const int64_t i = base + warp;
+    const int64_t p = before + __popc(mask & ((1u << warp) - 1u));
+    before += __popc(mask);
+    if (mask >> warp & 1u) {
+      const __nv_bfloat16 *src = R.h + i * R.h_stride, *lab = R.w + y * R.w_stride;
+      __nv_bfloat16 *dst = R.hc + p * R.d;
+      float dot = 0.f;
+#pragma unroll 2
+      for (int64_t c = 8 * lane; c < R.d; c += 256) {
+        float a[8], b[8];
+        load8(src, GBO_BF16, c, 8, R.vec != 0, a);
+        load8(lab, GBO_BF16, c, 8, true, b);
+        store8(dst + c, a, 8, true);
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(a[k], b[k], s);
+        dot += s;
+      }
+      dot = warp_sum(dot);
+      if (lane == 0) {
+        R.idx[p] = (int32_t)i;
+        R.lab[p] = (int32_t)y;
+        R.wt[p] = w;
+        R.ll2[p] = dot * R.scale2;
+        if (R.lse_in) R.lse2[p] = R.lse_in[i] * kLog2e;
+      }
+    } else if (i < R.n) {
+      if (lane == 0) {
+        if (R.loss) R.loss[i] = 0.f;
+        if (R.lse) R.lse[i] = 0.f;
+      }
+      if (R.dh)
+        for (int64_t c = lane; c < R.d; c += 32) st_elem(R.dh, R.dh_f32 ? GBO_F32 : GBO_BF16, i * R.dh_stride + c, 0.f);
+    } else if (all + (i - R.n) < end) {
+      const int64_t t = all + (i - R.n);
+      for (int64_t c = lane; c < R.d / 8; c += 32) reinterpret_cast<uint4 *>(R.hc + t * R.d)[c] = make_uint4(0, 0, 0, 0);
+      if (lane == 0) R.idx[t] = 0, R.lab[t] = -1, R.wt[t] = 0.f, R.lse2[t] = 0.f, R.ll2[t] = 0.f;
+    }
   }
-  const int32_t p = G.place[i];
-  if (p >= 0) {
-    const __nv_bfloat16 *src = G.h + i * G.h_stride;
-    __nv_bfloat16 *dst = G.hc + p * G.d;
-    if (G.vec)
-      for (int64_t c = lane; c < G.d / 8; c += 32) reinterpret_cast<uint4 *>(dst)[c] = reinterpret_cast<const uint4 *>(src)[c];
-    else
-      for (int64_t c = lane; c < G.d; c += 32) dst[c] = src[c];
-    return;
-  }
-  if (lane == 0) {
-    if (G.loss) G.loss[i] = 0.f;
-    if (G.lse) G.lse[i] = 0.f;
-  }
-  if (G.dh)
-    for (int64_t c = lane; c < G.d; c += 32) st_elem(G.dh, G.dh_f32 ? GBO_F32 : GBO_BF16, i * G.dh_stride + c, 0.f);
 }
 
 struct LseParams {
@@ -748,7 +753,7 @@ int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // Scratch of a call, in this order.  The tiles' statistics and P share their
 // room: the statistics are done with before P is written.
 struct XentSpace {
-  int64_t head, place, idx, lab, wt, lse2, ll2, sums, hc, acc, big;  // byte offsets
+  int64_t head, idx, lab, wt, lse2, ll2, sums, hc, acc, big;  // byte offsets
   int64_t n_pad, bytes;
   int64_t piece;  // columns of a piece of the vocabulary
   int32_t pieces;
@@ -768,7 +773,6 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, int
     return r;
   };
   s.head = take(sizeof(XentHead));
-  s.place = take(4 * s.n_pad);
   s.idx = take(4 * s.n_pad);
   s.lab = take(4 * s.n_pad);
   s.wt = take(4 * s.n_pad);
@@ -916,43 +920,42 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
   cudaError_t e;
 
   RowsParams R = {};
+  R.h = static_cast<const __nv_bfloat16 *>(a->h), R.w = static_cast<const __nv_bfloat16 *>(a->w);
   R.labels = a->labels, R.row_weight = a->row_weight, R.upstream = a->upstream, R.lse_in = forward ? nullptr : lse_in;
   R.head = reinterpret_cast<XentHead *>(ws + S.head);
-  R.place = reinterpret_cast<int32_t *>(ws + S.place);
   R.idx = reinterpret_cast<int32_t *>(ws + S.idx);
   R.lab = reinterpret_cast<int32_t *>(ws + S.lab);
   R.wt = reinterpret_cast<float *>(ws + S.wt);
   R.lse2 = reinterpret_cast<float *>(ws + S.lse2);
+  R.ll2 = reinterpret_cast<float *>(ws + S.ll2);
+  R.hc = reinterpret_cast<__nv_bfloat16 *>(ws + S.hc);
+  R.loss = loss, R.lse = lse, R.dh = g ? g->dh : nullptr;
   R.status = status;
-  R.n = a->n, R.n_pad = S.n_pad, R.v = a->v;
+  R.n = a->n, R.v = a->v, R.d = a->d;
+  R.h_stride = a->h_stride, R.w_stride = a->w_stride, R.dh_stride = g ? g->dh_stride : 0;
+  R.scale2 = a->logit_scale * kLog2e;
   R.labels64 = a->label_dtype == GBO_I64, R.mean = a->mean;
-  if ((e = launch_kernel(xent_rows_kernel, dim3(1), dim3(1024), 0, st, 1, R)) != cudaSuccess) return cuda_err(e);
-  count_launches(1);
-
-  GatherParams G = {};
-  G.h = static_cast<const __nv_bfloat16 *>(a->h);
-  G.hc = reinterpret_cast<__nv_bfloat16 *>(ws + S.hc);
-  G.head = R.head, G.place = R.place, G.loss = loss, G.lse = lse;
-  G.dh = g ? g->dh : nullptr;
-  G.n = a->n, G.n_pad = S.n_pad, G.d = a->d, G.h_stride = a->h_stride, G.dh_stride = g ? g->dh_stride : 0;
-  G.dh_f32 = g && g->dh_dtype == GBO_F32;
-  G.vec = a->h_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a->h) & 15) == 0;
-  if ((e = launch_kernel(xent_gather_kernel, dim3((unsigned)((a->n + kTile + 7) / 8)), dim3(256), 0, st, 1, G)) !=
-      cudaSuccess)
+  R.dh_f32 = g && g->dh_dtype == GBO_F32;
+  R.vec = a->h_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a->h) & 15) == 0;
+  // eight blocks an SM at most: each reads all labels
+  const int64_t virt = a->n + kTile, most = (int64_t)8 * sm;
+  R.per_block = up_to((virt + most - 1) / most, 8);
+  if ((e = launch_kernel(xent_rows_kernel, dim3((unsigned)((virt + R.per_block - 1) / R.per_block)), dim3(256), 0, st, 1,
+                         R)) != cudaSuccess)
     return cuda_err(e);
   count_launches(1);
 
   XentParams P;
   memset(&P, 0, sizeof P);
   P.head = R.head, P.idx = R.idx, P.lab = R.lab, P.wt = R.wt, P.lse2 = R.lse2;
-  P.ll2 = reinterpret_cast<float *>(ws + S.ll2);
+  P.ll2 = R.ll2;
   P.status = status;
   P.d = (int32_t)a->d;
   P.scale = a->logit_scale, P.scale2 = a->logit_scale * kLog2e, P.z = a->z_loss;
   const int64_t m_tiles = S.n_pad / kTile, d_tiles = (a->d + kTile - 1) / kTile;
   bool maps = true;
   if (a->n > 0) {
-    maps = map_2d(&P.mapA, G.hc, a->d, S.n_pad, a->d, kBlockK, BM) &&
+    maps = map_2d(&P.mapA, R.hc, a->d, S.n_pad, a->d, kBlockK, BM) &&
            map_2d(&P.mapB, a->w, a->d, a->v, a->w_stride, kBlockK, BM);
     if (!maps) return xent_fail(GBO_ERR_CUDA, "tensor map of H or W");
   }
@@ -1003,7 +1006,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
              map_2d(&Q.mapA, pbuf, P.v_piece, S.n_pad, S.piece, kBlockK, BM) &&
              map_2d(&Q.mapB, a->w, a->d, a->v, a->w_stride, 64, kBlockK) &&
              map_2d(&Q.mapA2, pbuf, P.v_piece, S.n_pad, S.piece, 64, kBlockK) &&
-             map_2d(&Q.mapB2, G.hc, a->d, S.n_pad, a->d, 64, kBlockK);
+             map_2d(&Q.mapB2, R.hc, a->d, S.n_pad, a->d, 64, kBlockK);
       if (!maps) return xent_fail(GBO_ERR_CUDA, "tensor map of P");
       if (a->n > 0 && (e = launch_xent<kModeP>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) return cuda_err(e);
       const int64_t items = (P.dh ? m_tiles * d_tiles : 0) + (P.dw ? n_tiles * d_tiles : 0);

@@ -58,6 +58,7 @@ class RotarySpec:
             self._freq, self.magnitude = B.gbo_rope_frequencies(self.rot_dim, base, s)
         self.opts = B.RopeOpts(self.head_dim, self.rot_dim, int(offset), LAYOUTS[layout],
                                ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double)), self.magnitude, 0.0)
+        self._eps, self._scratch = {}, {}  # options by eps, scratch sizes by heads
 
     @property
     def frequencies(self):
@@ -65,12 +66,22 @@ class RotarySpec:
 
     def with_eps(self, eps):
         """The options with the norm's eps (the same frequencies)."""
-        o = self.opts
-        return B.RopeOpts(o.head_dim, o.rot_dim, o.offset, o.layout, o.freq, o.magnitude, float(eps))
+        o = self._eps.get(eps)
+        if o is None:
+            o = self.opts
+            o = self._eps[eps] = B.RopeOpts(o.head_dim, o.rot_dim, o.offset, o.layout, o.freq, o.magnitude, float(eps))
+        return o
+
+    def backward_workspace(self, table):
+        """Scratch bytes of the gains' gradients for a table's numbers of heads (and its device)."""
+        key = (table[0]["dy"].device, *(e["dy"].shape[2] if e["dgain"] is not None else 0 for e in table))
+        need = self._scratch.get(key)
+        if need is None:
+            need = self._scratch[key] = max(16, B.gbo_rope_workspace_bytes(table, self.opts))
+        return need
 
 
-def _like(x):
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+_like = torch.empty_like
 
 
 def rotary(x, positions, spec, *, inverse=False, out=None, stream=None):
@@ -101,7 +112,7 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_gain, k_gain, positions, spe
     table = [dict(x=q, dy=dq_out, y=dq, gain=q_gain, dgain=dgq, norm=True),
              dict(x=k, dy=dk_out, y=dk, gain=k_gain, dgain=dgk, norm=True)]
     opts = spec.with_eps(eps)
-    ws = torch.empty(max(16, B.gbo_rope_workspace_bytes(table, opts)), dtype=torch.uint8, device=q.device)
+    ws = torch.empty(spec.backward_workspace(table), dtype=torch.uint8, device=q.device)
     B.gbo_rope_backward(table, opts, positions, ws, stream)
     return dq, dk, dgq, dgk
 
