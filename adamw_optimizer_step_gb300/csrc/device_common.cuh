@@ -27,11 +27,11 @@ namespace gbo {
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" :::); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Launch `kernel` (with programmatic stream serialization when enabled, and,
+// Launch `kernel` (with programmatic stream serialization if `pdl`, and,
 // with cluster > 1, clusters of that many CTAs along x).
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                                 int cluster, Args &&...args) {
+inline cudaError_t launch_kernel_as(int32_t pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t stream, int cluster, Args &&...args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = grid;
@@ -40,7 +40,7 @@ inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block
   cfg.stream = stream;
   int n = 0;
   attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[n].val.programmaticStreamSerializationAllowed = pdl_enabled(stream);
+  attr[n].val.programmaticStreamSerializationAllowed = pdl;
   ++n;
   if (cluster > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
@@ -52,6 +52,12 @@ inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                 int cluster, Args &&...args) {
+  return launch_kernel_as(pdl_enabled(stream), kernel, grid, block, smem, stream, cluster, std::forward<Args>(args)...);
 }
 
 __device__ __forceinline__ float ld_elem(const void *base, int32_t dtype, int64_t idx) {

@@ -272,6 +272,9 @@ void count_launches(uint64_t n);
 // attribute (gbo_testing_set_pdl; by default only while the stream is being
 // captured into a CUDA graph).
 int32_t pdl_enabled(void *stream);
+// Whether the attribute is allowed at all (gbo_testing_set_pdl(0) forbids it):
+// for calls that carry it on direct launches too.
+int32_t pdl_allowed();
 
 // Error and device helpers of the host code, for entry points that live in
 // other files: record a message for gbo_last_error, clear it, and check

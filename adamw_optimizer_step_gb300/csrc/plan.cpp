@@ -31,6 +31,8 @@ static std::atomic<int32_t> g_fused_mom{0};    // see gbo_testing_set_fused_mome
 void count_launches(uint64_t n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 // see gbo_testing_set_pdl: 2 (the default) in CUDA graph capture only
 static std::atomic<int32_t> g_pdl{2};
+int32_t pdl_allowed() { return g_pdl.load(std::memory_order_relaxed) != 0; }
+
 int32_t pdl_enabled(void *stream) {
   const int32_t mode = g_pdl.load(std::memory_order_relaxed);
   if (mode != 2) return mode;

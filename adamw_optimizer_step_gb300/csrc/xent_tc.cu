@@ -24,8 +24,12 @@
 //   products dH += P W and dW = P^T H of one piece of the vocabulary in one
 //           launch, from the piece's P
 // The backward pass forms the logits again, piece by piece of the
-// vocabulary, so its scratch is one piece of P; P is rounded to bf16 once,
-// from the fp32 accumulator and the fp32 lse (the tensor cores take 16-bit
+// vocabulary, so its scratch is one piece of P.  Where the workspace has room
+// for the whole vocabulary's P, gbo_xent_grad keeps the logits there between
+// the passes instead, in 16 bits each (kKeepStep), which replaces one of the
+// four products by a pass over that room:
+//   convert P in place of the kept logits
+// P is rounded to bf16 once, from the fp32 lse (the tensor cores take 16-bit
 // operands: the same rounding as a bf16 gradient of the logits), and sums
 // over tokens and vocabulary are fp32.
 //
@@ -73,6 +77,16 @@ constexpr int kSweepTiles = 32;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Logits kept between the passes: (l - label's logit) in bits, in steps of
+// 2^-9, as 16-bit integers.  A step moves P by at most 2^-10 ln 2 = 2^-10.5 of
+// it (2^-11.4 root mean square), against 2^-8 (2^-9.3) of P's rounding to
+// bf16.  The range is 64 bits (44 nats) either way.  Entries below it are 2^-64
+// of the label's probability: taken as 0.  A row tile with an entry above
+// it, or one that is not finite, is marked and its P formed again from H
+// and W.
+constexpr float kKeepStep = 512.f;  // steps a bit
+constexpr float kKeepMost = 63.9f;  // bits
+
 enum XentMode { kModeStats = 0, kModeP = 1, kModeProducts = 2 };
 
 // Per-call scalars in the workspace.
@@ -80,7 +94,7 @@ struct XentHead {
   int32_t rows;      // rows that count
   float weight_sum;  // sum of their weights
   float g;           // factor of the gradients
-  int32_t pad;
+  int32_t redo;      // some tile's kept logits are out of their range (see kKeepStep)
 };
 
 struct XentParams {
@@ -92,13 +106,19 @@ struct XentParams {
   const float *wt, *lse2;    // weight (0: padding), lse in bits
   const float *ll2;          // the label's logit in bits
   float2 *part;              // forward: (maximum, sum) per vocabulary tile and place
-  float *dh_acc;             // fp32 sums over the pieces, places x d
+  float *dh_acc;             // fp32 sums of dH, `splits` times places x d
+  XentHead *head_out;        // forward with kept logits: where `redo` is set
+  int32_t *redo;             // per row tile: its kept logits are out of range
   void *dh, *dw;
   int32_t *status;
   int64_t part_ld;           // places per vocabulary tile in part
   int64_t dh_stride, dw_stride, v0;
   int32_t v_piece, d;        // columns of this piece
   int32_t dh_f32, dw_f32, dh_vec, dw_vec, dw_add, first_piece, last_piece;
+  int32_t splits, split_kit; // dH: cuts of its K axis (the piece's columns), stages in each
+  int32_t keep;              // forward: store the logits
+  int32_t only_redo;         // P: only the tiles of `redo`
+  int64_t acc_ld;            // elements of one split's dh_acc
   float scale2;              // logit scale in bits: s log2 e
   float scale, z;
 };
@@ -125,7 +145,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 struct XentItem {
-  int tm, tn, kit;
+  int tm, tn, kit, split;
   bool dw;
 };
 
@@ -141,13 +161,13 @@ struct XentPlan {
 template <int kMode>
 __device__ __forceinline__ XentPlan make_plan(const XentParams &P, int cid, int ncl) {
   XentPlan q;
-  q.rows = P.head->rows;
+  q.rows = kMode == kModeP && P.only_redo && !P.head->redo ? 0 : P.head->rows;
   q.m_tiles = (q.rows + kTile - 1) / kTile;
   q.n_tiles = (P.v_piece + kTile - 1) / kTile;
   q.d_tiles = (P.d + kTile - 1) / kTile;
-  q.dh_items = P.dh ? q.m_tiles * q.d_tiles : 0;
+  q.dh_items = P.dh ? q.m_tiles * q.d_tiles * P.splits : 0;
   q.dw_items = P.dw ? q.n_tiles * q.d_tiles : 0;
-  q.dh_kit = (P.v_piece + kStageK - 1) / kStageK;
+  q.dh_kit = P.splits > 1 ? P.split_kit : (P.v_piece + kStageK - 1) / kStageK;
   q.dw_kit = (q.rows + kStageK - 1) / kStageK;
   q.ncl = ncl;
   q.cid = cid;
@@ -159,7 +179,7 @@ __device__ __forceinline__ XentPlan make_plan(const XentParams &P, int cid, int 
 // Item k of this pair; false: there is none.
 //   logits: round-robin over the pairs; a sweep of kSweepTiles row tiles
 //     takes the vocabulary tile by tile.
-//   products: dH items (K = the piece's width) first, round-robin; `wide`
+//   products: dH items (K = the piece's width, or a cut of it) first, round-robin; `wide`
 //     pairs get one more than the others, who therefore take `extra` dW items
 //     (K = rows) of the same total length first; the rest of dW is dealt to
 //     all.  Items are independent, so the split changes no result.
@@ -181,9 +201,10 @@ __device__ __forceinline__ bool item_at(const XentPlan &q, const XentParams &P, 
     const int mine = q.dh_items / q.ncl + (q.cid < q.wide ? 1 : 0);
     if (k < mine) {
       const int t = q.cid + (int)k * q.ncl;
-      it.tm = t / q.d_tiles;
-      it.tn = t % q.d_tiles;
-      it.kit = q.dh_kit;
+      it.split = t % P.splits;
+      it.tn = t / P.splits % q.d_tiles;
+      it.tm = t / P.splits / q.d_tiles;
+      it.kit = max(0, min(q.dh_kit, (P.v_piece + kStageK - 1) / kStageK - it.split * q.dh_kit));
       it.dw = false;
       return true;
     }
@@ -214,10 +235,10 @@ struct Ring {
 };
 
 // Load one item's stages.  m0, n0: this CTA's first row of A and of B (their
-// columns when MN-major); k0: first row of B's K axis.  Only the leader arms
+// columns when MN-major); ka0, kb0: where K begins in A and B.  Only the leader arms
 // the barrier, for both CTAs' bytes.
 template <bool kAmn, bool kBmn>
-__device__ __forceinline__ bool produce(const CUtensorMap *ma, const CUtensorMap *mb, int m0, int n0, int kb0, int kit,
+__device__ __forceinline__ bool produce(const CUtensorMap *ma, const CUtensorMap *mb, int m0, int n0, int ka0, int kb0, int kit,
                                         uint32_t smem, uint32_t full0, uint32_t empty0, uint32_t full_lead0,
                                         bool leader, Ring &ring, uint32_t *armed_parity, uint32_t &armed,
                                         volatile int32_t *abort_flag) {
@@ -235,13 +256,13 @@ __device__ __forceinline__ bool produce(const CUtensorMap *ma, const CUtensorMap
       const uint32_t sa = smem + ring.stage * kStageBytes + sub * kSubBytes, sb = sa + kOpBytes;
       const int k = kb * kStageK + sub * kBlockK;
       if constexpr (!kAmn) {
-        tma_load_3d_pair(sa, ma, fb, k, m0, 0);
+        tma_load_3d_pair(sa, ma, fb, ka0 + k, m0, 0);
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) tma_load_3d_pair(sa + h * 8192, ma, fb, m0 + h * 64, k, 0);
+        for (int h = 0; h < 2; ++h) tma_load_3d_pair(sa + h * 8192, ma, fb, m0 + h * 64, ka0 + k, 0);
       }
       if constexpr (!kBmn) {
-        tma_load_3d_pair(sb, mb, fb, k, n0, 0);
+        tma_load_3d_pair(sb, mb, fb, kb0 + k, n0, 0);
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) tma_load_3d_pair(sb + h * 8192, mb, fb, n0 + h * 64, kb0 + k, 0);
@@ -288,6 +309,39 @@ __device__ __forceinline__ void softmax_add(const float (&t)[32], float &m, floa
   for (int k = 0; k < 32; ++k) a += exp2_fast(t[k] - at);
   s = fmaf(s, exp2_fast(m - at), a);
   m = mn;
+}
+
+// Store a warp's 32 x 32 block of logits (in bits) as 16-bit steps from the
+// row's label's logit, through the next of its two staging slots.  A float
+// of 1.5 2^23 plus an integer holds that integer in its low bits.
+__device__ __forceinline__ void keep_block(const CUtensorMap *map, uint32_t stage, int &slot, const float (&v)[32],
+                                           float ll2, int x0, int y0, int lane) {
+  const uint32_t dst = stage + (uint32_t)(slot * kSlotBytes);
+  slot ^= 1;
+  if (lane == 0) bulk_wait_read<1>();
+  __syncwarp();
+  uint32_t w[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    uint32_t h[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float steps = fminf(fmaxf((v[2 * k + e] - ll2) * kKeepStep, -32768.f), 32767.f);
+      h[e] = __float_as_uint(steps + 12582912.f);
+    }
+    w[k] = __byte_perm(h[0], h[1], 0x5410);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + sw64(lane, q)), "r"(w[4 * q]),
+                 "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                 : "memory");
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(map, dst, x0, y0, 0);
+    bulk_commit();
+  }
 }
 
 template <int kMode>
@@ -347,16 +401,18 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       uint32_t armed = 0, armed_parity[kStages] = {};
       XentItem it;
       for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
+        if (kMode == kModeP && P.only_redo && !P.redo[it.tm]) continue;
         const int m0 = it.tm * kTile + (int)crank * BM, n0 = it.tn * kTile + (int)crank * BM;
         bool ok;
         if constexpr (kMode != kModeProducts)
-          ok = produce<false, false>(&P.mapA, &P.mapB, m0, (int)P.v0 + n0, 0, it.kit, ring0, full0, empty0, full_lead0,
-                                     leader, ring, armed_parity, armed, abort_flag);
+          ok = produce<false, false>(&P.mapA, &P.mapB, m0, (int)P.v0 + n0, 0, 0, it.kit, ring0, full0, empty0,
+                                     full_lead0, leader, ring, armed_parity, armed, abort_flag);
         else if (!it.dw)
-          ok = produce<false, true>(&P.mapA, &P.mapB, m0, n0, (int)P.v0, it.kit, ring0, full0, empty0, full_lead0,
-                                    leader, ring, armed_parity, armed, abort_flag);
+          ok = produce<false, true>(&P.mapA, &P.mapB, m0, n0, it.split * P.split_kit * kStageK,
+                                    (int)P.v0 + it.split * P.split_kit * kStageK, it.kit, ring0, full0, empty0,
+                                    full_lead0, leader, ring, armed_parity, armed, abort_flag);
         else
-          ok = produce<true, true>(&P.mapA2, &P.mapB2, m0, n0, 0, it.kit, ring0, full0, empty0, full_lead0, leader,
+          ok = produce<true, true>(&P.mapA2, &P.mapB2, m0, n0, 0, 0, it.kit, ring0, full0, empty0, full_lead0, leader,
                                    ring, armed_parity, armed, abort_flag);
         if (!ok) { give_up(); break; }
       }
@@ -373,6 +429,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       bool issued = false;
       XentItem it;
       for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
+        if (kMode == kModeP && P.only_redo && !P.redo[it.tm]) continue;
         if (!mbar_wait_cluster(acce0 + 8 * acc, acc_phase ^ 1)) { give_up(); break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
@@ -399,6 +456,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
     uint32_t acc_phase = 0;
     XentItem it;
     for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
+      if (kMode == kModeP && P.only_redo && !P.redo[it.tm]) continue;
       const int i0 = it.tm * kTile + (int)crank * BM + quarter * 32, i = i0 + lane;
       const int c0 = it.tn * kTile;
       // per-row values of this tile, fetched while its products run
@@ -414,7 +472,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       tc_fence_after();
       const uint32_t trow = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile);
       if constexpr (kMode == kModeStats) {
-        if (i0 < q.rows) {
+        if (i0 < q.rows || P.keep) {  // (rows behind the last one are stored too: their P is set to 0 later)
           float m = -INFINITY, s = 0.f;
 #pragma unroll 1
           for (int ch = 0; ch < kTile / 32; ++ch) {
@@ -433,7 +491,12 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
               for (int j = 0; j < 32; ++j)
                 if (col0 + j >= P.v_piece) v[j] = -INFINITY;
             }
+            if (P.keep) keep_block(&P.mapO, stage, slot, v, ll2, col0, i0, lane);
             softmax_add(v, m, s);
+          }
+          if (P.keep && i < q.rows && !(m - ll2 <= kKeepMost && s < INFINITY)) {
+            P.redo[it.tm] = 1;  // every writer writes the same
+            P.head_out->redo = 1;
           }
           if (i < q.rows) P.part[(int64_t)it.tn * P.part_ld + i] = make_float2(m, s);
         }
@@ -506,16 +569,21 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
           float v[32];
           tmem_ld32(trow + ch * 32, v);
           if (!ok) continue;
+          if (it.kit == 0) {  // a narrow last piece may end before the last cut: nothing was multiplied
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
           const uint32_t mask = prefix_mask(P.d - col0);
           const bool whole = mask == 0xffffffffu;
-          float *sum = P.dh_acc + (int64_t)i * P.d + col0;  // d is a multiple of 8: 32-byte aligned
+          // d is a multiple of 8: 32-byte aligned
+          float *sum = P.dh_acc + it.split * P.acc_ld + (int64_t)i * P.d + col0;
           if (!P.first_piece) {
             float w[32];
             load_row32(sum, w, whole, mask);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += w[j];
           }
-          if (!P.last_piece) {
+          if (!P.last_piece || P.splits > 1) {
             store_row32(sum, v, whole, mask);
             continue;
           }
@@ -562,6 +630,7 @@ struct RowsParams {
   int64_t n, v, d, h_stride, w_stride, dh_stride;
   int64_t per_block;     // rows a block takes, a multiple of 8
   float scale2;
+  int32_t *redo;         // per row tile, cleared; NULL: no logits are kept
   int32_t labels64, mean, dh_f32, vec;
 };
 
@@ -612,7 +681,10 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const __grid_constant__ 
       R.head->rows = all;
       R.head->weight_sum = ws;
       R.head->g = R.mean ? (all > 0 ? up / ws : 0.f) : up;
+      R.head->redo = 0;
     }
+    if (R.redo)
+      for (int64_t k = threadIdx.x; k < (R.n + kTile - 1) / kTile; k += 256) R.redo[k] = 0;
   }
   const int64_t end = ((int64_t)all + kTile - 1) / kTile * kTile;
   for (int64_t base = row0; base < min(row0 + R.per_block, R.n + kTile); base += 8) {
@@ -734,15 +806,105 @@ __global__ void __launch_bounds__(256) xent_lse_kernel(const __grid_constant__ L
   if (threadIdx.x == 0) L.sums[blockIdx.x] = a;
 }
 
-__global__ void __launch_bounds__(1024) xent_totals_kernel(const float *sums, int n, const XentHead *head,
-                                                           float *totals) {
+struct TotalsParams {
+  const float *sums;
+  const XentHead *head;
+  float *totals;
+  int32_t n;
+};
+
+__global__ void __launch_bounds__(1024) xent_totals_kernel(const __grid_constant__ TotalsParams T) {
   pdl_launch();
   __shared__ float red[32];
   pdl_wait();
   float a = 0.f;
-  for (int k = threadIdx.x; k < n; k += 1024) a += sums[k];
+  for (int k = threadIdx.x; k < T.n; k += 1024) a += T.sums[k];
   a = block_sum(a, red);
-  if (threadIdx.x == 0) totals[0] = a, totals[1] = head->weight_sum;
+  if (threadIdx.x == 0) T.totals[0] = a, T.totals[1] = T.head->weight_sum;
+}
+
+struct ConvertParams {
+  const XentHead *head;
+  const int32_t *redo, *lab;
+  const float *wt, *lse2, *ll2;
+  uint16_t *p;   // kept logits, replaced by P in bf16
+  int64_t ld;
+  int32_t v;
+  float scale, z;
+};
+
+constexpr int kConvertCols = 256 * 8 * 2;  // columns of a block
+
+// P from the kept logits, in place: 2 bytes read and written per entry, HBM
+// bound.  One row and kConvertCols columns a block.
+__global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant__ ConvertParams C) {
+  pdl_launch();
+  const uint32_t across = (uint32_t)(C.v + kConvertCols - 1) / kConvertCols;
+  const int64_t i = blockIdx.x / across;
+  const int c0 = (int)(blockIdx.x % across) * kConvertCols + threadIdx.x * 8;
+  pdl_wait();
+  const int rows = C.head->rows;
+  if (i >= ((int64_t)rows + kTile - 1) / kTile * kTile || C.redo[i / kTile]) return;
+  uint16_t *row = C.p + i * C.ld;
+  float wt = 0.f, off = 0.f, peak = 0.f, mult = 0.f;
+  int lab = -1;
+  if (i < rows) {
+    const float lse2 = C.lse2[i];
+    wt = C.wt[i], lab = C.lab[i], off = C.ll2[i] - lse2;
+    mult = wt * C.scale, peak = mult * fmaf(2.f * C.z, lse2 * kLn2, 1.f);
+  }
+  uint4 raw[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (c0 + u * 2048 < C.v) raw[u] = *reinterpret_cast<const uint4 *>(row + c0 + u * 2048);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int c = c0 + u * 2048;
+    if (c >= C.v) continue;
+    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int q = (int)(int16_t)(w[e / 2] >> (16 * (e & 1)));
+      const float x = peak * exp2_fast(fmaf((float)q, 1.f / kKeepStep, off));
+      v[e] = wt == 0.f || q == -32768 ? 0.f : x;
+    }
+    if (lab >= c && lab < c + 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (lab == c + e) v[e] -= mult;
+    }
+    store8(reinterpret_cast<__nv_bfloat16 *>(row + c), v, 8, true);
+  }
+}
+
+struct JoinParams {
+  const XentHead *head;
+  const int32_t *idx;
+  const float *acc;
+  void *dh;
+  int64_t acc_ld, d, dh_stride;
+  int32_t splits, dh_f32;
+};
+
+// dH from the cuts of its K axis, added in their order.  Four columns a thread.
+__global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ JoinParams J) {
+  pdl_launch();
+  const int64_t i = blockIdx.x;
+  pdl_wait();
+  if (i >= J.head->rows) return;
+  const float g = J.head->g;
+  const int64_t row = J.idx[i] * J.dh_stride;
+  for (int64_t c = 4 * threadIdx.x; c < J.d; c += 1024) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < J.splits; ++s) {
+      const float4 b = *reinterpret_cast<const float4 *>(J.acc + s * J.acc_ld + i * J.d + c);
+      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    const float v[4] = {g * a.x, g * a.y, g * a.z, g * a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) st_elem(J.dh, J.dh_f32 ? GBO_F32 : GBO_BF16, row + c + e, v[e]);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -750,22 +912,28 @@ __global__ void __launch_bounds__(1024) xent_totals_kernel(const float *sums, in
 
 int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// Scratch of a call, in this order.  The tiles' statistics and P share their
-// room: the statistics are done with before P is written.
+// Scratch of a call, in this order.
 struct XentSpace {
-  int64_t head, idx, lab, wt, lse2, ll2, sums, hc, acc, big;  // byte offsets
+  int64_t head, redo, idx, lab, wt, lse2, ll2, sums, hc, acc, part, p;  // byte offsets
   int64_t n_pad, bytes;
-  int64_t piece;  // columns of a piece of the vocabulary
+  int64_t piece;            // columns of a piece of the vocabulary
   int32_t pieces;
+  int32_t keep;             // logits are kept between the passes, in P's room
+  int32_t splits, split_kit;
 };
 
 constexpr int64_t kPieceBytes = int64_t(2) << 30;  // P of one piece, unless the caller caps the workspace
+constexpr int64_t kKeepBytes = int64_t(8) << 30;   // kept logits, likewise
+constexpr int kPairs = 76;                         // CTA pairs of the device
 
-// grad: with the backward pass.  piece: columns per piece (0: as many as
-// kPieceBytes holds).
-XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, int64_t piece) {
+// grad: with the backward pass.  keep: the whole vocabulary's logits are kept
+// from the forward pass (one piece); else piece: columns per piece (0: as many
+// as kPieceBytes holds), and the tiles' statistics and P share their room (the
+// statistics are done with before P is written).
+XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, bool keep, int64_t piece) {
   XentSpace s = {};
   s.n_pad = up_to(std::max<int64_t>(n, 1), kTile);
+  s.keep = keep;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t r = at;
@@ -773,6 +941,7 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, int
     return r;
   };
   s.head = take(sizeof(XentHead));
+  s.redo = take(4 * s.n_pad / kTile);
   s.idx = take(4 * s.n_pad);
   s.lab = take(4 * s.n_pad);
   s.wt = take(4 * s.n_pad);
@@ -780,34 +949,62 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, int
   s.ll2 = take(4 * s.n_pad);
   s.sums = take(4 * s.n_pad);
   s.hc = take(2 * s.n_pad * d);
-  int64_t big = forward ? 8 * s.n_pad * ((v + kTile - 1) / kTile) : 0;
-  if (grad) {
-    if (piece <= 0) piece = kPieceBytes / (2 * s.n_pad);
-    piece = std::max<int64_t>(kTile, piece / kTile * kTile);
-    s.pieces = (int32_t)((v + piece - 1) / piece);
-    s.piece = up_to((v + s.pieces - 1) / s.pieces, kTile);  // even pieces
-    s.pieces = (int32_t)((v + s.piece - 1) / s.piece);
-    s.acc = take(s.pieces > 1 ? 4 * s.n_pad * d : 0);
-    big = std::max(big, 2 * s.n_pad * s.piece);
+  const int64_t part = forward ? 8 * s.n_pad * ((v + kTile - 1) / kTile) : 0;
+  if (!grad) {
+    s.part = take(part);
+    s.bytes = at;
+    return s;
   }
-  s.big = take(big);
+  if (keep) piece = up_to(v, kTile);
+  else if (piece <= 0) piece = kPieceBytes / (2 * s.n_pad);
+  piece = std::max<int64_t>(kTile, piece / kTile * kTile);
+  s.pieces = (int32_t)((v + piece - 1) / piece);
+  s.piece = up_to((v + s.pieces - 1) / s.pieces, kTile);  // even pieces
+  s.pieces = (int32_t)((v + s.piece - 1) / s.piece);
+  // With few rows dH has few items, each with the whole piece as its K:
+  // cut K until no item is longer than half a pair's share of the launch,
+  // but no shorter than 8 stages.  777 x 32003 x 1032: products 184 us uncut
+  // (20 items of 251 stages on 76 pairs).
+  const int64_t m_tiles = s.n_pad / kTile, d_tiles = (d + kTile - 1) / kTile;
+  const int64_t dh_kit = (s.piece + kStageK - 1) / kStageK;
+  const int64_t share =
+      std::max<int64_t>(1, (m_tiles * d_tiles * dh_kit + s.piece / kTile * d_tiles * (s.n_pad / kStageK)) / kPairs);
+  int64_t splits = std::min<int64_t>(std::min<int64_t>(16, std::max<int64_t>(1, dh_kit / 8)), (2 * dh_kit + share - 1) / share);
+  s.split_kit = (int32_t)((dh_kit + splits - 1) / splits);
+  s.splits = (int32_t)((dh_kit + s.split_kit - 1) / s.split_kit);
+  s.acc = take(s.pieces > 1 || s.splits > 1 ? 4 * s.splits * s.n_pad * d : 0);
+  if (keep) {
+    s.part = take(part);
+    s.p = take(2 * s.n_pad * s.piece);
+  } else {
+    s.part = s.p = take(std::max(part, 2 * s.n_pad * s.piece));
+  }
   s.bytes = at;
   return s;
 }
 
-// The widest pieces whose workspace fits `bytes` (false: not even one tile).
+// What a call does without a cap.
+XentSpace default_space(int64_t n, int64_t v, int64_t d) {
+  const bool keep = 2 * up_to(std::max<int64_t>(n, 1), kTile) * up_to(v, kTile) <= kKeepBytes;
+  return space_of(n, v, d, true, true, keep, 0);
+}
+
+// The fastest schedule whose workspace fits `bytes`: kept logits, else the
+// widest pieces (false: not even one of kTile columns).
 bool fit_space(int64_t n, int64_t v, int64_t d, bool forward, int64_t bytes, XentSpace *out) {
-  XentSpace s = space_of(n, v, d, true, forward, 0);
-  if (s.bytes > bytes) {
-    int64_t lo = 1, hi = up_to(v, kTile) / kTile;  // pieces of lo tiles fit, of hi do not
-    if (space_of(n, v, d, true, forward, kTile).bytes > bytes) return false;
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) / 2;
-      (space_of(n, v, d, true, forward, mid * kTile).bytes <= bytes ? lo : hi) = mid;
-    }
-    s = space_of(n, v, d, true, forward, lo * kTile);
+  if (forward) {
+    *out = space_of(n, v, d, true, true, true, 0);
+    if (out->bytes <= bytes) return true;
   }
-  *out = s;
+  *out = space_of(n, v, d, true, forward, false, 0);
+  if (out->bytes <= bytes) return true;
+  int64_t lo = 1, hi = up_to(v, kTile) / kTile;  // pieces of lo tiles fit, of hi do not
+  if (space_of(n, v, d, true, forward, false, kTile).bytes > bytes) return false;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    (space_of(n, v, d, true, forward, false, mid * kTile).bytes <= bytes ? lo : hi) = mid;
+  }
+  *out = space_of(n, v, d, true, forward, false, lo * kTile);
   return true;
 }
 
@@ -852,6 +1049,16 @@ int check_grads(const gbo_xent_args *a, const gbo_xent_grads *g) {
   return GBO_OK;
 }
 
+// The launches of a call depend on one another alone, and its kernels are
+// short when there are few rows: they carry the programmatic-dependent-launch
+// attribute on direct launches too (one token over 128000 x 2048: 108.0 ->
+// 101.8 us; 777 rows: 289.8 -> 277.1 us; thousands of rows: equal).
+template <typename K>
+cudaError_t chain(void (*kernel)(K), dim3 grid, dim3 block, cudaStream_t stream, const K &params) {
+  count_launches(1);
+  return launch_kernel_as(pdl_allowed(), kernel, grid, block, 0, stream, 1, params);
+}
+
 template <int kMode>
 cudaError_t launch_xent(const XentParams &P, int64_t items, int sm, cudaStream_t stream) {
   static std::once_flag once;
@@ -877,7 +1084,8 @@ cudaError_t launch_xent(const XentParams &P, int64_t items, int sm, cudaStream_t
   if (attr_err != cudaSuccess) return attr_err;
   const int64_t fit = std::max(1, resident > 0 ? std::min(resident, sm / 2) : sm / 2);
   const int clusters = (int)std::max<int64_t>(1, std::min(items, fit));
-  const cudaError_t e = launch_kernel(xent_kernel<kMode>, dim3(2 * clusters), dim3(kXentThreads), kXentSmem, stream, 2, P);
+  const cudaError_t e = launch_kernel_as(pdl_allowed(), xent_kernel<kMode>, dim3(2 * clusters), dim3(kXentThreads),
+                                         kXentSmem, stream, 2, P);
   count_launches(1);
   return e;
 }
@@ -911,7 +1119,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     if (!fit_space(a->n, a->v, a->d, forward, (int64_t)ws_bytes, &S))
       return xent_fail(GBO_ERR_WORKSPACE, "workspace too small for a piece of 256 columns");
   } else {
-    S = space_of(a->n, a->v, a->d, false, true, 0);
+    S = space_of(a->n, a->v, a->d, false, true, false, 0);
   }
   if (!workspace || (int64_t)ws_bytes < S.bytes) return xent_fail(GBO_ERR_WORKSPACE, "workspace missing or too small");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return xent_fail(GBO_ERR_WORKSPACE, "workspace must be 256-byte aligned");
@@ -930,6 +1138,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
   R.ll2 = reinterpret_cast<float *>(ws + S.ll2);
   R.hc = reinterpret_cast<__nv_bfloat16 *>(ws + S.hc);
   R.loss = loss, R.lse = lse, R.dh = g ? g->dh : nullptr;
+  R.redo = S.keep ? reinterpret_cast<int32_t *>(ws + S.redo) : nullptr;
   R.status = status;
   R.n = a->n, R.v = a->v, R.d = a->d;
   R.h_stride = a->h_stride, R.w_stride = a->w_stride, R.dh_stride = g ? g->dh_stride : 0;
@@ -940,10 +1149,9 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
   // eight blocks an SM at most: each reads all labels
   const int64_t virt = a->n + kTile, most = (int64_t)8 * sm;
   R.per_block = up_to((virt + most - 1) / most, 8);
-  if ((e = launch_kernel(xent_rows_kernel, dim3((unsigned)((virt + R.per_block - 1) / R.per_block)), dim3(256), 0, st, 1,
-                         R)) != cudaSuccess)
+  if ((e = chain(xent_rows_kernel, dim3((unsigned)((virt + R.per_block - 1) / R.per_block)), dim3(256), st, R)) !=
+      cudaSuccess)
     return cuda_err(e);
-  count_launches(1);
 
   XentParams P;
   memset(&P, 0, sizeof P);
@@ -960,7 +1168,13 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     if (!maps) return xent_fail(GBO_ERR_CUDA, "tensor map of H or W");
   }
   if (forward && a->n > 0) {
-    P.part = reinterpret_cast<float2 *>(ws + S.big);
+    P.part = reinterpret_cast<float2 *>(ws + S.part);
+    P.keep = S.keep;
+    if (S.keep) {
+      P.redo = R.redo, P.head_out = R.head;
+      if (!map_2d(&P.mapO, ws + S.p, a->v, S.n_pad, S.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return xent_fail(GBO_ERR_CUDA, "tensor map of the logits");
+    }
     P.part_ld = S.n_pad;
     P.v0 = 0, P.v_piece = (int32_t)a->v;
     const int64_t n_tiles = (a->v + kTile - 1) / kTile;
@@ -973,19 +1187,13 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     L.part_ld = S.n_pad, L.tiles = (int32_t)n_tiles, L.z = a->z_loss;
     while (L.rows_log2 < 5 && (1 << L.rows_log2) < a->n) ++L.rows_log2;
     const int blocks = (int)((a->n + (1 << L.rows_log2) - 1) >> L.rows_log2);
-    if ((e = launch_kernel(xent_lse_kernel, dim3(blocks), dim3(256), 0, st, 1, L)) != cudaSuccess) return cuda_err(e);
-    count_launches(1);
-    if (totals) {
-      if ((e = launch_kernel(xent_totals_kernel, dim3(1), dim3(1024), 0, st, 1, (const float *)L.sums, blocks,
-                             (const XentHead *)R.head, totals)) != cudaSuccess)
-        return cuda_err(e);
-      count_launches(1);
-    }
-  } else if (forward && totals) {
-    if ((e = launch_kernel(xent_totals_kernel, dim3(1), dim3(1024), 0, st, 1, (const float *)nullptr, 0,
-                           (const XentHead *)R.head, totals)) != cudaSuccess)
+    if ((e = chain(xent_lse_kernel, dim3(blocks), dim3(256), st, L)) != cudaSuccess) return cuda_err(e);
+    if (totals && (e = chain(xent_totals_kernel, dim3(1), dim3(1024), st, TotalsParams{L.sums, R.head, totals, blocks})) !=
+                      cudaSuccess)
       return cuda_err(e);
-    count_launches(1);
+  } else if (forward && totals) {
+    if ((e = chain(xent_totals_kernel, dim3(1), dim3(1024), st, TotalsParams{nullptr, R.head, totals, 0})) != cudaSuccess)
+      return cuda_err(e);
   }
   if (g) {
     P.dh = a->n > 0 ? g->dh : nullptr, P.dw = g->dw;
@@ -995,7 +1203,19 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     P.dw_vec = (reinterpret_cast<uintptr_t>(g->dw) & 15) == 0 && g->dw_stride % (P.dw_f32 ? 4 : 8) == 0;
     P.dw_add = g->accumulate_dw;
     P.dh_acc = reinterpret_cast<float *>(ws + S.acc);
-    void *pbuf = ws + S.big;
+    P.acc_ld = S.n_pad * a->d;
+    P.splits = S.splits, P.split_kit = S.split_kit;
+    void *pbuf = ws + S.p;
+    if (S.keep && a->n > 0) {
+      ConvertParams C = {};
+      C.head = R.head, C.redo = R.redo, C.lab = R.lab, C.wt = R.wt, C.lse2 = R.lse2, C.ll2 = R.ll2;
+      C.p = static_cast<uint16_t *>(pbuf), C.ld = S.piece, C.v = (int32_t)a->v;
+      C.scale = a->logit_scale, C.z = a->z_loss;
+      const int64_t blocks = (a->v + kConvertCols - 1) / kConvertCols * S.n_pad;
+      if (blocks > INT32_MAX) return xent_fail(GBO_ERR_SHAPE, "more kept logits than one launch takes: cap the workspace");
+      if ((e = chain(xent_convert_kernel, dim3((unsigned)blocks), dim3(256), st, C)) != cudaSuccess) return cuda_err(e);
+      P.redo = R.redo, P.only_redo = 1;
+    }
     for (int32_t c = 0; c < S.pieces; ++c) {
       P.v0 = c * S.piece;
       P.v_piece = (int32_t)std::min<int64_t>(S.piece, a->v - P.v0);
@@ -1009,8 +1229,15 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
              map_2d(&Q.mapB2, R.hc, a->d, S.n_pad, a->d, 64, kBlockK);
       if (!maps) return xent_fail(GBO_ERR_CUDA, "tensor map of P");
       if (a->n > 0 && (e = launch_xent<kModeP>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) return cuda_err(e);
-      const int64_t items = (P.dh ? m_tiles * d_tiles : 0) + (P.dw ? n_tiles * d_tiles : 0);
+      const int64_t items = (P.dh ? m_tiles * d_tiles * S.splits : 0) + (P.dw ? n_tiles * d_tiles : 0);
       if (items > 0 && (e = launch_xent<kModeProducts>(Q, items, sm, st)) != cudaSuccess) return cuda_err(e);
+    }
+    if (P.dh && S.splits > 1) {
+      JoinParams J = {};
+      J.head = R.head, J.idx = R.idx, J.acc = P.dh_acc, J.dh = P.dh;
+      J.acc_ld = P.acc_ld, J.d = a->d, J.dh_stride = P.dh_stride;
+      J.splits = S.splits, J.dh_f32 = P.dh_f32;
+      if ((e = chain(xent_join_kernel, dim3((unsigned)a->n), dim3(256), st, J)) != cudaSuccess) return cuda_err(e);
     }
   }
   return report_ok();
@@ -1023,10 +1250,10 @@ using namespace gbo;
 
 extern "C" size_t gbo_xent_workspace_bytes(int64_t n, int64_t v, int64_t d, int32_t grad, int64_t cap) {
   if (n < 0 || v < 1 || d < 8 || d % 8 || n > (int64_t(1) << 30) || v > (int64_t(1) << 30) || d > (1 << 20)) return 0;
-  if (!grad) return (size_t)space_of(n, v, d, false, true, 0).bytes;
+  if (!grad) return (size_t)space_of(n, v, d, false, true, false, 0).bytes;
   XentSpace s;
   if (cap > 0) return fit_space(n, v, d, true, cap, &s) ? (size_t)s.bytes : 0;
-  return (size_t)space_of(n, v, d, true, true, 0).bytes;
+  return (size_t)default_space(n, v, d).bytes;
 }
 
 extern "C" int gbo_xent_forward(const gbo_xent_args *args, float *loss, float *lse, float *totals, void *workspace,
