@@ -613,6 +613,218 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------------------
+// few rows
+
+// Statistics of at most kScoreRows rows: W is read once and its HBM traffic is
+// all there is, so the operands change places.  The vocabulary is M (tiles of
+// 128 rows of W), the rows are N = 32: a tile's products take an eighth of
+// the tensor core's time of a 256-wide tile, a stage of the ring is 32 KB of W
+// and 8 KB of H, and four of five are on their way while one is multiplied.
+// Each CTA takes a run of the vocabulary, equal to within 16 rows.  A thread
+// of the epilogue owns a row of W and keeps a running maximum and sum for
+// every row of H; lanes join once, at the end.
+// One token over 128000 x 2048 (524 MB), the whole call: 102 us with the
+// 256-wide tiles, 97 us here, where a plain reduction that reads W once takes
+// 92 us.  Three to six stages measure the same (98 to 101 us): HBM is the bound.
+// Prefetching each next tile's rows to L2 made it 137 us.
+constexpr int kScoreRows = 32;
+constexpr int kScoreUnit = 16;                                   // rows of W that a run is made of
+constexpr int kScoreB = kScoreRows * kBlockK * 2;                // 4 KB: H's rows, one K block
+constexpr int kScoreStage = 2 * (kOpBytes + kScoreB);
+constexpr int kScoreStages = 5;
+constexpr int kScoreSmem = 1024 + kScoreStages * kScoreStage + 256 + kScoreRows * 8;
+constexpr int kScoreTmem = 64;                                   // two 128 x 32 accumulators
+static_assert(kScoreSmem <= 232448, "shared memory per CTA");
+
+struct ScoreParams {
+  CUtensorMap mapW, mapW16, mapH;  // boxes of 128, 16 and 32 rows
+  const XentHead *head;
+  const int32_t *lab;
+  const float *ll2;
+  float2 *part;     // (maximum, sum) per CTA and epilogue warp, and row
+  const __nv_bfloat16 *w;
+  int32_t *status;
+  int64_t part_ld, w_stride;
+  int32_t v, d;
+  float scale2;
+};
+
+__global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constant__ ScoreParams P) {
+  pdl_launch();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kScoreStages * kScoreStage);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kScoreStages + 5);
+  volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
+  int32_t *lab_s = reinterpret_cast<int32_t *>(bars + 32);
+  float *ll2_s = reinterpret_cast<float *>(lab_s + kScoreRows);
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kScoreStages);
+  const uint32_t accf0 = smem_u32(bars + 2 * kScoreStages), acce0 = accf0 + 16, drain = accf0 + 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // this CTA's run of the vocabulary
+  const int units = (P.v + kScoreUnit - 1) / kScoreUnit, base = units / (int)gridDim.x, rem = units % (int)gridDim.x;
+  const int cid = blockIdx.x, row0 = kScoreUnit * (cid * base + min(cid, rem));
+  const int run = kScoreUnit * (base + (cid < rem ? 1 : 0)), end = min(row0 + run, P.v);
+  const int tiles = (run + BM - 1) / BM, kit = (P.d + kStageK - 1) / kStageK;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kScoreStages; ++s) mbar_init(full0 + 8 * s, 1), mbar_init(empty0 + 8 * s, 1);
+    for (int a = 0; a < 2; ++a) mbar_init(accf0 + 8 * a, 1), mbar_init(acce0 + 8 * a, kEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kScoreTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // While the rows are still being prepared: the first tile's rows of W on
+  // their way to L2 (a hint; nothing is read here that counts).
+  for (int r = row0 + (int)threadIdx.x; r < min(end, row0 + BM); r += 192)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(P.w + r * P.w_stride), "r"(2 * P.d) : "memory");
+  pdl_wait();
+  const int rows = P.head->rows;  // at most kScoreRows
+  if (threadIdx.x < kScoreRows) {
+    lab_s[threadIdx.x] = (int)threadIdx.x < rows ? P.lab[threadIdx.x] : -1;
+    ll2_s[threadIdx.x] = (int)threadIdx.x < rows ? P.ll2[threadIdx.x] : 0.f;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot, ring0 = smem_u32(smem);
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    flag_status(P.status, GBO_STATUS_TIMEOUT);
+  };
+  int stage = 0;
+  uint32_t phase = 0;
+  auto next = [&]() {
+    if (++stage == kScoreStages) stage = 0, phase ^= 1;
+  };
+  if (rows == 0) {
+    // nothing counts
+  } else if (warp == 0) {
+    if (lane == 0) {
+      uint32_t armed = 0, armed_parity = 0;
+      bool ok = true;
+      for (int t = 0; t < tiles && ok; ++t) {
+        // whole tiles in one box; the last one's 16-row groups one by one
+        // (its other rows are whatever the ring holds: accumulators that
+        // nobody reads)
+        const int left = run - t * BM, boxes = left >= BM ? 0 : left / kScoreUnit;
+        const uint32_t bytes = 2u * (uint32_t)((boxes ? boxes * (kOpBytes / 8) : kOpBytes) + kScoreB);
+        for (int kb = 0; kb < kit; ++kb) {
+          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1)) { give_up(); ok = false; break; }
+          if (*abort_flag) { ok = false; break; }
+          const uint32_t fb = full0 + 8 * stage;
+          mbar_expect_tx(fb, bytes);
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+            const uint32_t sa = ring0 + stage * kScoreStage + sub * kOpBytes;
+            const uint32_t sb = ring0 + stage * kScoreStage + 2 * kOpBytes + sub * kScoreB;
+            const int k = kb * kStageK + sub * kBlockK;
+            if (!boxes) tma_load_3d(sa, &P.mapW, fb, k, row0 + t * BM, 0);
+            for (int h = 0; h < boxes; ++h)
+              tma_load_3d(sa + h * (kOpBytes / 8), &P.mapW16, fb, k, row0 + t * BM + h * kScoreUnit, 0);
+            tma_load_3d(sb, &P.mapH, fb, k, 0, 0);
+          }
+          next();
+        }
+      }
+      if (*abort_flag)  // copies armed here land before shared memory goes away
+        for (int s = 0; s < kScoreStages; ++s)
+          if (armed >> s & 1u) (void)mbar_wait(full0 + 8 * s, armed_parity >> s & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kScoreRows >> 3) << 17) |
+                             ((uint32_t)(BM >> 4) << 24);
+      const uint64_t a0 = smem_desc(ring0, 16, 1024), b0 = smem_desc(ring0 + 2 * kOpBytes, 16, 1024);
+      bool issued = false, ok = true;
+      for (int t = 0; t < tiles && ok && !*abort_flag; ++t) {
+        const int acc = t & 1;
+        if (!mbar_wait(acce0 + 8 * acc, ((t >> 1) & 1) ^ 1)) { give_up(); break; }
+        tc_fence_after();
+        for (int kb = 0; kb < kit; ++kb) {
+          if (!mbar_wait(full0 + 8 * stage, phase)) { give_up(); ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int k = 0; k < kBlockK / 16; ++k) {
+              const uint64_t ad = a0 + ((uint32_t)(stage * kScoreStage + sub * kOpBytes) >> 4) + 2 * k;
+              const uint64_t bd = b0 + ((uint32_t)(stage * kScoreStage + sub * kScoreB) >> 4) + 2 * k;
+              asm volatile(
+                  "{\n\t.reg .pred p;\n\t"
+                  "setp.ne.b32 p, %4, 0;\n\t"
+                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_base + acc * kScoreRows),
+                  "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)((kb | sub | k) != 0))
+                  : "memory");
+            }
+          issued = true;
+          mma_commit_one(empty0 + 8 * stage);
+          next();
+        }
+        if (ok) mma_commit_one(accf0 + 8 * acc);
+      }
+      if (*abort_flag && issued) {
+        mma_commit_one(drain);
+        (void)mbar_wait(drain, 0);
+      }
+    }
+  } else {
+    const int quarter = warp & 3;
+    float m[kScoreRows], s[kScoreRows];
+#pragma unroll
+    for (int j = 0; j < kScoreRows; ++j) m[j] = -INFINITY, s[j] = 0.f;
+    bool ok = true;
+    for (int t = 0; t < tiles; ++t) {
+      const int acc = t & 1, r = row0 + t * BM + quarter * 32 + lane;
+      if (!mbar_wait(accf0 + 8 * acc, (t >> 1) & 1)) { give_up(); ok = false; break; }
+      tc_fence_after();
+      float v[kScoreRows];
+      tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kScoreRows), v);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acce0 + 8 * acc);
+#pragma unroll
+      for (int j = 0; j < kScoreRows; ++j) {
+        if (j >= rows) break;
+        float x = v[j] * P.scale2;
+        if (r == lab_s[j]) x = ll2_s[j];
+        if (r < end) {
+          const float mn = fmaxf(m[j], x), at = mn == -INFINITY ? 0.f : mn;
+          s[j] = fmaf(s[j], exp2_fast(m[j] - at), exp2_fast(x - at));
+          m[j] = mn;
+        }
+      }
+    }
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < kScoreRows; ++j) {
+        if (j >= rows) break;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const float m2 = __shfl_xor_sync(0xffffffffu, m[j], o), s2 = __shfl_xor_sync(0xffffffffu, s[j], o);
+          const float mn = fmaxf(m[j], m2), at = mn == -INFINITY ? 0.f : mn;
+          s[j] = s[j] * exp2_fast(m[j] - at) + s2 * exp2_fast(m2 - at);
+          m[j] = mn;
+        }
+        if (lane == 0) P.part[((int64_t)blockIdx.x * kEpiWarps + quarter) * P.part_ld + j] = make_float2(m[j], s[j]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kScoreTmem) : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // rows
 
 struct RowsParams {
@@ -701,7 +913,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const __grid_constant__ 
       const __nv_bfloat16 *src = R.h + i * R.h_stride, *lab = R.w + y * R.w_stride;
       __nv_bfloat16 *dst = R.hc + p * R.d;
       float dot = 0.f;
-#pragma unroll 2
+#pragma unroll 4
       for (int64_t c = 8 * lane; c < R.d; c += 256) {
         float a[8], b[8];
         load8(src, GBO_BF16, c, 8, R.vec != 0, a);
@@ -925,6 +1137,7 @@ struct XentSpace {
 constexpr int64_t kPieceBytes = int64_t(2) << 30;  // P of one piece, unless the caller caps the workspace
 constexpr int64_t kKeepBytes = int64_t(8) << 30;   // kept logits, likewise
 constexpr int kPairs = 76;                         // CTA pairs of the device
+constexpr int kMostSms = 256;
 
 // grad: with the backward pass.  keep: the whole vocabulary's logits are kept
 // from the forward pass (one piece); else piece: columns per piece (0: as many
@@ -949,7 +1162,10 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, boo
   s.ll2 = take(4 * s.n_pad);
   s.sums = take(4 * s.n_pad);
   s.hc = take(2 * s.n_pad * d);
-  const int64_t part = forward ? 8 * s.n_pad * ((v + kTile - 1) / kTile) : 0;
+  // statistics: per vocabulary tile, or (few rows) per CTA and epilogue warp
+  int64_t slots = (v + kTile - 1) / kTile;
+  if (n <= kScoreRows) slots = std::max<int64_t>(slots, kEpiWarps * kMostSms);
+  const int64_t part = forward ? 8 * s.n_pad * slots : 0;
   if (!grad) {
     s.part = take(part);
     s.bytes = at;
@@ -1101,6 +1317,30 @@ int cuda_err(cudaError_t e) {
   return xent_fail(GBO_ERR_CUDA, msg);
 }
 
+// Statistics of at most kScoreRows rows; *blocks: CTAs, each with a slot of
+// statistics per epilogue warp.
+int run_score(const gbo_xent_args *a, const XentParams &P, const RowsParams &R, int sm, cudaStream_t st, int *blocks) {
+  ScoreParams Q;
+  memset(&Q, 0, sizeof Q);
+  Q.head = P.head, Q.lab = P.lab, Q.ll2 = P.ll2, Q.part = P.part, Q.part_ld = P.part_ld, Q.status = P.status;
+  Q.w = R.w, Q.w_stride = a->w_stride, Q.v = (int32_t)a->v, Q.d = P.d, Q.scale2 = P.scale2;
+  if (!map_2d(&Q.mapW, a->w, a->d, a->v, a->w_stride, kBlockK, BM) ||
+      !map_2d(&Q.mapW16, a->w, a->d, a->v, a->w_stride, kBlockK, kScoreUnit) ||
+      !map_2d(&Q.mapH, R.hc, a->d, kTile, a->d, kBlockK, kScoreRows))
+    return xent_fail(GBO_ERR_CUDA, "tensor map of H or W");
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(xent_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+  });
+  if (attr_err != cudaSuccess) return cuda_err(attr_err);
+  // one CTA an SM, each with at least two 16-row units
+  *blocks = (int)std::min<int64_t>(std::min(sm, kMostSms), std::max<int64_t>(1, a->v / (2 * kScoreUnit)));
+  const cudaError_t e = launch_kernel_as(pdl_allowed(), xent_score_kernel, dim3(*blocks), dim3(192), kScoreSmem, st, 1, Q);
+  count_launches(1);
+  return e == cudaSuccess ? GBO_OK : cuda_err(e);
+}
+
 // forward: loss, lse, totals.  g: gradients too (lse_in: with the forward
 // pass skipped, its lse).
 int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, float *totals, const float *lse_in,
@@ -1177,8 +1417,14 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     }
     P.part_ld = S.n_pad;
     P.v0 = 0, P.v_piece = (int32_t)a->v;
-    const int64_t n_tiles = (a->v + kTile - 1) / kTile;
-    if ((e = launch_xent<kModeStats>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) return cuda_err(e);
+    int64_t n_tiles = (a->v + kTile - 1) / kTile;
+    if (a->n <= kScoreRows && !S.keep) {
+      int blocks = 0;
+      if ((rc = run_score(a, P, R, sm, st, &blocks)) != GBO_OK) return rc;
+      n_tiles = (int64_t)kEpiWarps * blocks;
+    } else if ((e = launch_xent<kModeStats>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) {
+      return cuda_err(e);
+    }
     LseParams L = {};
     L.head = R.head, L.part = P.part, L.ll2 = P.ll2, L.wt = R.wt, L.idx = R.idx;
     L.lse2 = R.lse2, L.loss = loss, L.lse = lse;

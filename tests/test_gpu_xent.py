@@ -78,7 +78,7 @@ def close(got, want, tol, dtype):
 
 
 SHAPES = [(1, 1, 8), (1, 300, 64), (5, 257, 72), (130, 256, 128), (300, 1000, 64), (257, 2049, 136), (513, 130, 264),
-          (64, 5003, 512)]
+          (64, 5003, 512), (32, 20011, 136), (17, 4099, 72)]
 
 
 @pytest.mark.parametrize("n,v,d", SHAPES)
