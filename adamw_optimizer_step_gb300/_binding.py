@@ -112,7 +112,7 @@ class XentArgs(ctypes.Structure):
     _fields_ = [("h", c_void_p), ("w", c_void_p), ("labels", c_void_p), ("row_weight", c_void_p),
                 ("upstream", c_void_p), ("n", c_int64), ("v", c_int64), ("d", c_int64), ("h_stride", c_int64),
                 ("w_stride", c_int64), ("logit_scale", c_float), ("z_loss", c_float), ("label_dtype", c_int32),
-                ("mean", c_int32)]
+                ("mean", c_int32), ("keep", c_int32), ("reserved", c_int32)]
 
 
 class XentGrads(ctypes.Structure):
@@ -613,7 +613,7 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
 
 
-def _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean):
+def _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean, keep=False):
     _rows_of(h, "h"), _rows_of(w, "w")
     if h.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
         raise TypeError("h and w must be bfloat16")
@@ -630,7 +630,7 @@ def _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean):
     return XentArgs(h.data_ptr(), w.data_ptr(), _dev_ptr(labels, "labels"), _dev_ptr(row_weight, "row_weight"),
                     _dev_ptr(upstream, "upstream"), n, w.shape[0], h.shape[1], _row_stride(h), _row_stride(w),
                     float(logit_scale), float(z_loss), GBO_I64 if labels.dtype == torch.int64 else GBO_I32,
-                    int(bool(mean)))
+                    int(bool(mean)), int(bool(keep)), 0)
 
 
 def _xent_grads(dh, dw, h, w, accumulate_dw):
@@ -654,10 +654,11 @@ def _out_f32(t, count, what):
 
 
 def gbo_xent_forward(h, w, labels, workspace, *, loss=None, lse=None, totals=None, row_weight=None, logit_scale=1.0,
-                     z_loss=0.0, dev_status=None, stream=None):
+                     z_loss=0.0, keep=False, dev_status=None, stream=None):
     """Cross entropy of each row of ``h`` @ ``w``.T against ``labels`` into ``loss``,
-    ``lse`` (n) and ``totals`` (2), whichever are given."""
-    a = _xent_args(h, w, labels, row_weight, None, logit_scale, z_loss, True)
+    ``lse`` (n) and ``totals`` (2), whichever are given.  ``keep``: leave the logits
+    in the workspace (of ``grad`` size) for gbo_xent_backward."""
+    a = _xent_args(h, w, labels, row_weight, None, logit_scale, z_loss, True, keep)
     _check(lib().gbo_xent_forward(ctypes.byref(a), _out_f32(loss, a.n, "loss"), _out_f32(lse, a.n, "lse"),
                                   _out_f32(totals, 2, "totals"), _dev_ptr(workspace, "workspace"),
                                   workspace.numel() * workspace.element_size(), _dev_ptr(dev_status, "dev_status"),
@@ -665,9 +666,10 @@ def gbo_xent_forward(h, w, labels, workspace, *, loss=None, lse=None, totals=Non
 
 
 def gbo_xent_backward(h, w, labels, lse, workspace, *, dh=None, dw=None, accumulate_dw=False, row_weight=None,
-                      upstream=None, mean=True, logit_scale=1.0, z_loss=0.0, dev_status=None, stream=None):
-    """Gradients into ``dh`` and ``dw`` from the forward's ``lse``."""
-    a = _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean)
+                      upstream=None, mean=True, logit_scale=1.0, z_loss=0.0, keep=False, dev_status=None, stream=None):
+    """Gradients into ``dh`` and ``dw`` from the forward's ``lse`` (``keep``: and the
+    logits that a forward with ``keep`` left in this workspace)."""
+    a = _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean, keep)
     g = _xent_grads(dh, dw, h, w, accumulate_dw)
     _check(lib().gbo_xent_backward(ctypes.byref(a), _out_f32(lse, a.n, "lse"), ctypes.byref(g),
                                    _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),

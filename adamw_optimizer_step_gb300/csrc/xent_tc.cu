@@ -842,7 +842,8 @@ struct RowsParams {
   int64_t n, v, d, h_stride, w_stride, dh_stride;
   int64_t per_block;     // rows a block takes, a multiple of 8
   float scale2;
-  int32_t *redo;         // per row tile, cleared; NULL: no logits are kept
+  int32_t *redo;         // per row tile, cleared; NULL: no logits will be kept
+  int32_t kept;          // logits and marks of an earlier forward stay
   int32_t labels64, mean, dh_f32, vec;
 };
 
@@ -893,7 +894,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const __grid_constant__ 
       R.head->rows = all;
       R.head->weight_sum = ws;
       R.head->g = R.mean ? (all > 0 ? up / ws : 0.f) : up;
-      R.head->redo = 0;
+      if (!R.kept) R.head->redo = 0;
     }
     if (R.redo)
       for (int64_t k = threadIdx.x; k < (R.n + kTile - 1) / kTile; k += 256) R.redo[k] = 0;
@@ -1246,6 +1247,7 @@ int check_args(const gbo_xent_args *a) {
   if (!std::isfinite(a->logit_scale) || !std::isfinite(a->z_loss))
     return xent_fail(GBO_ERR_INVALID_ARG, "non-finite logit_scale or z_loss");
   if (a->mean != 0 && a->mean != 1) return xent_fail(GBO_ERR_INVALID_ARG, "mean must be 0 or 1");
+  if (a->keep != 0 && a->keep != 1) return xent_fail(GBO_ERR_INVALID_ARG, "keep must be 0 or 1");
   return GBO_OK;
 }
 
@@ -1355,8 +1357,10 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
   int dev, sm = 0;
   if ((rc = require_device(&dev, &sm)) != GBO_OK) return rc;
   XentSpace S;
-  if (g) {
-    if (!fit_space(a->n, a->v, a->d, forward, (int64_t)ws_bytes, &S))
+  // the same schedule for both halves of a kept pair of calls
+  const bool whole = (forward && g) || a->keep;
+  if (g || a->keep) {
+    if (!fit_space(a->n, a->v, a->d, whole, (int64_t)ws_bytes, &S))
       return xent_fail(GBO_ERR_WORKSPACE, "workspace too small for a piece of 256 columns");
   } else {
     S = space_of(a->n, a->v, a->d, false, true, false, 0);
@@ -1378,7 +1382,9 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
   R.ll2 = reinterpret_cast<float *>(ws + S.ll2);
   R.hc = reinterpret_cast<__nv_bfloat16 *>(ws + S.hc);
   R.loss = loss, R.lse = lse, R.dh = g ? g->dh : nullptr;
-  R.redo = S.keep ? reinterpret_cast<int32_t *>(ws + S.redo) : nullptr;
+  int32_t *redo = reinterpret_cast<int32_t *>(ws + S.redo);
+  R.redo = S.keep && forward ? redo : nullptr;
+  R.kept = S.keep && !forward;
   R.status = status;
   R.n = a->n, R.v = a->v, R.d = a->d;
   R.h_stride = a->h_stride, R.w_stride = a->w_stride, R.dh_stride = g ? g->dh_stride : 0;
@@ -1411,7 +1417,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     P.part = reinterpret_cast<float2 *>(ws + S.part);
     P.keep = S.keep;
     if (S.keep) {
-      P.redo = R.redo, P.head_out = R.head;
+      P.redo = redo, P.head_out = R.head;
       if (!map_2d(&P.mapO, ws + S.p, a->v, S.n_pad, S.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
         return xent_fail(GBO_ERR_CUDA, "tensor map of the logits");
     }
@@ -1454,13 +1460,13 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     void *pbuf = ws + S.p;
     if (S.keep && a->n > 0) {
       ConvertParams C = {};
-      C.head = R.head, C.redo = R.redo, C.lab = R.lab, C.wt = R.wt, C.lse2 = R.lse2, C.ll2 = R.ll2;
+      C.head = R.head, C.redo = redo, C.lab = R.lab, C.wt = R.wt, C.lse2 = R.lse2, C.ll2 = R.ll2;
       C.p = static_cast<uint16_t *>(pbuf), C.ld = S.piece, C.v = (int32_t)a->v;
       C.scale = a->logit_scale, C.z = a->z_loss;
       const int64_t blocks = (a->v + kConvertCols - 1) / kConvertCols * S.n_pad;
       if (blocks > INT32_MAX) return xent_fail(GBO_ERR_SHAPE, "more kept logits than one launch takes: cap the workspace");
       if ((e = chain(xent_convert_kernel, dim3((unsigned)blocks), dim3(256), st, C)) != cudaSuccess) return cuda_err(e);
-      P.redo = R.redo, P.only_redo = 1;
+      P.redo = redo, P.only_redo = 1;
     }
     for (int32_t c = 0; c < S.pieces; ++c) {
       P.v0 = c * S.piece;

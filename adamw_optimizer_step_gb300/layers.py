@@ -184,27 +184,32 @@ class _QkNormRotary(torch.autograd.Function):
 
 class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, h, w, labels, row_weight, z_loss, logit_scale):
+    def forward(ctx, h, w, labels, row_weight, z_loss, logit_scale, workspace_cap):
         n, d = h.shape
+        wb = w.to(torch.bfloat16)
+        grad = ctx.needs_input_grad[0] or ctx.needs_input_grad[1]
         lse = torch.empty(n, dtype=torch.float32, device=h.device)
         totals = torch.empty(2, dtype=torch.float32, device=h.device)
-        linear_cross_entropy(h, w, labels, z_loss=z_loss, logit_scale=logit_scale, lse=lse, totals=totals,
-                             row_weight=row_weight)
-        ctx.save_for_backward(h, w, labels, row_weight, lse)
-        ctx.rest = (z_loss, logit_scale)
+        ws = torch.empty(B.gbo_xent_workspace_bytes(n, w.shape[0], d, grad, workspace_cap), dtype=torch.uint8,
+                         device=h.device)
+        B.gbo_xent_forward(h, wb, labels, ws, lse=lse, totals=totals, row_weight=row_weight, logit_scale=logit_scale,
+                           z_loss=z_loss, keep=grad)
+        ctx.save_for_backward(h, wb, labels, row_weight, lse)
+        ctx.rest = (z_loss, logit_scale, w.dtype, ws)
         return torch.where(totals[1] != 0, totals[0] / totals[1], torch.zeros_like(totals[0]))
 
     @staticmethod
     def backward(ctx, up):
         h, w, labels, row_weight, lse = ctx.saved_tensors
-        z_loss, logit_scale = ctx.rest
+        z_loss, logit_scale, w_dtype, ws = ctx.rest
+        if ws is None:
+            raise RuntimeError("the loss's workspace is used up by its first backward pass")
+        ctx.rest = (z_loss, logit_scale, w_dtype, None)
         dh = _like(h) if ctx.needs_input_grad[0] else None
-        dw = _like(w) if ctx.needs_input_grad[1] else None
-        ws = torch.empty(B.gbo_xent_workspace_bytes(h.shape[0], w.shape[0], h.shape[1], True), dtype=torch.uint8,
-                         device=h.device)
+        dw = torch.empty(w.shape, dtype=w_dtype, device=w.device) if ctx.needs_input_grad[1] else None
         B.gbo_xent_backward(h, w, labels, lse, ws, dh=dh, dw=dw, row_weight=row_weight,
-                            upstream=up.float().reshape(1), logit_scale=logit_scale, z_loss=z_loss)
-        return dh, dw, None, None, None, None
+                            upstream=up.float().reshape(1), logit_scale=logit_scale, z_loss=z_loss, keep=True)
+        return dh, dw, None, None, None, None, None
 
 
 def rotary_autograd(x, positions, spec):
@@ -217,6 +222,9 @@ def qk_norm_rotary_autograd(q, k, q_gain, k_gain, positions, spec, eps=1e-6):
     return _QkNormRotary.apply(q, k, q_gain, k_gain, positions, spec, eps)
 
 
-def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_scale=1.0):
-    """Mean loss over the rows that count, with its gradients by ``h`` and ``w``."""
-    return _LinearCrossEntropy.apply(h, w, labels, row_weight, z_loss, logit_scale)
+def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_scale=1.0, workspace_cap=0):
+    """Mean loss over the rows that count, with its gradients by ``h`` (bf16) and ``w``
+    (bf16, or a float32 master table, which is cast for the products and gets a
+    float32 gradient).  Between the passes the workspace (``workspace_cap``) keeps the
+    logits in 16 bits where it has room for them."""
+    return _LinearCrossEntropy.apply(h, w, labels, row_weight, z_loss, logit_scale, workspace_cap)

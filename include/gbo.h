@@ -489,6 +489,10 @@ typedef struct {
   float z_loss;            /* 0 for none                                                       */
   int32_t label_dtype;     /* GBO_I32 | GBO_I64                                                */
   int32_t mean;            /* 1: divide by the sum of the weights of the rows that count       */
+  int32_t keep;            /* 1: gbo_xent_forward leaves its logits (16 bits each) in the workspace,
+                              where it has room for them, and gbo_xent_backward, given the same
+                              arguments and the workspace untouched, uses them                 */
+  int32_t reserved;        /* set to 0                                                         */
 } gbo_xent_args;
 
 typedef struct {
@@ -503,12 +507,15 @@ typedef struct {
 } gbo_xent_grads;
 
 /*
- * Bytes of device workspace.  grad 0: gbo_xent_forward.  grad 1:
- * gbo_xent_grad and gbo_xent_backward; these work through the vocabulary in
- * pieces whose gradients of the logits (bf16) fit the workspace they are
- * given: a larger workspace means fewer pieces.  cap > 0: the most that fits
- * in `cap` bytes; 0: pieces of 2 GiB.  0 when the arguments are out of range
- * or not even a piece of 256 columns fits the cap.
+ * Bytes of device workspace.  grad 0: gbo_xent_forward alone.  grad 1:
+ * gbo_xent_grad, gbo_xent_backward, and gbo_xent_forward with keep.  With
+ * room for the whole vocabulary's gradients of the logits (2 bytes each),
+ * the logits are kept there between the passes, in steps of 2^-9 bits from
+ * the label's; otherwise they are formed again, piece by piece of the
+ * vocabulary, each piece as wide as the workspace allows and 2 GiB at most
+ * (a third more tensor core work).  cap > 0: the most that fits in `cap` bytes; 0: kept logits up
+ * to 8 GiB, else pieces of 2 GiB.  0 when the arguments are out of range or
+ * not even a piece of 256 columns fits the cap.
  */
 size_t gbo_xent_workspace_bytes(int64_t n, int64_t v, int64_t d, int32_t grad, int64_t cap);
 

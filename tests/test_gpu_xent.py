@@ -296,15 +296,38 @@ def test_gradient_against_differences():
     assert abs(num - got) <= tol
 
 
-def test_autograd_matches_the_call():
-    H, W, y = inputs(96, 333, 64, 57, ignored=0.1)
-    Hg, Wg = H.clone().requires_grad_(), W.clone().requires_grad_()
-    loss = layers.linear_cross_entropy_loss(Hg, Wg, y, z_loss=1e-3)
-    (3.0 * loss).backward()
+@pytest.mark.parametrize("cap", ["keep", "pieces"])
+def test_autograd_matches_the_formula(cap):
+    """Logits kept from the forward pass, or formed again; bf16 weights and a float32
+    master table, whose gradient is float32."""
+    H, W, y = inputs(96, 1333, 64, 57, ignored=0.1)
     want = Want(H, W, y, z=1e-3, upstream=3.0)
-    close(loss.detach(), want.total / want.weight, want.total_tol / want.weight, torch.float32)
-    close(Hg.grad, want.dh, want.dh_tol, torch.bfloat16)
-    close(Wg.grad, want.dw, want.dw_tol, torch.bfloat16)
+    cap = 0 if cap == "keep" else smallest_cap(96, 1333, 64)
+    for master in (False, True):
+        Hg, Wg = H.clone().requires_grad_(), (W.float() if master else W.clone()).requires_grad_()
+        loss = layers.linear_cross_entropy_loss(Hg, Wg, y, z_loss=1e-3, workspace_cap=cap)
+        (3.0 * loss).backward()
+        close(loss.detach(), want.total / want.weight, want.total_tol / want.weight, torch.float32)
+        close(Hg.grad, want.dh, want.dh_tol, torch.bfloat16)
+        close(Wg.grad, want.dw, want.dw_tol, Wg.dtype)
+
+
+def test_kept_logits_between_two_calls():
+    """forward with keep, then backward on its workspace: the gradients of one call,
+    among them of tiles that are out of the kept range; other kernels in between."""
+    H, W, y = inputs(600, 1100, 72, 58, ignored=0.1)
+    H[300:310] *= 100
+    want = Want(H, W, y)
+    assert (want.loss > 50).any()
+    ws = torch.empty(B.gbo_xent_workspace_bytes(600, 1100, 72, True), dtype=torch.uint8, device="cuda")
+    loss, lse = torch.empty(600, device="cuda"), torch.empty(600, device="cuda")
+    B.gbo_xent_forward(H, W, y, ws, loss=loss, lse=lse, keep=True)
+    layers.linear_cross_entropy(W, H, torch.zeros(1100, dtype=torch.long, device="cuda"))
+    dh, dw = torch.empty_like(H), torch.empty_like(W)
+    B.gbo_xent_backward(H, W, y, lse, ws, dh=dh, dw=dw, keep=True)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(dh, want.dh, want.dh_tol, torch.bfloat16)
+    close(dw, want.dw, want.dw_tol, torch.bfloat16)
 
 
 def test_repeatable_on_a_stream_and_in_a_graph():
