@@ -115,6 +115,7 @@ struct XentParams {
   int64_t dh_stride, dw_stride, v0;
   int32_t v_piece, d;        // columns of this piece
   int32_t dh_f32, dw_f32, dh_vec, dw_vec, dw_add, first_piece, last_piece;
+  int32_t dw_tma;            // products: dW leaves through mapO
   int32_t splits, split_kit; // dH: cuts of its K axis (the piece's columns), stages in each
   int32_t keep;              // forward: store the logits
   int32_t only_redo;         // P: only the tiles of `redo`
@@ -123,9 +124,9 @@ struct XentParams {
   float scale, z;
 };
 
-__device__ __forceinline__ uint32_t idesc_of(bool a_mn, bool b_mn) {
+__device__ __forceinline__ uint32_t idesc_of(bool a_mn, bool b_mn, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-         ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 }
 
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -146,6 +147,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 struct XentItem {
   int tm, tn, kit, split;
+  int steps;  // K in steps of 16: the last stage is multiplied as far as K goes
+  int half;   // columns of B per CTA: 128, less in the last tile of d columns
   bool dw;
 };
 
@@ -195,16 +198,25 @@ __device__ __forceinline__ bool item_at(const XentPlan &q, const XentParams &P, 
     it.tn = r / gm;
     it.tm = g * kSweepTiles + r % gm;
     it.kit = (P.d + kStageK - 1) / kStageK;
+    it.steps = (P.d + 15) / 16;
+    it.half = BM;
     it.dw = false;
     return true;
   } else {
+    // products: the last tile of d columns multiplies no more than it holds
+    // (a multiple of 32 columns, half of them per CTA)
+    auto half_of = [&](int tn) { return min(BM, (P.d - tn * kTile + 31) / 32 * 16); };
     const int mine = q.dh_items / q.ncl + (q.cid < q.wide ? 1 : 0);
     if (k < mine) {
       const int t = q.cid + (int)k * q.ncl;
       it.split = t % P.splits;
       it.tn = t / P.splits % q.d_tiles;
       it.tm = t / P.splits / q.d_tiles;
-      it.kit = max(0, min(q.dh_kit, (P.v_piece + kStageK - 1) / kStageK - it.split * q.dh_kit));
+      const int k0 = it.split * q.dh_kit * kStageK;
+      const int len = max(0, min(q.dh_kit * kStageK, P.v_piece - k0));
+      it.kit = (len + kStageK - 1) / kStageK;
+      it.steps = (len + 15) / 16;
+      it.half = half_of(it.tn);
       it.dw = false;
       return true;
     }
@@ -221,6 +233,8 @@ __device__ __forceinline__ bool item_at(const XentPlan &q, const XentParams &P, 
     it.tm = (int)(t / q.d_tiles);
     it.tn = (int)(t % q.d_tiles);
     it.kit = q.dw_kit;
+    it.steps = (q.rows + 15) / 16;
+    it.half = half_of(it.tn);
     it.dw = true;
     return true;
   }
@@ -238,15 +252,18 @@ struct Ring {
 // columns when MN-major); ka0, kb0: where K begins in A and B.  Only the leader arms
 // the barrier, for both CTAs' bytes.
 template <bool kAmn, bool kBmn>
-__device__ __forceinline__ bool produce(const CUtensorMap *ma, const CUtensorMap *mb, int m0, int n0, int ka0, int kb0, int kit,
-                                        uint32_t smem, uint32_t full0, uint32_t empty0, uint32_t full_lead0,
+__device__ __forceinline__ bool produce(const CUtensorMap *ma, const CUtensorMap *mb, int m0, int n0, int ka0, int kb0,
+                                        int kit, int half, uint32_t smem, uint32_t full0, uint32_t empty0, uint32_t full_lead0,
                                         bool leader, Ring &ring, uint32_t *armed_parity, uint32_t &armed,
                                         volatile int32_t *abort_flag) {
+  // MN-major B: boxes of 64 columns
+  const int b_boxes = kBmn ? (half + 63) / 64 : 2;
+  const uint32_t bytes = 2u * (kStageBytes - 2u * 8192u * (uint32_t)(2 - b_boxes));
   for (int kb = 0; kb < kit; ++kb) {
     if (!mbar_wait(empty0 + 8 * ring.stage, ring.phase ^ 1)) return false;
     if (*abort_flag) return true;
     if (leader) {
-      mbar_expect_tx(full0 + 8 * ring.stage, 2u * kStageBytes);
+      mbar_expect_tx(full0 + 8 * ring.stage, bytes);
       armed |= 1u << ring.stage;
       armed_parity[ring.stage] = ring.phase;
     }
@@ -264,8 +281,7 @@ __device__ __forceinline__ bool produce(const CUtensorMap *ma, const CUtensorMap
       if constexpr (!kBmn) {
         tma_load_3d_pair(sb, mb, fb, kb0 + k, n0, 0);
       } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) tma_load_3d_pair(sb + h * 8192, mb, fb, n0 + h * 64, kb0 + k, 0);
+        for (int h = 0; h < b_boxes; ++h) tma_load_3d_pair(sb + h * 8192, mb, fb, n0 + h * 64, kb0 + k, 0);
       }
     }
     ring.next();
@@ -274,21 +290,22 @@ __device__ __forceinline__ bool produce(const CUtensorMap *ma, const CUtensorMap
 }
 
 template <bool kAmn, bool kBmn>
-__device__ __forceinline__ bool multiply(uint32_t smem, uint32_t full0, uint32_t empty0, uint32_t d_tmem, int kit,
-                                         Ring &ring, bool &issued) {
-  const uint32_t idesc = idesc_of(kAmn, kBmn);
+__device__ __forceinline__ bool multiply(uint32_t smem, uint32_t full0, uint32_t empty0, uint32_t d_tmem,
+                                         const XentItem &it, Ring &ring, bool &issued) {
+  const uint32_t idesc = idesc_of(kAmn, kBmn, 2 * it.half);
   const uint64_t a0 = smem_desc(smem, kAmn ? 8192 : 16, 1024);
   const uint64_t b0 = smem_desc(smem + kOpBytes, kBmn ? 8192 : 16, 1024);
   constexpr uint32_t astep = (kAmn ? 2048 : 32) >> 4, bstep = (kBmn ? 2048 : 32) >> 4;
-  for (int kb = 0; kb < kit; ++kb) {
+  for (int kb = 0; kb < it.kit; ++kb) {
     if (!mbar_wait(full0 + 8 * ring.stage, ring.phase)) return false;
     tc_fence_after();
+    const int left = it.steps - kb * (kStageK / 16);
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       const uint32_t off = (uint32_t)(ring.stage * kStageBytes + sub * kSubBytes) >> 4;
 #pragma unroll
       for (int k = 0; k < kBlockK / 16; ++k)
-        mma_pair(d_tmem, a0 + off + k * astep, b0 + off + k * bstep, idesc, (kb | sub | k) != 0);
+        if (sub * (kBlockK / 16) + k < left) mma_pair(d_tmem, a0 + off + k * astep, b0 + off + k * bstep, idesc, (kb | sub | k) != 0);
     }
     issued = true;
     mma_commit_pair_mc(empty0 + 8 * ring.stage, 0x3);
@@ -340,6 +357,33 @@ __device__ __forceinline__ void keep_block(const CUtensorMap *map, uint32_t stag
   __syncwarp();
   if (lane == 0) {
     tma_store_3d(map, dst, x0, y0, 0);
+    bulk_commit();
+  }
+}
+
+// Store, or add, a warp's 32 x 32 fp32 block (128-byte rows in the 128-byte
+// swizzle: 16-byte chunk q of row r at chunk q ^ (r & 7)).
+__device__ __forceinline__ void store_block_f32(const CUtensorMap *map, uint32_t stage, int &slot, const float (&v)[32],
+                                                bool add, int x0, int y0, int lane) {
+  const uint32_t dst = stage + (uint32_t)(slot * kSlotBytes);
+  slot ^= 1;
+  if (lane == 0) bulk_wait_read<1>();
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + lane * 128 + ((q ^ (lane & 7)) << 4)),
+                 "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
+                 : "memory");
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (add)
+      asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                       reinterpret_cast<uint64_t>(map)),
+                   "r"(dst), "r"(x0), "r"(y0), "r"(0)
+                   : "memory");
+    else
+      tma_store_3d(map, dst, x0, y0, 0);
     bulk_commit();
   }
 }
@@ -402,18 +446,18 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       XentItem it;
       for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
         if (kMode == kModeP && P.only_redo && !P.redo[it.tm]) continue;
-        const int m0 = it.tm * kTile + (int)crank * BM, n0 = it.tn * kTile + (int)crank * BM;
+        const int m0 = it.tm * kTile + (int)crank * BM, n0 = it.tn * kTile + (int)crank * it.half;
         bool ok;
         if constexpr (kMode != kModeProducts)
-          ok = produce<false, false>(&P.mapA, &P.mapB, m0, (int)P.v0 + n0, 0, 0, it.kit, ring0, full0, empty0,
+          ok = produce<false, false>(&P.mapA, &P.mapB, m0, (int)P.v0 + n0, 0, 0, it.kit, it.half, ring0, full0, empty0,
                                      full_lead0, leader, ring, armed_parity, armed, abort_flag);
         else if (!it.dw)
           ok = produce<false, true>(&P.mapA, &P.mapB, m0, n0, it.split * P.split_kit * kStageK,
-                                    (int)P.v0 + it.split * P.split_kit * kStageK, it.kit, ring0, full0, empty0,
+                                    (int)P.v0 + it.split * P.split_kit * kStageK, it.kit, it.half, ring0, full0, empty0,
                                     full_lead0, leader, ring, armed_parity, armed, abort_flag);
         else
-          ok = produce<true, true>(&P.mapA2, &P.mapB2, m0, n0, 0, 0, it.kit, ring0, full0, empty0, full_lead0, leader,
-                                   ring, armed_parity, armed, abort_flag);
+          ok = produce<true, true>(&P.mapA2, &P.mapB2, m0, n0, 0, 0, it.kit, it.half, ring0, full0, empty0, full_lead0,
+                                   leader, ring, armed_parity, armed, abort_flag);
         if (!ok) { give_up(); break; }
       }
       if (*abort_flag && leader) {  // copies armed here land before shared memory goes away
@@ -435,11 +479,11 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
         bool ok;
         if constexpr (kMode != kModeProducts)
-          ok = multiply<false, false>(ring0, full0, empty0, d_tmem, it.kit, ring, issued);
+          ok = multiply<false, false>(ring0, full0, empty0, d_tmem, it, ring, issued);
         else if (!it.dw)
-          ok = multiply<false, true>(ring0, full0, empty0, d_tmem, it.kit, ring, issued);
+          ok = multiply<false, true>(ring0, full0, empty0, d_tmem, it, ring, issued);
         else
-          ok = multiply<true, true>(ring0, full0, empty0, d_tmem, it.kit, ring, issued);
+          ok = multiply<true, true>(ring0, full0, empty0, d_tmem, it, ring, issued);
         if (!ok) { give_up(); break; }
         mma_commit_pair_mc(accf0 + 8 * acc, 0x3);
         if (++acc == 2) acc = 0, acc_phase ^= 1;
@@ -521,6 +565,21 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
           }
           tma_store_block(&P.mapO, stage, slot, v, false, col0, i0, 0, lane);
+        }
+      } else if (it.dw && P.dw_tma) {
+        // 32 x 32 blocks through the staging slots; what is added to dW (fp32)
+        // is added by the store
+        const float g = P.head->g;
+#pragma unroll 1
+        for (int ch = 0; ch < kTile / 32; ++ch) {
+          const int col0 = c0 + 32 * ch;
+          if (col0 >= P.d || i0 >= P.v_piece) break;
+          float v[32];
+          tmem_ld32(trow + ch * 32, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = it.kit > 0 ? g * v[j] : 0.f;  // no rows: nothing was multiplied
+          if (P.dw_f32) store_block_f32(&P.mapO, stage, slot, v, P.dw_add != 0, col0, (int)P.v0 + i0, lane);
+          else tma_store_block(&P.mapO, stage, slot, v, false, col0, (int)P.v0 + i0, 0, lane);
         }
       } else if (it.dw) {
         const float g = P.head->g;
@@ -1479,6 +1538,13 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
              map_2d(&Q.mapB, a->w, a->d, a->v, a->w_stride, 64, kBlockK) &&
              map_2d(&Q.mapA2, pbuf, P.v_piece, S.n_pad, S.piece, 64, kBlockK) &&
              map_2d(&Q.mapB2, R.hc, a->d, S.n_pad, a->d, 64, kBlockK);
+      // dW by TMA where its rows are 16-byte aligned (adding to bf16 stays with the
+      // threads: the sum is rounded once)
+      Q.dw_tma = P.dw && P.dw_vec && !(P.dw_add && !P.dw_f32);
+      if (Q.dw_tma)  // (a table too far apart for a map stays with the threads)
+        Q.dw_tma = P.dw_f32 ? encode_map(&Q.mapO, P.dw, a->d, a->v, 1, P.dw_stride, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B,
+                                         CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4)
+                            : map_2d(&Q.mapO, P.dw, a->d, a->v, P.dw_stride, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
       if (!maps) return xent_fail(GBO_ERR_CUDA, "tensor map of P");
       if (a->n > 0 && (e = launch_xent<kModeP>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) return cuda_err(e);
       const int64_t items = (P.dh ? m_tiles * d_tiles * S.splits : 0) + (P.dw ? n_tiles * d_tiles : 0);
