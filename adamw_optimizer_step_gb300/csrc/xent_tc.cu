@@ -894,11 +894,11 @@ struct RowsParams {
   XentHead *head;
   int32_t *idx, *lab;    // place -> row, label
   float *wt, *lse2, *ll2;
-  __nv_bfloat16 *hc;     // H by places
+  __nv_bfloat16 *hc;     // H by places, rows hc_stride apart
   float *loss, *lse;     // of rows left out: 0
   void *dh;
   int32_t *status;
-  int64_t n, v, d, h_stride, w_stride, dh_stride;
+  int64_t n, v, d, h_stride, w_stride, dh_stride, hc_stride;
   int64_t per_block;     // rows a block takes, a multiple of 8
   float scale2;
   int32_t *redo;         // per row tile, cleared; NULL: no logits will be kept
@@ -971,7 +971,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const __grid_constant__ 
     before += __popc(mask);
     if (mask >> warp & 1u) {
       const __nv_bfloat16 *src = R.h + i * R.h_stride, *lab = R.w + y * R.w_stride;
-      __nv_bfloat16 *dst = R.hc + p * R.d;
+      __nv_bfloat16 *dst = R.hc + p * R.hc_stride;
       float dot = 0.f;
 #pragma unroll 4
       for (int64_t c = 8 * lane; c < R.d; c += 256) {
@@ -1001,7 +1001,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const __grid_constant__ 
         for (int64_t c = lane; c < R.d; c += 32) st_elem(R.dh, R.dh_f32 ? GBO_F32 : GBO_BF16, i * R.dh_stride + c, 0.f);
     } else if (all + (i - R.n) < end) {
       const int64_t t = all + (i - R.n);
-      for (int64_t c = lane; c < R.d / 8; c += 32) reinterpret_cast<uint4 *>(R.hc + t * R.d)[c] = make_uint4(0, 0, 0, 0);
+      for (int64_t c = lane; c < R.d / 8; c += 32) reinterpret_cast<uint4 *>(R.hc + t * R.hc_stride)[c] = make_uint4(0, 0, 0, 0);
       if (lane == 0) R.idx[t] = 0, R.lab[t] = -1, R.wt[t] = 0.f, R.lse2[t] = 0.f, R.ll2[t] = 0.f;
     }
   }
@@ -1187,7 +1187,7 @@ int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // Scratch of a call, in this order.
 struct XentSpace {
   int64_t head, redo, idx, lab, wt, lse2, ll2, sums, hc, acc, part, p;  // byte offsets
-  int64_t n_pad, bytes;
+  int64_t n_pad, bytes, hc_ld;
   int64_t piece;            // columns of a piece of the vocabulary
   int32_t pieces;
   int32_t keep;             // logits are kept between the passes, in P's room
@@ -1221,7 +1221,9 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, boo
   s.lse2 = take(4 * s.n_pad);
   s.ll2 = take(4 * s.n_pad);
   s.sums = take(4 * s.n_pad);
-  s.hc = take(2 * s.n_pad * d);
+  // rows of whole 128-byte lines: TMA reads a row that straddles two lines as two
+  s.hc_ld = up_to(d, 64);
+  s.hc = take(2 * s.n_pad * s.hc_ld);
   // statistics: per vocabulary tile, or (few rows) per CTA and epilogue warp
   int64_t slots = (v + kTile - 1) / kTile;
   if (n <= kScoreRows) slots = std::max<int64_t>(slots, kEpiWarps * kMostSms);
@@ -1387,7 +1389,7 @@ int run_score(const gbo_xent_args *a, const XentParams &P, const RowsParams &R, 
   Q.w = R.w, Q.w_stride = a->w_stride, Q.v = (int32_t)a->v, Q.d = P.d, Q.scale2 = P.scale2;
   if (!map_2d(&Q.mapW, a->w, a->d, a->v, a->w_stride, kBlockK, BM) ||
       !map_2d(&Q.mapW16, a->w, a->d, a->v, a->w_stride, kBlockK, kScoreUnit) ||
-      !map_2d(&Q.mapH, R.hc, a->d, kTile, a->d, kBlockK, kScoreRows))
+      !map_2d(&Q.mapH, R.hc, a->d, kTile, R.hc_stride, kBlockK, kScoreRows))
     return xent_fail(GBO_ERR_CUDA, "tensor map of H or W");
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
@@ -1447,6 +1449,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
   R.status = status;
   R.n = a->n, R.v = a->v, R.d = a->d;
   R.h_stride = a->h_stride, R.w_stride = a->w_stride, R.dh_stride = g ? g->dh_stride : 0;
+  R.hc_stride = S.hc_ld;
   R.scale2 = a->logit_scale * kLog2e;
   R.labels64 = a->label_dtype == GBO_I64, R.mean = a->mean;
   R.dh_f32 = g && g->dh_dtype == GBO_F32;
@@ -1468,7 +1471,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
   const int64_t m_tiles = S.n_pad / kTile, d_tiles = (a->d + kTile - 1) / kTile;
   bool maps = true;
   if (a->n > 0) {
-    maps = map_2d(&P.mapA, R.hc, a->d, S.n_pad, a->d, kBlockK, BM) &&
+    maps = map_2d(&P.mapA, R.hc, a->d, S.n_pad, S.hc_ld, kBlockK, BM) &&
            map_2d(&P.mapB, a->w, a->d, a->v, a->w_stride, kBlockK, BM);
     if (!maps) return xent_fail(GBO_ERR_CUDA, "tensor map of H or W");
   }
@@ -1537,7 +1540,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
              map_2d(&Q.mapA, pbuf, P.v_piece, S.n_pad, S.piece, kBlockK, BM) &&
              map_2d(&Q.mapB, a->w, a->d, a->v, a->w_stride, 64, kBlockK) &&
              map_2d(&Q.mapA2, pbuf, P.v_piece, S.n_pad, S.piece, 64, kBlockK) &&
-             map_2d(&Q.mapB2, R.hc, a->d, S.n_pad, a->d, 64, kBlockK);
+             map_2d(&Q.mapB2, R.hc, a->d, S.n_pad, S.hc_ld, 64, kBlockK);
       // dW by TMA where its rows are 16-byte aligned (adding to bf16 stays with the
       // threads: the sum is rounded once)
       Q.dw_tma = P.dw && P.dw_vec && !(P.dw_add && !P.dw_f32);
