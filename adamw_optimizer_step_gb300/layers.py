@@ -3,7 +3,9 @@ positions, per-head q/k norms with rotation, and the tied classifier's cross
 entropy with its gradients.
 
 Each allocates its outputs and scratch with torch's allocator and makes one
-library call on the current stream.  ``rotary_autograd``, ``qk_norm_rotary_autograd``
+library call, on torch's current stream (under ``torch.cuda.stream(s)`` both the
+memory and the work belong to ``s``; the binding's functions take a stream and
+the caller's buffers).  ``rotary_autograd``, ``qk_norm_rotary_autograd``
 and ``linear_cross_entropy_loss`` are the same operators inside autograd, so
 that ``loss.backward()`` leaves the gradients that
 :class:`~.routing.HybridOptimizer` steps.
@@ -84,27 +86,27 @@ class RotarySpec:
 _like = torch.empty_like
 
 
-def rotary(x, positions, spec, *, inverse=False, out=None, stream=None):
+def rotary(x, positions, spec, *, inverse=False, out=None):
     """``x`` rotated (``inverse``: turned back, which is the rotation's gradient).
     ``out`` may be ``x``."""
     y = _like(x) if out is None else out
     if inverse:
-        B.gbo_rope_backward([dict(dy=x, y=y)], spec.opts, positions, None, stream)
+        B.gbo_rope_backward([dict(dy=x, y=y)], spec.opts, positions)
     else:
-        B.gbo_rope_forward([dict(x=x, y=y)], spec.opts, positions, stream)
+        B.gbo_rope_forward([dict(x=x, y=y)], spec.opts, positions)
     return y
 
 
-def qk_norm_rotary(q, k, q_gain, k_gain, positions, spec, *, eps=1e-6, stream=None):
+def qk_norm_rotary(q, k, q_gain, k_gain, positions, spec, *, eps=1e-6):
     """Queries and keys normed per head (root mean square, gain of head_dim float32
     values or None) and rotated, in one launch."""
     yq, yk = _like(q), _like(k)
     B.gbo_rope_forward([dict(x=q, y=yq, gain=q_gain, norm=True), dict(x=k, y=yk, gain=k_gain, norm=True)],
-                       spec.with_eps(eps), positions, stream)
+                       spec.with_eps(eps), positions)
     return yq, yk
 
 
-def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_gain, k_gain, positions, spec, *, eps=1e-6, stream=None):
+def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_gain, k_gain, positions, spec, *, eps=1e-6):
     """Gradients of :func:`qk_norm_rotary` by q, k and the gains (None where the gain is)."""
     dq, dk = _like(q), _like(k)
     dgq = torch.empty_like(q_gain) if q_gain is not None else None
@@ -113,25 +115,24 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_gain, k_gain, positions, spe
              dict(x=k, dy=dk_out, y=dk, gain=k_gain, dgain=dgk, norm=True)]
     opts = spec.with_eps(eps)
     ws = torch.empty(spec.backward_workspace(table), dtype=torch.uint8, device=q.device)
-    B.gbo_rope_backward(table, opts, positions, ws, stream)
+    B.gbo_rope_backward(table, opts, positions, ws)
     return dq, dk, dgq, dgk
 
 
 def linear_cross_entropy(h, w, labels, *, z_loss=0.0, logit_scale=1.0, lse=None, totals=None, row_weight=None,
-                         dev_status=None, stream=None):
+                         dev_status=None):
     """Loss of each row of ``h`` (n x d, bf16) against ``labels`` under the classifier
     ``w`` (v x d, bf16); rows with negative labels are left out (loss 0)."""
     n, d = h.shape
     loss = torch.empty(n, dtype=torch.float32, device=h.device)
     ws = torch.empty(B.gbo_xent_workspace_bytes(n, w.shape[0], d), dtype=torch.uint8, device=h.device)
     B.gbo_xent_forward(h, w, labels, ws, loss=loss, lse=lse, totals=totals, row_weight=row_weight,
-                       logit_scale=logit_scale, z_loss=z_loss, dev_status=dev_status, stream=stream)
+                       logit_scale=logit_scale, z_loss=z_loss, dev_status=dev_status)
     return loss
 
 
 def linear_cross_entropy_grad(h, w, labels, *, z_loss=0.0, logit_scale=1.0, mean=True, row_weight=None, upstream=None,
-                              dh=None, dw=None, accumulate_dw=False, totals=None, workspace_cap=0, dev_status=None,
-                              stream=None):
+                              dh=None, dw=None, accumulate_dw=False, totals=None, workspace_cap=0, dev_status=None):
     """(losses, dh, dw): the losses of :func:`linear_cross_entropy` and the gradients
     of their (weighted) mean, or sum with ``mean=False``, by ``h`` and ``w``, in one
     call.  ``dh``, ``dw``: buffers to write (bf16 or float32; with ``accumulate_dw``
@@ -145,7 +146,7 @@ def linear_cross_entropy_grad(h, w, labels, *, z_loss=0.0, logit_scale=1.0, mean
                      device=h.device)
     B.gbo_xent_grad(h, w, labels, ws, loss=loss, totals=totals, dh=dh, dw=dw, accumulate_dw=accumulate_dw,
                     row_weight=row_weight, upstream=upstream, mean=mean, logit_scale=logit_scale, z_loss=z_loss,
-                    dev_status=dev_status, stream=stream)
+                    dev_status=dev_status)
     return loss, dh, dw
 
 

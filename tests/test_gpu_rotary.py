@@ -272,7 +272,7 @@ def test_stream_and_graph():
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     y = torch.empty_like(x)
-    layers.rotary(x, pos, spec, out=y, stream=s)
+    B.gbo_rope_forward([dict(x=x, y=y)], spec.opts, pos, stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(y, want)
     torch.cuda.synchronize()

@@ -272,6 +272,16 @@ def test_strided_and_misaligned_rows():
     got = layers.linear_cross_entropy_grad(wide[:, 5:77], Wide[:, 8:80], y, dh=oh[:, 3:75], dw=ow[:, 1:73])
     assert torch.equal(got[0], loss) and torch.equal(oh[:, 3:75], dh) and torch.equal(ow[:, 1:73], dw)
     assert torch.all(oh[:, :3] == 0) and torch.all(ow[:, 73:] == 0) and torch.all(ow[:, 0] == 0)
+    # slices whose rows are 16-byte aligned, and added to where they are not
+    ow = torch.full((400, 88), 3.0, dtype=torch.bfloat16, device="cuda")
+    got = layers.linear_cross_entropy_grad(H, W, y, dw=ow[:, 8:80])
+    assert torch.equal(ow[:, 8:80], dw) and torch.all(ow[:, :8] == 3) and torch.all(ow[:, 80:] == 3)
+    _, _, dw32 = layers.linear_cross_entropy_grad(H, W, y, dw=torch.empty(400, 72, device="cuda"))
+    for width, first in ((96, 4), (75, 1)):
+        ow = torch.full((400, width), 3.0, device="cuda")
+        layers.linear_cross_entropy_grad(H, W, y, dw=ow[:, first:first + 72], accumulate_dw=True)
+        assert torch.equal(ow[:, first:first + 72], 3.0 + dw32)
+        assert torch.all(ow[:, :first] == 3) and torch.all(ow[:, first + 72:] == 3)
 
 
 def test_gradient_against_differences():
