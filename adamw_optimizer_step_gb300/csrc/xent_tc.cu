@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const __grid_constant__ 
   int all = 0, before = 0;
   float wsum = 0.f;
   bool bad = false;
-#pragma unroll 4
+#pragma unroll 8
   for (int64_t i = threadIdx.x; i < R.n; i += 256) {
     int64_t y;
     float w;
@@ -973,7 +973,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const __grid_constant__ 
       const __nv_bfloat16 *src = R.h + i * R.h_stride, *lab = R.w + y * R.w_stride;
       __nv_bfloat16 *dst = R.hc + p * R.hc_stride;
       float dot = 0.f;
-#pragma unroll 4
+#pragma unroll 8
       for (int64_t c = 8 * lane; c < R.d; c += 256) {
         float a[8], b[8];
         load8(src, GBO_BF16, c, 8, R.vec != 0, a);
@@ -1019,15 +1019,18 @@ struct LseParams {
   float z;
 };
 
-// Join the tiles' (maximum, sum) pairs of each row.  A block of 256 threads
-// takes 2^rows_log2 rows, consecutive threads consecutive rows, and 256 >>
-// rows_log2 strands of tiles; strands join in a fixed tree.
-__global__ void __launch_bounds__(256) xent_lse_kernel(const __grid_constant__ LseParams L) {
+constexpr int kLseThreads = 1024;
+
+// Join the tiles' (maximum, sum) pairs of each row.  A block takes
+// 2^rows_log2 rows, consecutive threads consecutive rows, and kLseThreads >>
+// rows_log2 strands of tiles; strands join in a fixed tree.  Latency bound:
+// 256 threads a block took 18 us for 8192 rows of 500 tiles.
+__global__ void __launch_bounds__(kLseThreads) xent_lse_kernel(const __grid_constant__ LseParams L) {
   pdl_launch();
-  __shared__ float2 red[256];
-  __shared__ float wl[256];
+  __shared__ float2 red[kLseThreads];
+  __shared__ float wl[kLseThreads];
   pdl_wait();
-  const int nr = 1 << L.rows_log2, strands = 256 >> L.rows_log2;
+  const int nr = 1 << L.rows_log2, strands = kLseThreads >> L.rows_log2;
   const int r = threadIdx.x & (nr - 1), strand = threadIdx.x >> L.rows_log2;
   const int rows = L.head->rows;
   const int64_t i = (int64_t)blockIdx.x * nr + r;
@@ -1501,7 +1504,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     L.part_ld = S.n_pad, L.tiles = (int32_t)n_tiles, L.z = a->z_loss;
     while (L.rows_log2 < 5 && (1 << L.rows_log2) < a->n) ++L.rows_log2;
     const int blocks = (int)((a->n + (1 << L.rows_log2) - 1) >> L.rows_log2);
-    if ((e = chain(xent_lse_kernel, dim3(blocks), dim3(256), st, L)) != cudaSuccess) return cuda_err(e);
+    if ((e = chain(xent_lse_kernel, dim3(blocks), dim3(kLseThreads), st, L)) != cudaSuccess) return cuda_err(e);
     if (totals && (e = chain(xent_totals_kernel, dim3(1), dim3(1024), st, TotalsParams{L.sums, R.head, totals, blocks})) !=
                       cudaSuccess)
       return cuda_err(e);
