@@ -164,11 +164,11 @@ def lib():
         "gbo_rope_backward": (c_int32, [c_void_p, c_int32, ctypes.POINTER(RopeOpts), c_int64, c_int64, c_void_p,
                                         c_void_p, c_size_t, c_void_p]),
         "gbo_xent_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int64]),
-        "gbo_xent_forward": (c_int32, [ctypes.POINTER(XentArgs), c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+        "gbo_xent_forward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                        c_void_p, c_void_p]),
-        "gbo_xent_backward": (c_int32, [ctypes.POINTER(XentArgs), c_void_p, ctypes.POINTER(XentGrads), c_void_p,
+        "gbo_xent_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p,
                                         c_size_t, c_void_p, c_void_p]),
-        "gbo_xent_grad": (c_int32, [ctypes.POINTER(XentArgs), c_void_p, c_void_p, c_void_p, ctypes.POINTER(XentGrads),
+        "gbo_xent_grad": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                     c_void_p, c_size_t, c_void_p, c_void_p]),
         "gbo_testing_wait_timeout": (c_int32, [c_void_p, ctypes.c_uint32, c_void_p]),
         "gbo_testing_set_small_chain": (c_int32, [c_int32]),
@@ -514,15 +514,15 @@ _ELEMENT = {torch.float32: GBO_F32, torch.bfloat16: GBO_BF16}
 _INDEX = {torch.int32: GBO_I32, torch.int64: GBO_I64}
 
 
-def _heads_of(t, what, like):
+def _heads_of(t, what, shape, dtype):
     """Strides of a (batch, seq, heads, dim) tensor whose head elements are consecutive."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % what)
-    if t.shape != like.shape or t.dtype != like.dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError("x, dy and y differ in shape or dtype")
     s = t.stride()
-    if s[3] != 1 and t.shape[3] > 1:
+    if s[3] != 1 and shape[3] > 1:
         raise ValueError("the elements of a head of %s must be consecutive" % what)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
     return s[:3]
 
 
@@ -550,13 +550,15 @@ def _rope_table(tensors, opts, positions):
             batch, seq = shape[0], shape[1]
         elif batch != shape[0] or seq != shape[1]:
             raise ValueError("the tensors of one call have the same batch and length")
-        if y.dtype not in _ELEMENT:
-            raise TypeError("tensor dtype must be float32 or bfloat16, got %s" % y.dtype)
+        dtype = y.dtype
+        if dtype not in _ELEMENT:
+            raise TypeError("tensor dtype must be float32 or bfloat16, got %s" % dtype)
         table += _PACK_ROPE_TENSOR(
             0 if x is None else x.data_ptr(), 0 if dy is None else dy.data_ptr(), y.data_ptr(),
             _rope_gain(get("gain"), "gain", dim), _rope_gain(get("dgain"), "dgain", dim),
-            *(_ZERO3 if x is None else _heads_of(x, "x", y)), *(_ZERO3 if dy is None else _heads_of(dy, "dy", y)),
-            *_heads_of(y, "y", y), shape[2], _ELEMENT[y.dtype], 1 if get("norm") else 0, 0)
+            *(_ZERO3 if x is None else _heads_of(x, "x", shape, dtype)),
+            *(_ZERO3 if dy is None else _heads_of(dy, "dy", shape, dtype)), *_heads_of(y, "y", shape, dtype), shape[2],
+            _ELEMENT[dtype], 1 if get("norm") else 0, 0)
     if isinstance(positions, int):
         return table, batch, seq, _PACK_ROPE_POSITIONS(0, 0, 0, positions, GBO_I64, 0)
     index = _INDEX.get(positions.dtype)
@@ -601,50 +603,51 @@ def gbo_xent_workspace_bytes(n, v, d, grad=False, cap=0):
     return int(lib().gbo_xent_workspace_bytes(int(n), int(v), int(d), int(bool(grad)), int(cap)))
 
 
-def _rows_of(t, what):
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be two-dimensional with consecutive row elements" % what)
+_PACK_XENT_ARGS = struct.Struct("@5P5q2f4i").pack     # XentArgs
+_PACK_XENT_GRADS = struct.Struct("@2P2q4i").pack      # XentGrads
+
+
+def _rows_of(t, what, shape=None):
+    """Row stride of a two-dimensional CUDA tensor with consecutive row elements."""
+    s = t.shape
+    if len(s) != 2 or (shape is not None and s != shape):
+        raise ValueError("%s must be two-dimensional%s" % (what, "" if shape is None else " %s" % (tuple(shape),)))
+    stride = t.stride()
+    if stride[1] != 1 and s[1] > 1:
+        raise ValueError("the row elements of %s must be consecutive" % what)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % what)
-    return t
-
-
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    return stride[0] if s[0] > 1 else max(s[1], stride[0])
 
 
 def _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean, keep=False):
-    _rows_of(h, "h"), _rows_of(w, "w")
+    """The packed arguments and the number of rows."""
+    h_stride, w_stride = _rows_of(h, "h"), _rows_of(w, "w")
     if h.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
         raise TypeError("h and w must be bfloat16")
-    if h.shape[1] != w.shape[1]:
+    n, d = h.shape
+    v, dw = w.shape
+    if d != dw:
         raise ValueError("h and w differ in width")
-    if labels.dtype not in (torch.int32, torch.int64):
+    index = _INDEX.get(labels.dtype)
+    if index is None:
         raise TypeError("labels must be int32 or int64")
-    n = h.shape[0]
     if labels.numel() != n:
         raise ValueError("one label per row of h")
-    for t, count, what in ((row_weight, n, "row_weight"), (upstream, 1, "upstream")):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != count):
-            raise ValueError("%s must be %d float32 values" % (what, count))
-    return XentArgs(h.data_ptr(), w.data_ptr(), _dev_ptr(labels, "labels"), _dev_ptr(row_weight, "row_weight"),
-                    _dev_ptr(upstream, "upstream"), n, w.shape[0], h.shape[1], _row_stride(h), _row_stride(w),
-                    float(logit_scale), float(z_loss), GBO_I64 if labels.dtype == torch.int64 else GBO_I32,
-                    int(bool(mean)), int(bool(keep)), 0)
+    weight = _out_f32(row_weight, n, "row_weight") or 0
+    up = _out_f32(upstream, 1, "upstream") or 0
+    return _PACK_XENT_ARGS(h.data_ptr(), w.data_ptr(), _dev_ptr(labels, "labels"), weight, up, n, v, d, h_stride, w_stride,
+                           logit_scale, z_loss, index, 1 if mean else 0, 1 if keep else 0, 0), n
 
 
 def _xent_grads(dh, dw, h, w, accumulate_dw):
-    g = XentGrads()
+    dh_ptr = dw_ptr = dh_stride = dw_stride = 0
+    dh_type = dw_type = GBO_BF16
     if dh is not None:
-        if _rows_of(dh, "dh").shape != h.shape:
-            raise ValueError("dh must have the shape of h")
-        g.dh, g.dh_stride, g.dh_dtype = dh.data_ptr(), _row_stride(dh), _dtype(dh)
+        dh_stride, dh_ptr, dh_type = _rows_of(dh, "dh", h.shape), dh.data_ptr(), _dtype(dh)
     if dw is not None:
-        if _rows_of(dw, "dw").shape != w.shape:
-            raise ValueError("dw must have the shape of w")
-        g.dw, g.dw_stride, g.dw_dtype = dw.data_ptr(), _row_stride(dw), _dtype(dw)
-    g.accumulate_dw = int(bool(accumulate_dw))
-    return g
+        dw_stride, dw_ptr, dw_type = _rows_of(dw, "dw", w.shape), dw.data_ptr(), _dtype(dw)
+    return _PACK_XENT_GRADS(dh_ptr, dw_ptr, dh_stride, dw_stride, dh_type, dw_type, 1 if accumulate_dw else 0, 0)
 
 
 def _out_f32(t, count, what):
@@ -658,8 +661,8 @@ def gbo_xent_forward(h, w, labels, workspace, *, loss=None, lse=None, totals=Non
     """Cross entropy of each row of ``h`` @ ``w``.T against ``labels`` into ``loss``,
     ``lse`` (n) and ``totals`` (2), whichever are given.  ``keep``: leave the logits
     in the workspace (of ``grad`` size) for gbo_xent_backward."""
-    a = _xent_args(h, w, labels, row_weight, None, logit_scale, z_loss, True, keep)
-    _check(lib().gbo_xent_forward(ctypes.byref(a), _out_f32(loss, a.n, "loss"), _out_f32(lse, a.n, "lse"),
+    a, n = _xent_args(h, w, labels, row_weight, None, logit_scale, z_loss, True, keep)
+    _check(lib().gbo_xent_forward(a, _out_f32(loss, n, "loss"), _out_f32(lse, n, "lse"),
                                   _out_f32(totals, 2, "totals"), _dev_ptr(workspace, "workspace"),
                                   workspace.numel() * workspace.element_size(), _dev_ptr(dev_status, "dev_status"),
                                   _stream(stream)))
@@ -669,9 +672,9 @@ def gbo_xent_backward(h, w, labels, lse, workspace, *, dh=None, dw=None, accumul
                       upstream=None, mean=True, logit_scale=1.0, z_loss=0.0, keep=False, dev_status=None, stream=None):
     """Gradients into ``dh`` and ``dw`` from the forward's ``lse`` (``keep``: and the
     logits that a forward with ``keep`` left in this workspace)."""
-    a = _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean, keep)
+    a, n = _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean, keep)
     g = _xent_grads(dh, dw, h, w, accumulate_dw)
-    _check(lib().gbo_xent_backward(ctypes.byref(a), _out_f32(lse, a.n, "lse"), ctypes.byref(g),
+    _check(lib().gbo_xent_backward(a, _out_f32(lse, n, "lse"), g,
                                    _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
                                    _dev_ptr(dev_status, "dev_status"), _stream(stream)))
 
@@ -680,10 +683,10 @@ def gbo_xent_grad(h, w, labels, workspace, *, loss=None, lse=None, totals=None, 
                   accumulate_dw=False, row_weight=None, upstream=None, mean=True, logit_scale=1.0, z_loss=0.0,
                   dev_status=None, stream=None):
     """Losses and gradients in one call."""
-    a = _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean)
+    a, n = _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean)
     g = _xent_grads(dh, dw, h, w, accumulate_dw)
-    _check(lib().gbo_xent_grad(ctypes.byref(a), _out_f32(loss, a.n, "loss"), _out_f32(lse, a.n, "lse"),
-                               _out_f32(totals, 2, "totals"), ctypes.byref(g), _dev_ptr(workspace, "workspace"),
+    _check(lib().gbo_xent_grad(a, _out_f32(loss, n, "loss"), _out_f32(lse, n, "lse"),
+                               _out_f32(totals, 2, "totals"), g, _dev_ptr(workspace, "workspace"),
                                workspace.numel() * workspace.element_size(), _dev_ptr(dev_status, "dev_status"),
                                _stream(stream)))
 

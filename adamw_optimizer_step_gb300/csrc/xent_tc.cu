@@ -65,8 +65,13 @@ constexpr int kOpBytes = BM * kBlockK * 2;     // 16 KB: 128 rows of A, or of B,
 constexpr int kSubBytes = 2 * kOpBytes;
 constexpr int kStageBytes = 2 * kSubBytes;
 constexpr int kStages = 3;
-constexpr int kEpiWarps = 4;
-constexpr int kWarpStage = 2 * kSlotBytes;     // two store slots a warp
+// Epilogue warps: two per TMEM lane quarter, 128 columns of the tile each.
+// With one, statistics, 16-bit logits and their store took 10,500 clocks a
+// tile, more than the products of a tile below d = 1300 (8 d clocks).
+constexpr int kEpiWarps = 8;
+constexpr int kSpan = kTile / (kEpiWarps / 4);  // columns of a warp
+constexpr int kBlockBytes = 2048;              // 32 x 32 16-bit values
+constexpr int kWarpStage = 2 * kBlockBytes;    // two store slots a warp, or one of fp32
 constexpr int kSmemUsed = kStages * kStageBytes + kEpiWarps * kWarpStage;
 constexpr int kXentSmem = 1024 + kSmemUsed + 256;
 constexpr int kXentThreads = 64 + 32 * kEpiWarps;
@@ -100,7 +105,7 @@ struct XentHead {
 struct XentParams {
   CUtensorMap mapA, mapB;    // logits: H, W (K-major); products: P K-major, W MN-major (dH)
   CUtensorMap mapA2, mapB2;  // products: P MN-major, H MN-major (dW)
-  CUtensorMap mapO;          // P, 32 x 32 boxes
+  CUtensorMap mapO;          // stores: kept logits, P or dW, 32 x 32 boxes
   const XentHead *head;
   const int32_t *idx, *lab;  // place -> row, label; up to a whole tile
   const float *wt, *lse2;    // weight (0: padding), lse in bits
@@ -158,7 +163,7 @@ struct XentPlan {
   int dh_items, dw_items, d_tiles;  // products
   int dh_kit, dw_kit;
   int ncl, cid;
-  int extra, wide;                  // products: see item_at
+  int extra, wide, mine;            // products: see item_at
 };
 
 template <int kMode>
@@ -175,6 +180,7 @@ __device__ __forceinline__ XentPlan make_plan(const XentParams &P, int cid, int 
   q.ncl = ncl;
   q.cid = cid;
   q.wide = q.dh_items % ncl;
+  q.mine = q.dh_items / ncl + (cid < q.wide ? 1 : 0);
   q.extra = q.wide ? (q.dh_kit + q.dw_kit / 2) / max(1, q.dw_kit) : 0;
   return q;
 }
@@ -191,12 +197,18 @@ __device__ __forceinline__ bool item_at(const XentPlan &q, const XentParams &P, 
   if constexpr (kMode != kModeProducts) {
     const int64_t t = q.cid + k * q.ncl;
     if (t >= (int64_t)q.m_tiles * q.n_tiles) return false;
-    const int64_t sweep = (int64_t)kSweepTiles * q.n_tiles;
-    const int g = (int)(t / sweep);
-    const int r = (int)(t - g * sweep);
-    const int gm = min(kSweepTiles, q.m_tiles - g * kSweepTiles);
-    it.tn = r / gm;
-    it.tm = g * kSweepTiles + r % gm;
+    // (a sweep has fewer than 2^31 items; 64-bit divisions took a quarter of the item's time)
+    uint32_t g = 0, r;
+    if (q.m_tiles <= kSweepTiles) {
+      r = (uint32_t)t;
+    } else {
+      const int64_t sweep = (int64_t)kSweepTiles * q.n_tiles;
+      g = (uint32_t)(t / sweep);
+      r = (uint32_t)(t - g * sweep);
+    }
+    const uint32_t gm = (uint32_t)min(kSweepTiles, q.m_tiles - (int)g * kSweepTiles);
+    it.tn = (int)(r / gm);
+    it.tm = (int)(g * kSweepTiles + r % gm);
     it.kit = (P.d + kStageK - 1) / kStageK;
     it.steps = (P.d + 15) / 16;
     it.half = BM;
@@ -206,12 +218,11 @@ __device__ __forceinline__ bool item_at(const XentPlan &q, const XentParams &P, 
     // products: the last tile of d columns multiplies no more than it holds
     // (a multiple of 32 columns, half of them per CTA)
     auto half_of = [&](int tn) { return min(BM, (P.d - tn * kTile + 31) / 32 * 16); };
-    const int mine = q.dh_items / q.ncl + (q.cid < q.wide ? 1 : 0);
-    if (k < mine) {
-      const int t = q.cid + (int)k * q.ncl;
-      it.split = t % P.splits;
-      it.tn = t / P.splits % q.d_tiles;
-      it.tm = t / P.splits / q.d_tiles;
+    if (k < q.mine) {
+      const uint32_t t = (uint32_t)(q.cid + (int)k * q.ncl), u = t / (uint32_t)P.splits;
+      it.split = (int)(t - u * (uint32_t)P.splits);
+      it.tm = (int)(u / (uint32_t)q.d_tiles);
+      it.tn = (int)(u - (uint32_t)it.tm * (uint32_t)q.d_tiles);
       const int k0 = it.split * q.dh_kit * kStageK;
       const int len = max(0, min(q.dh_kit * kStageK, P.v_piece - k0));
       it.kit = (len + kStageK - 1) / kStageK;
@@ -220,7 +231,7 @@ __device__ __forceinline__ bool item_at(const XentPlan &q, const XentParams &P, 
       it.dw = false;
       return true;
     }
-    k -= mine;
+    k -= q.mine;
     const int64_t narrow = q.ncl - q.wide, head = (int64_t)q.extra * narrow;
     int64_t t;
     if (q.cid >= q.wide && k < q.extra) {
@@ -230,8 +241,8 @@ __device__ __forceinline__ bool item_at(const XentPlan &q, const XentParams &P, 
       t = head + q.cid + k * q.ncl;
     }
     if (t >= q.dw_items) return false;
-    it.tm = (int)(t / q.d_tiles);
-    it.tn = (int)(t % q.d_tiles);
+    it.tm = (int)((uint32_t)t / (uint32_t)q.d_tiles);
+    it.tn = (int)((uint32_t)t - (uint32_t)it.tm * (uint32_t)q.d_tiles);
     it.kit = q.dw_kit;
     it.steps = (q.rows + 15) / 16;
     it.half = half_of(it.tn);
@@ -328,16 +339,9 @@ __device__ __forceinline__ void softmax_add(const float (&t)[32], float &m, floa
   m = mn;
 }
 
-// Store a warp's 32 x 32 block of logits (in bits) as 16-bit steps from the
-// row's label's logit, through the next of its two staging slots.  A float
+// 32 logits (in bits) as 16-bit steps from the row's label's logit.  A float
 // of 1.5 2^23 plus an integer holds that integer in its low bits.
-__device__ __forceinline__ void keep_block(const CUtensorMap *map, uint32_t stage, int &slot, const float (&v)[32],
-                                           float ll2, int x0, int y0, int lane) {
-  const uint32_t dst = stage + (uint32_t)(slot * kSlotBytes);
-  slot ^= 1;
-  if (lane == 0) bulk_wait_read<1>();
-  __syncwarp();
-  uint32_t w[16];
+__device__ __forceinline__ void pack_steps(const float (&v)[32], float ll2, uint32_t (&w)[16]) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     uint32_t h[2];
@@ -348,6 +352,21 @@ __device__ __forceinline__ void keep_block(const CUtensorMap *map, uint32_t stag
     }
     w[k] = __byte_perm(h[0], h[1], 0x5410);
   }
+}
+
+__device__ __forceinline__ void pack_row(const float (&v)[32], uint32_t (&w)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+}
+
+// Store a warp's 32 x 32 block of 16-bit values through the next of its two
+// slots (64-byte rows in the 64-byte swizzle).
+__device__ __forceinline__ void store_block(const CUtensorMap *map, uint32_t stage, int &slot, const uint32_t (&w)[16],
+                                            int x0, int y0, int lane) {
+  const uint32_t dst = stage + (uint32_t)(slot * kBlockBytes);
+  slot ^= 1;
+  if (lane == 0) bulk_wait_read<1>();  // the store that last used this slot has read it
+  __syncwarp();
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + sw64(lane, q)), "r"(w[4 * q]),
@@ -361,13 +380,11 @@ __device__ __forceinline__ void keep_block(const CUtensorMap *map, uint32_t stag
   }
 }
 
-// Store, or add, a warp's 32 x 32 fp32 block (128-byte rows in the 128-byte
-// swizzle: 16-byte chunk q of row r at chunk q ^ (r & 7)).
-__device__ __forceinline__ void store_block_f32(const CUtensorMap *map, uint32_t stage, int &slot, const float (&v)[32],
-                                                bool add, int x0, int y0, int lane) {
-  const uint32_t dst = stage + (uint32_t)(slot * kSlotBytes);
-  slot ^= 1;
-  if (lane == 0) bulk_wait_read<1>();
+// Store, or add, a warp's 32 x 32 fp32 block, which takes both slots (128-byte
+// rows in the 128-byte swizzle: 16-byte chunk q of row r at chunk q ^ (r & 7)).
+__device__ __forceinline__ void store_block_f32(const CUtensorMap *map, uint32_t dst, const float (&v)[32], bool add,
+                                                int x0, int y0, int lane) {
+  if (lane == 0) bulk_wait_read<0>();
   __syncwarp();
 #pragma unroll
   for (int q = 0; q < 8; ++q)
@@ -494,7 +511,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       }
     }
   } else {
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t stage = smem_u32(smem + kStages * kStageBytes + (warp - 2) * kWarpStage);
     int slot = 0, acc = 0;
     uint32_t acc_phase = 0;
@@ -502,7 +519,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
     for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
       if (kMode == kModeP && P.only_redo && !P.redo[it.tm]) continue;
       const int i0 = it.tm * kTile + (int)crank * BM + quarter * 32, i = i0 + lane;
-      const int c0 = it.tn * kTile;
+      const int c0 = it.tn * kTile + part * kSpan;
       // per-row values of this tile, fetched while its products run
       int lab = -1;
       float wt = 0.f, lse2 = 0.f, ll2 = 0.f;
@@ -514,12 +531,12 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       }
       if (!mbar_wait(accf0 + 8 * acc, acc_phase)) { give_up(); break; }
       tc_fence_after();
-      const uint32_t trow = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile);
+      const uint32_t trow = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile + part * kSpan);
       if constexpr (kMode == kModeStats) {
         if (i0 < q.rows || P.keep) {  // (rows behind the last one are stored too: their P is set to 0 later)
           float m = -INFINITY, s = 0.f;
 #pragma unroll 1
-          for (int ch = 0; ch < kTile / 32; ++ch) {
+          for (int ch = 0; ch < kSpan / 32; ++ch) {
             const int col0 = c0 + 32 * ch;
             if (col0 >= P.v_piece) break;
             float v[32];
@@ -535,19 +552,23 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
               for (int j = 0; j < 32; ++j)
                 if (col0 + j >= P.v_piece) v[j] = -INFINITY;
             }
-            if (P.keep) keep_block(&P.mapO, stage, slot, v, ll2, col0, i0, lane);
+            if (P.keep) {
+              uint32_t w[16];
+              pack_steps(v, ll2, w);
+              store_block(&P.mapO, stage, slot, w, col0, i0, lane);
+            }
             softmax_add(v, m, s);
           }
           if (P.keep && i < q.rows && !(m - ll2 <= kKeepMost && s < INFINITY)) {
             P.redo[it.tm] = 1;  // every writer writes the same
             P.head_out->redo = 1;
           }
-          if (i < q.rows) P.part[(int64_t)it.tn * P.part_ld + i] = make_float2(m, s);
+          if (i < q.rows && c0 < P.v_piece) P.part[(int64_t)(it.tn * (kTile / kSpan) + part) * P.part_ld + i] = make_float2(m, s);
         }
       } else if constexpr (kMode == kModeP) {
         const float mult = wt * P.scale, peak = mult * fmaf(2.f * P.z, lse2 * kLn2, 1.f);
 #pragma unroll 1
-        for (int ch = 0; ch < kTile / 32; ++ch) {
+        for (int ch = 0; ch < kSpan / 32; ++ch) {
           const int col0 = c0 + 32 * ch;
           if (col0 >= P.v_piece) break;
           float v[32];
@@ -564,29 +585,35 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
           }
-          tma_store_block(&P.mapO, stage, slot, v, false, col0, i0, 0, lane);
+          uint32_t w[16];
+          pack_row(v, w);
+          store_block(&P.mapO, stage, slot, w, col0, i0, lane);
         }
       } else if (it.dw && P.dw_tma) {
-        // 32 x 32 blocks through the staging slots; what is added to dW (fp32)
-        // is added by the store
+        // through the staging slots; what is added to dW (fp32) is added by the store
         const float g = P.head->g;
 #pragma unroll 1
-        for (int ch = 0; ch < kTile / 32; ++ch) {
+        for (int ch = 0; ch < kSpan / 32; ++ch) {
           const int col0 = c0 + 32 * ch;
           if (col0 >= P.d || i0 >= P.v_piece) break;
           float v[32];
           tmem_ld32(trow + ch * 32, v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = it.kit > 0 ? g * v[j] : 0.f;  // no rows: nothing was multiplied
-          if (P.dw_f32) store_block_f32(&P.mapO, stage, slot, v, P.dw_add != 0, col0, (int)P.v0 + i0, lane);
-          else tma_store_block(&P.mapO, stage, slot, v, false, col0, (int)P.v0 + i0, 0, lane);
+          if (P.dw_f32) {
+            store_block_f32(&P.mapO, stage, v, P.dw_add != 0, col0, (int)P.v0 + i0, lane);
+          } else {
+            uint32_t w[16];
+            pack_row(v, w);
+            store_block(&P.mapO, stage, slot, w, col0, (int)P.v0 + i0, lane);
+          }
         }
       } else if (it.dw) {
         const float g = P.head->g;
         const int64_t row = P.v0 + i;
         const bool ok = i < P.v_piece;
 #pragma unroll 1
-        for (int ch = 0; ch < kTile / 32; ++ch) {
+        for (int ch = 0; ch < kSpan / 32; ++ch) {
           const int col0 = c0 + 32 * ch;
           if (col0 >= P.d || i0 >= P.v_piece) break;
           float v[32];
@@ -622,7 +649,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         const bool ok = i < q.rows;
         const int64_t row = ok ? P.idx[i] : 0;
 #pragma unroll 1
-        for (int ch = 0; ch < kTile / 32; ++ch) {
+        for (int ch = 0; ch < kSpan / 32; ++ch) {
           const int col0 = c0 + 32 * ch;
           if (col0 >= P.d || i0 >= q.rows) break;
           float v[32];
@@ -692,6 +719,7 @@ constexpr int kScoreB = kScoreRows * kBlockK * 2;                // 4 KB: H's ro
 constexpr int kScoreStage = 2 * (kOpBytes + kScoreB);
 constexpr int kScoreStages = 5;
 constexpr int kScoreSmem = 1024 + kScoreStages * kScoreStage + 256 + kScoreRows * 8;
+constexpr int kScoreWarps = 4;                                   // epilogue
 constexpr int kScoreTmem = 64;                                   // two 128 x 32 accumulators
 static_assert(kScoreSmem <= 232448, "shared memory per CTA");
 
@@ -727,7 +755,7 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
   const int tiles = (run + BM - 1) / BM, kit = (P.d + kStageK - 1) / kStageK;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kScoreStages; ++s) mbar_init(full0 + 8 * s, 1), mbar_init(empty0 + 8 * s, 1);
-    for (int a = 0; a < 2; ++a) mbar_init(accf0 + 8 * a, 1), mbar_init(acce0 + 8 * a, kEpiWarps);
+    for (int a = 0; a < 2; ++a) mbar_init(accf0 + 8 * a, 1), mbar_init(acce0 + 8 * a, kScoreWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -872,7 +900,7 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
           s[j] = s[j] * exp2_fast(m[j] - at) + s2 * exp2_fast(m2 - at);
           m[j] = mn;
         }
-        if (lane == 0) P.part[((int64_t)blockIdx.x * kEpiWarps + quarter) * P.part_ld + j] = make_float2(m[j], s[j]);
+        if (lane == 0) P.part[((int64_t)blockIdx.x * kScoreWarps + quarter) * P.part_ld + j] = make_float2(m[j], s[j]);
       }
     }
   }
@@ -1172,6 +1200,7 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ 
   const int64_t row = J.idx[i] * J.dh_stride;
   for (int64_t c = 4 * threadIdx.x; c < J.d; c += 1024) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int s = 0; s < J.splits; ++s) {
       const float4 b = *reinterpret_cast<const float4 *>(J.acc + s * J.acc_ld + i * J.d + c);
       a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
@@ -1192,6 +1221,7 @@ struct XentSpace {
   int64_t head, redo, idx, lab, wt, lse2, ll2, sums, hc, acc, part, p;  // byte offsets
   int64_t n_pad, bytes, hc_ld;
   int64_t piece;            // columns of a piece of the vocabulary
+  int64_t ld;               // elements of a row of P: an odd number of 128-byte lines
   int32_t pieces;
   int32_t keep;             // logits are kept between the passes, in P's room
   int32_t splits, split_kit;
@@ -1227,9 +1257,9 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, boo
   // rows of whole 128-byte lines: TMA reads a row that straddles two lines as two
   s.hc_ld = up_to(d, 64);
   s.hc = take(2 * s.n_pad * s.hc_ld);
-  // statistics: per vocabulary tile, or (few rows) per CTA and epilogue warp
-  int64_t slots = (v + kTile - 1) / kTile;
-  if (n <= kScoreRows) slots = std::max<int64_t>(slots, kEpiWarps * kMostSms);
+  // statistics: per epilogue warp's columns, or (few rows) per CTA and epilogue warp
+  int64_t slots = (v + kSpan - 1) / kSpan;
+  if (n <= kScoreRows) slots = std::max<int64_t>(slots, kScoreWarps * kMostSms);
   const int64_t part = forward ? 8 * s.n_pad * slots : 0;
   if (!grad) {
     s.part = take(part);
@@ -1254,11 +1284,14 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, boo
   s.split_kit = (int32_t)((dh_kit + splits - 1) / splits);
   s.splits = (int32_t)((dh_kit + s.split_kit - 1) / s.split_kit);
   s.acc = take(s.pieces > 1 || s.splits > 1 ? 4 * s.splits * s.n_pad * d : 0);
+  // dW reads P by columns: rows a power of two apart would all lie in the same
+  // few memory channels
+  s.ld = s.piece + 64;
   if (keep) {
     s.part = take(part);
-    s.p = take(2 * s.n_pad * s.piece);
+    s.p = take(2 * s.n_pad * s.ld);
   } else {
-    s.part = s.p = take(std::max(part, 2 * s.n_pad * s.piece));
+    s.part = s.p = take(std::max(part, 2 * s.n_pad * s.ld));
   }
   s.bytes = at;
   return s;
@@ -1483,16 +1516,17 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     P.keep = S.keep;
     if (S.keep) {
       P.redo = redo, P.head_out = R.head;
-      if (!map_2d(&P.mapO, ws + S.p, a->v, S.n_pad, S.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+      if (!map_2d(&P.mapO, ws + S.p, a->v, S.n_pad, S.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
         return xent_fail(GBO_ERR_CUDA, "tensor map of the logits");
     }
     P.part_ld = S.n_pad;
     P.v0 = 0, P.v_piece = (int32_t)a->v;
-    int64_t n_tiles = (a->v + kTile - 1) / kTile;
+    const int64_t n_tiles = (a->v + kTile - 1) / kTile;
+    int64_t slots = (a->v + kSpan - 1) / kSpan;
     if (a->n <= kScoreRows && !S.keep) {
       int blocks = 0;
       if ((rc = run_score(a, P, R, sm, st, &blocks)) != GBO_OK) return rc;
-      n_tiles = (int64_t)kEpiWarps * blocks;
+      slots = (int64_t)kScoreWarps * blocks;
     } else if ((e = launch_xent<kModeStats>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) {
       return cuda_err(e);
     }
@@ -1501,7 +1535,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     L.lse2 = R.lse2, L.loss = loss, L.lse = lse;
     L.sums = totals ? reinterpret_cast<float *>(ws + S.sums) : nullptr;
     L.status = status;
-    L.part_ld = S.n_pad, L.tiles = (int32_t)n_tiles, L.z = a->z_loss;
+    L.part_ld = S.n_pad, L.tiles = (int32_t)slots, L.z = a->z_loss;
     while (L.rows_log2 < 5 && (1 << L.rows_log2) < a->n) ++L.rows_log2;
     const int blocks = (int)((a->n + (1 << L.rows_log2) - 1) >> L.rows_log2);
     if ((e = chain(xent_lse_kernel, dim3(blocks), dim3(kLseThreads), st, L)) != cudaSuccess) return cuda_err(e);
@@ -1526,7 +1560,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     if (S.keep && a->n > 0) {
       ConvertParams C = {};
       C.head = R.head, C.redo = redo, C.lab = R.lab, C.wt = R.wt, C.lse2 = R.lse2, C.ll2 = R.ll2;
-      C.p = static_cast<uint16_t *>(pbuf), C.ld = S.piece, C.v = (int32_t)a->v;
+      C.p = static_cast<uint16_t *>(pbuf), C.ld = S.ld, C.v = (int32_t)a->v;
       C.scale = a->logit_scale, C.z = a->z_loss;
       const int64_t blocks = (a->v + kConvertCols - 1) / kConvertCols * S.n_pad;
       if (blocks > INT32_MAX) return xent_fail(GBO_ERR_SHAPE, "more kept logits than one launch takes: cap the workspace");
@@ -1539,10 +1573,10 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
       P.first_piece = c == 0, P.last_piece = c + 1 == S.pieces;
       const int64_t n_tiles = (P.v_piece + kTile - 1) / kTile;
       XentParams Q = P;
-      maps = map_2d(&P.mapO, pbuf, P.v_piece, S.n_pad, S.piece, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
-             map_2d(&Q.mapA, pbuf, P.v_piece, S.n_pad, S.piece, kBlockK, BM) &&
+      maps = map_2d(&P.mapO, pbuf, P.v_piece, S.n_pad, S.ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
+             map_2d(&Q.mapA, pbuf, P.v_piece, S.n_pad, S.ld, kBlockK, BM) &&
              map_2d(&Q.mapB, a->w, a->d, a->v, a->w_stride, 64, kBlockK) &&
-             map_2d(&Q.mapA2, pbuf, P.v_piece, S.n_pad, S.piece, 64, kBlockK) &&
+             map_2d(&Q.mapA2, pbuf, P.v_piece, S.n_pad, S.ld, 64, kBlockK) &&
              map_2d(&Q.mapB2, R.hc, a->d, S.n_pad, S.hc_ld, 64, kBlockK);
       // dW by TMA where its rows are 16-byte aligned (adding to bf16 stays with the
       // threads: the sum is rounded once)

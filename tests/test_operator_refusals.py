@@ -232,16 +232,16 @@ def test_cross_entropy_null_and_misaligned(L):
 
 def test_cross_entropy_workspace_sizes():
     size = B.gbo_xent_workspace_bytes
-    # losses alone: a copy of the rows and 8 bytes per row and 256 columns
+    # losses alone: a copy of the rows and 8 bytes per row and 128 columns
     n, v, d = 8192, 128000, 2048
     forward = size(n, v, d)
-    assert 2 * n * d + 8 * n * v // 256 <= forward <= 1.02 * (2 * n * d + 8 * n * v // 256)
+    assert 2 * n * d + 8 * n * v // 128 <= forward <= 1.02 * (2 * n * d + 8 * n * v // 128)
     # gradients: 2 bytes a logit, kept whole up to 8 GiB
     assert size(n, v, d, True) >= forward + 2 * n * v
     # more rows: pieces of at most 2 GiB (beside the row copy, the fp32 sums and statistics)
     n = 65536
     big = size(n, v, d, True)
-    assert big < (2 << 30) + 2 * n * d + 4 * n * d + 64 * n + 8 * n * v // 256
+    assert big < (2 << 30) + 2 * n * d + 4 * n * d + 256 * n + 8 * n * v // 128
     # a cap is kept to, and the least one is a piece of 256 columns
     for cap in (1 << 30, 1 << 31, 1 << 32, 1 << 34):
         got = size(n, v, d, True, cap)
