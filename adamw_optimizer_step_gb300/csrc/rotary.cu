@@ -492,6 +492,7 @@ __global__ void __launch_bounds__(1024) rope_dgain_kernel(const __grid_constant_
   if (!S.dgain[ti]) return;
   float a = 0.f;
   if (col < S.dim)
+#pragma unroll 4
     for (int r = threadIdx.y; r < S.rows[ti]; r += 32) a += S.part[ti][(int64_t)r * S.dim + col];
   red[threadIdx.y][threadIdx.x] = a;
   __syncthreads();

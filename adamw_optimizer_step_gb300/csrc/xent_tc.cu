@@ -163,8 +163,12 @@ struct XentPlan {
   int dh_items, dw_items, d_tiles;  // products
   int dh_kit, dw_kit;
   int ncl, cid;
-  int extra, wide, mine;            // products: see item_at
+  int extra, wide, mine;            // products: see Walk
 };
+
+// What an item of `kit` stages costs, in stages: its epilogue takes 5 of them
+// where its products take less, and another goes to its start and end.
+__host__ __device__ __forceinline__ int item_cost(int kit) { return (kit < 5 ? 5 : kit) + 1; }
 
 template <int kMode>
 __device__ __forceinline__ XentPlan make_plan(const XentParams &P, int cid, int ncl) {
@@ -181,75 +185,112 @@ __device__ __forceinline__ XentPlan make_plan(const XentParams &P, int cid, int 
   q.cid = cid;
   q.wide = q.dh_items % ncl;
   q.mine = q.dh_items / ncl + (cid < q.wide ? 1 : 0);
-  q.extra = q.wide ? (q.dh_kit + q.dw_kit / 2) / max(1, q.dw_kit) : 0;
+  const int dw_cost = item_cost(q.dw_kit);
+  q.extra = q.wide ? (item_cost(q.dh_kit) + dw_cost / 2) / dw_cost : 0;
   return q;
 }
 
-// Item k of this pair; false: there is none.
+// The items of this pair, one after another.
 //   logits: round-robin over the pairs; a sweep of kSweepTiles row tiles
 //     takes the vocabulary tile by tile.
-//   products: dH items (K = the piece's width, or a cut of it) first, round-robin; `wide`
-//     pairs get one more than the others, who therefore take `extra` dW items
-//     (K = rows) of the same total length first; the rest of dW is dealt to
-//     all.  Items are independent, so the split changes no result.
+//   products: dH items (K = the piece's width, or a cut of it) first, round-robin;
+//     `wide` pairs get one more than the others, who therefore take `extra`
+//     dW items (K = rows) of the same total length first; the rest of dW is
+//     dealt to all.  Items are independent, so the split changes no result.
+// Tile coordinates advance by the step's quotient and remainder: a division
+// per item and role took 1000 clocks, a sixth of a short item.
 template <int kMode>
-__device__ __forceinline__ bool item_at(const XentPlan &q, const XentParams &P, int64_t k, XentItem &it) {
-  if constexpr (kMode != kModeProducts) {
-    const int64_t t = q.cid + k * q.ncl;
-    if (t >= (int64_t)q.m_tiles * q.n_tiles) return false;
-    // (a sweep has fewer than 2^31 items; 64-bit divisions took a quarter of the item's time)
-    uint32_t g = 0, r;
-    if (q.m_tiles <= kSweepTiles) {
-      r = (uint32_t)t;
-    } else {
-      const int64_t sweep = (int64_t)kSweepTiles * q.n_tiles;
-      g = (uint32_t)(t / sweep);
-      r = (uint32_t)(t - g * sweep);
-    }
-    const uint32_t gm = (uint32_t)min(kSweepTiles, q.m_tiles - (int)g * kSweepTiles);
-    it.tn = (int)(r / gm);
-    it.tm = (int)(g * kSweepTiles + r % gm);
-    it.kit = (P.d + kStageK - 1) / kStageK;
-    it.steps = (P.d + 15) / 16;
-    it.half = BM;
-    it.dw = false;
-    return true;
-  } else {
-    // products: the last tile of d columns multiplies no more than it holds
-    // (a multiple of 32 columns, half of them per CTA)
-    auto half_of = [&](int tn) { return min(BM, (P.d - tn * kTile + 31) / 32 * 16); };
-    if (k < q.mine) {
-      const uint32_t t = (uint32_t)(q.cid + (int)k * q.ncl), u = t / (uint32_t)P.splits;
-      it.split = (int)(t - u * (uint32_t)P.splits);
-      it.tm = (int)(u / (uint32_t)q.d_tiles);
-      it.tn = (int)(u - (uint32_t)it.tm * (uint32_t)q.d_tiles);
-      const int k0 = it.split * q.dh_kit * kStageK;
-      const int len = max(0, min(q.dh_kit * kStageK, P.v_piece - k0));
-      it.kit = (len + kStageK - 1) / kStageK;
-      it.steps = (len + 15) / 16;
-      it.half = half_of(it.tn);
+struct Walk {
+  const XentPlan &q;
+  const XentParams &P;
+  int64_t t = 0;               // the next item of the phase
+  int phase = 0, count = 0;
+  int row = 0, col = 0;        // its coordinates; logits: row within the sweep
+  int sweep = 0, rows = 1;     // logits: the sweep and its row tiles
+  int step_row = 0, step_col = 0, step = 0;
+
+  __device__ __forceinline__ Walk(const XentPlan &q_, const XentParams &P_) : q(q_), P(P_) {}
+
+  __device__ __forceinline__ bool next(XentItem &it) {
+    if constexpr (kMode != kModeProducts) {
+      bool seek = phase == 0;
+      if (seek) {
+        phase = 1;
+        t = q.cid;
+      } else {
+        t += q.ncl;
+        row += step_row;
+        col += step_col;
+        if (row >= rows) row -= rows, ++col;
+        seek = col >= q.n_tiles;
+      }
+      if (t >= (int64_t)q.m_tiles * q.n_tiles) return false;
+      if (seek) {
+        const int64_t size = (int64_t)kSweepTiles * q.n_tiles;
+        sweep = (int)(t / size);
+        const int r = (int)(t - sweep * size);
+        rows = min(kSweepTiles, q.m_tiles - sweep * kSweepTiles);
+        col = r / rows, row = r % rows;
+        step_col = q.ncl / rows, step_row = q.ncl % rows;
+      }
+      it.tn = col;
+      it.tm = sweep * kSweepTiles + row;
+      it.kit = (P.d + kStageK - 1) / kStageK;
+      it.steps = (P.d + 15) / 16;
+      it.half = BM;
       it.dw = false;
       return true;
-    }
-    k -= q.mine;
-    const int64_t narrow = q.ncl - q.wide, head = (int64_t)q.extra * narrow;
-    int64_t t;
-    if (q.cid >= q.wide && k < q.extra) {
-      t = (q.cid - q.wide) + k * narrow;
     } else {
-      if (q.cid >= q.wide) k -= q.extra;
-      t = head + q.cid + k * q.ncl;
+      if (phase == 0) phase = 1;
+      if (phase == 1) {
+        if (count < q.mine) {
+          const int i = q.cid + count * q.ncl, u = i / P.splits;
+          ++count;
+          it.split = i - u * P.splits;
+          it.tm = u / q.d_tiles;
+          it.tn = u - it.tm * q.d_tiles;
+          const int k0 = it.split * q.dh_kit * kStageK;
+          const int len = max(0, min(q.dh_kit * kStageK, P.v_piece - k0));
+          it.kit = (len + kStageK - 1) / kStageK;
+          it.steps = (len + 15) / 16;
+          it.half = half_of(it.tn);
+          it.dw = false;
+          return true;
+        }
+        count = 0;
+        if (q.cid >= q.wide && q.extra > 0) enter(2, q.cid - q.wide, q.ncl - q.wide);
+        else enter(3, (int64_t)q.extra * (q.ncl - q.wide) + q.cid, q.ncl);
+      }
+      if (phase == 2 && count == q.extra) enter(3, (int64_t)q.extra * (q.ncl - q.wide) + q.cid, q.ncl);
+      if (t >= q.dw_items) return false;
+      it.tm = row;
+      it.tn = col;
+      it.kit = q.dw_kit;
+      it.steps = (q.rows + 15) / 16;
+      it.half = half_of(col);
+      it.dw = true;
+      ++count;
+      t += step;
+      row += step_row;
+      col += step_col;
+      if (col >= q.d_tiles) col -= q.d_tiles, ++row;
+      return true;
     }
-    if (t >= q.dw_items) return false;
-    it.tm = (int)((uint32_t)t / (uint32_t)q.d_tiles);
-    it.tn = (int)((uint32_t)t - (uint32_t)it.tm * (uint32_t)q.d_tiles);
-    it.kit = q.dw_kit;
-    it.steps = (q.rows + 15) / 16;
-    it.half = half_of(it.tn);
-    it.dw = true;
-    return true;
   }
-}
+
+ private:
+  // the last tile of d columns multiplies no more than it holds (a multiple
+  // of 32 columns, half of them per CTA)
+  __device__ __forceinline__ int half_of(int tn) const { return min(BM, (P.d - tn * kTile + 31) / 32 * 16); }
+
+  __device__ __forceinline__ void enter(int to, int64_t at, int by) {
+    phase = to;
+    t = at;
+    step = by;
+    row = (int)(at / q.d_tiles), col = (int)(at - (int64_t)row * q.d_tiles);
+    step_row = by / q.d_tiles, step_col = by - step_row * q.d_tiles;
+  }
+};
 
 struct Ring {
   int stage;
@@ -461,7 +502,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       Ring ring = {0, 0};
       uint32_t armed = 0, armed_parity[kStages] = {};
       XentItem it;
-      for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
+      Walk<kMode> walk(q, P);
+      while (!*abort_flag && walk.next(it)) {
         if (kMode == kModeP && P.only_redo && !P.redo[it.tm]) continue;
         const int m0 = it.tm * kTile + (int)crank * BM, n0 = it.tn * kTile + (int)crank * it.half;
         bool ok;
@@ -489,7 +531,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       uint32_t acc_phase = 0;
       bool issued = false;
       XentItem it;
-      for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
+      Walk<kMode> walk(q, P);
+      while (!*abort_flag && walk.next(it)) {
         if (kMode == kModeP && P.only_redo && !P.redo[it.tm]) continue;
         if (!mbar_wait_cluster(acce0 + 8 * acc, acc_phase ^ 1)) { give_up(); break; }
         tc_fence_after();
@@ -516,7 +559,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
     int slot = 0, acc = 0;
     uint32_t acc_phase = 0;
     XentItem it;
-    for (int64_t k = 0; !*abort_flag && item_at<kMode>(q, P, k, it); ++k) {
+    Walk<kMode> walk(q, P);
+    while (!*abort_flag && walk.next(it)) {
       if (kMode == kModeP && P.only_redo && !P.redo[it.tm]) continue;
       const int i0 = it.tm * kTile + (int)crank * BM + quarter * 32, i = i0 + lane;
       const int c0 = it.tn * kTile + part * kSpan;
@@ -1279,7 +1323,7 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, boo
   const int64_t m_tiles = s.n_pad / kTile, d_tiles = (d + kTile - 1) / kTile;
   const int64_t dh_kit = (s.piece + kStageK - 1) / kStageK;
   const int64_t share =
-      std::max<int64_t>(1, (m_tiles * d_tiles * dh_kit + s.piece / kTile * d_tiles * (s.n_pad / kStageK)) / kPairs);
+      std::max<int64_t>(1, (m_tiles * d_tiles * dh_kit + s.piece / kTile * d_tiles * item_cost((int)(s.n_pad / kStageK))) / kPairs);
   int64_t splits = std::min<int64_t>(std::min<int64_t>(16, std::max<int64_t>(1, dh_kit / 8)), (2 * dh_kit + share - 1) / share);
   s.split_kit = (int32_t)((dh_kit + splits - 1) / splits);
   s.splits = (int32_t)((dh_kit + s.split_kit - 1) / s.split_kit);
