@@ -84,7 +84,13 @@ CASES = [
      torch.float32),
     (512, 512, 0, "half", dict(kind="ntk", factor=2.0), 1, 9, 2, torch.bfloat16),
     (512, 256, 128, "interleaved", None, 1, 9, 2, torch.float32),
-    (72, 36, 4, "interleaved", None, 2, 11, 3, torch.float32),
+    (72, 36, 4, "interleaved", None, 2, 11, 3, torch.float32),  # 8-byte chunks
+    (72, 72, 0, "half", None, 2, 11, 3, torch.bfloat16),        # 8-byte chunks
+    (72, 36, 36, "interleaved", None, 1, 70, 3, torch.bfloat16),  # 4-byte chunks
+    (72, 72, 0, "interleaved", None, 1, 9, 2, torch.float32),
+    (76, 20, 8, "half", None, 1, 9, 2, torch.bfloat16),         # 4-byte chunks, an odd number of them copied
+    (504, 500, 4, "half", None, 1, 5, 2, torch.bfloat16),       # 4-byte chunks, several a lane
+    (508, 508, 0, "interleaved", None, 1, 5, 2, torch.float32),
     (80, 20, 60, "half", None, 1, 7, 1, torch.bfloat16),
     (40, 24, 8, "half", None, 2, 3, 2, torch.bfloat16),     # an odd number of copied chunks
     (7, 2, 3, "half", None, 1, 5, 3, torch.bfloat16),       # odd head
@@ -230,9 +236,12 @@ def test_strides_and_layouts(dtype):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     swapped = q.transpose(1, 2).contiguous().transpose(1, 2)
     assert torch.equal(layers.rotary(swapped, pos, spec), layers.rotary(q.contiguous(), pos, spec))
-    odd = torch.empty(q.numel() + 1, dtype=dtype, device="cuda")[1:].view(q.shape)
-    odd.copy_(q)
-    near(layers.rotary(odd, pos, spec), *turn64(q, pos[None].expand(2, 19), spec), dtype)
+    for off in (1, 2, 4):  # an element, 4 or 8 bytes, 8 or 16 bytes behind a 16-byte boundary
+        odd = torch.empty(q.numel() + off, dtype=dtype, device="cuda")[off:].view(q.shape)
+        odd.copy_(q)
+        near(layers.rotary(odd, pos, spec), *turn64(q, pos[None].expand(2, 19), spec), dtype)
+        got = layers.qk_norm_rotary(odd, k, gain, gain, pos, spec)[0]
+        assert torch.allclose(got.float(), a[0].float(), rtol=2.0 ** -7 if dtype == torch.bfloat16 else 1e-5, atol=1e-6)
     # the start as a number
     assert torch.equal(layers.rotary(q, 11, spec), layers.rotary(q, pos + 11, spec))
 
