@@ -747,17 +747,15 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
       // start, some 2 us, is not worth less), while four blocks an SM remain
       const int64_t round = (int64_t)groups * X.per_item * o->head_dim * (dtype == GBO_BF16 ? 2 : 4);
       const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>((32768 + round - 1) / round, want / (4 * sm)));
-      // backward: a block's end (its sums of the gains) is dear, too: where all
-      // blocks have two rounds at most, the resident ones (two an SM) take
-      // them all, equally (1974 tokens x 20 heads of 128: 18.6 -> 13.3 us)
-      int64_t take;
-      if (!back) {
-        take = std::min<int64_t>((want + rounds - 1) / rounds, 1 << 20);
-      } else if (few) {
-        const int64_t most = std::max<int64_t>(1, nblk[i] / (kRopeBackBlocks / 2)), each = (want + most - 1) / most;
-        take = (want + each - 1) / each;
-      } else {
-        take = std::min<int64_t>(want, nblk[i]);
+      // gradients of a norm: a block's end (its sums of the gains) is dear, too:
+      // where all blocks have two rounds at most, the resident ones (two an SM
+      // with chunks of eight elements, four with fewer) take them all, equally
+      // (1974 tokens x 20 heads of 128: 18.6 -> 13.3 us)
+      int64_t take = std::min<int64_t>((want + rounds - 1) / rounds, 1 << 20);
+      if (back && norm) {
+        const int64_t most = few ? std::max<int64_t>(1, nblk[i] * (CH == 8 ? 2 : 4) / kRopeBackBlocks) : nblk[i];
+        const int64_t each = few ? (want + most - 1) / most : 1;
+        take = std::min<int64_t>((want + each - 1) / each, nblk[i]);
       }
       X.block0 = (int32_t)blocks;
       X.nblk = (int32_t)take;
