@@ -541,9 +541,16 @@ __global__ void __launch_bounds__(1024) rope_dgain_kernel(const __grid_constant_
   pdl_wait();
   if (!S.dgain[ti]) return;
   float a = 0.f;
-  if (col < S.dim)
-#pragma unroll 4
-    for (int r = threadIdx.y; r < S.rows[ti]; r += 32) a += S.part[ti][(int64_t)r * S.dim + col];
+  if (col < S.dim) {
+    const float *part = S.part[ti] + col;
+    for (int r0 = threadIdx.y; r0 < S.rows[ti]; r0 += 32 * 16) {  // sixteen rows in flight
+      float v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) v[u] = r0 + 32 * u < S.rows[ti] ? part[(int64_t)(r0 + 32 * u) * S.dim] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) a += v[u];
+    }
+  }
   red[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
   const float v = warp_sum(red[threadIdx.x][threadIdx.y]);

@@ -491,7 +491,7 @@ typedef struct {
   int32_t mean;            /* 1: divide by the sum of the weights of the rows that count       */
   int32_t keep;            /* 1: gbo_xent_forward leaves its logits (16 bits each) in the workspace,
                               where it has room for them, and gbo_xent_backward, given the same
-                              arguments and the workspace untouched, uses them                 */
+                              arguments and the workspace untouched, uses them up              */
   int32_t reserved;        /* set to 0                                                         */
 } gbo_xent_args;
 

@@ -372,3 +372,26 @@ def test_large_tile_sweep():
     close(loss, want.loss, want.loss_tol, torch.float32)
     close(dh, want.dh, want.dh_tol, torch.bfloat16)
     close(dw, want.dw, want.dw_tol, torch.bfloat16)
+
+
+@pytest.mark.parametrize("ignored", [0.0, 0.4])
+def test_many_rows_in_one_and_in_two_calls(ignored):
+    """Thousands of rows with tiles among them that are out of the kept range, all of
+    them counting or a part, in one call and in a kept pair of calls."""
+    H, W, y = inputs(6500, 777, 72, 67, ignored=ignored)
+    H[1000:1003] *= 100
+    H[4000] *= 100
+    want = Want(H, W, y)
+    assert (want.loss > 50).any()
+    loss, dh, dw = layers.linear_cross_entropy_grad(H, W, y)
+    lse, ws = torch.empty(6500, device="cuda"), torch.empty(B.gbo_xent_workspace_bytes(6500, 777, 72, True),
+                                                            dtype=torch.uint8, device="cuda")
+    totals = torch.empty(2, device="cuda")
+    B.gbo_xent_forward(H, W, y, ws, lse=lse, totals=totals, keep=True)
+    dh2, dw2 = torch.empty_like(H), torch.empty_like(W)
+    B.gbo_xent_backward(H, W, y, lse, ws, dh=dh2, dw=dw2, keep=True)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(totals[0], want.total, want.total_tol, torch.float32)
+    for a, b in ((dh, dw), (dh2, dw2)):
+        close(a, want.dh, want.dh_tol, torch.bfloat16)
+        close(b, want.dw, want.dw_tol, torch.bfloat16)
