@@ -7,13 +7,14 @@
 //             dgain_j = sum e_j u_j
 // Bound: HBM.  Each element is read once and written once (backward: x and
 // dy read, dx written); a head's norm stays in registers and warp shuffles.
-// Measured on 32768 tokens x 20 heads of 128 in bf16: forward 57 us, 5.9 TB/s
-// (87% of a copy); backward 96 us, 5.2 TB/s; 32768 x 32 heads of 192 with 64
+// Measured on 32768 tokens x 20 heads of 128 in bf16: forward 56 us, 5.9 TB/s
+// (88% of a copy); backward 95 us, 5.3 TB/s; 32768 x 32 heads of 192 with 64
 // rotated and no norm: 120 us, 6.7 TB/s.  What carried the forward there from
 // 88 us: the asynchronous ring (heads in flight without registers), two fp32
 // lanes per instruction, hardware sines for bf16, 32-bit index division.  The
 // backward's 111 registers leave 16 warps an SM; at 80 (24 warps) it spills
-// and measured 127 us.
+// and measured 127 us.  Carrying the ring on into the next item, sines kept
+// negated in registers and sums without loops were slower or no faster.
 //
 // Work split.  A head is cut into units of two 16-byte chunks: the two halves
 // of a run of pairs (GBO_ROPE_HALF), two chunks of whole pairs

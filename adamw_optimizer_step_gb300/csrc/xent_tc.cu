@@ -34,11 +34,19 @@
 // over tokens and vocabulary are fp32.
 //
 // Bound: tensor cores (2 n v d operations a product) from a few hundred rows
-// on, W's HBM traffic below.
+// on, W's HBM traffic below.  Measured, of cuBLAS's 1944 TFLOP/s burst rate:
+// losses of 4096 rows, 128256 x 2048: 1.04 ms alone, 1.22 ms in a loop under
+// the power limit (2.07 and 1.76 PFLOP/s); losses and gradients of 8192 rows,
+// 128000 x 2048: 7.8 and 8.2 ms (6 n v d operations: 1.65 and 1.56 PFLOP/s;
+// forward 2.29 ms, convert 0.63 at 6.7 TB/s, products 4.70); 9.95 ms when the
+// backward pass formed the logits again.  Converting the logits of one part
+// of the rows beside the products of the next, in warps of their own, hid the
+// conversion but slowed the products: 7.7 and 8.2 ms, not kept.  Prefetching
+// operands to L2 slowed the products by a tenth.
 //
 // The GEMM kernel is warp-specialised and persistent like the Newton-Schulz
 // one: CTA pairs (cta_group::2), 256 x 256 tiles, TMA ring of three 64 KB
-// stages, two fp32 accumulators in TMEM, four epilogue warps per CTA; every
+// stages, two fp32 accumulators in TMEM, eight epilogue warps per CTA; every
 // wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -755,7 +763,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
 // every row of H; lanes join once, at the end.
 // One token over 128000 x 2048 (524 MB), the whole call: 102 us with the
 // 256-wide tiles, 97 us here, where a plain reduction that reads W once takes
-// 92 us.  Three to six stages measure the same (98 to 101 us): HBM is the bound.
+// 92 us.  Three to six stages, 64-row tiles and stages twice as wide measure
+// the same or less: HBM is the bound (the kernel alone: 85 us, 6.1 TB/s).
 // Prefetching each next tile's rows to L2 made it 137 us.
 constexpr int kScoreRows = 32;
 constexpr int kScoreUnit = 16;                                   // rows of W that a run is made of
