@@ -21,13 +21,14 @@
 // (GBO_ROPE_INTERLEAVED), or two chunks that are only copied.  A unit's pairs
 // are thus in one thread, and no rotation crosses lanes.  Heads, rotated parts
 // or addresses that 16 bytes do not divide take chunks of 8 or 4 bytes, or of
-// one element, in the same kernel.  A group of G lanes (a power of two) holds one head, one unit each
-// (two for long fp32 heads); it walks over several heads of one token, so the
-// cosines and sines of the token are computed once for them.
+// one element, in the same kernel.  A group of G lanes (a power of two) holds
+// one head, one unit each (more for long heads in narrow chunks); it walks
+// over several heads of one token, so the cosines and sines of the token are
+// computed once for them.
 //
 // Angles: t f_j in turns is a 64-bit fixed-point product modulo 2^64, exact
-// for every 64-bit position; the top 32 bits go to sincospif.  No table of
-// cosines is read.
+// for every 64-bit position; its top 32 bits are the angle (turn_of).  No
+// table of cosines is read.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
