@@ -76,7 +76,7 @@ class RotarySpec:
 
     def backward_workspace(self, table):
         """Scratch bytes of the gains' gradients for a table's numbers of heads (and its device)."""
-        key = (table[0]["dy"].device, *(e["dy"].shape[2] if e["dgain"] is not None else 0 for e in table))
+        key = (table[0]["dy"].device, *((e["dy"].shape[2], e["dgain"] is not None) for e in table))
         need = self._scratch.get(key)
         if need is None:
             need = self._scratch[key] = max(16, B.gbo_rope_workspace_bytes(table, self.opts))

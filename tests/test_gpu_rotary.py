@@ -323,3 +323,17 @@ def test_workspace_refused_when_small():
             B.gbo_rope_backward(table, spec.opts, 0, ws)
         assert e.value.code == -6
     assert ctypes.sizeof(B.RopeTensor) == B.gbo_struct_size(8)
+
+
+def test_scratch_of_one_gain_among_other_heads():
+    """One spec, a gain of the queries alone, and keys of fewer heads than the call
+    before: the scratch is sized for this call's heads, not the last one's."""
+    spec = layers.RotarySpec(64)
+    gq = torch.ones(64, device="cuda")
+    for kv in (16, 4, 1, 8):
+        q, k = torch.randn(1, 900, 4, 64, device="cuda"), torch.randn(1, 900, kv, 64, device="cuda")
+        dq, dk, dgq, dgk = layers.qk_norm_rotary_backward(q, k, q, k, gq, None, 0, spec)
+        alone = layers.RotarySpec(64)
+        want = layers.qk_norm_rotary_backward(q, k, q, k, gq, None, 0, alone)
+        assert dgk is None and torch.equal(dgq, want[2])
+        assert torch.equal(dq, want[0]) and torch.equal(dk, want[1])
