@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const __grid_constant__ 
       const float up = R.upstream ? *R.upstream : 1.f;
       R.head->rows = all;
       R.head->weight_sum = ws;
-      R.head->g = R.mean ? (all > 0 ? up / ws : 0.f) : up;
+      R.head->g = R.mean ? (ws != 0.f ? up / ws : 0.f) : up;
       if (!R.kept) R.head->redo = 0;
     }
     if (R.redo)

@@ -470,7 +470,8 @@ size_t gbo_rope_workspace_bytes(const gbo_rope_tensor *tensors, int32_t n, const
  *   L = upstream * (sum_i w_i loss_i) / (mean ? sum_i w_i : 1).
  * Row i is left out (loss and gradients 0, whatever stands in it) when its
  * label is negative or its weight w_i is 0; a label >= v leaves the row out
- * too and sets GBO_STATUS_BAD_LABEL.  With no row left, every output is 0.
+ * too and sets GBO_STATUS_BAD_LABEL.  With no row left, every output is 0; a
+ * mean whose weights sum to 0 has gradients 0.
  * H, W are bf16 (an fp32 master table is cast by its owner, once per step);
  * products accumulate in fp32, exponentials and sums are fp32.
  */
@@ -513,9 +514,9 @@ typedef struct {
  * the logits are kept there between the passes, in steps of 2^-9 bits from
  * the label's; otherwise they are formed again, piece by piece of the
  * vocabulary, each piece as wide as the workspace allows and 2 GiB at most
- * (a third more tensor core work).  cap > 0: the most that fits in `cap` bytes; 0: kept logits up
- * to 8 GiB, else pieces of 2 GiB.  0 when the arguments are out of range or
- * not even a piece of 256 columns fits the cap.
+ * (a third more tensor core work).  cap > 0: the most that fits in `cap`
+ * bytes; 0: kept logits up to 8 GiB, else pieces of 2 GiB.  0 when the
+ * arguments are out of range or not even a piece of 256 columns fits the cap.
  */
 size_t gbo_xent_workspace_bytes(int64_t n, int64_t v, int64_t d, int32_t grad, int64_t cap);
 

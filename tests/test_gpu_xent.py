@@ -395,3 +395,14 @@ def test_many_rows_in_one_and_in_two_calls(ignored):
     for a, b in ((dh, dw), (dh2, dw2)):
         close(a, want.dh, want.dh_tol, torch.bfloat16)
         close(b, want.dw, want.dw_tol, torch.bfloat16)
+
+
+def test_weights_that_sum_to_zero():
+    """The mean over weights +1 and -1: the loss and its gradients are 0, not inf."""
+    H, W, y = inputs(2, 300, 64, 71)
+    weight = torch.tensor([1.0, -1.0], device="cuda")
+    Hg, Wg = H.clone().requires_grad_(), W.clone().requires_grad_()
+    loss = layers.linear_cross_entropy_loss(Hg, Wg, y, weight)
+    loss.backward()
+    assert loss.item() == 0
+    assert torch.equal(Hg.grad, torch.zeros_like(H)) and torch.equal(Wg.grad, torch.zeros_like(W))
