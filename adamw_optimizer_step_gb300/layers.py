@@ -19,6 +19,7 @@ transposed (batch, heads, seq, dim) tensor).  Positions are an integer tensor
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as B
 
@@ -158,28 +159,44 @@ def _rows(t):
     return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
+def _save_positions(ctx, positions, *tensors):
+    """Saved as a tensor, so that autograd notices positions that change before the
+    backward pass; an int is kept beside it."""
+    ctx.start = positions if isinstance(positions, int) else None
+    ctx.save_for_backward(None if ctx.start is not None else positions, *tensors)
+
+
+def _saved_positions(ctx):
+    positions, *tensors = ctx.saved_tensors
+    return (positions if ctx.start is None else ctx.start, *tensors)
+
+
 class _Rotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, positions, spec):
-        ctx.spec, ctx.positions = spec, positions
+        ctx.spec = spec
+        _save_positions(ctx, positions)
         return rotary(x, positions, spec)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
-        return rotary(_rows(dy), ctx.positions, ctx.spec, inverse=True), None, None
+        return rotary(_rows(dy), _saved_positions(ctx)[0], ctx.spec, inverse=True), None, None
 
 
 class _QkNormRotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_gain, k_gain, positions, spec, eps):
-        ctx.save_for_backward(q, k, q_gain, k_gain)
-        ctx.rest = (positions, spec, eps)
+        ctx.rest = (spec, eps)
+        _save_positions(ctx, positions, q, k, q_gain, k_gain)
         return qk_norm_rotary(q, k, q_gain, k_gain, positions, spec, eps=eps)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
-        positions, spec, eps = ctx.rest
-        grads = qk_norm_rotary_backward(_rows(dq), _rows(dk), *ctx.saved_tensors, positions, spec, eps=eps)
+        spec, eps = ctx.rest
+        positions, *saved = _saved_positions(ctx)
+        grads = qk_norm_rotary_backward(_rows(dq), _rows(dk), *saved, positions, spec, eps=eps)
         return (*grads, None, None, None)
 
 
@@ -196,20 +213,24 @@ class _LinearCrossEntropy(torch.autograd.Function):
         B.gbo_xent_forward(h, wb, labels, ws, lse=lse, totals=totals, row_weight=row_weight, logit_scale=logit_scale,
                            z_loss=z_loss, keep=grad)
         ctx.save_for_backward(h, wb, labels, row_weight, lse)
-        ctx.rest = (z_loss, logit_scale, w.dtype, ws)
+        ctx.rest = (z_loss, logit_scale, workspace_cap, w.dtype, ws)
         return torch.where(totals[1] != 0, totals[0] / totals[1], torch.zeros_like(totals[0]))
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, up):
         h, w, labels, row_weight, lse = ctx.saved_tensors
-        z_loss, logit_scale, w_dtype, ws = ctx.rest
-        if ws is None:
-            raise RuntimeError("the loss's workspace is used up by its first backward pass")
-        ctx.rest = (z_loss, logit_scale, w_dtype, None)
+        z_loss, logit_scale, workspace_cap, w_dtype, ws = ctx.rest
+        keep = ws is not None
+        # the first pass uses the kept logits up; another one (retain_graph) forms them again
+        ctx.rest = (z_loss, logit_scale, workspace_cap, w_dtype, None)
+        if not keep:
+            ws = torch.empty(B.gbo_xent_workspace_bytes(h.shape[0], *w.shape, True, workspace_cap), dtype=torch.uint8,
+                             device=h.device)
         dh = _like(h) if ctx.needs_input_grad[0] else None
         dw = torch.empty(w.shape, dtype=w_dtype, device=w.device) if ctx.needs_input_grad[1] else None
         B.gbo_xent_backward(h, w, labels, lse, ws, dh=dh, dw=dw, row_weight=row_weight,
-                            upstream=up.float().reshape(1), logit_scale=logit_scale, z_loss=z_loss, keep=True)
+                            upstream=up.float().reshape(1), logit_scale=logit_scale, z_loss=z_loss, keep=keep)
         return dh, dw, None, None, None, None, None
 
 

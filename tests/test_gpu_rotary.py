@@ -337,3 +337,17 @@ def test_scratch_of_one_gain_among_other_heads():
         want = layers.qk_norm_rotary_backward(q, k, q, k, gq, None, 0, alone)
         assert dgk is None and torch.equal(dgq, want[2])
         assert torch.equal(dq, want[0]) and torch.equal(dk, want[1])
+
+
+def test_positions_changed_before_the_backward_pass_are_noticed():
+    spec = layers.RotarySpec(32)
+    q, k = (torch.randn(1, 8, n, 32, device="cuda", requires_grad=True) for n in (2, 1))
+    pos = torch.arange(8, device="cuda")
+    y = layers.rotary_autograd(q, pos, spec)
+    yq, yk = layers.qk_norm_rotary_autograd(q, k, None, None, pos, spec)
+    y.sum().backward(retain_graph=True)  # unchanged: taken
+    pos += 1
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
+    with pytest.raises(RuntimeError):
+        (yq.sum() + yk.sum()).backward()

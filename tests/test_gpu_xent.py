@@ -406,3 +406,21 @@ def test_weights_that_sum_to_zero():
     loss.backward()
     assert loss.item() == 0
     assert torch.equal(Hg.grad, torch.zeros_like(H)) and torch.equal(Wg.grad, torch.zeros_like(W))
+
+
+@pytest.mark.parametrize("cap", ["keep", "pieces"])
+def test_two_backward_passes(cap):
+    """retain_graph: the second pass has no kept logits, and the same gradients by its own
+    bounds; a gradient of a gradient is refused."""
+    H, W, y = inputs(70, 900, 64, 72, ignored=0.1)
+    want = Want(H, W, y)
+    cap = 0 if cap == "keep" else smallest_cap(70, 900, 64)
+    Hg, Wg = H.clone().requires_grad_(), W.clone().requires_grad_()
+    loss = layers.linear_cross_entropy_loss(Hg, Wg, y, workspace_cap=cap)
+    for _ in range(2):
+        dh, dw = torch.autograd.grad(loss, (Hg, Wg), retain_graph=True)
+        close(dh, want.dh, want.dh_tol, torch.bfloat16)
+        close(dw, want.dw, want.dw_tol, torch.bfloat16)
+    dh, = torch.autograd.grad(loss, Hg, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dh.float().sum().backward()
