@@ -617,7 +617,7 @@ def _rows_of(t, what, shape=None):
         raise ValueError("the row elements of %s must be consecutive" % what)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % what)
-    return stride[0] if s[0] > 1 else max(s[1], stride[0])
+    return stride[0] if s[0] > 1 else s[1]  # (of one row any stride will do)
 
 
 def _xent_args(h, w, labels, row_weight, upstream, logit_scale, z_loss, mean, keep=False):

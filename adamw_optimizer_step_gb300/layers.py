@@ -40,6 +40,7 @@ class RotarySpec:
 
     def __init__(self, head_dim, rot_dim=None, offset=0, layout="half", base=10000.0, scaling=None, frequencies=None,
                  magnitude=1.0):
+        self._made_of = (head_dim, rot_dim, offset, layout, base, scaling, frequencies, magnitude)
         self.head_dim = int(head_dim)
         self.rot_dim = self.head_dim - int(offset) if rot_dim is None else int(rot_dim)
         if layout not in LAYOUTS:
@@ -62,6 +63,9 @@ class RotarySpec:
         self.opts = B.RopeOpts(self.head_dim, self.rot_dim, int(offset), LAYOUTS[layout],
                                ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double)), self.magnitude, 0.0)
         self._eps, self._scratch = {}, {}  # options by eps, scratch sizes by heads
+
+    def __reduce__(self):  # a model that holds one can be copied and saved
+        return RotarySpec, self._made_of
 
     @property
     def frequencies(self):
@@ -202,7 +206,7 @@ class _QkNormRotary(torch.autograd.Function):
 
 class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, h, w, labels, row_weight, z_loss, logit_scale, workspace_cap):
+    def forward(ctx, h, w, labels, row_weight, z_loss, logit_scale, workspace_cap, dev_status):
         n, d = h.shape
         wb = w.to(torch.bfloat16)
         grad = ctx.needs_input_grad[0] or ctx.needs_input_grad[1]
@@ -211,27 +215,28 @@ class _LinearCrossEntropy(torch.autograd.Function):
         ws = torch.empty(B.gbo_xent_workspace_bytes(n, w.shape[0], d, grad, workspace_cap), dtype=torch.uint8,
                          device=h.device)
         B.gbo_xent_forward(h, wb, labels, ws, lse=lse, totals=totals, row_weight=row_weight, logit_scale=logit_scale,
-                           z_loss=z_loss, keep=grad)
+                           z_loss=z_loss, keep=grad, dev_status=dev_status)
         ctx.save_for_backward(h, wb, labels, row_weight, lse)
-        ctx.rest = (z_loss, logit_scale, workspace_cap, w.dtype, ws)
+        ctx.rest = (z_loss, logit_scale, workspace_cap, w.dtype, ws, dev_status)
         return torch.where(totals[1] != 0, totals[0] / totals[1], torch.zeros_like(totals[0]))
 
     @staticmethod
     @once_differentiable
     def backward(ctx, up):
         h, w, labels, row_weight, lse = ctx.saved_tensors
-        z_loss, logit_scale, workspace_cap, w_dtype, ws = ctx.rest
+        z_loss, logit_scale, workspace_cap, w_dtype, ws, dev_status = ctx.rest
         keep = ws is not None
         # the first pass uses the kept logits up; another one (retain_graph) forms them again
-        ctx.rest = (z_loss, logit_scale, workspace_cap, w_dtype, None)
+        ctx.rest = (z_loss, logit_scale, workspace_cap, w_dtype, None, dev_status)
         if not keep:
             ws = torch.empty(B.gbo_xent_workspace_bytes(h.shape[0], *w.shape, True, workspace_cap), dtype=torch.uint8,
                              device=h.device)
         dh = _like(h) if ctx.needs_input_grad[0] else None
         dw = torch.empty(w.shape, dtype=w_dtype, device=w.device) if ctx.needs_input_grad[1] else None
         B.gbo_xent_backward(h, w, labels, lse, ws, dh=dh, dw=dw, row_weight=row_weight,
-                            upstream=up.float().reshape(1), logit_scale=logit_scale, z_loss=z_loss, keep=keep)
-        return dh, dw, None, None, None, None, None
+                            upstream=up.float().reshape(1), logit_scale=logit_scale, z_loss=z_loss, keep=keep,
+                            dev_status=dev_status)
+        return dh, dw, None, None, None, None, None, None
 
 
 def rotary_autograd(x, positions, spec):
@@ -244,9 +249,11 @@ def qk_norm_rotary_autograd(q, k, q_gain, k_gain, positions, spec, eps=1e-6):
     return _QkNormRotary.apply(q, k, q_gain, k_gain, positions, spec, eps)
 
 
-def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_scale=1.0, workspace_cap=0):
+def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_scale=1.0, workspace_cap=0,
+                              dev_status=None):
     """Mean loss over the rows that count, with its gradients by ``h`` (bf16) and ``w``
     (bf16, or a float32 master table, which is cast for the products and gets a
     float32 gradient).  Between the passes the workspace (``workspace_cap``) keeps the
-    logits in 16 bits where it has room for them."""
-    return _LinearCrossEntropy.apply(h, w, labels, row_weight, z_loss, logit_scale, workspace_cap)
+    logits in 16 bits where it has room for them.  ``dev_status``: a CUDA int32 that
+    takes ``GBO_STATUS_BAD_LABEL`` and ``GBO_STATUS_NONFINITE``."""
+    return _LinearCrossEntropy.apply(h, w, labels, row_weight, z_loss, logit_scale, workspace_cap, dev_status)

@@ -424,3 +424,24 @@ def test_two_backward_passes(cap):
     dh, = torch.autograd.grad(loss, Hg, create_graph=True)
     with pytest.raises(RuntimeError):
         dh.float().sum().backward()
+
+
+def test_status_and_single_rows_through_autograd():
+    """A label outside the vocabulary is told; one row of h and of w, slices whose strides
+    belong to wider tensors of an odd width."""
+    H, W, y = inputs(5, 300, 64, 73)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    layers.linear_cross_entropy_loss(H, W, y, dev_status=status)
+    assert status.item() == 0
+    y[2] = 300
+    layers.linear_cross_entropy_loss(H, W, y, dev_status=status)
+    assert status.item() == 4
+    wide = torch.zeros(3, 65, dtype=torch.bfloat16, device="cuda")
+    wide[:1, :64] = H[:1]
+    one = wide[:1, :64]
+    loss, dh, dw = layers.linear_cross_entropy_grad(one, one, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    # one class: its probability is 1, the loss and the gradients 0 (P off by the bound of lse)
+    want = Want(one, one, torch.zeros(1, dtype=torch.int64))
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(dh, want.dh, want.dh_tol, torch.bfloat16)
+    close(dw, want.dw, want.dw_tol, torch.bfloat16)

@@ -250,3 +250,14 @@ def test_cross_entropy_workspace_sizes():
     assert size(64, 1000, 64, True, 1000) == 0
     for bad in ((-1, 10, 8), (4, 0, 8), (4, 10, 12), (4, 10, 0)):
         assert size(*bad) == 0
+
+
+def test_a_spec_can_be_copied_and_saved(L):
+    import copy
+    import pickle
+    spec = layers.RotarySpec(64, 32, 16, "interleaved", 1e6,
+                             scaling=dict(kind="yarn", factor=4.0, trained=4096, fast=32, slow=1))
+    for other in (copy.deepcopy(spec), pickle.loads(pickle.dumps(spec))):
+        assert other.frequencies == spec.frequencies and other.opts.magnitude == spec.opts.magnitude
+        assert (other.opts.offset, other.opts.layout, other.rot_dim) == (16, B.GBO_ROPE_INTERLEAVED, 32)
+        assert ctypes.addressof(other.opts.freq.contents) != ctypes.addressof(spec.opts.freq.contents)
