@@ -27,7 +27,7 @@
 // vocabulary, so its scratch is one piece of P.  Where the workspace has room
 // for the whole vocabulary's P, gbo_xent_grad keeps the logits there between
 // the passes instead, in 16 bits each (kKeepStep), which replaces one of the
-// four products by a pass over that room:
+// four products by a pass over that room (see kNarrow):
 //   convert P in place of the kept logits
 // P is rounded to bf16 once, from the fp32 lse (the tensor cores take 16-bit
 // operands: the same rounding as a bf16 gradient of the logits), and sums
@@ -755,9 +755,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
 
 // Statistics of at most kScoreRows rows: W is read once and its HBM traffic is
 // all there is, so the operands change places.  The vocabulary is M (tiles of
-// 128 rows of W), the rows are N = 32: a tile's products take an eighth of
-// the tensor core's time of a 256-wide tile, a stage of the ring is 32 KB of W
-// and 8 KB of H, and four of five are on their way while one is multiplied.
+// 128 rows of W), the rows are N = 16, a stage of the ring is 32 KB of W and
+// 4 KB of H, and five of six are on their way while one is multiplied.
 // Each CTA takes a run of the vocabulary, equal to within 16 rows.  A thread
 // of the epilogue owns a row of W and keeps a running maximum and sum for
 // every row of H; lanes join once, at the end.
@@ -765,19 +764,25 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
 // 256-wide tiles, 97 us here, where a plain reduction that reads W once takes
 // 92 us.  Three to six stages, 64-row tiles and stages twice as wide measure
 // the same or less: HBM is the bound (the kernel alone: 85 us, 6.1 TB/s).
-// Prefetching each next tile's rows to L2 made it 137 us.
-constexpr int kScoreRows = 32;
+// Prefetching each next tile's rows to L2 made it 137 us.  More rows: the
+// epilogue grows with them (the whole call, here / 256-wide tiles, in us: 1
+// row of 40000 x 1024 20.3 / 24.2, of 32000 x 1024 20.4 / 19.8; 16 rows of
+// 32000 x 1024 22.5 / 19.6, of 128000 x 1024 56.8 / 56.6, of 128000 x 2048
+// 99.7 / 104.0; a variant of 32 rows at 32: 24.2 / 19.6, 58.2 / 56.7, 100.5 /
+// 103.9).
+constexpr int kScoreRows = 16;
 constexpr int kScoreUnit = 16;                                   // rows of W that a run is made of
-constexpr int kScoreB = kScoreRows * kBlockK * 2;                // 4 KB: H's rows, one K block
+constexpr int kScoreB = kScoreRows * kBlockK * 2;                // 2 KB: H's rows, one K block
 constexpr int kScoreStage = 2 * (kOpBytes + kScoreB);
-constexpr int kScoreStages = 5;
+constexpr int kScoreStages = 6;
 constexpr int kScoreSmem = 1024 + kScoreStages * kScoreStage + 256 + kScoreRows * 8;
 constexpr int kScoreWarps = 4;                                   // epilogue
-constexpr int kScoreTmem = 64;                                   // two 128 x 32 accumulators
+constexpr int kScoreTmem = 2 * kScoreRows;                       // two 128 x 16 accumulators
+constexpr int kScoreAhead = 4;                                   // rows whose sums run side by side
 static_assert(kScoreSmem <= 232448, "shared memory per CTA");
 
 struct ScoreParams {
-  CUtensorMap mapW, mapW16, mapH;  // boxes of 128, 16 and 32 rows
+  CUtensorMap mapW, mapW16, mapH;  // boxes of 128, 16 and 16 rows
   const XentHead *head;
   const int32_t *lab;
   const float *ll2;
@@ -788,6 +793,20 @@ struct ScoreParams {
   int32_t v, d;
   float scale2;
 };
+
+// The 32 lanes' rows of 16 consecutive fp32 TMEM columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+}
 
 __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constant__ ScoreParams P) {
   pdl_launch();
@@ -922,16 +941,17 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
       if (!mbar_wait(accf0 + 8 * acc, (t >> 1) & 1)) { give_up(); ok = false; break; }
       tc_fence_after();
       float v[kScoreRows];
-      tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kScoreRows), v);
+      tmem_ld16(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kScoreRows), v);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acce0 + 8 * acc);
 #pragma unroll
-      for (int j = 0; j < kScoreRows; ++j) {
-        if (j >= rows) break;
-        float x = v[j] * P.scale2;
-        if (r == lab_s[j]) x = ll2_s[j];
-        if (r < end) {
+      for (int j0 = 0; j0 < kScoreRows; j0 += kScoreAhead) {
+        if (j0 >= rows) break;
+#pragma unroll
+        for (int j = j0; j < j0 + kScoreAhead; ++j) {  // rows behind the last one: zeros that nobody reads
+          const float l = r == lab_s[j] ? ll2_s[j] : v[j] * P.scale2;
+          const float x = r < end ? l : -INFINITY;
           const float mn = fmaxf(m[j], x), at = mn == -INFINITY ? 0.f : mn;
           s[j] = fmaf(s[j], exp2_fast(m[j] - at), exp2_fast(x - at));
           m[j] = mn;
@@ -940,16 +960,22 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
     }
     if (ok) {
 #pragma unroll
-      for (int j = 0; j < kScoreRows; ++j) {
-        if (j >= rows) break;
+      for (int j0 = 0; j0 < kScoreRows; j0 += kScoreAhead) {
+        if (j0 >= rows) break;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-          const float m2 = __shfl_xor_sync(0xffffffffu, m[j], o), s2 = __shfl_xor_sync(0xffffffffu, s[j], o);
-          const float mn = fmaxf(m[j], m2), at = mn == -INFINITY ? 0.f : mn;
-          s[j] = s[j] * exp2_fast(m[j] - at) + s2 * exp2_fast(m2 - at);
-          m[j] = mn;
+#pragma unroll
+          for (int j = j0; j < j0 + kScoreAhead; ++j) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m[j], o), s2 = __shfl_xor_sync(0xffffffffu, s[j], o);
+            const float mn = fmaxf(m[j], m2), at = mn == -INFINITY ? 0.f : mn;
+            s[j] = s[j] * exp2_fast(m[j] - at) + s2 * exp2_fast(m2 - at);
+            m[j] = mn;
+          }
         }
-        if (lane == 0) P.part[((int64_t)blockIdx.x * kScoreWarps + quarter) * P.part_ld + j] = make_float2(m[j], s[j]);
+#pragma unroll
+        for (int j = j0; j < j0 + kScoreAhead; ++j)
+          if (lane == 0 && j < rows)
+            P.part[((int64_t)blockIdx.x * kScoreWarps + quarter) * P.part_ld + j] = make_float2(m[j], s[j]);
       }
     }
   }
@@ -1292,6 +1318,13 @@ struct XentSpace {
 
 constexpr int64_t kPieceBytes = int64_t(2) << 30;  // P of one piece, unless the caller caps the workspace
 constexpr int64_t kKeepBytes = int64_t(8) << 30;   // kept logits, likewise
+// Logits are kept unless they are many and their rows narrow: then forming
+// them again costs less than storing and converting them (us, kept / formed
+// again, rows x columns: 4096 x 32000 at d = 64 312 / 263, d = 256 333 / 297,
+// d = 512 414 / 395 alone and 419 / 412 in a loop, d = 1024 594 / 660; 256 x
+// 32000 at d = 64 42.3 / 40.8, d = 256 48.5 / 48.2; 256 x 1000 at d = 64 24.8
+// / 26.4, d = 256 28.1 / 31.0).
+constexpr int64_t kNarrow = 512, kMany = int64_t(1) << 23;
 constexpr int kPairs = 76;                         // CTA pairs of the device
 constexpr int kMostSms = 256;
 
@@ -1360,16 +1393,18 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, boo
   return s;
 }
 
+bool keeps(int64_t n, int64_t v, int64_t d) { return d >= kNarrow || up_to(n, kTile) * v < kMany; }
+
 // What a call does without a cap.
 XentSpace default_space(int64_t n, int64_t v, int64_t d) {
-  const bool keep = 2 * up_to(std::max<int64_t>(n, 1), kTile) * up_to(v, kTile) <= kKeepBytes;
+  const bool keep = keeps(n, v, d) && 2 * up_to(std::max<int64_t>(n, 1), kTile) * up_to(v, kTile) <= kKeepBytes;
   return space_of(n, v, d, true, true, keep, 0);
 }
 
-// The fastest schedule whose workspace fits `bytes`: kept logits, else the
-// widest pieces (false: not even one of kTile columns).
+// The fastest schedule whose workspace fits `bytes`: kept logits (see
+// kNarrow), else the widest pieces (false: not even one of kTile columns).
 bool fit_space(int64_t n, int64_t v, int64_t d, bool forward, int64_t bytes, XentSpace *out) {
-  if (forward) {
+  if (forward && keeps(n, v, d)) {
     *out = space_of(n, v, d, true, true, true, 0);
     if (out->bytes <= bytes) return true;
   }
@@ -1599,7 +1634,10 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     L.sums = totals ? reinterpret_cast<float *>(ws + S.sums) : nullptr;
     L.status = status;
     L.part_ld = S.n_pad, L.tiles = (int32_t)slots, L.z = a->z_loss;
-    while (L.rows_log2 < 5 && (1 << L.rows_log2) < a->n) ++L.rows_log2;
+    // four rows a block (a sector of statistics), more where that is more than
+    // two blocks an SM: with 32 rows a block from the start, 256 rows of
+    // 128000 x 2048 took 113.5 us in all instead of 107.6
+    while (L.rows_log2 < 5 && (1 << L.rows_log2) < a->n && (L.rows_log2 < 2 || a->n >> L.rows_log2 > 2 * sm)) ++L.rows_log2;
     const int blocks = (int)((a->n + (1 << L.rows_log2) - 1) >> L.rows_log2);
     if ((e = chain(xent_lse_kernel, dim3(blocks), dim3(kLseThreads), st, L)) != cudaSuccess) return cuda_err(e);
     if (totals && (e = chain(xent_totals_kernel, dim3(1), dim3(1024), st, TotalsParams{L.sums, R.head, totals, blocks})) !=

@@ -491,7 +491,7 @@ typedef struct {
   int32_t label_dtype;     /* GBO_I32 | GBO_I64                                                */
   int32_t mean;            /* 1: divide by the sum of the weights of the rows that count       */
   int32_t keep;            /* 1: gbo_xent_forward leaves its logits (16 bits each) in the workspace,
-                              where it has room for them, and gbo_xent_backward, given the same
+                              where they are kept at all, and gbo_xent_backward, given the same
                               arguments and the workspace untouched, uses them up              */
   int32_t reserved;        /* set to 0                                                         */
 } gbo_xent_args;
@@ -510,11 +510,12 @@ typedef struct {
 /*
  * Bytes of device workspace.  grad 0: gbo_xent_forward alone.  grad 1:
  * gbo_xent_grad, gbo_xent_backward, and gbo_xent_forward with keep.  With
- * room for the whole vocabulary's gradients of the logits (2 bytes each),
- * the logits are kept there between the passes, in steps of 2^-9 bits from
- * the label's; otherwise they are formed again, piece by piece of the
- * vocabulary, each piece as wide as the workspace allows and 2 GiB at most
- * (a third more tensor core work).  cap > 0: the most that fits in `cap`
+ * room for the whole vocabulary's gradients of the logits (2 bytes each), the
+ * logits are kept there between the passes, in steps of 2^-9 bits from the
+ * label's.  Otherwise (and for 2^23 logits and more of rows narrower than 512,
+ * where it is faster) they are formed again, piece by piece of the vocabulary,
+ * each piece as wide as the workspace allows and 2 GiB at most (a third more
+ * tensor core work).  cap > 0: the most that fits in `cap`
  * bytes; 0: kept logits up to 8 GiB, else pieces of 2 GiB.  0 when the
  * arguments are out of range or not even a piece of 256 columns fits the cap.
  */

@@ -150,10 +150,11 @@ def test_pieces_of_the_vocabulary():
     assert B.gbo_xent_workspace_bytes(300, 3001, 128, True, least // 2) == 0
 
 
-def test_kept_logits_out_of_range():
+@pytest.mark.parametrize("d", [64, 520])
+def test_kept_logits_out_of_range(d):
     """A few rows whose largest logit is more than 64 bits above their label's, among
-    others: their tiles are formed again; the rest is kept."""
-    H, W, y = inputs(700, 900, 64, 23)
+    others: their tiles are formed again; the rest is kept (of wide rows)."""
+    H, W, y = inputs(700, 900, d, 23)
     H[300:310] *= 60
     H[650] *= 100
     want = Want(H, W, y)
@@ -306,13 +307,14 @@ def test_gradient_against_differences():
     assert abs(num - got) <= tol
 
 
+@pytest.mark.parametrize("d", [64, 520])
 @pytest.mark.parametrize("cap", ["keep", "pieces"])
-def test_autograd_matches_the_formula(cap):
+def test_autograd_matches_the_formula(cap, d):
     """Logits kept from the forward pass, or formed again; bf16 weights and a float32
     master table, whose gradient is float32."""
-    H, W, y = inputs(96, 1333, 64, 57, ignored=0.1)
+    H, W, y = inputs(96, 1333, d, 57, ignored=0.1)
     want = Want(H, W, y, z=1e-3, upstream=3.0)
-    cap = 0 if cap == "keep" else smallest_cap(96, 1333, 64)
+    cap = 0 if cap == "keep" else smallest_cap(96, 1333, d)
     for master in (False, True):
         Hg, Wg = H.clone().requires_grad_(), (W.float() if master else W.clone()).requires_grad_()
         loss = layers.linear_cross_entropy_loss(Hg, Wg, y, z_loss=1e-3, workspace_cap=cap)
@@ -322,14 +324,15 @@ def test_autograd_matches_the_formula(cap):
         close(Wg.grad, want.dw, want.dw_tol, Wg.dtype)
 
 
-def test_kept_logits_between_two_calls():
+@pytest.mark.parametrize("d", [72, 520])
+def test_kept_logits_between_two_calls(d):
     """forward with keep, then backward on its workspace: the gradients of one call,
     among them of tiles that are out of the kept range; other kernels in between."""
-    H, W, y = inputs(600, 1100, 72, 58, ignored=0.1)
+    H, W, y = inputs(600, 1100, d, 58, ignored=0.1)
     H[300:310] *= 100
     want = Want(H, W, y)
     assert (want.loss > 50).any()
-    ws = torch.empty(B.gbo_xent_workspace_bytes(600, 1100, 72, True), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(B.gbo_xent_workspace_bytes(600, 1100, d, True), dtype=torch.uint8, device="cuda")
     loss, lse = torch.empty(600, device="cuda"), torch.empty(600, device="cuda")
     B.gbo_xent_forward(H, W, y, ws, loss=loss, lse=lse, keep=True)
     layers.linear_cross_entropy(W, H, torch.zeros(1100, dtype=torch.long, device="cuda"))
@@ -397,6 +400,24 @@ def test_many_rows_in_one_and_in_two_calls(ignored):
         close(b, want.dw, want.dw_tol, torch.bfloat16)
 
 
+@pytest.mark.parametrize("n", [2, 5, 31, 32, 33])
+def test_few_rows_among_rows_left_out(n):
+    """Losses of few rows (those that count are fewer still), statistics of runs of the
+    vocabulary that end inside a tile; repeated with the same bits."""
+    H, W, y = inputs(n, 5003, 200, 80 + n, ignored=0.4)
+    want = Want(H, W, y)
+    loss = layers.linear_cross_entropy(H, W, y)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    assert torch.equal(loss, layers.linear_cross_entropy(H, W, y))
+    W[-7:] = 0
+    W[-7:, 0] = -float("inf")  # logits of -inf where h_0 > 0: no part in the sum
+    H[:, 0] = H[:, 0].abs() + 1
+    y = torch.where(y >= 4990, y - 4990, y)
+    loss = layers.linear_cross_entropy(H, W, y)
+    want = Want(H, W[:-7], y)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+
+
 def test_weights_that_sum_to_zero():
     """The mean over weights +1 and -1: the loss and its gradients are 0, not inf."""
     H, W, y = inputs(2, 300, 64, 71)
@@ -408,13 +429,14 @@ def test_weights_that_sum_to_zero():
     assert torch.equal(Hg.grad, torch.zeros_like(H)) and torch.equal(Wg.grad, torch.zeros_like(W))
 
 
+@pytest.mark.parametrize("d", [64, 512])
 @pytest.mark.parametrize("cap", ["keep", "pieces"])
-def test_two_backward_passes(cap):
+def test_two_backward_passes(cap, d):
     """retain_graph: the second pass has no kept logits, and the same gradients by its own
     bounds; a gradient of a gradient is refused."""
-    H, W, y = inputs(70, 900, 64, 72, ignored=0.1)
+    H, W, y = inputs(70, 900, d, 72, ignored=0.1)
     want = Want(H, W, y)
-    cap = 0 if cap == "keep" else smallest_cap(70, 900, 64)
+    cap = 0 if cap == "keep" else smallest_cap(70, 900, d)
     Hg, Wg = H.clone().requires_grad_(), W.clone().requires_grad_()
     loss = layers.linear_cross_entropy_loss(Hg, Wg, y, workspace_cap=cap)
     for _ in range(2):
@@ -445,3 +467,24 @@ def test_status_and_single_rows_through_autograd():
     close(loss, want.loss, want.loss_tol, torch.float32)
     close(dh, want.dh, want.dh_tol, torch.bfloat16)
     close(dw, want.dw, want.dw_tol, torch.bfloat16)
+
+
+def test_many_wide_rows_in_one_and_in_two_calls():
+    """The same with rows wide enough for kept logits; rows that are out of the kept range
+    have the class of their smallest logit as their label."""
+    H, W, y = inputs(6500, 777, 520, 68, ignored=0.2)
+    for r in (1000, 1002, 4000):
+        H[r] *= 100
+        y[r] = (W.double() @ H[r].double()).argmin()
+    want = Want(H, W, y)
+    assert (want.loss[[1000, 1002, 4000]] > 64).all()
+    loss, dh, dw = layers.linear_cross_entropy_grad(H, W, y)
+    lse, ws = torch.empty(6500, device="cuda"), torch.empty(B.gbo_xent_workspace_bytes(6500, 777, 520, True),
+                                                            dtype=torch.uint8, device="cuda")
+    B.gbo_xent_forward(H, W, y, ws, lse=lse, keep=True)
+    dh2, dw2 = torch.empty_like(H), torch.empty_like(W)
+    B.gbo_xent_backward(H, W, y, lse, ws, dh=dh2, dw=dw2, keep=True)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    for a, b in ((dh, dw), (dh2, dw2)):
+        close(a, want.dh, want.dh_tol, torch.bfloat16)
+        close(b, want.dw, want.dw_tol, torch.bfloat16)
