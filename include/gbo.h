@@ -512,7 +512,8 @@ typedef struct {
  * gbo_xent_grad, gbo_xent_backward, and gbo_xent_forward with keep.  With
  * room for the whole vocabulary's gradients of the logits (2 bytes each), the
  * logits are kept there between the passes, in steps of 2^-9 bits from the
- * label's.  Otherwise (and for 2^23 logits and more of rows narrower than 512,
+ * label's (what has less than 2^-64 of the label's probability counts as 0).
+ * Otherwise (and for 2^23 logits and more of rows narrower than 512,
  * where it is faster) they are formed again, piece by piece of the vocabulary,
  * each piece as wide as the workspace allows and 2 GiB at most (a third more
  * tensor core work).  cap > 0: the most that fits in `cap`

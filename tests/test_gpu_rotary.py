@@ -351,3 +351,24 @@ def test_positions_changed_before_the_backward_pass_are_noticed():
         y.sum().backward()
     with pytest.raises(RuntimeError):
         (yq.sum() + yk.sum()).backward()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last tokens come out as in a call of their own."""
+    seq, nh, dim = 140000, 120, 128
+    assert seq * nh * dim > 2 ** 31
+    spec = layers.RotarySpec(dim)
+    x = torch.empty(1, seq, nh, dim, dtype=torch.bfloat16, device="cuda")
+    x[:, :, 0] = 1.0
+    x[:, :, 1:].copy_(torch.randn(1, 1, nh - 1, dim, device="cuda"))
+    x[:, -9:].copy_(torch.randn(1, 9, nh, dim, device="cuda"))
+    tail, k = x[:, -9:].clone(), torch.ones(1, seq, 1, dim, dtype=torch.bfloat16, device="cuda")
+    start = 5
+    y = layers.rotary(x, start, spec)
+    assert torch.equal(y[:, -9:], layers.rotary(tail, start + seq - 9, spec))
+    gain = torch.linspace(0.5, 1.5, dim, device="cuda")
+    y, _ = layers.qk_norm_rotary(x, k, gain, None, start, spec)
+    assert torch.equal(y[:, -9:], layers.qk_norm_rotary(tail, k[:, -9:], gain, None, start + seq - 9, spec)[0])
+    dx = layers.qk_norm_rotary_backward(y, k, x, k, gain, None, start, spec)[0]
+    want = layers.qk_norm_rotary_backward(y[:, -9:].clone(), k[:, -9:], tail, k[:, -9:], gain, None, start + seq - 9, spec)[0]
+    assert torch.equal(dx[:, -9:], want)

@@ -488,3 +488,55 @@ def test_many_wide_rows_in_one_and_in_two_calls():
     for a, b in ((dh, dw), (dh2, dw2)):
         close(a, want.dh, want.dh_tol, torch.bfloat16)
         close(b, want.dw, want.dw_tol, torch.bfloat16)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements of W, of dW and of kept logits: losses and dH of sampled
+    rows, and dW of sampled classes, the last ones among them."""
+    n, v, d = 2100, 1050000, 2056
+    assert v * d > 2 ** 31 and n * v > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(91)
+    W = torch.empty(v, d, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, v, 131072):
+        W[a:a + 131072] = torch.randn(min(131072, v - a), d, generator=g, device="cuda") / d ** 0.5
+    y = torch.randint(0, v, (n,), generator=g, device="cuda")
+    y[-1], y[0], y[7] = v - 1, 0, -1
+    H = (torch.randn(n, d, generator=g, device="cuda") + 6 * W[y.clamp(min=0)].float()).bfloat16()
+    cap = 16 << 30
+    assert B.gbo_xent_workspace_bytes(n, v, d, True, cap) > 2 * n * v
+    lse = torch.empty(n, device="cuda")
+    ws = torch.empty(B.gbo_xent_workspace_bytes(n, v, d, True, cap), dtype=torch.uint8, device="cuda")
+    loss, dh, dw = torch.empty(n, device="cuda"), torch.empty_like(H), torch.empty_like(W)
+    B.gbo_xent_grad(H, W, y, ws, loss=loss, lse=lse, dh=dh, dw=dw)
+    del ws
+    rows = torch.tensor([0, 6, 1031, n - 1], device="cuda")
+    Hr = H[rows].double()
+    L = torch.cat([Hr @ W[a:a + 65536].double().T for a in range(0, v, 65536)], 1)
+    size = torch.cat([Hr.abs() @ W[a:a + 65536].double().abs().T for a in range(0, v, 65536)], 1)
+    D, want_lse = 2 * d * U * size, torch.logsumexp(L, 1)
+    dl = D.max(1).values + 64 * U * (want_lse.abs() + 1)
+    at, pick = torch.arange(4, device="cuda"), y[rows]
+    want = want_lse - L[at, pick]
+    tol = dl + D[at, pick] + 64 * U * (want_lse.abs() + 1)
+    assert torch.all((loss[rows].double() - want).abs() <= tol + 2 * U * want.abs())
+    gain = 1.0 / (n - 1)
+    soft = torch.softmax(L, 1)
+    P = soft.clone()
+    P[at, pick] -= 1
+    dP = 2.0 ** -8 * P.abs() + soft * (2 * (D + dl[:, None]) + 2.0 ** -10)
+    parts = [(P[:, a:a + 65536] @ w, dP[:, a:a + 65536] @ w.abs(), P[:, a:a + 65536].abs() @ w.abs())
+             for a in range(0, v, 65536) for w in (W[a:a + 65536].double(),)]
+    want, off, terms = (sum(p[k] for p in parts) for k in range(3))
+    tol = gain * (off + 2 * v * U * terms)
+    assert torch.all((dh[rows].double() - gain * want).abs() <= tol * (1 + 2.0 ** -7) + 2.0 ** -8 * (gain * want).abs())
+    assert not dh[7].any() and loss[7] == 0
+    classes = torch.tensor([0, 1, 524287, 1048575, 1048576, v - 2, v - 1], device="cuda")
+    use, Hd, Wc = (y >= 0)[:, None], H.double(), W[classes].double()
+    Lc = Hd @ Wc.T
+    D = 2 * d * U * (Hd.abs() @ Wc.abs().T)
+    soft = torch.where(use, (Lc - lse.double()[:, None]).exp(), 0.0)
+    P = soft - (y[:, None] == classes).double()
+    # (lse is the kernel's, within 64 u (|lse| + 1) and the largest D of its row)
+    dP = 2.0 ** -8 * P.abs() + soft * (2 * (D + dl.max() + 64 * U * (lse.double().abs() + 1)[:, None]) + 2.0 ** -10)
+    want, tol = gain * (P.T @ Hd), gain * (dP.T @ Hd.abs() + 2 * n * U * (P.abs().T @ Hd.abs()))
+    assert torch.all((dw[classes].double() - want).abs() <= tol * (1 + 2.0 ** -7) + 2.0 ** -8 * want.abs())
