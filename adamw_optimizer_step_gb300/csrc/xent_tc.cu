@@ -37,8 +37,8 @@
 // on, W's HBM traffic below.  Measured, of cuBLAS's 1944 TFLOP/s burst rate:
 // losses of 4096 rows, 128256 x 2048: 1.04 ms alone, 1.22 ms in a loop under
 // the power limit (2.07 and 1.76 PFLOP/s); losses and gradients of 8192 rows,
-// 128000 x 2048: 7.8 and 8.2 ms (6 n v d operations: 1.65 and 1.56 PFLOP/s;
-// forward 2.29 ms, convert 0.63 at 6.7 TB/s, products 4.70); 9.95 ms when the
+// 128000 x 2048: 7.75 and 8.2 ms (6 n v d operations: 1.65 and 1.56 PFLOP/s;
+// forward 2.29 ms, convert 0.59 at 7.2 TB/s, products 4.70); 9.95 ms when the
 // backward pass formed the logits again.  Converting the logits of one part
 // of the rows beside the products of the next, in warps of their own, hid the
 // conversion but slowed the products: 7.7 and 8.2 ms, not kept.  Prefetching
@@ -1225,19 +1225,26 @@ struct ConvertParams {
   float scale, z;
 };
 
-constexpr int kConvertCols = 256 * 8 * 2;  // columns of a block
+constexpr int kConvertThreads = 256, kConvertLoads = 4;
+constexpr int kConvertCols = kConvertThreads * 8 * kConvertLoads;  // columns of a block
 
 // P from the kept logits, in place: 2 bytes read and written per entry, HBM
-// bound.  One row and kConvertCols columns a block.
-__global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant__ ConvertParams C) {
+// bound.  One row and kConvertCols columns a block; 1 / 2 / 4 / 8 loads of 16
+// bytes in flight a thread: 835 / 639 / 586 / 587 us for 8192 x 128000 (7.2
+// TB/s, the last logits of the forward pass from L2).
+__global__ void __launch_bounds__(kConvertThreads) xent_convert_kernel(const __grid_constant__ ConvertParams C) {
   pdl_launch();
   const uint32_t across = (uint32_t)(C.v + kConvertCols - 1) / kConvertCols;
   const int64_t i = blockIdx.x / across;
   const int c0 = (int)(blockIdx.x % across) * kConvertCols + threadIdx.x * 8;
   pdl_wait();
-  const int rows = C.head->rows;
-  if (i >= ((int64_t)rows + kTile - 1) / kTile * kTile || C.redo[i / kTile]) return;
+  const int rows = C.head->rows, redo = C.redo[i / kTile];
+  if (i >= ((int64_t)rows + kTile - 1) / kTile * kTile || redo) return;
   uint16_t *row = C.p + i * C.ld;
+  uint4 raw[kConvertLoads];
+#pragma unroll
+  for (int u = 0; u < kConvertLoads; ++u)
+    if (c0 + u * (8 * kConvertThreads) < C.v) raw[u] = *reinterpret_cast<const uint4 *>(row + c0 + u * (8 * kConvertThreads));
   float wt = 0.f, off = 0.f, peak = 0.f, mult = 0.f;
   int lab = -1;
   if (i < rows) {
@@ -1245,13 +1252,9 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
     wt = C.wt[i], lab = C.lab[i], off = C.ll2[i] - lse2;
     mult = wt * C.scale, peak = mult * fmaf(2.f * C.z, lse2 * kLn2, 1.f);
   }
-  uint4 raw[2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
-    if (c0 + u * 2048 < C.v) raw[u] = *reinterpret_cast<const uint4 *>(row + c0 + u * 2048);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int c = c0 + u * 2048;
+  for (int u = 0; u < kConvertLoads; ++u) {
+    const int c = c0 + u * (8 * kConvertThreads);
     if (c >= C.v) continue;
     const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
     float v[8];
@@ -1665,7 +1668,7 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
       C.scale = a->logit_scale, C.z = a->z_loss;
       const int64_t blocks = (a->v + kConvertCols - 1) / kConvertCols * S.n_pad;
       if (blocks > INT32_MAX) return xent_fail(GBO_ERR_SHAPE, "more kept logits than one launch takes: cap the workspace");
-      if ((e = chain(xent_convert_kernel, dim3((unsigned)blocks), dim3(256), st, C)) != cudaSuccess) return cuda_err(e);
+      if ((e = chain(xent_convert_kernel, dim3((unsigned)blocks), dim3(kConvertThreads), st, C)) != cudaSuccess) return cuda_err(e);
       P.redo = redo, P.only_redo = 1;
     }
     for (int32_t c = 0; c < S.pieces; ++c) {
