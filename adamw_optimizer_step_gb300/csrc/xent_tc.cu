@@ -753,36 +753,38 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 // few rows
 
-// Statistics of at most kScoreRows rows: W is read once and its HBM traffic is
-// all there is, so the operands change places.  The vocabulary is M (tiles of
-// 128 rows of W), the rows are N = 16, a stage of the ring is 32 KB of W and
-// 4 KB of H, and five of six are on their way while one is multiplied.
-// Each CTA takes a run of the vocabulary, equal to within 16 rows.  A thread
-// of the epilogue owns a row of W and keeps a running maximum and sum for
-// every row of H; lanes join once, at the end.
+// Statistics of at most 32 rows: W is read once and its HBM traffic is all
+// there is, so the operands change places.  The vocabulary is M (tiles of 128
+// rows of W), the rows are N = 16 or 32, a stage of the ring is 32 KB of W and
+// 4 or 8 KB of H, and four of five are on their way while one is multiplied.
+// A thread of the epilogue owns a row of W and keeps a running maximum and sum
+// for every row of H; lanes join once, at the end.
+// CTAs take whole tiles in turn, so that all SMs read one window of W; what
+// the last rounds of them leave is cut equally, in one or two tiles a CTA with
+// a box of their own height (a tile in boxes of 16 rows moves at a third of
+// the rate, and one run of consecutive rows a CTA from the start costs 2%).
 // One token over 128000 x 2048 (524 MB), the whole call: 102 us with the
-// 256-wide tiles, 97 us here, where a plain reduction that reads W once takes
-// 92 us.  Three to six stages, 64-row tiles and stages twice as wide measure
-// the same or less: HBM is the bound (the kernel alone: 85 us, 6.1 TB/s).
-// Prefetching each next tile's rows to L2 made it 137 us.  More rows: the
-// epilogue grows with them (the whole call, here / 256-wide tiles, in us: 1
-// row of 40000 x 1024 20.3 / 24.2, of 32000 x 1024 20.4 / 19.8; 16 rows of
-// 32000 x 1024 22.5 / 19.6, of 128000 x 1024 56.8 / 56.6, of 128000 x 2048
-// 99.7 / 104.0; a variant of 32 rows at 32: 24.2 / 19.6, 58.2 / 56.7, 100.5 /
-// 103.9).
-constexpr int kScoreRows = 16;
+// 256-wide tiles; here 97 us with runs that end in 16-row boxes, 87 us as it
+// is (a plain reduction that reads W once takes 92 us).  Four or six stages,
+// 64-row tiles and stages twice as wide measure the same or more: HBM is the
+// bound.  Prefetching each next tile's rows to L2 made it 137 us.
+constexpr int kScoreMost = 32;
 constexpr int kScoreUnit = 16;                                   // rows of W that a run is made of
-constexpr int kScoreB = kScoreRows * kBlockK * 2;                // 2 KB: H's rows, one K block
-constexpr int kScoreStage = 2 * (kOpBytes + kScoreB);
-constexpr int kScoreStages = 6;
-constexpr int kScoreSmem = 1024 + kScoreStages * kScoreStage + 256 + kScoreRows * 8;
+constexpr int kScoreStages = 5;
 constexpr int kScoreWarps = 4;                                   // epilogue
-constexpr int kScoreTmem = 2 * kScoreRows;                       // two 128 x 16 accumulators
 constexpr int kScoreAhead = 4;                                   // rows whose sums run side by side
-static_assert(kScoreSmem <= 232448, "shared memory per CTA");
+
+template <int kRows>
+struct ScoreShape {
+  static constexpr int kB = kRows * kBlockK * 2;                 // H's rows, one K block
+  static constexpr int kStage = 2 * (kOpBytes + kB);
+  static constexpr int kSmem = 1024 + kScoreStages * kStage + 256 + kRows * 8;
+  static constexpr int kTmem = 2 * kRows;                        // two accumulators of 128 x kRows
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
 
 struct ScoreParams {
-  CUtensorMap mapW, mapW16, mapH;  // boxes of 128, 16 and 16 rows
+  CUtensorMap mapW, mapRest, mapH;  // boxes of 128, `step` and kRows rows
   const XentHead *head;
   const int32_t *lab;
   const float *ll2;
@@ -791,6 +793,7 @@ struct ScoreParams {
   int32_t *status;
   int64_t part_ld, w_stride;
   int32_t v, d;
+  int32_t whole, step;  // whole tiles of a CTA, rows of its other tiles
   float scale2;
 };
 
@@ -808,7 +811,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
 }
 
+template <int kRows>
 __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constant__ ScoreParams P) {
+  using Shape = ScoreShape<kRows>;
+  constexpr int kScoreStage = Shape::kStage, kScoreB = Shape::kB;
   pdl_launch();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -816,15 +822,18 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kScoreStages + 5);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
   int32_t *lab_s = reinterpret_cast<int32_t *>(bars + 32);
-  float *ll2_s = reinterpret_cast<float *>(lab_s + kScoreRows);
+  float *ll2_s = reinterpret_cast<float *>(lab_s + kRows);
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kScoreStages);
   const uint32_t accf0 = smem_u32(bars + 2 * kScoreStages), acce0 = accf0 + 16, drain = accf0 + 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // this CTA's run of the vocabulary
-  const int units = (P.v + kScoreUnit - 1) / kScoreUnit, base = units / (int)gridDim.x, rem = units % (int)gridDim.x;
-  const int cid = blockIdx.x, row0 = kScoreUnit * (cid * base + min(cid, rem));
-  const int run = kScoreUnit * (base + (cid < rem ? 1 : 0)), end = min(row0 + run, P.v);
-  const int tiles = (run + BM - 1) / BM, kit = (P.d + kStageK - 1) / kStageK;
+  // this CTA's rows of W: `whole` tiles, dealt out, then an equal run of what
+  // is left, in tiles of `step` rows
+  const int cid = blockIdx.x, ncta = gridDim.x, kit = (P.d + kStageK - 1) / kStageK;
+  const int rest = P.whole * ncta * BM;
+  const int units = (P.v - rest + kScoreUnit - 1) / kScoreUnit, base = units / ncta, rem = units % ncta;
+  const int run0 = rest + kScoreUnit * (cid * base + min(cid, rem)), run = kScoreUnit * (base + (cid < rem ? 1 : 0));
+  const int tiles = P.whole + (run + P.step - 1) / P.step;
+  auto tile_row = [&](int t) { return t < P.whole ? (t * ncta + cid) * BM : run0 + (t - P.whole) * P.step; };
   if (threadIdx.x == 0) {
     for (int s = 0; s < kScoreStages; ++s) mbar_init(full0 + 8 * s, 1), mbar_init(empty0 + 8 * s, 1);
     for (int a = 0; a < 2; ++a) mbar_init(accf0 + 8 * a, 1), mbar_init(acce0 + 8 * a, kScoreWarps);
@@ -834,13 +843,13 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(kScoreTmem)
+                 "r"(Shape::kTmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  const int rows = P.head->rows;  // at most kScoreRows
-  if (threadIdx.x < kScoreRows) {
+  const int rows = P.head->rows;  // at most kRows
+  if (threadIdx.x < kRows) {
     lab_s[threadIdx.x] = (int)threadIdx.x < rows ? P.lab[threadIdx.x] : -1;
     ll2_s[threadIdx.x] = (int)threadIdx.x < rows ? P.ll2[threadIdx.x] : 0.f;
   }
@@ -864,11 +873,9 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
       uint32_t armed = 0, armed_parity = 0;
       bool ok = true;
       for (int t = 0; t < tiles && ok; ++t) {
-        // whole tiles in one box; the last one's 16-row groups one by one
-        // (its other rows are whatever the ring holds: accumulators that
-        // nobody reads)
-        const int left = run - t * BM, boxes = left >= BM ? 0 : left / kScoreUnit;
-        const uint32_t bytes = 2u * (uint32_t)((boxes ? boxes * (kOpBytes / 8) : kOpBytes) + kScoreB);
+        const bool full = t < P.whole;
+        const int r0 = tile_row(t);
+        const uint32_t bytes = 2u * (uint32_t)((full ? BM : P.step) * kBlockK * 2 + kScoreB);
         for (int kb = 0; kb < kit; ++kb) {
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1)) { give_up(); ok = false; break; }
           if (*abort_flag) { ok = false; break; }
@@ -881,9 +888,7 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
             const uint32_t sa = ring0 + stage * kScoreStage + sub * kOpBytes;
             const uint32_t sb = ring0 + stage * kScoreStage + 2 * kOpBytes + sub * kScoreB;
             const int k = kb * kStageK + sub * kBlockK;
-            if (!boxes) tma_load_3d(sa, &P.mapW, fb, k, row0 + t * BM, 0);
-            for (int h = 0; h < boxes; ++h)
-              tma_load_3d(sa + h * (kOpBytes / 8), &P.mapW16, fb, k, row0 + t * BM + h * kScoreUnit, 0);
+            tma_load_3d(sa, full ? &P.mapW : &P.mapRest, fb, k, r0, 0);
             tma_load_3d(sb, &P.mapH, fb, k, 0, 0);
           }
           next();
@@ -895,7 +900,7 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kScoreRows >> 3) << 17) |
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 3) << 17) |
                              ((uint32_t)(BM >> 4) << 24);
       const uint64_t a0 = smem_desc(ring0, 16, 1024), b0 = smem_desc(ring0 + 2 * kOpBytes, 16, 1024);
       bool issued = false, ok = true;
@@ -915,7 +920,7 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
               asm volatile(
                   "{\n\t.reg .pred p;\n\t"
                   "setp.ne.b32 p, %4, 0;\n\t"
-                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_base + acc * kScoreRows),
+                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_base + acc * kRows),
                   "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)((kb | sub | k) != 0))
                   : "memory");
             }
@@ -932,21 +937,25 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
     }
   } else {
     const int quarter = warp & 3;
-    float m[kScoreRows], s[kScoreRows];
+    float m[kRows], s[kRows];
 #pragma unroll
-    for (int j = 0; j < kScoreRows; ++j) m[j] = -INFINITY, s[j] = 0.f;
+    for (int j = 0; j < kRows; ++j) m[j] = -INFINITY, s[j] = 0.f;
     bool ok = true;
     for (int t = 0; t < tiles; ++t) {
-      const int acc = t & 1, r = row0 + t * BM + quarter * 32 + lane;
+      const int acc = t & 1, r0 = tile_row(t), r = r0 + quarter * 32 + lane;
+      // (a tile of the run may end in rows that are the next CTA's, or in none)
+      const int end = min(t < P.whole ? P.v : min(run0 + run, r0 + P.step), P.v);
       if (!mbar_wait(accf0 + 8 * acc, (t >> 1) & 1)) { give_up(); ok = false; break; }
       tc_fence_after();
-      float v[kScoreRows];
-      tmem_ld16(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kScoreRows), v);
+      float v[kRows];
+      const uint32_t at = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kRows);
+      if constexpr (kRows == 16) tmem_ld16(at, v);
+      else tmem_ld32(at, v);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acce0 + 8 * acc);
 #pragma unroll
-      for (int j0 = 0; j0 < kScoreRows; j0 += kScoreAhead) {
+      for (int j0 = 0; j0 < kRows; j0 += kScoreAhead) {
         if (j0 >= rows) break;
 #pragma unroll
         for (int j = j0; j < j0 + kScoreAhead; ++j) {  // rows behind the last one: zeros that nobody reads
@@ -960,7 +969,7 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
     }
     if (ok) {
 #pragma unroll
-      for (int j0 = 0; j0 < kScoreRows; j0 += kScoreAhead) {
+      for (int j0 = 0; j0 < kRows; j0 += kScoreAhead) {
         if (j0 >= rows) break;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -983,7 +992,7 @@ __global__ void __launch_bounds__(192, 1) xent_score_kernel(const __grid_constan
   __syncthreads();
   tc_fence_after();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kScoreTmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(Shape::kTmem) : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -1367,7 +1376,7 @@ XentSpace space_of(int64_t n, int64_t v, int64_t d, bool grad, bool forward, boo
   s.hc = take(2 * s.n_pad * s.hc_ld);
   // statistics: per epilogue warp's columns, or (few rows) per CTA and epilogue warp
   int64_t slots = (v + kSpan - 1) / kSpan;
-  if (n <= kScoreRows) slots = std::max<int64_t>(slots, kScoreWarps * kMostSms);
+  if (n <= kScoreMost) slots = std::max<int64_t>(slots, kScoreWarps * kMostSms);
   const int64_t part = forward ? 8 * s.n_pad * slots : 0;
   if (!grad) {
     s.part = take(part);
@@ -1526,26 +1535,47 @@ int cuda_err(cudaError_t e) {
   return xent_fail(GBO_ERR_CUDA, msg);
 }
 
-// Statistics of at most kScoreRows rows; *blocks: CTAs, each with a slot of
+// Few rows: which kernel takes their statistics (see xent_score_kernel; 0: the
+// 256-wide tiles).  Up to 16 rows, and up to 32 where the table is large: the
+// epilogue grows with the rows.  Us, 16 / 32 / wide, for 1 row of 128000 x 2048
+// 87.0 / 88.0 / 103.3, of 32000 x 1024 15.8 / 16.5 / 19.8; 16 rows 88.7 / 89.5
+// / 104.0 and 17.9 / 18.3 / 19.6, of 1000 x 64 10.6 / 10.7 / 10.0; 32 rows of
+// 128000 x 2048 - / 91.6 / 101.7, 128000 x 320 - / 25.4 / 30.1, 50257 x 768 -
+// / 22.2 / 21.1, 32000 x 1024 - / 21.0 / 19.5.
+constexpr int64_t kScoreTable = 80000000;  // bytes
+int score_rows(int64_t n, int64_t v, int64_t d) {
+  return n <= 16 ? 16 : n <= kScoreMost && 2 * v * d >= kScoreTable ? 32 : 0;
+}
+
+// Statistics of at most kRows rows; *blocks: CTAs, each with a slot of
 // statistics per epilogue warp.
+template <int kRows>
 int run_score(const gbo_xent_args *a, const XentParams &P, const RowsParams &R, int sm, cudaStream_t st, int *blocks) {
   ScoreParams Q;
   memset(&Q, 0, sizeof Q);
   Q.head = P.head, Q.lab = P.lab, Q.ll2 = P.ll2, Q.part = P.part, Q.part_ld = P.part_ld, Q.status = P.status;
   Q.w = R.w, Q.w_stride = a->w_stride, Q.v = (int32_t)a->v, Q.d = P.d, Q.scale2 = P.scale2;
-  if (!map_2d(&Q.mapW, a->w, a->d, a->v, a->w_stride, kBlockK, BM) ||
-      !map_2d(&Q.mapW16, a->w, a->d, a->v, a->w_stride, kBlockK, kScoreUnit) ||
-      !map_2d(&Q.mapH, R.hc, a->d, kTile, R.hc_stride, kBlockK, kScoreRows))
-    return xent_fail(GBO_ERR_CUDA, "tensor map of H or W");
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(xent_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+    attr_err = cudaFuncSetAttribute(xent_score_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    ScoreShape<kRows>::kSmem);
   });
   if (attr_err != cudaSuccess) return cuda_err(attr_err);
   // one CTA an SM, each with at least two 16-row units
   *blocks = (int)std::min<int64_t>(std::min(sm, kMostSms), std::max<int64_t>(1, a->v / (2 * kScoreUnit)));
-  const cudaError_t e = launch_kernel_as(pdl_allowed(), xent_score_kernel, dim3(*blocks), dim3(192), kScoreSmem, st, 1, Q);
+  // rounds of whole tiles; the last round and what is left are one run a CTA
+  const int64_t round = (int64_t)BM * *blocks;
+  Q.whole = (int32_t)std::max<int64_t>(0, (a->v - 1) / round - 1);
+  const int64_t units = (a->v - Q.whole * round + kScoreUnit - 1) / kScoreUnit, most = (units + *blocks - 1) / *blocks;
+  const int64_t parts = (most * kScoreUnit + BM - 1) / BM;
+  Q.step = (int32_t)((most + parts - 1) / parts * kScoreUnit);
+  if (!map_2d(&Q.mapW, a->w, a->d, a->v, a->w_stride, kBlockK, BM) ||
+      !map_2d(&Q.mapRest, a->w, a->d, a->v, a->w_stride, kBlockK, Q.step) ||
+      !map_2d(&Q.mapH, R.hc, a->d, kTile, R.hc_stride, kBlockK, kRows))
+    return xent_fail(GBO_ERR_CUDA, "tensor map of H or W");
+  const cudaError_t e = launch_kernel_as(pdl_allowed(), xent_score_kernel<kRows>, dim3(*blocks), dim3(192),
+                                         ScoreShape<kRows>::kSmem, st, 1, Q);
   count_launches(1);
   return e == cudaSuccess ? GBO_OK : cuda_err(e);
 }
@@ -1633,9 +1663,10 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     P.v0 = 0, P.v_piece = (int32_t)a->v;
     const int64_t n_tiles = (a->v + kTile - 1) / kTile;
     int64_t slots = (a->v + kSpan - 1) / kSpan;
-    if (a->n <= kScoreRows && !S.keep) {
+    if (const int few = S.keep ? 0 : score_rows(a->n, a->v, a->d)) {
       int blocks = 0;
-      if ((rc = run_score(a, P, R, sm, st, &blocks)) != GBO_OK) return rc;
+      rc = few == 16 ? run_score<16>(a, P, R, sm, st, &blocks) : run_score<32>(a, P, R, sm, st, &blocks);
+      if (rc != GBO_OK) return rc;
       slots = (int64_t)kScoreWarps * blocks;
     } else if ((e = launch_xent<kModeStats>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) {
       return cuda_err(e);

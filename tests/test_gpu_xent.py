@@ -418,6 +418,19 @@ def test_few_rows_among_rows_left_out(n):
     close(loss, want.loss, want.loss_tol, torch.float32)
 
 
+@pytest.mark.parametrize("n,v,d", [(1, 40009, 72), (16, 58369, 64), (3, 38913, 200), (17, 40009, 1000), (32, 60001, 680)])
+def test_few_rows_of_large_tables(n, v, d):
+    """Tables of several tiles an SM, whose last rows are cut in runs that end anywhere."""
+    H, W, y = inputs(n, v, d, v + n, ignored=0.2 if n > 3 else 0.0)
+    y[-1] = v - 1
+    want = Want(H, W, y)
+    lse, totals = torch.empty(n, device="cuda"), torch.empty(2, device="cuda")
+    loss = layers.linear_cross_entropy(H, W, y, lse=lse, totals=totals)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(lse, torch.where(want.use, want.lse, torch.zeros_like(want.lse)), want.loss_tol, torch.float32)
+    close(totals[0], want.total, want.total_tol, torch.float32)
+
+
 def test_weights_that_sum_to_zero():
     """The mean over weights +1 and -1: the loss and its gradients are 0, not inf."""
     H, W, y = inputs(2, 300, 64, 71)
