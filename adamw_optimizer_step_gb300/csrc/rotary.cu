@@ -8,13 +8,15 @@
 // Bound: HBM.  Each element is read once and written once (backward: x and
 // dy read, dx written); a head's norm stays in registers and warp shuffles.
 // Measured on 32768 tokens x 20 heads of 128 in bf16: forward 56 us, 5.9 TB/s
-// (88% of a copy); backward 95 us, 5.3 TB/s; 32768 x 32 heads of 192 with 64
-// rotated and no norm: 120 us, 6.7 TB/s.  What carried the forward there from
-// 88 us: the asynchronous ring (heads in flight without registers), two fp32
-// lanes per instruction, hardware sines for bf16, 32-bit index division.  The
-// backward's 111 registers leave 16 warps an SM; at 80 (24 warps) it spills
-// and measured 127 us.  Carrying the ring on into the next item, sines kept
-// negated in registers and sums without loops were slower or no faster.
+// (88% of a copy); backward 92 us, 5.5 TB/s (88 us in a graph); 32768 x 32
+// heads of 192 with 64 rotated and no norm: 120 us, 6.7 TB/s.  What carried
+// the forward there from 88 us: the asynchronous ring (heads in flight without
+// registers), two fp32 lanes per instruction, hardware sines for bf16, 32-bit
+// index division.  The backward's 111 registers leave 16 warps an SM; at 80
+// (24 warps) it spills and measured 127 us.  Carrying the ring on into the
+// next item, sines kept negated in registers and sums without loops were
+// slower or no faster; as many blocks as are resident, which loop, 67 us
+// forward.
 //
 // Work split.  A head is cut into units of two 16-byte chunks: the two halves
 // of a run of pairs (GBO_ROPE_HALF), two chunks of whole pairs
@@ -46,11 +48,16 @@ namespace gbo {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-// Backward: blocks per SM that share out the tokens (each leaves one row of
-// partial gain gradients).  2 are resident; 2 / 6 / 12 measured 96.8 / 95.8 /
-// 100.9 us on 32768 tokens x 20 heads of 128 in bf16.
-constexpr int kRopeBackBlocks = 6;
+// Threads of a block.  The gradients of a norm, whose 111 registers leave 16
+// warps an SM either way, take their tokens in smaller blocks: 64 / 128 / 256
+// threads 95 / 92 / 95 us (32768 tokens x 20 heads of 128 in bf16); forward
+// 63 / 58 / 56.
+constexpr int rope_threads(bool norm, bool back) { return norm && back ? 128 : 256; }
+// Gradients of a norm: blocks per SM that share out the tokens (each leaves
+// one row of partial gain gradients), four of them resident: 4 / 6 / 8 / 10 /
+// 12 / 16 measured 91 / 102 / 88 / 94 / 88 / 89 us on the same tokens, 4 / 8 /
+// 12 / 16 87 / 88 / 83 / 83 on 16384 in fp32.
+constexpr int kRopeBackBlocks = 12;
 // Heads a group walks over at most: 2 / 4 / 8 / 16 measured 111 / 67 / 57 / 58
 // us forward on the same tokens.
 constexpr int kMaxHeads = 8;
@@ -257,7 +264,7 @@ __device__ __forceinline__ void rotate(float2 *v, const float2 *c, const float2 
 constexpr int ring_depth(int ch) { return ch == 1 ? 0 : 4; }
 // Bytes of a block's ring: per head in flight, x and / or dy, UPL units of two chunks a thread.
 constexpr int ring_bytes(int chunk_bytes, int ch, int upl, bool norm, bool back) {
-  return ring_depth(ch) * (norm && back ? 2 : 1) * upl * 2 * chunk_bytes * kRopeThreads;
+  return ring_depth(ch) * (norm && back ? 2 : 1) * upl * 2 * chunk_bytes * rope_threads(norm, back);
 }
 
 // UPL: units per lane.  kNorm: with the per-head norm.  kBack: gradients.
@@ -269,8 +276,10 @@ constexpr int ring_bytes(int chunk_bytes, int ch, int upl, bool norm, bool back)
 // waits for another and the loads in flight take no registers: kDepth heads a
 // thread (forward 2 / 3 / 4: 60 / 58 / 57 us; backward 2 / 3 / 4: 97 / 95 / 94).
 template <typename T, int CH, int UPL, bool kNorm, bool kBack>
-__global__ void __launch_bounds__(kRopeThreads, CH == 1 || UPL > 1 ? 1 : kNorm && kBack ? 2 : 4) rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(rope_threads(kNorm, kBack), CH == 1 || UPL > 1 ? 1 : 4)
+    rope_kernel(const __grid_constant__ RopeParams P) {
   pdl_launch();
+  constexpr int kThreads = rope_threads(kNorm, kBack);
   constexpr bool kGrad = kNorm && kBack;
   constexpr bool kUseX = kNorm || !kBack;
   constexpr int kDepth = ring_depth(CH);
@@ -283,9 +292,9 @@ __global__ void __launch_bounds__(kRopeThreads, CH == 1 || UPL > 1 ? 1 : kNorm &
   int ti = 0;
   while (ti + 1 < P.n && (int)blockIdx.x >= P.t[ti + 1].block0) ++ti;
   const RopeTensor &X = P.t[ti];
-  for (int i = threadIdx.x; i < P.rot / 2; i += kRopeThreads) turns[i] = P.turns[i];
+  for (int i = threadIdx.x; i < P.rot / 2; i += kThreads) turns[i] = P.turns[i];
   const int G = P.group, g = threadIdx.x / G, lane_g = threadIdx.x - g * G;
-  const int groups = kRopeThreads / G;
+  const int groups = kThreads / G;
   Unit unit[UPL];
 #pragma unroll
   for (int k = 0; k < UPL; ++k) {
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(kRopeThreads, CH == 1 || UPL > 1 ? 1 : kNorm &
   }
   constexpr int kBytes = CH * (int)sizeof(T);  // of a chunk
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * kBytes;
-  constexpr uint32_t kPiece = kRopeThreads * kBytes;
+  constexpr uint32_t kPiece = kThreads * kBytes;
   auto slot = [&](int d, int in, int k, int which) { return slot0 + (uint32_t)(((d * kIn + in) * UPL + k) * 2 + which) * kPiece; };
   if constexpr (kDepth > 0) {  // chunks that a unit lacks stay zero
     bool lacks = false;
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(kRopeThreads, CH == 1 || UPL > 1 ? 1 : kNorm &
       for (int i = 0; i < CH; ++i) gain_r[k][i] = make_float2(gain_at(k, 2 * i), gain_at(k, 2 * i + 1));
   }
   if constexpr (kGrad) {
-    for (int i = threadIdx.x; i < P.dim; i += kRopeThreads) gain_s[i] = X.gain ? X.gain[i] : 1.f;
+    for (int i = threadIdx.x; i < P.dim; i += kThreads) gain_s[i] = X.gain ? X.gain[i] : 1.f;
 #pragma unroll
     for (int k = 0; k < UPL; ++k)
 #pragma unroll
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(kRopeThreads, CH == 1 || UPL > 1 ? 1 : kNorm &
   if constexpr (kGrad) {
     if (!X.part) return;
     // the groups of a warp by a butterfly, the warps one after another: a fixed order
-    for (int i = threadIdx.x; i < P.dim; i += kRopeThreads) dg_s[i] = 0.f;
+    for (int i = threadIdx.x; i < P.dim; i += kThreads) dg_s[i] = 0.f;
 #pragma unroll
     for (int k = 0; k < UPL; ++k)
 #pragma unroll
@@ -509,7 +518,7 @@ __global__ void __launch_bounds__(kRopeThreads, CH == 1 || UPL > 1 ? 1 : kNorm &
           dg[k][i].x += __shfl_xor_sync(0xffffffffu, dg[k][i].x, o);
           dg[k][i].y += __shfl_xor_sync(0xffffffffu, dg[k][i].y, o);
         }
-    for (int q = 0; q < kRopeThreads / 32; ++q) {
+    for (int q = 0; q < kThreads / 32; ++q) {
       __syncthreads();
       if ((int)(threadIdx.x >> 5) == q && (int)(threadIdx.x & 31) < G) {
 #pragma unroll
@@ -523,7 +532,7 @@ __global__ void __launch_bounds__(kRopeThreads, CH == 1 || UPL > 1 ? 1 : kNorm &
     }
     __syncthreads();
     float *out = X.part + (int64_t)((int)blockIdx.x - X.block0) * P.dim;
-    for (int i = threadIdx.x; i < P.dim; i += kRopeThreads) out[i] = dg_s[i];
+    for (int i = threadIdx.x; i < P.dim; i += kThreads) out[i] = dg_s[i];
   }
 }
 
@@ -605,7 +614,8 @@ cudaError_t launch_rope_n(const RopeParams &P, int blocks, cudaStream_t stream) 
                                     smem);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  return launch_kernel(rope_kernel<T, CH, UPL, kNorm, kBack>, dim3(blocks), dim3(kRopeThreads), smem, stream, 1, P);
+  return launch_kernel(rope_kernel<T, CH, UPL, kNorm, kBack>, dim3(blocks), dim3(rope_threads(kNorm, kBack)), smem,
+                       stream, 1, P);
 }
 
 template <typename T, int CH, int UPL, bool kBack>
@@ -702,7 +712,7 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
   if (norm)
     while (P.group < 32 && P.group < P.units) P.group *= 2;
   else
-    P.group = std::min(P.units, kRopeThreads);
+    P.group = std::min(P.units, rope_threads(false, back));
   const int upl = (P.units + P.group - 1) / P.group;
   P.dim = o->head_dim, P.rot = o->rot_dim, P.offset = o->offset;
   P.interleaved = o->layout == GBO_ROPE_INTERLEAVED;
@@ -718,16 +728,16 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
     P.turns[j] = frac >= 1.0 ? 0 : (uint64_t)std::ldexp(frac, 64);
   }
   P.n = 0;
-  const int groups = kRopeThreads / P.group;
+  const int groups = rope_threads(norm, back) / P.group;
   const int64_t tokens = batch * seq;
   int32_t nblk[GBO_ROPE_MAX_TENSORS] = {};
   if (back) back_blocks(tensors, n, sm, nblk);
   int64_t all_heads = 0;
   for (int32_t i = 0; i < n; ++i) all_heads += tensors[i].heads;
   // heads a group walks over: up to kMaxHeads while the groups still fill the
-  // device (four 256-thread blocks an SM), so that a token's cosines are shared
+  // device (1024 threads an SM), so that a token's cosines are shared
   int32_t per_item = 1;
-  while (per_item < kMaxHeads && tokens * all_heads / (2 * per_item) >= (int64_t)sm * 4 * groups) per_item *= 2;
+  while (per_item < kMaxHeads && tokens * all_heads / (2 * per_item) >= (int64_t)sm * (1024 / P.group)) per_item *= 2;
   int64_t rounds_all = 0;
   for (int32_t i = 0; i < n; ++i) rounds_all += (tokens * ((tensors[i].heads + per_item - 1) / per_item) + groups - 1) / groups;
   const bool few = rounds_all <= (int64_t)2 * kRopeBackBlocks * sm;
@@ -757,15 +767,12 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
       const int64_t round = (int64_t)groups * X.per_item * o->head_dim * (dtype == GBO_BF16 ? 2 : 4);
       const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>((32768 + round - 1) / round, want / (4 * sm)));
       // gradients of a norm: a block's end (its sums of the gains) is dear, too:
-      // where all blocks have two rounds at most, the resident ones (two an SM
-      // with chunks of eight elements, four with fewer) take them all, equally
-      // (1974 tokens x 20 heads of 128: 18.6 -> 13.3 us)
+      // where all blocks have two rounds at most, the resident ones (four an SM
+      // with chunks of eight elements, eight with fewer) take them all (1974
+      // tokens x 20 heads of 128: 18.6 -> 12.6 us)
       int64_t take = std::min<int64_t>((want + rounds - 1) / rounds, 1 << 20);
-      if (back && norm) {
-        const int64_t most = few ? std::max<int64_t>(1, nblk[i] * (CH == 8 ? 2 : 4) / kRopeBackBlocks) : nblk[i];
-        const int64_t each = few ? (want + most - 1) / most : 1;
-        take = std::min<int64_t>((want + each - 1) / each, nblk[i]);
-      }
+      if (back && norm)
+        take = std::min<int64_t>(want, few ? std::max<int64_t>(1, nblk[i] * (CH == 8 ? 4 : 8) / kRopeBackBlocks) : nblk[i]);
       X.block0 = (int32_t)blocks;
       X.nblk = (int32_t)take;
       blocks += take;
