@@ -7,12 +7,12 @@
 //             dgain_j = sum e_j u_j
 // Bound: HBM.  Each element is read once and written once (backward: x and
 // dy read, dx written); a head's norm stays in registers and warp shuffles.
-// Measured on 32768 tokens x 20 heads of 128 in bf16: forward 56 us, 5.9 TB/s
-// (88% of a copy); backward 92 us, 5.5 TB/s (88 us in a graph); 32768 x 32
-// heads of 192 with 64 rotated and no norm: 120 us, 6.7 TB/s.  What carried
+// Measured on 32768 tokens x 20 heads of 128 in bf16: forward 54 us, 6.2 TB/s
+// (91% of a copy); backward 90 us, 5.6 TB/s; 32768 x 32 heads of 192 with 64
+// rotated and no norm: 117 us, 6.9 TB/s.  What carried
 // the forward there from 88 us: the asynchronous ring (heads in flight without
 // registers), two fp32 lanes per instruction, hardware sines for bf16, 32-bit
-// index division.  The backward's 111 registers leave 16 warps an SM; at 80
+// index division.  The backward's 113 registers leave 16 warps an SM; at 80
 // (24 warps) it spills and measured 127 us.  Carrying the ring on into the
 // next item, sines kept negated in registers and sums without loops were
 // slower or no faster; as many blocks as are resident, which loop, 67 us
@@ -48,7 +48,7 @@ namespace gbo {
 
 namespace {
 
-// Threads of a block.  The gradients of a norm, whose 111 registers leave 16
+// Threads of a block.  The gradients of a norm, whose 113 registers leave 16
 // warps an SM either way, take their tokens in smaller blocks: 64 / 128 / 256
 // threads 95 / 92 / 95 us (32768 tokens x 20 heads of 128 in bf16); forward
 // 63 / 58 / 56.
@@ -614,8 +614,11 @@ cudaError_t launch_rope_n(const RopeParams &P, int blocks, cudaStream_t stream) 
                                     smem);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  return launch_kernel(rope_kernel<T, CH, UPL, kNorm, kBack>, dim3(blocks), dim3(rope_threads(kNorm, kBack)), smem,
-                       stream, 1, P);
+  // A block's start (its units, gains and turns) overlaps the end of the kernel
+  // before it on the stream, on direct launches too: queries and keys 56.3 ->
+  // 54.3 us, their gradients 92.4 -> 90.1, heads of 192 119.9 -> 116.6 in a loop.
+  return launch_kernel_as(pdl_allowed(), rope_kernel<T, CH, UPL, kNorm, kBack>, dim3(blocks),
+                          dim3(rope_threads(kNorm, kBack)), smem, stream, 1, P);
 }
 
 template <typename T, int CH, int UPL, bool kBack>
