@@ -163,6 +163,12 @@ def _rows(t):
     return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
+def _constant(value, what):
+    """Refuse a tensor whose gradient the caller waits for and would not get."""
+    if isinstance(value, torch.Tensor) and value.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s has no gradient here: detach it" % what)
+
+
 def _save_positions(ctx, positions, *tensors):
     """Saved as a tensor, so that autograd notices positions that change before the
     backward pass; an int is kept beside it."""
@@ -246,6 +252,7 @@ def rotary_autograd(x, positions, spec):
 
 def qk_norm_rotary_autograd(q, k, q_gain, k_gain, positions, spec, eps=1e-6):
     """:func:`qk_norm_rotary` with its gradients by q, k and the gains."""
+    _constant(eps, "eps")
     return _QkNormRotary.apply(q, k, q_gain, k_gain, positions, spec, eps)
 
 
@@ -255,5 +262,9 @@ def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_s
     (bf16, or a float32 master table, which is cast for the products and gets a
     float32 gradient).  Between the passes the workspace (``workspace_cap``) keeps the
     logits in 16 bits where it has room for them.  ``dev_status``: a CUDA int32 that
-    takes ``GBO_STATUS_BAD_LABEL`` and ``GBO_STATUS_NONFINITE``."""
+    takes ``GBO_STATUS_BAD_LABEL`` and ``GBO_STATUS_NONFINITE``.  ``row_weight``,
+    ``z_loss`` and ``logit_scale`` are constants: refused when they require a gradient."""
+    _constant(row_weight, "row_weight")
+    _constant(z_loss, "z_loss")
+    _constant(logit_scale, "logit_scale")
     return _LinearCrossEntropy.apply(h, w, labels, row_weight, z_loss, logit_scale, workspace_cap, dev_status)
