@@ -212,10 +212,9 @@ class _QkNormRotary(torch.autograd.Function):
 
 class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, h, w, labels, row_weight, z_loss, logit_scale, workspace_cap, dev_status):
+    def forward(ctx, h, w, labels, row_weight, z_loss, logit_scale, workspace_cap, dev_status, grad):
         n, d = h.shape
         wb = w.to(torch.bfloat16)
-        grad = ctx.needs_input_grad[0] or ctx.needs_input_grad[1]
         lse = torch.empty(n, dtype=torch.float32, device=h.device)
         totals = torch.empty(2, dtype=torch.float32, device=h.device)
         ws = torch.empty(B.gbo_xent_workspace_bytes(n, w.shape[0], d, grad, workspace_cap), dtype=torch.uint8,
@@ -242,7 +241,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         B.gbo_xent_backward(h, w, labels, lse, ws, dh=dh, dw=dw, row_weight=row_weight,
                             upstream=up.float().reshape(1), logit_scale=logit_scale, z_loss=z_loss, keep=keep,
                             dev_status=dev_status)
-        return dh, dw, None, None, None, None, None, None
+        return dh, dw, None, None, None, None, None, None, None
 
 
 def rotary_autograd(x, positions, spec):
@@ -261,10 +260,14 @@ def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_s
     """Mean loss over the rows that count, with its gradients by ``h`` (bf16) and ``w``
     (bf16, or a float32 master table, which is cast for the products and gets a
     float32 gradient).  Between the passes the workspace (``workspace_cap``) keeps the
-    logits in 16 bits where it has room for them.  ``dev_status``: a CUDA int32 that
+    logits in 16 bits where it has room for them; under ``torch.no_grad()``, or when neither
+    requires a gradient, it is that of :func:`linear_cross_entropy`.  ``dev_status``: a CUDA int32 that
     takes ``GBO_STATUS_BAD_LABEL`` and ``GBO_STATUS_NONFINITE``.  ``row_weight``,
     ``z_loss`` and ``logit_scale`` are constants: refused when they require a gradient."""
     _constant(row_weight, "row_weight")
     _constant(z_loss, "z_loss")
     _constant(logit_scale, "logit_scale")
-    return _LinearCrossEntropy.apply(h, w, labels, row_weight, z_loss, logit_scale, workspace_cap, dev_status)
+    # (within apply grad mode is off, and ctx.needs_input_grad says what requires a gradient
+    # whether or not a backward pass can follow)
+    grad = torch.is_grad_enabled() and (h.requires_grad or w.requires_grad)
+    return _LinearCrossEntropy.apply(h, w, labels, row_weight, z_loss, logit_scale, workspace_cap, dev_status, grad)

@@ -1,0 +1,65 @@
+"""Corners of the rotary and cross-entropy operators that need a GPU: memory of the loss
+in autograd.
+
+Tolerances are those of test_gpu_rotary.py and test_gpu_xent.py, derived there; where
+another one is taken its reason stands beside it."""
+
+import pytest
+import torch
+
+from adamw_optimizer_step_gb300 import _binding as B
+from adamw_optimizer_step_gb300 import layers
+from tests.test_gpu_xent import Want, close, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from adamw_optimizer_step_gb300 import build
+    build.build()
+    B.lib()
+
+
+# ---------------------------------------------------------------------------
+# memory of the loss in autograd
+
+# small tensors of a call (lse, totals, the mean, upstream), and torch's blocks of 512 bytes
+SLACK = 1 << 16
+
+
+def peak_of(call):
+    torch.cuda.synchronize()
+    base = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    kept = call()
+    torch.cuda.synchronize()
+    return torch.cuda.max_memory_allocated() - base, torch.cuda.memory_allocated() - base, kept
+
+
+def test_memory_of_the_loss():
+    """Without gradients: the workspace of the losses alone, and the same losses.  With
+    them: one workspace from the forward to the backward pass, given back after it
+    although the loss is still held."""
+    n, v, d = 500, 20011, 512
+    H, W, y = inputs(n, v, d, 7, ignored=0.1)
+    small, large = (B.gbo_xent_workspace_bytes(n, v, d, grad) for grad in (False, True))
+    assert large > small + 2 * n * v  # the logits are kept
+    H.requires_grad_()
+    W.requires_grad_()
+    want = Want(H.detach(), W.detach(), y)
+    layers.linear_cross_entropy_loss(H, W, y)  # (first-call set-up is no part of it)
+    with torch.no_grad():
+        peak, _, loss = peak_of(lambda: layers.linear_cross_entropy_loss(H, W, y))
+    assert peak <= small + SLACK
+    close(loss, want.total / want.weight, want.total_tol / want.weight, torch.float32)
+
+    def step():
+        loss = layers.linear_cross_entropy_loss(H, W, y)
+        loss.backward()
+        return loss
+
+    grads = 2 * (n + v) * d
+    peak, left, loss = peak_of(step)
+    assert large <= peak <= large + grads + SLACK
+    assert left <= grads + SLACK and loss.grad_fn is not None

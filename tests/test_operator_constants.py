@@ -54,3 +54,19 @@ def test_the_norms_eps_is_a_constant_too():
     with pytest.raises(ValueError, match="eps"):
         layers.qk_norm_rotary_autograd(q, q, None, None, 0, layers.RotarySpec(8),
                                        eps=torch.tensor(1e-6, requires_grad=True))
+
+
+def test_without_gradients_the_loss_takes_the_losses_own_path(calls):
+    """Under no_grad and inference_mode nothing is kept for a backward pass: the workspace
+    of the losses alone, although the table requires a gradient."""
+    h, w, y = inputs()
+    w.requires_grad_()
+    for off in (torch.no_grad, torch.inference_mode):
+        with off():
+            loss = layers.linear_cross_entropy_loss(h, w, y)
+        assert calls.pop() == dict(keep=False, bytes=1000) and loss.item() == 3.0 and not calls
+    with torch.no_grad(), torch.enable_grad():
+        layers.linear_cross_entropy_loss(h, w, y)
+    assert calls.pop() == dict(keep=True, bytes=2000)
+    layers.linear_cross_entropy_loss(h, w.detach(), y)  # nothing requires a gradient
+    assert calls.pop() == dict(keep=False, bytes=1000)
