@@ -73,10 +73,11 @@ class RotarySpec:
 
     def with_eps(self, eps):
         """The options with the norm's eps (the same frequencies)."""
+        eps = float(eps)  # a tensor's value, not the tensor, is the key
         o = self._eps.get(eps)
         if o is None:
             o = self.opts
-            o = self._eps[eps] = B.RopeOpts(o.head_dim, o.rot_dim, o.offset, o.layout, o.freq, o.magnitude, float(eps))
+            o = self._eps[eps] = B.RopeOpts(o.head_dim, o.rot_dim, o.offset, o.layout, o.freq, o.magnitude, eps)
         return o
 
     def backward_workspace(self, table):
@@ -252,7 +253,7 @@ def rotary_autograd(x, positions, spec):
 def qk_norm_rotary_autograd(q, k, q_gain, k_gain, positions, spec, eps=1e-6):
     """:func:`qk_norm_rotary` with its gradients by q, k and the gains."""
     _constant(eps, "eps")
-    return _QkNormRotary.apply(q, k, q_gain, k_gain, positions, spec, eps)
+    return _QkNormRotary.apply(q, k, q_gain, k_gain, positions, spec, float(eps))
 
 
 def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_scale=1.0, workspace_cap=0,
@@ -270,4 +271,5 @@ def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_s
     # (within apply grad mode is off, and ctx.needs_input_grad says what requires a gradient
     # whether or not a backward pass can follow)
     grad = torch.is_grad_enabled() and (h.requires_grad or w.requires_grad)
-    return _LinearCrossEntropy.apply(h, w, labels, row_weight, z_loss, logit_scale, workspace_cap, dev_status, grad)
+    return _LinearCrossEntropy.apply(h, w, labels, row_weight, float(z_loss), float(logit_scale), workspace_cap,
+                                     dev_status, grad)

@@ -70,3 +70,25 @@ def test_without_gradients_the_loss_takes_the_losses_own_path(calls):
     assert calls.pop() == dict(keep=True, bytes=2000)
     layers.linear_cross_entropy_loss(h, w.detach(), y)  # nothing requires a gradient
     assert calls.pop() == dict(keep=False, bytes=1000)
+
+
+def test_constants_given_as_tensors_are_read_when_the_call_is_made(calls, monkeypatch):
+    """A tensor that changes afterwards changes neither an options record made earlier nor
+    the backward pass, and its next value is taken."""
+    spec, eps = layers.RotarySpec(8), torch.tensor(1e-3)
+    assert abs(spec.with_eps(eps).eps - 1e-3) < 1e-9
+    eps.fill_(1e-5)
+    assert abs(spec.with_eps(eps).eps - 1e-5) < 1e-11
+    assert spec.with_eps(1e-3) is spec.with_eps(torch.tensor(1e-3, dtype=torch.float64))
+
+    given = []
+    wrapped = {name: getattr(B, name) for name in ("gbo_xent_forward", "gbo_xent_backward")}
+    for name, call in wrapped.items():
+        monkeypatch.setattr(B, name, lambda *a, call=call, **k: (given.append((k["z_loss"], k["logit_scale"])),
+                                                                call(*a, **k)))
+    h, w, y = inputs()
+    z, scale = torch.tensor(0.25), torch.tensor(0.5)
+    loss = layers.linear_cross_entropy_loss(h.requires_grad_(), w, y, z_loss=z, logit_scale=scale)
+    z.fill_(7.0), scale.fill_(7.0)
+    loss.backward()
+    assert given == [(0.25, 0.5)] * 2
