@@ -837,7 +837,8 @@ extern "C" int gbo_rope_frequencies(int32_t rot_dim, double base, const gbo_rope
   const int half = rot_dim / 2;
   double b = base;
   if (kind == GBO_ROPE_SCALE_NTK) b = base * std::pow(s->factor, rot_dim / (rot_dim - 2.0));
-  *magnitude = kind == GBO_ROPE_SCALE_YARN ? 0.1 * std::log(s->factor) + 1.0 : 1.0;
+  // a context that is not stretched keeps its scores
+  *magnitude = kind == GBO_ROPE_SCALE_YARN && s->factor > 1.0 ? 0.1 * std::log(s->factor) + 1.0 : 1.0;
   double low = 0.0, high = 0.0;
   if (kind == GBO_ROPE_SCALE_YARN) {
     auto index_at = [&](double turns) {

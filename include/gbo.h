@@ -369,7 +369,7 @@ int gbo_adamw_step(const gbo_adamw_desc *descs, int32_t n, const gbo_adamw_opts 
 #define GBO_ROPE_SCALE_YARN 3       /* f_j below index low, f_j / factor above high, linear in j between,
                                        where a frequency of index low (high) turns `fast` (`slow`) times
                                        over the trained length (floor and ceiling, within 0 .. rot_dim - 1);
-                                       magnitude = 0.1 ln(factor) + 1                                     */
+                                       magnitude = 0.1 ln(factor) + 1, or 1 for factors up to 1           */
 #define GBO_ROPE_SCALE_WAVELENGTH 4 /* with n_j = trained f_j / 2 pi turns over the trained length: f_j
                                        where n_j >= fast, f_j / factor where n_j <= slow, linear in n_j
                                        between                                                            */
