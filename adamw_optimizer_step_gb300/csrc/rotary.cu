@@ -28,9 +28,10 @@
 // over several heads of one token, so the cosines and sines of the token are
 // computed once for them.
 //
-// Angles: t f_j in turns is a 64-bit fixed-point product modulo 2^64, exact
-// for every 64-bit position; its top 32 bits are the angle (turn_of).  No
-// table of cosines is read.
+// Angles: t f_j in turns is a 64-bit fixed-point product modulo 2^64, which
+// rounds nothing for any 64-bit position; its top 32 bits are the angle
+// (turn_of).  What is rounded is the factor, f_j / 2 pi (turns_of).  No table
+// of cosines is read.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -592,6 +593,20 @@ int check_opts(const gbo_rope_opts *o) {
   return GBO_OK;
 }
 
+// A frequency in turns per position, modulo one turn, in 64-bit fixed point.
+// The quotient is off by at most 2^-52 of it (its rounding and that of 2 pi),
+// its fraction is exact, and what falls below 2^-64 turns is cut off: an angle
+// t f is off by at most |t| (2^-52 |f| + 2^-61) radians.  Formed from |f|: the
+// fraction of a small negative quotient, 1 - |f| / 2 pi, would round to 2^-54
+// turns whatever f (660 times that bound at f = -1e-4).  More bits of 2 pi
+// would not help a frequency that a power of the base made: it has a double's
+// rounding itself.
+uint64_t turns_of(double f) {
+  const double turn = std::fabs(f) / 6.283185307179586476925286766559;
+  const uint64_t frac = (uint64_t)std::ldexp(turn - std::floor(turn), 64);
+  return f < 0.0 ? 0 - frac : frac;
+}
+
 // Blocks that share a backward call's tokens over its tensors, in
 // proportion to their heads (a function of the table and the device alone,
 // so that dgain's order of summation does not change from call to call).
@@ -725,11 +740,7 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
     P.pos = pos->ptr, P.pos_b = pos->stride_b, P.pos_s = pos->stride_s, P.start = pos->start;
     P.pos64 = pos->dtype == GBO_I64;
   }
-  for (int j = 0; j < o->rot_dim / 2; ++j) {
-    const double turn = o->freq[j] / 6.283185307179586476925286766559;
-    const double frac = turn - std::floor(turn);  // [0, 1], 1 only by rounding
-    P.turns[j] = frac >= 1.0 ? 0 : (uint64_t)std::ldexp(frac, 64);
-  }
+  for (int j = 0; j < o->rot_dim / 2; ++j) P.turns[j] = turns_of(o->freq[j]);
   P.n = 0;
   const int groups = rope_threads(norm, back) / P.group;
   const int64_t tokens = batch * seq;

@@ -436,9 +436,12 @@ typedef struct {
  * same batch x seq tokens in one launch, each with its per-head norm before
  * the rotation (norm = 1) or without:
  *   y = R_t (x / sqrt(mean x^2 + eps) * gain).
- * Arithmetic in fp32, rounded once.  The angle t f_j is reduced to a turn
- * exactly for any 64-bit position (a fixed-point product modulo one turn),
- * so long contexts lose no accuracy; negative positions turn backwards.
+ * Arithmetic in fp32, rounded once.  The angle t f_j is reduced by a
+ * fixed-point product modulo one turn that rounds nothing for any 64-bit
+ * position; f_j / 2 pi enters it as a double.  The angle is off by at most
+ * |t| (2^-52 |f_j| + 2^-61) radians: with f_j = 1 by 4e-9 at position 2^24 and
+ * 5e-7 at 2^31; from 2^34 on that is more than the pass rounds (2^-18 of a
+ * pair at most).  Negative positions turn backwards.
  * Errors: INVALID_ARG, SHAPE, DTYPE, CUDA.
  */
 int gbo_rope_forward(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *opts, int64_t batch,

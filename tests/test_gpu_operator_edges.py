@@ -1,15 +1,18 @@
 """Corners of the rotary and cross-entropy operators that need a GPU: memory of the loss
-in autograd.
+in autograd, frequencies of either sign at long positions.
 
 Tolerances are those of test_gpu_rotary.py and test_gpu_xent.py, derived there; where
 another one is taken its reason stands beside it."""
+
+import math
+from fractions import Fraction
 
 import pytest
 import torch
 
 from adamw_optimizer_step_gb300 import _binding as B
 from adamw_optimizer_step_gb300 import layers
-from tests.test_gpu_xent import Want, close, inputs
+from tests.test_gpu_xent import U, Want, close, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +69,31 @@ def test_memory_of_the_loss():
     peak, left, loss = peak_of(step)
     assert large <= peak <= large + grads + SLACK
     assert left <= grads + SLACK and loss.grad_fn is not None
+
+
+# ---------------------------------------------------------------------------
+# angles
+
+# more digits than any rational here needs
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_angles_keep_their_bound(sign):
+    """Against rationals with 80 digits of pi: beside the rounding of the pass (64 u of the
+    pair, see test_gpu_rotary.py) the angle is off by at most |t| (2^-52 |f| + 2^-61), the
+    bound that gbo.h states, for frequencies of either sign."""
+    freq = [sign * f for f in (1.0, 0.3, 1e-2, 1e-3, 1e-4, 1e-8, 2.0 ** -40, 17.5)]
+    spec = layers.RotarySpec(16, frequencies=freq)
+    x = torch.randn(1, 6, 1, 16, generator=torch.Generator().manual_seed(4)).cuda()
+    values = [1, 2 ** 24 + 1, 2 ** 31 + 3, 2 ** 40 + 12345, -(2 ** 33) - 7, 2 ** 52 + 1]
+    got = layers.rotary(x, torch.tensor([values], device="cuda"), spec).double().cpu()
+    for s, t in enumerate(values):
+        for j, f in enumerate(freq):
+            turns = Fraction(t) * Fraction(f) / (2 * PI)
+            angle = 2 * math.pi * float(turns - math.floor(turns))
+            c, sn = math.cos(angle), math.sin(angle)
+            a, b = x[0, s, 0, j].item(), x[0, s, 0, j + 8].item()
+            tol = (64 * U + abs(t) * (2.0 ** -52 * abs(f) + 2.0 ** -61)) * (abs(a) + abs(b))
+            assert abs(got[0, s, 0, j].item() - (a * c - b * sn)) <= tol, (t, f)
+            assert abs(got[0, s, 0, j + 8].item() - (a * sn + b * c)) <= tol, (t, f)
