@@ -39,11 +39,11 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
-#include <mutex>
 
 #include "device_common.cuh"
 #include "gbo.h"
 #include "internal.h"
+#include "per_device.h"
 
 namespace gbo {
 
@@ -620,15 +620,13 @@ void back_blocks(const gbo_rope_tensor *t, int32_t n, int sm_count, int32_t *nbl
 }
 
 template <typename T, int CH, int UPL, bool kNorm, bool kBack>
-cudaError_t launch_rope_n(const RopeParams &P, int blocks, cudaStream_t stream) {
+cudaError_t launch_rope_n(const RopeParams &P, int blocks, int dev, cudaStream_t stream) {
   constexpr int smem = ring_bytes(CH * (int)sizeof(T), CH, UPL, kNorm, kBack);
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(rope_kernel<T, CH, UPL, kNorm, kBack>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    smem);
+  static PerDevice<cudaError_t> limit;
+  const cudaError_t *err = limit.of(dev, [](cudaError_t &e) {
+    e = cudaFuncSetAttribute(rope_kernel<T, CH, UPL, kNorm, kBack>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
-  if (attr_err != cudaSuccess) return attr_err;
+  if (!err || *err != cudaSuccess) return err ? *err : cudaErrorInvalidDevice;
   // A block's start (its units, gains and turns) overlaps the end of the kernel
   // before it on the stream, on direct launches too: queries and keys 56.3 ->
   // 54.3 us, their gradients 92.4 -> 90.1, heads of 192 119.9 -> 116.6 in a loop.
@@ -637,24 +635,24 @@ cudaError_t launch_rope_n(const RopeParams &P, int blocks, cudaStream_t stream) 
 }
 
 template <typename T, int CH, int UPL, bool kBack>
-cudaError_t launch_rope(const RopeParams &P, bool norm, int blocks, cudaStream_t stream) {
-  return norm ? launch_rope_n<T, CH, UPL, true, kBack>(P, blocks, stream)
-              : launch_rope_n<T, CH, UPL, false, kBack>(P, blocks, stream);
+cudaError_t launch_rope(const RopeParams &P, bool norm, int blocks, int dev, cudaStream_t stream) {
+  return norm ? launch_rope_n<T, CH, UPL, true, kBack>(P, blocks, dev, stream)
+              : launch_rope_n<T, CH, UPL, false, kBack>(P, blocks, dev, stream);
 }
 
 // units a lane: at most 256 pairs a head, over groups of 32 lanes
 template <typename T, bool kBack>
-cudaError_t dispatch_rope(const RopeParams &P, int chunk, int upl, bool norm, int blocks, cudaStream_t stream) {
+cudaError_t dispatch_rope(const RopeParams &P, int chunk, int upl, bool norm, int blocks, int dev, cudaStream_t stream) {
   if (chunk == 1)
-    return upl <= 2 ? launch_rope<T, 1, 2, kBack>(P, norm, blocks, stream)
-                    : launch_rope<T, 1, 8, kBack>(P, norm, blocks, stream);
+    return upl <= 2 ? launch_rope<T, 1, 2, kBack>(P, norm, blocks, dev, stream)
+                    : launch_rope<T, 1, 8, kBack>(P, norm, blocks, dev, stream);
   if (chunk == 2)
-    return upl == 1 ? launch_rope<T, 2, 1, kBack>(P, norm, blocks, stream)
-                    : launch_rope<T, 2, 4, kBack>(P, norm, blocks, stream);
+    return upl == 1 ? launch_rope<T, 2, 1, kBack>(P, norm, blocks, dev, stream)
+                    : launch_rope<T, 2, 4, kBack>(P, norm, blocks, dev, stream);
   if (chunk == 4)
-    return upl == 1 ? launch_rope<T, 4, 1, kBack>(P, norm, blocks, stream)
-                    : launch_rope<T, 4, 2, kBack>(P, norm, blocks, stream);
-  if constexpr (sizeof(T) == 2) return launch_rope<T, 8, 1, kBack>(P, norm, blocks, stream);
+    return upl == 1 ? launch_rope<T, 4, 1, kBack>(P, norm, blocks, dev, stream)
+                    : launch_rope<T, 4, 2, kBack>(P, norm, blocks, dev, stream);
+  if constexpr (sizeof(T) == 2) return launch_rope<T, 8, 1, kBack>(P, norm, blocks, dev, stream);
   return cudaErrorInvalidValue;  // fp32 chunks have at most four elements
 }
 
@@ -801,11 +799,11 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
   cudaError_t err = cudaSuccess;
   if (blocks > 0) {
     if (dtype == GBO_BF16)
-      err = back ? dispatch_rope<__nv_bfloat16, true>(P, CH, upl, norm, (int)blocks, st)
-                 : dispatch_rope<__nv_bfloat16, false>(P, CH, upl, norm, (int)blocks, st);
+      err = back ? dispatch_rope<__nv_bfloat16, true>(P, CH, upl, norm, (int)blocks, dev, st)
+                 : dispatch_rope<__nv_bfloat16, false>(P, CH, upl, norm, (int)blocks, dev, st);
     else
-      err = back ? dispatch_rope<float, true>(P, CH, upl, norm, (int)blocks, st)
-                 : dispatch_rope<float, false>(P, CH, upl, norm, (int)blocks, st);
+      err = back ? dispatch_rope<float, true>(P, CH, upl, norm, (int)blocks, dev, st)
+                 : dispatch_rope<float, false>(P, CH, upl, norm, (int)blocks, dev, st);
     count_launches(1);
   }
   if (err == cudaSuccess && any_dgain) {

@@ -56,10 +56,10 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
-#include <mutex>
 
 #include "device_common.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "tc_common.cuh"
 
 namespace gbo {
@@ -1493,14 +1493,19 @@ cudaError_t chain(void (*kernel)(K), dim3 grid, dim3 block, cudaStream_t stream,
   return launch_kernel_as(pdl_allowed(), kernel, grid, block, 0, stream, 1, params);
 }
 
+// The kernel's shared memory limit was raised (or not), and the CTA pairs that
+// are resident together.
+struct PairState {
+  cudaError_t err = cudaSuccess;
+  int resident = 0;
+};
+
 template <int kMode>
-cudaError_t launch_xent(const XentParams &P, int64_t items, int sm, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int resident = 0;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(xent_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kXentSmem);
-    if (attr_err != cudaSuccess) return;
+cudaError_t launch_xent(const XentParams &P, int64_t items, int sm, int dev, cudaStream_t stream) {
+  static PerDevice<PairState> states;
+  const PairState *state = states.of(dev, [&](PairState &s) {
+    s.err = cudaFuncSetAttribute(xent_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kXentSmem);
+    if (s.err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1512,10 +1517,11 @@ cudaError_t launch_xent(const XentParams &P, int64_t items, int sm, cudaStream_t
     cfg.blockDim = dim3(kXentThreads);
     cfg.dynamicSmemBytes = kXentSmem;
     cfg.gridDim = dim3(2 * std::max(1, sm / 2));
-    if (cudaOccupancyMaxActiveClusters(&resident, xent_kernel<kMode>, &cfg) != cudaSuccess) resident = 0;
+    if (cudaOccupancyMaxActiveClusters(&s.resident, xent_kernel<kMode>, &cfg) != cudaSuccess) s.resident = 0;
     (void)cudaGetLastError();
   });
-  if (attr_err != cudaSuccess) return attr_err;
+  if (!state || state->err != cudaSuccess) return state ? state->err : cudaErrorInvalidDevice;
+  const int resident = state->resident;
   const int64_t fit = std::max(1, resident > 0 ? std::min(resident, sm / 2) : sm / 2);
   const int clusters = (int)std::max<int64_t>(1, std::min(items, fit));
   const cudaError_t e = launch_kernel_as(pdl_allowed(), xent_kernel<kMode>, dim3(2 * clusters), dim3(kXentThreads),
@@ -1550,18 +1556,18 @@ int score_rows(int64_t n, int64_t v, int64_t d) {
 // Statistics of at most kRows rows; *blocks: CTAs, each with a slot of
 // statistics per epilogue warp.
 template <int kRows>
-int run_score(const gbo_xent_args *a, const XentParams &P, const RowsParams &R, int sm, cudaStream_t st, int *blocks) {
+int run_score(const gbo_xent_args *a, const XentParams &P, const RowsParams &R, int sm, int dev, cudaStream_t st,
+              int *blocks) {
   ScoreParams Q;
   memset(&Q, 0, sizeof Q);
   Q.head = P.head, Q.lab = P.lab, Q.ll2 = P.ll2, Q.part = P.part, Q.part_ld = P.part_ld, Q.status = P.status;
   Q.w = R.w, Q.w_stride = a->w_stride, Q.v = (int32_t)a->v, Q.d = P.d, Q.scale2 = P.scale2;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(xent_score_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    ScoreShape<kRows>::kSmem);
+  static PerDevice<cudaError_t> limit;
+  const cudaError_t *err = limit.of(dev, [](cudaError_t &e) {
+    e = cudaFuncSetAttribute(xent_score_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ScoreShape<kRows>::kSmem);
   });
-  if (attr_err != cudaSuccess) return cuda_err(attr_err);
+  if (!err || *err != cudaSuccess) return cuda_err(err ? *err : cudaErrorInvalidDevice);
   // one CTA an SM, each with at least two 16-row units
   *blocks = (int)std::min<int64_t>(std::min(sm, kMostSms), std::max<int64_t>(1, a->v / (2 * kScoreUnit)));
   // rounds of whole tiles; the last round and what is left are one run a CTA
@@ -1665,10 +1671,10 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
     int64_t slots = (a->v + kSpan - 1) / kSpan;
     if (const int few = S.keep ? 0 : score_rows(a->n, a->v, a->d)) {
       int blocks = 0;
-      rc = few == 16 ? run_score<16>(a, P, R, sm, st, &blocks) : run_score<32>(a, P, R, sm, st, &blocks);
+      rc = few == 16 ? run_score<16>(a, P, R, sm, dev, st, &blocks) : run_score<32>(a, P, R, sm, dev, st, &blocks);
       if (rc != GBO_OK) return rc;
       slots = (int64_t)kScoreWarps * blocks;
-    } else if ((e = launch_xent<kModeStats>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) {
+    } else if ((e = launch_xent<kModeStats>(P, m_tiles * n_tiles, sm, dev, st)) != cudaSuccess) {
       return cuda_err(e);
     }
     LseParams L = {};
@@ -1730,9 +1736,9 @@ int xent_run(const gbo_xent_args *a, bool forward, float *loss, float *lse, floa
                                          CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4)
                             : map_2d(&Q.mapO, P.dw, a->d, a->v, P.dw_stride, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
       if (!maps) return xent_fail(GBO_ERR_CUDA, "tensor map of P");
-      if (a->n > 0 && (e = launch_xent<kModeP>(P, m_tiles * n_tiles, sm, st)) != cudaSuccess) return cuda_err(e);
+      if (a->n > 0 && (e = launch_xent<kModeP>(P, m_tiles * n_tiles, sm, dev, st)) != cudaSuccess) return cuda_err(e);
       const int64_t items = (P.dh ? m_tiles * d_tiles * S.splits : 0) + (P.dw ? n_tiles * d_tiles : 0);
-      if (items > 0 && (e = launch_xent<kModeProducts>(Q, items, sm, st)) != cudaSuccess) return cuda_err(e);
+      if (items > 0 && (e = launch_xent<kModeProducts>(Q, items, sm, dev, st)) != cudaSuccess) return cuda_err(e);
     }
     if (P.dh && S.splits > 1) {
       JoinParams J = {};
