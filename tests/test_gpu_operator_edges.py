@@ -1,5 +1,6 @@
 """Corners of the rotary and cross-entropy operators that need a GPU: memory of the loss
-in autograd, frequencies of either sign at long positions.
+in autograd, frequencies of either sign at long positions, in-place norms,
+tables of three and four tensors.
 
 Tolerances are those of test_gpu_rotary.py and test_gpu_xent.py, derived there; where
 another one is taken its reason stands beside it."""
@@ -97,3 +98,74 @@ def test_angles_keep_their_bound(sign):
             tol = (64 * U + abs(t) * (2.0 ** -52 * abs(f) + 2.0 ** -61)) * (abs(a) + abs(b))
             assert abs(got[0, s, 0, j].item() - (a * c - b * sn)) <= tol, (t, f)
             assert abs(got[0, s, 0, j + 8].item() - (a * sn + b * c)) <= tol, (t, f)
+
+
+# ---------------------------------------------------------------------------
+# rotary: in place with a norm, three and four tensors
+
+def rotary_inputs(counts, dim, dtype, seed, batch=2, seq=67):
+    gen = torch.Generator().manual_seed(seed)
+    made = lambda *shape: torch.randn(*shape, generator=gen)  # noqa: E731
+    return [(made(batch, seq, h, dim).to(dtype).cuda(), made(batch, seq, h, dim).to(dtype).cuda(),
+             (1 + 0.3 * made(dim)).cuda()) for h in counts]
+
+
+def backward(table, spec):
+    ws = torch.empty(max(16, B.gbo_rope_workspace_bytes(table, spec.opts)), dtype=torch.uint8, device="cuda")
+    B.gbo_rope_backward(table, spec.with_eps(1e-6), 11, ws)
+
+
+# chunks of 16, 8 and 4 bytes and of one element
+@pytest.mark.parametrize("dim,rot,offset", [(128, 64, 32), (72, 36, 4), (76, 20, 8), (7, 2, 3)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_in_place_with_a_norm(dim, rot, offset, dtype):
+    """The output in the input's place, the input's gradient in the gradient's: the same bits."""
+    spec = layers.RotarySpec(dim, rot_dim=rot, offset=offset)
+    (x, dy, gain), = rotary_inputs((9,), dim, dtype, dim)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    B.gbo_rope_forward([dict(x=x, y=y, gain=gain, norm=True)], spec.with_eps(1e-6), 11)
+    dgain, again = torch.empty_like(gain), torch.empty_like(gain)
+    backward([dict(x=x, dy=dy, y=dx, gain=gain, dgain=dgain, norm=True)], spec)
+    backward([dict(x=x, dy=dy, y=dy, gain=gain, dgain=again, norm=True)], spec)
+    assert torch.equal(dy, dx) and torch.equal(again, dgain)
+    B.gbo_rope_forward([dict(x=x, y=x, gain=gain, norm=True)], spec.with_eps(1e-6), 11)
+    assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("counts", [(6, 2, 1), (6, 2, 1, 3), (5, 0, 2, 1)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_three_and_four_tensors(counts, norm):
+    """Each tensor of a table as in a call of its own (its heads do not meet the others');
+    the gains' gradients, whose order of summation depends on the table, by their bound."""
+    spec = layers.RotarySpec(64, rot_dim=32, offset=16, layout="interleaved")
+    tensors = rotary_inputs(counts, 64, torch.bfloat16, sum(counts))
+    extra = (lambda gain: dict(gain=gain, norm=True)) if norm else (lambda gain: {})
+    ys, dxs = [torch.empty_like(t[0]) for t in tensors], [torch.empty_like(t[0]) for t in tensors]
+    B.gbo_rope_forward([dict(x=x, y=y, **extra(g)) for (x, _, g), y in zip(tensors, ys)], spec.with_eps(1e-6), 11)
+    dgains = [torch.full((64,), float("nan"), device="cuda") for _ in tensors]
+    table = [dict(x=x, dy=dy, y=dx, **extra(g)) for (x, dy, g), dx in zip(tensors, dxs)]
+    if norm:
+        for e, dg in zip(table, dgains):
+            e["dgain"] = dg
+        backward(table, spec)
+    else:
+        for e in table:
+            del e["x"]
+        B.gbo_rope_backward(table, spec.opts, 11)
+    for (x, dy, gain), y, dx, dg in zip(tensors, ys, dxs, dgains):
+        want, want_dx, one = torch.empty_like(x), torch.empty_like(x), torch.empty_like(gain)
+        B.gbo_rope_forward([dict(x=x, y=want, **extra(gain))], spec.with_eps(1e-6), 11)
+        assert torch.equal(y, want)
+        if norm:
+            backward([dict(x=x, dy=dy, y=want_dx, dgain=one, **extra(gain))], spec)
+            # two sums of the same fp32 terms e_j u_j: either is off by at most (terms + 128) u of
+            # the terms' sizes, which are within the pair's |dy| times |u|
+            u = x.double() * (x.double().square().mean(-1, keepdim=True) + 1e-6).rsqrt()
+            e = dy.double().abs()
+            e[..., 16:48] = (e[..., 16:48:2] + e[..., 17:48:2]).repeat_interleave(2, -1)
+            terms = x.numel() // 64
+            assert torch.all((dg.double() - one.double()).abs()
+                             <= 2 * (terms + 128) * U * (e * u.abs()).sum((0, 1, 2)) + 1e-30)
+        else:
+            B.gbo_rope_backward([dict(dy=dy, y=want_dx)], spec.opts, 11)
+        assert torch.equal(dx, want_dx)
