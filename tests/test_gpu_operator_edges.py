@@ -1,6 +1,6 @@
 """Corners of the rotary and cross-entropy operators that need a GPU: memory of the loss
 in autograd, frequencies of either sign at long positions, in-place norms,
-tables of three and four tensors.
+tables of three and four tensors, sweeps of rows over pieces of the vocabulary.
 
 Tolerances are those of test_gpu_rotary.py and test_gpu_xent.py, derived there; where
 another one is taken its reason stands beside it."""
@@ -169,3 +169,56 @@ def test_three_and_four_tensors(counts, norm):
         else:
             B.gbo_rope_backward([dict(dy=dy, y=want_dx)], spec.opts, 11)
         assert torch.equal(dx, want_dx)
+
+
+# ---------------------------------------------------------------------------
+# cross entropy: sweeps of rows, pieces of the vocabulary, cuts of dH's axis
+
+def schedule(n, v, d, piece_tiles):
+    """(bytes, columns of a piece, pieces, cuts of dH's axis, columns of a cut) of a call whose
+    pieces are `piece_tiles` tiles of 256 columns at most: the arithmetic of the
+    workspace, which the tests below check against its size."""
+    up = lambda x, m: (x + m - 1) // m * m  # noqa: E731
+    rows = up(max(n, 1), 256)
+    size = [up(x, 1024) for x in (16, 4 * rows // 256) + 6 * (4 * rows,) + (2 * rows * up(d, 64),)]
+    part = 8 * rows * max(-(-v // 128), 1024 if n <= 32 else 0)
+    pieces = -(-v // (256 * piece_tiles))
+    piece = up(-(-v // pieces), 256)
+    pieces = -(-v // piece)
+    d_tiles, kit, dw_kit = -(-d // 256), -(-piece // 128), rows // 128
+    share = max(1, (rows // 256 * d_tiles * kit + piece // 256 * d_tiles * (max(dw_kit, 5) + 1)) // 76)
+    cut = -(-kit // min(16, max(1, kit // 8), -(-2 * kit // share)))
+    cuts = -(-kit // cut)
+    size.append(up(4 * cuts * rows * d, 1024) if pieces > 1 or cuts > 1 else 0)
+    size.append(up(max(part, 2 * rows * (piece + 64)), 1024))
+    return sum(size), piece, pieces, cuts, 128 * cut
+
+
+def check_pieces(n, v, d, piece_tiles, seed):
+    nbytes, piece, pieces, cuts, cut = schedule(n, v, d, piece_tiles)
+    assert B.gbo_xent_workspace_bytes(n, v, d, True, nbytes) == nbytes < B.gbo_xent_workspace_bytes(n, v, d, True)
+    H, W, y = inputs(n, v, d, seed, ignored=0.02)
+    for k, edge in enumerate(e for c in range(1, pieces) for e in (c * piece - 1, c * piece)):
+        y[3 * k] = edge  # labels on both sides of every seam
+    y[0], y[-1] = 0, v - 1
+    want = Want(H, W, y, z=1e-3)
+    dh, dw = torch.full_like(H, float("nan")), torch.full_like(W, float("nan"))
+    loss, _, _ = layers.linear_cross_entropy_grad(H, W, y, z_loss=1e-3, dh=dh, dw=dw, workspace_cap=nbytes)
+    close(loss, want.loss, want.loss_tol, torch.float32)
+    close(dh, want.dh, want.dh_tol, torch.bfloat16)
+    close(dw, want.dw, want.dw_tol, torch.bfloat16)
+    return piece, pieces, cuts, cut
+
+
+def test_sweeps_of_rows_over_pieces_of_the_vocabulary():
+    """More rows than one sweep takes (8192), three pieces and more."""
+    _, pieces, _, _ = check_pieces(8500, 1030, 72, 1, 62)
+    assert pieces >= 3
+
+
+def test_a_last_piece_that_ends_before_the_last_cut():
+    """Nine pieces, dH's axis cut in two: the last piece's 412 columns end before the second
+    cut begins, and the sums over the pieces before it stay."""
+    v = 82 * 256 - 100
+    piece, pieces, cuts, cut = check_pieces(100, v, 64, 10, 63)
+    assert pieces == 9 and cuts == 2 and v - (pieces - 1) * piece <= cut
