@@ -69,7 +69,7 @@ struct RopeTensor {
   const float *gain;
   float *part;             // backward: dgain partials, nblk rows of D, or NULL
   int64_t xs[3], ds[3], ys[3];
-  int32_t heads, norm;
+  int32_t heads;
   int32_t per_item;        // heads a group walks over
   int32_t head_blocks;     // ceil(heads / per_item)
   int32_t block0, nblk;    // this tensor's blocks
@@ -769,7 +769,7 @@ int rope_run(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *o, 
       RopeTensor &X = P.t[P.n++];
       X.x = t.x, X.dy = t.dy, X.y = t.y, X.gain = t.gain;
       for (int k = 0; k < 3; ++k) X.xs[k] = t.x_stride[k], X.ds[k] = t.dy_stride[k], X.ys[k] = t.y_stride[k];
-      X.heads = t.heads, X.norm = t.norm;
+      X.heads = t.heads;
       X.head_blocks = (t.heads + per_item - 1) / per_item;
       X.per_item = (t.heads + X.head_blocks - 1) / X.head_blocks;
       X.items = tokens * X.head_blocks;

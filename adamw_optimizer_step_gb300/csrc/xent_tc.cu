@@ -789,9 +789,8 @@ struct ScoreParams {
   const int32_t *lab;
   const float *ll2;
   float2 *part;     // (maximum, sum) per CTA and epilogue warp, and row
-  const __nv_bfloat16 *w;
   int32_t *status;
-  int64_t part_ld, w_stride;
+  int64_t part_ld;
   int32_t v, d;
   int32_t whole, step;  // whole tiles of a CTA, rows of its other tiles
   float scale2;
@@ -1561,7 +1560,7 @@ int run_score(const gbo_xent_args *a, const XentParams &P, const RowsParams &R, 
   ScoreParams Q;
   memset(&Q, 0, sizeof Q);
   Q.head = P.head, Q.lab = P.lab, Q.ll2 = P.ll2, Q.part = P.part, Q.part_ld = P.part_ld, Q.status = P.status;
-  Q.w = R.w, Q.w_stride = a->w_stride, Q.v = (int32_t)a->v, Q.d = P.d, Q.scale2 = P.scale2;
+  Q.v = (int32_t)a->v, Q.d = P.d, Q.scale2 = P.scale2;
   static PerDevice<cudaError_t> limit;
   const cudaError_t *err = limit.of(dev, [](cudaError_t &e) {
     e = cudaFuncSetAttribute(xent_score_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
