@@ -9,10 +9,12 @@
 // dy read, dx written); a head's norm stays in registers and warp shuffles.
 // Measured on 32768 tokens x 20 heads of 128 in bf16: forward 54 us, 6.2 TB/s
 // (91% of a copy); backward 90 us, 5.6 TB/s; 32768 x 32 heads of 192 with 64
-// rotated and no norm: 117 us, 6.9 TB/s.  What carried
-// the forward there from 88 us: the asynchronous ring (heads in flight without
-// registers), two fp32 lanes per instruction, hardware sines for bf16, 32-bit
-// index division.  The backward's 113 registers leave 16 warps an SM; at 80
+// rotated and no norm: 117 us, 6.9 TB/s.  What carried the forward there from
+// 88 us: the asynchronous ring (heads in flight without registers), two fp32
+// lanes per instruction, hardware sines for bf16, 32-bit index division.  The
+// bf16 forward with a norm holds to 64 registers for four blocks an SM, for
+// which it spills 20 bytes: with 79, unspilled, three blocks take 57.1 us
+// instead of 54.5.  The backward's 113 registers leave 16 warps an SM; at 80
 // (24 warps) it spills and measured 127 us.  Carrying the ring on into the
 // next item, sines kept negated in registers and sums without loops were
 // slower or no faster; as many blocks as are resident, which loop, 67 us
@@ -607,9 +609,12 @@ uint64_t turns_of(double f) {
   return f < 0.0 ? 0 - frac : frac;
 }
 
-// Blocks that share a backward call's tokens over its tensors, in
-// proportion to their heads (a function of the table and the device alone,
-// so that dgain's order of summation does not change from call to call).
+// Blocks that share a backward call's tokens over its tensors at most, in
+// proportion to their heads: a function of the table's heads and the device
+// alone, so that it bounds the scratch.  How many of them a launch takes, and
+// with that dgain's order of summation, also goes by the number of tokens and
+// by the chunks that the addresses allow: calls of one shape and alignment
+// give the same bits.
 void back_blocks(const gbo_rope_tensor *t, int32_t n, int sm_count, int32_t *nblk) {
   int64_t heads = 0;
   for (int32_t i = 0; i < n; ++i) heads += t[i].heads;

@@ -5,7 +5,11 @@ entropy with its gradients.
 Each allocates its outputs and scratch with torch's allocator and makes one
 library call, on torch's current stream (under ``torch.cuda.stream(s)`` both the
 memory and the work belong to ``s``; the binding's functions take a stream and
-the caller's buffers).  ``rotary_autograd``, ``qk_norm_rotary_autograd``
+the caller's buffers).  No call waits for the GPU, so what is found there is told
+in ``dev_status`` alone, a CUDA int32 of the caller's that the cross entropy ORs
+its ``GBO_STATUS_*`` bits into: without one, a label outside the vocabulary
+leaves its row out and a wait that ran out (``GBO_STATUS_TIMEOUT``, outputs invalid)
+goes unnoticed.  ``rotary_autograd``, ``qk_norm_rotary_autograd``
 and ``linear_cross_entropy_loss`` are the same operators inside autograd, so
 that ``loss.backward()`` leaves the gradients that
 :class:`~.routing.HybridOptimizer` steps.
@@ -143,7 +147,8 @@ def linear_cross_entropy_grad(h, w, labels, *, z_loss=0.0, logit_scale=1.0, mean
     of their (weighted) mean, or sum with ``mean=False``, by ``h`` and ``w``, in one
     call.  ``dh``, ``dw``: buffers to write (bf16 or float32; with ``accumulate_dw``
     dw is added to).  ``workspace_cap``: bytes of scratch at most (more pieces of the
-    vocabulary)."""
+    vocabulary).  Without a cap the logits are kept in 16 bits, up to 8 GiB; see
+    ``gbo_xent_workspace_bytes``."""
     n, d = h.shape
     loss = torch.empty(n, dtype=torch.float32, device=h.device)
     dh = _like(h) if dh is None else dh
@@ -262,9 +267,9 @@ def linear_cross_entropy_loss(h, w, labels, row_weight=None, z_loss=0.0, logit_s
     (bf16, or a float32 master table, which is cast for the products and gets a
     float32 gradient).  Between the passes the workspace (``workspace_cap``) keeps the
     logits in 16 bits where it has room for them; under ``torch.no_grad()``, or when neither
-    requires a gradient, it is that of :func:`linear_cross_entropy`.  ``dev_status``: a CUDA int32 that
-    takes ``GBO_STATUS_BAD_LABEL`` and ``GBO_STATUS_NONFINITE``.  ``row_weight``,
-    ``z_loss`` and ``logit_scale`` are constants: refused when they require a gradient."""
+    requires a gradient, it is that of :func:`linear_cross_entropy`.  ``dev_status``: a
+    CUDA int32 for the status bits of both passes.  ``row_weight``, ``z_loss`` and
+    ``logit_scale`` are constants: refused when they require a gradient."""
     _constant(row_weight, "row_weight")
     _constant(z_loss, "z_loss")
     _constant(logit_scale, "logit_scale")

@@ -467,7 +467,11 @@ size_t gbo_rope_workspace_bytes(const gbo_rope_tensor *tensors, int32_t n, const
 
 /*
  * Loss of a large-vocabulary classifier (the tied embedding as the output
- * layer) and its gradients, without the n x v logits in memory.
+ * layer) and its gradients.  The n x v logits are never in memory in fp32:
+ * the losses alone leave none; with gradients they are kept between the
+ * passes in 16 bits each, where the workspace has room for them, or formed
+ * again piece by piece of the vocabulary (gbo_xent_workspace_bytes, whose cap
+ * bounds what they take).
  *   l = logit_scale H W^T,  lse_i = log sum_j exp l_ij,
  *   loss_i = lse_i - l_{i, y_i} + z_loss lse_i^2,
  *   L = upstream * (sum_i w_i loss_i) / (mean ? sum_i w_i : 1).
@@ -520,8 +524,9 @@ typedef struct {
  * where it is faster) they are formed again, piece by piece of the vocabulary,
  * each piece as wide as the workspace allows and 2 GiB at most (a third more
  * tensor core work).  cap > 0: the most that fits in `cap`
- * bytes; 0: kept logits up to 8 GiB, else pieces of 2 GiB.  0 when the
- * arguments are out of range or not even a piece of 256 columns fits the cap.
+ * bytes; 0: kept logits up to 8 GiB, else pieces of 2 GiB (at
+ * 128000 x 2048, 32768 rows take 8.2 GiB and 33792 take 2.0).  Returns 0 when the arguments are
+ * out of range or not even a piece of 256 columns fits the cap.
  */
 size_t gbo_xent_workspace_bytes(int64_t n, int64_t v, int64_t d, int32_t grad, int64_t cap);
 
