@@ -120,8 +120,22 @@ class XentGrads(ctypes.Structure):
                 ("dh_dtype", c_int32), ("dw_dtype", c_int32), ("accumulate_dw", c_int32), ("reserved", c_int32)]
 
 
+class AttnArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("q_lengths", c_void_p), ("k_lengths", c_void_p),
+                ("documents", c_void_p), ("batch", c_int64), ("sq", c_int64), ("sk", c_int64),
+                ("q_stride", c_int64 * 3), ("k_stride", c_int64 * 3), ("v_stride", c_int64 * 3), ("window", c_int64),
+                ("q_heads", c_int32), ("k_heads", c_int32), ("dk", c_int32), ("dv", c_int32),
+                ("n_documents", c_int32), ("causal", c_int32), ("dtype", c_int32), ("scale", c_float)]
+
+
+class AttnGrads(ctypes.Structure):
+    _fields_ = [("dy", c_void_p), ("y", c_void_p), ("lse", c_void_p), ("dq", c_void_p), ("dk", c_void_p),
+                ("dv", c_void_p), ("dy_stride", c_int64 * 3), ("y_stride", c_int64 * 3), ("dq_stride", c_int64 * 3),
+                ("dk_stride", c_int64 * 3), ("dv_stride", c_int64 * 3)]
+
+
 _STRUCTS = (MuonDesc, MuonOpts, Tensor, AdamWDesc, AdamWOpts, PlanInfo, RopeScaling, RopeOpts, RopeTensor,
-            RopePositions, XentArgs, XentGrads)
+            RopePositions, XentArgs, XentGrads, AttnArgs, AttnGrads)
 _lib = None
 
 
@@ -170,6 +184,11 @@ def lib():
                                         c_size_t, c_void_p, c_void_p]),
         "gbo_xent_grad": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                     c_void_p, c_size_t, c_void_p, c_void_p]),
+        "gbo_attn_forward_workspace_bytes": (c_size_t, [c_void_p]),
+        "gbo_attn_backward_workspace_bytes": (c_size_t, [c_void_p]),
+        "gbo_attn_forward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
+                                       c_void_p]),
+        "gbo_attn_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
         "gbo_testing_wait_timeout": (c_int32, [c_void_p, ctypes.c_uint32, c_void_p]),
         "gbo_testing_set_small_chain": (c_int32, [c_int32]),
         "gbo_testing_set_fused_gram": (c_int32, [c_int32]),
@@ -689,6 +708,92 @@ def gbo_xent_grad(h, w, labels, workspace, *, loss=None, lse=None, totals=None, 
                                _out_f32(totals, 2, "totals"), g, _dev_ptr(workspace, "workspace"),
                                workspace.numel() * workspace.element_size(), _dev_ptr(dev_status, "dev_status"),
                                _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# attention
+
+_PACK_ATTN_ARGS = struct.Struct("@6P13q7if").pack     # AttnArgs
+_PACK_ATTN_GRADS = struct.Struct("@6P15q").pack       # AttnGrads
+_PACK_STRIDE = struct.Struct("@3q").pack
+
+
+def _attn_heads(t, what, batch, seq, heads, dim):
+    """Strides of a (batch, seq, heads, dim) bfloat16 tensor whose head elements are consecutive."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError("%s must be bfloat16, got %s" % (what, t.dtype))
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != batch or shape[1] != seq or shape[2] != heads or shape[3] != dim:
+        raise ValueError("%s must be (%d, %d, %d, %d), got %s" % (what, batch, seq, heads, dim, tuple(shape)))
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError("the elements of a head of %s must be consecutive" % what)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    return s[:3]
+
+
+def _attn_index(t, count, what):
+    if t is None:
+        return 0
+    if t.dtype is not torch.int32 or t.dim() != 1 or (count is not None and t.shape[0] != count):
+        raise ValueError("%s must be %sint32 values" % (what, "" if count is None else "%d " % count))
+    return _dev_ptr(t, what)
+
+
+def attn_args(q, k, v, *, causal=True, window=0, scale=None, q_lengths=None, k_lengths=None, documents=None):
+    """The packed arguments of the attention calls (``gbo_attn_args``): tensors
+    (batch, seq, heads, dim), lengths int32 (batch), documents int32 (count + 1)."""
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be (batch, seq, heads, dim)")
+    batch, sq, hq, dk = q.shape
+    sk, hk, dv = k.shape[1], k.shape[2], v.shape[3]
+    qs, ks, vs = (_attn_heads(q, "q", batch, sq, hq, dk), _attn_heads(k, "k", batch, sk, hk, dk),
+                  _attn_heads(v, "v", batch, sk, hk, dv))
+    docs = _attn_index(documents, None, "documents")
+    n_docs = documents.shape[0] - 1 if documents is not None else 0
+    return _PACK_ATTN_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), _attn_index(q_lengths, batch, "q_lengths"),
+                           _attn_index(k_lengths, batch, "k_lengths"), docs, batch, sq, sk, *qs, *ks, *vs, int(window),
+                           hq, hk, dk, dv, n_docs, 1 if causal else 0, GBO_BF16,
+                           dk ** -0.5 if scale is None else float(scale))
+
+
+def gbo_attn_forward_workspace_bytes(args):
+    """Workspace of a forward call with these arguments (of :func:`attn_args`)."""
+    return int(lib().gbo_attn_forward_workspace_bytes(args))
+
+
+def gbo_attn_backward_workspace_bytes(args):
+    return int(lib().gbo_attn_backward_workspace_bytes(args))
+
+
+def _workspace(t):
+    return _dev_ptr(t, "workspace"), 0 if t is None else t.numel() * t.element_size()
+
+
+def gbo_attn_forward(args, q, v, y, workspace=None, *, lse=None, dev_status=None, stream=None):
+    """Attention of ``args`` (of :func:`attn_args`, from ``q`` and ``v`` among others)
+    into ``y`` (batch, seq, heads, dv) and ``lse`` (batch, seq, heads float32)."""
+    b, sq, hq, _ = q.shape
+    ys = _PACK_STRIDE(*_attn_heads(y, "y", b, sq, hq, v.shape[3]))
+    ws, nbytes = _workspace(workspace)
+    _check(lib().gbo_attn_forward(args, y.data_ptr(), ys, _out_f32(lse, b * sq * hq, "lse"), ws, nbytes,
+                                  _dev_ptr(dev_status, "dev_status"), _stream(stream)))
+
+
+def gbo_attn_backward(args, q, k, v, dy, y, lse, workspace, *, dq=None, dk=None, dv=None, dev_status=None, stream=None):
+    """Gradients into ``dq``, ``dk`` and ``dv``, whichever are given, from the
+    forward's ``y`` and ``lse``."""
+    b, sq, hq, d = q.shape
+    sk, hk, e = v.shape[1:]
+    sizes = (("dy", dy, sq, hq, e), ("y", y, sq, hq, e), ("dq", dq, sq, hq, d), ("dk", dk, sk, hk, d), ("dv", dv, sk, hk, e))
+    ptrs, strides = [], []
+    for what, t, n, h, w in sizes:
+        ptrs.append(0 if t is None else t.data_ptr())
+        strides += _ZERO3 if t is None else _attn_heads(t, what, b, n, h, w)
+    grads = _PACK_ATTN_GRADS(ptrs[0], ptrs[1], _out_f32(lse, b * sq * hq, "lse"), *ptrs[2:], *strides)
+    ws, nbytes = _workspace(workspace)
+    _check(lib().gbo_attn_backward(args, grads, ws, nbytes, _dev_ptr(dev_status, "dev_status"), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

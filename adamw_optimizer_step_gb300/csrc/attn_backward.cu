@@ -1,0 +1,758 @@
+// Attention, gradients (gbo_attn_backward).  With P = softmax(scale Q K^T) over
+// the keys seen and D_i = dy_i . y_i:
+//   dV = P^T dY,  dS = scale P (dY V^T - D),  dQ = dS K,  dK = dS^T Q.
+// P is formed again from the forward's lse: P = 2^(S c - lse log2(e)).
+//
+//   attn_delta_kernel  per row: -lse log2(e) and D
+//   attn_dkv_kernel    a CTA holds 128 keys and walks over the rows that see them
+//   attn_dq_kernel     a CTA holds 128 rows and walks over the keys that they see
+//
+// Two walks form S and dP twice (7 products instead of 5), and in return no
+// sum crosses CTAs: no atomics, results that repeat bit for bit, no fp32 dQ in
+// memory.  Every sum stays in TMEM for a CTA's whole walk, the query heads that
+// share a key head among them.  P and dS are rounded to bf16 once, as operands of
+// products (2^-9 relative each); sums are fp32.
+#include "attn_common.cuh"
+
+namespace gbo {
+
+namespace {
+
+constexpr int kBwdWarps = 8;  // elementwise: two groups of four, each half of the columns
+constexpr float kLog2ePlain = 1.4426950408889634f;
+
+// ---------------------------------------------------------------------------
+// -lse log2(e) and D of each row: 16 lanes to a row.  A row that sees nothing
+// (lse = -inf) gets -inf and 0, whatever stands in it: its P and dS are 0.
+
+struct DeltaParams {
+  const __nv_bfloat16 *dy, *y;
+  const float *lse;
+  float2 *stats;
+  int64_t ds[3], ys[3], rows;
+  int32_t sq, heads, dv;
+};
+
+__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ DeltaParams P) {
+  pdl_launch();
+  pdl_wait();
+  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 15;
+  const bool in = row < P.rows;
+  float d = 0.f, lse = -INFINITY;
+  if (in) {
+    lse = P.lse[row];
+    const int64_t bt = row / P.heads, b = bt / P.sq;
+    const int64_t h = row - bt * P.heads, t = bt - b * P.sq;
+    if (lane * 8 < P.dv) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(P.dy + b * P.ds[0] + t * P.ds[1] + h * P.ds[2] + lane * 8);
+      const uint4 v = *reinterpret_cast<const uint4 *>(P.y + b * P.ys[0] + t * P.ys[1] + h * P.ys[2] + lane * 8);
+      const uint32_t a[4] = {u.x, u.y, u.z, u.w}, c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        d = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(c[e] << 16), d);
+        d = fmaf(__uint_as_float(a[e] & 0xffff0000u), __uint_as_float(c[e] & 0xffff0000u), d);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if (in && lane == 0) P.stats[row] = lse == -INFINITY ? make_float2(-INFINITY, 0.f) : make_float2(-lse * kLog2ePlain, d);
+}
+
+struct BwdParams {
+  CUtensorMap q, k, v, dy;  // loads
+  CUtensorMap o1, o2;       // stores: dK and dV, or dQ
+  AttnMask mask;
+  AttnShape shape;
+  const float2 *stats;      // (batch, sq, heads)
+  int32_t *status;
+  int32_t tiles;            // of keys, or of tokens
+  int32_t has1, has2;       // which outputs are wanted
+};
+
+// ---------------------------------------------------------------------------
+// dK, dV
+
+// Transposed: keys are the rows (lanes of TMEM), kQt query rows the columns.
+//   S^T = K Q^T, P^T; dP^T = V dY^T, dS^T; dV += P^T dY, dK += dS^T Q
+// P^T and dS^T go back into TMEM in bf16 over S^T and dP^T, as the A operand.
+// Products run in the order
+//   dV(i) S(i+1) dK(i) dP(i+1)
+// so that the tensor cores form S(i+1) while dS(i) is computed, and dP(i+1) while
+// P(i+1) is.
+template <int kKb, int kVb, int kQt>
+struct Dkv {
+  static constexpr int kKTile = kKb * kAttnBlock, kVTile = kVb * kAttnBlock;
+  static constexpr int kQBlock = kQt * 128, kQStage = kKb * kQBlock, kDStage = kVb * kQBlock;
+  static constexpr int kQStages = 3, kDStages = kKb == 2 ? 2 : 3, kStats = 2;
+  static constexpr int kRing = kKTile + kVTile, kStatAt = kRing + kQStages * kQStage + kDStages * kDStage;
+  static constexpr int kUsed = kStatAt + kStats * kQt * 8;
+  // kv, q full/empty, dy full/empty, stats full/empty, S, P, dP, dS, done
+  static constexpr int kBars = 1 + 2 * kQStages + 2 * kDStages + 2 * kStats + 5;
+  static constexpr int kSmem = kUsed + kBars * 8 + 16;
+  static constexpr uint32_t kDp = kQt, kDv = 2 * kQt, kDk = 2 * kQt + kVb * 64;  // TMEM columns
+  static_assert(kDk + kKb * 64 <= 512, "TMEM columns");
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+constexpr int kDkvThreads = (kBwdWarps + 3) * 32;
+
+// Sixteen-lane halves of a row's columns go back as bf16 pairs.
+template <int kCols>
+__device__ __forceinline__ void put_pairs(uint32_t taddr, const uint32_t *p) {
+  if constexpr (kCols == 64) tmem_put(taddr, p);
+  else tmem_put16(taddr, p);
+}
+
+template <int kKb, int kVb, int kQt>
+__global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_constant__ BwdParams P) {
+  using C = Dkv<kKb, kVb, kQt>;
+  pdl_launch();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kUsed);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
+  volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
+  const uint32_t kvfull = smem_u32(bars), qfull0 = kvfull + 8, qempty0 = qfull0 + 8 * C::kQStages;
+  const uint32_t dfull0 = qempty0 + 8 * C::kQStages, dempty0 = dfull0 + 8 * C::kDStages;
+  const uint32_t tfull0 = dempty0 + 8 * C::kDStages, tempty0 = tfull0 + 8 * C::kStats;
+  const uint32_t sfull = tempty0 + 8 * C::kStats, pready = sfull + 8, dpfull = pready + 8, dsready = dpfull + 8;
+  const uint32_t done = dsready + 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 1 + 2 * C::kQStages + 2 * C::kDStages; ++s) mbar_init(kvfull + 8 * s, 1);
+    for (int s = 0; s < C::kStats; ++s) {
+      mbar_init(tfull0 + 8 * s, 32);
+      mbar_init(tempty0 + 8 * s, kBwdWarps);
+    }
+    mbar_init(sfull, 1);
+    mbar_init(pready, kBwdWarps);
+    mbar_init(dpfull, 1);
+    mbar_init(dsready, kBwdWarps);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kBwdWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  const AttnShape &A = P.shape;
+  // early keys first: with a causal mask most queries see them
+  int idx = blockIdx.x;
+  const int kh = idx % A.k_heads;
+  idx /= A.k_heads;
+  const int b = idx % A.batch, k0 = idx / A.batch * kAttnTile;
+  const AttnSeq seq = attn_seq(P.mask, b);
+  const int tokens = kQt >> A.pack;
+  int tt0 = 0, n_tok = 0, full_lo = 0, full_hi = 0;  // token tiles that see these keys
+  {
+    const int a = max(k0, seq.k_lo), e = min(k0 + kAttnTile, seq.k_hi);
+    if (e > a) {
+      const Span first = queries_of(P.mask, seq, a), last = queries_of(P.mask, seq, e - 1);
+      if (last.hi > first.lo) {
+        tt0 = first.lo / tokens, n_tok = (last.hi + tokens - 1) / tokens - tt0;
+        full_lo = last.lo, full_hi = first.hi;
+      }
+    }
+  }
+  const int steps = n_tok * A.head_blocks, group = A.q_heads / A.k_heads;
+  const uint32_t kt = smem_u32(smem), vt = kt + C::kKTile, qring = kt + C::kRing;
+  const uint32_t dring = qring + C::kQStages * C::kQStage;
+  float *const stats = reinterpret_cast<float *>(smem + C::kStatAt);
+  const AttnGuard guard = {abort_flag, P.status};
+
+  if (warp == kBwdWarps + 1) {
+    if (lane == 0 && steps > 0) {
+      uint32_t q_armed = 0, q_par = 0, d_armed = 0, d_par = 0;
+      mbar_expect_tx(kvfull, (uint32_t)(A.kb + A.vb) * kAttnBlock);
+      for (int c = 0; c < A.kb; ++c) tma_load_4d(kt + c * kAttnBlock, &P.k, kvfull, 64 * c, kh, k0, b);
+      for (int c = 0; c < A.vb; ++c) tma_load_4d(vt + c * kAttnBlock, &P.v, kvfull, 64 * c, kh, k0, b);
+      int qs = 0, ds = 0, tt = 0, hb = 0;
+      uint32_t qp = 0, dp = 0;
+      for (int i = 0; i < steps; ++i) {
+        const int h0 = kh * group + (hb << A.pack), t0 = (tt0 + tt) * tokens;
+        if (!guard.wait(qempty0 + 8 * qs, qp ^ 1)) break;
+        mbar_expect_tx(qfull0 + 8 * qs, (uint32_t)(A.kb * C::kQBlock));
+        for (int c = 0; c < A.kb; ++c)
+          tma_load_4d(qring + qs * C::kQStage + c * C::kQBlock, &P.q, qfull0 + 8 * qs, 64 * c, h0, t0, b);
+        q_armed |= 1u << qs, q_par = (q_par & ~(1u << qs)) | (qp << qs);
+        if (++qs == C::kQStages) qs = 0, qp ^= 1;
+        if (!guard.wait(dempty0 + 8 * ds, dp ^ 1)) break;
+        mbar_expect_tx(dfull0 + 8 * ds, (uint32_t)(A.vb * C::kQBlock));
+        for (int c = 0; c < A.vb; ++c)
+          tma_load_4d(dring + ds * C::kDStage + c * C::kQBlock, &P.dy, dfull0 + 8 * ds, 64 * c, h0, t0, b);
+        d_armed |= 1u << ds, d_par = (d_par & ~(1u << ds)) | (dp << ds);
+        if (++ds == C::kDStages) ds = 0, dp ^= 1;
+        if (++tt == n_tok) tt = 0, ++hb;
+      }
+      if (guard.aborted()) {  // copies in flight land before shared memory goes away
+        (void)mbar_wait(kvfull, 0);
+        for (int s = 0; s < C::kQStages; ++s)
+          if (q_armed >> s & 1u) (void)mbar_wait(qfull0 + 8 * s, q_par >> s & 1u);
+        for (int s = 0; s < C::kDStages; ++s)
+          if (d_armed >> s & 1u) (void)mbar_wait(dfull0 + 8 * s, d_par >> s & 1u);
+      }
+    }
+  } else if (warp == kBwdWarps + 2) {
+    // the rows' statistics, a stage ahead of the elementwise warps
+    int s = 0, tt = 0, hb = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < steps; ++i) {
+      const int h0 = kh * group + (hb << A.pack), t0 = (tt0 + tt) * tokens;
+      float2 x[kQt / 32];
+#pragma unroll
+      for (int u = 0; u < kQt / 32; ++u) {
+        const int r = u * 32 + lane, t = t0 + (r >> A.pack);
+        x[u] = make_float2(-INFINITY, 0.f);
+        if (t >= seq.q_lo && t < seq.q_hi)
+          x[u] = P.stats[((int64_t)b * P.mask.sq + t) * A.q_heads + h0 + (r & ((1 << A.pack) - 1))];
+      }
+      if (!guard.wait_warp(tempty0 + 8 * s, ph ^ 1)) break;
+#pragma unroll
+      for (int u = 0; u < kQt / 32; ++u) {
+        stats[s * 2 * kQt + u * 32 + lane] = x[u].x;
+        stats[s * 2 * kQt + kQt + u * 32 + lane] = x[u].y;
+      }
+      mbar_arrive(tfull0 + 8 * s);
+      if (++s == C::kStats) s = 0, ph ^= 1;
+      if (++tt == n_tok) tt = 0, ++hb;
+    }
+  } else if (warp == kBwdWarps) {
+    bool ok = steps > 0 && guard.wait_warp(kvfull, 0);
+    // rows of dead queries may hold anything, and 0 x NaN is not 0
+    auto clean = [&](int i, uint32_t tile, int blocks) {
+      const int t0 = (tt0 + i % n_tok) * tokens;
+      if (t0 < seq.q_lo || (t0 + tokens > seq.q_hi && seq.q_hi < P.mask.sq))
+        zero_rows(tile, blocks, kQt, C::kQBlock, max(0, seq.q_lo - t0) << A.pack, min(tokens, seq.q_hi - t0) << A.pack, lane);
+    };
+    auto s_product = [&](int i) {
+      const int st = i % C::kQStages;
+      if (!guard.wait_warp(qfull0 + 8 * st, (i / C::kQStages) & 1)) return false;
+      const uint32_t q = qring + st * C::kQStage;
+      clean(i, q, A.kb);
+      tc_fence_after();
+      if (lane == 0) {
+        product_ss(tmem, kt, q, A.k_steps, C::kQBlock, kQt);
+        mma_commit_one(sfull);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto dp_product = [&](int i) {
+      const int st = i % C::kDStages;
+      if (!guard.wait_warp(dfull0 + 8 * st, (i / C::kDStages) & 1)) return false;
+      const uint32_t d = dring + st * C::kDStage;
+      clean(i, d, A.vb);
+      tc_fence_after();
+      if (lane == 0) {
+        product_ss(tmem + C::kDp, vt, d, (A.dv + 15) / 16, C::kQBlock, kQt);
+        mma_commit_one(dpfull);
+      }
+      __syncwarp();
+      return true;
+    };
+    if (ok) ok = s_product(0) && dp_product(0);
+    for (int i = 0; i < steps && ok; ++i) {
+      if (!(ok = guard.wait_warp(pready, i & 1))) break;
+      tc_fence_after();
+      if (lane == 0) {
+        product_ts(tmem + C::kDv, tmem, kQt / 2, dring + (i % C::kDStages) * C::kDStage, kQt / 16, C::kQBlock, A.v_cols, i > 0);
+        mma_commit_one(dempty0 + 8 * (i % C::kDStages));
+      }
+      __syncwarp();
+      if (i + 1 < steps && !(ok = s_product(i + 1))) break;
+      if (!(ok = guard.wait_warp(dsready, i & 1))) break;
+      tc_fence_after();
+      if (lane == 0) {
+        product_ts(tmem + C::kDk, tmem + C::kDp, kQt / 2, qring + (i % C::kQStages) * C::kQStage, kQt / 16, C::kQBlock,
+                   A.k_steps * 16, i > 0);
+        mma_commit_one(qempty0 + 8 * (i % C::kQStages));
+        if (i + 1 == steps) mma_commit_one(done);
+      }
+      __syncwarp();
+      if (i + 1 < steps) ok = dp_product(i + 1);
+    }
+  } else {
+    constexpr int kCols = kQt / 2;
+    const int grp = warp >> 2, row = (warp & 3) * 32 + lane, key = k0 + row;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t S = trow + grp * kCols, D = S + C::kDp;
+    const bool live = key >= seq.k_lo && key < seq.k_hi;
+    Span seen = {0, 0};
+    if (live && steps > 0) seen = queries_of(P.mask, seq, key);
+    const float2 c2 = make_float2(A.scale2, A.scale2);
+    bool ok = true;
+    int st = 0, tt = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < steps; ++i) {
+      const int t0 = (tt0 + tt) * tokens;
+      const bool masked = t0 < full_lo || t0 + tokens > full_hi;
+      const int lo = (min(max(seen.lo - t0, 0), tokens) << A.pack) - grp * kCols;
+      const int hi = (min(max(seen.hi - t0, 0), tokens) << A.pack) - grp * kCols;
+      if (!(ok = guard.wait_warp(tfull0 + 8 * st, ph) && guard.wait_warp(sfull, i & 1))) break;
+      tc_fence_after();
+      const float4 *nl = reinterpret_cast<const float4 *>(stats + st * 2 * kQt + grp * kCols);
+      const float4 *dl = reinterpret_cast<const float4 *>(stats + st * 2 * kQt + kQt + grp * kCols);
+      uint32_t r[kCols], w[kCols / 2];
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) tmem_get(S + c, r + c);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) tmem_wait(r + c);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 4) {
+        const float4 l = nl[c / 4];
+        const float2 x = f2_fma(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), c2, make_float2(l.x, l.y));
+        const float2 y = f2_fma(make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), c2, make_float2(l.z, l.w));
+        float p[4] = {ex2(x.x), ex2(x.y), ex2(y.x), ex2(y.y)};
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < lo || c + e >= hi) p[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[c + e] = __float_as_uint(p[e]);
+        w[c / 2] = pack_bf16(p[0], p[1]);
+        w[c / 2 + 1] = pack_bf16(p[2], p[3]);
+      }
+      put_pairs<kCols>(S, w);
+      tmem_put_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pready);
+      if (!(ok = guard.wait_warp(dpfull, i & 1))) break;
+      tc_fence_after();
+      uint32_t g[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) tmem_get(D + c, g + c);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) tmem_wait(g + c);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 4) {
+        const float4 d = dl[c / 4];
+        float2 x = f2_add(make_float2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), make_float2(-d.x, -d.y));
+        float2 y = f2_add(make_float2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3])), make_float2(-d.z, -d.w));
+        x = f2_mul(x, make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])));
+        y = f2_mul(y, make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])));
+        if (masked) {
+          float *e[4] = {&x.x, &x.y, &y.x, &y.y};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c + k < lo || c + k >= hi) *e[k] = 0.f;
+        }
+        w[c / 2] = pack_bf16(x.x, x.y);
+        w[c / 2 + 1] = pack_bf16(y.x, y.y);
+      }
+      put_pairs<kCols>(D, w);
+      tmem_put_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(dsready);
+        mbar_arrive(tempty0 + 8 * st);
+      }
+      if (++st == C::kStats) st = 0, ph ^= 1;
+      if (++tt == n_tok) tt = 0;
+    }
+    if (ok && steps > 0) ok = guard.wait_warp(done, 0);
+    tc_fence_after();
+    if (ok) {
+      // one group writes dV, the other dK, through the places of V and K
+      const bool is_k = grp == 1;
+      const int blocks = is_k ? A.kb : A.vb;
+      const float f = is_k ? A.scale : 1.f;
+      const uint32_t from = trow + (is_k ? C::kDk : C::kDv), out = is_k ? kt : vt;
+      if (is_k ? P.has1 : P.has2) {
+#pragma unroll 1
+        for (int c = 0; c < blocks * 64; c += 32) {
+          uint32_t r[32];
+          float v[32];
+          if (steps > 0) {
+            tmem_get(from + c, r);
+            tmem_wait(r);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = steps > 0 && live ? __uint_as_float(r[e]) * f : 0.f;
+          put_tile_row(out, row, c, v);
+        }
+        fence_async_smem();
+        __syncwarp();
+        const int r0 = (warp & 3) * 32;
+        if (lane == 0 && k0 + r0 < P.mask.sk) {
+          for (int c = 0; c < blocks; ++c)
+            tma_store_4d(is_k ? &P.o1 : &P.o2, out + c * kAttnBlock + r0 * 128, 64 * c, kh, k0 + r0, b);
+          bulk_commit();
+          bulk_wait_all();
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kBwdWarps)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// dQ
+
+// Rows are the lanes: S = Q K^T, dP = dY V^T, dS over S as the A operand,
+// dQ += dS K.  With room for two S (heads of up to 128) the products run
+//   S(j+1) dP(j+1) dQ(j)
+// so dS(j) is computed beside two of them; else dP(j+1) dQ(j) S(j+1).
+template <int kKb, int kVb>
+struct Dq {
+  static constexpr int kQTile = kKb * kAttnBlock, kDTile = kVb * kAttnBlock;
+  static constexpr int kBufs = kKb == 3 ? 1 : 2;
+  static constexpr int kKStages = kKb == 1 ? 4 : kKb == 2 ? 3 : 2, kVStages = kKb == 1 ? 4 : kKb == 2 ? 2 : 1;
+  static constexpr int kKRing = kQTile + kDTile, kVRing = kKRing + kKStages * kQTile;
+  static constexpr int kUsed = kVRing + kVStages * kDTile;
+  // rows, K full/empty, V full/empty, S (two), dP, dP read, dS, done
+  static constexpr int kBars = 1 + 2 * kKStages + 2 * kVStages + 6;
+  static constexpr int kSmem = kUsed + kBars * 8 + 16;
+  static constexpr uint32_t kDp = kBufs * 128, kDq = kDp + 128;  // TMEM columns
+  static_assert(kDq + kKb * 64 <= 512, "TMEM columns");
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+constexpr int kDqThreads = (kBwdWarps + 2) * 32;
+
+template <int kKb, int kVb>
+__global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_constant__ BwdParams P) {
+  using C = Dq<kKb, kVb>;
+  pdl_launch();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kUsed);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
+  volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
+  const uint32_t rfull = smem_u32(bars), kfull0 = rfull + 8, kempty0 = kfull0 + 8 * C::kKStages;
+  const uint32_t vfull0 = kempty0 + 8 * C::kKStages, vempty0 = vfull0 + 8 * C::kVStages;
+  const uint32_t sfull0 = vempty0 + 8 * C::kVStages, dpfull = sfull0 + 16, dpread = dpfull + 8, dsready = dpread + 8;
+  const uint32_t done = dsready + 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 1 + 2 * C::kKStages + 2 * C::kVStages + 3; ++s) mbar_init(rfull + 8 * s, 1);
+    mbar_init(dpread, kBwdWarps);
+    mbar_init(dsready, kBwdWarps);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kBwdWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  const AttnShape &A = P.shape;
+  const int hb_all = A.k_heads * A.head_blocks;
+  int idx = blockIdx.x;
+  const int hb = idx % hb_all;
+  idx /= hb_all;
+  const int b = idx % A.batch, tb = P.tiles - 1 - idx / A.batch;  // later queries first
+  const int kh = hb / A.head_blocks, h0 = kh * (A.q_heads / A.k_heads) + ((hb % A.head_blocks) << A.pack);
+  const int tokens = kAttnTile >> A.pack, t0 = tb * tokens;
+  const AttnSeq seq = attn_seq(P.mask, b);
+  const TileKeys tk = tile_keys(P.mask, seq, t0, tokens);
+  const int steps = max(0, tk.j1 - tk.j0);
+  const uint32_t qt = smem_u32(smem), dt = qt + C::kQTile, kring = qt + C::kKRing, vring = qt + C::kVRing;
+  const AttnGuard guard = {abort_flag, P.status};
+
+  if (warp == kBwdWarps + 1) {
+    if (lane == 0 && steps > 0) {
+      uint32_t k_armed = 0, k_par = 0, v_armed = 0, v_par = 0;
+      mbar_expect_tx(rfull, (uint32_t)(A.kb + A.vb) * kAttnBlock);
+      for (int c = 0; c < A.kb; ++c) tma_load_4d(qt + c * kAttnBlock, &P.q, rfull, 64 * c, h0, t0, b);
+      for (int c = 0; c < A.vb; ++c) tma_load_4d(dt + c * kAttnBlock, &P.dy, rfull, 64 * c, h0, t0, b);
+      int ks = 0, vs = 0;
+      uint32_t kp = 0, vp = 0;
+      for (int i = 0; i < steps; ++i) {
+        const int k0 = (tk.j0 + i) * kAttnTile;
+        if (!guard.wait(kempty0 + 8 * ks, kp ^ 1)) break;
+        mbar_expect_tx(kfull0 + 8 * ks, (uint32_t)A.kb * kAttnBlock);
+        for (int c = 0; c < A.kb; ++c)
+          tma_load_4d(kring + ks * C::kQTile + c * kAttnBlock, &P.k, kfull0 + 8 * ks, 64 * c, kh, k0, b);
+        k_armed |= 1u << ks, k_par = (k_par & ~(1u << ks)) | (kp << ks);
+        if (++ks == C::kKStages) ks = 0, kp ^= 1;
+        if (!guard.wait(vempty0 + 8 * vs, vp ^ 1)) break;
+        mbar_expect_tx(vfull0 + 8 * vs, (uint32_t)A.vb * kAttnBlock);
+        for (int c = 0; c < A.vb; ++c)
+          tma_load_4d(vring + vs * C::kDTile + c * kAttnBlock, &P.v, vfull0 + 8 * vs, 64 * c, kh, k0, b);
+        v_armed |= 1u << vs, v_par = (v_par & ~(1u << vs)) | (vp << vs);
+        if (++vs == C::kVStages) vs = 0, vp ^= 1;
+      }
+      if (guard.aborted()) {  // copies in flight land before shared memory goes away
+        (void)mbar_wait(rfull, 0);
+        for (int s = 0; s < C::kKStages; ++s)
+          if (k_armed >> s & 1u) (void)mbar_wait(kfull0 + 8 * s, k_par >> s & 1u);
+        for (int s = 0; s < C::kVStages; ++s)
+          if (v_armed >> s & 1u) (void)mbar_wait(vfull0 + 8 * s, v_par >> s & 1u);
+      }
+    }
+  } else if (warp == kBwdWarps) {
+    bool ok = steps > 0 && guard.wait_warp(rfull, 0);
+    auto s_product = [&](int i) {
+      const int st = i % C::kKStages, k0 = (tk.j0 + i) * kAttnTile;
+      if (!guard.wait_warp(kfull0 + 8 * st, (i / C::kKStages) & 1)) return false;
+      const uint32_t k = kring + st * C::kQTile;
+      // keys that no row sees may hold anything, and 0 x NaN is not 0
+      if (k0 < seq.k_lo || (k0 + kAttnTile > seq.k_hi && seq.k_hi < P.mask.sk))
+        zero_rows(k, A.kb, kAttnTile, kAttnBlock, seq.k_lo - k0, seq.k_hi - k0, lane);
+      tc_fence_after();
+      if (lane == 0) {
+        product_ss(tmem + (i % C::kBufs) * 128, qt, k, A.k_steps, kAttnBlock, kAttnTile);
+        mma_commit_one(sfull0 + 8 * (i % C::kBufs));
+      }
+      __syncwarp();
+      return true;
+    };
+    auto dp_product = [&](int i) {
+      const int st = i % C::kVStages;
+      if (!guard.wait_warp(vfull0 + 8 * st, (i / C::kVStages) & 1)) return false;
+      if (i > 0 && !guard.wait_warp(dpread, (i - 1) & 1)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        product_ss(tmem + C::kDp, dt, vring + st * C::kDTile, (A.dv + 15) / 16, kAttnBlock, kAttnTile);
+        mma_commit_one(dpfull);
+        mma_commit_one(vempty0 + 8 * st);
+      }
+      __syncwarp();
+      return true;
+    };
+    if (ok) ok = s_product(0) && dp_product(0);
+    for (int i = 0; i < steps && ok; ++i) {
+      if (i + 1 < steps) {
+        if (C::kBufs == 2 && !(ok = s_product(i + 1))) break;
+        if (!(ok = dp_product(i + 1))) break;
+      }
+      if (!(ok = guard.wait_warp(dsready, i & 1))) break;
+      tc_fence_after();
+      if (lane == 0) {
+        product_ts(tmem + C::kDq, tmem + (i % C::kBufs) * 128, 64, kring + (i % C::kKStages) * C::kQTile, kAttnTile / 16,
+                   kAttnBlock, A.k_steps * 16, i > 0);
+        mma_commit_one(kempty0 + 8 * (i % C::kKStages));
+        if (i + 1 == steps) mma_commit_one(done);
+      }
+      __syncwarp();
+      if (C::kBufs == 1 && i + 1 < steps) ok = s_product(i + 1);
+    }
+  } else {
+    const int grp = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int token = t0 + (row >> A.pack), head = h0 + (row & ((1 << A.pack) - 1));
+    const bool live = token >= seq.q_lo && token < seq.q_hi;
+    Span keys = {0, 0};
+    float2 stat = make_float2(-INFINITY, 0.f);
+    if (live) {
+      keys = keys_of(P.mask, seq, token);
+      stat = P.stats[((int64_t)b * P.mask.sq + token) * A.q_heads + head];
+    }
+    const float2 c2 = make_float2(A.scale2, A.scale2), nl = make_float2(stat.x, stat.x), nd = make_float2(-stat.y, -stat.y);
+    bool ok = true;
+    for (int i = 0; i < steps; ++i) {
+      const int buf = i % C::kBufs;
+      const uint32_t S = trow + buf * 128 + grp * 64, D = trow + C::kDp + grp * 64;
+      if (!(ok = guard.wait_warp(sfull0 + 8 * buf, (i / C::kBufs) & 1))) break;
+      tc_fence_after();
+      uint32_t r[64];
+      tmem_get(S, r);
+      tmem_get(S + 32, r + 32);
+      tmem_wait(r);
+      tmem_wait(r + 32);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        const float2 x = f2_fma(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), c2, nl);
+        r[c] = __float_as_uint(ex2(x.x)), r[c + 1] = __float_as_uint(ex2(x.y));
+      }
+      if (!(ok = guard.wait_warp(dpfull, i & 1))) break;
+      tc_fence_after();
+      uint32_t g[64];
+      tmem_get(D, g);
+      tmem_get(D + 32, g + 32);
+      tmem_wait(g);
+      tmem_wait(g + 32);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dpread);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        float2 x = f2_add(make_float2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), nd);
+        x = f2_mul(x, make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])));
+        g[c] = __float_as_uint(x.x), g[c + 1] = __float_as_uint(x.y);
+      }
+      if (tk.masked(tk.j0 + i)) {
+        const int lo = keys.lo - (tk.j0 + i) * kAttnTile - grp * 64, hi = keys.hi - (tk.j0 + i) * kAttnTile - grp * 64;
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c < lo || c >= hi) g[c] = 0u;
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) w[c] = pack_bf16(__uint_as_float(g[2 * c]), __uint_as_float(g[2 * c + 1]));
+      tmem_put(S, w);
+      tmem_put_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dsready);
+    }
+    if (ok && steps > 0) ok = guard.wait_warp(done, 0);
+    tc_fence_after();
+    if (ok) {
+      const int r0 = (warp & 3) * 32;
+      for (int blk = grp; blk < A.kb; blk += 2) {  // through the queries' place
+#pragma unroll 1
+        for (int c = blk * 64; c < blk * 64 + 64; c += 32) {
+          uint32_t r[32];
+          float v[32];
+          if (steps > 0) {
+            tmem_get(trow + C::kDq + c, r);
+            tmem_wait(r);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = steps > 0 && live ? __uint_as_float(r[e]) * A.scale : 0.f;
+          put_tile_row(qt, row, c, v);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && t0 + (r0 >> A.pack) < P.mask.sq) {
+          tma_store_4d(&P.o1, qt + blk * kAttnBlock + r0 * 128, 64 * blk, h0, t0 + (r0 >> A.pack), b);
+          bulk_commit();
+          bulk_wait_all();
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kBwdWarps)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+template <int kKb, int kVb, int kQt>
+cudaError_t launch_dkv(const BwdParams &P, int64_t grid, int dev, cudaStream_t st) {
+  using C = Dkv<kKb, kVb, kQt>;
+  static PerDevice<cudaError_t> limit;
+  const cudaError_t *err = limit.of(dev, [](cudaError_t &e) {
+    e = cudaFuncSetAttribute(attn_dkv_kernel<kKb, kVb, kQt>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (!err || *err != cudaSuccess) return err ? *err : cudaErrorInvalidDevice;
+  count_launches(1);
+  return launch_kernel_as(pdl_allowed(), attn_dkv_kernel<kKb, kVb, kQt>, dim3((unsigned)grid), dim3(kDkvThreads), C::kSmem, st,
+                          1, P);
+}
+
+template <int kKb, int kVb>
+cudaError_t launch_dq(const BwdParams &P, int64_t grid, int dev, cudaStream_t st) {
+  using C = Dq<kKb, kVb>;
+  static PerDevice<cudaError_t> limit;
+  const cudaError_t *err = limit.of(dev, [](cudaError_t &e) {
+    e = cudaFuncSetAttribute(attn_dq_kernel<kKb, kVb>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (!err || *err != cudaSuccess) return err ? *err : cudaErrorInvalidDevice;
+  count_launches(1);
+  return launch_kernel_as(pdl_allowed(), attn_dq_kernel<kKb, kVb>, dim3((unsigned)grid), dim3(kDqThreads), C::kSmem, st, 1, P);
+}
+
+}  // namespace
+}  // namespace gbo
+
+using namespace gbo;
+
+extern "C" size_t gbo_attn_backward_workspace_bytes(const gbo_attn_args *args) {
+  if (check_attn_sizes(args) != GBO_OK) return 0;
+  return (size_t)args->batch * args->sq * args->q_heads * sizeof(float2);
+}
+
+extern "C" int gbo_attn_backward(const gbo_attn_args *a, const gbo_attn_grads *g, void *workspace, size_t ws_bytes,
+                                 int32_t *dev_status, gbo_stream_t stream) {
+  int rc = check_attn(a);
+  if (rc != GBO_OK) return rc;
+  if (!g) return attn_fail(GBO_ERR_INVALID_ARG, "grads is NULL");
+  if ((reinterpret_cast<uintptr_t>(g->lse) | reinterpret_cast<uintptr_t>(dev_status)) & 3)
+    return attn_fail(GBO_ERR_INVALID_ARG, "misaligned lse or status pointer");
+  const bool queries = a->batch > 0 && a->sq > 0, keys = a->batch > 0 && a->sk > 0;
+  if (queries && keys) {
+    if ((rc = check_heads(g->dy, g->dy_stride, a->batch, a->sq, a->q_heads)) != GBO_OK) return rc;
+    if ((rc = check_heads(g->y, g->y_stride, a->batch, a->sq, a->q_heads)) != GBO_OK) return rc;
+    if (!g->lse) return attn_fail(GBO_ERR_INVALID_ARG, "lse is NULL");
+  }
+  if (queries && g->dq && (rc = check_heads(g->dq, g->dq_stride, a->batch, a->sq, a->q_heads)) != GBO_OK) return rc;
+  if (keys && g->dk && (rc = check_heads(g->dk, g->dk_stride, a->batch, a->sk, a->k_heads)) != GBO_OK) return rc;
+  if (keys && g->dv && (rc = check_heads(g->dv, g->dv_stride, a->batch, a->sk, a->k_heads)) != GBO_OK) return rc;
+  int dev, sm = 0;
+  if ((rc = require_device(&dev, &sm)) != GBO_OK) return rc;
+  const int64_t rows = a->batch * a->sq * a->q_heads;
+  if (queries && keys) {
+    if (!workspace || ws_bytes < (size_t)rows * sizeof(float2))
+      return attn_fail(GBO_ERR_WORKSPACE, "workspace missing or smaller than gbo_attn_backward_workspace_bytes");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return attn_fail(GBO_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  }
+  AttnShape S;
+  AttnMask M;
+  fill_shape(a, &S, &M, kAttnMaxPack);
+  const int cfg = attn_config(a);
+  const int qt = cfg == 2 ? 64 : kAttnTile;  // rows of a step of the keys' walk
+  const uint32_t heads = 1u << S.pack;
+  const int64_t q_tiles = (a->sq + (kAttnTile >> S.pack) - 1) / (kAttnTile >> S.pack), k_tiles = (a->sk + kAttnTile - 1) / kAttnTile;
+  const int64_t dkv_grid = keys && (g->dk || g->dv) ? k_tiles * a->batch * a->k_heads : 0;
+  const int64_t dq_grid = queries && g->dq ? q_tiles * a->batch * a->k_heads * S.head_blocks : 0;
+  if (dkv_grid > INT32_MAX || dq_grid > INT32_MAX || rows > (int64_t)INT32_MAX * 16)
+    return attn_fail(GBO_ERR_SHAPE, "more rows than one launch takes");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  BwdParams P;
+  memset(&P, 0, sizeof P);
+  P.mask = M, P.shape = S, P.stats = static_cast<const float2 *>(workspace), P.status = dev_status;
+  BwdParams Q = P;
+  DeltaParams D;
+  memset(&D, 0, sizeof D);
+  bool maps = true;
+  if (queries && keys) {
+    D.dy = static_cast<const __nv_bfloat16 *>(g->dy), D.y = static_cast<const __nv_bfloat16 *>(g->y);
+    D.lse = g->lse, D.stats = static_cast<float2 *>(workspace);
+    const int64_t extent[3] = {a->batch, a->sq, a->q_heads};
+    for (int i = 0; i < 3; ++i) D.ds[i] = extent[i] > 1 ? g->dy_stride[i] : 0, D.ys[i] = extent[i] > 1 ? g->y_stride[i] : 0;
+    D.rows = rows, D.sq = (int32_t)a->sq, D.heads = a->q_heads, D.dv = a->dv;
+    maps = heads_map(&P.k, a->k, a->dk, a->k_heads, a->sk, a->batch, a->k_stride, 1, kAttnTile) &&
+           heads_map(&P.v, a->v, a->dv, a->k_heads, a->sk, a->batch, a->v_stride, 1, kAttnTile) &&
+           heads_map(&P.q, a->q, a->dk, a->q_heads, a->sq, a->batch, a->q_stride, heads, qt >> S.pack) &&
+           heads_map(&P.dy, g->dy, a->dv, a->q_heads, a->sq, a->batch, g->dy_stride, heads, qt >> S.pack);
+    Q.k = P.k, Q.v = P.v, Q.q = P.q, Q.dy = P.dy;
+    if (qt != kAttnTile)
+      maps = maps && heads_map(&Q.q, a->q, a->dk, a->q_heads, a->sq, a->batch, a->q_stride, heads, kAttnTile >> S.pack) &&
+             heads_map(&Q.dy, g->dy, a->dv, a->q_heads, a->sq, a->batch, g->dy_stride, heads, kAttnTile >> S.pack);
+  }
+  if (dkv_grid && g->dk) maps = maps && heads_map(&P.o1, g->dk, a->dk, a->k_heads, a->sk, a->batch, g->dk_stride, 1, 32);
+  if (dkv_grid && g->dv) maps = maps && heads_map(&P.o2, g->dv, a->dv, a->k_heads, a->sk, a->batch, g->dv_stride, 1, 32);
+  if (dq_grid) maps = maps && heads_map(&Q.o1, g->dq, a->dk, a->q_heads, a->sq, a->batch, g->dq_stride, heads, 32 >> S.pack);
+  if (!maps) return attn_fail(GBO_ERR_CUDA, "tensor map of queries, keys, values or gradients");
+  P.has1 = g->dk != nullptr, P.has2 = g->dv != nullptr;
+  Q.tiles = (int32_t)q_tiles;
+  if (queries && keys && (dkv_grid || dq_grid)) {
+    count_launches(1);
+    e = launch_kernel_as(pdl_allowed(), attn_delta_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, st, 1, D);
+  }
+  if (e == cudaSuccess && dkv_grid)
+    e = cfg == 0 ? launch_dkv<1, 1, 128>(P, dkv_grid, dev, st)
+                 : cfg == 1 ? launch_dkv<2, 2, 128>(P, dkv_grid, dev, st) : launch_dkv<3, 2, 64>(P, dkv_grid, dev, st);
+  if (e == cudaSuccess && dq_grid)
+    e = cfg == 0 ? launch_dq<1, 1>(Q, dq_grid, dev, st) : cfg == 1 ? launch_dq<2, 2>(Q, dq_grid, dev, st) : launch_dq<3, 2>(Q, dq_grid, dev, st);
+  return e == cudaSuccess ? report_ok() : attn_cuda(e);
+}

@@ -1,0 +1,441 @@
+// Pieces shared by the attention kernels: which keys a query sees, the mapping
+// of a tile's rows to tokens and heads, TMEM and tcgen05 wrappers, bounded
+// waits, tensor maps, and the checks of the arguments.
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "gbo.h"
+#include "internal.h"
+#include "per_device.h"
+#include "tc_common.cuh"
+
+namespace gbo {
+
+constexpr int64_t kAttnMaxLength = int64_t(1) << 30;
+constexpr int kAttnMaxPack = 5;          // heads of a block: 32 at most, so that a warp's rows are whole tokens
+constexpr int kAttnTile = 128;           // rows and keys of a tile
+constexpr int kAttnBlock = 128 * 128;    // bytes of 128 rows of 64 bf16 (one 128-byte line each)
+
+// Which keys the queries of a sequence see.  Query t sees the keys of one
+// interval, whose ends do not decrease with t; so does a key of its queries.
+struct AttnMask {
+  const int32_t *q_len, *k_len;  // per sequence, or NULL: sq, sk
+  const int32_t *docs;           // first tokens of n_docs documents and the end of the last, or NULL
+  int32_t n_docs, causal, window, sq, sk;
+};
+
+struct AttnSeq {
+  int32_t q_lo, q_hi;  // queries that may see a key at all
+  int32_t k_lo, k_hi;  // keys that may be seen at all: what stands in others reaches nothing
+  int32_t shift;       // query t stands at position t + shift among the keys
+};
+
+struct Span {
+  int32_t lo, hi;
+  __device__ __forceinline__ bool empty() const { return hi <= lo; }
+};
+
+// (arguments of an entry point may hold anything a caller put on the device)
+__device__ __forceinline__ int32_t clamp_to(int32_t v, int32_t most) { return min(max(v, 0), most); }
+
+__device__ __forceinline__ AttnSeq attn_seq(const AttnMask &M, int b) {
+  AttnSeq s;
+  const int32_t lq = M.q_len ? clamp_to(M.q_len[b], M.sq) : M.sq, lk = M.k_len ? clamp_to(M.k_len[b], M.sk) : M.sk;
+  s.shift = lk - lq;
+  s.q_lo = 0, s.q_hi = lk > 0 ? lq : 0;
+  s.k_lo = 0, s.k_hi = lq > 0 ? lk : 0;
+  if (M.causal) s.q_lo = min(max(0, -s.shift), s.q_hi);
+  if (M.docs) {
+    s.q_lo = s.k_lo = clamp_to(M.docs[0], M.sk);
+    s.q_hi = s.k_hi = max(s.k_lo, clamp_to(M.docs[M.n_docs], M.sk));
+  }
+  return s;
+}
+
+// The document of token t: the last one that starts at or before it.
+__device__ __forceinline__ Span attn_doc(const AttnMask &M, int t) {
+  int lo = 0, hi = M.n_docs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (M.docs[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return {clamp_to(M.docs[lo], M.sk), clamp_to(M.docs[lo + 1], M.sk)};
+}
+
+// Keys that query t (q_lo <= t < q_hi) sees.
+__device__ __forceinline__ Span keys_of(const AttnMask &M, const AttnSeq &s, int t) {
+  Span r = {s.k_lo, s.k_hi};
+  const int at = t + s.shift;
+  if (M.causal) r.hi = min(r.hi, at + 1);
+  if (M.window) r.lo = max(r.lo, at - M.window + 1);
+  if (M.docs) {
+    const Span d = attn_doc(M, t);
+    r.lo = max(r.lo, d.lo), r.hi = min(r.hi, d.hi);
+  }
+  return r;
+}
+
+// Queries that see key j (k_lo <= j < k_hi).
+__device__ __forceinline__ Span queries_of(const AttnMask &M, const AttnSeq &s, int j) {
+  Span r = {s.q_lo, s.q_hi};
+  const int at = j - s.shift;
+  if (M.causal) r.lo = max(r.lo, at);
+  if (M.window) r.hi = min(r.hi, at + M.window);
+  if (M.docs) {
+    const Span d = attn_doc(M, j);
+    r.lo = max(r.lo, d.lo), r.hi = min(r.hi, d.hi);
+  }
+  return r;
+}
+
+// Heads and tiles.  The `group` query heads of one key head are cut into
+// blocks of 2^pack heads, and a tile's rows are those heads of consecutive
+// tokens: row r is token t0 + (r >> pack), head h0 + (r & mask).  Heads of a
+// block share the tile's keys and its causal border, so the shared keys are
+// loaded once and the tiles along the border stay small.
+struct AttnShape {
+  int32_t batch, q_heads, k_heads, head_blocks, pack;  // head_blocks: per key head
+  int32_t dk, dv, kb, vb;                              // elements of a head; blocks of 64 of them
+  int32_t k_steps, v_cols;                             // dk in steps of 16, dv rounded up to 16
+  float scale, scale2;                                 // scale, and scale log2(e)
+};
+
+// What a row tile sees: tiles [j0, j1) of 128 keys, of which those within
+// [full_lo, full_hi) need no mask.
+struct TileKeys {
+  int32_t j0, j1, full_lo, full_hi;
+  __device__ __forceinline__ bool has(int j) const { return j >= j0 && j < j1; }
+  __device__ __forceinline__ bool masked(int j) const { return j * kAttnTile < full_lo || (j + 1) * kAttnTile > full_hi; }
+};
+
+__device__ __forceinline__ TileKeys tile_keys(const AttnMask &M, const AttnSeq &s, int t0, int tokens) {
+  TileKeys k = {0, 0, 0, 0};
+  const int a = max(t0, s.q_lo), b = min(t0 + tokens, s.q_hi);
+  if (a >= b) return k;
+  const Span first = keys_of(M, s, a), last = b - 1 == a ? first : keys_of(M, s, b - 1);
+  if (last.hi <= first.lo) return k;
+  k.j0 = first.lo / kAttnTile, k.j1 = (last.hi + kAttnTile - 1) / kAttnTile;
+  // (rows that see nothing are written as zeros whatever they sum up)
+  k.full_lo = last.lo, k.full_hi = first.hi;
+  return k;
+}
+
+// ---------------------------------------------------------------------------
+// PTX wrappers
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint64_t as_bits(float2 a) { return *reinterpret_cast<uint64_t *>(&a); }
+__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)), "l"(as_bits(c)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, uint32_t src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// 32 columns of this warp's 32 lanes of TMEM; the values may be used after
+// tmem_wait of the same registers, which orders every use behind the wait.
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// kind::f16: bf16 operands, fp32 sums, M = 128, N = n; A K-major.
+__host__ __device__ constexpr uint32_t attn_idesc(bool b_mn_major, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A from TMEM: 128 lanes, a 32-bit column holds two consecutive K.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D = A B^T over `steps` steps of 16, A (128 rows) and B (rows of n) both
+// K-major in blocks of 64 columns; a_block, b_block: bytes of a block.
+__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t b_block, int n) {
+  const uint32_t idesc = attn_idesc(false, n);
+  const uint64_t ad = smem_desc(a, 16, 1024), bd = smem_desc(b, 16, 1024);
+  for (int k = 0; k < steps; ++k) {
+    const uint32_t in = (uint32_t)((k & 3) * 32);
+    mma_ss(d, ad + (((uint32_t)(k >> 2) * kAttnBlock + in) >> 4), bd + (((uint32_t)(k >> 2) * b_block + in) >> 4), idesc,
+           k != 0);
+  }
+}
+
+// D (+)= A B over K = 16 `steps`, A in TMEM from column a on, B with K along its
+// rows (MN-major) in blocks of 64 columns of b_block bytes, n columns in all.
+// The second half of A's steps stands a_second columns after the first.
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t a_second, uint32_t b, int steps, uint32_t b_block,
+                                           int n, bool accumulate) {
+  const uint32_t idesc = attn_idesc(true, n);
+  const uint64_t bd = smem_desc(b, b_block, 1024);
+  const int half = steps >> 1;
+#pragma unroll 8
+  for (int k = 0; k < steps; ++k)
+    mma_ts(d, a + (k < half ? 0 : a_second) + (uint32_t)((k < half ? k : k - half) * 8), bd + ((uint32_t)(k * 2048) >> 4),
+           idesc, accumulate || k != 0);
+}
+
+// ---------------------------------------------------------------------------
+// waits
+
+// Bounded waits of one CTA: the first to run out of time raises the flag and
+// the status, and every other wait of the CTA gives up when it sees the flag.
+struct AttnGuard {
+  volatile int32_t *abort_flag;
+  int32_t *status;
+
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t spin = 1;; ++spin) {
+      if (mbar_try(bar, parity)) return true;
+      if ((spin & 63u) == 0) {
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > kWaitNs) {
+          *abort_flag = 1;
+          flag_status(status, GBO_STATUS_TIMEOUT);
+          return false;
+        }
+      }
+    }
+  }
+  // The same by all lanes of a warp, which come back together with one answer.
+  __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) const {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t spin = 1;; ++spin) {
+      if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+      if ((spin & 63u) == 0) {
+        const bool late = global_ns() - t0 > kWaitNs;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+          if (!*abort_flag) {
+            *abort_flag = 1;
+            flag_status(status, GBO_STATUS_TIMEOUT);
+          }
+          return false;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ bool aborted() const { return *abort_flag != 0; }
+};
+
+// Zero the rows outside [lo, hi) of a tile of `rows` rows in `blocks` blocks of 64
+// columns, by the lanes of one warp, for tensor cores that read it next.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int blocks, int rows, uint32_t block_bytes, int lo, int hi, int lane) {
+  for (int b = 0; b < blocks; ++b)
+    for (int c = lane; c < rows * 8; c += 32) {
+      const int r = c >> 3;
+      if (r < lo || r >= hi)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (uint32_t)b * block_bytes + (uint32_t)c * 16u),
+                     "r"(0)
+                     : "memory");
+    }
+  fence_async_smem();
+  __syncwarp();
+}
+
+// 32 values of row r as bf16 into columns c0 .. c0 + 31 of a tile of 128 rows in
+// blocks of 64 columns with the 128-byte swizzle of the tensor maps.
+__device__ __forceinline__ void put_tile_row(uint32_t tile, int r, int c0, const float *v) {
+  const uint32_t line = tile + (uint32_t)(c0 >> 6) * kAttnBlock + (uint32_t)r * 128u;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t chunk = (uint32_t)(((c0 & 63) >> 3) + q);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((chunk ^ (uint32_t)(r & 7)) << 4)),
+                 "r"(pack_bf16(v[8 * q], v[8 * q + 1])), "r"(pack_bf16(v[8 * q + 2], v[8 * q + 3])),
+                 "r"(pack_bf16(v[8 * q + 4], v[8 * q + 5])), "r"(pack_bf16(v[8 * q + 6], v[8 * q + 7]))
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+namespace {
+
+int attn_fail(int code, const char *msg) { return report_error(code, msg); }
+
+int attn_cuda(cudaError_t e) {
+  char msg[200];
+  snprintf(msg, sizeof msg, "attention kernels: %s", cudaGetErrorString(e));
+  return report_error(GBO_ERR_CUDA, msg);
+}
+
+// A map over (dim, heads, tokens, batch) of bf16 heads, box 64 x heads x tokens.
+bool heads_map(CUtensorMap *map, const void *base, int64_t dim, int64_t heads, int64_t tokens, int64_t batch,
+               const int64_t stride[3], uint32_t box_heads, uint32_t box_tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)batch};
+  // (an axis of length one may have any stride; a map wants multiples of 16 bytes)
+  auto bytes = [](int64_t n, int64_t s) { return (cuuint64_t)(n > 1 ? s * 2 : 16); };
+  const cuuint64_t strides[3] = {bytes(heads, stride[2]), bytes(tokens, stride[1]), bytes(batch, stride[0])};
+  const cuuint32_t box[4] = {64, box_heads, box_tokens, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int check_heads(const void *p, const int64_t stride[3], int64_t batch, int64_t tokens, int64_t heads) {
+  if (!p) return attn_fail(GBO_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (reinterpret_cast<uintptr_t>(p) & 15) return attn_fail(GBO_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  const int64_t n[3] = {batch, tokens, heads};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (stride[i] <= 0 || stride[i] % 8 || stride[i] >= (int64_t(1) << 39)))
+      return attn_fail(GBO_ERR_INVALID_ARG, "strides must be positive multiples of 8 elements, below 2^39");
+  return GBO_OK;
+}
+
+// (no pointer is looked at: sizes are asked for before memory is there)
+int check_attn_sizes(const gbo_attn_args *a) {
+  if (!a) return attn_fail(GBO_ERR_INVALID_ARG, "args is NULL");
+  if (a->dtype != GBO_BF16) return attn_fail(GBO_ERR_DTYPE, "queries, keys and values must be GBO_BF16");
+  if (a->batch < 0 || a->sq < 0 || a->sk < 0 || a->sq > kAttnMaxLength || a->sk > kAttnMaxLength || a->batch > kAttnMaxLength)
+    return attn_fail(GBO_ERR_SHAPE, "batch, sq and sk must be in 0..2^30");
+  if (a->k_heads < 1 || a->q_heads < a->k_heads || a->q_heads % a->k_heads)
+    return attn_fail(GBO_ERR_SHAPE, "q_heads must be a positive multiple of k_heads");
+  if (a->q_heads > 65536) return attn_fail(GBO_ERR_SHAPE, "at most 65536 heads");
+  if (a->dk < 8 || a->dk % 8 || a->dk > GBO_ATTN_MAX_DK || a->dv < 8 || a->dv % 8 || a->dv > GBO_ATTN_MAX_DV)
+    return attn_fail(GBO_ERR_SHAPE, "dk must be a multiple of 8 in 8..192, dv one in 8..128");
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return attn_fail(GBO_ERR_INVALID_ARG, "scale must be > 0 and finite");
+  if (a->causal != 0 && a->causal != 1) return attn_fail(GBO_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (a->window < 0 || (a->window > 0 && !a->causal))
+    return attn_fail(GBO_ERR_INVALID_ARG, "window must be >= 0, and needs causal = 1");
+  return GBO_OK;
+}
+
+int check_attn(const gbo_attn_args *a) {
+  int rc = check_attn_sizes(a);
+  if (rc != GBO_OK) return rc;
+  if ((reinterpret_cast<uintptr_t>(a->q_lengths) | reinterpret_cast<uintptr_t>(a->k_lengths) |
+       reinterpret_cast<uintptr_t>(a->documents)) & 3)
+    return attn_fail(GBO_ERR_INVALID_ARG, "misaligned lengths or documents");
+  if (a->documents) {
+    if (a->n_documents < 1) return attn_fail(GBO_ERR_INVALID_ARG, "documents without a number of documents");
+    if (a->batch > 1 || a->sq != a->sk || a->q_lengths || a->k_lengths)
+      return attn_fail(GBO_ERR_INVALID_ARG, "documents need one row of as many queries as keys, without lengths");
+  } else if (a->n_documents != 0) {
+    return attn_fail(GBO_ERR_INVALID_ARG, "n_documents without documents");
+  }
+  if (a->batch == 0 || a->sq == 0) return GBO_OK;
+  rc = check_heads(a->q, a->q_stride, a->batch, a->sq, a->q_heads);
+  if (rc == GBO_OK && a->sk > 0) rc = check_heads(a->k, a->k_stride, a->batch, a->sk, a->k_heads);
+  if (rc == GBO_OK && a->sk > 0) rc = check_heads(a->v, a->v_stride, a->batch, a->sk, a->k_heads);
+  return rc;
+}
+
+void fill_shape(const gbo_attn_args *a, AttnShape *S, AttnMask *M, int most_pack) {
+  const int group = a->q_heads / a->k_heads;
+  S->batch = (int32_t)a->batch, S->q_heads = a->q_heads, S->k_heads = a->k_heads;
+  S->pack = 0;
+  while (S->pack < most_pack && group % (2 << S->pack) == 0) ++S->pack;
+  S->head_blocks = group >> S->pack;
+  S->dk = a->dk, S->dv = a->dv;
+  S->kb = (a->dk + 63) / 64, S->vb = (a->dv + 63) / 64;
+  S->k_steps = (a->dk + 15) / 16, S->v_cols = (a->dv + 15) / 16 * 16;
+  S->scale = a->scale, S->scale2 = a->scale * 1.4426950408889634f;
+  M->q_len = a->q_lengths, M->k_len = a->k_lengths, M->docs = a->documents;
+  M->n_docs = a->n_documents, M->causal = a->causal;
+  M->sq = (int32_t)a->sq, M->sk = (int32_t)a->sk;
+  // a window that spans every key hides none
+  M->window = a->window >= a->sk ? 0 : (int32_t)a->window;
+}
+
+// Which instance of a kernel template a head size takes: blocks of 64 elements.
+inline int attn_config(const gbo_attn_args *a) { return a->dk <= 64 && a->dv <= 64 ? 0 : a->dk <= 128 ? 1 : 2; }
+
+}  // namespace
+
+}  // namespace gbo

@@ -794,6 +794,8 @@ size_t gbo_struct_size(int32_t which) {
     case 9: return sizeof(gbo_rope_positions);
     case 10: return sizeof(gbo_xent_args);
     case 11: return sizeof(gbo_xent_grads);
+    case 12: return sizeof(gbo_attn_args);
+    case 13: return sizeof(gbo_attn_grads);
     default: return 0;
   }
 }

@@ -162,6 +162,51 @@ def linear_cross_entropy_grad(h, w, labels, *, z_loss=0.0, logit_scale=1.0, mean
 
 
 # ---------------------------------------------------------------------------
+# attention
+
+def _scratch(need, device):
+    """A workspace of ``need`` bytes, or None where none is needed."""
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def attention(q, k, v, *, causal=True, window=0, scale=None, q_lengths=None, k_lengths=None, documents=None, out=None,
+              return_lse=False, dev_status=None):
+    """Softmax attention of ``q`` (batch, sq, q_heads, dk) over ``k`` and ``v`` (batch,
+    sk, k_heads, dk and dv), all bfloat16: a training batch, a prompt, or single
+    tokens (sq = 1) over a cache.  ``q_heads`` is a multiple of ``k_heads``.
+
+    ``causal``: the last query of a sequence sees all its keys, each one before it
+    a key less; ``window`` > 0: only the last ``window`` of these.  ``q_lengths``,
+    ``k_lengths``: int32 CUDA tensors (batch), what each sequence of a padded batch,
+    or its cache, holds.  ``documents``: int32 CUDA tensor, the first tokens of
+    sequences packed into one row and the end of the last.  ``scale``: of the
+    scores, 1 / sqrt(dk) by default.  Queries that see nothing get 0.
+
+    With ``return_lse`` also the log of each row's sum (batch, sq, q_heads), which
+    :func:`attention_backward` takes."""
+    args = B.attn_args(q, k, v, causal=causal, window=window, scale=scale, q_lengths=q_lengths, k_lengths=k_lengths,
+                       documents=documents)
+    b, sq, hq, _ = q.shape
+    y = torch.empty(b, sq, hq, v.shape[3], dtype=q.dtype, device=q.device) if out is None else out
+    lse = torch.empty(b, sq, hq, dtype=torch.float32, device=q.device) if return_lse else None
+    ws = _scratch(B.gbo_attn_forward_workspace_bytes(args), q.device)
+    B.gbo_attn_forward(args, q, v, y, ws, lse=lse, dev_status=dev_status)
+    return (y, lse) if return_lse else y
+
+
+def attention_backward(dy, q, k, v, y, lse, *, causal=True, window=0, scale=None, q_lengths=None, k_lengths=None,
+                       documents=None, wanted=(True, True, True), dev_status=None):
+    """Gradients of :func:`attention` by q, k and v (None where not ``wanted``) from its
+    output ``y``, its ``lse`` and the gradient ``dy``; the same masks as there."""
+    args = B.attn_args(q, k, v, causal=causal, window=window, scale=scale, q_lengths=q_lengths, k_lengths=k_lengths,
+                       documents=documents)
+    grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device) if w else None for t, w in zip((q, k, v), wanted)]
+    ws = _scratch(B.gbo_attn_backward_workspace_bytes(args), q.device)
+    B.gbo_attn_backward(args, q, k, v, dy, y, lse, ws, dq=grads[0], dk=grads[1], dv=grads[2], dev_status=dev_status)
+    return tuple(grads)
+
+
+# ---------------------------------------------------------------------------
 # autograd
 
 def _rows(t):

@@ -463,6 +463,90 @@ int gbo_rope_backward(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_
                       gbo_stream_t stream);
 size_t gbo_rope_workspace_bytes(const gbo_rope_tensor *tensors, int32_t n, const gbo_rope_opts *opts);
 
+/* ---- attention -------------------------------------------------------------- */
+
+/*
+ * Between the rotation of queries and keys and the output projection, in
+ * training (with gradients), over a prompt, and for single tokens over a cache.
+ * Query head h reads key head h / (q_heads / k_heads).  With lq queries and lk
+ * keys in a sequence, query i < lq sees the keys j < lk with
+ *   j <= i + lk - lq             causal = 1 (the last query sees every key),
+ *   j >  i + lk - lq - window    window > 0 (with causal = 1),
+ *   start <= j < end             documents: those of the document that i lies in,
+ * and over the keys seen
+ *   y_i = sum_j p_ij v_j,  p_ij = exp(scale q_i k_j - lse_i),
+ *   lse_i = log sum_j exp(scale q_i k_j).
+ * Queries that see nothing (past their sequence's length or behind the last
+ * document, or before the first key) get y = 0, lse = -inf and gradients 0;
+ * every row of an output is written.  What stands in queries past lq, keys and
+ * values past lk, or outside the documents (NaN, infinities, memory never
+ * written) reaches nothing.  Elsewhere a value that is not finite may reach
+ * rows whose mask hides it.
+ * Tensors are bf16 heads as in gbo_rope_tensor, 16-byte aligned, their strides
+ * positive multiples of 8 elements; products accumulate in fp32, exponentials
+ * and sums are fp32, p is rounded to bf16 as an operand of a product.
+ */
+#define GBO_ATTN_MAX_DK 192
+#define GBO_ATTN_MAX_DV 128
+
+typedef struct {
+  const void *q;  /* device: batch x sq x q_heads x dk                                       */
+  const void *k;  /* device: batch x sk x k_heads x dk                                       */
+  const void *v;  /* device: batch x sk x k_heads x dv                                       */
+  const int32_t *q_lengths; /* device, batch: lq of each sequence (clamped to 0..sq); NULL: sq   */
+  const int32_t *k_lengths; /* device, batch: lk of each sequence (clamped to 0..sk); NULL: sk   */
+  const int32_t *documents; /* device, n_documents + 1, not decreasing: first tokens of the documents
+                               packed into the row and the end of the last, or NULL.  Needs
+                               batch <= 1, sq = sk and no lengths                              */
+  int64_t batch, sq, sk;    /* 0 .. 2^30                                                       */
+  int64_t q_stride[3], k_stride[3], v_stride[3]; /* elements: batch, position, head            */
+  int64_t window;           /* 0: none                                                         */
+  int32_t q_heads, k_heads; /* q_heads a multiple of k_heads                                   */
+  int32_t dk;               /* a multiple of 8, 8 .. GBO_ATTN_MAX_DK                           */
+  int32_t dv;               /* a multiple of 8, 8 .. GBO_ATTN_MAX_DV                           */
+  int32_t n_documents;      /* with documents, >= 1; else 0                                    */
+  int32_t causal;           /* 0 | 1                                                           */
+  int32_t dtype;            /* GBO_BF16                                                        */
+  float scale;              /* > 0, e.g. 1 / sqrt(dk)                                          */
+} gbo_attn_args;
+
+/* Bytes of device workspace of the calls below on the current device (0 where
+ * none is needed, or with arguments that are refused); no pointer is read.
+ * The forward pass needs some where few rows' keys are split over CTAs. */
+size_t gbo_attn_forward_workspace_bytes(const gbo_attn_args *args);
+size_t gbo_attn_backward_workspace_bytes(const gbo_attn_args *args);
+
+/*
+ * Forward.
+ *   y         device, bf16, batch x sq x q_heads x dv, y_stride apart; written whole
+ *   lse       device fp32, batch x sq x q_heads, contiguous, or NULL
+ *   workspace device, 256-byte aligned; may be NULL where its size is 0
+ * A wait that ran out sets GBO_STATUS_TIMEOUT.
+ * Errors: INVALID_ARG, SHAPE, DTYPE, WORKSPACE, CUDA.
+ */
+int gbo_attn_forward(const gbo_attn_args *args, void *y, const int64_t *y_stride, float *lse, void *workspace,
+                     size_t ws_bytes, int32_t *dev_status, gbo_stream_t stream);
+
+typedef struct {
+  const void *dy;   /* device, bf16: gradient of the forward's y                            */
+  const void *y;    /* device, bf16: the forward's y                                        */
+  const float *lse; /* device: the forward's lse                                            */
+  void *dq;         /* device, bf16, or NULL: not wanted                                    */
+  void *dk;         /* device, bf16, or NULL                                                */
+  void *dv;         /* device, bf16, or NULL                                                */
+  int64_t dy_stride[3], y_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
+} gbo_attn_grads;
+
+/*
+ * Gradients of gbo_attn_forward, written (not added), each rounded once:
+ *   dv_j = sum_i p_ij dy_i,  ds_ij = scale p_ij (dy_i v_j - dy_i y_i),
+ *   dq_i = sum_j ds_ij k_j,  dk_j = sum_i ds_ij q_i,
+ * the sums over i over all query heads that read key head j's.  p is formed
+ * again from lse; no sum crosses thread blocks, so results repeat bit for bit.
+ */
+int gbo_attn_backward(const gbo_attn_args *args, const gbo_attn_grads *grads, void *workspace, size_t ws_bytes,
+                      int32_t *dev_status, gbo_stream_t stream);
+
 /* ---- softmax cross entropy of the tied classifier -------------------------- */
 
 /*
@@ -594,8 +678,8 @@ int32_t gbo_abi_version(void);
 /* sizeof of an ABI struct, for binding checks: 0 gbo_muon_desc,
  * 1 gbo_muon_opts, 2 gbo_tensor, 3 gbo_adamw_desc, 4 gbo_adamw_opts,
  * 5 gbo_plan_info, 6 gbo_rope_scaling, 7 gbo_rope_opts, 8 gbo_rope_tensor,
- * 9 gbo_rope_positions, 10 gbo_xent_args, 11 gbo_xent_grads; 0 for other
- * values. */
+ * 9 gbo_rope_positions, 10 gbo_xent_args, 11 gbo_xent_grads,
+ * 12 gbo_attn_args, 13 gbo_attn_grads; 0 for other values. */
 size_t gbo_struct_size(int32_t which);
 
 /* Number of kernels this library has launched in this process. */
