@@ -36,6 +36,12 @@ GBO_ROPE_SCALE_NTK = 2
 GBO_ROPE_SCALE_YARN = 3
 GBO_ROPE_SCALE_WAVELENGTH = 4
 GBO_ROPE_MAX_TENSORS = 4
+GBO_GATE_NONE = 0
+GBO_GATE_ELEMENT = 1
+GBO_GATE_ROW = 2
+GBO_SCALE_NONE = 0
+GBO_SCALE_ONE = 1
+GBO_SCALE_VECTOR = 2
 GBO_MAX_VIEW_DIMS = 6
 GBO_N_PHASES = 6
 PHASE_NAMES = ("momentum", "gram", "product", "square", "rows", "final")
@@ -134,8 +140,23 @@ class AttnGrads(ctypes.Structure):
                 ("dk_stride", c_int64 * 3), ("dv_stride", c_int64 * 3)]
 
 
+class ResidualArgs(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("block", c_void_p), ("gate", c_void_p), ("scale", c_void_p), ("post_gain", c_void_p),
+                ("pre_gain", c_void_p), ("dev_seed", c_void_p), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("n", c_int64), ("d", c_int64), ("x_stride", c_int64), ("block_stride", c_int64),
+                ("gate_stride", c_int64), ("dropout", ctypes.c_double), ("x_dtype", c_int32), ("block_dtype", c_int32),
+                ("has_block", c_int32), ("post_norm", c_int32), ("pre_norm", c_int32), ("gate_mode", c_int32),
+                ("gate_sigmoid", c_int32), ("scale_mode", c_int32), ("eps", c_float), ("reserved", c_int32)]
+
+
+class ResidualGrads(ctypes.Structure):
+    _fields_ = [("dx_out", c_void_p), ("dh", c_void_p), ("dx", c_void_p), ("dblock", c_void_p), ("dgate", c_void_p),
+                ("dscale", c_void_p), ("dpost_gain", c_void_p), ("dpre_gain", c_void_p), ("dx_out_stride", c_int64),
+                ("dh_stride", c_int64), ("dx_stride", c_int64), ("dblock_stride", c_int64), ("dgate_stride", c_int64)]
+
+
 _STRUCTS = (MuonDesc, MuonOpts, Tensor, AdamWDesc, AdamWOpts, PlanInfo, RopeScaling, RopeOpts, RopeTensor,
-            RopePositions, XentArgs, XentGrads, AttnArgs, AttnGrads)
+            RopePositions, XentArgs, XentGrads, AttnArgs, AttnGrads, ResidualArgs, ResidualGrads)
 _lib = None
 
 
@@ -189,6 +210,11 @@ def lib():
         "gbo_attn_forward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
                                        c_void_p]),
         "gbo_attn_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+        "gbo_residual_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int32]),
+        "gbo_residual_forward": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+        "gbo_residual_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "gbo_dropout": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64, c_int32, ctypes.c_double,
+                                  ctypes.c_uint64, ctypes.c_uint64, c_void_p, c_void_p]),
         "gbo_testing_wait_timeout": (c_int32, [c_void_p, ctypes.c_uint32, c_void_p]),
         "gbo_testing_set_small_chain": (c_int32, [c_int32]),
         "gbo_testing_set_fused_gram": (c_int32, [c_int32]),
@@ -794,6 +820,108 @@ def gbo_attn_backward(args, q, k, v, dy, y, lse, workspace, *, dq=None, dk=None,
     grads = _PACK_ATTN_GRADS(ptrs[0], ptrs[1], _out_f32(lse, b * sq * hq, "lse"), *ptrs[2:], *strides)
     ws, nbytes = _workspace(workspace)
     _check(lib().gbo_attn_backward(args, grads, ws, nbytes, _dev_ptr(dev_status, "dev_status"), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# residual update and dropout
+
+_PACK_RESIDUAL_ARGS = struct.Struct("@7P2Q5qd8ifi").pack    # ResidualArgs
+_PACK_RESIDUAL_GRADS = struct.Struct("@8P5q").pack          # ResidualGrads
+_U64 = (1 << 64) - 1
+
+
+def _seed_of(seed):
+    """(host seed, device pointer of it) of an int or a CUDA int64 tensor of one value."""
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype is not torch.int64 or seed.numel() != 1 or not seed.is_cuda:
+            raise ValueError("a seed in a tensor is one int64 value on the device")
+        return 0, seed.data_ptr()
+    return int(seed) & _U64, 0
+
+
+def residual_args(x, block, *, post_norm=False, pre_norm=True, post_gain=None, pre_gain=None, gate=None,
+                  gate_kind="sigmoid", scale=None, dropout=0.0, seed=0, offset=0, eps=1e-6, block_dtype=None):
+    """The packed arguments of the residual calls (``gbo_residual_args``): ``x``
+    (the updated stream, backward; None there without ``pre_norm``), ``block`` (or
+    None) and ``gate`` two-dimensional, gains and scale float32."""
+    if gate_kind not in ("sigmoid", "linear"):
+        raise ValueError("gate_kind must be sigmoid or linear")
+    n, d = x.shape
+    xs = _rows_of(x, "x")
+    bt, bs, ba, gp, gs, mode = block_dtype or x.dtype, 0, 0, 0, 0, GBO_GATE_NONE
+    if block is not None:
+        bt, bs, ba = block.dtype, _rows_of(block, "block", x.shape), block.data_ptr()
+    if gate is not None:
+        if gate.dtype != bt:
+            raise ValueError("gate has the dtype of block")
+        mode = GBO_GATE_ROW if gate.shape == (n, 1) and d != 1 else GBO_GATE_ELEMENT
+        gs, gp = _rows_of(gate, "gate", (n, 1) if mode == GBO_GATE_ROW else (n, d)), gate.data_ptr()
+    if x.dtype not in _ELEMENT or bt not in _ELEMENT:
+        raise TypeError("tensor dtype must be float32 or bfloat16, got %s and %s" % (x.dtype, bt))
+    sp, smode = 0, GBO_SCALE_NONE
+    if scale is not None:
+        smode = GBO_SCALE_ONE if scale.numel() == 1 else GBO_SCALE_VECTOR
+        sp = _out_f32(scale, 1 if smode == GBO_SCALE_ONE else d, "scale")
+    host, dev = _seed_of(seed)
+    return _PACK_RESIDUAL_ARGS(x.data_ptr(), ba, gp, sp, _out_f32(post_gain, d, "post_gain") or 0,
+                               _out_f32(pre_gain, d, "pre_gain") or 0, dev, host, int(offset) & _U64, n, d, xs, bs, gs,
+                               float(dropout), _ELEMENT[x.dtype], _ELEMENT[bt], 0 if block is None else 1,
+                               1 if post_norm else 0, 1 if pre_norm else 0, mode, 1 if gate_kind == "sigmoid" else 0, smode,
+                               float(eps), 0)
+
+
+def _rows_or_null(t, what, shape, dtype):
+    """(pointer, row stride) of a two-dimensional tensor, or of none."""
+    if t is None:
+        return 0, 0
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    return t.data_ptr(), _rows_of(t, what, shape)
+
+
+def gbo_residual_forward(args, x_out, h, shape, x_dtype, block_dtype, stream=None):
+    """Residual update of ``args`` (of :func:`residual_args`) into ``x_out`` and ``h``
+    (each may be None where there is nothing to write), ``shape`` (n, d) both."""
+    xp, xs = _rows_or_null(x_out, "x_out", shape, x_dtype)
+    hp, hs = _rows_or_null(h, "h", shape, block_dtype)
+    _check(lib().gbo_residual_forward(args, xp, xs, hp, hs, _stream(stream)))
+
+
+@functools.lru_cache(maxsize=256)
+def _residual_workspace(n, d, sums, device):
+    return int(lib().gbo_residual_workspace_bytes(n, d, sums))
+
+
+def gbo_residual_workspace_bytes(n, d, sums):
+    """Workspace of a backward call that writes ``sums`` of dscale, dpost_gain and dpre_gain."""
+    return int(lib().gbo_residual_workspace_bytes(int(n), int(d), int(sums)))
+
+
+def gbo_residual_backward(args, workspace, shape, x_dtype, block_dtype, *, dx_out=None, dh=None, dx=None, dblock=None,
+                          dgate=None, dscale=None, dpost_gain=None, dpre_gain=None, stream=None):
+    """Gradients of the residual update, whichever are given to be written."""
+    n, d = shape
+    oxp, oxs = _rows_or_null(dx_out, "dx_out", shape, x_dtype)
+    ohp, ohs = _rows_or_null(dh, "dh", shape, block_dtype)
+    xp, xs = _rows_or_null(dx, "dx", shape, x_dtype)
+    bp, bs = _rows_or_null(dblock, "dblock", shape, block_dtype)
+    gp, gs = _rows_or_null(dgate, "dgate", None if dgate is None else (n, dgate.shape[1]), block_dtype)
+    grads = _PACK_RESIDUAL_GRADS(oxp, ohp, xp, bp, gp,
+                                 (_out_f32(dscale, 1 if dscale.numel() == 1 else d, "dscale") if dscale is not None else 0),
+                                 _out_f32(dpost_gain, d, "dpost_gain") or 0, _out_f32(dpre_gain, d, "dpre_gain") or 0, oxs,
+                                 ohs, xs, bs, gs)
+    ws, nbytes = _workspace(workspace)
+    _check(lib().gbo_residual_backward(args, grads, ws, nbytes, _stream(stream)))
+
+
+def gbo_dropout(x, y, p, seed, offset=0, stream=None):
+    """Dropout of the two-dimensional ``x`` into ``y`` (which may be ``x``)."""
+    if x.dtype not in _ELEMENT or y.dtype != x.dtype:
+        raise TypeError("x and y must both be float32 or bfloat16, got %s and %s" % (x.dtype, y.dtype))
+    xs, ys = _rows_of(x, "x"), _rows_of(y, "y", x.shape)
+    host, dev = _seed_of(seed)
+    _check(lib().gbo_dropout(x.data_ptr(), xs, y.data_ptr(), ys, x.shape[0], x.shape[1], _ELEMENT[x.dtype], float(p),
+                             host, int(offset) & _U64, dev, _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -796,6 +796,8 @@ size_t gbo_struct_size(int32_t which) {
     case 11: return sizeof(gbo_xent_grads);
     case 12: return sizeof(gbo_attn_args);
     case 13: return sizeof(gbo_attn_grads);
+    case 14: return sizeof(gbo_residual_args);
+    case 15: return sizeof(gbo_residual_grads);
     default: return 0;
   }
 }

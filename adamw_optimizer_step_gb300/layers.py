@@ -207,6 +207,88 @@ def attention_backward(dy, q, k, v, y, lse, *, causal=True, window=0, scale=None
 
 
 # ---------------------------------------------------------------------------
+# the residual update between two blocks, dropout
+
+def _flat(t, d):
+    """Rows of the last axis, as a two-dimensional view where strides allow it."""
+    return t if t.dim() == 2 else t.reshape(-1, d)
+
+
+def residual_norm(x, block=None, *, post_norm=False, pre_norm=True, post_gain=None, pre_gain=None, gate=None,
+                  gate_kind="sigmoid", scale=None, dropout=0.0, seed=0, offset=0, eps=1e-6, x_out=None):
+    """(x', h): the residual stream ``x`` (..., d) after a block's output ``block``, and
+    the next block's input, in one pass:
+
+        u = block, normed with ``post_norm`` (root mean square, times ``post_gain``)
+        x' = x + scale * gate * dropout(u);  h = x' normed with ``pre_norm``, times ``pre_gain``
+
+    ``gate``: (..., d) or (..., 1), through a sigmoid or (``gate_kind="linear"``) as it
+    is; ``scale``: float32, one value or d; gains: float32, d, or None for ones.
+    ``dropout``: its probability, drawn from ``seed`` (an int, or a CUDA int64 tensor
+    that is read when the kernel runs) and ``offset``, see ``gbo_residual_args``.
+    ``block=None``: the norm alone, and x' is ``x``.  ``x`` and ``block`` are bfloat16 or
+    float32, ``block`` bfloat16 where ``x`` is; ``h`` has the dtype of ``block``.
+    ``x_out`` may be ``x``.  Without ``pre_norm`` h is None."""
+    d = x.shape[-1]
+    x2 = _flat(x, d)
+    b2 = None if block is None else _flat(block, d)
+    g2 = None if gate is None else _flat(gate, gate.shape[-1])
+    bt = x.dtype if block is None else block.dtype
+    args = B.residual_args(x2, b2, post_norm=post_norm, pre_norm=pre_norm, post_gain=post_gain, pre_gain=pre_gain,
+                           gate=g2, gate_kind=gate_kind, scale=scale, dropout=dropout, seed=seed, offset=offset, eps=eps)
+    if block is None:
+        xo = None
+    elif x_out is None:
+        xo = torch.empty(x2.shape, dtype=x.dtype, device=x.device)
+    else:
+        xo = x_out.view(x2.shape)
+    h = torch.empty(x2.shape, dtype=bt, device=x.device) if pre_norm else None
+    B.gbo_residual_forward(args, xo, h, x2.shape, x.dtype, bt)
+    return x if xo is None else xo.view(x.shape), None if h is None else h.view(x.shape)
+
+
+def residual_norm_backward(dx_out, dh, x_new, block=None, *, post_norm=False, pre_norm=True, post_gain=None,
+                           pre_gain=None, gate=None, gate_kind="sigmoid", scale=None, dropout=0.0, seed=0, offset=0,
+                           eps=1e-6, wanted=("dx", "dblock", "dgate", "dscale", "dpost_gain", "dpre_gain")):
+    """Gradients of :func:`residual_norm` from those of x' (``dx_out``, None for none) and
+    of h (``dh``), the updated stream ``x_new`` and the block's output: a dict with
+    ``dx``, ``dblock``, ``dgate``, ``dscale``, ``dpost_gain`` and ``dpre_gain`` (None for
+    what was not given or is not ``wanted``)."""
+    d = x_new.shape[-1]
+    shape = x_new.shape
+    x2 = _flat(x_new, d)
+    b2 = None if block is None else _flat(block, d)
+    g2 = None if gate is None else _flat(gate, gate.shape[-1])
+    bt = x_new.dtype if block is None else block.dtype
+    args = B.residual_args(x2, b2, post_norm=post_norm, pre_norm=pre_norm, post_gain=post_gain, pre_gain=pre_gain,
+                           gate=g2, gate_kind=gate_kind, scale=scale, dropout=dropout, seed=seed, offset=offset, eps=eps)
+    like = {"dx": x2, "dblock": b2, "dgate": g2, "dscale": scale, "dpost_gain": post_gain, "dpre_gain": pre_gain}
+    out = {k: torch.empty(t.shape, dtype=t.dtype, device=x2.device) if t is not None and k in wanted else None
+           for k, t in like.items()}
+    sums = sum(out[k] is not None for k in ("dscale", "dpost_gain", "dpre_gain"))
+    ws = _scratch(B._residual_workspace(*x2.shape, sums, x2.device) if sums else 0, x2.device)
+    B.gbo_residual_backward(args, ws, x2.shape, x_new.dtype, bt, dx_out=None if dx_out is None else _flat(dx_out, d),
+                            dh=None if dh is None else _flat(dh, d), **out)
+    for k, t in (("dx", x_new), ("dblock", block), ("dgate", gate)):
+        if out[k] is not None:
+            out[k] = out[k].view(shape if k != "dgate" else t.shape)
+    return out
+
+
+def dropout(x, p, seed, *, offset=0, out=None):
+    """``x`` with elements dropped with probability ``p`` (a multiple of 2^-16) and the
+    others divided by the share kept.  Which ones follows from ``seed`` (an int, or a
+    CUDA int64 tensor that is read when the kernel runs), ``offset`` and an element's
+    place alone: no mask is kept, and the same call on a gradient is the gradient."""
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    if x.dim() == 2:
+        B.gbo_dropout(x, y, p, seed, offset)
+    else:
+        B.gbo_dropout(x.reshape(1, -1), y.view(1, -1), p, seed, offset)
+    return y
+
+
+# ---------------------------------------------------------------------------
 # autograd
 
 def _rows(t):

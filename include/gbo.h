@@ -547,6 +547,103 @@ typedef struct {
 int gbo_attn_backward(const gbo_attn_args *args, const gbo_attn_grads *grads, void *workspace, size_t ws_bytes,
                       int32_t *dev_status, gbo_stream_t stream);
 
+/* ---- the residual update between two blocks, and dropout ------------------------ */
+
+/*
+ * Rows of d elements of the residual stream x take a block's output o, with a
+ * norm after the block and one before the next (the hidden norms, whose gains
+ * are AdamW parameters), a gate, a scale and dropout.  rho(t) = 1 / sqrt(mean t^2 + eps):
+ *   u  = o rho(o) post_gain                (post_norm = 0: o)
+ *   x' = x + scale gate(a) m u             (m: dropout's factors)
+ *   h  = x' rho(x') pre_gain               (pre_norm = 1)
+ * gate(a) = 1 / (1 + exp(-a)), or a itself; a is one value an element or one a
+ * row.  scale is one fp32 number or d of them.  Arithmetic in fp32, each output
+ * rounded once (h comes from x' before its rounding).  has_block = 0: the norm
+ * alone, x' = x.
+ *
+ * Dropout.  Element e = row d + column takes 16 bits of Philox 4x32-10 (Salmon,
+ * Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3") with the
+ * key `seed` at the counter (e / 8, offset), 64 bits each, low words first: bits
+ * 16 (e mod 2) of word (e mod 8) / 2.  Draws below limit = round(65536 p) (ties
+ * to even) drop the element, the others multiply it by 65536 / (65536 - limit).
+ * No mask is stored: the backward pass draws again.
+ */
+#define GBO_RESIDUAL_MAX_D 16384
+
+#define GBO_GATE_NONE 0
+#define GBO_GATE_ELEMENT 1 /* n rows of d values      */
+#define GBO_GATE_ROW 2     /* one value a row         */
+#define GBO_SCALE_NONE 0
+#define GBO_SCALE_ONE 1
+#define GBO_SCALE_VECTOR 2
+
+typedef struct {
+  const void *x;          /* device, n rows of d, x_dtype.  Backward: x', the updated stream
+                             (read with pre_norm only)                                     */
+  const void *block;      /* device, n rows of d, block_dtype: o; NULL with has_block = 0      */
+  const void *gate;       /* device, block_dtype: a; NULL with GBO_GATE_NONE                   */
+  const float *scale;     /* device, 1 or d values; NULL with GBO_SCALE_NONE                   */
+  const float *post_gain; /* device, d values, or NULL: 1                                      */
+  const float *pre_gain;  /* device, d values, or NULL: 1                                      */
+  const int64_t *dev_seed; /* device, one value read when the kernel runs, or NULL: seed       */
+  uint64_t seed;
+  uint64_t offset;
+  int64_t n, d;           /* rows; elements of a row, 1 .. GBO_RESIDUAL_MAX_D                  */
+  int64_t x_stride, block_stride, gate_stride; /* elements between rows                        */
+  double dropout;         /* 0 <= p < 1                                                        */
+  int32_t x_dtype;        /* GBO_F32 | GBO_BF16: the stream and its gradients                  */
+  int32_t block_dtype;    /* GBO_BF16, or GBO_F32 with x in GBO_F32: o, a, h and their gradients */
+  int32_t has_block;      /* 0 | 1                                                             */
+  int32_t post_norm, pre_norm; /* 0 | 1                                                        */
+  int32_t gate_mode;      /* GBO_GATE_*                                                        */
+  int32_t gate_sigmoid;   /* 1: 1 / (1 + exp(-a)); 0: a itself                                 */
+  int32_t scale_mode;     /* GBO_SCALE_*                                                       */
+  float eps;              /* of both norms, >= 0                                               */
+  int32_t reserved;       /* set to 0                                                          */
+} gbo_residual_args;
+
+/*
+ *   x_out  device, n rows of d, x_dtype: x' (may be x, with its stride); NULL with has_block = 0
+ *   h      device, n rows of d, block_dtype (may be block, with its stride); NULL with pre_norm = 0
+ * Errors: INVALID_ARG, SHAPE, DTYPE, CUDA.
+ */
+int gbo_residual_forward(const gbo_residual_args *args, void *x_out, int64_t x_out_stride, void *h, int64_t h_stride,
+                         gbo_stream_t stream);
+
+typedef struct {
+  const void *dx_out; /* device, x_dtype: gradient of x' from what else reads it, or NULL: none   */
+  const void *dh;     /* device, block_dtype: gradient of h; NULL with pre_norm = 0                */
+  void *dx;           /* device, x_dtype: gradient of x (may be dx_out), or NULL: not wanted       */
+  void *dblock;       /* device, block_dtype: of o (may be dh), or NULL                            */
+  void *dgate;        /* device, block_dtype, n rows of d or of 1, or NULL                         */
+  float *dscale;      /* device, 1 or d values, written, or NULL                                   */
+  float *dpost_gain;  /* device, d values, written, or NULL                                        */
+  float *dpre_gain;   /* device, d values, written, or NULL                                        */
+  int64_t dx_out_stride, dh_stride, dx_stride, dblock_stride, dgate_stride;
+} gbo_residual_grads;
+
+/*
+ * Gradients.  With g the whole gradient of x' (dx_out and what comes through h):
+ *   dx = g,  dgate = g scale m u gate'(a),  du = g scale gate(a) m,
+ *   dscale = sum g gate(a) m u,  dpost_gain = sum du o rho(o),  dpre_gain = sum dh x' rho(x')
+ * and dblock is du through the norm.  Sums over rows are fp32, in a fixed order.
+ *   workspace  device, >= gbo_residual_workspace_bytes(n, d, number of dscale,
+ *              dpost_gain and dpre_gain wanted) bytes, 16-byte aligned; may be
+ *              NULL when none is wanted
+ * Errors: INVALID_ARG, SHAPE, DTYPE, WORKSPACE, CUDA.
+ */
+int gbo_residual_backward(const gbo_residual_args *args, const gbo_residual_grads *grads, void *workspace, size_t ws_bytes,
+                          gbo_stream_t stream);
+size_t gbo_residual_workspace_bytes(int64_t n, int64_t d, int32_t sums);
+
+/*
+ * Dropout alone: n rows of d elements, y = m x (y may be x, with its stride); its
+ * gradient is the same call on the gradient.  dev_seed as above.
+ * Errors: INVALID_ARG, SHAPE, DTYPE, CUDA.
+ */
+int gbo_dropout(const void *x, int64_t x_stride, void *y, int64_t y_stride, int64_t n, int64_t d, int32_t dtype, double p,
+                uint64_t seed, uint64_t offset, const int64_t *dev_seed, gbo_stream_t stream);
+
 /* ---- softmax cross entropy of the tied classifier -------------------------- */
 
 /*
@@ -679,7 +776,8 @@ int32_t gbo_abi_version(void);
  * 1 gbo_muon_opts, 2 gbo_tensor, 3 gbo_adamw_desc, 4 gbo_adamw_opts,
  * 5 gbo_plan_info, 6 gbo_rope_scaling, 7 gbo_rope_opts, 8 gbo_rope_tensor,
  * 9 gbo_rope_positions, 10 gbo_xent_args, 11 gbo_xent_grads,
- * 12 gbo_attn_args, 13 gbo_attn_grads; 0 for other values. */
+ * 12 gbo_attn_args, 13 gbo_attn_grads, 14 gbo_residual_args,
+ * 15 gbo_residual_grads; 0 for other values. */
 size_t gbo_struct_size(int32_t which);
 
 /* Number of kernels this library has launched in this process. */
