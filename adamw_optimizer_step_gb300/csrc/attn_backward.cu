@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
   const uint32_t tfull0 = dempty0 + 8 * C::kDStages, tempty0 = tfull0 + 8 * C::kStats;
   const uint32_t sfull = tempty0 + 8 * C::kStats, pready = sfull + 8, dpfull = pready + 8, dsready = dpfull + 8;
   const uint32_t done = dsready + 8;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 1 + 2 * C::kQStages + 2 * C::kDStages; ++s) mbar_init(kvfull + 8 * s, 1);
     for (int s = 0; s < C::kStats; ++s) {
@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
       const uint32_t q = qring + st * C::kQStage;
       clean(i, q, A.kb);
       tc_fence_after();
-      if (lane == 0) {
-        product_ss(tmem, kt, q, A.k_steps, C::kQBlock, kQt);
+      if (elect_one()) {
+        product_ss<kKb>(tmem, kt, q, A.k_steps, C::kQBlock, kQt);
         mma_commit_one(sfull);
       }
       __syncwarp();
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
       const uint32_t d = dring + st * C::kDStage;
       clean(i, d, A.vb);
       tc_fence_after();
-      if (lane == 0) {
-        product_ss(tmem + C::kDp, vt, d, (A.dv + 15) / 16, C::kQBlock, kQt);
+      if (elect_one()) {
+        product_ss<kVb>(tmem + C::kDp, vt, d, A.v_cols / 16, C::kQBlock, kQt);
         mma_commit_one(dpfull);
       }
       __syncwarp();
@@ -262,17 +262,17 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
     for (int i = 0; i < steps && ok; ++i) {
       if (!(ok = guard.wait_warp(pready, i & 1))) break;
       tc_fence_after();
-      if (lane == 0) {
-        product_ts(tmem + C::kDv, tmem, kQt / 2, dring + (i % C::kDStages) * C::kDStage, kQt / 16, C::kQBlock, A.v_cols, i > 0);
+      if (elect_one()) {
+        product_ts<kQt / 16>(tmem + C::kDv, tmem, kQt / 2, dring + (i % C::kDStages) * C::kDStage, C::kQBlock, A.v_cols, i > 0);
         mma_commit_one(dempty0 + 8 * (i % C::kDStages));
       }
       __syncwarp();
       if (i + 1 < steps && !(ok = s_product(i + 1))) break;
       if (!(ok = guard.wait_warp(dsready, i & 1))) break;
       tc_fence_after();
-      if (lane == 0) {
-        product_ts(tmem + C::kDk, tmem + C::kDp, kQt / 2, qring + (i % C::kQStages) * C::kQStage, kQt / 16, C::kQBlock,
-                   A.k_steps * 16, i > 0);
+      if (elect_one()) {
+        product_ts<kQt / 16>(tmem + C::kDk, tmem + C::kDp, kQt / 2, qring + (i % C::kQStages) * C::kQStage, C::kQBlock,
+                             A.k_steps * 16, i > 0);
         mma_commit_one(qempty0 + 8 * (i % C::kQStages));
         if (i + 1 == steps) mma_commit_one(done);
       }
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
   const uint32_t vfull0 = kempty0 + 8 * C::kKStages, vempty0 = vfull0 + 8 * C::kVStages;
   const uint32_t sfull0 = vempty0 + 8 * C::kVStages, dpfull = sfull0 + 16, dpread = dpfull + 8, dsready = dpread + 8;
   const uint32_t done = dsready + 8;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 1 + 2 * C::kKStages + 2 * C::kVStages + 3; ++s) mbar_init(rfull + 8 * s, 1);
     mbar_init(dpread, kBwdWarps);
@@ -511,8 +511,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
       if (k0 < seq.k_lo || (k0 + kAttnTile > seq.k_hi && seq.k_hi < P.mask.sk))
         zero_rows(k, A.kb, kAttnTile, kAttnBlock, seq.k_lo - k0, seq.k_hi - k0, lane);
       tc_fence_after();
-      if (lane == 0) {
-        product_ss(tmem + (i % C::kBufs) * 128, qt, k, A.k_steps, kAttnBlock, kAttnTile);
+      if (elect_one()) {
+        product_ss<kKb>(tmem + (i % C::kBufs) * 128, qt, k, A.k_steps, kAttnBlock, kAttnTile);
         mma_commit_one(sfull0 + 8 * (i % C::kBufs));
       }
       __syncwarp();
@@ -523,8 +523,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
       if (!guard.wait_warp(vfull0 + 8 * st, (i / C::kVStages) & 1)) return false;
       if (i > 0 && !guard.wait_warp(dpread, (i - 1) & 1)) return false;
       tc_fence_after();
-      if (lane == 0) {
-        product_ss(tmem + C::kDp, dt, vring + st * C::kDTile, (A.dv + 15) / 16, kAttnBlock, kAttnTile);
+      if (elect_one()) {
+        product_ss<kVb>(tmem + C::kDp, dt, vring + st * C::kDTile, A.v_cols / 16, kAttnBlock, kAttnTile);
         mma_commit_one(dpfull);
         mma_commit_one(vempty0 + 8 * st);
       }
@@ -539,9 +539,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
       }
       if (!(ok = guard.wait_warp(dsready, i & 1))) break;
       tc_fence_after();
-      if (lane == 0) {
-        product_ts(tmem + C::kDq, tmem + (i % C::kBufs) * 128, 64, kring + (i % C::kKStages) * C::kQTile, kAttnTile / 16,
-                   kAttnBlock, A.k_steps * 16, i > 0);
+      if (elect_one()) {
+        product_ts<8>(tmem + C::kDq, tmem + (i % C::kBufs) * 128, 64, kring + (i % C::kKStages) * C::kQTile, kAttnBlock,
+                      A.k_steps * 16, i > 0);
         mma_commit_one(kempty0 + 8 * (i % C::kKStages));
         if (i + 1 == steps) mma_commit_one(done);
       }

@@ -220,49 +220,80 @@ __host__ __device__ constexpr uint32_t attn_idesc(bool b_mn_major, int n) {
          ((uint32_t)(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+// The low word of a descriptor whose high word is this one: stride 1024 bytes,
+// version 1, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); }
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
 
 // A from TMEM: 128 lanes, a 32-bit column holds two consecutive K.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
 
-// D = A B^T over `steps` steps of 16, A (128 rows) and B (rows of n) both
-// K-major in blocks of 64 columns; a_block, b_block: bytes of a block.
-__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t b_block, int n) {
-  const uint32_t idesc = attn_idesc(false, n);
-  const uint64_t ad = smem_desc(a, 16, 1024), bd = smem_desc(b, 16, 1024);
-  for (int k = 0; k < steps; ++k) {
-    const uint32_t in = (uint32_t)((k & 3) * 32);
-    mma_ss(d, ad + (((uint32_t)(k >> 2) * kAttnBlock + in) >> 4), bd + (((uint32_t)(k >> 2) * b_block + in) >> 4), idesc,
-           k != 0);
+// The products are issued by one thread, and each step of 16 keeps the tensor
+// cores busy for 64 clocks or less: the steps are unrolled and their descriptors
+// are one base and constants.
+
+// D (+)= A B^T over `steps` (1..4) steps of 16 of one block of 64 columns, both
+// K-major.
+__device__ __forceinline__ void product_block(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc, bool accumulate) {
+  const uint32_t al = desc_low(a, 16), bl = desc_low(b, 16);
+  if (steps == 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mma_ss(d, al + 2 * k, bl + 2 * k, idesc, accumulate || k > 0);
+  } else {
+    for (int k = 0; k < steps; ++k) mma_ss(d, al + 2 * k, bl + 2 * k, idesc, accumulate || k > 0);
   }
 }
 
-// D (+)= A B over K = 16 `steps`, A in TMEM from column a on, B with K along its
-// rows (MN-major) in blocks of 64 columns of b_block bytes, n columns in all.
-// The second half of A's steps stands a_second columns after the first.
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t a_second, uint32_t b, int steps, uint32_t b_block,
-                                           int n, bool accumulate) {
+// D = A B^T over `steps` steps of 16, at most kBlocks blocks of 64 columns: A of
+// 128 rows, B of n rows with b_block bytes a block.
+template <int kBlocks>
+__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t b_block, int n) {
+  const uint32_t idesc = attn_idesc(false, n);
+#pragma unroll
+  for (int c = 0; c < kBlocks; ++c)
+    if (4 * c < steps) product_block(d, a + c * kAttnBlock, b + c * b_block, min(4, steps - 4 * c), idesc, c > 0);
+}
+
+// D (+)= A B over kSteps steps of K = 16, A in TMEM from column a on, B with K along
+// its rows (MN-major) in blocks of 64 columns of b_block bytes, n columns in all.
+// The second half of A's steps stands a_second columns after the first's start.
+template <int kSteps>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t a_second, uint32_t b, uint32_t b_block, int n,
+                                           bool accumulate) {
   const uint32_t idesc = attn_idesc(true, n);
-  const uint64_t bd = smem_desc(b, b_block, 1024);
-  const int half = steps >> 1;
-#pragma unroll 8
-  for (int k = 0; k < steps; ++k)
-    mma_ts(d, a + (k < half ? 0 : a_second) + (uint32_t)((k < half ? k : k - half) * 8), bd + ((uint32_t)(k * 2048) >> 4),
-           idesc, accumulate || k != 0);
+  const uint32_t bl = desc_low(b, b_block);
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k)
+    mma_ts(d, a + (k < kSteps / 2 ? k * 8 : a_second + (k - kSteps / 2) * 8), bl + k * (2048 >> 4), idesc, accumulate || k > 0);
 }
 
 // ---------------------------------------------------------------------------

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
   const uint32_t qfull0 = smem_u32(bars), full0 = qfull0 + 16, empty0 = full0 + 8 * C::kRing;
   const uint32_t sfull0 = empty0 + 8 * C::kRing, pready0 = sfull0 + 16, odone0 = pready0 + 16;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2 + 2 * C::kRing; ++s) mbar_init(qfull0 + 8 * s, 1);
     for (int t = 0; t < 2; ++t) {
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
       for (int c = 0; c < count && ok; ++c) ok = guard.wait_warp(full0 + 8 * ((first + c) % C::kRing), ((first + c) / C::kRing) & 1);
     };
     auto release = [&](int first, int count) {
-      if (lane == 0)
+      if (elect_one())
         for (int c = 0; c < count; ++c) mma_commit_one(empty0 + 8 * ((first + c) % C::kRing));
     };
     for (int j = J0; j <= J1 && J1 > J0 && ok; ++j) {
@@ -177,16 +177,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
         if (pv && tk[t].has(j - 1)) {
           if (!(ok = guard.wait_warp(pready0 + 8 * t, np[t] & 1))) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const int slot = vpos % C::kRing;
+            const uint32_t o = tmem + C::kO + t * kVb * 64, p = tmem + t * 128, v = ring0 + slot * kAttnBlock;
             if (A.vb == 1 || slot + 1 < C::kRing) {
-              product_ts(tmem + C::kO + t * kVb * 64, tmem + t * 128, 64, ring0 + slot * kAttnBlock, kAttnTile / 16, kAttnBlock,
-                         A.v_cols, np[t] > 0);
+              product_ts<8>(o, p, 64, v, kAttnBlock, A.v_cols, np[t] > 0);
             } else {  // the values' two blocks lie at the ring's ends
-              product_ts(tmem + C::kO + t * kVb * 64, tmem + t * 128, 64, ring0 + slot * kAttnBlock, kAttnTile / 16, kAttnBlock,
-                         64, np[t] > 0);
-              product_ts(tmem + C::kO + t * kVb * 64 + 64, tmem + t * 128, 64, ring0, kAttnTile / 16, kAttnBlock, A.v_cols - 64,
-                         np[t] > 0);
+              product_ts<8>(o, p, 64, v, kAttnBlock, 64, np[t] > 0);
+              product_ts<8>(o + 64, p, 64, ring0, kAttnBlock, A.v_cols - 64, np[t] > 0);
             }
             mma_commit_one(odone0 + 8 * t);
           }
@@ -199,13 +197,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
           if (!ok) break;
           q_here[t] = true;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t idesc = attn_idesc(false, kAttnTile);
-            for (int k = 0; k < A.k_steps; ++k) {
-              const uint32_t in = (uint32_t)((k & 3) * 32);
-              mma_ss(tmem + t * 128, smem_desc(q0 + t * C::kQTile + (k >> 2) * kAttnBlock + in, 16, 1024),
-                     smem_desc(ring0 + ((kpos + (k >> 2)) % C::kRing) * kAttnBlock + in, 16, 1024), idesc, k != 0);
-            }
+#pragma unroll
+            for (int c = 0; c < kKb; ++c)
+              if (c < A.kb)
+                product_block(tmem + t * 128, q0 + t * C::kQTile + c * kAttnBlock, ring0 + ((kpos + c) % C::kRing) * kAttnBlock,
+                              min(4, A.k_steps - 4 * c), idesc, c > 0);
             mma_commit_one(sfull0 + 8 * t);
           }
           __syncwarp();
