@@ -18,7 +18,7 @@ namespace gbo {
 
 namespace {
 
-constexpr int kBwdWarps = 8;  // elementwise: two groups of four, each half of the columns
+constexpr int kBwdWarps = 16;  // elementwise: four groups of four, each a quarter of a tile's columns
 constexpr float kLog2ePlain = 1.4426950408889634f;
 
 // ---------------------------------------------------------------------------
@@ -88,21 +88,14 @@ struct Dkv {
   static constexpr int kQStages = 3, kDStages = kKb == 2 ? 2 : 3, kStats = 2;
   static constexpr int kRing = kKTile + kVTile, kStatAt = kRing + kQStages * kQStage + kDStages * kDStage;
   static constexpr int kUsed = kStatAt + kStats * kQt * 8;
-  // kv, q full/empty, dy full/empty, stats full/empty, S, P, dP, dS, done
-  static constexpr int kBars = 1 + 2 * kQStages + 2 * kDStages + 2 * kStats + 5;
+  // kv, q full/empty, dy full/empty, stats full/empty, S, P, dP, dS, drained (two), raw
+  static constexpr int kBars = 1 + 2 * kQStages + 2 * kDStages + 2 * kStats + 4 + 2 + 1;
   static constexpr int kSmem = kUsed + kBars * 8 + 16;
   static constexpr uint32_t kDp = kQt, kDv = 2 * kQt, kDk = 2 * kQt + kVb * 64;  // TMEM columns
   static_assert(kDk + kKb * 64 <= 512, "TMEM columns");
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
-constexpr int kDkvThreads = (kBwdWarps + 3) * 32;
-
-// Sixteen-lane halves of a row's columns go back as bf16 pairs.
-template <int kCols>
-__device__ __forceinline__ void put_pairs(uint32_t taddr, const uint32_t *p) {
-  if constexpr (kCols == 64) tmem_put(taddr, p);
-  else tmem_put16(taddr, p);
-}
+constexpr int kDkvThreads = (kBwdWarps + 4) * 32;
 
 template <int kKb, int kVb, int kQt>
 __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_constant__ BwdParams P) {
@@ -116,10 +109,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
   const uint32_t dfull0 = qempty0 + 8 * C::kQStages, dempty0 = dfull0 + 8 * C::kDStages;
   const uint32_t tfull0 = dempty0 + 8 * C::kDStages, tempty0 = tfull0 + 8 * C::kStats;
   const uint32_t sfull = tempty0 + 8 * C::kStats, pready = sfull + 8, dpfull = pready + 8, dsready = dpfull + 8;
-  const uint32_t done = dsready + 8;
+  const uint32_t done0 = dsready + 8, raw = done0 + 16;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 1 + 2 * C::kQStages + 2 * C::kDStages; ++s) mbar_init(kvfull + 8 * s, 1);
+    for (int s = 0; s < 1 + 2 * C::kQStages + C::kDStages; ++s) mbar_init(kvfull + 8 * s, 1);
+    for (int s = 0; s < C::kDStages; ++s) mbar_init(dempty0 + 8 * s, 2);  // dP and dV
     for (int s = 0; s < C::kStats; ++s) {
       mbar_init(tfull0 + 8 * s, 32);
       mbar_init(tempty0 + 8 * s, kBwdWarps);
@@ -128,7 +122,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
     mbar_init(pready, kBwdWarps);
     mbar_init(dpfull, 1);
     mbar_init(dsready, kBwdWarps);
-    mbar_init(done, 1);
+    for (int s = 0; s < 3; ++s) mbar_init(done0 + 8 * s, 1);  // (and raw)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -168,39 +162,30 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
   float *const stats = reinterpret_cast<float *>(smem + C::kStatAt);
   const AttnGuard guard = {abort_flag, P.status};
 
-  if (warp == kBwdWarps + 1) {
-    if (lane == 0 && steps > 0) {
-      uint32_t q_armed = 0, q_par = 0, d_armed = 0, d_par = 0;
-      mbar_expect_tx(kvfull, (uint32_t)(A.kb + A.vb) * kAttnBlock);
-      for (int c = 0; c < A.kb; ++c) tma_load_4d(kt + c * kAttnBlock, &P.k, kvfull, 64 * c, kh, k0, b);
-      for (int c = 0; c < A.vb; ++c) tma_load_4d(vt + c * kAttnBlock, &P.v, kvfull, 64 * c, kh, k0, b);
-      int qs = 0, ds = 0, tt = 0, hb = 0;
-      uint32_t qp = 0, dp = 0;
-      for (int i = 0; i < steps; ++i) {
-        const int h0 = kh * group + (hb << A.pack), t0 = (tt0 + tt) * tokens;
-        if (!guard.wait(qempty0 + 8 * qs, qp ^ 1)) break;
-        mbar_expect_tx(qfull0 + 8 * qs, (uint32_t)(A.kb * C::kQBlock));
-        for (int c = 0; c < A.kb; ++c)
-          tma_load_4d(qring + qs * C::kQStage + c * C::kQBlock, &P.q, qfull0 + 8 * qs, 64 * c, h0, t0, b);
-        q_armed |= 1u << qs, q_par = (q_par & ~(1u << qs)) | (qp << qs);
-        if (++qs == C::kQStages) qs = 0, qp ^= 1;
-        if (!guard.wait(dempty0 + 8 * ds, dp ^ 1)) break;
-        mbar_expect_tx(dfull0 + 8 * ds, (uint32_t)(A.vb * C::kQBlock));
-        for (int c = 0; c < A.vb; ++c)
-          tma_load_4d(dring + ds * C::kDStage + c * C::kQBlock, &P.dy, dfull0 + 8 * ds, 64 * c, h0, t0, b);
-        d_armed |= 1u << ds, d_par = (d_par & ~(1u << ds)) | (dp << ds);
-        if (++ds == C::kDStages) ds = 0, dp ^= 1;
-        if (++tt == n_tok) tt = 0, ++hb;
+  if (warp == kBwdWarps + 2) {
+    uint32_t raw_phase = 0;
+    TileRing Q(qfull0, qempty0, qring, C::kQStage, C::kQStages), D(dfull0, dempty0, dring, C::kDStage, C::kDStages);
+    Armed kv;
+    if (steps > 0) {
+      if (elect_one()) {
+        mbar_expect_tx(kvfull, (uint32_t)(A.kb + A.vb) * kAttnBlock);
+        for (int c = 0; c < A.kb; ++c) tma_load_4d(kt + c * kAttnBlock, &P.k, kvfull, 64 * c, kh, k0, b);
+        for (int c = 0; c < A.vb; ++c) tma_load_4d(vt + c * kAttnBlock, &P.v, kvfull, 64 * c, kh, k0, b);
       }
-      if (guard.aborted()) {  // copies in flight land before shared memory goes away
-        (void)mbar_wait(kvfull, 0);
-        for (int s = 0; s < C::kQStages; ++s)
-          if (q_armed >> s & 1u) (void)mbar_wait(qfull0 + 8 * s, q_par >> s & 1u);
-        for (int s = 0; s < C::kDStages; ++s)
-          if (d_armed >> s & 1u) (void)mbar_wait(dfull0 + 8 * s, d_par >> s & 1u);
-      }
+      __syncwarp();
+      kv.set(0, 0);
     }
-  } else if (warp == kBwdWarps + 2) {
+    int tt = 0, hb = 0;
+    for (int i = 0; i < steps; ++i) {
+      const int h0 = kh * group + (hb << A.pack), t0 = (tt0 + tt) * tokens;
+      const bool dirty = t0 < seq.q_lo || (t0 + tokens > seq.q_hi && seq.q_hi < P.mask.sq);
+      const int lo = max(0, seq.q_lo - t0) << A.pack, hi = min(tokens, seq.q_hi - t0) << A.pack;
+      if (!Q.load(guard, &P.q, A.kb, C::kQBlock, h0, t0, b, dirty, raw, raw_phase, kQt, lo, hi, lane)) break;
+      if (!D.load(guard, &P.dy, A.vb, C::kQBlock, h0, t0, b, dirty, raw, raw_phase, kQt, lo, hi, lane)) break;
+      if (++tt == n_tok) tt = 0, ++hb;
+    }
+    if (guard.aborted()) kv.settle(kvfull), Q.armed.settle(qfull0), D.armed.settle(dfull0);
+  } else if (warp == kBwdWarps + 3) {
     // the rows' statistics, a stage ahead of the elementwise warps
     int s = 0, tt = 0, hb = 0;
     uint32_t ph = 0;
@@ -225,62 +210,64 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
       if (++tt == n_tok) tt = 0, ++hb;
     }
   } else if (warp == kBwdWarps) {
+    // S(i + 1) behind dV(i), whose P stands over S(i)
+    RingAt Q, D;
     bool ok = steps > 0 && guard.wait_warp(kvfull, 0);
-    // rows of dead queries may hold anything, and 0 x NaN is not 0
-    auto clean = [&](int i, uint32_t tile, int blocks) {
-      const int t0 = (tt0 + i % n_tok) * tokens;
-      if (t0 < seq.q_lo || (t0 + tokens > seq.q_hi && seq.q_hi < P.mask.sq))
-        zero_rows(tile, blocks, kQt, C::kQBlock, max(0, seq.q_lo - t0) << A.pack, min(tokens, seq.q_hi - t0) << A.pack, lane);
-    };
-    auto s_product = [&](int i) {
-      const int st = i % C::kQStages;
-      if (!guard.wait_warp(qfull0 + 8 * st, (i / C::kQStages) & 1)) return false;
-      const uint32_t q = qring + st * C::kQStage;
-      clean(i, q, A.kb);
-      tc_fence_after();
-      if (elect_one()) {
-        product_ss<kKb>(tmem, kt, q, A.k_steps, C::kQBlock, kQt);
-        mma_commit_one(sfull);
+    for (int i = 0; i <= steps && ok; ++i) {
+      if (i > 0) {
+        if (!guard.wait_warp(dfull0 + 8 * D.stage, D.phase) || !guard.wait_warp(pready, (i - 1) & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          product_ts<kQt / 16, 4>(tmem + C::kDv, tmem, kQt / 4, dring + D.stage * C::kDStage, C::kQBlock, A.v_cols, i > 1);
+          mma_commit_one(dempty0 + 8 * D.stage);
+        }
+        __syncwarp();
+        D.next(C::kDStages);
       }
-      __syncwarp();
-      return true;
-    };
-    auto dp_product = [&](int i) {
-      const int st = i % C::kDStages;
-      if (!guard.wait_warp(dfull0 + 8 * st, (i / C::kDStages) & 1)) return false;
-      const uint32_t d = dring + st * C::kDStage;
-      clean(i, d, A.vb);
-      tc_fence_after();
-      if (elect_one()) {
-        product_ss<kVb>(tmem + C::kDp, vt, d, A.v_cols / 16, C::kQBlock, kQt);
-        mma_commit_one(dpfull);
+      if (i < steps) {
+        if (!guard.wait_warp(qfull0 + 8 * Q.stage, Q.phase)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          product_ss<kKb>(tmem, kt, qring + Q.stage * C::kQStage, A.k_steps, C::kQBlock, kQt);
+          mma_commit_one(sfull);
+        }
+        __syncwarp();
+        Q.next(C::kQStages);
       }
-      __syncwarp();
-      return true;
-    };
-    if (ok) ok = s_product(0) && dp_product(0);
-    for (int i = 0; i < steps && ok; ++i) {
-      if (!(ok = guard.wait_warp(pready, i & 1))) break;
-      tc_fence_after();
-      if (elect_one()) {
-        product_ts<kQt / 16>(tmem + C::kDv, tmem, kQt / 2, dring + (i % C::kDStages) * C::kDStage, C::kQBlock, A.v_cols, i > 0);
-        mma_commit_one(dempty0 + 8 * (i % C::kDStages));
-      }
-      __syncwarp();
-      if (i + 1 < steps && !(ok = s_product(i + 1))) break;
-      if (!(ok = guard.wait_warp(dsready, i & 1))) break;
-      tc_fence_after();
-      if (elect_one()) {
-        product_ts<kQt / 16>(tmem + C::kDk, tmem + C::kDp, kQt / 2, qring + (i % C::kQStages) * C::kQStage, C::kQBlock,
-                             A.k_steps * 16, i > 0);
-        mma_commit_one(qempty0 + 8 * (i % C::kQStages));
-        if (i + 1 == steps) mma_commit_one(done);
-      }
-      __syncwarp();
-      if (i + 1 < steps) ok = dp_product(i + 1);
     }
+    drain_products(done0);
+  } else if (warp == kBwdWarps + 1) {
+    // dP(i + 1) behind dK(i), whose dS stands over dP(i); that is the last to read
+    // the queries' tile
+    RingAt Q, D;
+    bool ok = steps > 0 && guard.wait_warp(kvfull, 0);
+    for (int i = 0; i <= steps && ok; ++i) {
+      if (i > 0) {
+        if (!guard.wait_warp(qfull0 + 8 * Q.stage, Q.phase) || !guard.wait_warp(dsready, (i - 1) & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          product_ts<kQt / 16, 4>(tmem + C::kDk, tmem + C::kDp, kQt / 4, qring + Q.stage * C::kQStage, C::kQBlock,
+                                  A.k_steps * 16, i > 1);
+          mma_commit_one(qempty0 + 8 * Q.stage);
+        }
+        __syncwarp();
+        Q.next(C::kQStages);
+      }
+      if (i < steps) {
+        if (!guard.wait_warp(dfull0 + 8 * D.stage, D.phase)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          product_ss<kVb>(tmem + C::kDp, vt, dring + D.stage * C::kDStage, A.v_cols / 16, C::kQBlock, kQt);
+          mma_commit_one(dpfull);
+          mma_commit_one(dempty0 + 8 * D.stage);
+        }
+        __syncwarp();
+        D.next(C::kDStages);
+      }
+    }
+    drain_products(done0 + 8);
   } else {
-    constexpr int kCols = kQt / 2;
+    constexpr int kCols = kQt / 4;
     const int grp = warp >> 2, row = (warp & 3) * 32 + lane, key = k0 + row;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t S = trow + grp * kCols, D = S + C::kDp;
@@ -301,10 +288,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
       const float4 *nl = reinterpret_cast<const float4 *>(stats + st * 2 * kQt + grp * kCols);
       const float4 *dl = reinterpret_cast<const float4 *>(stats + st * 2 * kQt + kQt + grp * kCols);
       uint32_t r[kCols], w[kCols / 2];
-#pragma unroll
-      for (int c = 0; c < kCols; c += 32) tmem_get(S + c, r + c);
-#pragma unroll
-      for (int c = 0; c < kCols; c += 32) tmem_wait(r + c);
+      tmem_read<kCols>(S, r);
 #pragma unroll
       for (int c = 0; c < kCols; c += 4) {
         const float4 l = nl[c / 4];
@@ -321,7 +305,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
         w[c / 2] = pack_bf16(p[0], p[1]);
         w[c / 2 + 1] = pack_bf16(p[2], p[3]);
       }
-      put_pairs<kCols>(S, w);
+      tmem_write<kCols>(S, w);
       tmem_put_wait();
       tc_fence_before();
       __syncwarp();
@@ -329,10 +313,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
       if (!(ok = guard.wait_warp(dpfull, i & 1))) break;
       tc_fence_after();
       uint32_t g[kCols];
-#pragma unroll
-      for (int c = 0; c < kCols; c += 32) tmem_get(D + c, g + c);
-#pragma unroll
-      for (int c = 0; c < kCols; c += 32) tmem_wait(g + c);
+      tmem_read<kCols>(D, g);
 #pragma unroll
       for (int c = 0; c < kCols; c += 4) {
         const float4 d = dl[c / 4];
@@ -349,7 +330,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
         w[c / 2] = pack_bf16(x.x, x.y);
         w[c / 2 + 1] = pack_bf16(y.x, y.y);
       }
-      put_pairs<kCols>(D, w);
+      tmem_write<kCols>(D, w);
       tmem_put_wait();
       tc_fence_before();
       __syncwarp();
@@ -360,37 +341,35 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
       if (++st == C::kStats) st = 0, ph ^= 1;
       if (++tt == n_tok) tt = 0;
     }
-    if (ok && steps > 0) ok = guard.wait_warp(done, 0);
+    if (ok) ok = guard.wait_warp(done0, 0) && guard.wait_warp(done0 + 8, 0);
     tc_fence_after();
     if (ok) {
-      // one group writes dV, the other dK, through the places of V and K
-      const bool is_k = grp == 1;
-      const int blocks = is_k ? A.kb : A.vb;
+      // two groups write dV, the others dK, blocks of 64 columns in turn, through
+      // the places of V and K
+      const bool is_k = grp >= 2;
+      const int blocks = is_k ? A.kb : A.vb, r0 = (warp & 3) * 32;
       const float f = is_k ? A.scale : 1.f;
       const uint32_t from = trow + (is_k ? C::kDk : C::kDv), out = is_k ? kt : vt;
       if (is_k ? P.has1 : P.has2) {
+        for (int blk = grp & 1; blk < blocks; blk += 2) {
 #pragma unroll 1
-        for (int c = 0; c < blocks * 64; c += 32) {
-          uint32_t r[32];
-          float v[32];
-          if (steps > 0) {
-            tmem_get(from + c, r);
-            tmem_wait(r);
-          }
+          for (int c = blk * 64; c < blk * 64 + 64; c += 32) {
+            uint32_t r[32];
+            float v[32];
+            if (steps > 0) tmem_read<32>(from + c, r);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = steps > 0 && live ? __uint_as_float(r[e]) * f : 0.f;
-          put_tile_row(out, row, c, v);
+            for (int e = 0; e < 32; ++e) v[e] = steps > 0 && live ? __uint_as_float(r[e]) * f : 0.f;
+            put_tile_row(out, row, c, v);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0 && k0 + r0 < P.mask.sk) {
+            tma_store_4d(is_k ? &P.o1 : &P.o2, out + blk * kAttnBlock + r0 * 128, 64 * blk, kh, k0 + r0, b);
+            bulk_commit();
+            bulk_wait_all();
+          }
+          __syncwarp();
         }
-        fence_async_smem();
-        __syncwarp();
-        const int r0 = (warp & 3) * 32;
-        if (lane == 0 && k0 + r0 < P.mask.sk) {
-          for (int c = 0; c < blocks; ++c)
-            tma_store_4d(is_k ? &P.o1 : &P.o2, out + c * kAttnBlock + r0 * 128, 64 * c, kh, k0 + r0, b);
-          bulk_commit();
-          bulk_wait_all();
-        }
-        __syncwarp();
       }
     }
   }
@@ -415,14 +394,14 @@ struct Dq {
   static constexpr int kKStages = kKb == 1 ? 4 : kKb == 2 ? 3 : 2, kVStages = kKb == 1 ? 4 : kKb == 2 ? 2 : 1;
   static constexpr int kKRing = kQTile + kDTile, kVRing = kKRing + kKStages * kQTile;
   static constexpr int kUsed = kVRing + kVStages * kDTile;
-  // rows, K full/empty, V full/empty, S (two), dP, dP read, dS, done
-  static constexpr int kBars = 1 + 2 * kKStages + 2 * kVStages + 6;
+  // rows, K full/empty, V full/empty, S (two), dP, dP read, dS, drained (two), raw
+  static constexpr int kBars = 1 + 2 * kKStages + 2 * kVStages + 5 + 2 + 1;
   static constexpr int kSmem = kUsed + kBars * 8 + 16;
   static constexpr uint32_t kDp = kBufs * 128, kDq = kDp + 128;  // TMEM columns
   static_assert(kDq + kKb * 64 <= 512, "TMEM columns");
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
-constexpr int kDqThreads = (kBwdWarps + 2) * 32;
+constexpr int kDqThreads = (kBwdWarps + 3) * 32;
 
 template <int kKb, int kVb>
 __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_constant__ BwdParams P) {
@@ -435,13 +414,13 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
   const uint32_t rfull = smem_u32(bars), kfull0 = rfull + 8, kempty0 = kfull0 + 8 * C::kKStages;
   const uint32_t vfull0 = kempty0 + 8 * C::kKStages, vempty0 = vfull0 + 8 * C::kVStages;
   const uint32_t sfull0 = vempty0 + 8 * C::kVStages, dpfull = sfull0 + 16, dpread = dpfull + 8, dsready = dpread + 8;
-  const uint32_t done = dsready + 8;
+  const uint32_t done0 = dsready + 8, raw = done0 + 16;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 1 + 2 * C::kKStages + 2 * C::kVStages + 3; ++s) mbar_init(rfull + 8 * s, 1);
     mbar_init(dpread, kBwdWarps);
     mbar_init(dsready, kBwdWarps);
-    mbar_init(done, 1);
+    for (int s = 0; s < 3; ++s) mbar_init(done0 + 8 * s, 1);  // (and raw)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -470,84 +449,71 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
   const uint32_t qt = smem_u32(smem), dt = qt + C::kQTile, kring = qt + C::kKRing, vring = qt + C::kVRing;
   const AttnGuard guard = {abort_flag, P.status};
 
-  if (warp == kBwdWarps + 1) {
-    if (lane == 0 && steps > 0) {
-      uint32_t k_armed = 0, k_par = 0, v_armed = 0, v_par = 0;
-      mbar_expect_tx(rfull, (uint32_t)(A.kb + A.vb) * kAttnBlock);
-      for (int c = 0; c < A.kb; ++c) tma_load_4d(qt + c * kAttnBlock, &P.q, rfull, 64 * c, h0, t0, b);
-      for (int c = 0; c < A.vb; ++c) tma_load_4d(dt + c * kAttnBlock, &P.dy, rfull, 64 * c, h0, t0, b);
-      int ks = 0, vs = 0;
-      uint32_t kp = 0, vp = 0;
-      for (int i = 0; i < steps; ++i) {
-        const int k0 = (tk.j0 + i) * kAttnTile;
-        if (!guard.wait(kempty0 + 8 * ks, kp ^ 1)) break;
-        mbar_expect_tx(kfull0 + 8 * ks, (uint32_t)A.kb * kAttnBlock);
-        for (int c = 0; c < A.kb; ++c)
-          tma_load_4d(kring + ks * C::kQTile + c * kAttnBlock, &P.k, kfull0 + 8 * ks, 64 * c, kh, k0, b);
-        k_armed |= 1u << ks, k_par = (k_par & ~(1u << ks)) | (kp << ks);
-        if (++ks == C::kKStages) ks = 0, kp ^= 1;
-        if (!guard.wait(vempty0 + 8 * vs, vp ^ 1)) break;
-        mbar_expect_tx(vfull0 + 8 * vs, (uint32_t)A.vb * kAttnBlock);
-        for (int c = 0; c < A.vb; ++c)
-          tma_load_4d(vring + vs * C::kDTile + c * kAttnBlock, &P.v, vfull0 + 8 * vs, 64 * c, kh, k0, b);
-        v_armed |= 1u << vs, v_par = (v_par & ~(1u << vs)) | (vp << vs);
-        if (++vs == C::kVStages) vs = 0, vp ^= 1;
+  if (warp == kBwdWarps + 2) {
+    uint32_t raw_phase = 0;
+    TileRing K(kfull0, kempty0, kring, C::kQTile, C::kKStages), V(vfull0, vempty0, vring, C::kDTile, C::kVStages);
+    Armed rows;
+    if (steps > 0) {
+      if (elect_one()) {
+        mbar_expect_tx(rfull, (uint32_t)(A.kb + A.vb) * kAttnBlock);
+        for (int c = 0; c < A.kb; ++c) tma_load_4d(qt + c * kAttnBlock, &P.q, rfull, 64 * c, h0, t0, b);
+        for (int c = 0; c < A.vb; ++c) tma_load_4d(dt + c * kAttnBlock, &P.dy, rfull, 64 * c, h0, t0, b);
       }
-      if (guard.aborted()) {  // copies in flight land before shared memory goes away
-        (void)mbar_wait(rfull, 0);
-        for (int s = 0; s < C::kKStages; ++s)
-          if (k_armed >> s & 1u) (void)mbar_wait(kfull0 + 8 * s, k_par >> s & 1u);
-        for (int s = 0; s < C::kVStages; ++s)
-          if (v_armed >> s & 1u) (void)mbar_wait(vfull0 + 8 * s, v_par >> s & 1u);
-      }
+      __syncwarp();
+      rows.set(0, 0);
     }
+    for (int i = 0; i < steps; ++i) {
+      const int k0 = (tk.j0 + i) * kAttnTile;
+      const bool dirty = k0 < seq.k_lo || (k0 + kAttnTile > seq.k_hi && seq.k_hi < P.mask.sk);
+      if (!K.load(guard, &P.k, A.kb, kAttnBlock, kh, k0, b, dirty, raw, raw_phase, kAttnTile, seq.k_lo - k0, seq.k_hi - k0, lane))
+        break;
+      if (!V.load(guard, &P.v, A.vb, kAttnBlock, kh, k0, b, false, raw, raw_phase, 0, 0, 0, lane)) break;
+    }
+    if (guard.aborted()) rows.settle(rfull), K.armed.settle(kfull0), V.armed.settle(vfull0);
   } else if (warp == kBwdWarps) {
-    bool ok = steps > 0 && guard.wait_warp(rfull, 0);
+    // S ahead of dQ where there are two places for S, else behind it
+    RingAt K, behind;  // S's and dQ's tile of keys
     auto s_product = [&](int i) {
-      const int st = i % C::kKStages, k0 = (tk.j0 + i) * kAttnTile;
-      if (!guard.wait_warp(kfull0 + 8 * st, (i / C::kKStages) & 1)) return false;
-      const uint32_t k = kring + st * C::kQTile;
-      // keys that no row sees may hold anything, and 0 x NaN is not 0
-      if (k0 < seq.k_lo || (k0 + kAttnTile > seq.k_hi && seq.k_hi < P.mask.sk))
-        zero_rows(k, A.kb, kAttnTile, kAttnBlock, seq.k_lo - k0, seq.k_hi - k0, lane);
+      if (!guard.wait_warp(kfull0 + 8 * K.stage, K.phase)) return false;
       tc_fence_after();
       if (elect_one()) {
-        product_ss<kKb>(tmem + (i % C::kBufs) * 128, qt, k, A.k_steps, kAttnBlock, kAttnTile);
+        product_ss<kKb>(tmem + (i % C::kBufs) * 128, qt, kring + K.stage * C::kQTile, A.k_steps, kAttnBlock, kAttnTile);
         mma_commit_one(sfull0 + 8 * (i % C::kBufs));
       }
       __syncwarp();
+      K.next(C::kKStages);
       return true;
     };
-    auto dp_product = [&](int i) {
-      const int st = i % C::kVStages;
-      if (!guard.wait_warp(vfull0 + 8 * st, (i / C::kVStages) & 1)) return false;
-      if (i > 0 && !guard.wait_warp(dpread, (i - 1) & 1)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        product_ss<kVb>(tmem + C::kDp, dt, vring + st * C::kDTile, A.v_cols / 16, kAttnBlock, kAttnTile);
-        mma_commit_one(dpfull);
-        mma_commit_one(vempty0 + 8 * st);
-      }
-      __syncwarp();
-      return true;
-    };
-    if (ok) ok = s_product(0) && dp_product(0);
+    bool ok = steps > 0 && guard.wait_warp(rfull, 0) && s_product(0);
     for (int i = 0; i < steps && ok; ++i) {
-      if (i + 1 < steps) {
-        if (C::kBufs == 2 && !(ok = s_product(i + 1))) break;
-        if (!(ok = dp_product(i + 1))) break;
-      }
-      if (!(ok = guard.wait_warp(dsready, i & 1))) break;
+      if (C::kBufs == 2 && i + 1 < steps && !s_product(i + 1)) break;
+      if (!guard.wait_warp(dsready, i & 1)) break;
       tc_fence_after();
       if (elect_one()) {
-        product_ts<8>(tmem + C::kDq, tmem + (i % C::kBufs) * 128, 64, kring + (i % C::kKStages) * C::kQTile, kAttnBlock,
-                      A.k_steps * 16, i > 0);
-        mma_commit_one(kempty0 + 8 * (i % C::kKStages));
-        if (i + 1 == steps) mma_commit_one(done);
+        product_ts<8, 4>(tmem + C::kDq, tmem + (i % C::kBufs) * 128, 32, kring + behind.stage * C::kQTile, kAttnBlock,
+                         A.k_steps * 16, i > 0);
+        mma_commit_one(kempty0 + 8 * behind.stage);
       }
       __syncwarp();
+      behind.next(C::kKStages);
       if (C::kBufs == 1 && i + 1 < steps) ok = s_product(i + 1);
     }
+    drain_products(done0);
+  } else if (warp == kBwdWarps + 1) {
+    RingAt V;
+    bool ok = steps > 0 && guard.wait_warp(rfull, 0);
+    for (int i = 0; i < steps && ok; ++i) {
+      if (!guard.wait_warp(vfull0 + 8 * V.stage, V.phase) || (i > 0 && !guard.wait_warp(dpread, (i - 1) & 1))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        product_ss<kVb>(tmem + C::kDp, dt, vring + V.stage * C::kDTile, A.v_cols / 16, kAttnBlock, kAttnTile);
+        mma_commit_one(dpfull);
+        mma_commit_one(vempty0 + 8 * V.stage);
+      }
+      __syncwarp();
+      V.next(C::kVStages);
+    }
+    drain_products(done0 + 8);
   } else {
     const int grp = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -563,63 +529,52 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
     bool ok = true;
     for (int i = 0; i < steps; ++i) {
       const int buf = i % C::kBufs;
-      const uint32_t S = trow + buf * 128 + grp * 64, D = trow + C::kDp + grp * 64;
+      const uint32_t S = trow + buf * 128 + grp * 32, D = trow + C::kDp + grp * 32;
       if (!(ok = guard.wait_warp(sfull0 + 8 * buf, (i / C::kBufs) & 1))) break;
       tc_fence_after();
-      uint32_t r[64];
-      tmem_get(S, r);
-      tmem_get(S + 32, r + 32);
-      tmem_wait(r);
-      tmem_wait(r + 32);
+      uint32_t r[32], g[32], w[16];
+      tmem_read<32>(S, r);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
+      for (int c = 0; c < 32; c += 2) {
         const float2 x = f2_fma(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), c2, nl);
         r[c] = __float_as_uint(ex2(x.x)), r[c + 1] = __float_as_uint(ex2(x.y));
       }
       if (!(ok = guard.wait_warp(dpfull, i & 1))) break;
       tc_fence_after();
-      uint32_t g[64];
-      tmem_get(D, g);
-      tmem_get(D + 32, g + 32);
-      tmem_wait(g);
-      tmem_wait(g + 32);
+      tmem_read<32>(D, g);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(dpread);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
+      for (int c = 0; c < 32; c += 2) {
         float2 x = f2_add(make_float2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), nd);
         x = f2_mul(x, make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])));
         g[c] = __float_as_uint(x.x), g[c + 1] = __float_as_uint(x.y);
       }
       if (tk.masked(tk.j0 + i)) {
-        const int lo = keys.lo - (tk.j0 + i) * kAttnTile - grp * 64, hi = keys.hi - (tk.j0 + i) * kAttnTile - grp * 64;
+        const int lo = keys.lo - (tk.j0 + i) * kAttnTile - grp * 32, hi = keys.hi - (tk.j0 + i) * kAttnTile - grp * 32;
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
+        for (int c = 0; c < 32; ++c)
           if (c < lo || c >= hi) g[c] = 0u;
       }
-      uint32_t w[32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) w[c] = pack_bf16(__uint_as_float(g[2 * c]), __uint_as_float(g[2 * c + 1]));
-      tmem_put(S, w);
+      for (int c = 0; c < 16; ++c) w[c] = pack_bf16(__uint_as_float(g[2 * c]), __uint_as_float(g[2 * c + 1]));
+      tmem_write<32>(S, w);
       tmem_put_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(dsready);
     }
-    if (ok && steps > 0) ok = guard.wait_warp(done, 0);
+    if (ok) ok = guard.wait_warp(done0, 0);
     tc_fence_after();
     if (ok) {
       const int r0 = (warp & 3) * 32;
-      for (int blk = grp; blk < A.kb; blk += 2) {  // through the queries' place
+      for (int blk = grp; blk < A.kb; blk += 4) {  // through the queries' place
 #pragma unroll 1
         for (int c = blk * 64; c < blk * 64 + 64; c += 32) {
           uint32_t r[32];
           float v[32];
-          if (steps > 0) {
-            tmem_get(trow + C::kDq + c, r);
-            tmem_wait(r);
-          }
+          if (steps > 0) tmem_read<32>(trow + C::kDq + c, r);
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = steps > 0 && live ? __uint_as_float(r[e]) * A.scale : 0.f;
           put_tile_row(qt, row, c, v);

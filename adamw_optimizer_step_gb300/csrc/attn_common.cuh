@@ -134,6 +134,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 __device__ __forceinline__ uint64_t as_bits(float2 a) { return *reinterpret_cast<uint64_t *>(&a); }
 __device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
   uint64_t d;
@@ -191,6 +197,37 @@ __device__ __forceinline__ void tmem_wait(uint32_t *r) {
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_get16(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait16(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// kCols (16, 32 or 64) columns, waited for.
+template <int kCols>
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[kCols]) {
+  if constexpr (kCols == 16) {
+    tmem_get16(taddr, r);
+    tmem_wait16(r);
+  } else {
+#pragma unroll
+    for (int c = 0; c < kCols; c += 32) tmem_get(taddr + c, r + c);
+#pragma unroll
+    for (int c = 0; c < kCols; c += 32) tmem_wait(r + c);
+  }
+}
+
 __device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -210,6 +247,20 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t *r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_put8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// kCols values as bf16 pairs in kCols / 2 columns.
+template <int kCols>
+__device__ __forceinline__ void tmem_write(uint32_t taddr, const uint32_t (&r)[kCols / 2]) {
+  if constexpr (kCols == 16) tmem_put8(taddr, r);
+  else if constexpr (kCols == 32) tmem_put16(taddr, r);
+  else tmem_put(taddr, r);
 }
 
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -283,17 +334,18 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a, uint32_t b, i
     if (4 * c < steps) product_block(d, a + c * kAttnBlock, b + c * b_block, min(4, steps - 4 * c), idesc, c > 0);
 }
 
-// D (+)= A B over kSteps steps of K = 16, A in TMEM from column a on, B with K along
-// its rows (MN-major) in blocks of 64 columns of b_block bytes, n columns in all.
-// The second half of A's steps stands a_second columns after the first's start.
-template <int kSteps>
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t a_second, uint32_t b, uint32_t b_block, int n,
+// D (+)= A B over kSteps steps of K = 16, A in TMEM, B with K along its rows
+// (MN-major) in blocks of 64 columns of b_block bytes, n columns in all.  A was
+// written by kParts warps, each to the start of its own part_stride columns.
+template <int kSteps, int kParts>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t part_stride, uint32_t b, uint32_t b_block, int n,
                                            bool accumulate) {
+  constexpr int kEach = kSteps / kParts;
   const uint32_t idesc = attn_idesc(true, n);
   const uint32_t bl = desc_low(b, b_block);
 #pragma unroll
   for (int k = 0; k < kSteps; ++k)
-    mma_ts(d, a + (k < kSteps / 2 ? k * 8 : a_second + (k - kSteps / 2) * 8), bl + k * (2048 >> 4), idesc, accumulate || k > 0);
+    mma_ts(d, a + (k / kEach) * part_stride + (k % kEach) * 8, bl + k * (2048 >> 4), idesc, accumulate || k > 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -339,6 +391,81 @@ struct AttnGuard {
     }
   }
   __device__ __forceinline__ bool aborted() const { return *abort_flag != 0; }
+};
+
+// Stages of a ring whose copies were started: after a wait that ran out, they
+// land (or run out of time, too) before shared memory goes away.
+struct Armed {
+  uint32_t mask = 0, parity = 0;
+  __device__ __forceinline__ void set(int stage, uint32_t phase) {
+    mask |= 1u << stage;
+    parity = (parity & ~(1u << stage)) | (phase << stage);
+  }
+  __device__ __forceinline__ void settle(uint32_t bars) const {
+    for (int s = 0; s < 32; ++s)
+      if (mask >> s & 1u) (void)mbar_wait(bars + 8 * s, parity >> s & 1u);
+  }
+};
+
+// Wait until every product this warp's elected lane has issued is done: nothing
+// reads shared memory or writes TMEM when the CTA goes on to give them up.
+__device__ __forceinline__ void drain_products(uint32_t bar) {
+  if (elect_one()) mma_commit_one(bar);
+  __syncwarp();
+  (void)mbar_wait(bar, 0);
+  __syncwarp();
+}
+
+__device__ __forceinline__ void zero_rows(uint32_t tile, int blocks, int rows, uint32_t block_bytes, int lo, int hi, int lane);
+
+// A ring of tiles that one warp fills by TMA and that tensor cores read.  A tile
+// with rows that reach nothing (of which one may hold anything, and 0 x NaN is
+// not 0) is loaded through a barrier of its own and those rows are zeroed before
+// the tile counts as loaded.
+struct TileRing {
+  uint32_t full, empty, base, bytes;  // barriers, first tile, bytes from tile to tile
+  int stages, stage = 0;
+  uint32_t phase = 0;
+  Armed armed;
+
+  __device__ __forceinline__ TileRing(uint32_t full_, uint32_t empty_, uint32_t base_, uint32_t bytes_, int stages_)
+      : full(full_), empty(empty_), base(base_), bytes(bytes_), stages(stages_) {}
+
+  // All lanes of the warp; false when a wait ran out.
+  __device__ __forceinline__ bool load(const AttnGuard &guard, const CUtensorMap *map, int blocks, uint32_t block_bytes, int head,
+                                       int token, int batch, bool dirty, uint32_t raw, uint32_t &raw_phase, int rows, int lo,
+                                       int hi, int lane) {
+    if (!guard.wait_warp(empty + 8 * stage, phase ^ 1)) return false;
+    const uint32_t bar = dirty ? raw : full + 8 * stage, tile = base + stage * bytes;
+    if (elect_one()) {
+      mbar_expect_tx(bar, (uint32_t)blocks * block_bytes);
+      for (int c = 0; c < blocks; ++c) tma_load_4d(tile + c * block_bytes, map, bar, 64 * c, head, token, batch);
+    }
+    __syncwarp();
+    if (dirty) {
+      if (!guard.wait_warp(raw, raw_phase)) {
+        (void)mbar_wait(raw, raw_phase);
+        return false;
+      }
+      raw_phase ^= 1;
+      zero_rows(tile, blocks, rows, block_bytes, lo, hi, lane);
+      if (elect_one()) mbar_arrive(full + 8 * stage);
+      __syncwarp();
+    } else {
+      armed.set(stage, phase);
+    }
+    if (++stage == stages) stage = 0, phase ^= 1;
+    return true;
+  }
+};
+
+// A reader's place in such a ring.
+struct RingAt {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) stage = 0, phase ^= 1;
+  }
 };
 
 // Zero the rows outside [lo, hi) of a tile of `rows` rows in `blocks` blocks of 64

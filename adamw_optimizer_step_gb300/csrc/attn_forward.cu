@@ -8,8 +8,8 @@
 // attn_forward_kernel.  A CTA holds two tiles of 128 rows (heads of consecutive
 // tokens, see AttnShape) and streams their keys and values in tiles of 128.
 // Per tile of rows and of keys: S = Q K^T (TMEM), P = 2^(S c - m) with c =
-// scale log2(e) by the four warps of the row tile, a row to a thread, back into
-// TMEM in bf16 over S, O += P V (TMEM).  While the softmax of one row tile
+// scale log2(e) by the eight warps of the row tile, half a row to a thread, back
+// into TMEM in bf16 over S, O += P V (TMEM).  While the softmax of one row tile
 // runs, the tensor cores work for the other: PV0(j-1) S0(j) PV1(j-1) S1(j).
 // m is a running maximum that is moved, and O rescaled, only when a row's
 // maximum grows by more than 2^8: until then P is at most 2^8 and its rounding
@@ -21,18 +21,21 @@ namespace gbo {
 
 namespace {
 
-constexpr int kFwdSoftWarps = 8;
-constexpr int kFwdThreads = (kFwdSoftWarps + 2) * 32;
+constexpr int kFwdSoftWarps = 16;  // for each row tile two groups of four, each half of the keys
+constexpr int kFwdThreads = (kFwdSoftWarps + 3) * 32;
 constexpr float kRescale = 8.f;  // in bits
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int kKb, int kVb>
 struct Fwd {
-  static constexpr int kQTile = kKb * kAttnBlock;
-  static constexpr int kRing = kKb == 3 ? 8 : 10;  // blocks of keys and values
-  static constexpr int kUsed = 2 * kQTile + kRing * kAttnBlock;
-  static constexpr int kBars = 2 + 2 * kRing + 6;
-  static constexpr int kSmem = 1024 + kUsed + kBars * 8 + 16;
+  static constexpr int kQTile = kKb * kAttnBlock, kVTile = kVb * kAttnBlock;  // (a tile of keys is as large as one of queries)
+  static constexpr int kKStages = kKb == 1 ? 5 : kKb == 2 ? 3 : 2, kVStages = kKb == 1 ? 5 : kKb == 2 ? 2 : 1;
+  static constexpr int kKRing = 2 * kQTile, kVRing = kKRing + kKStages * kQTile;
+  static constexpr int kUsed = kVRing + kVStages * kVTile;
+  // queries (two), keys and values full/empty, raw, S, P, O (two each), pairs of warps, drained (two)
+  static constexpr int kBars = 2 + 2 * kKStages + 2 * kVStages + 1 + 6 + 8 + 2;
+  static constexpr int kHalves = 2 * 2 * kAttnTile * 4;  // half of the keys, row tile, row: a float
+  static constexpr int kSmem = kUsed + kHalves + kBars * 8 + 16;
   static constexpr uint32_t kO = 256;  // TMEM: S0, S1 of 128 columns, O0, O1 of kVb * 64
   static constexpr uint32_t kCols = 512;
   static_assert(kVb * kAttnBlock <= kQTile, "the output leaves through the queries' place");
@@ -55,21 +58,34 @@ template <int kKb, int kVb>
 __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __grid_constant__ FwdParams P) {
   using C = Fwd<kKb, kVb>;
   pdl_launch();
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kUsed);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float *const halves = reinterpret_cast<float *>(smem + C::kUsed);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kUsed + C::kHalves);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
-  const uint32_t qfull0 = smem_u32(bars), full0 = qfull0 + 16, empty0 = full0 + 8 * C::kRing;
-  const uint32_t sfull0 = empty0 + 8 * C::kRing, pready0 = sfull0 + 16, odone0 = pready0 + 16;
+  const uint32_t qfull0 = smem_u32(bars), kfull0 = qfull0 + 16, kempty0 = kfull0 + 8 * C::kKStages;
+  const uint32_t vfull0 = kempty0 + 8 * C::kKStages, vempty0 = vfull0 + 8 * C::kVStages, raw = vempty0 + 8 * C::kVStages;
+  const uint32_t sfull0 = raw + 8, pready0 = sfull0 + 16, odone0 = pready0 + 16, pair0 = odone0 + 16;
+  const uint32_t drain0 = pair0 + 64;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 + 2 * C::kRing; ++s) mbar_init(qfull0 + 8 * s, 1);
+    for (int s = 0; s < 2; ++s) mbar_init(qfull0 + 8 * s, 1);
+    for (int s = 0; s < C::kKStages; ++s) {
+      mbar_init(kfull0 + 8 * s, 1);
+      mbar_init(kempty0 + 8 * s, 2);  // both row tiles
+    }
+    for (int s = 0; s < C::kVStages; ++s) {
+      mbar_init(vfull0 + 8 * s, 1);
+      mbar_init(vempty0 + 8 * s, 2);
+    }
+    mbar_init(raw, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(sfull0 + 8 * t, 1);
-      mbar_init(pready0 + 8 * t, 4);
+      mbar_init(pready0 + 8 * t, 8);
       mbar_init(odone0 + 8 * t, 1);
     }
+    for (int t = 0; t < 8; ++t) mbar_init(pair0 + 8 * t, 2);
+    for (int t = 0; t < 2; ++t) mbar_init(drain0 + 8 * t, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -115,109 +131,86 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
       tk[t].j1 = max(tk[t].j0, min(tk[t].j1, J1));
     }
   }
-  const uint32_t q0 = smem_u32(smem), ring0 = q0 + 2 * C::kQTile;
+  const uint32_t q0 = smem_u32(smem), kring = q0 + C::kKRing, vring = q0 + C::kVRing;
   const AttnGuard guard = {abort_flag, P.status};
-  const int per = A.kb + A.vb;  // ring blocks of one tile of keys and values
 
-  if (warp == kFwdSoftWarps + 1) {
-    if (lane == 0) {
-      uint32_t armed = 0, parity = 0;
-      for (int t = 0; t < 2; ++t)
-        if (tk[t].j1 > tk[t].j0) {
+  if (warp == kFwdSoftWarps + 2) {
+    uint32_t raw_phase = 0;
+    TileRing K(kfull0, kempty0, kring, C::kQTile, C::kKStages), V(vfull0, vempty0, vring, C::kVTile, C::kVStages);
+    Armed q;
+    for (int t = 0; t < 2; ++t)
+      if (tk[t].j1 > tk[t].j0) {
+        if (elect_one()) {
           mbar_expect_tx(qfull0 + 8 * t, (uint32_t)A.kb * kAttnBlock);
           for (int c = 0; c < A.kb; ++c)
             tma_load_4d(q0 + t * C::kQTile + c * kAttnBlock, &P.q, qfull0 + 8 * t, 64 * c, h0, t0 + t * tokens, b);
         }
-      int slot = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int j = J0; ok && j < J1; ++j)
-        for (int c = 0; c < per; ++c) {
-          if (!(ok = guard.wait(empty0 + 8 * slot, phase ^ 1))) break;
-          mbar_expect_tx(full0 + 8 * slot, kAttnBlock);
-          const bool key = c < A.kb;
-          tma_load_4d(ring0 + slot * kAttnBlock, key ? &P.k : &P.v, full0 + 8 * slot, 64 * (key ? c : c - A.kb), kh,
-                      j * kAttnTile, b);
-          armed |= 1u << slot;
-          parity = (parity & ~(1u << slot)) | (phase << slot);
-          if (++slot == C::kRing) slot = 0, phase ^= 1;
-        }
-      if (guard.aborted()) {  // copies in flight land before shared memory goes away
-        for (int t = 0; t < 2; ++t)
-          if (tk[t].j1 > tk[t].j0) (void)mbar_wait(qfull0 + 8 * t, 0);
-        for (int s = 0; s < C::kRing; ++s)
-          if (armed >> s & 1u) (void)mbar_wait(full0 + 8 * s, parity >> s & 1u);
+        __syncwarp();
+        q.set(t, 0);
       }
+    for (int j = J0; j < J1; ++j) {
+      const int k0 = j * kAttnTile;
+      if (!K.load(guard, &P.k, A.kb, kAttnBlock, kh, k0, b, false, raw, raw_phase, 0, 0, 0, lane)) break;
+      const bool dirty = k0 < seq.k_lo || (k0 + kAttnTile > seq.k_hi && seq.k_hi < P.mask.sk);
+      if (!V.load(guard, &P.v, A.vb, kAttnBlock, kh, k0, b, dirty, raw, raw_phase, kAttnTile, seq.k_lo - k0, seq.k_hi - k0, lane))
+        break;
     }
-  } else if (warp == kFwdSoftWarps) {
-    // Steps j: PV of tile j - 1 and S of tile j, for one row tile and then the
-    // other.  P stands over S, and products run in order, so S(j) may be issued
-    // right behind PV(j - 1).
-    bool ok = true, q_here[2] = {false, false};
-    uint32_t np[2] = {0, 0};
-    auto wait_blocks = [&](int first, int count) {
-      for (int c = 0; c < count && ok; ++c) ok = guard.wait_warp(full0 + 8 * ((first + c) % C::kRing), ((first + c) / C::kRing) & 1);
-    };
-    auto release = [&](int first, int count) {
-      if (elect_one())
-        for (int c = 0; c < count; ++c) mma_commit_one(empty0 + 8 * ((first + c) % C::kRing));
-    };
-    for (int j = J0; j <= J1 && J1 > J0 && ok; ++j) {
-      const int kpos = (j - J0) * per, vpos = kpos - per + A.kb;
-      const bool pv = j > J0, sc = j < J1;
-      if (pv) {
-        wait_blocks(vpos, A.vb);
-        if (!ok) break;
-        const int k0 = (j - 1) * kAttnTile;
-        if (k0 < seq.k_lo || (k0 + kAttnTile > seq.k_hi && seq.k_hi < P.mask.sk))
-          for (int c = 0; c < A.vb; ++c)
-            zero_rows(ring0 + ((vpos + c) % C::kRing) * kAttnBlock, 1, kAttnTile, kAttnBlock, seq.k_lo - k0, seq.k_hi - k0, lane);
-      }
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (pv && tk[t].has(j - 1)) {
-          if (!(ok = guard.wait_warp(pready0 + 8 * t, np[t] & 1))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const int slot = vpos % C::kRing;
-            const uint32_t o = tmem + C::kO + t * kVb * 64, p = tmem + t * 128, v = ring0 + slot * kAttnBlock;
-            if (A.vb == 1 || slot + 1 < C::kRing) {
-              product_ts<8>(o, p, 64, v, kAttnBlock, A.v_cols, np[t] > 0);
-            } else {  // the values' two blocks lie at the ring's ends
-              product_ts<8>(o, p, 64, v, kAttnBlock, 64, np[t] > 0);
-              product_ts<8>(o + 64, p, 64, ring0, kAttnBlock, A.v_cols - 64, np[t] > 0);
-            }
+    if (guard.aborted()) q.settle(qfull0), K.armed.settle(kfull0), V.armed.settle(vfull0);
+  } else if (warp >= kFwdSoftWarps) {
+    // The tensor cores' work for row tile t: PV(j - 1), then S(j); P stands over S,
+    // and one thread's products run in order.  Each tile has a warp of its own, so
+    // that one's waits lie beside the other's products.
+    const int t = warp - kFwdSoftWarps;
+    const uint32_t S = tmem + t * 128, O = tmem + C::kO + t * kVb * 64, q = q0 + t * C::kQTile;
+    bool started = false;
+    uint32_t np = 0;
+    RingAt K, V;
+    for (int j = J0; j <= J1 && J1 > J0; ++j) {
+      if (j > J0) {
+        if (!guard.wait_warp(vfull0 + 8 * V.stage, V.phase)) break;
+        const bool mine = tk[t].has(j - 1);
+        if (mine && !guard.wait_warp(pready0 + 8 * t, np & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (mine) {
+            product_ts<8, 2>(O, S, 64, vring + V.stage * C::kVTile, kAttnBlock, A.v_cols, np > 0);
             mma_commit_one(odone0 + 8 * t);
+            mma_commit_one(vempty0 + 8 * V.stage);
+          } else {
+            mbar_arrive(vempty0 + 8 * V.stage);
           }
-          __syncwarp();
-          ++np[t];
         }
-        if (sc && tk[t].has(j)) {
-          if (t == 0 || !tk[0].has(j)) wait_blocks(kpos, A.kb);
-          if (ok && !q_here[t]) ok = guard.wait_warp(qfull0 + 8 * t, 0);
-          if (!ok) break;
-          q_here[t] = true;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t idesc = attn_idesc(false, kAttnTile);
-#pragma unroll
-            for (int c = 0; c < kKb; ++c)
-              if (c < A.kb)
-                product_block(tmem + t * 128, q0 + t * C::kQTile + c * kAttnBlock, ring0 + ((kpos + c) % C::kRing) * kAttnBlock,
-                              min(4, A.k_steps - 4 * c), idesc, c > 0);
-            mma_commit_one(sfull0 + 8 * t);
-          }
-          __syncwarp();
-        }
+        __syncwarp();
+        np += mine;
+        V.next(C::kVStages);
       }
-      if (!ok) break;
-      if (sc) wait_blocks(kpos, A.kb);  // (a tile no row sees)
-      if (pv) release(vpos, A.vb);
-      if (sc) release(kpos, A.kb);
+      if (j < J1) {
+        if (!guard.wait_warp(kfull0 + 8 * K.stage, K.phase)) break;
+        const bool mine = tk[t].has(j);
+        if (mine && !started && !guard.wait_warp(qfull0 + 8 * t, 0)) break;
+        started |= mine;
+        tc_fence_after();
+        if (elect_one()) {
+          if (mine) {
+            product_ss<kKb>(S, q, kring + K.stage * C::kQTile, A.k_steps, kAttnBlock, kAttnTile);
+            mma_commit_one(sfull0 + 8 * t);
+            mma_commit_one(kempty0 + 8 * K.stage);
+          } else {
+            mbar_arrive(kempty0 + 8 * K.stage);
+          }
+        }
+        __syncwarp();
+        K.next(C::kKStages);
+      }
     }
+    drain_products(drain0 + 8 * t);
   } else {
-    const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+    // Rows of tile t, keys 64 half .. of each of its key tiles.  The two warps of
+    // a row exchange their maxima, and their sums at the end.
+    const int t = warp >> 3, half = warp >> 2 & 1, row = (warp & 3) * 32 + lane;
+    const uint32_t pair = pair0 + 8 * (t * 4 + (warp & 3));
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t S = trow + t * 128, O = trow + C::kO + t * kVb * 64;
+    const uint32_t S = trow + t * 128 + half * 64, O = trow + C::kO + t * kVb * 64;
     const int token = t0 + t * tokens + (row >> A.pack), head = h0 + (row & ((1 << A.pack) - 1));
     const bool live = token >= seq.q_lo && token < seq.q_hi;
     Span keys = {0, 0};
@@ -225,28 +218,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     int n = 0;
+    float *const my_slot = halves + (half * 2 + t) * kAttnTile + row;
+    const float *const their_slot = halves + ((half ^ 1) * 2 + t) * kAttnTile + row;
+    // This row's value of the other warp.  A slot is written again only after
+    // products that waited for both warps' P, and so for their reads.
+    auto exchange = [&](float v, int turn, float &other) {
+      *my_slot = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      if (!guard.wait_warp(pair, turn & 1)) return false;
+      other = *their_slot;
+      return true;
+    };
     for (int j = tk[t].j0; j < tk[t].j1; ++j, ++n) {
       if (!(ok = guard.wait_warp(sfull0 + 8 * t, n & 1))) break;
       tc_fence_after();
-      uint32_t r[128];
+      const bool masked = tk[t].masked(j);
+      const int lo = keys.lo - j * kAttnTile - half * 64, hi = keys.hi - j * kAttnTile - half * 64;
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      {
+        uint32_t r[64];
+        tmem_read<64>(S, r);
+        if (masked) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_get(S + 32 * c, r + 32 * c);
+          for (int c = 0; c < 64; ++c)
+            if (c < lo || c >= hi) r[c] = 0xff800000u;  // -inf
+        }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_wait(r + 32 * c);
-      if (tk[t].masked(j)) {
-        const int lo = keys.lo - j * kAttnTile, hi = keys.hi - j * kAttnTile;
+        for (int c = 0; c < 64; c += 8)
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c < lo || c >= hi) r[c] = 0xff800000u;  // -inf
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(r[c + e]), __uint_as_float(r[c + e + 4]));
       }
-      float mx[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(r[c]), __uint_as_float(r[4 + c]));
-#pragma unroll
-      for (int c = 8; c < 128; c += 4)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(r[c + e]));
-      const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.scale2);
+      float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), theirs;
+      if (!(ok = exchange(mine, n, theirs))) break;
+      const float mn = fmaxf(m, fmaxf(mine, theirs) * A.scale2);
       if (__any_sync(0xffffffffu, mn > m + kRescale)) {
         const float a = ex2(m - (mn == -INFINITY ? 0.f : mn));  // (m = -inf: 0)
         l *= a;
@@ -255,32 +260,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
           if (!(ok = guard.wait_warp(odone0 + 8 * t, (n - 1) & 1))) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < A.vb * 64; c += 32) {
+          for (int c = half * 32; c < A.vb * 64; c += 64) {
             uint32_t o[32];
-            tmem_get(O + c, o);
-            tmem_wait(o);
+            tmem_read<32>(O + c, o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
             tmem_put(O + c, o);
           }
         }
       }
-      const float2 c2 = make_float2(A.scale2, A.scale2), at2 = [&] {
-        const float at = m == -INFINITY ? 0.f : -m;
-        return make_float2(at, at);
-      }();
+      const float at = m == -INFINITY ? 0.f : -m;
+      const float2 c2 = make_float2(A.scale2, A.scale2), at2 = make_float2(at, at);
       float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
+        uint32_t r[32], p[16];
+        tmem_read<32>(S + 32 * h, r);
+        if (masked) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float2 x = f2_fma(make_float2(__uint_as_float(r[64 * h + 2 * c]), __uint_as_float(r[64 * h + 2 * c + 1])), c2, at2);
+          for (int c = 0; c < 32; ++c)
+            if (32 * h + c < lo || 32 * h + c >= hi) r[c] = 0xff800000u;
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float2 x = f2_fma(make_float2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), c2, at2);
           x.x = ex2(x.x), x.y = ex2(x.y);
           sum[c & 1] = f2_add(sum[c & 1], x);
           p[c] = pack_bf16(x.x, x.y);
         }
-        tmem_put(S + 64 * h, p);
+        tmem_put16(S + 16 * h, p);
       }
       const float2 both = f2_add(sum[0], sum[1]);
       l += both.x + both.y;
@@ -289,7 +297,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
       __syncwarp();
       if (lane == 0) mbar_arrive(pready0 + 8 * t);
     }
-    if (ok && n > 0) ok = guard.wait_warp(odone0 + 8 * t, (n - 1) & 1);
+    if (ok && n > 0) {
+      float theirs = 0.f;
+      ok = guard.wait_warp(odone0 + 8 * t, (n - 1) & 1) && exchange(l, n, theirs);
+      l += theirs;
+    }
     tc_fence_after();
     if (ok && t0 + t * tokens < P.mask.sq) {
       const bool in = token < P.mask.sq;
@@ -297,40 +309,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
       // (a sum of 0 is a row that sees nothing; NaN stays)
       const float inv = live && l != 0.f ? 1.f / l : 0.f;
       if (P.splits == 1) {
-        if (in && P.lse) P.lse[at] = live ? m * kLn2 + logf(l) : -INFINITY;
+        if (in && P.lse && half == 0) P.lse[at] = live ? m * kLn2 + logf(l) : -INFINITY;
         const uint32_t out = q0 + t * C::kQTile;  // the queries have been read
+        for (int blk = half; blk < A.vb; blk += 2) {  // 64 columns
 #pragma unroll 1
-        for (int c = 0; c < A.vb * 64; c += 32) {
-          uint32_t o[32];
-          float f[32];
-          if (n > 0) {
-            tmem_get(O + c, o);
-            tmem_wait(o);
-          }
+          for (int c = blk * 64; c < blk * 64 + 64; c += 32) {
+            uint32_t o[32];
+            float f[32];
+            if (n > 0) tmem_read<32>(O + c, o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] = n > 0 && inv != 0.f ? __uint_as_float(o[e]) * inv : 0.f;
-          put_tile_row(out, row, c, f);
+            for (int e = 0; e < 32; ++e) f[e] = n > 0 && inv != 0.f ? __uint_as_float(o[e]) * inv : 0.f;
+            put_tile_row(out, row, c, f);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int r0 = (warp & 3) * 32;  // this warp's rows
+            tma_store_4d(&P.y, out + blk * kAttnBlock + r0 * 128, 64 * blk, h0, t0 + t * tokens + (r0 >> A.pack), b);
+            bulk_commit();
+            bulk_wait_all();
+          }
+          __syncwarp();
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          const int r0 = (warp & 3) * 32;  // this warp's rows
-          for (int c = 0; c < A.vb; ++c)
-            tma_store_4d(&P.y, out + c * kAttnBlock + r0 * 128, 64 * c, h0, t0 + t * tokens + (r0 >> A.pack), b);
-          bulk_commit();
-          bulk_wait_all();
-        }
-        __syncwarp();
       } else {
-        if (in) P.part_lse[split * P.rows + at] = live && l != 0.f ? m + log2f(l) : -INFINITY;
+        if (in && half == 0) P.part_lse[split * P.rows + at] = live && l != 0.f ? m + log2f(l) : -INFINITY;
         float *dst = P.part_o + (split * P.rows + at) * A.dv;
 #pragma unroll 1
-        for (int c = 0; c < A.dv; c += 32) {
+        for (int c = half * 32; c < A.dv; c += 64) {
           uint32_t o[32];
-          if (n > 0) {
-            tmem_get(O + c, o);
-            tmem_wait(o);
-          }
+          if (n > 0) tmem_read<32>(O + c, o);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             if (in && c + 4 * q < A.dv) {
@@ -370,7 +377,7 @@ struct Tok {
   static constexpr int kStages = kKb == 1 ? 6 : kKb == 2 ? 3 : 2;
   static constexpr int kJoin = kTokWarps * 16 * (kVb * 64 + 4) * 4;  // outputs, maxima and sums of the warps
   static constexpr int kUsed = kStages * kStage > kJoin ? kStages * kStage : kJoin;
-  static constexpr int kSmem = 1024 + kUsed + (2 * kStages) * 8 + 16;
+  static constexpr int kSmem = kUsed + (2 * kStages) * 8 + 16;
   static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
 };
 
@@ -415,8 +422,7 @@ template <int kKb, int kVb>
 __global__ void __launch_bounds__(kTokThreads, 2) attn_token_kernel(const __grid_constant__ TokParams P) {
   using C = Tok<kKb, kVb>;
   pdl_launch();
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kUsed);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(bars + 2 * C::kStages);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::kStages, ring0 = smem_u32(smem);
