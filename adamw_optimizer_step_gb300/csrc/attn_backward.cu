@@ -88,8 +88,8 @@ struct Dkv {
   static constexpr int kQStages = 3, kDStages = kKb == 2 ? 2 : 3, kStats = 2;
   static constexpr int kRing = kKTile + kVTile, kStatAt = kRing + kQStages * kQStage + kDStages * kDStage;
   static constexpr int kUsed = kStatAt + kStats * kQt * 8;
-  // kv, q full/empty, dy full/empty, stats full/empty, S, P, dP, dS, drained (two), raw
-  static constexpr int kBars = 1 + 2 * kQStages + 2 * kDStages + 2 * kStats + 4 + 2 + 1;
+  // kv, q full/empty, dy full/empty, stats full/empty, S, P, dP, dS, drained (two), raw, turns (two)
+  static constexpr int kBars = 1 + 2 * kQStages + 2 * kDStages + 2 * kStats + 4 + 2 + 1 + 2;
   static constexpr int kSmem = kUsed + kBars * 8 + 16;
   static constexpr uint32_t kDp = kQt, kDv = 2 * kQt, kDk = 2 * kQt + kVb * 64;  // TMEM columns
   static_assert(kDk + kKb * 64 <= 512, "TMEM columns");
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
   const uint32_t dfull0 = qempty0 + 8 * C::kQStages, dempty0 = dfull0 + 8 * C::kDStages;
   const uint32_t tfull0 = dempty0 + 8 * C::kDStages, tempty0 = tfull0 + 8 * C::kStats;
   const uint32_t sfull = tempty0 + 8 * C::kStats, pready = sfull + 8, dpfull = pready + 8, dsready = dpfull + 8;
-  const uint32_t done0 = dsready + 8, raw = done0 + 16;
+  const uint32_t done0 = dsready + 8, raw = done0 + 16, turn0 = raw + 8;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 1 + 2 * C::kQStages + C::kDStages; ++s) mbar_init(kvfull + 8 * s, 1);
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
     mbar_init(pready, kBwdWarps);
     mbar_init(dpfull, 1);
     mbar_init(dsready, kBwdWarps);
-    for (int s = 0; s < 3; ++s) mbar_init(done0 + 8 * s, 1);  // (and raw)
+    for (int s = 0; s < 5; ++s) mbar_init(done0 + 8 * s, 1);  // (and raw and turns)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -210,60 +210,59 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
       if (++tt == n_tok) tt = 0, ++hb;
     }
   } else if (warp == kBwdWarps) {
-    // S(i + 1) behind dV(i), whose P stands over S(i)
+    // S(i + 1) behind dV(i), whose P stands over S(i).  The two issuing warps take
+    // turns, so that S(i + 1) is not held up by dK(i) and dP(i + 1).
     RingAt Q, D;
+    uint32_t turn = 1;
     bool ok = steps > 0 && guard.wait_warp(kvfull, 0);
     for (int i = 0; i <= steps && ok; ++i) {
-      if (i > 0) {
-        if (!guard.wait_warp(dfull0 + 8 * D.stage, D.phase) || !guard.wait_warp(pready, (i - 1) & 1)) break;
-        tc_fence_after();
-        if (elect_one()) {
+      if (i < steps && !guard.wait_warp(qfull0 + 8 * Q.stage, Q.phase)) break;
+      if (i > 0 && (!guard.wait_warp(dfull0 + 8 * D.stage, D.phase) || !guard.wait_warp(pready, (i - 1) & 1))) break;
+      if (!guard.wait_warp(turn0, turn)) break;
+      turn ^= 1;
+      tc_fence_after();
+      if (elect_one()) {
+        if (i > 0) {
           product_ts<kQt / 16, 4>(tmem + C::kDv, tmem, kQt / 4, dring + D.stage * C::kDStage, C::kQBlock, A.v_cols, i > 1);
           mma_commit_one(dempty0 + 8 * D.stage);
         }
-        __syncwarp();
-        D.next(C::kDStages);
+        if (i < steps) product_ss<kKb>(tmem, kt, qring + Q.stage * C::kQStage, A.k_steps, C::kQBlock, kQt);
+        mbar_arrive(turn0 + 8);
+        if (i < steps) mma_commit_one(sfull);
       }
-      if (i < steps) {
-        if (!guard.wait_warp(qfull0 + 8 * Q.stage, Q.phase)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          product_ss<kKb>(tmem, kt, qring + Q.stage * C::kQStage, A.k_steps, C::kQBlock, kQt);
-          mma_commit_one(sfull);
-        }
-        __syncwarp();
-        Q.next(C::kQStages);
-      }
+      __syncwarp();
+      if (i > 0) D.next(C::kDStages);
+      if (i < steps) Q.next(C::kQStages);
     }
     drain_products(done0);
   } else if (warp == kBwdWarps + 1) {
     // dP(i + 1) behind dK(i), whose dS stands over dP(i); that is the last to read
     // the queries' tile
     RingAt Q, D;
+    uint32_t turn = 0;
     bool ok = steps > 0 && guard.wait_warp(kvfull, 0);
     for (int i = 0; i <= steps && ok; ++i) {
-      if (i > 0) {
-        if (!guard.wait_warp(qfull0 + 8 * Q.stage, Q.phase) || !guard.wait_warp(dsready, (i - 1) & 1)) break;
-        tc_fence_after();
-        if (elect_one()) {
+      if (i < steps && !guard.wait_warp(dfull0 + 8 * D.stage, D.phase)) break;
+      if (i > 0 && (!guard.wait_warp(qfull0 + 8 * Q.stage, Q.phase) || !guard.wait_warp(dsready, (i - 1) & 1))) break;
+      if (!guard.wait_warp(turn0 + 8, turn)) break;
+      turn ^= 1;
+      tc_fence_after();
+      if (elect_one()) {
+        if (i > 0) {
           product_ts<kQt / 16, 4>(tmem + C::kDk, tmem + C::kDp, kQt / 4, qring + Q.stage * C::kQStage, C::kQBlock,
                                   A.k_steps * 16, i > 1);
           mma_commit_one(qempty0 + 8 * Q.stage);
         }
-        __syncwarp();
-        Q.next(C::kQStages);
-      }
-      if (i < steps) {
-        if (!guard.wait_warp(dfull0 + 8 * D.stage, D.phase)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          product_ss<kVb>(tmem + C::kDp, vt, dring + D.stage * C::kDStage, A.v_cols / 16, C::kQBlock, kQt);
+        if (i < steps) product_ss<kVb>(tmem + C::kDp, vt, dring + D.stage * C::kDStage, A.v_cols / 16, C::kQBlock, kQt);
+        mbar_arrive(turn0);
+        if (i < steps) {
           mma_commit_one(dpfull);
           mma_commit_one(dempty0 + 8 * D.stage);
         }
-        __syncwarp();
-        D.next(C::kDStages);
       }
+      __syncwarp();
+      if (i > 0) Q.next(C::kQStages);
+      if (i < steps) D.next(C::kDStages);
     }
     drain_products(done0 + 8);
   } else {
