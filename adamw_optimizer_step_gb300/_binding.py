@@ -211,8 +211,8 @@ def lib():
                                        c_void_p]),
         "gbo_attn_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
         "gbo_residual_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int32]),
-        "gbo_residual_forward": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
-        "gbo_residual_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "gbo_residual_forward": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
+        "gbo_residual_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
         "gbo_dropout": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64, c_int32, ctypes.c_double,
                                   ctypes.c_uint64, ctypes.c_uint64, c_void_p, c_void_p]),
         "gbo_testing_wait_timeout": (c_int32, [c_void_p, ctypes.c_uint32, c_void_p]),
@@ -879,12 +879,12 @@ def _rows_or_null(t, what, shape, dtype):
     return t.data_ptr(), _rows_of(t, what, shape)
 
 
-def gbo_residual_forward(args, x_out, h, shape, x_dtype, block_dtype, stream=None):
+def gbo_residual_forward(args, x_out, h, shape, x_dtype, block_dtype, dev_status=None, stream=None):
     """Residual update of ``args`` (of :func:`residual_args`) into ``x_out`` and ``h``
     (each may be None where there is nothing to write), ``shape`` (n, d) both."""
     xp, xs = _rows_or_null(x_out, "x_out", shape, x_dtype)
     hp, hs = _rows_or_null(h, "h", shape, block_dtype)
-    _check(lib().gbo_residual_forward(args, xp, xs, hp, hs, _stream(stream)))
+    _check(lib().gbo_residual_forward(args, xp, xs, hp, hs, _dev_ptr(dev_status, "dev_status"), _stream(stream)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -898,7 +898,7 @@ def gbo_residual_workspace_bytes(n, d, sums):
 
 
 def gbo_residual_backward(args, workspace, shape, x_dtype, block_dtype, *, dx_out=None, dh=None, dx=None, dblock=None,
-                          dgate=None, dscale=None, dpost_gain=None, dpre_gain=None, stream=None):
+                          dgate=None, dscale=None, dpost_gain=None, dpre_gain=None, dev_status=None, stream=None):
     """Gradients of the residual update, whichever are given to be written."""
     n, d = shape
     oxp, oxs = _rows_or_null(dx_out, "dx_out", shape, x_dtype)
@@ -911,7 +911,7 @@ def gbo_residual_backward(args, workspace, shape, x_dtype, block_dtype, *, dx_ou
                                  _out_f32(dpost_gain, d, "dpost_gain") or 0, _out_f32(dpre_gain, d, "dpre_gain") or 0, oxs,
                                  ohs, xs, bs, gs)
     ws, nbytes = _workspace(workspace)
-    _check(lib().gbo_residual_backward(args, grads, ws, nbytes, _stream(stream)))
+    _check(lib().gbo_residual_backward(args, grads, ws, nbytes, _dev_ptr(dev_status, "dev_status"), _stream(stream)))
 
 
 def gbo_dropout(x, y, p, seed, offset=0, stream=None):

@@ -145,11 +145,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
   const int b = idx % A.batch, k0 = idx / A.batch * kAttnTile;
   const AttnSeq seq = attn_seq(P.mask, b);
   const int tokens = kQt >> A.pack;
+  const DocWindow docs = doc_window(P.mask, k0);
   int tt0 = 0, n_tok = 0, full_lo = 0, full_hi = 0;  // token tiles that see these keys
   {
     const int a = max(k0, seq.k_lo), e = min(k0 + kAttnTile, seq.k_hi);
     if (e > a) {
-      const Span first = queries_of(P.mask, seq, a), last = queries_of(P.mask, seq, e - 1);
+      const Span first = queries_of(P.mask, seq, docs, a), last = queries_of(P.mask, seq, docs, e - 1);
       if (last.hi > first.lo) {
         tt0 = first.lo / tokens, n_tok = (last.hi + tokens - 1) / tokens - tt0;
         full_lo = last.lo, full_hi = first.hi;
@@ -271,8 +272,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t S = trow + grp * kCols, D = S + C::kDp;
     const bool live = key >= seq.k_lo && key < seq.k_hi;
-    Span seen = {0, 0};
-    if (live && steps > 0) seen = queries_of(P.mask, seq, key);
+    Span seen = queries_of(P.mask, seq, docs, key);
+    if (!live) seen = {0, 0};
     const float2 c2 = make_float2(A.scale2, A.scale2);
     bool ok = true;
     int st = 0, tt = 0;
@@ -443,7 +444,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
   const int kh = hb / A.head_blocks, h0 = kh * (A.q_heads / A.k_heads) + ((hb % A.head_blocks) << A.pack);
   const int tokens = kAttnTile >> A.pack, t0 = tb * tokens;
   const AttnSeq seq = attn_seq(P.mask, b);
-  const TileKeys tk = tile_keys(P.mask, seq, t0, tokens);
+  const DocWindow docs = doc_window(P.mask, t0);
+  const TileKeys tk = tile_keys(P.mask, seq, docs, t0, tokens);
   const int steps = max(0, tk.j1 - tk.j0);
   const uint32_t qt = smem_u32(smem), dt = qt + C::kQTile, kring = qt + C::kKRing, vring = qt + C::kVRing;
   const AttnGuard guard = {abort_flag, P.status};
@@ -518,10 +520,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int token = t0 + (row >> A.pack), head = h0 + (row & ((1 << A.pack) - 1));
     const bool live = token >= seq.q_lo && token < seq.q_hi;
-    Span keys = {0, 0};
+    Span keys = keys_of(P.mask, seq, docs, token);
+    if (!live) keys = {0, 0};
     float2 stat = make_float2(-INFINITY, 0.f);
     if (live) {
-      keys = keys_of(P.mask, seq, token);
       stat = P.stats[((int64_t)b * P.mask.sq + token) * A.q_heads + head];
     }
     const float2 c2 = make_float2(A.scale2, A.scale2), nl = make_float2(stat.x, stat.x), nd = make_float2(-stat.y, -stat.y);

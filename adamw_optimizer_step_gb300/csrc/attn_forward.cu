@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
   const int tokens = kAttnTile >> A.pack, t0 = tb * 2 * tokens;
   const AttnSeq seq = attn_seq(P.mask, b);
   TileKeys tk[2];
-  for (int t = 0; t < 2; ++t) tk[t] = tile_keys(P.mask, seq, t0 + t * tokens, tokens);
+  const DocWindow docs = doc_window(P.mask, t0);
+  for (int t = 0; t < 2; ++t) tk[t] = tile_keys(P.mask, seq, docs, t0 + t * tokens, tokens);
   // the keys of both tiles together, and this CTA's share of them
   int J0 = 0, J1 = 0;
   if (tk[0].j1 > tk[0].j0) J0 = tk[0].j0, J1 = tk[0].j1;
@@ -209,8 +210,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
     const uint32_t S = trow + t * 128 + half * 64, O = trow + C::kO + t * kVb * 64;
     const int token = t0 + t * tokens + (row >> A.pack), head = h0 + (row & ((1 << A.pack) - 1));
     const bool live = token >= seq.q_lo && token < seq.q_hi;
-    Span keys = {0, 0};
-    if (live) keys = keys_of(P.mask, seq, token);
+    Span keys = keys_of(P.mask, seq, docs, token);
+    if (!live) keys = {0, 0};
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     int n = 0;
@@ -441,9 +442,10 @@ __global__ void __launch_bounds__(kTokThreads, 2) attn_token_kernel(const __grid
   const AttnSeq seq = attn_seq(P.mask, b);
   // stages that some row sees, and this CTA's share
   const int a0 = max(0, seq.q_lo), a1 = min(P.mask.sq, seq.q_hi);
+  const DocWindow docs = doc_window(P.mask, a0);
   int J0 = 0, J1 = 0;
   if (a1 > a0) {
-    const Span first = keys_of(P.mask, seq, a0), last = keys_of(P.mask, seq, a1 - 1);
+    const Span first = keys_of(P.mask, seq, docs, a0), last = keys_of(P.mask, seq, docs, a1 - 1);
     if (last.hi > first.lo) J0 = first.lo / kTokKeys, J1 = (last.hi + kTokKeys - 1) / kTokKeys;
   }
   const int each = (J1 - J0 + P.splits - 1) / P.splits;
@@ -488,7 +490,8 @@ __global__ void __launch_bounds__(kTokThreads, 2) attn_token_kernel(const __grid
     for (int h = 0; h < 2; ++h) {
       const int r = r0 + 8 * h, t = r / P.group, head = kh * P.group + r % P.group;
       const bool in = r < rows && t >= seq.q_lo && t < seq.q_hi;
-      if (in) keys[h] = keys_of(P.mask, seq, t);
+      const Span seen = keys_of(P.mask, seq, docs, t);
+      if (in) keys[h] = seen;
       const __nv_bfloat16 *src = P.q + (b * P.qs[0] + t * P.qs[1] + head * P.qs[2]);
 #pragma unroll
       for (int k = 0; k < kKb * 4; ++k)
@@ -713,16 +716,21 @@ FwdPlan plan_forward(const gbo_attn_args *a, const AttnShape &S, int sm) {
     p.items = (int64_t)p.token_blocks * a->batch * a->k_heads * S.head_blocks;
     tiles = (a->sk + kAttnTile - 1) / kAttnTile;
   }
-  const int64_t seen = a->window > 0 ? std::min<int64_t>(tiles, a->window / (p.token ? kTokKeys : kAttnTile) + 2) : tiles;
-  // The split that ends first, a CTA's start and end counted as `fixed` tiles
+  int64_t seen = a->window > 0 ? std::min<int64_t>(tiles, a->window / (p.token ? kTokKeys : kAttnTile) + 2) : tiles;
+  if (a->documents) seen = std::min<int64_t>(seen, tiles / a->n_documents + 1);
+  // The split that ends first, in microseconds: a step of a CTA takes 1.4 (128 keys
+  // for two row tiles; 64 keys of a cache, two CTAs an SM), its start and end as
+  // much as `fixed` steps, and the parts are written and read once, 4 bytes an
+  // element, with a launch of 5.  Without the parts' bytes in the account, 8192 tokens
+  // of 13 documents were split in two: 183 us instead of 70.
   const int64_t at_once = (int64_t)sm * (p.token ? 2 : 1), fixed = p.token ? 6 : 4;
-  int64_t best = INT64_MAX;
+  double best = 0.0;
   p.splits = 1;
-  for (int s = 1; s <= kMaxSplits && s * 2 <= std::max<int64_t>(seen, 2); ++s) {
-    if (s > 1 && p.items * s > 16 * at_once) break;
+  for (int s = 1; s <= kMaxSplits && (s == 1 || s * 2 <= seen); ++s) {
     const int64_t rounds = (p.items * s + at_once - 1) / at_once;
-    const int64_t cost = rounds * ((seen + s - 1) / s + fixed) + (s > 1 ? fixed : 0);
-    if (cost < best) best = cost, p.splits = s;
+    const double join = s > 1 ? 5.0 + (double)p.rows * s * a->dv * 8.0 / 6e6 : 0.0;
+    const double cost = (double)rounds * (double)((seen + s - 1) / s + fixed) * 1.4 + join;
+    if (s == 1 || cost < best) best = cost, p.splits = s;
   }
   p.o_bytes = p.splits > 1 ? ((size_t)p.splits * p.rows * a->dv * 4 + 255) / 256 * 256 : 0;
   p.bytes = p.splits > 1 ? p.o_bytes + (size_t)p.splits * p.rows * 4 : 0;

@@ -215,7 +215,8 @@ def _flat(t, d):
 
 
 def residual_norm(x, block=None, *, post_norm=False, pre_norm=True, post_gain=None, pre_gain=None, gate=None,
-                  gate_kind="sigmoid", scale=None, dropout=0.0, seed=0, offset=0, eps=1e-6, x_out=None):
+                  gate_kind="sigmoid", scale=None, dropout=0.0, seed=0, offset=0, eps=1e-6, x_out=None,
+                  dev_status=None):
     """(x', h): the residual stream ``x`` (..., d) after a block's output ``block``, and
     the next block's input, in one pass:
 
@@ -243,13 +244,13 @@ def residual_norm(x, block=None, *, post_norm=False, pre_norm=True, post_gain=No
     else:
         xo = x_out.view(x2.shape)
     h = torch.empty(x2.shape, dtype=bt, device=x.device) if pre_norm else None
-    B.gbo_residual_forward(args, xo, h, x2.shape, x.dtype, bt)
+    B.gbo_residual_forward(args, xo, h, x2.shape, x.dtype, bt, dev_status)
     return x if xo is None else xo.view(x.shape), None if h is None else h.view(x.shape)
 
 
 def residual_norm_backward(dx_out, dh, x_new, block=None, *, post_norm=False, pre_norm=True, post_gain=None,
                            pre_gain=None, gate=None, gate_kind="sigmoid", scale=None, dropout=0.0, seed=0, offset=0,
-                           eps=1e-6, wanted=("dx", "dblock", "dgate", "dscale", "dpost_gain", "dpre_gain")):
+                           eps=1e-6, wanted=("dx", "dblock", "dgate", "dscale", "dpost_gain", "dpre_gain"), dev_status=None):
     """Gradients of :func:`residual_norm` from those of x' (``dx_out``, None for none) and
     of h (``dh``), the updated stream ``x_new`` and the block's output: a dict with
     ``dx``, ``dblock``, ``dgate``, ``dscale``, ``dpost_gain`` and ``dpre_gain`` (None for
@@ -268,7 +269,7 @@ def residual_norm_backward(dx_out, dh, x_new, block=None, *, post_norm=False, pr
     sums = sum(out[k] is not None for k in ("dscale", "dpost_gain", "dpre_gain"))
     ws = _scratch(B._residual_workspace(*x2.shape, sums, x2.device) if sums else 0, x2.device)
     B.gbo_residual_backward(args, ws, x2.shape, x_new.dtype, bt, dx_out=None if dx_out is None else _flat(dx_out, d),
-                            dh=None if dh is None else _flat(dh, d), **out)
+                            dh=None if dh is None else _flat(dh, d), dev_status=dev_status, **out)
     for k, t in (("dx", x_new), ("dblock", block), ("dgate", gate)):
         if out[k] is not None:
             out[k] = out[k].view(shape if k != "dgate" else t.shape)

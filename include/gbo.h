@@ -605,10 +605,11 @@ typedef struct {
 /*
  *   x_out  device, n rows of d, x_dtype: x' (may be x, with its stride); NULL with has_block = 0
  *   h      device, n rows of d, block_dtype (may be block, with its stride); NULL with pre_norm = 0
+ * A wait that ran out sets GBO_STATUS_TIMEOUT.
  * Errors: INVALID_ARG, SHAPE, DTYPE, CUDA.
  */
 int gbo_residual_forward(const gbo_residual_args *args, void *x_out, int64_t x_out_stride, void *h, int64_t h_stride,
-                         gbo_stream_t stream);
+                         int32_t *dev_status, gbo_stream_t stream);
 
 typedef struct {
   const void *dx_out; /* device, x_dtype: gradient of x' from what else reads it, or NULL: none   */
@@ -633,7 +634,7 @@ typedef struct {
  * Errors: INVALID_ARG, SHAPE, DTYPE, WORKSPACE, CUDA.
  */
 int gbo_residual_backward(const gbo_residual_args *args, const gbo_residual_grads *grads, void *workspace, size_t ws_bytes,
-                          gbo_stream_t stream);
+                          int32_t *dev_status, gbo_stream_t stream);
 size_t gbo_residual_workspace_bytes(int64_t n, int64_t d, int32_t sums);
 
 /*
