@@ -10,6 +10,7 @@
 
 #include "gbo.h"
 #include "internal.h"
+#include "pairs.cuh"
 #include "per_device.h"
 #include "tc_common.cuh"
 
@@ -175,23 +176,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
-}
-
-__device__ __forceinline__ uint64_t as_bits(float2 a) { return *reinterpret_cast<uint64_t *>(&a); }
-__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)), "l"(as_bits(c)));
-  return *reinterpret_cast<float2 *>(&d);
-}
-__device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)));
-  return *reinterpret_cast<float2 *>(&d);
-}
-__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)));
-  return *reinterpret_cast<float2 *>(&d);
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w) {

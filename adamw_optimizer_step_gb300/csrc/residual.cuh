@@ -34,6 +34,7 @@
 #include "dropout.cuh"
 #include "gbo.h"
 #include "internal.h"
+#include "pairs.cuh"
 #include "per_device.h"
 #include "tc_common.cuh"
 
@@ -82,11 +83,11 @@ __device__ __forceinline__ void group_sum(float (&v)[kCount], int group, int in_
     for (int i = 0; i < kCount; ++i) r[i * 16 + warp] = v[i];
   asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(group) : "memory");
 #pragma unroll
-  for (int i = 0; i < kCount; ++i) {
-    float t = 0.f;
-    for (int w = 0; w < warps; ++w) t += r[i * 16 + w];
-    v[i] = t;
-  }
+  for (int i = 0; i < kCount; ++i) v[i] = (lane & 15) < warps ? r[i * 16 + (lane & 15)] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o /= 2)
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
 // A thread's elements of a row: kVec, kIter chunks of eight consecutive ones;
@@ -148,57 +149,15 @@ __device__ __forceinline__ void row_store(T *row, int d, int in_group, int group
   }
 }
 
-// A column table (a gain, the scale).  Kernels with a ring keep it in shared memory:
-// a thread loads its own columns there once and reads them back (no other thread
-// does).  From global memory each use would wait for L2, behind the row's joins.
-template <int kIter, bool kVec, bool kRing>
-struct Table {
-  const float *at;  // NULL: none
-  int d;
-
-  __device__ __forceinline__ Table(const float *t, int d_, uint8_t *&smem, int in_group, int group) : at(t), d(d_) {
-    if constexpr (kRing) {
-      if (!t) return;
-      float *keep = reinterpret_cast<float *>(smem);
-      smem += (int64_t)d * 4;
+// v *= a column table (gains, scales), where there is one.
+template <int kIter, bool kVec>
+__device__ __forceinline__ void times_table(const float *t, int d, int in_group, int group, float (&v)[kIter * 8]) {
+  if (!t) return;
+  float w[kIter * 8];
+  row_load<float, kIter, kVec>(t, d, in_group, group, w);
 #pragma unroll
-      for (int it = 0; it < kIter; ++it) {
-        const int c = column<true>(it, 0, in_group, group);
-        if (c < d) {
-          float4 *to = reinterpret_cast<float4 *>(keep);
-          const float4 *from = reinterpret_cast<const float4 *>(t + c);
-          to[c / 8] = from[0], to[d / 8 + c / 8] = from[1];  // first halves, then second: no bank twice
-        }
-      }
-      at = keep;
-    }
-  }
-  __device__ __forceinline__ void load(int in_group, int group, float (&w)[kIter * 8]) const {
-    if constexpr (kRing) {
-#pragma unroll
-      for (int it = 0; it < kIter; ++it) {
-        const int c = column<true>(it, 0, in_group, group);
-        if (c < d) {
-          const float4 a = reinterpret_cast<const float4 *>(at)[c / 8], b = reinterpret_cast<const float4 *>(at)[d / 8 + c / 8];
-          w[it * 8] = a.x, w[it * 8 + 1] = a.y, w[it * 8 + 2] = a.z, w[it * 8 + 3] = a.w;
-          w[it * 8 + 4] = b.x, w[it * 8 + 5] = b.y, w[it * 8 + 6] = b.z, w[it * 8 + 7] = b.w;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[it * 8 + e] = 0.f;
-        }
-      }
-    } else {
-      row_load<float, kIter, kVec>(at, d, in_group, group, w);
-    }
-  }
-  __device__ __forceinline__ void times(int in_group, int group, float (&v)[kIter * 8]) const {
-    if (!at) return;
-    float w[kIter * 8];
-    load(in_group, group, w);
-#pragma unroll
-    for (int e = 0; e < kIter * 8; ++e) v[e] *= w[e];
-  }
-};
+  for (int e = 0; e < kIter * 8; ++e) v[e] *= w[e];
+}
 
 // u *= dropout's factors of row `row`.
 template <int kIter, bool kVec>
@@ -221,145 +180,171 @@ __device__ __forceinline__ void row_drop(const ResParams &P, uint64_t key, int64
   }
 }
 
-// 1 / (1 + exp(-a)) and its slope, or a and 1.  The slope is f f exp(-a) for
-// positive a, where 1 - f would cancel, and f (1 - f) for others, where exp(-a)
-// may be infinite.
+// 1 / (1 + exp(-a)) and its slope, or a and 1.  From e = exp(-|a|) and q = 1 / (1 + e)
+// the gate is q or e q, the slope e q q: nothing cancels, nothing overflows.
 __device__ __forceinline__ float gate_of(float a, int sigmoid, float *slope = nullptr) {
   if (!sigmoid) {
     if (slope) *slope = 1.f;
     return a;
   }
-  const float e = __expf(-a), f = __fdividef(1.f, 1.f + e);
-  if (slope) *slope = a > 0.f ? f * f * e : f * (1.f - f);
-  return f;
+  const float e = __expf(-fabsf(a)), q = __fdividef(1.f, 1.f + e), eq = e * q;
+  if (slope) *slope = eq * q;
+  return a >= 0.f ? q : a < 0.f ? eq : a;  // (NaN stays)
 }
 
-// Rows on their way into shared memory, one a stage: the input tensors of a row
-// one behind the other, by bulk copies that thread 0 issues `stages` rows ahead.
-// Loads are then in flight all the time at no cost in registers, while a row's
-// two sums over its threads and its arithmetic take their time.
-template <bool kRing>
-struct RowRing {
-  const ResParams &P;
-  uint8_t *base;
-  uint32_t bar0;
-  volatile int32_t *late;
-  int stage = 0;
-  uint32_t phase = 0;
+// ---------------------------------------------------------------------------
+// rows through shared memory
 
-  __device__ __forceinline__ RowRing(const ResParams &p, uint8_t *b, uint32_t bars, volatile int32_t *l)
-      : P(p), base(b), bar0(bars), late(l) {}
+// Rows of 16-byte chunks come through a ring of stages in shared memory: the
+// input tensors of a row one behind the other, by bulk copies that thread 0
+// issues up to `stages` rows ahead.  Loads are then in flight all the time at no
+// cost in registers, while a row's two sums over its threads and its arithmetic
+// take their time.  A stage is filled again behind the first join of the next
+// row, which every thread reaches after its last read of the stage.  (A warp of
+// its own for the copies takes registers from the others: 18 warps an SM have 96
+// each, 16 have 128.)  The column tables stand behind the ring: from global memory
+// each use would wait for L2 behind the row's joins.  What bounds these kernels
+// then is instructions: arithmetic is two lanes at a time, factors of a column are
+// multiplied into one table at the start.
+enum { kInX = 0, kInBlock = 1, kInGate = 2, kInDxo = 3, kInDh = 4, kInputs = 5 };
+
+struct RowRing {
+  uint32_t base, full0, stage_bytes;
+  int stages;
+  volatile int32_t *late;
+  int32_t *status;
+  int stage = 0, to_fill = 0;
+  uint32_t phase = 0;
 
   static __device__ __forceinline__ void copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                  "r"(bytes), "r"(bar)
                  : "memory");
   }
-  // Thread 0: start the copies of row `row` into stage s.
-  template <typename XT, typename BT>
-  __device__ __forceinline__ void fill(int s, int64_t row, bool back) {
-    const uint32_t bar = bar0 + 8 * s, xb = (uint32_t)P.d * sizeof(XT), bb = (uint32_t)P.d * sizeof(BT);
-    uint32_t dst = smem_u32(base) + (uint32_t)s * P.stage_bytes;
-    mbar_expect_tx(bar, (uint32_t)P.stage_bytes);
-    auto put = [&](const void *src, int64_t stride, uint32_t bytes) {
-      copy(dst, static_cast<const uint8_t *>(src) + row * stride * (bytes / (uint32_t)P.d), bytes, bar);
-      dst += bytes;
-    };
-    if (!back || P.pre) put(P.x, P.xs, xb);
-    if (P.block) put(P.block, P.bs, bb);
-    if (P.gate_mode == kGateElement) put(P.gate, P.as, bb);
-    if (back && P.dxo) put(P.dxo, P.dxos, xb);
-    if (back && P.pre) put(P.dh, P.dhs, bb);
-  }
-  // All threads: the stage of the next row has arrived (or, flagged, has not).
-  __device__ __forceinline__ const uint8_t *wait() {
-    if (!*late && !mbar_wait(bar0 + 8 * stage, phase)) {
+  // All threads: the stage of the next row has arrived.  A wait that runs out is
+  // flagged, and every later one passes at once: the outputs are invalid.
+  __device__ __forceinline__ uint32_t take() const {
+    const uint32_t bar = full0 + 8 * stage;
+    if (!mbar_try(bar, phase) && !*late && !mbar_wait(bar, phase)) {
       *late = 1;
-      flag_status(P.status, GBO_STATUS_TIMEOUT);
+      flag_status(status, GBO_STATUS_TIMEOUT);
     }
-    return base + (int64_t)stage * P.stage_bytes;
+    return base + (uint32_t)stage * stage_bytes;
   }
   __device__ __forceinline__ void next() {
-    if (++stage == P.stages) stage = 0, phase ^= 1;
+    if (++stage == stages) stage = 0, phase ^= 1;
   }
 };
 
-// The places of a row's tensors: in global memory, or one behind the other in a
-// stage of the ring.
-template <typename XT, typename BT>
-struct RowIn {
-  const XT *x, *dxo;
-  const BT *block, *gate, *dh;
+// Thread 0: a row's tensors from `src` (NULL: none), `by` bytes on from row to row.
+struct RowFeed {
+  const uint8_t *src[kInputs];
+  int64_t by[kInputs];
+  uint32_t bytes[kInputs];
+  int64_t left;  // rows
+
+  __device__ __forceinline__ void fill(RowRing &r) {
+    if (left <= 0) return;
+    --left;
+    const uint32_t bar = r.full0 + 8 * r.to_fill;
+    uint32_t dst = r.base + (uint32_t)r.to_fill * r.stage_bytes;
+    mbar_expect_tx(bar, r.stage_bytes);
+#pragma unroll
+    for (int i = 0; i < kInputs; ++i)
+      if (src[i]) {
+        RowRing::copy(dst, src[i], bytes[i], bar);
+        src[i] += by[i];
+        dst += bytes[i];
+      }
+    if (++r.to_fill == r.stages) r.to_fill = 0;
+  }
 };
 
-template <typename XT, typename BT, bool kRing>
-__device__ __forceinline__ RowIn<XT, BT> row_in(const ResParams &P, const uint8_t *stage, int64_t row, bool back) {
-  RowIn<XT, BT> r;
-  if constexpr (kRing) {
-    auto take = [&](bool there, int64_t bytes) {
-      const uint8_t *at = stage;
-      if (there) stage += bytes;
-      return at;
-    };
-    const int64_t xb = P.d * (int64_t)sizeof(XT), bb = P.d * (int64_t)sizeof(BT);
-    r.x = reinterpret_cast<const XT *>(take(!back || P.pre, xb));
-    r.block = reinterpret_cast<const BT *>(take(P.block != nullptr, bb));
-    r.gate = reinterpret_cast<const BT *>(take(P.gate_mode == kGateElement, bb));
-    r.dxo = reinterpret_cast<const XT *>(take(back && P.dxo, xb));
-    r.dh = reinterpret_cast<const BT *>(take(back && P.pre, bb));
-    if (P.gate_mode == kGateRow) r.gate = static_cast<const BT *>(P.gate) + row * P.as;
+// Eight elements at a shared-memory address.
+template <typename T>
+__device__ __forceinline__ void lds8(uint32_t at, float2 *v) {
+  uint32_t w[4];
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
   } else {
-    r.x = static_cast<const XT *>(P.x) + row * P.xs;
-    r.block = static_cast<const BT *>(P.block) + row * P.bs;
-    r.gate = static_cast<const BT *>(P.gate) + row * P.as;
-    r.dxo = static_cast<const XT *>(P.dxo) + row * P.dxos;
-    r.dh = static_cast<const BT *>(P.dh) + row * P.dhs;
+    v[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    v[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at + 16)
+                 : "memory");
+    v[2] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    v[3] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
   }
-  return r;
 }
 
-// What both kernels begin with: groups of threads, their rows, the ring.
-#define GBO_RESIDUAL_PROLOGUE(back)                                                                          \
-  pdl_launch();                                                                                              \
-  constexpr int N = kIter * 8;                                                                               \
-  extern __shared__ __align__(128) uint8_t ring_smem[];                                                      \
-  __shared__ float red[4][96];                                                                               \
-  __shared__ uint64_t bars[kMaxStages];                                                                      \
-  __shared__ int32_t late;                                                                                   \
-  const int group = P.group, in_group = threadIdx.x & (group - 1), d = (int)P.d;                             \
-  const int unit = max(group, 32), g = threadIdx.x / unit; /* a join of warps, or a warp of groups */        \
-  const int groups = blockDim.x / group, sub = group < 32 ? (threadIdx.x & 31) / group : 0;                  \
-  int turn = 0;                                                                                              \
-  RowRing<kRing> ring(P, ring_smem, smem_u32(bars), &late);                                                  \
-  if constexpr (kRing) {                                                                                     \
-    if (threadIdx.x == 0) {                                                                                  \
-      for (int s = 0; s < P.stages; ++s) mbar_init(smem_u32(bars + s), 1);                                   \
-      late = 0;                                                                                              \
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");                                     \
-    }                                                                                                        \
-    __syncthreads();                                                                                         \
-  }                                                                                                          \
-  pdl_wait();                                                                                                \
-  const uint64_t key = P.drop.dev_seed ? (uint64_t)*P.drop.dev_seed : P.drop.seed;                           \
-  const float s1 = P.scale_mode == kScaleOne ? *P.scale : 1.f;                                               \
-  uint8_t *table_smem = ring_smem + (kRing ? (int64_t)P.stages * P.stage_bytes : 0);                         \
-  const Table<kIter, kVec, kRing> pre_gain(P.pre_gain, d, table_smem, in_group, group);                      \
-  const Table<kIter, kVec, kRing> post_gain(P.post_gain, d, table_smem, in_group, group);                    \
-  const Table<kIter, kVec, kRing> scale(P.scale_mode == kScaleVector ? P.scale : nullptr, d, table_smem, in_group, group); \
-  const int64_t step = (int64_t)gridDim.x * groups;                                                          \
-  const int64_t row0 = (int64_t)blockIdx.x * groups + (group < 32 ? g * (32 / group) : g);                   \
-  if constexpr (kRing)                                                                                       \
-    if (threadIdx.x == 0)                                                                                    \
-      for (int s = 0; s < P.stages && row0 + s * step < P.n; ++s) ring.template fill<XT, BT>(s, row0 + s * step, back)
-
-// ... and end a row with: the stage is read, its next row may come.
-#define GBO_RESIDUAL_ROW_END(back)                                                                           \
-  if constexpr (kRing) {                                                                                     \
-    __syncthreads();                                                                                         \
-    if (threadIdx.x == 0 && base + P.stages * step < P.n)                                                    \
-      ring.template fill<XT, BT>(ring.stage, base + P.stages * step, back);                                  \
-    ring.next();                                                                                             \
+template <typename T>
+__device__ __forceinline__ void stg8(T *p, const float2 *v) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
+                                               pack_bf16(v[3].x, v[3].y));
+  } else {
+    float4 *f = reinterpret_cast<float4 *>(p);
+    f[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y), f[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   }
+}
+
+// A table's values of chunk c: first halves of all chunks, then second halves, so
+// that a warp's 16-byte reads meet in no bank.  Each thread reads back what it
+// wrote.
+struct ColumnTable {
+  uint32_t at, half;
+  __device__ __forceinline__ void put(int c, const float *v) const {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + 16 * c), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+                 : "memory");
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + half + 16 * c), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  }
+  __device__ __forceinline__ void get(int c, float2 *v) const {
+    float w[8];
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]) : "r"(at + 16 * c) : "memory");
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(w[4]), "=f"(w[5]), "=f"(w[6]), "=f"(w[7])
+                 : "r"(at + half + 16 * c)
+                 : "memory");
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = make_float2(w[2 * k], w[2 * k + 1]);
+  }
+};
+
+__device__ __forceinline__ float table_at(const float *t, int64_t c) { return t ? t[c] : 1.f; }
+
+// Sums of up to three values over a CTA of 2 to 16 warps.
+template <int kCount>
+__device__ __forceinline__ void cta_sum(float (&v)[kCount], float *red, int &turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  float *r = red + turn;
+  turn ^= 48;  // the other turn's values may still be read
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) r[i * 16 + warp] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) v[i] = (lane & 15) < warps ? r[i * 16 + (lane & 15)] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+
+// Dropout's factors of eight elements, times v.
+__device__ __forceinline__ void drop8(const DropArgs &D, uint64_t key, uint64_t element, float2 *v) {
+  const uint4 w = philox(key, element >> 3, D.offset);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    v[k] = f2_mul(v[k], make_float2(drop_factor(w, 2 * k, D.limit, D.keep), drop_factor(w, 2 * k + 1, D.limit, D.keep)));
+}
 
 // ---------------------------------------------------------------------------
 // host
@@ -424,31 +409,48 @@ struct ResCut {
 
 constexpr int kSmemMost = 220 * 1024;  // of an SM's shared memory, for rings and tables
 
-// A row goes to as many threads as it has chunks of eight elements, up to 512.
-// Rows of 16-byte chunks and 128 threads or more come through a ring, whose CTAs
-// (1024 threads an SM forward, 512 for the gradients) share the SM's shared memory.
-// `row_bytes`: of a row's inputs; `table_bytes`: of the column tables.
-ResCut cut_of(int64_t n, int64_t d, int sm, bool back, bool vec, int64_t row_bytes, int64_t table_bytes) {
+// A row goes to as many threads as it has chunks of eight elements, up to 512;
+// where rows come through a ring, to half as many in the forward pass (what a row
+// costs beside its elements is half as much then), one CTA of 64 threads or more
+// a row, 512 threads an SM.  The cut of the gradients' partial rows is the same
+// with a ring and without.  `row_bytes`: of a row's inputs.
+ResCut cut_of(int64_t n, int64_t d, int sm, bool back, bool vec, int64_t row_bytes) {
   ResCut c;
   const int64_t chunks = (d + 7) / 8;
+  c.stages = 0;
+  if (vec && chunks >= 64 && chunks <= 2 * kMaxGroup) {
+    c.group = 64;
+    const int want = back ? 1 : 2;
+    while (c.group < kMaxGroup && (int64_t)c.group * want < chunks) c.group *= 2;
+    c.iter = (int32_t)((chunks + c.group - 1) / c.group);
+    c.threads = c.group;
+    const int per_sm = std::max(1, 512 / c.threads);
+    const int64_t room = kSmemMost / per_sm - 2 * 4 * d;
+    if (room >= 2 * row_bytes) {
+      c.stages = (int32_t)std::min<int64_t>(kMaxStages, room / row_bytes);
+      c.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm * per_sm, n));
+      return c;
+    }
+  }
   c.group = 4;
   while (c.group < kMaxGroup && c.group < chunks) c.group *= 2;
   c.iter = 1;
   while ((int64_t)c.group * c.iter < chunks) c.iter *= 2;
   c.threads = std::max(c.group, 128);
-  c.stages = 0;
   const int64_t groups = c.threads / c.group;
-  const int per_sm = std::max(1, (back ? 512 : 1024) / c.threads);
-  if (vec && c.group >= 128 && c.iter <= 2 && table_bytes + 2 * row_bytes <= kSmemMost)
-    c.stages = (int32_t)std::min<int64_t>(kMaxStages, std::max<int64_t>(2, (kSmemMost / per_sm - table_bytes) / row_bytes));
   // gradients: as many blocks as leave the partial rows few; each goes over many rows
-  const int64_t most = (int64_t)sm * per_sm;
+  const int64_t most = (int64_t)sm * std::max(1, (back ? 512 : 1024) / c.threads);
   c.blocks = (int32_t)std::max<int64_t>(1, std::min(most, (n + groups - 1) / groups));
   return c;
 }
 
 // Partial rows of a backward call.
 int64_t parts_of(const ResCut &c) { return (int64_t)c.blocks * (c.threads / std::max(c.group, 32)); }
+
+// The most that any cut of these sizes leaves.
+int64_t most_parts(int64_t n, int64_t d, int sm) {
+  return std::max(parts_of(cut_of(n, d, sm, true, true, 0)), parts_of(cut_of(n, d, sm, true, false, 0)));
+}
 
 using ResKernel = void (*)(ResParams);
 
@@ -458,11 +460,10 @@ int kernel_slot(const ResCut &c, int32_t xt, int32_t bt) {
 
 // kernel_of: the instance of the pass's kernel for two types, a cut and 16-byte chunks.
 template <typename Pick>
-cudaError_t dispatch_res(ResParams &P, const ResCut &c, bool vec, int32_t xt, int32_t bt, int64_t table_bytes, int dev, cudaStream_t st,
-                         Pick kernel_of) {
+cudaError_t dispatch_res(ResParams &P, const ResCut &c, bool vec, int32_t xt, int32_t bt, int dev, cudaStream_t st, Pick kernel_of) {
   const ResKernel k = kernel_of(xt, bt, c, vec);
   P.group = c.group, P.stages = c.stages;
-  const size_t smem = c.stages ? (size_t)c.stages * P.stage_bytes + table_bytes : 0;
+  const size_t smem = c.stages ? (size_t)c.stages * P.stage_bytes + 2 * 4 * P.d : 0;
   if (c.stages) {
     static PerDevice<cudaError_t> limit[6];
     const cudaError_t *err = limit[kernel_slot(c, xt, bt)].of(dev, [&](cudaError_t &e) {
@@ -487,10 +488,6 @@ void fill_res(const gbo_residual_args *a, const DropArgs &drop, ResParams *P) {
   P->eps = a->eps, P->inv_d = 1.f / (float)a->d;
   P->post = a->post_norm, P->pre = a->pre_norm, P->gate_mode = a->gate_mode, P->sigmoid = a->gate_sigmoid && a->gate_mode;
   P->scale_mode = a->scale_mode;
-}
-
-int64_t table_bytes(const gbo_residual_args *a) {
-  return 4 * a->d * ((a->pre_gain != nullptr) + (a->post_gain != nullptr) + (a->scale_mode == GBO_SCALE_VECTOR));
 }
 
 bool inputs_vec(const gbo_residual_args *a) {

@@ -16,24 +16,38 @@ __device__ __forceinline__ void warp_join(float (&v)[N], int group) {
     }
 }
 
-template <typename XT, typename BT, int kIter, bool kVec, bool kRing>
+template <typename XT, typename BT, int kIter, bool kVec>
 __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __grid_constant__ ResParams P) {
-  GBO_RESIDUAL_PROLOGUE(true);
+  pdl_launch();
+  constexpr int N = kIter * 8;
+  __shared__ float red[4][96];
+  const int group = P.group, in_group = threadIdx.x & (group - 1), d = (int)P.d;
+  const int unit = max(group, 32), g = threadIdx.x / unit;  // a join of warps, or a warp of groups
+  const int groups = blockDim.x / group, sub = group < 32 ? (threadIdx.x & 31) / group : 0;
+  int turn = 0;
+  pdl_wait();
+  const int64_t step = (int64_t)gridDim.x * groups;
+  const int64_t row0 = (int64_t)blockIdx.x * groups + (group < 32 ? g * (32 / group) : g);
+  const uint64_t key = P.drop.dev_seed ? (uint64_t)*P.drop.dev_seed : P.drop.seed;
+  const float s1 = P.scale_mode == kScaleOne ? *P.scale : 1.f;
   float a_pre[N], a_post[N], a_scale[N];  // sums over this group's rows
 #pragma unroll
   for (int e = 0; e < N; ++e) a_pre[e] = a_post[e] = a_scale[e] = 0.f;
   for (int64_t base = row0; base < P.n; base += step) {
     const int64_t row = base + sub;
     const int dr = row < P.n ? d : 0;
-    const uint8_t *stage = nullptr;
-    if constexpr (kRing) stage = ring.wait();
-    const RowIn<XT, BT> in = row_in<XT, BT, kRing>(P, stage, row, true);
+    struct {
+      const XT *x, *dxo;
+      const BT *block, *gate, *dh;
+    } const in = {static_cast<const XT *>(P.x) + row * P.xs, static_cast<const XT *>(P.dxo) + row * P.dxos,
+                  static_cast<const BT *>(P.block) + row * P.bs, static_cast<const BT *>(P.gate) + row * P.as,
+                  static_cast<const BT *>(P.dh) + row * P.dhs};
     float sum[3] = {0.f, 0.f, 0.f};
     if (P.pre) {
       float x[N], w[N];
       row_load<XT, kIter, kVec>(in.x, dr, in_group, group, x);
       row_load<BT, kIter, kVec>(in.dh, dr, in_group, group, w);
-      pre_gain.times(in_group, group, w);
+      times_table<kIter, kVec>(P.pre_gain, d, in_group, group, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         sum[0] = fmaf(x[e], x[e], sum[0]);
@@ -64,7 +78,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
       const float r = rsqrtf(fmaf(sum[0], P.inv_d, P.eps)), c = sum[1] * P.inv_d * r * r;
 #pragma unroll
       for (int e = 0; e < N; ++e) a_pre[e] = fmaf(w[e], x[e] * r, a_pre[e]);
-      pre_gain.times(in_group, group, w);
+      times_table<kIter, kVec>(P.pre_gain, d, in_group, group, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) dx[e] = fmaf(r, w[e] - x[e] * c, dx[e]);
     }
@@ -79,7 +93,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
       float u[N], da[N], join[2] = {0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < N; ++e) u[e] = o[e];
-      post_gain.times(in_group, group, u);
+      times_table<kIter, kVec>(P.post_gain, d, in_group, group, u);
 #pragma unroll
       for (int e = 0; e < N; ++e) u[e] *= dx[e];  // g m u
       if (P.gate_mode == kGateElement) {
@@ -100,9 +114,9 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
           dx[e] *= s1 * row_gate;
         }
       }
-      if (scale.at) {
+      if (P.scale_mode == kScaleVector) {
         float w[N];
-        scale.load(in_group, group, w);
+        row_load<float, kIter, kVec>(P.scale, d, in_group, group, w);
 #pragma unroll
         for (int e = 0; e < N; ++e) da[e] *= w[e], dx[e] *= w[e];
       }
@@ -113,7 +127,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
         join[1] += da[e];
         a_post[e] = fmaf(dx[e], o[e], a_post[e]);
       }
-      post_gain.times(in_group, group, dx);
+      times_table<kIter, kVec>(P.post_gain, d, in_group, group, dx);
 #pragma unroll
       for (int e = 0; e < N; ++e) join[0] = fmaf(dx[e], o[e], join[0]);
       if (P.post || P.gate_mode == kGateRow) group_sum(join, group, in_group, red[g], turn, 1 + g);
@@ -128,7 +142,6 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
         row_store<BT, kIter, kVec>(static_cast<BT *>(P.h) + row * P.hs, dr, in_group, group, dx);
       }
     }
-    GBO_RESIDUAL_ROW_END(true)
   }
   if (!(P.want_pre | P.want_post | P.want_scale)) return;
   warp_join(a_pre, group);
@@ -141,6 +154,199 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
   if (P.want_pre) row_store<float, kIter, kVec>(part, dw, in_group, group, a_pre), part += rows;
   if (P.want_post) row_store<float, kIter, kVec>(part, dw, in_group, group, a_post), part += rows;
   if (P.want_scale) row_store<float, kIter, kVec>(part, dw, in_group, group, a_scale);
+}
+
+// The same through a ring, a CTA to a row.  With t = g m v, v = o rho(o), the table
+// M = scale post_gain (s1 where the scale is one number) and the gate f:
+//   A = sum t f:  dscale = post_gain A, dpost_gain = scale A
+//   da = t M f',  w = g m f M,  mean(w v) = mean(t f M),  do = rho(o) (w - v mean(w v))
+template <typename XT, typename BT, int kIter>
+__global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const __grid_constant__ ResParams P) {
+  pdl_launch();
+  extern __shared__ __align__(128) uint8_t ring_smem[];
+  __shared__ float red[96];
+  __shared__ uint64_t bars[kMaxStages];
+  __shared__ int32_t late;
+  constexpr int N = kIter * 4;  // pairs of elements
+  const int tid = threadIdx.x, threads = blockDim.x, chunks = (int)P.d / 8;
+  RowRing ring{smem_u32(ring_smem), smem_u32(bars), (uint32_t)P.stage_bytes, P.stages, &late, P.status};
+  if (tid == 0) {
+    for (int s = 0; s < P.stages; ++s) mbar_init(ring.full0 + 8 * s, 1);
+    late = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_wait();
+  const int64_t row0 = blockIdx.x, step = gridDim.x;
+  const uint32_t xb = (uint32_t)P.d * sizeof(XT), bb = (uint32_t)P.d * sizeof(BT);
+  const bool gated = P.gate_mode == kGateElement;
+  RowFeed feed{};
+  if (tid == 0) {
+    auto set = [&](int i, const void *p, int64_t stride, uint32_t bytes, int size) {
+      if (!p) return;
+      feed.src[i] = static_cast<const uint8_t *>(p) + row0 * stride * size;
+      feed.by[i] = step * stride * size, feed.bytes[i] = bytes;
+    };
+    if (P.pre) set(kInX, P.x, P.xs, xb, sizeof(XT));
+    set(kInBlock, P.block, P.bs, bb, sizeof(BT));
+    if (gated) set(kInGate, P.gate, P.as, bb, sizeof(BT));
+    set(kInDxo, P.dxo, P.dxos, xb, sizeof(XT));
+    if (P.pre) set(kInDh, P.dh, P.dhs, bb, sizeof(BT));
+    feed.left = (P.n - row0 + step - 1) / step;
+    for (int s = 0; s < P.stages; ++s) feed.fill(ring);
+  }
+  // a stage's tensors
+  const uint32_t to_block = P.pre ? xb : 0, to_gate = to_block + (P.block ? bb : 0), to_dxo = to_gate + (gated ? bb : 0);
+  const uint32_t to_dh = to_dxo + (P.dxo ? xb : 0);
+  const uint64_t key = P.drop.dev_seed ? (uint64_t)*P.drop.dev_seed : P.drop.seed;
+  const float s1 = P.scale_mode == kScaleOne ? *P.scale : 1.f;
+  const float *const scale = P.scale_mode == kScaleVector ? P.scale : nullptr;
+  const ColumnTable mul = {ring.base + P.stages * ring.stage_bytes, (uint32_t)chunks * 16};
+  const ColumnTable pre = {mul.at + 2 * mul.half, mul.half};
+  float2 a_pre[N], a_all[N];
+#pragma unroll
+  for (int it = 0; it < kIter; ++it) {
+    const int c = it * threads + tid;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a_pre[4 * it + k] = a_all[4 * it + k] = f2_of(0.f);
+    if (c < chunks) {
+      float v[8], w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = s1 * table_at(P.post_gain, c * 8 + e) * table_at(scale, c * 8 + e);
+        w[e] = table_at(P.pre_gain, c * 8 + e);
+      }
+      mul.put(c, v);
+      pre.put(c, w);
+    }
+  }
+  int turn = 0;
+  for (int64_t row = row0; row < P.n; row += step) {
+    const uint32_t at = ring.take();
+    float2 x[N], dh[N], o[N];
+    float2 s0 = f2_of(0.f), sx = f2_of(0.f), so = f2_of(0.f);
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int c = it * threads + tid;
+      if (c < chunks) {
+        if (P.pre) {
+          float2 t[4];
+          lds8<XT>(at + c * 8 * sizeof(XT), x + 4 * it);
+          lds8<BT>(at + to_dh + c * 8 * sizeof(BT), dh + 4 * it);
+          pre.get(c, t);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            s0 = f2_fma(x[4 * it + k], x[4 * it + k], s0);
+            sx = f2_fma(f2_mul(dh[4 * it + k], t[k]), x[4 * it + k], sx);
+          }
+        }
+        if (P.post) {
+          lds8<BT>(at + to_block + c * 8 * sizeof(BT), o + 4 * it);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) so = f2_fma(o[4 * it + k], o[4 * it + k], so);
+        }
+      }
+    }
+    float sum[3] = {s0.x + s0.y, sx.x + sx.y, so.x + so.y};
+    if (P.pre || P.post) cta_sum(sum, red, turn);
+    else __syncthreads();
+    if (tid == 0 && row != row0) feed.fill(ring);
+    const float r = rsqrtf(fmaf(sum[0], P.inv_d, P.eps)), ro = P.post ? rsqrtf(fmaf(sum[2], P.inv_d, P.eps)) : 1.f;
+    const float2 r2 = f2_of(r), c2 = f2_of(-sum[1] * P.inv_d * r * r), ro2 = f2_of(ro);
+    float row_slope = 0.f;
+    float row_gate = 1.f;
+    if (P.gate_mode == kGateRow) row_gate = gate_of((float)static_cast<const BT *>(P.gate)[row * P.as], P.sigmoid, &row_slope);
+    float2 g[N], j0 = f2_of(0.f), j1 = f2_of(0.f);
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int c = it * threads + tid;
+      if (c < chunks) {
+        float2 *const dx = g + 4 * it;
+        if (P.dxo) {
+          lds8<XT>(at + to_dxo + c * 8 * sizeof(XT), dx);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dx[k] = f2_of(0.f);
+        }
+        if (P.pre) {
+          float2 t[4];
+          pre.get(c, t);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = 4 * it + k;
+            a_pre[i] = f2_fma(dh[i], f2_mul(x[i], r2), a_pre[i]);
+            dx[k] = f2_fma(r2, f2_fma(x[i], c2, f2_mul(dh[i], t[k])), dx[k]);
+          }
+        }
+        if (P.xo) stg8(static_cast<XT *>(P.xo) + row * P.xos + c * 8, dx);
+        if (P.block) {
+          float2 M[4], a[4];
+          float2 *const v = o + 4 * it;
+          if (!P.post) lds8<BT>(at + to_block + c * 8 * sizeof(BT), v);
+          if (P.drop.limit) drop8(P.drop, key, (uint64_t)(row * P.d + c * 8), dx);
+          mul.get(c, M);
+          if (gated) lds8<BT>(at + to_gate + c * 8 * sizeof(BT), a);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[k] = f2_mul(v[k], ro2);
+            const float2 t = f2_mul(dx[k], v[k]);
+            float2 f = f2_of(row_gate), slope = f2_of(row_slope);
+            if (gated) f.x = gate_of(a[k].x, P.sigmoid, &slope.x), f.y = gate_of(a[k].y, P.sigmoid, &slope.y);
+            const float2 tf = f2_mul(t, f);
+            a_all[4 * it + k] = f2_add(a_all[4 * it + k], tf);
+            a[k] = f2_mul(f2_mul(t, M[k]), slope);
+            j1 = f2_add(j1, a[k]);
+            j0 = f2_fma(tf, M[k], j0);
+            dx[k] = f2_mul(dx[k], f2_mul(f, M[k]));
+          }
+          if (gated && P.dgate) stg8(static_cast<BT *>(P.dgate) + row * P.das + c * 8, a);
+          if (P.h && !P.post) stg8(static_cast<BT *>(P.h) + row * P.hs + c * 8, dx);
+        }
+      }
+    }
+    if (P.post || P.gate_mode == kGateRow) {
+      float join[2] = {j0.x + j0.y, j1.x + j1.y};
+      cta_sum(join, red, turn);
+      if (P.gate_mode == kGateRow && P.dgate && tid == 0)
+        st_elem(P.dgate, sizeof(BT) == 2 ? GBO_BF16 : GBO_F32, row * P.das, join[1]);
+      if (P.h && P.post) {
+        const float2 m2 = f2_of(-join[0] * P.inv_d);
+#pragma unroll
+        for (int it = 0; it < kIter; ++it) {
+          const int c = it * threads + tid;
+          if (c < chunks) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) g[4 * it + k] = f2_mul(ro2, f2_fma(o[4 * it + k], m2, g[4 * it + k]));
+            stg8(static_cast<BT *>(P.h) + row * P.hs + c * 8, g + 4 * it);
+          }
+        }
+      }
+    }
+    ring.next();
+  }
+  const int64_t rows = (int64_t)gridDim.x * P.d;
+#pragma unroll
+  for (int it = 0; it < kIter; ++it) {
+    const int c = it * threads + tid;
+    if (c < chunks) {
+      float *part = P.part + (int64_t)blockIdx.x * P.d + c * 8;
+      if (P.want_pre) stg8(part, a_pre + 4 * it), part += rows;
+#pragma unroll
+      for (int which = 0; which < 2; ++which)
+        if (which == 0 ? P.want_post : P.want_scale) {
+          float2 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float *const t = which == 0 ? scale : P.post_gain;
+            const float one = which == 0 ? s1 : 1.f;
+            v[k] = f2_mul(a_all[4 * it + k],
+                          make_float2(one * table_at(t, c * 8 + 2 * k), one * table_at(t, c * 8 + 2 * k + 1)));
+          }
+          stg8(part, v);
+          part += rows;
+        }
+    }
+  }
 }
 
 // The partial rows added up, in a fixed order: 32 columns a block.  Of a scale
@@ -188,11 +394,11 @@ __global__ void __launch_bounds__(1024) residual_one_kernel(const float *__restr
 
 template <typename XT, typename BT>
 ResKernel pick(const ResCut &c, bool vec) {
-  if (c.stages) return c.iter == 1 ? residual_backward_kernel<XT, BT, 1, true, true> : residual_backward_kernel<XT, BT, 2, true, true>;
-  if (vec) return c.iter == 1 ? residual_backward_kernel<XT, BT, 1, true, false> : residual_backward_kernel<XT, BT, 4, true, false>;
-  return c.iter == 1   ? residual_backward_kernel<XT, BT, 1, false, false>
-         : c.iter == 2 ? residual_backward_kernel<XT, BT, 2, false, false>
-                       : residual_backward_kernel<XT, BT, 4, false, false>;
+  if (c.stages) return c.iter == 1 ? residual_backward_ring_kernel<XT, BT, 1> : residual_backward_ring_kernel<XT, BT, 2>;
+  if (vec) return c.iter == 1 ? residual_backward_kernel<XT, BT, 1, true> : residual_backward_kernel<XT, BT, 4, true>;
+  return c.iter == 1   ? residual_backward_kernel<XT, BT, 1, false>
+         : c.iter == 2 ? residual_backward_kernel<XT, BT, 2, false>
+                       : residual_backward_kernel<XT, BT, 4, false>;
 }
 
 ResKernel kernel_of(int32_t xt, int32_t bt, const ResCut &c, bool vec) {
@@ -208,8 +414,7 @@ using namespace gbo;
 extern "C" size_t gbo_residual_workspace_bytes(int64_t n, int64_t d, int32_t sums) {
   int dev, sm = 0;
   if (n < 0 || d < 1 || d > GBO_RESIDUAL_MAX_D || sums < 0 || sums > 3 || require_device(&dev, &sm) != GBO_OK) return 0;
-  const ResCut c = cut_of(n, d, sm, true, false, 0, 0);  // (the ring changes no block)
-  return sums ? (size_t)parts_of(c) * d * sums * 4 + (size_t)d * 4 : 0;
+  return sums ? (size_t)most_parts(n, d, sm) * d * sums * 4 + (size_t)d * 4 : 0;
 }
 
 extern "C" int gbo_residual_backward(const gbo_residual_args *a, const gbo_residual_grads *g, void *workspace, size_t ws_bytes,
@@ -257,10 +462,10 @@ extern "C" int gbo_residual_backward(const gbo_residual_args *a, const gbo_resid
   P.status = dev_status;
   P.stage_bytes = (int32_t)(a->d * (size_of(a->x_dtype) * (a->pre_norm + (g->dx_out != nullptr)) +
                                     size_of(a->block_dtype) * (a->has_block + (a->gate_mode == GBO_GATE_ELEMENT) + a->pre_norm)));
-  const ResCut c = cut_of(a->n, a->d, sm, true, vec, P.stage_bytes, table_bytes(a));
+  const ResCut c = cut_of(a->n, a->d, sm, true, vec, P.stage_bytes);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (a->n > 0 || sums) e = dispatch_res(P, c, vec, a->x_dtype, a->block_dtype, table_bytes(a), dev, st, kernel_of);
+  if (a->n > 0 || sums) e = dispatch_res(P, c, vec, a->x_dtype, a->block_dtype, dev, st, kernel_of);
   if (e == cudaSuccess && sums) {
     ResSum S;
     memset(&S, 0, sizeof S);

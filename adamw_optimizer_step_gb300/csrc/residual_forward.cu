@@ -5,20 +5,28 @@ namespace gbo {
 
 namespace {
 
-template <typename XT, typename BT, int kIter, bool kVec, bool kRing>
+template <typename XT, typename BT, int kIter, bool kVec>
 __global__ void __launch_bounds__(kMaxGroup) residual_forward_kernel(const __grid_constant__ ResParams P) {
-  GBO_RESIDUAL_PROLOGUE(false);
+  pdl_launch();
+  constexpr int N = kIter * 8;
+  __shared__ float red[4][96];
+  const int group = P.group, in_group = threadIdx.x & (group - 1), d = (int)P.d;
+  const int unit = max(group, 32), g = threadIdx.x / unit;  // a join of warps, or a warp of groups
+  const int groups = blockDim.x / group, sub = group < 32 ? (threadIdx.x & 31) / group : 0;
+  int turn = 0;
+  pdl_wait();
+  const int64_t step = (int64_t)gridDim.x * groups;
+  const int64_t row0 = (int64_t)blockIdx.x * groups + (group < 32 ? g * (32 / group) : g);
+  const uint64_t key = P.drop.dev_seed ? (uint64_t)*P.drop.dev_seed : P.drop.seed;
+  const float s1 = P.scale_mode == kScaleOne ? *P.scale : 1.f;
   for (int64_t base = row0; base < P.n; base += step) {
     const int64_t row = base + sub;
     const int dr = row < P.n ? d : 0;  // (the last warp may hold fewer rows than groups)
-    const uint8_t *stage = nullptr;
-    if constexpr (kRing) stage = ring.wait();
-    const RowIn<XT, BT> in = row_in<XT, BT, kRing>(P, stage, row, false);
     float x[N];
-    row_load<XT, kIter, kVec>(in.x, dr, in_group, group, x);
+    row_load<XT, kIter, kVec>(static_cast<const XT *>(P.x) + row * P.xs, dr, in_group, group, x);
     if (P.block) {
       float u[N];
-      row_load<BT, kIter, kVec>(in.block, dr, in_group, group, u);
+      row_load<BT, kIter, kVec>(static_cast<const BT *>(P.block) + row * P.bs, dr, in_group, group, u);
       float f = s1;
       if (P.post) {
         float sum[1] = {0.f};
@@ -26,17 +34,17 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_kernel(const __gri
         for (int e = 0; e < N; ++e) sum[0] = fmaf(u[e], u[e], sum[0]);
         group_sum(sum, group, in_group, red[g], turn, 1 + g);
         f *= rsqrtf(fmaf(sum[0], P.inv_d, P.eps));
-        post_gain.times(in_group, group, u);
+        times_table<kIter, kVec>(P.post_gain, d, in_group, group, u);
       }
       if (P.drop.limit) row_drop<kIter, kVec>(P, key, row, in_group, group, u);
       if (P.gate_mode == kGateElement) {
         float a[N];
-        row_load<BT, kIter, kVec>(in.gate, dr, in_group, group, a);
+        row_load<BT, kIter, kVec>(static_cast<const BT *>(P.gate) + row * P.as, dr, in_group, group, a);
 #pragma unroll
         for (int e = 0; e < N; ++e) u[e] *= gate_of(a[e], P.sigmoid);
       }
-      scale.times(in_group, group, u);
-      if (P.gate_mode == kGateRow && dr) f *= gate_of((float)*in.gate, P.sigmoid);
+      if (P.scale_mode == kScaleVector) times_table<kIter, kVec>(P.scale, d, in_group, group, u);
+      if (P.gate_mode == kGateRow && dr) f *= gate_of((float)static_cast<const BT *>(P.gate)[row * P.as], P.sigmoid);
 #pragma unroll
       for (int e = 0; e < N; ++e) x[e] = fmaf(f, u[e], x[e]);
       row_store<XT, kIter, kVec>(static_cast<XT *>(P.xo) + row * P.xos, dr, in_group, group, x);
@@ -49,10 +57,156 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_kernel(const __gri
       const float r = rsqrtf(fmaf(sum[0], P.inv_d, P.eps));
 #pragma unroll
       for (int e = 0; e < N; ++e) x[e] *= r;
-      pre_gain.times(in_group, group, x);
+      times_table<kIter, kVec>(P.pre_gain, d, in_group, group, x);
       row_store<BT, kIter, kVec>(static_cast<BT *>(P.h) + row * P.hs, dr, in_group, group, x);
     }
-    GBO_RESIDUAL_ROW_END(false)
+  }
+}
+
+// The same through a ring, a CTA to a row.  post_gain and scale stand in one table:
+// x' = x + (s1 rho(o) gate_row) table gate m o.
+template <typename XT, typename BT, int kIter>
+__global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const __grid_constant__ ResParams P) {
+  pdl_launch();
+  extern __shared__ __align__(128) uint8_t ring_smem[];
+  __shared__ float red[96];
+  __shared__ uint64_t bars[kMaxStages];
+  __shared__ int32_t late;
+  constexpr int N = kIter * 4;  // pairs of elements
+  const int tid = threadIdx.x, threads = blockDim.x, chunks = (int)P.d / 8;
+  RowRing ring{smem_u32(ring_smem), smem_u32(bars), (uint32_t)P.stage_bytes, P.stages, &late, P.status};
+  if (tid == 0) {
+    for (int s = 0; s < P.stages; ++s) mbar_init(ring.full0 + 8 * s, 1);
+    late = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_wait();
+  const int64_t row0 = blockIdx.x, step = gridDim.x;
+  const uint32_t xb = (uint32_t)P.d * sizeof(XT), bb = (uint32_t)P.d * sizeof(BT);
+  RowFeed feed{};
+  if (tid == 0) {
+    auto set = [&](int i, const void *p, int64_t stride, uint32_t bytes, int size) {
+      if (!p) return;
+      feed.src[i] = static_cast<const uint8_t *>(p) + row0 * stride * size;
+      feed.by[i] = step * stride * size, feed.bytes[i] = bytes;
+    };
+    set(kInX, P.x, P.xs, xb, sizeof(XT));
+    set(kInBlock, P.block, P.bs, bb, sizeof(BT));
+    if (P.gate_mode == kGateElement) set(kInGate, P.gate, P.as, bb, sizeof(BT));
+    feed.left = (P.n - row0 + step - 1) / step;
+    for (int s = 0; s < P.stages; ++s) feed.fill(ring);
+  }
+  const uint64_t key = P.drop.dev_seed ? (uint64_t)*P.drop.dev_seed : P.drop.seed;
+  const float s1 = P.scale_mode == kScaleOne ? *P.scale : 1.f;
+  const ColumnTable mul = {ring.base + P.stages * ring.stage_bytes, (uint32_t)chunks * 16};
+  const ColumnTable pre = {mul.at + 2 * mul.half, mul.half};
+  const bool muls = P.post_gain || P.scale_mode == kScaleVector;
+#pragma unroll
+  for (int it = 0; it < kIter; ++it) {
+    const int c = it * threads + tid;
+    if (c < chunks) {
+      float v[8], w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = table_at(P.post_gain, c * 8 + e) * table_at(P.scale_mode == kScaleVector ? P.scale : nullptr, c * 8 + e);
+        w[e] = table_at(P.pre_gain, c * 8 + e);
+      }
+      mul.put(c, v);
+      pre.put(c, w);
+    }
+  }
+  int turn = 0;
+  for (int64_t row = row0; row < P.n; row += step) {
+    const uint32_t at = ring.take();
+    float2 x[N];
+    bool joined = false;
+    auto join = [&](float v) {
+      float sum[1] = {v};
+      cta_sum(sum, red, turn);
+      if (!joined && tid == 0 && row != row0) feed.fill(ring);
+      joined = true;
+      return rsqrtf(fmaf(sum[0], P.inv_d, P.eps));
+    };
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int c = it * threads + tid;
+      if (c < chunks) {
+        lds8<XT>(at + c * 8 * sizeof(XT), x + 4 * it);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[4 * it + k] = f2_of(0.f);
+      }
+    }
+    if (P.block) {
+      float2 u[N];
+      float2 ss = f2_of(0.f);
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const int c = it * threads + tid;
+        if (c < chunks) {
+          lds8<BT>(at + xb + c * 8 * sizeof(BT), u + 4 * it);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ss = f2_fma(u[4 * it + k], u[4 * it + k], ss);
+        }
+      }
+      float f = s1;
+      if (P.gate_mode == kGateRow) f *= gate_of((float)static_cast<const BT *>(P.gate)[row * P.as], P.sigmoid);
+      if (P.post) f *= join(ss.x + ss.y);
+      const float2 f2 = f2_of(f);
+      XT *const out = static_cast<XT *>(P.xo) + row * P.xos;
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const int c = it * threads + tid;
+        if (c < chunks) {
+          float2 *const v = u + 4 * it;
+          if (muls) {
+            float2 t[4];
+            mul.get(c, t);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = f2_mul(v[k], t[k]);
+          }
+          if (P.drop.limit) drop8(P.drop, key, (uint64_t)(row * P.d + c * 8), v);
+          if (P.gate_mode == kGateElement) {
+            float2 a[4];
+            lds8<BT>(at + xb + bb + c * 8 * sizeof(BT), a);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = f2_mul(v[k], make_float2(gate_of(a[k].x, P.sigmoid), gate_of(a[k].y, P.sigmoid)));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[4 * it + k] = f2_fma(f2, v[k], x[4 * it + k]);
+          stg8(out + c * 8, x + 4 * it);
+        }
+      }
+    }
+    if (P.pre) {
+      float2 ss = f2_of(0.f);
+#pragma unroll
+      for (int k = 0; k < N; ++k) ss = f2_fma(x[k], x[k], ss);
+      const float2 r = f2_of(join(ss.x + ss.y));
+      BT *const out = static_cast<BT *>(P.h) + row * P.hs;
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const int c = it * threads + tid;
+        if (c < chunks) {
+          float2 *const v = x + 4 * it;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = f2_mul(v[k], r);
+          if (P.pre_gain) {
+            float2 t[4];
+            pre.get(c, t);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = f2_mul(v[k], t[k]);
+          }
+          stg8(out + c * 8, v);
+        }
+      }
+    }
+    if (!joined) {
+      __syncthreads();
+      if (tid == 0 && row != row0) feed.fill(ring);
+    }
+    ring.next();
   }
 }
 
@@ -100,11 +254,11 @@ __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ Dr
 
 template <typename XT, typename BT>
 ResKernel pick(const ResCut &c, bool vec) {
-  if (c.stages) return c.iter == 1 ? residual_forward_kernel<XT, BT, 1, true, true> : residual_forward_kernel<XT, BT, 2, true, true>;
-  if (vec) return c.iter == 1 ? residual_forward_kernel<XT, BT, 1, true, false> : residual_forward_kernel<XT, BT, 4, true, false>;
-  return c.iter == 1   ? residual_forward_kernel<XT, BT, 1, false, false>
-         : c.iter == 2 ? residual_forward_kernel<XT, BT, 2, false, false>
-                       : residual_forward_kernel<XT, BT, 4, false, false>;
+  if (c.stages) return c.iter == 1 ? residual_forward_ring_kernel<XT, BT, 1> : residual_forward_ring_kernel<XT, BT, 2>;
+  if (vec) return c.iter == 1 ? residual_forward_kernel<XT, BT, 1, true> : residual_forward_kernel<XT, BT, 4, true>;
+  return c.iter == 1   ? residual_forward_kernel<XT, BT, 1, false>
+         : c.iter == 2 ? residual_forward_kernel<XT, BT, 2, false>
+                       : residual_forward_kernel<XT, BT, 4, false>;
 }
 
 ResKernel kernel_of(int32_t xt, int32_t bt, const ResCut &c, bool vec) {
@@ -139,8 +293,8 @@ extern "C" int gbo_residual_forward(const gbo_residual_args *a, void *x_out, int
   const bool vec = inputs_vec(a) && vec_ok(x_out, x_out_stride, a->n) && vec_ok(h, h_stride, a->n);
   P.status = dev_status;
   P.stage_bytes = (int32_t)(a->d * (size_of(a->x_dtype) + size_of(a->block_dtype) * (a->has_block + (a->gate_mode == GBO_GATE_ELEMENT))));
-  const ResCut c = cut_of(a->n, a->d, sm, false, vec, P.stage_bytes, table_bytes(a));
-  const cudaError_t e = dispatch_res(P, c, vec, a->x_dtype, a->block_dtype, table_bytes(a), dev, reinterpret_cast<cudaStream_t>(stream), kernel_of);
+  const ResCut c = cut_of(a->n, a->d, sm, false, vec, P.stage_bytes);
+  const cudaError_t e = dispatch_res(P, c, vec, a->x_dtype, a->block_dtype, dev, reinterpret_cast<cudaStream_t>(stream), kernel_of);
   return e == cudaSuccess ? report_ok() : res_cuda(e);
 }
 
