@@ -420,13 +420,12 @@ ResCut cut_of(int64_t n, int64_t d, int sm, bool back, bool vec, int64_t row_byt
   c.stages = 0;
   if (vec && chunks >= 64 && chunks <= 2 * kMaxGroup) {
     c.group = 64;
-    const int want = back ? 1 : 2;
-    while (c.group < kMaxGroup && (int64_t)c.group * want < chunks) c.group *= 2;
+    while (c.group < kMaxGroup && (int64_t)c.group * (back ? 1 : 2) < chunks) c.group *= 2;
     c.iter = (int32_t)((chunks + c.group - 1) / c.group);
     c.threads = c.group;
-    const int per_sm = std::max(1, 512 / c.threads);
-    const int64_t room = kSmemMost / per_sm - 2 * 4 * d;
-    if (room >= 2 * row_bytes) {
+    for (int per_sm = std::max(1, 512 / c.threads); per_sm > 0; --per_sm) {
+      const int64_t room = kSmemMost / per_sm - 2 * 4 * d;
+      if (room < 2 * row_bytes) continue;
       c.stages = (int32_t)std::min<int64_t>(kMaxStages, room / row_bytes);
       c.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm * per_sm, n));
       return c;

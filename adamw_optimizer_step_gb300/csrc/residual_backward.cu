@@ -223,27 +223,27 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
   int turn = 0;
   for (int64_t row = row0; row < P.n; row += step) {
     const uint32_t at = ring.take();
-    float2 x[N], dh[N], o[N];
     float2 s0 = f2_of(0.f), sx = f2_of(0.f), so = f2_of(0.f);
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int c = it * threads + tid;
       if (c < chunks) {
         if (P.pre) {
-          float2 t[4];
-          lds8<XT>(at + c * 8 * sizeof(XT), x + 4 * it);
-          lds8<BT>(at + to_dh + c * 8 * sizeof(BT), dh + 4 * it);
+          float2 t[4], x[4], dh[4];
+          lds8<XT>(at + c * 8 * sizeof(XT), x);
+          lds8<BT>(at + to_dh + c * 8 * sizeof(BT), dh);
           pre.get(c, t);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            s0 = f2_fma(x[4 * it + k], x[4 * it + k], s0);
-            sx = f2_fma(f2_mul(dh[4 * it + k], t[k]), x[4 * it + k], sx);
+            s0 = f2_fma(x[k], x[k], s0);
+            sx = f2_fma(f2_mul(dh[k], t[k]), x[k], sx);
           }
         }
         if (P.post) {
-          lds8<BT>(at + to_block + c * 8 * sizeof(BT), o + 4 * it);
+          float2 o[4];
+          lds8<BT>(at + to_block + c * 8 * sizeof(BT), o);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) so = f2_fma(o[4 * it + k], o[4 * it + k], so);
+          for (int k = 0; k < 4; ++k) so = f2_fma(o[k], o[k], so);
         }
       }
     }
@@ -251,12 +251,13 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
     if (P.pre || P.post) cta_sum(sum, red, turn);
     else __syncthreads();
     if (tid == 0 && row != row0) feed.fill(ring);
+    // (the row is read again: held over the join, two chunks a thread would spill)
     const float r = rsqrtf(fmaf(sum[0], P.inv_d, P.eps)), ro = P.post ? rsqrtf(fmaf(sum[2], P.inv_d, P.eps)) : 1.f;
     const float2 r2 = f2_of(r), c2 = f2_of(-sum[1] * P.inv_d * r * r), ro2 = f2_of(ro);
     float row_slope = 0.f;
     float row_gate = 1.f;
     if (P.gate_mode == kGateRow) row_gate = gate_of((float)static_cast<const BT *>(P.gate)[row * P.as], P.sigmoid, &row_slope);
-    float2 g[N], j0 = f2_of(0.f), j1 = f2_of(0.f);
+    float2 g[N], o[N], j0 = f2_of(0.f), j1 = f2_of(0.f);
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int c = it * threads + tid;
@@ -269,20 +270,21 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
           for (int k = 0; k < 4; ++k) dx[k] = f2_of(0.f);
         }
         if (P.pre) {
-          float2 t[4];
+          float2 t[4], x[4], dh[4];
+          lds8<XT>(at + c * 8 * sizeof(XT), x);
+          lds8<BT>(at + to_dh + c * 8 * sizeof(BT), dh);
           pre.get(c, t);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int i = 4 * it + k;
-            a_pre[i] = f2_fma(dh[i], f2_mul(x[i], r2), a_pre[i]);
-            dx[k] = f2_fma(r2, f2_fma(x[i], c2, f2_mul(dh[i], t[k])), dx[k]);
+            a_pre[4 * it + k] = f2_fma(dh[k], f2_mul(x[k], r2), a_pre[4 * it + k]);
+            dx[k] = f2_fma(r2, f2_fma(x[k], c2, f2_mul(dh[k], t[k])), dx[k]);
           }
         }
         if (P.xo) stg8(static_cast<XT *>(P.xo) + row * P.xos + c * 8, dx);
         if (P.block) {
           float2 M[4], a[4];
           float2 *const v = o + 4 * it;
-          if (!P.post) lds8<BT>(at + to_block + c * 8 * sizeof(BT), v);
+          lds8<BT>(at + to_block + c * 8 * sizeof(BT), v);
           if (P.drop.limit) drop8(P.drop, key, (uint64_t)(row * P.d + c * 8), dx);
           mul.get(c, M);
           if (gated) lds8<BT>(at + to_gate + c * 8 * sizeof(BT), a);
