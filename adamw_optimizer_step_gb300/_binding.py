@@ -754,9 +754,13 @@ def _attn_heads(t, what, batch, seq, heads, dim):
     s = t.stride()
     if s[3] != 1:
         raise ValueError("the elements of a head of %s must be consecutive" % what)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % what)
     return s[:3]
+
+
+def _on_device(**tensors):
+    for what, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % what)
 
 
 def _attn_index(t, count, what):
@@ -776,6 +780,7 @@ def attn_args(q, k, v, *, causal=True, window=0, scale=None, q_lengths=None, k_l
     sk, hk, dv = k.shape[1], k.shape[2], v.shape[3]
     qs, ks, vs = (_attn_heads(q, "q", batch, sq, hq, dk), _attn_heads(k, "k", batch, sk, hk, dk),
                   _attn_heads(v, "v", batch, sk, hk, dv))
+    _on_device(q=q, k=k, v=v)
     docs = _attn_index(documents, None, "documents")
     n_docs = documents.shape[0] - 1 if documents is not None else 0
     return _PACK_ATTN_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), _attn_index(q_lengths, batch, "q_lengths"),
@@ -802,6 +807,7 @@ def gbo_attn_forward(args, q, v, y, workspace=None, *, lse=None, dev_status=None
     into ``y`` (batch, seq, heads, dv) and ``lse`` (batch, seq, heads float32)."""
     b, sq, hq, _ = q.shape
     ys = _PACK_STRIDE(*_attn_heads(y, "y", b, sq, hq, v.shape[3]))
+    _on_device(y=y)
     ws, nbytes = _workspace(workspace)
     _check(lib().gbo_attn_forward(args, y.data_ptr(), ys, _out_f32(lse, b * sq * hq, "lse"), ws, nbytes,
                                   _dev_ptr(dev_status, "dev_status"), _stream(stream)))
@@ -813,6 +819,7 @@ def gbo_attn_backward(args, q, k, v, dy, y, lse, workspace, *, dq=None, dk=None,
     b, sq, hq, d = q.shape
     sk, hk, e = v.shape[1:]
     sizes = (("dy", dy, sq, hq, e), ("y", y, sq, hq, e), ("dq", dq, sq, hq, d), ("dk", dk, sk, hk, d), ("dv", dv, sk, hk, e))
+    _on_device(dy=dy, y=y, dq=dq, dk=dk, dv=dv)
     ptrs, strides = [], []
     for what, t, n, h, w in sizes:
         ptrs.append(0 if t is None else t.data_ptr())

@@ -11,7 +11,7 @@
 // sum crosses CTAs: no atomics, results that repeat bit for bit, no fp32 dQ in
 // memory.  Every sum stays in TMEM for a CTA's whole walk, the query heads that
 // share a key head among them.  P and dS are rounded to bf16 once, as operands of
-// products (2^-9 relative each); sums are fp32.
+// products (by 2^-8 of them at most); sums are fp32.
 #include "attn_common.cuh"
 
 namespace gbo {

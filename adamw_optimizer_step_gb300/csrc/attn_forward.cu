@@ -14,7 +14,7 @@
 // m is a running maximum that is moved, and O rescaled, only when a row's
 // maximum grows by more than 2^8: until then P is at most 2^8 and its rounding
 // is relative, so nothing is lost; sums are fp32.  P is rounded to bf16 once
-// (2^-9 relative, as the operand of the product); the sum takes it unrounded.
+// (2^-8 of it at most, as the operand of the product); the sum takes it unrounded.
 #include "attn_common.cuh"
 
 namespace gbo {

@@ -1,17 +1,19 @@
 """Torch-facing calls of the operators around the optimizer step: rotary
-positions, per-head q/k norms with rotation, and the tied classifier's cross
-entropy with its gradients.
+positions, per-head q/k norms with rotation, attention, the residual update with
+the norms around it, dropout, and the tied classifier's cross entropy, each with
+its gradients.
 
 Each allocates its outputs and scratch with torch's allocator and makes one
 library call, on torch's current stream (under ``torch.cuda.stream(s)`` both the
 memory and the work belong to ``s``; the binding's functions take a stream and
 the caller's buffers).  No call waits for the GPU, so what is found there is told
-in ``dev_status`` alone, a CUDA int32 of the caller's that the cross entropy ORs
-its ``GBO_STATUS_*`` bits into: without one, a label outside the vocabulary
-leaves its row out and a wait that ran out (``GBO_STATUS_TIMEOUT``, outputs invalid)
-goes unnoticed.  ``rotary_autograd``, ``qk_norm_rotary_autograd``
-and ``linear_cross_entropy_loss`` are the same operators inside autograd, so
-that ``loss.backward()`` leaves the gradients that
+in ``dev_status`` alone, a CUDA int32 of the caller's that the cross entropy,
+attention and the residual update OR their ``GBO_STATUS_*`` bits into: without one,
+a label outside the vocabulary leaves its row out and a wait that ran out
+(``GBO_STATUS_TIMEOUT``, outputs invalid) goes unnoticed.  ``rotary_autograd``,
+``qk_norm_rotary_autograd``, ``attention_autograd``, ``residual_norm_autograd``,
+``dropout_autograd`` and ``linear_cross_entropy_loss`` are the same operators inside
+autograd, so that ``loss.backward()`` leaves the gradients that
 :class:`~.routing.HybridOptimizer` steps.
 
 Heads are (batch, seq, heads, dim) tensors whose last axis is contiguous; any
@@ -376,6 +378,130 @@ class _LinearCrossEntropy(torch.autograd.Function):
                             upstream=up.float().reshape(1), logit_scale=logit_scale, z_loss=z_loss, keep=keep,
                             dev_status=dev_status)
         return dh, dw, None, None, None, None, None, None, None
+
+
+def _aligned_heads(t):
+    """``t`` as attention takes it: consecutive head elements, positive strides of whole
+    16-byte pieces (autograd hands over expanded gradients and slices of any place)."""
+    s, n = t.stride(), t.shape
+    ok = s[3] == 1 and t.data_ptr() % 16 == 0 and all(n[i] <= 1 or (s[i] > 0 and s[i] % 8 == 0) for i in range(3))
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, q_lengths, k_lengths, documents, causal, window, scale, dev_status):
+        mask = dict(causal=causal, window=window, scale=scale)
+        y, lse = attention(q, k, v, q_lengths=q_lengths, k_lengths=k_lengths, documents=documents, return_lse=True,
+                           dev_status=dev_status, **mask)
+        ctx.rest = (mask, dev_status)
+        ctx.save_for_backward(q, k, v, y, lse, q_lengths, k_lengths, documents)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        q, k, v, y, lse, q_lengths, k_lengths, documents = ctx.saved_tensors
+        mask, dev_status = ctx.rest
+        grads = attention_backward(_aligned_heads(dy), q, k, v, y, lse, q_lengths=q_lengths, k_lengths=k_lengths,
+                                   documents=documents, wanted=ctx.needs_input_grad[:3], dev_status=dev_status, **mask)
+        return (*grads, None, None, None, None, None, None, None)
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, block, gate, scale, post_gain, pre_gain, seed, rest):
+        ctx.set_materialize_grads(False)
+        x_new, h = residual_norm(x, block, gate=gate, scale=scale, post_gain=post_gain, pre_gain=pre_gain, seed=seed,
+                                 **rest)
+        ctx.rest = rest
+        ctx.host_seed = None if isinstance(seed, torch.Tensor) else seed
+        ctx.save_for_backward(x_new, block, gate, scale, post_gain, pre_gain, seed if ctx.host_seed is None else None)
+        return x_new, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dx_out, dh):
+        if dx_out is None and dh is None:
+            return (None,) * 8
+        x_new, block, gate, scale, post_gain, pre_gain, seed = ctx.saved_tensors
+        rest = dict(ctx.rest, seed=seed if ctx.host_seed is None else ctx.host_seed)
+        names = ("dx", "dblock", "dgate", "dscale", "dpost_gain", "dpre_gain")
+        wanted = [n for n, need in zip(names, ctx.needs_input_grad) if need]
+        if dh is None:  # nothing comes through the norm behind the update
+            rest["pre_norm"], pre_gain = False, None
+        d = x_new.shape[-1]
+        rows = lambda t: None if t is None else _rows(_flat(t, d))  # noqa: E731
+        dx_out, dh = (t if t is None or t.stride(0) >= d else t.contiguous() for t in (rows(dx_out), rows(dh)))
+        g = residual_norm_backward(dx_out, dh, x_new, block, gate=gate, scale=scale, post_gain=post_gain,
+                                   pre_gain=pre_gain, wanted=wanted, **rest)
+        return (*(g[n] for n in names), None, None)
+
+
+class _Norm(torch.autograd.Function):
+    """The norm alone: the residual update without a block."""
+
+    @staticmethod
+    def forward(ctx, x, gain, eps, dev_status):
+        ctx.rest = dict(eps=eps, dev_status=dev_status)
+        ctx.save_for_backward(x, gain)
+        return residual_norm(x, pre_gain=gain, **ctx.rest)[1]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        x, gain = ctx.saved_tensors
+        wanted = [n for n, need in zip(("dx", "dpre_gain"), ctx.needs_input_grad) if need]
+        dh = _rows(_flat(dh, x.shape[-1]))
+        dh = dh if dh.stride(0) >= x.shape[-1] else dh.contiguous()
+        g = residual_norm_backward(None, dh, x, pre_gain=gain, wanted=wanted, **ctx.rest)
+        return g["dx"], g["dpre_gain"], None, None
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, offset):
+        ctx.rest = (p, offset)
+        ctx.host_seed = None if isinstance(seed, torch.Tensor) else seed
+        ctx.save_for_backward(seed if ctx.host_seed is None else None)
+        return dropout(x, p, seed, offset=offset)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        p, offset = ctx.rest
+        seed = ctx.saved_tensors[0] if ctx.host_seed is None else ctx.host_seed
+        return dropout(dy.contiguous(), p, seed, offset=offset), None, None, None
+
+
+def attention_autograd(q, k, v, *, causal=True, window=0, scale=None, q_lengths=None, k_lengths=None, documents=None,
+                       dev_status=None):
+    """:func:`attention` with its gradients by q, k and v.  ``scale`` is a constant."""
+    _constant(scale, "scale")
+    return _Attention.apply(q, k, v, q_lengths, k_lengths, documents, bool(causal), int(window),
+                            None if scale is None else float(scale), dev_status)
+
+
+def residual_norm_autograd(x, block=None, *, post_norm=False, pre_norm=True, post_gain=None, pre_gain=None, gate=None,
+                           gate_kind="sigmoid", scale=None, dropout=0.0, seed=0, offset=0, eps=1e-6, dev_status=None):
+    """:func:`residual_norm` with its gradients by the stream, the block's output, the gate,
+    the scale and the gains.  Between the passes x' is kept, and no mask; ``dropout`` and
+    ``eps`` are constants."""
+    _constant(dropout, "dropout")
+    _constant(eps, "eps")
+    if block is None:
+        if post_norm or not pre_norm or gate is not None or scale is not None or post_gain is not None or float(dropout):
+            raise ValueError("without a block's output there is the norm alone")
+        return x, _Norm.apply(x, pre_gain, float(eps), dev_status)
+    rest = dict(post_norm=bool(post_norm), pre_norm=bool(pre_norm), gate_kind=gate_kind, dropout=float(dropout),
+                offset=int(offset), eps=float(eps), dev_status=dev_status)
+    return _ResidualNorm.apply(x, block, gate, scale, post_gain, pre_gain, seed, rest)
+
+
+def dropout_autograd(x, p, seed, *, offset=0):
+    """:func:`dropout` with its gradient (the same elements, drawn again)."""
+    _constant(p, "p")
+    return _Dropout.apply(x, float(p), seed, int(offset))
 
 
 def rotary_autograd(x, positions, spec):

@@ -4,9 +4,10 @@ around it, then asked for tokens one at a time.
     python examples/tied_lm.py [--steps 60]
 
 Per block: a fused projection gives queries, keys and values; the q/k norms
-(their gains on the AdamW path) and the rotation are one call each way; the
-loss of the tied embedding (AdamW, float32) is one call each way.  The
-projections step on the Muon path.  Sequences count upwards from a random
+(their gains on the AdamW path) and the rotation are one call each way, attention
+is one, and so is each residual update with the norm before the next block; the
+loss of the tied embedding (AdamW, float32) is one call each way.  The projections
+step on the Muon path.  Sequences count upwards from a random
 token with a random step, so what comes next is learnable in a few dozen steps.
 """
 
@@ -41,18 +42,24 @@ class Attention(nn.Module):
         q, k, v = heads.split((HEADS, KV_HEADS, KV_HEADS), dim=2)
         if torch.is_grad_enabled():
             q, k = layers.qk_norm_rotary_autograd(q, k, self.q_norm.weight, self.k_norm.weight, positions, self.spec)
+            y = layers.attention_autograd(q, k, v)
         else:
             q, k = layers.qk_norm_rotary(q, k, self.q_norm.weight, self.k_norm.weight, positions, self.spec)
-        if cache is not None:  # one token at a time: keys and values of the earlier ones
-            cache.append((k, v))
-            k, v = (torch.cat(t, dim=1) for t in zip(*cache))
-        q, k, v = (t.float().transpose(1, 2) for t in (q, k, v))
-        k, v = (t.repeat_interleave(HEADS // KV_HEADS, dim=1) for t in (k, v))
-        score = q @ k.transpose(-1, -2) / DIM ** 0.5
-        if cache is None:
-            score = score.masked_fill(torch.ones(s, s, dtype=torch.bool, device=x.device).triu(1), float("-inf"))
-        y = (score.softmax(-1) @ v).transpose(1, 2).reshape(b, s, HEADS * DIM)
-        return self.out(y.to(torch.bfloat16))
+            if cache is None:
+                y = layers.attention(q, k, v)
+            else:  # one token at a time: behind the keys and values of the earlier ones
+                keys, values, length = cache
+                keys[:, positions] = k[:, 0]
+                values[:, positions] = v[:, 0]
+                length.fill_(positions + 1)
+                y = layers.attention(q, keys, values, k_lengths=length)
+        return self.out(y.reshape(b, s, HEADS * DIM))
+
+
+def update(x, block, norm):
+    """(x + block, its norm): the residual stream and the next block's input."""
+    call = layers.residual_norm_autograd if torch.is_grad_enabled() else layers.residual_norm
+    return call(x, block, pre_gain=norm.weight)
 
 
 class Layer(nn.Module):
@@ -64,10 +71,11 @@ class Layer(nn.Module):
         self.gate_up_proj = nn.Linear(WIDTH, 2 * FFN, bias=False, dtype=torch.bfloat16)
         self.down = nn.Linear(FFN, WIDTH, bias=False, dtype=torch.bfloat16)
 
-    def forward(self, x, positions, cache=None):
-        x = x + self.attention(self.norm1(x.float()).to(torch.bfloat16), positions, cache)
-        gate, up = self.gate_up_proj(self.norm2(x.float()).to(torch.bfloat16)).chunk(2, dim=-1)
-        return x + self.down(F.silu(gate) * up)
+    def forward(self, x, h, next_norm, positions, cache=None):
+        """From the stream and its norm by ``norm1`` to the stream and its norm by ``next_norm``."""
+        x, h = update(x, self.attention(h, positions, cache), self.norm2)
+        gate, up = self.gate_up_proj(h).chunk(2, dim=-1)
+        return update(x, self.down(F.silu(gate) * up), next_norm)
 
 
 class TiedLM(nn.Module):
@@ -80,10 +88,12 @@ class TiedLM(nn.Module):
         self.norm = nn.RMSNorm(WIDTH)
 
     def hidden(self, tokens, positions, caches=None):
-        x = self.embedding(tokens).to(torch.bfloat16)
+        x, h = update(self.embedding(tokens).to(torch.bfloat16), None, self.layers[0].norm1)
         for n, layer in enumerate(self.layers):
-            x = layer(x, positions, None if caches is None else caches[n])
-        return self.norm(x.float()).to(torch.bfloat16)
+            last = n + 1 == len(self.layers)
+            x, h = layer(x, h, self.norm if last else self.layers[n + 1].norm1, positions,
+                         None if caches is None else caches[n])
+        return h
 
     def loss(self, tokens, labels):
         h = self.hidden(tokens, torch.arange(tokens.shape[1], device=tokens.device))
@@ -122,7 +132,8 @@ def train(steps, seed=0):
 def answer(model, prompt, count):
     """Greedy continuation of one prompt, a token at a time over the kept keys
     and values, and the model's loss on each token it gives."""
-    caches = [[] for _ in model.layers]
+    made = lambda: torch.zeros(1, len(prompt) + count, KV_HEADS, DIM, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    caches = [(made(), made(), torch.zeros(1, dtype=torch.int32, device="cuda")) for _ in model.layers]
     tokens, losses = list(prompt), []
     table = model.embedding.weight.to(torch.bfloat16)
     for t in range(len(prompt) + count - 1):
