@@ -653,7 +653,7 @@ extern "C" int gbo_attn_backward(const gbo_attn_args *a, const gbo_attn_grads *g
   if (keys && g->dk && (rc = check_heads(g->dk, g->dk_stride, a->batch, a->sk, a->k_heads)) != GBO_OK) return rc;
   if (keys && g->dv && (rc = check_heads(g->dv, g->dv_stride, a->batch, a->sk, a->k_heads)) != GBO_OK) return rc;
   int dev, sm = 0;
-  if ((rc = require_device(&dev, &sm)) != GBO_OK) return rc;
+  if ((rc = attn_device(&dev, &sm)) != GBO_OK) return rc;
   const int64_t rows = a->batch * a->sq * a->q_heads;
   if (queries && keys) {
     if (!workspace || ws_bytes < (size_t)rows * sizeof(float2))

@@ -531,6 +531,15 @@ int attn_cuda(cudaError_t e) {
   return report_error(GBO_ERR_CUDA, msg);
 }
 
+// The current device, made current in the driver too: on a thread that has made no
+// runtime call yet (autograd's, say) the driver has no context to encode maps in.
+int attn_device(int *dev, int *sm) {
+  const int rc = require_device(dev, sm);
+  if (rc != GBO_OK) return rc;
+  const cudaError_t e = cudaSetDevice(*dev);
+  return e == cudaSuccess ? GBO_OK : attn_cuda(e);
+}
+
 // A map over (dim, heads, tokens, batch) of bf16 heads, box 64 x heads x tokens.
 bool heads_map(CUtensorMap *map, const void *base, int64_t dim, int64_t heads, int64_t tokens, int64_t batch,
                const int64_t stride[3], uint32_t box_heads, uint32_t box_tokens) {

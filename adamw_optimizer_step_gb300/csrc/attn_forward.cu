@@ -787,7 +787,7 @@ extern "C" int gbo_attn_forward(const gbo_attn_args *a, void *y, const int64_t *
     if ((rc = check_heads(y, y_stride, a->batch, a->sq, a->q_heads)) != GBO_OK) return rc;
   }
   int dev, sm = 0;
-  if ((rc = require_device(&dev, &sm)) != GBO_OK) return rc;
+  if ((rc = attn_device(&dev, &sm)) != GBO_OK) return rc;
   if (none) return report_ok();
   AttnShape S;
   AttnMask M;

@@ -381,6 +381,23 @@ def test_autograd():
         g.sum().backward()
 
 
+def test_on_a_thread_of_its_own():
+    """A thread whose first call into CUDA is the operator's."""
+    import threading
+    q, k, v, dy = inputs(1, 130, 130, 2, 1, 64, 64, seed=16)
+    y, lse = layers.attention(q, k, v, return_lse=True)
+    grads = layers.attention_backward(dy, q, k, v, y, lse)
+    torch.cuda.synchronize()
+    for call, want in ((lambda: (layers.attention(q, k, v),), (y,)),
+                       (lambda: layers.attention_backward(dy, q, k, v, y, lse), grads)):
+        got = []
+        t = threading.Thread(target=lambda: got.append(call()))
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert got and all(torch.equal(a, b) for a, b in zip(got[0], want))
+
+
 def test_stream_and_graph():
     """On a side stream, and captured: a replay takes the lengths and values it finds."""
     q, k, v, dy = inputs(2, 130, 600, 4, 2, 64, 64, seed=17)
