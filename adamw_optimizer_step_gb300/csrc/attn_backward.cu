@@ -140,11 +140,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
   const AttnShape &A = P.shape;
   // early keys first: with a causal mask most queries see them
   int idx = blockIdx.x;
-  const int kh = idx % A.k_heads;
-  idx /= A.k_heads;
-  const int b = idx % A.batch, k0 = idx / A.batch * kAttnTile;
+  const int kh = A.by_k_heads.split(idx), b = A.by_batch.split(idx), k0 = idx * kAttnTile;
   const AttnSeq seq = attn_seq(P.mask, b);
-  const int tokens = kQt >> A.pack;
+  const int shift = (kQt == 128 ? 7 : 6) - A.pack, tokens = 1 << shift;
   const DocWindow docs = doc_window(P.mask, k0);
   int tt0 = 0, n_tok = 0, full_lo = 0, full_hi = 0;  // token tiles that see these keys
   {
@@ -152,12 +150,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
     if (e > a) {
       const Span first = queries_of(P.mask, seq, docs, a), last = queries_of(P.mask, seq, docs, e - 1);
       if (last.hi > first.lo) {
-        tt0 = first.lo / tokens, n_tok = (last.hi + tokens - 1) / tokens - tt0;
+        tt0 = first.lo >> shift, n_tok = ((last.hi + tokens - 1) >> shift) - tt0;
         full_lo = last.lo, full_hi = first.hi;
       }
     }
   }
-  const int steps = n_tok * A.head_blocks, group = A.q_heads / A.k_heads;
+  const int steps = n_tok * A.head_blocks, group = A.group;
   const uint32_t kt = smem_u32(smem), vt = kt + C::kKTile, qring = kt + C::kRing;
   const uint32_t dring = qring + C::kQStages * C::kQStage;
   float *const stats = reinterpret_cast<float *>(smem + C::kStatAt);
@@ -366,7 +364,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
           if (lane == 0 && k0 + r0 < P.mask.sk) {
             tma_store_4d(is_k ? &P.o1 : &P.o2, out + blk * kAttnBlock + r0 * 128, 64 * blk, kh, k0 + r0, b);
             bulk_commit();
-            bulk_wait_all();
+            bulk_wait_read<0>();  // (the writes themselves end with the kernel)
           }
           __syncwarp();
         }
@@ -436,12 +434,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
   pdl_wait();
 
   const AttnShape &A = P.shape;
-  const int hb_all = A.k_heads * A.head_blocks;
   int idx = blockIdx.x;
-  const int hb = idx % hb_all;
-  idx /= hb_all;
-  const int b = idx % A.batch, tb = P.tiles - 1 - idx / A.batch;  // later queries first
-  const int kh = hb / A.head_blocks, h0 = kh * (A.q_heads / A.k_heads) + ((hb % A.head_blocks) << A.pack);
+  int kh = A.by_all.split(idx);
+  const int b = A.by_batch.split(idx), tb = P.tiles - 1 - idx;  // later queries first
+  const int hb = A.by_blocks.split(kh), h0 = kh * A.group + (hb << A.pack);
   const int tokens = kAttnTile >> A.pack, t0 = tb * tokens;
   const AttnSeq seq = attn_seq(P.mask, b);
   const DocWindow docs = doc_window(P.mask, t0);
@@ -585,7 +581,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
         if (lane == 0 && t0 + (r0 >> A.pack) < P.mask.sq) {
           tma_store_4d(&P.o1, qt + blk * kAttnBlock + r0 * 128, 64 * blk, h0, t0 + (r0 >> A.pack), b);
           bulk_commit();
-          bulk_wait_all();
+          bulk_wait_read<0>();  // (the writes themselves end with the kernel)
         }
         __syncwarp();
       }

@@ -130,6 +130,27 @@ __device__ __forceinline__ Span queries_of(const AttnMask &M, const AttnSeq &s, 
   return r;
 }
 
+// Division by a number known to the host, of numbers below 2^31 (a division takes
+// some 100 clocks, and a CTA begins with several before its first load): with
+// 2^shift >= d, n / d = (high(mul n) + n) >> shift.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift); }
+  // n becomes n / d; returns what is left over
+  __device__ __forceinline__ int split(int &n) const {
+    const int q = div(n), r = n - q * (int)d;
+    n = q;
+    return r;
+  }
+};
+
+inline FastDiv fast_div(int64_t d) {
+  FastDiv f = {(uint32_t)d, 0, 0};
+  while ((int64_t(1) << f.shift) < d) ++f.shift;
+  f.mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << f.shift) - (uint64_t)d)) / (uint64_t)d + 1);
+  return f;
+}
+
 // Heads and tiles.  The `group` query heads of one key head are cut into
 // blocks of 2^pack heads, and a tile's rows are those heads of consecutive
 // tokens: row r is token t0 + (r >> pack), head h0 + (r & mask).  Heads of a
@@ -140,6 +161,8 @@ struct AttnShape {
   int32_t dk, dv, kb, vb;                              // elements of a head; blocks of 64 of them
   int32_t k_steps, v_cols;                             // dk in steps of 16, dv rounded up to 16
   float scale, scale2;                                 // scale, and scale log2(e)
+  int32_t group;                                       // query heads of a key head
+  FastDiv by_batch, by_k_heads, by_blocks, by_all;     // by_all: head blocks of all key heads
 };
 
 // What a row tile sees: tiles [j0, j1) of 128 keys, of which those within
@@ -610,6 +633,9 @@ void fill_shape(const gbo_attn_args *a, AttnShape *S, AttnMask *M, int most_pack
   S->pack = 0;
   while (S->pack < most_pack && group % (2 << S->pack) == 0) ++S->pack;
   S->head_blocks = group >> S->pack;
+  S->group = group;
+  S->by_batch = fast_div(std::max<int64_t>(a->batch, 1)), S->by_k_heads = fast_div(a->k_heads);
+  S->by_blocks = fast_div(S->head_blocks), S->by_all = fast_div((int64_t)a->k_heads * S->head_blocks);
   S->dk = a->dk, S->dv = a->dv;
   S->kb = (a->dk + 63) / 64, S->vb = (a->dv + 63) / 64;
   S->k_steps = (a->dk + 15) / 16, S->v_cols = (a->dv + 15) / 16 * 16;

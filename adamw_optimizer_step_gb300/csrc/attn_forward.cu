@@ -52,6 +52,7 @@ struct FwdParams {
   int32_t *status;
   int64_t rows;     // batch * sq * q_heads
   int32_t token_blocks, splits;
+  FastDiv by_splits;
 };
 
 template <int kKb, int kVb>
@@ -103,14 +104,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
 
   const AttnShape &A = P.shape;
   // later queries first: with a causal mask they have the most keys
-  const int hb_all = A.k_heads * A.head_blocks;
   int idx = blockIdx.x;
-  const int split = idx % P.splits;
-  idx /= P.splits;
-  const int hb = idx % hb_all;
-  idx /= hb_all;
-  const int b = idx % A.batch, tb = P.token_blocks - 1 - idx / A.batch;
-  const int kh = hb / A.head_blocks, h0 = kh * (A.q_heads / A.k_heads) + ((hb % A.head_blocks) << A.pack);
+  const int split = P.by_splits.split(idx);
+  int kh = A.by_all.split(idx);
+  const int b = A.by_batch.split(idx), tb = P.token_blocks - 1 - idx;
+  const int hb = A.by_blocks.split(kh), h0 = kh * A.group + (hb << A.pack);
   const int tokens = kAttnTile >> A.pack, t0 = tb * 2 * tokens;
   const AttnSeq seq = attn_seq(P.mask, b);
   TileKeys tk[2];
@@ -324,7 +322,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
             const int r0 = (warp & 3) * 32;  // this warp's rows
             tma_store_4d(&P.y, out + blk * kAttnBlock + r0 * 128, 64 * blk, h0, t0 + t * tokens + (r0 >> A.pack), b);
             bulk_commit();
-            bulk_wait_all();
+            bulk_wait_read<0>();  // (the writes themselves end with the kernel)
           }
           __syncwarp();
         }
@@ -824,7 +822,7 @@ extern "C" int gbo_attn_forward(const gbo_attn_args *a, void *y, const int64_t *
     memset(&F, 0, sizeof F);
     F.mask = M, F.shape = S;
     F.lse = lse, F.part_o = part_o, F.part_lse = part_lse, F.status = dev_status;
-    F.rows = p.rows, F.token_blocks = p.token_blocks, F.splits = p.splits;
+    F.rows = p.rows, F.token_blocks = p.token_blocks, F.splits = p.splits, F.by_splits = fast_div(p.splits);
     const uint32_t heads = 1u << S.pack;
     maps = heads_map(&F.q, a->q, a->dk, a->q_heads, a->sq, a->batch, a->q_stride, heads, kAttnTile >> S.pack) &&
            heads_map(&F.y, y, a->dv, a->q_heads, a->sq, a->batch, y_stride, heads, 32 >> S.pack);
