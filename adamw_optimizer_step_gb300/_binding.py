@@ -744,23 +744,16 @@ _PACK_ATTN_GRADS = struct.Struct("@6P15q").pack       # AttnGrads
 _PACK_STRIDE = struct.Struct("@3q").pack
 
 
-def _attn_heads(t, what, batch, seq, heads, dim):
+def _attn_heads(t, what, shape):
     """Strides of a (batch, seq, heads, dim) bfloat16 tensor whose head elements are consecutive."""
     if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be bfloat16, got %s" % (what, t.dtype))
-    shape = t.shape
-    if len(shape) != 4 or shape[0] != batch or shape[1] != seq or shape[2] != heads or shape[3] != dim:
-        raise ValueError("%s must be (%d, %d, %d, %d), got %s" % (what, batch, seq, heads, dim, tuple(shape)))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (what, tuple(shape), tuple(t.shape)))
     s = t.stride()
     if s[3] != 1:
         raise ValueError("the elements of a head of %s must be consecutive" % what)
     return s[:3]
-
-
-def _on_device(**tensors):
-    for what, t in tensors.items():
-        if t is not None and not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % what)
 
 
 def _attn_index(t, count, what):
@@ -776,11 +769,14 @@ def attn_args(q, k, v, *, causal=True, window=0, scale=None, q_lengths=None, k_l
     (batch, seq, heads, dim), lengths int32 (batch), documents int32 (count + 1)."""
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be (batch, seq, heads, dim)")
-    batch, sq, hq, dk = q.shape
-    sk, hk, dv = k.shape[1], k.shape[2], v.shape[3]
-    qs, ks, vs = (_attn_heads(q, "q", batch, sq, hq, dk), _attn_heads(k, "k", batch, sk, hk, dk),
-                  _attn_heads(v, "v", batch, sk, hk, dv))
-    _on_device(q=q, k=k, v=v)
+    q_shape, v_shape = q.shape, v.shape
+    batch, sq, hq, dk = q_shape
+    _, sk, hk, _ = k.shape
+    dv = v_shape[3]
+    qs, ks, vs = (_attn_heads(q, "q", q_shape), _attn_heads(k, "k", (batch, sk, hk, dk)),
+                  _attn_heads(v, "v", (batch, sk, hk, dv)))
+    if not (q.is_cuda and k.is_cuda and v.is_cuda):
+        raise ValueError("q, k and v must be CUDA tensors")
     docs = _attn_index(documents, None, "documents")
     n_docs = documents.shape[0] - 1 if documents is not None else 0
     return _PACK_ATTN_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), _attn_index(q_lengths, batch, "q_lengths"),
@@ -806,8 +802,9 @@ def gbo_attn_forward(args, q, v, y, workspace=None, *, lse=None, dev_status=None
     """Attention of ``args`` (of :func:`attn_args`, from ``q`` and ``v`` among others)
     into ``y`` (batch, seq, heads, dv) and ``lse`` (batch, seq, heads float32)."""
     b, sq, hq, _ = q.shape
-    ys = _PACK_STRIDE(*_attn_heads(y, "y", b, sq, hq, v.shape[3]))
-    _on_device(y=y)
+    ys = _PACK_STRIDE(*_attn_heads(y, "y", (b, sq, hq, v.shape[3])))
+    if not y.is_cuda:
+        raise ValueError("y must be a CUDA tensor")
     ws, nbytes = _workspace(workspace)
     _check(lib().gbo_attn_forward(args, y.data_ptr(), ys, _out_f32(lse, b * sq * hq, "lse"), ws, nbytes,
                                   _dev_ptr(dev_status, "dev_status"), _stream(stream)))
@@ -816,14 +813,19 @@ def gbo_attn_forward(args, q, v, y, workspace=None, *, lse=None, dev_status=None
 def gbo_attn_backward(args, q, k, v, dy, y, lse, workspace, *, dq=None, dk=None, dv=None, dev_status=None, stream=None):
     """Gradients into ``dq``, ``dk`` and ``dv``, whichever are given, from the
     forward's ``y`` and ``lse``."""
-    b, sq, hq, d = q.shape
-    sk, hk, e = v.shape[1:]
-    sizes = (("dy", dy, sq, hq, e), ("y", y, sq, hq, e), ("dq", dq, sq, hq, d), ("dk", dk, sk, hk, d), ("dv", dv, sk, hk, e))
-    _on_device(dy=dy, y=y, dq=dq, dk=dk, dv=dv)
-    ptrs, strides = [], []
-    for what, t, n, h, w in sizes:
-        ptrs.append(0 if t is None else t.data_ptr())
-        strides += _ZERO3 if t is None else _attn_heads(t, what, b, n, h, w)
+    q_shape, v_shape = q.shape, v.shape
+    b, sq, hq, _ = q_shape
+    y_shape = (b, sq, hq, v_shape[3])
+    ptrs, strides = [], ()
+    for what, t, shape in (("dy", dy, y_shape), ("y", y, y_shape), ("dq", dq, q_shape), ("dk", dk, k.shape), ("dv", dv, v_shape)):
+        if t is None:
+            ptrs.append(0)
+            strides += _ZERO3
+            continue
+        strides += _attn_heads(t, what, shape)
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % what)
+        ptrs.append(t.data_ptr())
     grads = _PACK_ATTN_GRADS(ptrs[0], ptrs[1], _out_f32(lse, b * sq * hq, "lse"), *ptrs[2:], *strides)
     ws, nbytes = _workspace(workspace)
     _check(lib().gbo_attn_backward(args, grads, ws, nbytes, _dev_ptr(dev_status, "dev_status"), _stream(stream)))

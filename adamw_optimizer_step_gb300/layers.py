@@ -166,11 +166,6 @@ def linear_cross_entropy_grad(h, w, labels, *, z_loss=0.0, logit_scale=1.0, mean
 # ---------------------------------------------------------------------------
 # attention
 
-def _scratch(need, device):
-    """A workspace of ``need`` bytes, or None where none is needed."""
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-
-
 def attention(q, k, v, *, causal=True, window=0, scale=None, q_lengths=None, k_lengths=None, documents=None, out=None,
               return_lse=False, dev_status=None):
     """Softmax attention of ``q`` (batch, sq, q_heads, dk) over ``k`` and ``v`` (batch,
@@ -188,10 +183,14 @@ def attention(q, k, v, *, causal=True, window=0, scale=None, q_lengths=None, k_l
     :func:`attention_backward` takes."""
     args = B.attn_args(q, k, v, causal=causal, window=window, scale=scale, q_lengths=q_lengths, k_lengths=k_lengths,
                        documents=documents)
-    b, sq, hq, _ = q.shape
-    y = torch.empty(b, sq, hq, v.shape[3], dtype=q.dtype, device=q.device) if out is None else out
-    lse = torch.empty(b, sq, hq, dtype=torch.float32, device=q.device) if return_lse else None
-    ws = _scratch(B.gbo_attn_forward_workspace_bytes(args), q.device)
+    shape = q.shape
+    if out is not None:
+        y = out
+    else:
+        y = _like(q) if shape[3] == v.shape[3] else q.new_empty((*shape[:3], v.shape[3]))
+    lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+    need = B.gbo_attn_forward_workspace_bytes(args)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     B.gbo_attn_forward(args, q, v, y, ws, lse=lse, dev_status=dev_status)
     return (y, lse) if return_lse else y
 
@@ -202,18 +201,19 @@ def attention_backward(dy, q, k, v, y, lse, *, causal=True, window=0, scale=None
     output ``y``, its ``lse`` and the gradient ``dy``; the same masks as there."""
     args = B.attn_args(q, k, v, causal=causal, window=window, scale=scale, q_lengths=q_lengths, k_lengths=k_lengths,
                        documents=documents)
-    grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device) if w else None for t, w in zip((q, k, v), wanted)]
-    ws = _scratch(B.gbo_attn_backward_workspace_bytes(args), q.device)
-    B.gbo_attn_backward(args, q, k, v, dy, y, lse, ws, dq=grads[0], dk=grads[1], dv=grads[2], dev_status=dev_status)
-    return tuple(grads)
+    dq, dk, dv = _like(q) if wanted[0] else None, _like(k) if wanted[1] else None, _like(v) if wanted[2] else None
+    need = B.gbo_attn_backward_workspace_bytes(args)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    B.gbo_attn_backward(args, q, k, v, dy, y, lse, ws, dq=dq, dk=dk, dv=dv, dev_status=dev_status)
+    return dq, dk, dv
 
 
 # ---------------------------------------------------------------------------
 # the residual update between two blocks, dropout
 
-def _flat(t, d):
+def _flat(t):
     """Rows of the last axis, as a two-dimensional view where strides allow it."""
-    return t if t.dim() == 2 else t.reshape(-1, d)
+    return t if t is None or t.dim() == 2 else t.reshape(-1, t.shape[-1])
 
 
 def residual_norm(x, block=None, *, post_norm=False, pre_norm=True, post_gain=None, pre_gain=None, gate=None,
@@ -232,21 +232,20 @@ def residual_norm(x, block=None, *, post_norm=False, pre_norm=True, post_gain=No
     ``block=None``: the norm alone, and x' is ``x``.  ``x`` and ``block`` are bfloat16 or
     float32, ``block`` bfloat16 where ``x`` is; ``h`` has the dtype of ``block``.
     ``x_out`` may be ``x``.  Without ``pre_norm`` h is None."""
-    d = x.shape[-1]
-    x2 = _flat(x, d)
-    b2 = None if block is None else _flat(block, d)
-    g2 = None if gate is None else _flat(gate, gate.shape[-1])
+    flat = x.dim() == 2
+    x2, b2, g2 = (x, block, gate) if flat else (_flat(x), _flat(block), _flat(gate))
     bt = x.dtype if block is None else block.dtype
     args = B.residual_args(x2, b2, post_norm=post_norm, pre_norm=pre_norm, post_gain=post_gain, pre_gain=pre_gain,
                            gate=g2, gate_kind=gate_kind, scale=scale, dropout=dropout, seed=seed, offset=offset, eps=eps)
+    shape = x2.shape
     if block is None:
         xo = None
-    elif x_out is None:
-        xo = torch.empty(x2.shape, dtype=x.dtype, device=x.device)
     else:
-        xo = x_out.view(x2.shape)
-    h = torch.empty(x2.shape, dtype=bt, device=x.device) if pre_norm else None
-    B.gbo_residual_forward(args, xo, h, x2.shape, x.dtype, bt, dev_status)
+        xo = _like(x2) if x_out is None else x_out if flat else x_out.view(shape)
+    h = _like(x2, dtype=bt) if pre_norm else None
+    B.gbo_residual_forward(args, xo, h, shape, x.dtype, bt, dev_status)
+    if flat:
+        return x if xo is None else xo, h
     return x if xo is None else xo.view(x.shape), None if h is None else h.view(x.shape)
 
 
@@ -257,24 +256,23 @@ def residual_norm_backward(dx_out, dh, x_new, block=None, *, post_norm=False, pr
     of h (``dh``), the updated stream ``x_new`` and the block's output: a dict with
     ``dx``, ``dblock``, ``dgate``, ``dscale``, ``dpost_gain`` and ``dpre_gain`` (None for
     what was not given or is not ``wanted``)."""
-    d = x_new.shape[-1]
-    shape = x_new.shape
-    x2 = _flat(x_new, d)
-    b2 = None if block is None else _flat(block, d)
-    g2 = None if gate is None else _flat(gate, gate.shape[-1])
+    flat = x_new.dim() == 2
+    x2, b2, g2, dx2, dh2 = ((x_new, block, gate, dx_out, dh) if flat else
+                            (_flat(x_new), _flat(block), _flat(gate), _flat(dx_out), _flat(dh)))
     bt = x_new.dtype if block is None else block.dtype
     args = B.residual_args(x2, b2, post_norm=post_norm, pre_norm=pre_norm, post_gain=post_gain, pre_gain=pre_gain,
                            gate=g2, gate_kind=gate_kind, scale=scale, dropout=dropout, seed=seed, offset=offset, eps=eps)
     like = {"dx": x2, "dblock": b2, "dgate": g2, "dscale": scale, "dpost_gain": post_gain, "dpre_gain": pre_gain}
-    out = {k: torch.empty(t.shape, dtype=t.dtype, device=x2.device) if t is not None and k in wanted else None
-           for k, t in like.items()}
-    sums = sum(out[k] is not None for k in ("dscale", "dpost_gain", "dpre_gain"))
-    ws = _scratch(B._residual_workspace(*x2.shape, sums, x2.device) if sums else 0, x2.device)
-    B.gbo_residual_backward(args, ws, x2.shape, x_new.dtype, bt, dx_out=None if dx_out is None else _flat(dx_out, d),
-                            dh=None if dh is None else _flat(dh, d), dev_status=dev_status, **out)
-    for k, t in (("dx", x_new), ("dblock", block), ("dgate", gate)):
-        if out[k] is not None:
-            out[k] = out[k].view(shape if k != "dgate" else t.shape)
+    out = {k: _like(t) if t is not None and k in wanted else None for k, t in like.items()}
+    sums = (out["dscale"] is not None) + (out["dpost_gain"] is not None) + (out["dpre_gain"] is not None)
+    shape, ws = x2.shape, None
+    if sums:
+        ws = torch.empty(B._residual_workspace(*shape, sums, x2.device), dtype=torch.uint8, device=x2.device)
+    B.gbo_residual_backward(args, ws, shape, x_new.dtype, bt, dx_out=dx2, dh=dh2, dev_status=dev_status, **out)
+    if not flat:
+        for k, t in (("dx", x_new), ("dblock", block), ("dgate", gate)):
+            if out[k] is not None:
+                out[k] = out[k].view(t.shape)
     return out
 
 
@@ -283,11 +281,12 @@ def dropout(x, p, seed, *, offset=0, out=None):
     others divided by the share kept.  Which ones follows from ``seed`` (an int, or a
     CUDA int64 tensor that is read when the kernel runs), ``offset`` and an element's
     place alone: no mask is kept, and the same call on a gradient is the gradient."""
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
     if x.dim() == 2:
+        y = _like(x) if out is None else out
         B.gbo_dropout(x, y, p, seed, offset)
-    else:
-        B.gbo_dropout(x.reshape(1, -1), y.view(1, -1), p, seed, offset)
+        return y
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    B.gbo_dropout(x.reshape(1, -1), y.view(1, -1), p, seed, offset)
     return y
 
 
@@ -431,7 +430,7 @@ class _ResidualNorm(torch.autograd.Function):
         if dh is None:  # nothing comes through the norm behind the update
             rest["pre_norm"], pre_gain = False, None
         d = x_new.shape[-1]
-        rows = lambda t: None if t is None else _rows(_flat(t, d))  # noqa: E731
+        rows = lambda t: None if t is None else _rows(_flat(t))  # noqa: E731
         dx_out, dh = (t if t is None or t.stride(0) >= d else t.contiguous() for t in (rows(dx_out), rows(dh)))
         g = residual_norm_backward(dx_out, dh, x_new, block, gate=gate, scale=scale, post_gain=post_gain,
                                    pre_gain=pre_gain, wanted=wanted, **rest)
@@ -452,7 +451,7 @@ class _Norm(torch.autograd.Function):
     def backward(ctx, dh):
         x, gain = ctx.saved_tensors
         wanted = [n for n, need in zip(("dx", "dpre_gain"), ctx.needs_input_grad) if need]
-        dh = _rows(_flat(dh, x.shape[-1]))
+        dh = _rows(_flat(dh))
         dh = dh if dh.stride(0) >= x.shape[-1] else dh.contiguous()
         g = residual_norm_backward(None, dh, x, pre_gain=gain, wanted=wanted, **ctx.rest)
         return g["dx"], g["dpre_gain"], None, None
