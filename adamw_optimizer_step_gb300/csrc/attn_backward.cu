@@ -392,8 +392,8 @@ struct Dq {
   static constexpr int kKStages = kKb == 1 ? 4 : kKb == 2 ? 3 : 2, kVStages = kKb == 1 ? 4 : kKb == 2 ? 2 : 1;
   static constexpr int kKRing = kQTile + kDTile, kVRing = kKRing + kKStages * kQTile;
   static constexpr int kUsed = kVRing + kVStages * kDTile;
-  // rows, K full/empty, V full/empty, S (two), dP, dP read, dS, drained (two), raw
-  static constexpr int kBars = 1 + 2 * kKStages + 2 * kVStages + 5 + 2 + 1;
+  // rows, K full/empty, V full/empty, S (two), dP, dP read, dS (two), drained (two), raw
+  static constexpr int kBars = 1 + 2 * kKStages + 2 * kVStages + 6 + 2 + 1;
   static constexpr int kSmem = kUsed + kBars * 8 + 16;
   static constexpr uint32_t kDp = kBufs * 128, kDq = kDp + 128;  // TMEM columns
   static_assert(kDq + kKb * 64 <= 512, "TMEM columns");
@@ -411,13 +411,15 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
   const uint32_t rfull = smem_u32(bars), kfull0 = rfull + 8, kempty0 = kfull0 + 8 * C::kKStages;
   const uint32_t vfull0 = kempty0 + 8 * C::kKStages, vempty0 = vfull0 + 8 * C::kVStages;
-  const uint32_t sfull0 = vempty0 + 8 * C::kVStages, dpfull = sfull0 + 16, dpread = dpfull + 8, dsready = dpread + 8;
-  const uint32_t done0 = dsready + 8, raw = done0 + 16;
+  const uint32_t sfull0 = vempty0 + 8 * C::kVStages, dpfull = sfull0 + 16, dpread = dpfull + 8, dsready0 = dpread + 8;
+  const uint32_t done0 = dsready0 + 16, raw = done0 + 16;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 1 + 2 * C::kKStages + 2 * C::kVStages + 3; ++s) mbar_init(rfull + 8 * s, 1);
     mbar_init(dpread, kBwdWarps);
-    mbar_init(dsready, kBwdWarps);
+    // one for each place of S: the next step's S is formed before this step's dS is waited for, so the elementwise
+    // warps may be a step ahead of the wait
+    for (int s = 0; s < 2; ++s) mbar_init(dsready0 + 8 * s, kBwdWarps);
     for (int s = 0; s < 3; ++s) mbar_init(done0 + 8 * s, 1);  // (and raw)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
     bool ok = steps > 0 && guard.wait_warp(rfull, 0) && s_product(0);
     for (int i = 0; i < steps && ok; ++i) {
       if (C::kBufs == 2 && i + 1 < steps && !s_product(i + 1)) break;
-      if (!guard.wait_warp(dsready, i & 1)) break;
+      if (!guard.wait_warp(dsready0 + 8 * (i % C::kBufs), (i / C::kBufs) & 1)) break;
       tc_fence_after();
       if (elect_one()) {
         product_ts<8, 4>(tmem + C::kDq, tmem + (i % C::kBufs) * 128, 32, kring + behind.stage * C::kQTile, kAttnBlock,
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
       tmem_put_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(dsready);
+      if (lane == 0) mbar_arrive(dsready0 + 8 * buf);
     }
     if (ok) ok = guard.wait_warp(done0, 0);
     tc_fence_after();
