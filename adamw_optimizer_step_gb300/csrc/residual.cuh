@@ -338,6 +338,36 @@ __device__ __forceinline__ void cta_sum(float (&v)[kCount], float *red, int &tur
     for (int i = 0; i < kCount; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
+// Four sums over a warp in nine steps' work: each of the first two steps halves the
+// values that a lane carries on.  Lanes 8 i to 8 i + 7 get sum i, in x.
+__device__ __forceinline__ float4 warp_sum4(float4 v, int lane) {
+  const bool hi = lane & 16, up = lane & 8;
+  float a = hi ? v.z : v.x, b = hi ? v.w : v.y;
+  a += __shfl_xor_sync(0xffffffffu, hi ? v.x : v.z, 16);
+  b += __shfl_xor_sync(0xffffffffu, hi ? v.y : v.w, 16);
+  float c = up ? b : a;
+  c += __shfl_xor_sync(0xffffffffu, up ? a : b, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+  return make_float4(c, 0.f, 0.f, 0.f);
+}
+
+// The warps' sums (2 to 16, zeros behind them) added up by every thread.
+__device__ __forceinline__ float4 cta_join(const float4 *red, int warps) {
+  float2 a = f2_of(0.f), b = f2_of(0.f);
+  auto four = [&](int w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = red[w + i];
+      a = f2_add(a, make_float2(v.x, v.y)), b = f2_add(b, make_float2(v.z, v.w));
+    }
+  };
+  four(0);
+  if (warps > 4) four(4);
+  if (warps > 8) four(8), four(12);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
 // Dropout's factors of eight elements, times v.
 __device__ __forceinline__ void drop8(const DropArgs &D, uint64_t key, uint64_t element, float2 *v) {
   const uint4 w = philox(key, element >> 3, D.offset);
@@ -448,7 +478,7 @@ int64_t parts_of(const ResCut &c) { return (int64_t)c.blocks * (c.threads / std:
 
 // The most that any cut of these sizes leaves.
 int64_t most_parts(int64_t n, int64_t d, int sm) {
-  return std::max(parts_of(cut_of(n, d, sm, true, true, 0)), parts_of(cut_of(n, d, sm, true, false, 0)));
+  return std::max(parts_of(cut_of(n, d, sm, true, true, 1)), parts_of(cut_of(n, d, sm, true, false, 1)));
 }
 
 using ResKernel = void (*)(ResParams);

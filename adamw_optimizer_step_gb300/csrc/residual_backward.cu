@@ -160,11 +160,14 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
 // M = scale post_gain (s1 where the scale is one number) and the gate f:
 //   A = sum t f:  dscale = post_gain A, dpost_gain = scale A
 //   da = t M f',  w = g m f M,  mean(w v) = mean(t f M),  do = rho(o) (w - v mean(w v))
+// One join of the CTA a row: the sums that start row i and the one that ends row
+// i - 1 cross the warps together, while the rows' other work fills the time between.
 template <typename XT, typename BT, int kIter>
 __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const __grid_constant__ ResParams P) {
   pdl_launch();
   extern __shared__ __align__(128) uint8_t ring_smem[];
-  __shared__ float red[96];
+  __shared__ float4 red[2][16];
+  __shared__ float red_gate[2][16];
   __shared__ uint64_t bars[kMaxStages];
   __shared__ int32_t late;
   constexpr int N = kIter * 4;  // pairs of elements
@@ -175,6 +178,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
     late = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid < 32) red[tid >> 4][tid & 15] = make_float4(0.f, 0.f, 0.f, 0.f);  // (warps that are not there)
   __syncthreads();
   pdl_wait();
   const int64_t row0 = blockIdx.x, step = gridDim.x;
@@ -220,9 +224,8 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
       pre.put(c, w);
     }
   }
-  int turn = 0;
-  for (int64_t row = row0; row < P.n; row += step) {
-    const uint32_t at = ring.take();
+  // this thread's part of a row's sums: x^2, pre_gain dh x, o^2
+  auto first_sums = [&](uint32_t at, float4 &s) {
     float2 s0 = f2_of(0.f), sx = f2_of(0.f), so = f2_of(0.f);
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
@@ -247,17 +250,60 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
         }
       }
     }
-    float sum[3] = {s0.x + s0.y, sx.x + sx.y, so.x + so.y};
-    if (P.pre || P.post) cta_sum(sum, red, turn);
-    else __syncthreads();
-    if (tid == 0 && row != row0) feed.fill(ring);
+    s.x = s0.x + s0.y, s.y = sx.x + sx.y, s.z = so.x + so.y;
+  };
+  const int warp = tid >> 5, lane = tid & 31;
+  // of the last row: w and v, rho(o), the part of sum w v, of the row gate's gradient
+  float2 g[N], o[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) g[e] = o[e] = f2_of(0.f);
+  float ro = 1.f, j1 = 0.f;
+  float4 sums = make_float4(0.f, 0.f, 0.f, 0.f);  // w: sum w v of the last row
+  int turn = 0;
+  uint32_t at = 0;
+  if (row0 < P.n) first_sums(at = ring.take(), sums);
+  for (int64_t row = row0; row < P.n + step; row += step) {  // (one turn more for the last row's block gradient)
+    const int64_t last = row - step;
+    sums = warp_sum4(sums, lane);
+    if ((lane & 7) == 0) reinterpret_cast<float *>(&red[turn][warp])[lane >> 3] = sums.x;
+    if (P.gate_mode == kGateRow) {
+      const float v = warp_sum(j1);
+      if (lane == 0) red_gate[turn][warp] = v;
+    }
+    __syncthreads();
+    sums = cta_join(red[turn], threads >> 5);
+    if (row != row0) {
+      if (tid == 0) {
+        feed.fill(ring);
+        if (P.gate_mode == kGateRow && P.dgate) {
+          float v = 0.f;
+          for (int w = 0; w < threads >> 5; ++w) v += red_gate[turn][w];
+          st_elem(P.dgate, sizeof(BT) == 2 ? GBO_BF16 : GBO_F32, last * P.das, v);
+        }
+      }
+      if (P.h && P.post) {
+        const float2 m2 = f2_of(-sums.w * P.inv_d), ro2 = f2_of(ro);
+#pragma unroll
+        for (int it = 0; it < kIter; ++it) {
+          const int c = it * threads + tid;
+          if (c < chunks) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) g[4 * it + k] = f2_mul(ro2, f2_fma(o[4 * it + k], m2, g[4 * it + k]));
+            stg8(static_cast<BT *>(P.h) + last * P.hs + c * 8, g + 4 * it);
+          }
+        }
+      }
+    }
+    turn ^= 1;
+    if (row >= P.n) break;
     // (the row is read again: held over the join, two chunks a thread would spill)
-    const float r = rsqrtf(fmaf(sum[0], P.inv_d, P.eps)), ro = P.post ? rsqrtf(fmaf(sum[2], P.inv_d, P.eps)) : 1.f;
-    const float2 r2 = f2_of(r), c2 = f2_of(-sum[1] * P.inv_d * r * r), ro2 = f2_of(ro);
+    const float r = rsqrtf(fmaf(sums.x, P.inv_d, P.eps));
+    ro = P.post ? rsqrtf(fmaf(sums.z, P.inv_d, P.eps)) : 1.f;
+    const float2 r2 = f2_of(r), c2 = f2_of(-sums.y * P.inv_d * r * r), ro2 = f2_of(ro);
     float row_slope = 0.f;
     float row_gate = 1.f;
     if (P.gate_mode == kGateRow) row_gate = gate_of((float)static_cast<const BT *>(P.gate)[row * P.as], P.sigmoid, &row_slope);
-    float2 g[N], o[N], j0 = f2_of(0.f), j1 = f2_of(0.f);
+    float2 j0 = f2_of(0.f), jg = f2_of(0.f);
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int c = it * threads + tid;
@@ -297,7 +343,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
             const float2 tf = f2_mul(t, f);
             a_all[4 * it + k] = f2_add(a_all[4 * it + k], tf);
             a[k] = f2_mul(f2_mul(t, M[k]), slope);
-            j1 = f2_add(j1, a[k]);
+            jg = f2_add(jg, a[k]);
             j0 = f2_fma(tf, M[k], j0);
             dx[k] = f2_mul(dx[k], f2_mul(f, M[k]));
           }
@@ -306,25 +352,10 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
         }
       }
     }
-    if (P.post || P.gate_mode == kGateRow) {
-      float join[2] = {j0.x + j0.y, j1.x + j1.y};
-      cta_sum(join, red, turn);
-      if (P.gate_mode == kGateRow && P.dgate && tid == 0)
-        st_elem(P.dgate, sizeof(BT) == 2 ? GBO_BF16 : GBO_F32, row * P.das, join[1]);
-      if (P.h && P.post) {
-        const float2 m2 = f2_of(-join[0] * P.inv_d);
-#pragma unroll
-        for (int it = 0; it < kIter; ++it) {
-          const int c = it * threads + tid;
-          if (c < chunks) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) g[4 * it + k] = f2_mul(ro2, f2_fma(o[4 * it + k], m2, g[4 * it + k]));
-            stg8(static_cast<BT *>(P.h) + row * P.hs + c * 8, g + 4 * it);
-          }
-        }
-      }
-    }
+    j1 = jg.x + jg.y;
     ring.next();
+    sums = make_float4(0.f, 0.f, 0.f, j0.x + j0.y);
+    if (row + step < P.n) first_sums(at = ring.take(), sums);
   }
   const int64_t rows = (int64_t)gridDim.x * P.d;
 #pragma unroll
