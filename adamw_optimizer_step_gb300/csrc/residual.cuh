@@ -13,13 +13,21 @@
 // Bound: HBM; every tensor is read or written once, a row stays in registers
 // from its loads to its stores.
 //
-// A group of 4 to 512 threads takes a row, eight consecutive elements to a
-// thread and chunk (16-byte loads); rows that 16 bytes do not divide take the
-// elements strided over the threads instead (coalesced, one element each).  The
-// sums of a row cross the group's warps through shared memory: two joins a row,
-// each of all sums known by then.  The sums over rows stay in a thread's
-// registers over all rows of its group (a thread keeps its columns), one partial
-// row a group is left at the end, and a second kernel adds them in a fixed order.
+// Three forms, by size:
+//   ring   rows of 505 to 8192 elements, a CTA each, through shared memory
+//   group  shorter rows, 4 to 64 threads each, eight elements a thread
+//   wide   longer ones, and those of which no ring holds two, a CTA each
+// Each comes with 16-byte chunks of eight consecutive elements a thread and, for
+// rows that 16 bytes do not divide or tensors that do not start there, with single
+// elements strided over the threads (coalesced).  Measured, bf16, against one form
+// for all (a group of threads that loads straight into registers, the row in
+// registers between its sums), us of the gradients and of the forward pass:
+//   32768 x 2048, gate and dropout    556 -> 231     (no gate or dropout) 84
+//   65600 x 1023, the same           2748 -> 811     903 -> 398
+//   8192 x 8192 (wide), the same     1652 -> 705     (ring) 163 -> 141
+//   4096 x 16384 (wide), the same    1020 -> 608     244 -> 198  The sums over rows stay with the
+// thread that has the columns (registers; wide: shared memory), one partial row a
+// group is left at the end, and a second kernel adds them in a fixed order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -43,6 +51,7 @@ namespace gbo {
 namespace {
 
 constexpr int kMaxGroup = 512;
+constexpr int kGroupThreads = 128;  // of the group form
 constexpr int kMaxStages = 6;
 
 struct ResParams {
@@ -90,113 +99,144 @@ __device__ __forceinline__ void group_sum(float (&v)[kCount], int group, int in_
     for (int i = 0; i < kCount; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-// A thread's elements of a row: kVec, kIter chunks of eight consecutive ones;
-// else 8 kIter single ones, `group` apart.
+// A thread's eight elements in part `it` of a row: kVec, consecutive ones; else
+// `group` apart.
 template <bool kVec>
 __device__ __forceinline__ int column(int it, int e, int in_group, int group) {
   return kVec ? (it * group + in_group) * 8 + e : (it * 8 + e) * group + in_group;
 }
 
 // (d = 0: a row that is not there, zeros)
-template <typename T, int kIter, bool kVec>
-__device__ __forceinline__ void row_load(const T *row, int d, int in_group, int group, float (&v)[kIter * 8]) {
+template <typename T, bool kVec>
+__device__ __forceinline__ void load_part(const T *row, int d, int it, int in_group, int group, float (&v)[8]) {
+  if constexpr (kVec) {
+    const int c = column<true>(it, 0, in_group, group);
+    if (c >= d) {
 #pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    if constexpr (kVec) {
-      const int c = column<true>(it, 0, in_group, group);
-      if (c < d) {
-        if constexpr (sizeof(T) == 2) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(row + c);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    } else if constexpr (sizeof(T) == 2) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(row + c);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            v[it * 8 + 2 * h] = __uint_as_float(w[h] << 16);
-            v[it * 8 + 2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
-          }
-        } else {
-          const float4 a = *reinterpret_cast<const float4 *>(row + c), b = *reinterpret_cast<const float4 *>(row + c + 4);
-          v[it * 8] = a.x, v[it * 8 + 1] = a.y, v[it * 8 + 2] = a.z, v[it * 8 + 3] = a.w;
-          v[it * 8 + 4] = b.x, v[it * 8 + 5] = b.y, v[it * 8 + 6] = b.z, v[it * 8 + 7] = b.w;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[it * 8 + e] = 0.f;
-      }
+      for (int h = 0; h < 4; ++h) v[2 * h] = __uint_as_float(w[h] << 16), v[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
     } else {
+      const float4 a = *reinterpret_cast<const float4 *>(row + c), b = *reinterpret_cast<const float4 *>(row + c + 4);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+  } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = column<false>(it, e, in_group, group);
-        v[it * 8 + e] = c < d ? (float)row[c] : 0.f;
-      }
+    for (int e = 0; e < 8; ++e) {
+      const int c = column<false>(it, e, in_group, group);
+      v[e] = c < d ? (float)row[c] : 0.f;
     }
   }
 }
 
-template <typename T, int kIter, bool kVec>
-__device__ __forceinline__ void row_store(T *row, int d, int in_group, int group, const float (&v)[kIter * 8]) {
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_part(T *row, int d, int it, int in_group, int group, const float (&v)[8]) {
+  if constexpr (kVec) {
+    const int c = column<true>(it, 0, in_group, group);
+    if (c < d) store8<T>(row + c, v, 8, true);
+  } else {
 #pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    if constexpr (kVec) {
-      const int c = column<true>(it, 0, in_group, group);
-      if (c < d) store8<T>(row + c, v + it * 8, 8, true);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = column<false>(it, e, in_group, group);
-        if (c < d) st_elem(row, sizeof(T) == 2 ? GBO_BF16 : GBO_F32, c, v[it * 8 + e]);
-      }
+    for (int e = 0; e < 8; ++e) {
+      const int c = column<false>(it, e, in_group, group);
+      if (c < d) st_elem(row, sizeof(T) == 2 ? GBO_BF16 : GBO_F32, c, v[e]);
     }
   }
 }
 
 // v *= a column table (gains, scales), where there is one.
-template <int kIter, bool kVec>
-__device__ __forceinline__ void times_table(const float *t, int d, int in_group, int group, float (&v)[kIter * 8]) {
+template <bool kVec>
+__device__ __forceinline__ void times_table(const float *t, int d, int it, int in_group, int group, float (&v)[8]) {
   if (!t) return;
-  float w[kIter * 8];
-  row_load<float, kIter, kVec>(t, d, in_group, group, w);
+  float w[8];
+  load_part<float, kVec>(t, d, it, in_group, group, w);
 #pragma unroll
-  for (int e = 0; e < kIter * 8; ++e) v[e] *= w[e];
+  for (int e = 0; e < 8; ++e) v[e] *= w[e];
 }
 
-// u *= dropout's factors of row `row`.
-template <int kIter, bool kVec>
-__device__ __forceinline__ void row_drop(const ResParams &P, uint64_t key, int64_t row, int in_group, int group,
-                                         float (&u)[kIter * 8]) {
+// v *= dropout's factors of row `row`, part `it`.  Eight consecutive elements share a
+// counter.  Where a thread's elements are single ones, the counters of the lanes'
+// elements are shared out: the lanes of a group in a warp (u of them, 8 or more)
+// cover, for each e, u consecutive elements, u / 8 counters and one more where the
+// row starts inside one.  The words cross through `slots`, the warp's own.
+constexpr int kDropSlots = 64;  // counters' words of a warp: u + 8 for each of 32 / u groups
+
+template <bool kVec>
+__device__ __forceinline__ void row_drop(const ResParams &P, uint64_t key, int64_t row, int it, int in_group, int group,
+                                         float (&v)[8], uint4 *slots) {
+  if constexpr (kVec) {
+    const uint64_t at = (uint64_t)(row * P.d + column<true>(it, 0, in_group, group));  // (a multiple of 8)
+    const uint4 w = philox(key, at >> 3, P.drop.offset);
 #pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    if constexpr (kVec) {
-      const uint64_t at = (uint64_t)(row * P.d + column<true>(it, 0, in_group, group));  // (a multiple of 8)
-      const uint4 w = philox(key, at >> 3, P.drop.offset);
+    for (int e = 0; e < 8; ++e) v[e] *= drop_factor(w, e, P.drop.limit, P.drop.keep);
+  } else {
+    const int u = min(group, 32), l = in_group & (u - 1);
+    uint4 *const mine = slots + (threadIdx.x >> 5) * kDropSlots + (threadIdx.x & 31) / u * (u + 8);
+    const uint64_t at = (uint64_t)(row * P.d + column<false>(it, 0, in_group - l, group));
+#pragma unroll 1
+    for (int q = l; q < u + 8; q += u)  // counter q / 8 of elements e = q % 8
+      mine[q] = philox(key, ((at + (uint64_t)(q & 7) * group) >> 3) + (q >> 3), P.drop.offset);
+    __syncwarp();
+    const int x = (int)(at & 7) + l;
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(mine + (x >> 3) * 8) + ((x & 7) >> 1);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u[it * 8 + e] *= drop_factor(w, e, P.drop.limit, P.drop.keep);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = column<false>(it, e, in_group, group);
-        if (c < P.d) u[it * 8 + e] *= drop_one(P.drop, key, (uint64_t)(row * P.d + c));
-      }
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t draw = (x & 1) ? w[4 * e] >> 16 : w[4 * e] & 0xffffu;
+      v[e] *= draw >= P.drop.limit ? P.drop.keep : 0.f;
     }
+    __syncwarp();
   }
 }
 
-// 1 / (1 + exp(-a)) and its slope, or a and 1.  From e = exp(-|a|) and q = 1 / (1 + e)
-// the gate is q or e q, the slope e q q: nothing cancels, nothing overflows.
-__device__ __forceinline__ float gate_of(float a, int sigmoid, float *slope = nullptr) {
+// 1 / (1 + exp(-a)) and its slope, or a and 1.  From e = exp(-a) and q = 1 / (1 + e)
+// the gate is q, the slope e q q: nothing cancels.  e is held below 2^126, so that
+// nothing overflows: a gate below 2^-126 becomes that.  (NaN stays: the minimum of
+// a NaN is NaN.)
+__device__ __forceinline__ float2 gate_of2(float2 a, int sigmoid, float2 &slope) {
   if (!sigmoid) {
-    if (slope) *slope = 1.f;
+    slope = f2_of(1.f);
     return a;
   }
-  const float e = __expf(-fabsf(a)), q = __fdividef(1.f, 1.f + e), eq = e * q;
-  if (slope) *slope = eq * q;
-  return a >= 0.f ? q : a < 0.f ? eq : a;  // (NaN stays)
+  a = f2_mul(a, f2_of(-1.4426950408889634f));
+  float2 e, q;
+  asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(a.x) : "f"(a.x));  // 126
+  asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(a.y) : "f"(a.y));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(a.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(a.y));
+  q = f2_add(e, f2_of(1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(q.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(q.y));
+  slope = f2_mul(f2_mul(e, q), q);
+  return q;
+}
+__device__ __forceinline__ float gate_of(float a, int sigmoid, float *slope = nullptr) {
+  float2 s;
+  const float q = gate_of2(f2_of(a), sigmoid, s).x;
+  if (slope) *slope = s.x;
+  return q;
+}
+
+// u times post_gain, dropout, the elements' gate and scale (forward).
+template <typename BT, bool kVec>
+__device__ __forceinline__ void block_factors(const ResParams &P, uint64_t key, int64_t row, int d, int it, int in_group, int group,
+                                              float (&u)[8], uint4 *slots) {
+  times_table<kVec>(P.post_gain, d, it, in_group, group, u);
+  if (P.drop.limit) row_drop<kVec>(P, key, row, it, in_group, group, u, slots);
+  if (P.gate_mode == kGateElement) {
+    float a[8];
+    load_part<BT, kVec>(static_cast<const BT *>(P.gate) + row * P.as, d, it, in_group, group, a);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] *= gate_of(a[e], P.sigmoid);
+  }
+  if (P.scale_mode == kScaleVector) times_table<kVec>(P.scale, d, it, in_group, group, u);
 }
 
 // ---------------------------------------------------------------------------
 // rows through shared memory
 
-// Rows of 16-byte chunks come through a ring of stages in shared memory: the
-// input tensors of a row one behind the other, by bulk copies that thread 0
+// Rows come through a ring of stages in shared memory: the input tensors of a row one behind the other, by bulk copies that thread 0
 // issues up to `stages` rows ahead.  Loads are then in flight all the time at no
 // cost in registers, while a row's two sums over its threads and its arithmetic
 // take their time.  A stage is filled again behind the first join of the next
@@ -237,25 +277,66 @@ struct RowRing {
 };
 
 // Thread 0: a row's tensors from `src` (NULL: none), `by` bytes on from row to row.
+// kOdd: rows start anywhere; their place is 16 bytes longer, and what is copied are
+// the 16-byte blocks that a row touches.  What a block holds beside the row lies
+// between the tensor's first and last element, but for the first row's start and the
+// last row's end: those elements are stored one by one.
+template <bool kOdd>
 struct RowFeed {
   const uint8_t *src[kInputs];
   int64_t by[kInputs];
   uint32_t bytes[kInputs];
-  int64_t left;  // rows
+  int64_t row, step, n;  // the next row, of n
 
+  static __host__ __device__ __forceinline__ uint32_t place(uint32_t bytes) { return kOdd ? (bytes + 15) / 16 * 16 + 16 : bytes; }
+
+  static __device__ __forceinline__ void by_hand(uint32_t dst, const uint8_t *p, uint32_t bytes) {
+    for (uint32_t b = 0; b < bytes; b += 2)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + b), "h"(*reinterpret_cast<const uint16_t *>(p + b)) : "memory");
+  }
   __device__ __forceinline__ void fill(RowRing &r) {
-    if (left <= 0) return;
-    --left;
+    if (row >= n) return;
     const uint32_t bar = r.full0 + 8 * r.to_fill;
     uint32_t dst = r.base + (uint32_t)r.to_fill * r.stage_bytes;
-    mbar_expect_tx(bar, r.stage_bytes);
+    if constexpr (kOdd) {
+      const bool first = row == 0, last = row == n - 1;
+      const uint8_t *lo[kInputs], *hi[kInputs];
+      uint32_t total = 0, at = dst;
+#pragma unroll
+      for (int i = 0; i < kInputs; ++i)
+        if (src[i]) {
+          const uint8_t *const p = src[i], *const end = p + bytes[i];
+          const uint32_t head = -(uint32_t)reinterpret_cast<uintptr_t>(p) & 15, tail = (uint32_t)reinterpret_cast<uintptr_t>(end) & 15;
+          const uint32_t before = (16 - head) & 15;  // bytes of p's block before it
+          lo[i] = first ? p + head : p - before;
+          hi[i] = last ? end - tail : end + ((16 - tail) & 15);
+          if (first) by_hand(at + before, p, head);
+          if (last) by_hand(at + before + (bytes[i] - tail), end - tail, tail);
+          total += (uint32_t)(hi[i] - lo[i]);
+          at += place(bytes[i]);
+        }
+      if (first | last) fence_async_smem();
+      mbar_expect_tx(bar, total);
+#pragma unroll
+      for (int i = 0; i < kInputs; ++i)
+        if (src[i]) {
+          const uint32_t before = (uint32_t)reinterpret_cast<uintptr_t>(src[i]) & 15;
+          RowRing::copy(dst + before + (int32_t)(lo[i] - src[i]), lo[i], (uint32_t)(hi[i] - lo[i]), bar);
+          dst += place(bytes[i]);
+        }
+    } else {
+      mbar_expect_tx(bar, r.stage_bytes);
+#pragma unroll
+      for (int i = 0; i < kInputs; ++i)
+        if (src[i]) {
+          RowRing::copy(dst, src[i], bytes[i], bar);
+          dst += bytes[i];
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kInputs; ++i)
-      if (src[i]) {
-        RowRing::copy(dst, src[i], bytes[i], bar);
-        src[i] += by[i];
-        dst += bytes[i];
-      }
+      if (src[i]) src[i] += by[i];
+    row += step;
     if (++r.to_fill == r.stages) r.to_fill = 0;
   }
 };
@@ -289,6 +370,77 @@ __device__ __forceinline__ void stg8(T *p, const float2 *v) {
     float4 *f = reinterpret_cast<float4 *>(p);
     f[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y), f[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   }
+}
+
+// Dropout's factors of eight elements, times v.
+__device__ __forceinline__ void drop8(const DropArgs &D, uint64_t key, uint64_t element, float2 *v) {
+  const uint4 w = philox(key, element >> 3, D.offset);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    v[k] = f2_mul(v[k], make_float2(drop_factor(w, 2 * k, D.limit, D.keep), drop_factor(w, 2 * k + 1, D.limit, D.keep)));
+}
+
+// A thread's part `it` of a row in a ring's stage and in memory.
+template <bool kOdd>
+struct RowPart {
+  int d, tid, threads;
+
+  __device__ __forceinline__ int chunk(int it) const { return it * threads + tid; }
+  __device__ __forceinline__ bool here(int it) const { return kOdd || chunk(it) * 8 < d; }
+  __device__ __forceinline__ int column(int it, int e) const { return gbo::column<!kOdd>(it, e, tid, threads); }
+  // `at`: the row's start
+  template <typename T>
+  __device__ __forceinline__ void get(uint32_t at, int it, float2 *v) const {
+    if constexpr (!kOdd) {
+      lds8<T>(at + chunk(it) * 8 * sizeof(T), v);
+    } else {
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = column(it, e);
+        w[e] = 0.f;
+        if (c < d) {
+          if constexpr (sizeof(T) == 2) {
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + c * 2) : "memory");
+            w[e] = __uint_as_float((uint32_t)x << 16);
+          } else {
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[e]) : "r"(at + c * 4) : "memory");
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = make_float2(w[2 * k], w[2 * k + 1]);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void put(T *row, int it, const float2 *v) const {
+    if constexpr (!kOdd) {
+      stg8(row + chunk(it) * 8, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = column(it, e);
+        if (c < d) st_elem(row, sizeof(T) == 2 ? GBO_BF16 : GBO_F32, c, (e & 1) ? v[e / 2].y : v[e / 2].x);
+      }
+    }
+  }
+  __device__ __forceinline__ void drop(const ResParams &P, uint64_t key, int64_t row, int it, float2 *v, uint4 *slots) const {
+    if constexpr (!kOdd) {
+      drop8(P.drop, key, (uint64_t)(row * P.d + chunk(it) * 8), v);
+    } else {
+      float w[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+      row_drop<false>(P, key, row, it, tid, threads, w, slots);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = make_float2(w[2 * k], w[2 * k + 1]);
+    }
+  }
+};
+
+// Where a row of a tensor starts in its place of a stage.
+template <bool kOdd, typename T>
+__device__ __forceinline__ uint32_t row_start(uint32_t place, const T *p, int64_t row, int64_t stride) {
+  return kOdd ? place + ((uint32_t)reinterpret_cast<uintptr_t>(p + row * stride) & 15) : place;
 }
 
 // A table's values of chunk c: first halves of all chunks, then second halves, so
@@ -368,14 +520,6 @@ __device__ __forceinline__ float4 cta_join(const float4 *red, int warps) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Dropout's factors of eight elements, times v.
-__device__ __forceinline__ void drop8(const DropArgs &D, uint64_t key, uint64_t element, float2 *v) {
-  const uint4 w = philox(key, element >> 3, D.offset);
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    v[k] = f2_mul(v[k], make_float2(drop_factor(w, 2 * k, D.limit, D.keep), drop_factor(w, 2 * k + 1, D.limit, D.keep)));
-}
-
 // ---------------------------------------------------------------------------
 // host
 
@@ -433,75 +577,87 @@ int check_residual(const gbo_residual_args *a, DropArgs *drop) {
 }
 
 // Threads to a row, chunks to a thread, the ring.
+enum { kFormGroup = 0, kFormRing = 1, kFormWide = 2 };
 struct ResCut {
-  int32_t group, iter, threads, blocks, stages;  // stages 0: no ring
+  int32_t form, group, iter, threads, blocks, stages, smem;
 };
 
 constexpr int kSmemMost = 220 * 1024;  // of an SM's shared memory, for rings and tables
 
-// A row goes to as many threads as it has chunks of eight elements, up to 512;
-// where rows come through a ring, to half as many in the forward pass (what a row
-// costs beside its elements is half as much then), one CTA of 64 threads or more
-// a row, 512 threads an SM.  The cut of the gradients' partial rows is the same
-// with a ring and without.  `row_bytes`: of a row's inputs.
+// Ring: a row goes to as many threads as it has chunks of eight elements, up to 512;
+// to half as many in the forward pass (what a row costs beside its elements is half
+// as much then); 512 threads an SM.  `row_bytes`: of a row's inputs, in their places.
 ResCut cut_of(int64_t n, int64_t d, int sm, bool back, bool vec, int64_t row_bytes) {
   ResCut c;
+  memset(&c, 0, sizeof c);
   const int64_t chunks = (d + 7) / 8;
-  c.stages = 0;
-  if (vec && chunks >= 64 && chunks <= 2 * kMaxGroup) {
+  auto blocks = [&](int per_sm, int64_t rows) {
+    c.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm * per_sm, (n + rows - 1) / rows));
+  };
+  if (chunks >= 64 && chunks <= 2 * kMaxGroup) {
     c.group = 64;
     while (c.group < kMaxGroup && (int64_t)c.group * (back ? 1 : 2) < chunks) c.group *= 2;
     c.iter = (int32_t)((chunks + c.group - 1) / c.group);
     c.threads = c.group;
+    const int64_t tables = 2 * 4 * (vec ? d : (int64_t)c.threads * c.iter * 8);
     for (int per_sm = std::max(1, 512 / c.threads); per_sm > 0; --per_sm) {
-      const int64_t room = kSmemMost / per_sm - 2 * 4 * d;
+      const int64_t slots = vec ? 0 : kMaxGroup / 32 * kDropSlots * 16, room = kSmemMost / per_sm - tables - slots;
       if (room < 2 * row_bytes) continue;
+      c.form = kFormRing;
       c.stages = (int32_t)std::min<int64_t>(kMaxStages, room / row_bytes);
-      c.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm * per_sm, n));
+      c.smem = (int32_t)(c.stages * row_bytes + tables);
+      blocks(per_sm, 1);
       return c;
     }
   }
-  c.group = 4;
-  while (c.group < kMaxGroup && c.group < chunks) c.group *= 2;
+  if (chunks >= 64) {
+    // x' in 32 bits; gradients: w, and two sums over rows
+    c.form = kFormWide;
+    c.group = c.threads = kMaxGroup;
+    c.iter = (int32_t)((chunks + kMaxGroup - 1) / kMaxGroup);
+    c.smem = c.iter * kMaxGroup * 8 * 4 * (back ? 3 : 1);
+    blocks(back ? std::max(1, std::min(2, kSmemMost / (c.smem + 16384))) : 2, 1);
+    return c;
+  }
+  c.group = vec ? 4 : 8;  // (single elements: dropout's counters are shared out by eight)
+  while (c.group < chunks) c.group *= 2;
   c.iter = 1;
-  while ((int64_t)c.group * c.iter < chunks) c.iter *= 2;
-  c.threads = std::max(c.group, 128);
-  const int64_t groups = c.threads / c.group;
+  c.threads = kGroupThreads;
   // gradients: as many blocks as leave the partial rows few; each goes over many rows
-  const int64_t most = (int64_t)sm * std::max(1, (back ? 512 : 1024) / c.threads);
-  c.blocks = (int32_t)std::max<int64_t>(1, std::min(most, (n + groups - 1) / groups));
+  blocks((back ? 512 : 1024) / c.threads, c.threads / c.group);
   return c;
 }
 
 // Partial rows of a backward call.
 int64_t parts_of(const ResCut &c) { return (int64_t)c.blocks * (c.threads / std::max(c.group, 32)); }
 
-// The most that any cut of these sizes leaves.
+// The most that any cut of these sizes leaves: a ring that has room for all of its
+// CTAs, or none.
 int64_t most_parts(int64_t n, int64_t d, int sm) {
-  return std::max(parts_of(cut_of(n, d, sm, true, true, 1)), parts_of(cut_of(n, d, sm, true, false, 1)));
+  int64_t most = 0;
+  for (bool vec : {false, true})
+    for (int64_t row_bytes : {int64_t(1), int64_t(kSmemMost)})
+      most = std::max(most, parts_of(cut_of(n, d, sm, true, vec, row_bytes)));
+  return most;
 }
 
-using ResKernel = void (*)(ResParams);
+using ResLaunch = cudaError_t (*)(ResParams &, const ResCut &, int, cudaStream_t);
 
-int kernel_slot(const ResCut &c, int32_t xt, int32_t bt) {
-  return (xt == GBO_BF16 ? 0 : bt == GBO_BF16 ? 1 : 2) * 2 + (c.iter > 1);
-}
-
-// kernel_of: the instance of the pass's kernel for two types, a cut and 16-byte chunks.
-template <typename Pick>
-cudaError_t dispatch_res(ResParams &P, const ResCut &c, bool vec, int32_t xt, int32_t bt, int dev, cudaStream_t st, Pick kernel_of) {
-  const ResKernel k = kernel_of(xt, bt, c, vec);
+template <auto kKernel>
+cudaError_t launch_res(ResParams &P, const ResCut &c, int dev, cudaStream_t st) {
   P.group = c.group, P.stages = c.stages;
-  const size_t smem = c.stages ? (size_t)c.stages * P.stage_bytes + 2 * 4 * P.d : 0;
-  if (c.stages) {
-    static PerDevice<cudaError_t> limit[6];
-    const cudaError_t *err = limit[kernel_slot(c, xt, bt)].of(dev, [&](cudaError_t &e) {
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+  if (c.smem) {
+    static PerDevice<cudaError_t> limit;
+    const cudaError_t *err = limit.of(dev, [](cudaError_t &e) {
+      cudaFuncAttributes own;
+      e = cudaFuncGetAttributes(&own, kKernel);
+      const int most = std::min(kSmemMost, 232448 - (int)own.sharedSizeBytes);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     });
     if (!err || *err != cudaSuccess) return err ? *err : cudaErrorInvalidDevice;
   }
   count_launches(1);
-  return launch_kernel_as(pdl_allowed(), k, dim3(c.blocks), dim3(c.threads), smem, st, 1, P);
+  return launch_kernel_as(pdl_allowed(), kKernel, dim3(c.blocks), dim3(c.threads), c.smem, st, 1, P);
 }
 
 bool vec_ok(const void *p, int64_t stride, int64_t n) {
@@ -517,6 +673,16 @@ void fill_res(const gbo_residual_args *a, const DropArgs &drop, ResParams *P) {
   P->eps = a->eps, P->inv_d = 1.f / (float)a->d;
   P->post = a->post_norm, P->pre = a->pre_norm, P->gate_mode = a->gate_mode, P->sigmoid = a->gate_sigmoid && a->gate_mode;
   P->scale_mode = a->scale_mode;
+}
+
+// A row's inputs in their places of a ring's stage.
+int64_t row_bytes(const ResParams &P, int32_t xt, int32_t bt, bool vec, bool back) {
+  const int64_t sizes[kInputs] = {!back || P.pre ? size_of(xt) : 0, P.block ? size_of(bt) : 0,
+                                  P.gate_mode == kGateElement ? size_of(bt) : 0, P.dxo ? size_of(xt) : 0, back && P.pre ? size_of(bt) : 0};
+  int64_t sum = 0;
+  for (int64_t size : sizes)
+    if (size) sum += vec ? RowFeed<false>::place((uint32_t)(P.d * size)) : RowFeed<true>::place((uint32_t)(P.d * size));
+  return sum;
 }
 
 bool inputs_vec(const gbo_residual_args *a) {

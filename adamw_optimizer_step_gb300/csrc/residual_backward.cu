@@ -16,11 +16,13 @@ __device__ __forceinline__ void warp_join(float (&v)[N], int group) {
     }
 }
 
-template <typename XT, typename BT, int kIter, bool kVec>
-__global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __grid_constant__ ResParams P) {
+// Rows below 512 elements: a group of threads a row.
+template <typename XT, typename BT, bool kVec>
+__global__ void __launch_bounds__(kGroupThreads, 4) residual_backward_kernel(const __grid_constant__ ResParams P) {
   pdl_launch();
-  constexpr int N = kIter * 8;
-  __shared__ float red[4][96];
+  constexpr int N = 8;
+  __shared__ float red[kGroupThreads / 32][96];
+  __shared__ uint4 slots[kVec ? 1 : kGroupThreads / 32 * kDropSlots];
   const int group = P.group, in_group = threadIdx.x & (group - 1), d = (int)P.d;
   const int unit = max(group, 32), g = threadIdx.x / unit;  // a join of warps, or a warp of groups
   const int groups = blockDim.x / group, sub = group < 32 ? (threadIdx.x & 31) / group : 0;
@@ -45,9 +47,9 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
     float sum[3] = {0.f, 0.f, 0.f};
     if (P.pre) {
       float x[N], w[N];
-      row_load<XT, kIter, kVec>(in.x, dr, in_group, group, x);
-      row_load<BT, kIter, kVec>(in.dh, dr, in_group, group, w);
-      times_table<kIter, kVec>(P.pre_gain, d, in_group, group, w);
+      load_part<XT, kVec>(in.x, dr, 0, in_group, group, x);
+      load_part<BT, kVec>(in.dh, dr, 0, in_group, group, w);
+      times_table<kVec>(P.pre_gain, d, 0, in_group, group, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         sum[0] = fmaf(x[e], x[e], sum[0]);
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
     }
     float o[N];
     if (P.block) {
-      row_load<BT, kIter, kVec>(in.block, dr, in_group, group, o);
+      load_part<BT, kVec>(in.block, dr, 0, in_group, group, o);
       if (P.post) {
 #pragma unroll
         for (int e = 0; e < N; ++e) sum[2] = fmaf(o[e], o[e], sum[2]);
@@ -66,38 +68,38 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
     const float ro = P.post ? rsqrtf(fmaf(sum[2], P.inv_d, P.eps)) : 1.f;
     float dx[N];
     if (P.dxo) {
-      row_load<XT, kIter, kVec>(in.dxo, dr, in_group, group, dx);
+      load_part<XT, kVec>(in.dxo, dr, 0, in_group, group, dx);
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) dx[e] = 0.f;
     }
     if (P.pre) {
       float x[N], w[N];
-      row_load<XT, kIter, kVec>(in.x, dr, in_group, group, x);
-      row_load<BT, kIter, kVec>(in.dh, dr, in_group, group, w);
+      load_part<XT, kVec>(in.x, dr, 0, in_group, group, x);
+      load_part<BT, kVec>(in.dh, dr, 0, in_group, group, w);
       const float r = rsqrtf(fmaf(sum[0], P.inv_d, P.eps)), c = sum[1] * P.inv_d * r * r;
 #pragma unroll
       for (int e = 0; e < N; ++e) a_pre[e] = fmaf(w[e], x[e] * r, a_pre[e]);
-      times_table<kIter, kVec>(P.pre_gain, d, in_group, group, w);
+      times_table<kVec>(P.pre_gain, d, 0, in_group, group, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) dx[e] = fmaf(r, w[e] - x[e] * c, dx[e]);
     }
-    if (P.xo) row_store<XT, kIter, kVec>(static_cast<XT *>(P.xo) + row * P.xos, dr, in_group, group, dx);
+    if (P.xo) store_part<XT, kVec>(static_cast<XT *>(P.xo) + row * P.xos, dr, 0, in_group, group, dx);
     if (P.block) {
       // v = o rho(o) in o; dx becomes g m, then du, then post_gain du
 #pragma unroll
       for (int e = 0; e < N; ++e) o[e] *= ro;
-      if (P.drop.limit) row_drop<kIter, kVec>(P, key, row, in_group, group, dx);
+      if (P.drop.limit) row_drop<kVec>(P, key, row, 0, in_group, group, dx, slots);
       float row_slope = 0.f;
       const float row_gate = P.gate_mode == kGateRow && dr ? gate_of((float)*in.gate, P.sigmoid, &row_slope) : 1.f;
       float u[N], da[N], join[2] = {0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < N; ++e) u[e] = o[e];
-      times_table<kIter, kVec>(P.post_gain, d, in_group, group, u);
+      times_table<kVec>(P.post_gain, d, 0, in_group, group, u);
 #pragma unroll
       for (int e = 0; e < N; ++e) u[e] *= dx[e];  // g m u
       if (P.gate_mode == kGateElement) {
-        row_load<BT, kIter, kVec>(in.gate, dr, in_group, group, da);
+        load_part<BT, kVec>(in.gate, dr, 0, in_group, group, da);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           float slope;
@@ -116,18 +118,18 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
       }
       if (P.scale_mode == kScaleVector) {
         float w[N];
-        row_load<float, kIter, kVec>(P.scale, d, in_group, group, w);
+        load_part<float, kVec>(P.scale, d, 0, in_group, group, w);
 #pragma unroll
         for (int e = 0; e < N; ++e) da[e] *= w[e], dx[e] *= w[e];
       }
       if (P.gate_mode == kGateElement && P.dgate)
-        row_store<BT, kIter, kVec>(static_cast<BT *>(P.dgate) + row * P.das, dr, in_group, group, da);
+        store_part<BT, kVec>(static_cast<BT *>(P.dgate) + row * P.das, dr, 0, in_group, group, da);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         join[1] += da[e];
         a_post[e] = fmaf(dx[e], o[e], a_post[e]);
       }
-      times_table<kIter, kVec>(P.post_gain, d, in_group, group, dx);
+      times_table<kVec>(P.post_gain, d, 0, in_group, group, dx);
 #pragma unroll
       for (int e = 0; e < N; ++e) join[0] = fmaf(dx[e], o[e], join[0]);
       if (P.post || P.gate_mode == kGateRow) group_sum(join, group, in_group, red[g], turn, 1 + g);
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
 #pragma unroll
           for (int e = 0; e < N; ++e) dx[e] = ro * (dx[e] - o[e] * c);
         }
-        row_store<BT, kIter, kVec>(static_cast<BT *>(P.h) + row * P.hs, dr, in_group, group, dx);
+        store_part<BT, kVec>(static_cast<BT *>(P.h) + row * P.hs, dr, 0, in_group, group, dx);
       }
     }
   }
@@ -151,27 +153,153 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_kernel(const __gr
   const int64_t rows = (int64_t)gridDim.x * units * P.d;
   float *part = P.part + ((int64_t)blockIdx.x * units + g) * P.d;
   const int dw = sub == 0 ? d : 0;
-  if (P.want_pre) row_store<float, kIter, kVec>(part, dw, in_group, group, a_pre), part += rows;
-  if (P.want_post) row_store<float, kIter, kVec>(part, dw, in_group, group, a_post), part += rows;
-  if (P.want_scale) row_store<float, kIter, kVec>(part, dw, in_group, group, a_scale);
+  if (P.want_pre) store_part<float, kVec>(part, dw, 0, in_group, group, a_pre), part += rows;
+  if (P.want_post) store_part<float, kVec>(part, dw, 0, in_group, group, a_post), part += rows;
+  if (P.want_scale) store_part<float, kVec>(part, dw, 0, in_group, group, a_scale);
 }
 
-// The same through a ring, a CTA to a row.  With t = g m v, v = o rho(o), the table
+// Rows that no ring has room for: a CTA a row, its tensors read two or three times
+// (from L2 after the first), w and the sums over rows in shared memory.  Names as
+// in the ring's form below.
+template <typename XT, typename BT, bool kVec>
+__global__ void __launch_bounds__(kMaxGroup) residual_backward_wide_kernel(const __grid_constant__ ResParams P) {
+  pdl_launch();
+  extern __shared__ __align__(128) uint8_t ring_smem[];
+  __shared__ float red[96];
+  __shared__ uint4 slots[kVec ? 1 : kMaxGroup / 32 * kDropSlots];
+  constexpr int threads = kMaxGroup;
+  const int tid = threadIdx.x, d = (int)P.d, its = (d + 8 * threads - 1) / (8 * threads), n = its * 8 * threads;
+  float *const w_kept = reinterpret_cast<float *>(ring_smem) + tid, *const a_pre = w_kept + n, *const a_all = a_pre + n;
+  int turn = 0;
+  for (int e = 0; e < its * 8; ++e) a_pre[e * threads] = a_all[e * threads] = 0.f;  // (a thread's own)
+  pdl_wait();
+  const uint64_t key = P.drop.dev_seed ? (uint64_t)*P.drop.dev_seed : P.drop.seed;
+  const float s1 = P.scale_mode == kScaleOne ? *P.scale : 1.f;
+  const float *const scale = P.scale_mode == kScaleVector ? P.scale : nullptr;
+  for (int64_t row = blockIdx.x; row < P.n; row += gridDim.x) {
+    const XT *const x_row = static_cast<const XT *>(P.x) + row * P.xs, *const dx_row = static_cast<const XT *>(P.dxo) + row * P.dxos;
+    const BT *const o_row = static_cast<const BT *>(P.block) + row * P.bs, *const dh_row = static_cast<const BT *>(P.dh) + row * P.dhs;
+    float sum[3] = {0.f, 0.f, 0.f};
+    for (int it = 0; it < its; ++it) {
+      float a[8], b[8];
+      if (P.pre) {
+        load_part<XT, kVec>(x_row, d, it, tid, threads, a);
+        load_part<BT, kVec>(dh_row, d, it, tid, threads, b);
+        times_table<kVec>(P.pre_gain, d, it, tid, threads, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[0] = fmaf(a[e], a[e], sum[0]), sum[1] = fmaf(b[e], a[e], sum[1]);
+      }
+      if (P.post) {
+        load_part<BT, kVec>(o_row, d, it, tid, threads, a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[2] = fmaf(a[e], a[e], sum[2]);
+      }
+    }
+    if (P.pre || P.post) cta_sum(sum, red, turn);
+    const float ro = P.post ? rsqrtf(fmaf(sum[2], P.inv_d, P.eps)) : 1.f;
+    const float r = P.pre ? rsqrtf(fmaf(sum[0], P.inv_d, P.eps)) : 1.f, c = sum[1] * P.inv_d * r * r;
+    float row_slope = 0.f, row_gate = 1.f;
+    if (P.gate_mode == kGateRow) row_gate = gate_of((float)static_cast<const BT *>(P.gate)[row * P.as], P.sigmoid, &row_slope);
+    float join[2] = {0.f, 0.f};
+    for (int it = 0; it < its; ++it) {
+      float dx[8], v[8], w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dx[e] = 0.f;
+      if (P.dxo) load_part<XT, kVec>(dx_row, d, it, tid, threads, dx);
+      if (P.pre) {
+        load_part<XT, kVec>(x_row, d, it, tid, threads, v);
+        load_part<BT, kVec>(dh_row, d, it, tid, threads, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a_pre[(it * 8 + e) * threads] += w[e] * (v[e] * r);
+        times_table<kVec>(P.pre_gain, d, it, tid, threads, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dx[e] = fmaf(r, w[e] - v[e] * c, dx[e]);
+      }
+      if (P.xo) store_part<XT, kVec>(static_cast<XT *>(P.xo) + row * P.xos, d, it, tid, threads, dx);
+      if (!P.block) continue;
+      if (P.drop.limit) row_drop<kVec>(P, key, row, it, tid, threads, dx, slots);
+      load_part<BT, kVec>(o_row, d, it, tid, threads, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = s1, v[e] *= ro;
+      times_table<kVec>(P.post_gain, d, it, tid, threads, w);
+      times_table<kVec>(scale, d, it, tid, threads, w);  // M
+      float a[8];
+      if (P.gate_mode == kGateElement) load_part<BT, kVec>(static_cast<const BT *>(P.gate) + row * P.as, d, it, tid, threads, a);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float f = row_gate, slope = row_slope;
+        if (P.gate_mode == kGateElement) f = gate_of(a[e], P.sigmoid, &slope);
+        const float t = dx[e] * v[e];
+        a_all[(it * 8 + e) * threads] += t * f;
+        a[e] = t * w[e] * slope;
+        join[1] += a[e];
+        join[0] = fmaf(t * f, w[e], join[0]);
+        w[e] *= dx[e] * f;
+      }
+      if (P.gate_mode == kGateElement && P.dgate)
+        store_part<BT, kVec>(static_cast<BT *>(P.dgate) + row * P.das, d, it, tid, threads, a);
+      if (!P.h) continue;
+      if (P.post) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w_kept[(it * 8 + e) * threads] = w[e];
+      } else {
+        store_part<BT, kVec>(static_cast<BT *>(P.h) + row * P.hs, d, it, tid, threads, w);
+      }
+    }
+    if (!(P.post || P.gate_mode == kGateRow)) continue;
+    cta_sum(join, red, turn);
+    if (P.gate_mode == kGateRow && P.dgate && tid == 0)
+      st_elem(P.dgate, sizeof(BT) == 2 ? GBO_BF16 : GBO_F32, row * P.das, join[1]);
+    if (!(P.h && P.post)) continue;
+    for (int it = 0; it < its; ++it) {
+      float v[8], w[8];
+      load_part<BT, kVec>(o_row, d, it, tid, threads, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = ro * (w_kept[(it * 8 + e) * threads] - v[e] * (ro * join[0] * P.inv_d));
+      store_part<BT, kVec>(static_cast<BT *>(P.h) + row * P.hs, d, it, tid, threads, w);
+    }
+  }
+  const int64_t rows = (int64_t)gridDim.x * P.d;
+  for (int it = 0; it < its; ++it) {
+    float *part = P.part + (int64_t)blockIdx.x * P.d;
+    float v[8];
+    if (P.want_pre) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = a_pre[(it * 8 + e) * threads];
+      store_part<float, kVec>(part, d, it, tid, threads, v), part += rows;
+    }
+    for (int which = 0; which < 2; ++which)
+      if (which == 0 ? P.want_post : P.want_scale) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = a_all[(it * 8 + e) * threads] * (which == 0 ? s1 : 1.f);
+        times_table<kVec>(which == 0 ? scale : P.post_gain, d, it, tid, threads, v);
+        store_part<float, kVec>(part, d, it, tid, threads, v), part += rows;
+      }
+  }
+}
+
+// Rows through a ring, a CTA to a row.  With t = g m v, v = o rho(o), the table
 // M = scale post_gain (s1 where the scale is one number) and the gate f:
 //   A = sum t f:  dscale = post_gain A, dpost_gain = scale A
 //   da = t M f',  w = g m f M,  mean(w v) = mean(t f M),  do = rho(o) (w - v mean(w v))
 // One join of the CTA a row: the sums that start row i and the one that ends row
 // i - 1 cross the warps together, while the rows' other work fills the time between.
-template <typename XT, typename BT, int kIter>
+// kAll: both norms, and every gradient of a row is there, as in training.  Without
+// the branches a row is few blocks of instructions whose loads and arithmetic
+// overlap (32768 x 2048 with gate and dropout: 273 -> 231 us, 4.7 TB/s; the rest is
+// issue slots, 600 instructions a warp and row at 60% of them).
+template <typename XT, typename BT, int kIter, bool kOdd, bool kAll>
 __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const __grid_constant__ ResParams P) {
   pdl_launch();
   extern __shared__ __align__(128) uint8_t ring_smem[];
   __shared__ float4 red[2][16];
   __shared__ float red_gate[2][16];
+  __shared__ uint4 slots[kOdd ? kMaxGroup / 32 * kDropSlots : 1];
   __shared__ uint64_t bars[kMaxStages];
   __shared__ int32_t late;
   constexpr int N = kIter * 4;  // pairs of elements
-  const int tid = threadIdx.x, threads = blockDim.x, chunks = (int)P.d / 8;
+  const int tid = threadIdx.x, threads = blockDim.x, d = (int)P.d, chunks = kOdd ? kIter * threads : d / 8;
+  const RowPart<kOdd> part = {d, tid, threads};
   RowRing ring{smem_u32(ring_smem), smem_u32(bars), (uint32_t)P.stage_bytes, P.stages, &late, P.status};
   if (tid == 0) {
     for (int s = 0; s < P.stages; ++s) mbar_init(ring.full0 + 8 * s, 1);
@@ -184,7 +312,9 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
   const int64_t row0 = blockIdx.x, step = gridDim.x;
   const uint32_t xb = (uint32_t)P.d * sizeof(XT), bb = (uint32_t)P.d * sizeof(BT);
   const bool gated = P.gate_mode == kGateElement;
-  RowFeed feed{};
+  const bool pre_norm = kAll || P.pre, post_norm = kAll || P.post, has_block = kAll || P.block, has_dxo = kAll || P.dxo;
+  const bool out_dx = kAll || P.xo, out_do = kAll || P.h;
+  RowFeed<kOdd> feed{};
   if (tid == 0) {
     auto set = [&](int i, const void *p, int64_t stride, uint32_t bytes, int size) {
       if (!p) return;
@@ -196,12 +326,13 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
     if (gated) set(kInGate, P.gate, P.as, bb, sizeof(BT));
     set(kInDxo, P.dxo, P.dxos, xb, sizeof(XT));
     if (P.pre) set(kInDh, P.dh, P.dhs, bb, sizeof(BT));
-    feed.left = (P.n - row0 + step - 1) / step;
+    feed.row = row0, feed.step = step, feed.n = P.n;
     for (int s = 0; s < P.stages; ++s) feed.fill(ring);
   }
   // a stage's tensors
-  const uint32_t to_block = P.pre ? xb : 0, to_gate = to_block + (P.block ? bb : 0), to_dxo = to_gate + (gated ? bb : 0);
-  const uint32_t to_dh = to_dxo + (P.dxo ? xb : 0);
+  const uint32_t xp = RowFeed<kOdd>::place(xb), bp = RowFeed<kOdd>::place(bb);
+  const uint32_t to_block = pre_norm ? xp : 0, to_gate = to_block + (has_block ? bp : 0), to_dxo = to_gate + (gated ? bp : 0);
+  const uint32_t to_dh = to_dxo + (has_dxo ? xp : 0);
   const uint64_t key = P.drop.dev_seed ? (uint64_t)*P.drop.dev_seed : P.drop.seed;
   const float s1 = P.scale_mode == kScaleOne ? *P.scale : 1.f;
   const float *const scale = P.scale_mode == kScaleVector ? P.scale : nullptr;
@@ -210,41 +341,43 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
   float2 a_pre[N], a_all[N];
 #pragma unroll
   for (int it = 0; it < kIter; ++it) {
-    const int c = it * threads + tid;
 #pragma unroll
     for (int k = 0; k < 4; ++k) a_pre[4 * it + k] = a_all[4 * it + k] = f2_of(0.f);
-    if (c < chunks) {
+    if (part.here(it)) {
       float v[8], w[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[e] = s1 * table_at(P.post_gain, c * 8 + e) * table_at(scale, c * 8 + e);
-        w[e] = table_at(P.pre_gain, c * 8 + e);
+        const int c = part.column(it, e);
+        v[e] = w[e] = 0.f;
+        if (c < d) v[e] = s1 * table_at(P.post_gain, c) * table_at(scale, c), w[e] = table_at(P.pre_gain, c);
       }
-      mul.put(c, v);
-      pre.put(c, w);
+      mul.put(part.chunk(it), v);
+      pre.put(part.chunk(it), w);
     }
   }
   // this thread's part of a row's sums: x^2, pre_gain dh x, o^2
-  auto first_sums = [&](uint32_t at, float4 &s) {
+  auto x_at = [&](uint32_t at, int64_t row) { return row_start<kOdd>(at, static_cast<const XT *>(P.x), row, P.xs); };
+  auto dh_at = [&](uint32_t at, int64_t row) { return row_start<kOdd>(at + to_dh, static_cast<const BT *>(P.dh), row, P.dhs); };
+  auto o_at = [&](uint32_t at, int64_t row) { return row_start<kOdd>(at + to_block, static_cast<const BT *>(P.block), row, P.bs); };
+  auto first_sums = [&](uint32_t at, int64_t row, float4 &s) {
     float2 s0 = f2_of(0.f), sx = f2_of(0.f), so = f2_of(0.f);
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-      const int c = it * threads + tid;
-      if (c < chunks) {
-        if (P.pre) {
+      if (part.here(it)) {
+        if (pre_norm) {
           float2 t[4], x[4], dh[4];
-          lds8<XT>(at + c * 8 * sizeof(XT), x);
-          lds8<BT>(at + to_dh + c * 8 * sizeof(BT), dh);
-          pre.get(c, t);
+          part.template get<XT>(x_at(at, row), it, x);
+          part.template get<BT>(dh_at(at, row), it, dh);
+          pre.get(part.chunk(it), t);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             s0 = f2_fma(x[k], x[k], s0);
             sx = f2_fma(f2_mul(dh[k], t[k]), x[k], sx);
           }
         }
-        if (P.post) {
+        if (post_norm) {
           float2 o[4];
-          lds8<BT>(at + to_block + c * 8 * sizeof(BT), o);
+          part.template get<BT>(o_at(at, row), it, o);
 #pragma unroll
           for (int k = 0; k < 4; ++k) so = f2_fma(o[k], o[k], so);
         }
@@ -261,7 +394,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
   float4 sums = make_float4(0.f, 0.f, 0.f, 0.f);  // w: sum w v of the last row
   int turn = 0;
   uint32_t at = 0;
-  if (row0 < P.n) first_sums(at = ring.take(), sums);
+  if (row0 < P.n) first_sums(at = ring.take(), row0, sums);
   for (int64_t row = row0; row < P.n + step; row += step) {  // (one turn more for the last row's block gradient)
     const int64_t last = row - step;
     sums = warp_sum4(sums, lane);
@@ -281,15 +414,14 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
           st_elem(P.dgate, sizeof(BT) == 2 ? GBO_BF16 : GBO_F32, last * P.das, v);
         }
       }
-      if (P.h && P.post) {
+      if (out_do && post_norm) {
         const float2 m2 = f2_of(-sums.w * P.inv_d), ro2 = f2_of(ro);
 #pragma unroll
         for (int it = 0; it < kIter; ++it) {
-          const int c = it * threads + tid;
-          if (c < chunks) {
+          if (part.here(it)) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) g[4 * it + k] = f2_mul(ro2, f2_fma(o[4 * it + k], m2, g[4 * it + k]));
-            stg8(static_cast<BT *>(P.h) + last * P.hs + c * 8, g + 4 * it);
+            part.put(static_cast<BT *>(P.h) + last * P.hs, it, g + 4 * it);
           }
         }
       }
@@ -298,7 +430,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
     if (row >= P.n) break;
     // (the row is read again: held over the join, two chunks a thread would spill)
     const float r = rsqrtf(fmaf(sums.x, P.inv_d, P.eps));
-    ro = P.post ? rsqrtf(fmaf(sums.z, P.inv_d, P.eps)) : 1.f;
+    ro = post_norm ? rsqrtf(fmaf(sums.z, P.inv_d, P.eps)) : 1.f;
     const float2 r2 = f2_of(r), c2 = f2_of(-sums.y * P.inv_d * r * r), ro2 = f2_of(ro);
     float row_slope = 0.f;
     float row_gate = 1.f;
@@ -306,40 +438,39 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
     float2 j0 = f2_of(0.f), jg = f2_of(0.f);
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-      const int c = it * threads + tid;
-      if (c < chunks) {
+      if (part.here(it)) {
         float2 *const dx = g + 4 * it;
-        if (P.dxo) {
-          lds8<XT>(at + to_dxo + c * 8 * sizeof(XT), dx);
+        if (has_dxo) {
+          part.template get<XT>(row_start<kOdd>(at + to_dxo, static_cast<const XT *>(P.dxo), row, P.dxos), it, dx);
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) dx[k] = f2_of(0.f);
         }
-        if (P.pre) {
+        if (pre_norm) {
           float2 t[4], x[4], dh[4];
-          lds8<XT>(at + c * 8 * sizeof(XT), x);
-          lds8<BT>(at + to_dh + c * 8 * sizeof(BT), dh);
-          pre.get(c, t);
+          part.template get<XT>(x_at(at, row), it, x);
+          part.template get<BT>(dh_at(at, row), it, dh);
+          pre.get(part.chunk(it), t);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             a_pre[4 * it + k] = f2_fma(dh[k], f2_mul(x[k], r2), a_pre[4 * it + k]);
             dx[k] = f2_fma(r2, f2_fma(x[k], c2, f2_mul(dh[k], t[k])), dx[k]);
           }
         }
-        if (P.xo) stg8(static_cast<XT *>(P.xo) + row * P.xos + c * 8, dx);
-        if (P.block) {
+        if (out_dx) part.put(static_cast<XT *>(P.xo) + row * P.xos, it, dx);
+        if (has_block) {
           float2 M[4], a[4];
           float2 *const v = o + 4 * it;
-          lds8<BT>(at + to_block + c * 8 * sizeof(BT), v);
-          if (P.drop.limit) drop8(P.drop, key, (uint64_t)(row * P.d + c * 8), dx);
-          mul.get(c, M);
-          if (gated) lds8<BT>(at + to_gate + c * 8 * sizeof(BT), a);
+          part.template get<BT>(o_at(at, row), it, v);
+          if (P.drop.limit) part.drop(P, key, row, it, dx, slots);
+          mul.get(part.chunk(it), M);
+          if (gated) part.template get<BT>(row_start<kOdd>(at + to_gate, static_cast<const BT *>(P.gate), row, P.as), it, a);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             v[k] = f2_mul(v[k], ro2);
             const float2 t = f2_mul(dx[k], v[k]);
             float2 f = f2_of(row_gate), slope = f2_of(row_slope);
-            if (gated) f.x = gate_of(a[k].x, P.sigmoid, &slope.x), f.y = gate_of(a[k].y, P.sigmoid, &slope.y);
+            if (gated) f = gate_of2(a[k], P.sigmoid, slope);
             const float2 tf = f2_mul(t, f);
             a_all[4 * it + k] = f2_add(a_all[4 * it + k], tf);
             a[k] = f2_mul(f2_mul(t, M[k]), slope);
@@ -347,23 +478,22 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
             j0 = f2_fma(tf, M[k], j0);
             dx[k] = f2_mul(dx[k], f2_mul(f, M[k]));
           }
-          if (gated && P.dgate) stg8(static_cast<BT *>(P.dgate) + row * P.das + c * 8, a);
-          if (P.h && !P.post) stg8(static_cast<BT *>(P.h) + row * P.hs + c * 8, dx);
+          if (gated && P.dgate) part.put(static_cast<BT *>(P.dgate) + row * P.das, it, a);
+          if (out_do && !post_norm) part.put(static_cast<BT *>(P.h) + row * P.hs, it, dx);
         }
       }
     }
     j1 = jg.x + jg.y;
     ring.next();
     sums = make_float4(0.f, 0.f, 0.f, j0.x + j0.y);
-    if (row + step < P.n) first_sums(at = ring.take(), sums);
+    if (row + step < P.n) first_sums(at = ring.take(), row + step, sums);
   }
   const int64_t rows = (int64_t)gridDim.x * P.d;
 #pragma unroll
   for (int it = 0; it < kIter; ++it) {
-    const int c = it * threads + tid;
-    if (c < chunks) {
-      float *part = P.part + (int64_t)blockIdx.x * P.d + c * 8;
-      if (P.want_pre) stg8(part, a_pre + 4 * it), part += rows;
+    if (part.here(it)) {
+      float *out = P.part + (int64_t)blockIdx.x * P.d;
+      if (P.want_pre) part.put(out, it, a_pre + 4 * it), out += rows;
 #pragma unroll
       for (int which = 0; which < 2; ++which)
         if (which == 0 ? P.want_post : P.want_scale) {
@@ -372,11 +502,11 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
           for (int k = 0; k < 4; ++k) {
             const float *const t = which == 0 ? scale : P.post_gain;
             const float one = which == 0 ? s1 : 1.f;
-            v[k] = f2_mul(a_all[4 * it + k],
-                          make_float2(one * table_at(t, c * 8 + 2 * k), one * table_at(t, c * 8 + 2 * k + 1)));
+            const int c0 = min(part.column(it, 2 * k), d - 1), c1 = min(part.column(it, 2 * k + 1), d - 1);
+            v[k] = f2_mul(a_all[4 * it + k], make_float2(one * table_at(t, c0), one * table_at(t, c1)));
           }
-          stg8(part, v);
-          part += rows;
+          part.put(out, it, v);
+          out += rows;
         }
     }
   }
@@ -425,18 +555,22 @@ __global__ void __launch_bounds__(1024) residual_one_kernel(const float *__restr
   if (threadIdx.x == 0) *out = a;
 }
 
-template <typename XT, typename BT>
-ResKernel pick(const ResCut &c, bool vec) {
-  if (c.stages) return c.iter == 1 ? residual_backward_ring_kernel<XT, BT, 1> : residual_backward_ring_kernel<XT, BT, 2>;
-  if (vec) return c.iter == 1 ? residual_backward_kernel<XT, BT, 1, true> : residual_backward_kernel<XT, BT, 4, true>;
-  return c.iter == 1   ? residual_backward_kernel<XT, BT, 1, false>
-         : c.iter == 2 ? residual_backward_kernel<XT, BT, 2, false>
-                       : residual_backward_kernel<XT, BT, 4, false>;
+template <typename XT, typename BT, bool kVec>
+ResLaunch pick(const ResCut &c, bool all) {
+  if (c.form == kFormWide) return launch_res<residual_backward_wide_kernel<XT, BT, kVec>>;
+  if (c.form == kFormGroup) return launch_res<residual_backward_kernel<XT, BT, kVec>>;
+  if constexpr (kVec)
+    if (all)
+      return c.iter == 1 ? launch_res<residual_backward_ring_kernel<XT, BT, 1, false, true>>
+                         : launch_res<residual_backward_ring_kernel<XT, BT, 2, false, true>>;
+  return c.iter == 1 ? launch_res<residual_backward_ring_kernel<XT, BT, 1, !kVec, false>>
+                     : launch_res<residual_backward_ring_kernel<XT, BT, 2, !kVec, false>>;
 }
 
-ResKernel kernel_of(int32_t xt, int32_t bt, const ResCut &c, bool vec) {
-  return xt == GBO_BF16 ? pick<__nv_bfloat16, __nv_bfloat16>(c, vec)
-                        : bt == GBO_BF16 ? pick<float, __nv_bfloat16>(c, vec) : pick<float, float>(c, vec);
+template <bool kVec>
+ResLaunch launcher(int32_t xt, int32_t bt, const ResCut &c, bool all) {
+  return xt == GBO_BF16 ? pick<__nv_bfloat16, __nv_bfloat16, kVec>(c, all)
+                        : bt == GBO_BF16 ? pick<float, __nv_bfloat16, kVec>(c, all) : pick<float, float, kVec>(c, all);
 }
 
 }  // namespace
@@ -493,12 +627,13 @@ extern "C" int gbo_residual_backward(const gbo_residual_args *a, const gbo_resid
                    vec_ok(g->dx, g->dx_stride, a->n) && vec_ok(g->dblock, g->dblock_stride, a->n) &&
                    (a->gate_mode != GBO_GATE_ELEMENT || vec_ok(g->dgate, g->dgate_stride, a->n));
   P.status = dev_status;
-  P.stage_bytes = (int32_t)(a->d * (size_of(a->x_dtype) * (a->pre_norm + (g->dx_out != nullptr)) +
-                                    size_of(a->block_dtype) * (a->has_block + (a->gate_mode == GBO_GATE_ELEMENT) + a->pre_norm)));
+  P.stage_bytes = (int32_t)row_bytes(P, a->x_dtype, a->block_dtype, vec, true);
   const ResCut c = cut_of(a->n, a->d, sm, true, vec, P.stage_bytes);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (a->n > 0 || sums) e = dispatch_res(P, c, vec, a->x_dtype, a->block_dtype, dev, st, kernel_of);
+  const bool all = P.pre && P.post && P.block && P.dxo && P.xo && P.h;
+  const ResLaunch launch = vec ? launcher<true>(a->x_dtype, a->block_dtype, c, all) : launcher<false>(a->x_dtype, a->block_dtype, c, all);
+  if (a->n > 0 || sums) e = launch(P, c, dev, st);
   if (e == cudaSuccess && sums) {
     ResSum S;
     memset(&S, 0, sizeof S);

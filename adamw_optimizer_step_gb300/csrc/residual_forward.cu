@@ -5,11 +5,12 @@ namespace gbo {
 
 namespace {
 
-template <typename XT, typename BT, int kIter, bool kVec>
-__global__ void __launch_bounds__(kMaxGroup) residual_forward_kernel(const __grid_constant__ ResParams P) {
+// Rows below 512 elements: a group of threads a row.
+template <typename XT, typename BT, bool kVec>
+__global__ void __launch_bounds__(kGroupThreads) residual_forward_kernel(const __grid_constant__ ResParams P) {
   pdl_launch();
-  constexpr int N = kIter * 8;
-  __shared__ float red[4][96];
+  __shared__ float red[kGroupThreads / 32][96];
+  __shared__ uint4 slots[kVec ? 1 : kGroupThreads / 32 * kDropSlots];
   const int group = P.group, in_group = threadIdx.x & (group - 1), d = (int)P.d;
   const int unit = max(group, 32), g = threadIdx.x / unit;  // a join of warps, or a warp of groups
   const int groups = blockDim.x / group, sub = group < 32 ? (threadIdx.x & 31) / group : 0;
@@ -22,58 +23,113 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_kernel(const __gri
   for (int64_t base = row0; base < P.n; base += step) {
     const int64_t row = base + sub;
     const int dr = row < P.n ? d : 0;  // (the last warp may hold fewer rows than groups)
-    float x[N];
-    row_load<XT, kIter, kVec>(static_cast<const XT *>(P.x) + row * P.xs, dr, in_group, group, x);
+    float x[8];
+    load_part<XT, kVec>(static_cast<const XT *>(P.x) + row * P.xs, dr, 0, in_group, group, x);
     if (P.block) {
-      float u[N];
-      row_load<BT, kIter, kVec>(static_cast<const BT *>(P.block) + row * P.bs, dr, in_group, group, u);
+      float u[8];
+      load_part<BT, kVec>(static_cast<const BT *>(P.block) + row * P.bs, dr, 0, in_group, group, u);
       float f = s1;
       if (P.post) {
         float sum[1] = {0.f};
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum[0] = fmaf(u[e], u[e], sum[0]);
+        for (int e = 0; e < 8; ++e) sum[0] = fmaf(u[e], u[e], sum[0]);
         group_sum(sum, group, in_group, red[g], turn, 1 + g);
         f *= rsqrtf(fmaf(sum[0], P.inv_d, P.eps));
-        times_table<kIter, kVec>(P.post_gain, d, in_group, group, u);
       }
-      if (P.drop.limit) row_drop<kIter, kVec>(P, key, row, in_group, group, u);
-      if (P.gate_mode == kGateElement) {
-        float a[N];
-        row_load<BT, kIter, kVec>(static_cast<const BT *>(P.gate) + row * P.as, dr, in_group, group, a);
-#pragma unroll
-        for (int e = 0; e < N; ++e) u[e] *= gate_of(a[e], P.sigmoid);
-      }
-      if (P.scale_mode == kScaleVector) times_table<kIter, kVec>(P.scale, d, in_group, group, u);
+      block_factors<BT, kVec>(P, key, row, dr, 0, in_group, group, u, slots);
       if (P.gate_mode == kGateRow && dr) f *= gate_of((float)static_cast<const BT *>(P.gate)[row * P.as], P.sigmoid);
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[e] = fmaf(f, u[e], x[e]);
-      row_store<XT, kIter, kVec>(static_cast<XT *>(P.xo) + row * P.xos, dr, in_group, group, x);
+      for (int e = 0; e < 8; ++e) x[e] = fmaf(f, u[e], x[e]);
+      store_part<XT, kVec>(static_cast<XT *>(P.xo) + row * P.xos, dr, 0, in_group, group, x);
     }
     if (P.pre) {
       float sum[1] = {0.f};
 #pragma unroll
-      for (int e = 0; e < N; ++e) sum[0] = fmaf(x[e], x[e], sum[0]);
+      for (int e = 0; e < 8; ++e) sum[0] = fmaf(x[e], x[e], sum[0]);
       group_sum(sum, group, in_group, red[g], turn, 1 + g);
       const float r = rsqrtf(fmaf(sum[0], P.inv_d, P.eps));
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[e] *= r;
-      times_table<kIter, kVec>(P.pre_gain, d, in_group, group, x);
-      row_store<BT, kIter, kVec>(static_cast<BT *>(P.h) + row * P.hs, dr, in_group, group, x);
+      for (int e = 0; e < 8; ++e) x[e] *= r;
+      times_table<kVec>(P.pre_gain, d, 0, in_group, group, x);
+      store_part<BT, kVec>(static_cast<BT *>(P.h) + row * P.hs, dr, 0, in_group, group, x);
     }
   }
 }
 
-// The same through a ring, a CTA to a row.  post_gain and scale stand in one table:
+// Rows that no ring has room for: a CTA a row, x' in shared memory, the block's
+// output read twice (the second time from L2).
+template <typename XT, typename BT, bool kVec>
+__global__ void __launch_bounds__(kMaxGroup, 2) residual_forward_wide_kernel(const __grid_constant__ ResParams P) {
+  pdl_launch();
+  extern __shared__ __align__(128) uint8_t ring_smem[];
+  __shared__ float red[96];
+  __shared__ uint4 slots[kVec ? 1 : kMaxGroup / 32 * kDropSlots];
+  float *const kept = reinterpret_cast<float *>(ring_smem) + threadIdx.x;
+  constexpr int threads = kMaxGroup;
+  const int tid = threadIdx.x, d = (int)P.d, its = (d + 8 * threads - 1) / (8 * threads);
+  int turn = 0;
+  pdl_wait();
+  const uint64_t key = P.drop.dev_seed ? (uint64_t)*P.drop.dev_seed : P.drop.seed;
+  const float s1 = P.scale_mode == kScaleOne ? *P.scale : 1.f;
+  for (int64_t row = blockIdx.x; row < P.n; row += gridDim.x) {
+    const XT *const x_row = static_cast<const XT *>(P.x) + row * P.xs;
+    const BT *const o_row = static_cast<const BT *>(P.block) + row * P.bs;
+    float f = s1, sum[1] = {0.f};
+    if (P.post) {
+      for (int it = 0; it < its; ++it) {
+        float o[8];
+        load_part<BT, kVec>(o_row, d, it, tid, threads, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[0] = fmaf(o[e], o[e], sum[0]);
+      }
+      cta_sum(sum, red, turn);
+      f *= rsqrtf(fmaf(sum[0], P.inv_d, P.eps));
+    }
+    if (P.gate_mode == kGateRow) f *= gate_of((float)static_cast<const BT *>(P.gate)[row * P.as], P.sigmoid);
+    sum[0] = 0.f;
+    for (int it = 0; it < its; ++it) {
+      float x[8];
+      load_part<XT, kVec>(x_row, d, it, tid, threads, x);
+      if (P.block) {
+        float u[8];
+        load_part<BT, kVec>(o_row, d, it, tid, threads, u);
+        block_factors<BT, kVec>(P, key, row, d, it, tid, threads, u, slots);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(f, u[e], x[e]);
+        store_part<XT, kVec>(static_cast<XT *>(P.xo) + row * P.xos, d, it, tid, threads, x);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum[0] = fmaf(x[e], x[e], sum[0]);
+        kept[(it * 8 + e) * threads] = x[e];
+      }
+    }
+    if (!P.pre) continue;
+    cta_sum(sum, red, turn);
+    const float r = rsqrtf(fmaf(sum[0], P.inv_d, P.eps));
+    for (int it = 0; it < its; ++it) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = kept[(it * 8 + e) * threads] * r;
+      times_table<kVec>(P.pre_gain, d, it, tid, threads, x);
+      store_part<BT, kVec>(static_cast<BT *>(P.h) + row * P.hs, d, it, tid, threads, x);
+    }
+  }
+}
+
+// Rows through a ring, a CTA to a row.  post_gain and scale stand in one table:
 // x' = x + (s1 rho(o) gate_row) table gate m o.
-template <typename XT, typename BT, int kIter>
+template <typename XT, typename BT, int kIter, bool kOdd>
 __global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const __grid_constant__ ResParams P) {
   pdl_launch();
   extern __shared__ __align__(128) uint8_t ring_smem[];
   __shared__ float red[96];
+  __shared__ uint4 slots[kOdd ? kMaxGroup / 32 * kDropSlots : 1];
   __shared__ uint64_t bars[kMaxStages];
   __shared__ int32_t late;
   constexpr int N = kIter * 4;  // pairs of elements
-  const int tid = threadIdx.x, threads = blockDim.x, chunks = (int)P.d / 8;
+  const int tid = threadIdx.x, threads = blockDim.x, d = (int)P.d, chunks = kOdd ? kIter * threads : d / 8;
+  const RowPart<kOdd> part = {d, tid, threads};
   RowRing ring{smem_u32(ring_smem), smem_u32(bars), (uint32_t)P.stage_bytes, P.stages, &late, P.status};
   if (tid == 0) {
     for (int s = 0; s < P.stages; ++s) mbar_init(ring.full0 + 8 * s, 1);
@@ -84,7 +140,8 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const 
   pdl_wait();
   const int64_t row0 = blockIdx.x, step = gridDim.x;
   const uint32_t xb = (uint32_t)P.d * sizeof(XT), bb = (uint32_t)P.d * sizeof(BT);
-  RowFeed feed{};
+  const uint32_t to_block = RowFeed<kOdd>::place(xb), to_gate = to_block + RowFeed<kOdd>::place(bb);  // (of a stage)
+  RowFeed<kOdd> feed{};
   if (tid == 0) {
     auto set = [&](int i, const void *p, int64_t stride, uint32_t bytes, int size) {
       if (!p) return;
@@ -94,7 +151,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const 
     set(kInX, P.x, P.xs, xb, sizeof(XT));
     set(kInBlock, P.block, P.bs, bb, sizeof(BT));
     if (P.gate_mode == kGateElement) set(kInGate, P.gate, P.as, bb, sizeof(BT));
-    feed.left = (P.n - row0 + step - 1) / step;
+    feed.row = row0, feed.step = step, feed.n = P.n;
     for (int s = 0; s < P.stages; ++s) feed.fill(ring);
   }
   const uint64_t key = P.drop.dev_seed ? (uint64_t)*P.drop.dev_seed : P.drop.seed;
@@ -104,22 +161,26 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const 
   const bool muls = P.post_gain || P.scale_mode == kScaleVector;
 #pragma unroll
   for (int it = 0; it < kIter; ++it) {
-    const int c = it * threads + tid;
-    if (c < chunks) {
+    if (part.here(it)) {
       float v[8], w[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[e] = table_at(P.post_gain, c * 8 + e) * table_at(P.scale_mode == kScaleVector ? P.scale : nullptr, c * 8 + e);
-        w[e] = table_at(P.pre_gain, c * 8 + e);
+        const int c = part.column(it, e);
+        v[e] = w[e] = 0.f;
+        if (c < d) {
+          v[e] = table_at(P.post_gain, c) * table_at(P.scale_mode == kScaleVector ? P.scale : nullptr, c);
+          w[e] = table_at(P.pre_gain, c);
+        }
       }
-      mul.put(c, v);
-      pre.put(c, w);
+      mul.put(part.chunk(it), v);
+      pre.put(part.chunk(it), w);
     }
   }
   int turn = 0;
   for (int64_t row = row0; row < P.n; row += step) {
     const uint32_t at = ring.take();
     float2 x[N];
+    const uint32_t x_at = row_start<kOdd>(at, static_cast<const XT *>(P.x), row, P.xs);
     bool joined = false;
     auto join = [&](float v) {
       float sum[1] = {v};
@@ -130,9 +191,8 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const 
     };
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
-      const int c = it * threads + tid;
-      if (c < chunks) {
-        lds8<XT>(at + c * 8 * sizeof(XT), x + 4 * it);
+      if (part.here(it)) {
+        part.template get<XT>(x_at, it, x + 4 * it);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[4 * it + k] = f2_of(0.f);
@@ -141,11 +201,11 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const 
     if (P.block) {
       float2 u[N];
       float2 ss = f2_of(0.f);
+      const uint32_t o_at = row_start<kOdd>(at + to_block, static_cast<const BT *>(P.block), row, P.bs);
 #pragma unroll
       for (int it = 0; it < kIter; ++it) {
-        const int c = it * threads + tid;
-        if (c < chunks) {
-          lds8<BT>(at + xb + c * 8 * sizeof(BT), u + 4 * it);
+        if (part.here(it)) {
+          part.template get<BT>(o_at, it, u + 4 * it);
 #pragma unroll
           for (int k = 0; k < 4; ++k) ss = f2_fma(u[4 * it + k], u[4 * it + k], ss);
         }
@@ -157,25 +217,27 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const 
       XT *const out = static_cast<XT *>(P.xo) + row * P.xos;
 #pragma unroll
       for (int it = 0; it < kIter; ++it) {
-        const int c = it * threads + tid;
-        if (c < chunks) {
+        if (part.here(it)) {
           float2 *const v = u + 4 * it;
           if (muls) {
             float2 t[4];
-            mul.get(c, t);
+            mul.get(part.chunk(it), t);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = f2_mul(v[k], t[k]);
           }
-          if (P.drop.limit) drop8(P.drop, key, (uint64_t)(row * P.d + c * 8), v);
+          if (P.drop.limit) part.drop(P, key, row, it, v, slots);
           if (P.gate_mode == kGateElement) {
             float2 a[4];
-            lds8<BT>(at + xb + bb + c * 8 * sizeof(BT), a);
+            part.template get<BT>(row_start<kOdd>(at + to_gate, static_cast<const BT *>(P.gate), row, P.as), it, a);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = f2_mul(v[k], make_float2(gate_of(a[k].x, P.sigmoid), gate_of(a[k].y, P.sigmoid)));
+            for (int k = 0; k < 4; ++k) {
+              float2 slope;
+              v[k] = f2_mul(v[k], gate_of2(a[k], P.sigmoid, slope));
+            }
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) x[4 * it + k] = f2_fma(f2, v[k], x[4 * it + k]);
-          stg8(out + c * 8, x + 4 * it);
+          part.put(out, it, x + 4 * it);
         }
       }
     }
@@ -187,18 +249,17 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const 
       BT *const out = static_cast<BT *>(P.h) + row * P.hs;
 #pragma unroll
       for (int it = 0; it < kIter; ++it) {
-        const int c = it * threads + tid;
-        if (c < chunks) {
+        if (part.here(it)) {
           float2 *const v = x + 4 * it;
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = f2_mul(v[k], r);
           if (P.pre_gain) {
             float2 t[4];
-            pre.get(c, t);
+            pre.get(part.chunk(it), t);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = f2_mul(v[k], t[k]);
           }
-          stg8(out + c * 8, v);
+          part.put(out, it, v);
         }
       }
     }
@@ -252,18 +313,18 @@ __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ Dr
   }
 }
 
-template <typename XT, typename BT>
-ResKernel pick(const ResCut &c, bool vec) {
-  if (c.stages) return c.iter == 1 ? residual_forward_ring_kernel<XT, BT, 1> : residual_forward_ring_kernel<XT, BT, 2>;
-  if (vec) return c.iter == 1 ? residual_forward_kernel<XT, BT, 1, true> : residual_forward_kernel<XT, BT, 4, true>;
-  return c.iter == 1   ? residual_forward_kernel<XT, BT, 1, false>
-         : c.iter == 2 ? residual_forward_kernel<XT, BT, 2, false>
-                       : residual_forward_kernel<XT, BT, 4, false>;
+template <typename XT, typename BT, bool kVec>
+ResLaunch pick(const ResCut &c) {
+  if (c.form == kFormWide) return launch_res<residual_forward_wide_kernel<XT, BT, kVec>>;
+  if (c.form == kFormGroup) return launch_res<residual_forward_kernel<XT, BT, kVec>>;
+  return c.iter == 1 ? launch_res<residual_forward_ring_kernel<XT, BT, 1, !kVec>>
+                     : launch_res<residual_forward_ring_kernel<XT, BT, 2, !kVec>>;
 }
 
-ResKernel kernel_of(int32_t xt, int32_t bt, const ResCut &c, bool vec) {
-  return xt == GBO_BF16 ? pick<__nv_bfloat16, __nv_bfloat16>(c, vec)
-                        : bt == GBO_BF16 ? pick<float, __nv_bfloat16>(c, vec) : pick<float, float>(c, vec);
+template <bool kVec>
+ResLaunch launcher(int32_t xt, int32_t bt, const ResCut &c) {
+  return xt == GBO_BF16 ? pick<__nv_bfloat16, __nv_bfloat16, kVec>(c)
+                        : bt == GBO_BF16 ? pick<float, __nv_bfloat16, kVec>(c) : pick<float, float, kVec>(c);
 }
 
 }  // namespace
@@ -292,9 +353,10 @@ extern "C" int gbo_residual_forward(const gbo_residual_args *a, void *x_out, int
   P.xo = x_out, P.xos = x_out_stride, P.h = h, P.hs = h_stride;
   const bool vec = inputs_vec(a) && vec_ok(x_out, x_out_stride, a->n) && vec_ok(h, h_stride, a->n);
   P.status = dev_status;
-  P.stage_bytes = (int32_t)(a->d * (size_of(a->x_dtype) + size_of(a->block_dtype) * (a->has_block + (a->gate_mode == GBO_GATE_ELEMENT))));
+  P.stage_bytes = (int32_t)row_bytes(P, a->x_dtype, a->block_dtype, vec, false);
   const ResCut c = cut_of(a->n, a->d, sm, false, vec, P.stage_bytes);
-  const cudaError_t e = dispatch_res(P, c, vec, a->x_dtype, a->block_dtype, dev, reinterpret_cast<cudaStream_t>(stream), kernel_of);
+  const ResLaunch launch = vec ? launcher<true>(a->x_dtype, a->block_dtype, c) : launcher<false>(a->x_dtype, a->block_dtype, c);
+  const cudaError_t e = launch(P, c, dev, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? report_ok() : res_cuda(e);
 }
 

@@ -242,6 +242,44 @@ def test_widths(d, types):
     Case(n, d, *types, gate="row", kind="linear", scale="one", seed=d + 1).check()
 
 
+# rows of single elements through the ring (from 505 elements to 8192) with one and two
+# chunks a thread, and rows that no ring has room for, with chunks and single elements
+ODD_AND_WIDE = [505, 513, 1030, 2051, 4097, 6001, 8191, 8193, 12288, 12291, 16383]
+
+
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(str(x)[6:] for x in t))
+@pytest.mark.parametrize("d", ODD_AND_WIDE)
+def test_odd_and_wide_rows(d, types):
+    Case(5, d, *types, gate="element", p=0.25, seed=d).check()
+    Case(400 if d < 3000 else 3, d, *types, gate="row", scale="one", seed=d + 1).check()
+    Case(4, d, *types, post=False, scale=None, seed=d + 2).check()
+    Case(4, d, *types, pre=False, p=0.1, seed=d + 3).check()
+
+
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(str(x)[6:] for x in t))
+@pytest.mark.parametrize("d,stride", [(1024, 1024), (1023, 1023), (1027, 1030), (4104, 4109)])
+@pytest.mark.parametrize("n", [1, 2, 9])
+def test_rows_that_start_and_end_anywhere(n, d, stride, types):
+    """Tensors that start and end inside a 16-byte block, with NaN around and between their rows."""
+    c = Case(n, d, *types, gate="element", p=0.1, seed=n)
+    at = [0]
+
+    def placed(t):
+        at[0] += 1
+        flat = torch.full((at[0] + (n - 1) * stride + d + 9,), float("nan"), dtype=t.dtype, device="cuda")
+        out = flat[at[0]:at[0] + (n - 1) * stride + d].as_strided((n, d), (stride, 1))
+        out.copy_(t)
+        return out
+
+    for name in ("x", "block", "gate", "dx_out", "dh"):
+        setattr(c, name, placed(getattr(c, name)))
+    x, _, _ = c.check()
+    want = c.backward(x)
+    got = layers.residual_norm_backward(c.dx_out, c.dh, placed(x), c.block, **c.kw())
+    for k, z in want.items():
+        c.near(got[k], z, k)
+
+
 @pytest.mark.parametrize("d", [64, 77, 1024])
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("pre", [True, False])
