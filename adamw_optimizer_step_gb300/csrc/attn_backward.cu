@@ -95,13 +95,10 @@ struct Dkv {
   static_assert(kDk + kKb * 64 <= 512, "TMEM columns");
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
-constexpr int kDkvThreads = (kBwdWarps + 4) * 32;
 
 template <int kKb, int kVb, int kQt>
-__global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_constant__ BwdParams P) {
+__device__ __forceinline__ void attn_dkv(const BwdParams &P, uint8_t *smem, int idx) {
   using C = Dkv<kKb, kVb, kQt>;
-  pdl_launch();
-  extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kUsed);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
@@ -139,7 +136,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attn_dkv_kernel(const __grid_c
 
   const AttnShape &A = P.shape;
   // early keys first: with a causal mask most queries see them
-  int idx = blockIdx.x;
   const int kh = A.by_k_heads.split(idx), b = A.by_batch.split(idx), k0 = idx * kAttnTile;
   const AttnSeq seq = attn_seq(P.mask, b);
   const int shift = (kQt == 128 ? 7 : 6) - A.pack, tokens = 1 << shift;
@@ -399,13 +395,10 @@ struct Dq {
   static_assert(kDq + kKb * 64 <= 512, "TMEM columns");
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
-constexpr int kDqThreads = (kBwdWarps + 3) * 32;
 
 template <int kKb, int kVb>
-__global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_constant__ BwdParams P) {
+__device__ __forceinline__ void attn_dq(const BwdParams &P, uint8_t *smem, int idx) {
   using C = Dq<kKb, kVb>;
-  pdl_launch();
-  extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kUsed);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
@@ -436,7 +429,6 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
   pdl_wait();
 
   const AttnShape &A = P.shape;
-  int idx = blockIdx.x;
   int kh = A.by_all.split(idx);
   const int b = A.by_batch.split(idx), tb = P.tiles - 1 - idx;  // later queries first
   const int hb = A.by_blocks.split(kh), h0 = kh * A.group + (hb << A.pack);
@@ -513,7 +505,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
       V.next(C::kVStages);
     }
     drain_products(done0 + 8);
-  } else {
+  } else if (warp < kBwdWarps) {
     const int grp = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int token = t0 + (row >> A.pack), head = h0 + (row & ((1 << A.pack) - 1));
@@ -596,32 +588,38 @@ __global__ void __launch_bounds__(kDqThreads, 1) attn_dq_kernel(const __grid_con
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
+// Both walks in one launch, the keys' tiles first: the queries' tiles start as the last
+// of those end, and one tail is waited for instead of two (2 x 8192 causal 1147 -> 1111 us,
+// 13 documents in 8192 tokens 175 -> 136).
+struct BothParams {
+  BwdParams keys, queries;
+  int32_t key_tiles;  // CTAs of the keys' walk
+};
+constexpr int kBwdThreads = (kBwdWarps + 4) * 32;
+
+template <int kKb, int kVb, int kQt>
+__global__ void __launch_bounds__(kBwdThreads, 1) attn_backward_kernel(const __grid_constant__ BothParams P) {
+  pdl_launch();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int idx = blockIdx.x;
+  if (idx < P.key_tiles) attn_dkv<kKb, kVb, kQt>(P.keys, smem, idx);
+  else attn_dq<kKb, kVb>(P.queries, smem, idx - P.key_tiles);
+}
+
 // ---------------------------------------------------------------------------
 // host
 
 template <int kKb, int kVb, int kQt>
-cudaError_t launch_dkv(const BwdParams &P, int64_t grid, int dev, cudaStream_t st) {
-  using C = Dkv<kKb, kVb, kQt>;
+cudaError_t launch_walks(const BothParams &P, int64_t grid, int dev, cudaStream_t st) {
+  constexpr int kSmem = std::max(Dkv<kKb, kVb, kQt>::kSmem, Dq<kKb, kVb>::kSmem);
   static PerDevice<cudaError_t> limit;
   const cudaError_t *err = limit.of(dev, [](cudaError_t &e) {
-    e = cudaFuncSetAttribute(attn_dkv_kernel<kKb, kVb, kQt>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(attn_backward_kernel<kKb, kVb, kQt>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
   if (!err || *err != cudaSuccess) return err ? *err : cudaErrorInvalidDevice;
   count_launches(1);
-  return launch_kernel_as(pdl_allowed(), attn_dkv_kernel<kKb, kVb, kQt>, dim3((unsigned)grid), dim3(kDkvThreads), C::kSmem, st,
+  return launch_kernel_as(pdl_allowed(), attn_backward_kernel<kKb, kVb, kQt>, dim3((unsigned)grid), dim3(kBwdThreads), kSmem, st,
                           1, P);
-}
-
-template <int kKb, int kVb>
-cudaError_t launch_dq(const BwdParams &P, int64_t grid, int dev, cudaStream_t st) {
-  using C = Dq<kKb, kVb>;
-  static PerDevice<cudaError_t> limit;
-  const cudaError_t *err = limit.of(dev, [](cudaError_t &e) {
-    e = cudaFuncSetAttribute(attn_dq_kernel<kKb, kVb>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  });
-  if (!err || *err != cudaSuccess) return err ? *err : cudaErrorInvalidDevice;
-  count_launches(1);
-  return launch_kernel_as(pdl_allowed(), attn_dq_kernel<kKb, kVb>, dim3((unsigned)grid), dim3(kDqThreads), C::kSmem, st, 1, P);
 }
 
 }  // namespace
@@ -667,14 +665,15 @@ extern "C" int gbo_attn_backward(const gbo_attn_args *a, const gbo_attn_grads *g
   const int64_t q_tiles = (a->sq + (kAttnTile >> S.pack) - 1) / (kAttnTile >> S.pack), k_tiles = (a->sk + kAttnTile - 1) / kAttnTile;
   const int64_t dkv_grid = keys && (g->dk || g->dv) ? k_tiles * a->batch * a->k_heads : 0;
   const int64_t dq_grid = queries && g->dq ? q_tiles * a->batch * a->k_heads * S.head_blocks : 0;
-  if (dkv_grid > INT32_MAX || dq_grid > INT32_MAX || rows > (int64_t)INT32_MAX * 16)
+  if (dkv_grid + dq_grid > INT32_MAX || rows > (int64_t)INT32_MAX * 16)
     return attn_fail(GBO_ERR_SHAPE, "more rows than one launch takes");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  BwdParams P;
-  memset(&P, 0, sizeof P);
+  BothParams both;
+  memset(&both, 0, sizeof both);
+  BwdParams &P = both.keys, &Q = both.queries;
   P.mask = M, P.shape = S, P.stats = static_cast<const float2 *>(workspace), P.status = dev_status;
-  BwdParams Q = P;
+  Q.mask = M, Q.shape = S, Q.stats = P.stats, Q.status = dev_status;
   DeltaParams D;
   memset(&D, 0, sizeof D);
   bool maps = true;
@@ -703,10 +702,10 @@ extern "C" int gbo_attn_backward(const gbo_attn_args *a, const gbo_attn_grads *g
     count_launches(1);
     e = launch_kernel_as(pdl_allowed(), attn_delta_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, st, 1, D);
   }
-  if (e == cudaSuccess && dkv_grid)
-    e = cfg == 0 ? launch_dkv<1, 1, 128>(P, dkv_grid, dev, st)
-                 : cfg == 1 ? launch_dkv<2, 2, 128>(P, dkv_grid, dev, st) : launch_dkv<3, 2, 64>(P, dkv_grid, dev, st);
-  if (e == cudaSuccess && dq_grid)
-    e = cfg == 0 ? launch_dq<1, 1>(Q, dq_grid, dev, st) : cfg == 1 ? launch_dq<2, 2>(Q, dq_grid, dev, st) : launch_dq<3, 2>(Q, dq_grid, dev, st);
+  both.key_tiles = (int32_t)dkv_grid;
+  const int64_t grid = dkv_grid + dq_grid;
+  if (e == cudaSuccess && grid)
+    e = cfg == 0 ? launch_walks<1, 1, 128>(both, grid, dev, st)
+                 : cfg == 1 ? launch_walks<2, 2, 128>(both, grid, dev, st) : launch_walks<3, 2, 64>(both, grid, dev, st);
   return e == cudaSuccess ? report_ok() : attn_cuda(e);
 }
