@@ -128,10 +128,6 @@ __device__ __forceinline__ void attn_dkv(const BwdParams &P, uint8_t *smem, int 
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
   const AttnShape &A = P.shape;
@@ -152,6 +148,25 @@ __device__ __forceinline__ void attn_dkv(const BwdParams &P, uint8_t *smem, int 
     }
   }
   const int steps = n_tok * A.head_blocks, group = A.group;
+  if (steps == 0) {
+    zero_block(smem);
+    if (threadIdx.x == 0) {
+      for (int r0 = 0; r0 < kAttnTile && k0 + r0 < P.mask.sk; r0 += 32) {
+        if (P.has1)
+          for (int c = 0; c < A.kb; ++c) tma_store_4d(&P.o1, smem_u32(smem), 64 * c, kh, k0 + r0, b);
+        if (P.has2)
+          for (int c = 0; c < A.vb; ++c) tma_store_4d(&P.o2, smem_u32(smem), 64 * c, kh, k0 + r0, b);
+      }
+      bulk_commit();
+      bulk_wait_read<0>();
+    }
+    if (warp == kBwdWarps) tmem_free(*tmem_slot, 512);
+    return;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   const uint32_t kt = smem_u32(smem), vt = kt + C::kKTile, qring = kt + C::kRing;
   const uint32_t dring = qring + C::kQStages * C::kQStage;
   float *const stats = reinterpret_cast<float *>(smem + C::kStatAt);
@@ -350,9 +365,9 @@ __device__ __forceinline__ void attn_dkv(const BwdParams &P, uint8_t *smem, int 
           for (int c = blk * 64; c < blk * 64 + 64; c += 32) {
             uint32_t r[32];
             float v[32];
-            if (steps > 0) tmem_read<32>(from + c, r);
+            tmem_read<32>(from + c, r);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = steps > 0 && live ? __uint_as_float(r[e]) * f : 0.f;
+            for (int e = 0; e < 32; ++e) v[e] = live ? __uint_as_float(r[e]) * f : 0.f;
             put_tile_row(out, row, c, v);
           }
           fence_async_smem();
@@ -370,8 +385,7 @@ __device__ __forceinline__ void attn_dkv(const BwdParams &P, uint8_t *smem, int 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kBwdWarps)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  if (warp == kBwdWarps) tmem_free(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -422,10 +436,6 @@ __device__ __forceinline__ void attn_dq(const BwdParams &P, uint8_t *smem, int i
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
   const AttnShape &A = P.shape;
@@ -437,6 +447,21 @@ __device__ __forceinline__ void attn_dq(const BwdParams &P, uint8_t *smem, int i
   const DocWindow docs = doc_window(P.mask, t0);
   const TileKeys tk = tile_keys(P.mask, seq, docs, t0, tokens);
   const int steps = max(0, tk.j1 - tk.j0);
+  if (steps == 0) {
+    zero_block(smem);
+    if (threadIdx.x == 0) {
+      for (int r0 = 0; r0 < kAttnTile && t0 + (r0 >> A.pack) < P.mask.sq; r0 += 32)
+        for (int c = 0; c < A.kb; ++c) tma_store_4d(&P.o1, smem_u32(smem), 64 * c, h0, t0 + (r0 >> A.pack), b);
+      bulk_commit();
+      bulk_wait_read<0>();
+    }
+    if (warp == kBwdWarps) tmem_free(*tmem_slot, 512);
+    return;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   const uint32_t qt = smem_u32(smem), dt = qt + C::kQTile, kring = qt + C::kKRing, vring = qt + C::kVRing;
   const AttnGuard guard = {abort_flag, P.status};
 
@@ -565,9 +590,9 @@ __device__ __forceinline__ void attn_dq(const BwdParams &P, uint8_t *smem, int i
         for (int c = blk * 64; c < blk * 64 + 64; c += 32) {
           uint32_t r[32];
           float v[32];
-          if (steps > 0) tmem_read<32>(trow + C::kDq + c, r);
+          tmem_read<32>(trow + C::kDq + c, r);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = steps > 0 && live ? __uint_as_float(r[e]) * A.scale : 0.f;
+          for (int e = 0; e < 32; ++e) v[e] = live ? __uint_as_float(r[e]) * A.scale : 0.f;
           put_tile_row(qt, row, c, v);
         }
         fence_async_smem();
@@ -584,8 +609,7 @@ __device__ __forceinline__ void attn_dq(const BwdParams &P, uint8_t *smem, int i
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kBwdWarps)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  if (warp == kBwdWarps) tmem_free(tmem, 512);
 }
 
 // Both walks in one launch, the keys' tiles first: the queries' tiles start as the last

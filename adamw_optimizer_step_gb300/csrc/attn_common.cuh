@@ -60,7 +60,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnMask &M, int b) {
 // 32 document starts (and the end of the last, where it is among them), one a
 // lane: those from the document that holds some token on, or all of them.  A
 // search in memory takes a dependent load a step, some 500 clocks each; one among
-// lanes takes a shuffle a step (13 documents in 8192 tokens: forward 190 -> 45 us).
+// lanes takes a shuffle a step.
 struct DocWindow {
   int32_t base, v;
 };
@@ -309,6 +309,10 @@ __device__ __forceinline__ void tmem_write(uint32_t taddr, const uint32_t (&r)[k
 
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+}
+
 // kind::f16: bf16 operands, fp32 sums, M = 128, N = n; A K-major.
 __host__ __device__ constexpr uint32_t attn_idesc(bool b_mn_major, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
@@ -539,6 +543,17 @@ __device__ __forceinline__ void put_tile_row(uint32_t tile, int r, int c0, const
                  "r"(pack_bf16(v[8 * q + 4], v[8 * q + 5])), "r"(pack_bf16(v[8 * q + 6], v[8 * q + 7]))
                  : "memory");
   }
+}
+
+// A block of 128 rows of zeros at the start of shared memory, for a tile that sees
+// nothing: its output is stored from there, and no pipeline starts for it.  All
+// threads of the CTA; orders tcgen05.alloc before what follows, too.
+__device__ __forceinline__ void zero_block(uint8_t *smem) {
+  for (int i = threadIdx.x; i < kAttnBlock / 16; i += blockDim.x) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
 }
 
 // ---------------------------------------------------------------------------

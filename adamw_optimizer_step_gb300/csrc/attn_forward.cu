@@ -96,10 +96,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
   const AttnShape &A = P.shape;
@@ -130,6 +126,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
       tk[t].j1 = max(tk[t].j0, min(tk[t].j1, J1));
     }
   }
+  if (P.splits == 1 && J1 <= J0) {
+    zero_block(smem);
+    if (threadIdx.x == 0) {
+      for (int r0 = 0; r0 < 2 * kAttnTile && t0 + (r0 >> A.pack) < P.mask.sq; r0 += 32)
+        for (int c = 0; c < A.vb; ++c) tma_store_4d(&P.y, smem_u32(smem), 64 * c, h0, t0 + (r0 >> A.pack), b);
+      bulk_commit();
+      bulk_wait_read<0>();
+    }
+    for (int r = threadIdx.x; P.lse && r < 2 * kAttnTile; r += kFwdThreads) {
+      const int token = t0 + (r >> A.pack), head = h0 + (r & ((1 << A.pack) - 1));
+      if (token < P.mask.sq) P.lse[((int64_t)b * P.mask.sq + token) * A.q_heads + head] = -INFINITY;
+    }
+    if (warp == kFwdSoftWarps) tmem_free(*tmem_slot, C::kCols);
+    return;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   const uint32_t q0 = smem_u32(smem), kring = q0 + C::kKRing, vring = q0 + C::kVRing;
   const AttnGuard guard = {abort_flag, P.status};
 
@@ -349,8 +364,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kFwdSoftWarps)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+  if (warp == kFwdSoftWarps) tmem_free(tmem, C::kCols);
 }
 
 // ---------------------------------------------------------------------------
