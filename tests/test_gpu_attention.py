@@ -461,3 +461,24 @@ def test_workspace_refused_when_small():
     for ws in (None, torch.empty(B.gbo_attn_backward_workspace_bytes(args) - 1, dtype=torch.uint8, device="cuda")):
         with pytest.raises(B.GboError, match="workspace"):
             B.gbo_attn_backward(args, q, k, v, dy, y, lse, ws, dq=torch.empty_like(q))
+
+
+def test_sequences_of_a_batch_are_the_sequences_alone():
+    """Many tiles a CTA's place could be mistaken in, some that see nothing: the same bits as of two sequences alone."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    made = lambda *s: torch.randn(*s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    b, s, h = 6, 500, 30
+    q, k, v, dy = made(b, s, h, 192), made(b, s, h, 192), made(b, s, h, 128), made(b, s, h, 128)
+    lengths = torch.tensor([500, 1, 0, 257, 128, 499], dtype=torch.int32, device="cuda")
+    for causal in (True, False):
+        mask = dict(causal=causal, q_lengths=lengths, k_lengths=lengths)
+        y, lse = layers.attention(q, k, v, return_lse=True, **mask)
+        grads = layers.attention_backward(dy, q, k, v, y, lse, **mask)
+        for i in range(0, b, 2):
+            part = slice(i, i + 2)
+            one = dict(causal=causal, q_lengths=lengths[part], k_lengths=lengths[part])
+            yi, li = layers.attention(q[part], k[part], v[part], return_lse=True, **one)
+            assert torch.equal(yi, y[part]) and torch.equal(li, lse[part])
+            gi = layers.attention_backward(dy[part], q[part], k[part], v[part], yi, li, **one)
+            for got, want in zip(gi, grads):
+                assert torch.equal(got, want[part])
