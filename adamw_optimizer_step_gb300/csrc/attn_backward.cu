@@ -3,15 +3,27 @@
 //   dV = P^T dY,  dS = scale P (dY V^T - D),  dQ = dS K,  dK = dS^T Q.
 // P is formed again from the forward's lse: P = 2^(S c - lse log2(e)).
 //
-//   attn_delta_kernel  per row: -lse log2(e) and D
-//   attn_dkv_kernel    a CTA holds 128 keys and walks over the rows that see them
-//   attn_dq_kernel     a CTA holds 128 rows and walks over the keys that they see
+//   attn_delta_kernel     per row: -lse log2(e) and D
+//   attn_backward_kernel  attn_dkv: a CTA holds 128 keys and walks over the rows that see them;
+//                         attn_dq: a CTA holds 128 rows and walks over the keys that they see
 //
 // Two walks form S and dP twice (7 products instead of 5), and in return no
 // sum crosses CTAs: no atomics, results that repeat bit for bit, no fp32 dQ in
 // memory.  Every sum stays in TMEM for a CTA's whole walk, the query heads that
 // share a key head among them.  P and dS are rounded to bf16 once, as operands of
-// products (by 2^-8 of them at most); sums are fp32.
+// products (by 2^-8 of them at most); sums are fp32.  With D from the rounded y, that
+// makes dQ's and dK's error 2.5e-3 of them against 1.7e-3 of the outputs' rounding
+// alone; dS as two bf16 numbers would take two products more.
+//
+// Measured, causal, 2 x 8192 tokens, 16 query and 4 key heads of 128: 1110 us, the
+// keys' walk alone 670 (1.64 PFLOP/s of the four products it forms), the queries'
+// alone 490 with the delta kernel (1.69 of three): 86% of a library product's rate.
+// Bound: tensor cores (active 72% at 4096 tokens, where the tail counts), then the
+// elementwise warps between S and dS.  13 documents in 8192 tokens 139 us, 6 x 777
+// tokens of 32 heads of 192 and 128 187 us: a CTA's start and end (9000 clocks).
+// Resident CTAs with several tiles each, the next one looked up ahead: 488 us in place
+// of 493 for the queries' walk, but 93 in place of 83 for the documents, whose tiles
+// are uneven.  Not kept.
 #include "attn_common.cuh"
 
 namespace gbo {
@@ -23,7 +35,8 @@ constexpr float kLog2ePlain = 1.4426950408889634f;
 
 // ---------------------------------------------------------------------------
 // -lse log2(e) and D of each row: 16 lanes to a row.  A row that sees nothing
-// (lse = -inf) gets -inf and 0, whatever stands in it: its P and dS are 0.
+// (lse = -inf) gets -inf and 0, whatever stands in it: its P and dS are 0.  Bound by
+// HBM (dy and y once); 10 us for 4096 x 16 heads of 128, from HBM.
 
 struct DeltaParams {
   const __nv_bfloat16 *dy, *y;

@@ -40,12 +40,6 @@ __device__ __forceinline__ float drop_factor(const uint4 &w, int e, uint32_t lim
   return ((e & 1) ? x >> 16 : x & 0xffffu) >= limit ? keep : 0.f;
 }
 
-// The factor of one element (ten rounds each: not inlined, rows of odd sizes call
-// it up to 32 times).
-__device__ __noinline__ static float drop_one(const DropArgs &D, uint64_t key, uint64_t element) {
-  return drop_factor(philox(key, element >> 3, D.offset), (int)(element & 7), D.limit, D.keep);
-}
-
 // limit and keep of a probability: nearest multiple of 2^-16, ties to even.
 // False for one outside 0 <= p < 1 (or that would round to 1).
 inline bool drop_of(double p, DropArgs *D) {

@@ -10,8 +10,8 @@
 //             da = g scale m u gate'(a),  du = g scale gate m,
 //             v = o rho(o), w = post_gain du:  do = rho(o) (w - v mean(w v)),
 //             dpost_gain = sum du v           (sums over rows)
-// Bound: HBM; every tensor is read or written once, a row stays in registers
-// from its loads to its stores.
+// Floor: HBM; every tensor is read or written once.  What bounds the forward pass
+// (without gate and dropout) is HBM, the gradients issue slots.
 //
 // Three forms, by size:
 //   ring   rows of 505 to 8192 elements, a CTA each, through shared memory
@@ -25,9 +25,10 @@
 //   32768 x 2048, gate and dropout    556 -> 231     (no gate or dropout) 84
 //   65600 x 1023, the same           2748 -> 811     903 -> 398
 //   8192 x 8192 (wide), the same     1652 -> 705     (ring) 163 -> 141
-//   4096 x 16384 (wide), the same    1020 -> 608     244 -> 198  The sums over rows stay with the
-// thread that has the columns (registers; wide: shared memory), one partial row a
-// group is left at the end, and a second kernel adds them in a fixed order.
+//   4096 x 16384 (wide), the same    1020 -> 608     244 -> 198
+// The sums over rows stay with the thread that has the columns (registers; wide: shared
+// memory), one partial row a group is left at the end, and a second kernel adds them in
+// a fixed order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -236,11 +237,12 @@ __device__ __forceinline__ void block_factors(const ResParams &P, uint64_t key, 
 // ---------------------------------------------------------------------------
 // rows through shared memory
 
-// Rows come through a ring of stages in shared memory: the input tensors of a row one behind the other, by bulk copies that thread 0
-// issues up to `stages` rows ahead.  Loads are then in flight all the time at no
-// cost in registers, while a row's two sums over its threads and its arithmetic
-// take their time.  A stage is filled again behind the first join of the next
-// row, which every thread reaches after its last read of the stage.  (A warp of
+// Rows come through a ring of stages in shared memory: the input tensors of a row
+// one behind the other, by bulk copies that thread 0 issues up to `stages` rows
+// ahead.  Loads are then in flight all the time at no cost in registers, while a
+// row's sums over its threads and its arithmetic take their time.  A stage is filled
+// again behind the first join of the next row, which every thread reaches after its
+// last read of the stage.  (A warp of
 // its own for the copies takes registers from the others: 18 warps an SM have 96
 // each, 16 have 128.)  The column tables stand behind the ring: from global memory
 // each use would wait for L2 behind the row's joins.  What bounds these kernels

@@ -337,11 +337,11 @@ int gbo_adamw_step(const gbo_adamw_desc *descs, int32_t n, const gbo_adamw_opts 
 
 /*
  * The gradients the AdamW path steps come from the model's forward and
- * backward passes; the next two groups of entry points are the two places
- * where the AdamW parameters of the OMN recipe other than the hidden norm
- * gains enter them: the q/k norm gains of a block (with the rotation that
- * follows them), and the tied embedding as the output classifier.  The
- * source pages state the parameters (128 + 128 gains a block, one tied
+ * backward passes; the groups of entry points from here on are where the
+ * AdamW parameters of the OMN recipe enter them, and what stands between: the
+ * q/k norm gains of a block (with the rotation that follows them), the tied
+ * embedding as the output classifier, attention, and the residual update with
+ * the hidden norms' gains.  The source pages state the parameters (128 + 128 gains a block, one tied
  * 128,256 x 2,048 table), not these passes; the formulas are the usual ones
  * and are written out here.
  *
