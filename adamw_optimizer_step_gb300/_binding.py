@@ -756,6 +756,14 @@ def _attn_heads(t, what, shape):
     return s[:3]
 
 
+def _here(*tensors):
+    """Refuse tensors (of those given) that are not on the current device: that is where a call's kernels run."""
+    device = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("tensors must be on the current device, cuda:%d, not on %s" % (device, t.device))
+
+
 def _attn_index(t, count, what):
     if t is None:
         return 0
@@ -777,6 +785,7 @@ def attn_args(q, k, v, *, causal=True, window=0, scale=None, q_lengths=None, k_l
                   _attn_heads(v, "v", (batch, sk, hk, dv)))
     if not (q.is_cuda and k.is_cuda and v.is_cuda):
         raise ValueError("q, k and v must be CUDA tensors")
+    _here(q, k, v, q_lengths, k_lengths, documents)
     docs = _attn_index(documents, None, "documents")
     n_docs = documents.shape[0] - 1 if documents is not None else 0
     return _PACK_ATTN_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), _attn_index(q_lengths, batch, "q_lengths"),
@@ -805,6 +814,7 @@ def gbo_attn_forward(args, q, v, y, workspace=None, *, lse=None, dev_status=None
     ys = _PACK_STRIDE(*_attn_heads(y, "y", (b, sq, hq, v.shape[3])))
     if not y.is_cuda:
         raise ValueError("y must be a CUDA tensor")
+    _here(y, lse, workspace, dev_status)
     ws, nbytes = _workspace(workspace)
     _check(lib().gbo_attn_forward(args, y.data_ptr(), ys, _out_f32(lse, b * sq * hq, "lse"), ws, nbytes,
                                   _dev_ptr(dev_status, "dev_status"), _stream(stream)))
@@ -826,6 +836,7 @@ def gbo_attn_backward(args, q, k, v, dy, y, lse, workspace, *, dq=None, dk=None,
         if not t.is_cuda:
             raise ValueError("%s must be a CUDA tensor" % what)
         ptrs.append(t.data_ptr())
+    _here(dy, y, lse, dq, dk, dv, workspace, dev_status)
     grads = _PACK_ATTN_GRADS(ptrs[0], ptrs[1], _out_f32(lse, b * sq * hq, "lse"), *ptrs[2:], *strides)
     ws, nbytes = _workspace(workspace)
     _check(lib().gbo_attn_backward(args, grads, ws, nbytes, _dev_ptr(dev_status, "dev_status"), _stream(stream)))
@@ -844,6 +855,7 @@ def _seed_of(seed):
     if isinstance(seed, torch.Tensor):
         if seed.dtype is not torch.int64 or seed.numel() != 1 or not seed.is_cuda:
             raise ValueError("a seed in a tensor is one int64 value on the device")
+        _here(seed)
         return 0, seed.data_ptr()
     return int(seed) & _U64, 0
 
@@ -871,6 +883,7 @@ def residual_args(x, block, *, post_norm=False, pre_norm=True, post_gain=None, p
     if scale is not None:
         smode = GBO_SCALE_ONE if scale.numel() == 1 else GBO_SCALE_VECTOR
         sp = _out_f32(scale, 1 if smode == GBO_SCALE_ONE else d, "scale")
+    _here(x, block, gate, scale, post_gain, pre_gain)
     host, dev = _seed_of(seed)
     return _PACK_RESIDUAL_ARGS(x.data_ptr(), ba, gp, sp, _out_f32(post_gain, d, "post_gain") or 0,
                                _out_f32(pre_gain, d, "pre_gain") or 0, dev, host, int(offset) & _U64, n, d, xs, bs, gs,
@@ -893,6 +906,7 @@ def gbo_residual_forward(args, x_out, h, shape, x_dtype, block_dtype, dev_status
     (each may be None where there is nothing to write), ``shape`` (n, d) both."""
     xp, xs = _rows_or_null(x_out, "x_out", shape, x_dtype)
     hp, hs = _rows_or_null(h, "h", shape, block_dtype)
+    _here(x_out, h, dev_status)
     _check(lib().gbo_residual_forward(args, xp, xs, hp, hs, _dev_ptr(dev_status, "dev_status"), _stream(stream)))
 
 
@@ -910,6 +924,7 @@ def gbo_residual_backward(args, workspace, shape, x_dtype, block_dtype, *, dx_ou
                           dgate=None, dscale=None, dpost_gain=None, dpre_gain=None, dev_status=None, stream=None):
     """Gradients of the residual update, whichever are given to be written."""
     n, d = shape
+    _here(dx_out, dh, dx, dblock, dgate, dscale, dpost_gain, dpre_gain, workspace, dev_status)
     oxp, oxs = _rows_or_null(dx_out, "dx_out", shape, x_dtype)
     ohp, ohs = _rows_or_null(dh, "dh", shape, block_dtype)
     xp, xs = _rows_or_null(dx, "dx", shape, x_dtype)
@@ -928,6 +943,7 @@ def gbo_dropout(x, y, p, seed, offset=0, stream=None):
     if x.dtype not in _ELEMENT or y.dtype != x.dtype:
         raise TypeError("x and y must both be float32 or bfloat16, got %s and %s" % (x.dtype, y.dtype))
     xs, ys = _rows_of(x, "x"), _rows_of(y, "y", x.shape)
+    _here(x, y)
     host, dev = _seed_of(seed)
     _check(lib().gbo_dropout(x.data_ptr(), xs, y.data_ptr(), ys, x.shape[0], x.shape[1], _ELEMENT[x.dtype], float(p),
                              host, int(offset) & _U64, dev, _stream(stream)))

@@ -482,3 +482,13 @@ def test_sequences_of_a_batch_are_the_sequences_alone():
             gi = layers.attention_backward(dy[part], q[part], k[part], v[part], yi, li, **one)
             for got, want in zip(gi, grads):
                 assert torch.equal(got, want[part])
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Where the current device is another one than the tensors' (here: as the binding sees it)."""
+    q, k, v = (torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    y, lse = layers.attention(q, k, v, return_lse=True)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for call in (lambda: layers.attention(q, k, v), lambda: layers.attention_backward(y, q, k, v, y, lse)):
+        with pytest.raises(ValueError, match="on the current device"):
+            call()

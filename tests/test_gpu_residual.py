@@ -501,3 +501,13 @@ def test_workspace_refused_when_small():
     for ws in (None, torch.empty(need - 1, dtype=torch.uint8, device="cuda"), torch.empty(need + 8, dtype=torch.uint8, device="cuda")[8:]):
         with pytest.raises(B.GboError, match="workspace"):
             B.gbo_residual_backward(args, ws, (40, 128), BF16, BF16, dx_out=c.dx_out, dh=c.dh, dpre_gain=out)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Where the current device is another one than the tensors' (here: as the binding sees it)."""
+    c = Case(4, 64)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for call in (lambda: layers.residual_norm(c.x, c.block, **c.kw()), lambda: layers.dropout(c.x, 0.5, 1),
+                 lambda: layers.residual_norm_backward(c.dx_out, c.dh, c.x, c.block, **c.kw())):
+        with pytest.raises(ValueError, match="on the current device"):
+            call()
