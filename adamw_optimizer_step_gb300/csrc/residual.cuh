@@ -588,7 +588,9 @@ constexpr int kSmemMost = 220 * 1024;  // of an SM's shared memory, for rings an
 
 // Ring: a row goes to as many threads as it has chunks of eight elements, up to 512;
 // to half as many in the forward pass (what a row costs beside its elements is half
-// as much then); 512 threads an SM.  `row_bytes`: of a row's inputs, in their places.
+// as much then); 512 threads an SM.  Gradients of single elements, two chunks a thread,
+// spill (8194 x 8190: 1303 us, the wide form 651): those rows take the wide form, shorter
+// ones the ring (65600 x 1023: 811 us, wide 2544).  `row_bytes`: of a row's inputs, in their places.
 ResCut cut_of(int64_t n, int64_t d, int sm, bool back, bool vec, int64_t row_bytes) {
   ResCut c;
   memset(&c, 0, sizeof c);
@@ -596,7 +598,7 @@ ResCut cut_of(int64_t n, int64_t d, int sm, bool back, bool vec, int64_t row_byt
   auto blocks = [&](int per_sm, int64_t rows) {
     c.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm * per_sm, (n + rows - 1) / rows));
   };
-  if (chunks >= 64 && chunks <= 2 * kMaxGroup) {
+  if (chunks >= 64 && chunks <= 2 * kMaxGroup && (vec || !back || chunks <= kMaxGroup)) {
     c.group = 64;
     while (c.group < kMaxGroup && (int64_t)c.group * (back ? 1 : 2) < chunks) c.group *= 2;
     c.iter = (int32_t)((chunks + c.group - 1) / c.group);

@@ -559,12 +559,15 @@ template <typename XT, typename BT, bool kVec>
 ResLaunch pick(const ResCut &c, bool all) {
   if (c.form == kFormWide) return launch_res<residual_backward_wide_kernel<XT, BT, kVec>>;
   if (c.form == kFormGroup) return launch_res<residual_backward_kernel<XT, BT, kVec>>;
-  if constexpr (kVec)
+  if constexpr (!kVec) {
+    return launch_res<residual_backward_ring_kernel<XT, BT, 1, true, false>>;
+  } else {
     if (all)
       return c.iter == 1 ? launch_res<residual_backward_ring_kernel<XT, BT, 1, false, true>>
                          : launch_res<residual_backward_ring_kernel<XT, BT, 2, false, true>>;
-  return c.iter == 1 ? launch_res<residual_backward_ring_kernel<XT, BT, 1, !kVec, false>>
-                     : launch_res<residual_backward_ring_kernel<XT, BT, 2, !kVec, false>>;
+    return c.iter == 1 ? launch_res<residual_backward_ring_kernel<XT, BT, 1, false, false>>
+                       : launch_res<residual_backward_ring_kernel<XT, BT, 2, false, false>>;
+  }
 }
 
 template <bool kVec>
