@@ -511,3 +511,26 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
                  lambda: layers.residual_norm_backward(c.dx_out, c.dh, c.x, c.block, **c.kw())):
         with pytest.raises(ValueError, match="on the current device"):
             call()
+
+
+@pytest.mark.parametrize("d", [64, 77, 1023, 1024, 6144, 8199, 12288])
+@pytest.mark.parametrize("post", [True, False])
+def test_outputs_in_the_places_of_inputs(d, post):
+    """x' over x and h over the block's output; dx over dx_out and dblock over dh: the same bits."""
+    c = Case(700 if d < 2000 else 5, d, gate="element", post=post, seed=9)
+    x, h = layers.residual_norm(c.x, c.block, **c.kw())
+    want = layers.residual_norm_backward(c.dx_out, c.dh, x, c.block, **c.kw())
+    shape = (c.n, d)
+    args = B.residual_args(c.x, c.block, **c.kw())
+    x_in, block_in = c.x.clone(), c.block.clone()
+    B.gbo_residual_forward(args, c.x, c.block, shape, BF16, BF16)
+    assert torch.equal(c.x, x) and torch.equal(c.block, h)
+    c.x, c.block = x_in, block_in
+    args = B.residual_args(x, c.block, **c.kw())
+    sums = {k: torch.empty_like(want[k]) for k in ("dscale", "dpost_gain", "dpre_gain") if want[k] is not None}
+    ws = torch.empty(B.gbo_residual_workspace_bytes(c.n, d, len(sums)), dtype=torch.uint8, device="cuda")
+    dgate = torch.empty_like(c.gate)
+    B.gbo_residual_backward(args, ws, shape, BF16, BF16, dx_out=c.dx_out, dh=c.dh, dx=c.dx_out, dblock=c.dh, dgate=dgate, **sums)
+    assert torch.equal(c.dx_out, want["dx"]) and torch.equal(c.dh, want["dblock"]) and torch.equal(dgate, want["dgate"])
+    for k, t in sums.items():
+        assert torch.equal(t, want[k])
