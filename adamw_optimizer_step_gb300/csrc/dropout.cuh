@@ -37,7 +37,7 @@ __device__ __forceinline__ uint4 philox(uint64_t key, uint64_t i, uint64_t offse
 // Factor of element e (0..7) of those draws: 0 or keep.
 __device__ __forceinline__ float drop_factor(const uint4 &w, int e, uint32_t limit, float keep) {
   const uint32_t x = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
-  return ((e & 1) ? x >> 16 : x & 0xffffu) >= limit ? keep : 0.f;
+  return ((e & 1) ? x : x << 16) >= limit << 16 ? keep : 0.f;  // (compared in the upper half)
 }
 
 // limit and keep of a probability: nearest multiple of 2^-16, ties to even.

@@ -395,6 +395,10 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
   int turn = 0;
   uint32_t at = 0;
   if (row0 < P.n) first_sums(at = ring.take(), row0, sums);
+  // this thread's row of each output, moved on from row to row (the block's gradient a row behind)
+  XT *out_x = static_cast<XT *>(P.xo) + row0 * P.xos;
+  BT *out_gate = static_cast<BT *>(P.dgate) + row0 * P.das, *out_o = static_cast<BT *>(P.h) + row0 * P.hs;
+  const int64_t x_by = step * P.xos, gate_by = step * P.das, o_by = step * P.hs;
   for (int64_t row = row0; row < P.n + step; row += step) {  // (one turn more for the last row's block gradient)
     const int64_t last = row - step;
     sums = warp_sum4(sums, lane);
@@ -421,9 +425,10 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
           if (part.here(it)) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) g[4 * it + k] = f2_mul(ro2, f2_fma(o[4 * it + k], m2, g[4 * it + k]));
-            part.put(static_cast<BT *>(P.h) + last * P.hs, it, g + 4 * it);
+            part.put(out_o, it, g + 4 * it);
           }
         }
+        out_o += o_by;
       }
     }
     turn ^= 1;
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
             dx[k] = f2_fma(r2, f2_fma(x[k], c2, f2_mul(dh[k], t[k])), dx[k]);
           }
         }
-        if (out_dx) part.put(static_cast<XT *>(P.xo) + row * P.xos, it, dx);
+        if (out_dx) part.put(out_x, it, dx);
         if (has_block) {
           float2 M[4], a[4];
           float2 *const v = o + 4 * it;
@@ -471,18 +476,20 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
             const float2 t = f2_mul(dx[k], v[k]);
             float2 f = f2_of(row_gate), slope = f2_of(row_slope);
             if (gated) f = gate_of2(a[k], P.sigmoid, slope);
-            const float2 tf = f2_mul(t, f);
-            a_all[4 * it + k] = f2_add(a_all[4 * it + k], tf);
-            a[k] = f2_mul(f2_mul(t, M[k]), slope);
+            const float2 tm = f2_mul(t, M[k]);
+            a_all[4 * it + k] = f2_fma(t, f, a_all[4 * it + k]);
+            a[k] = f2_mul(tm, slope);
             jg = f2_add(jg, a[k]);
-            j0 = f2_fma(tf, M[k], j0);
+            j0 = f2_fma(tm, f, j0);
             dx[k] = f2_mul(dx[k], f2_mul(f, M[k]));
           }
-          if (gated && P.dgate) part.put(static_cast<BT *>(P.dgate) + row * P.das, it, a);
-          if (out_do && !post_norm) part.put(static_cast<BT *>(P.h) + row * P.hs, it, dx);
+          if (gated && P.dgate) part.put(out_gate, it, a);
+          if (out_do && !post_norm) part.put(out_o, it, dx);
         }
       }
     }
+    out_x += x_by, out_gate += gate_by;
+    if (!post_norm) out_o += o_by;
     j1 = jg.x + jg.y;
     ring.next();
     sums = make_float4(0.f, 0.f, 0.f, j0.x + j0.y);
