@@ -385,15 +385,19 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a, uint32_t b, i
 // D (+)= A B over kSteps steps of K = 16, A in TMEM, B with K along its rows
 // (MN-major) in blocks of 64 columns of b_block bytes, n columns in all.  A was
 // written by kParts warps, each to the start of its own part_stride columns.
-template <int kSteps, int kParts>
+// [kFrom, kTo) of each part's steps: a part may be multiplied piece by piece.
+template <int kSteps, int kParts, int kFrom = 0, int kTo = kSteps / kParts>
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t part_stride, uint32_t b, uint32_t b_block, int n,
                                            bool accumulate) {
   constexpr int kEach = kSteps / kParts;
   const uint32_t idesc = attn_idesc(true, n);
   const uint32_t bl = desc_low(b, b_block);
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k)
-    mma_ts(d, a + (k / kEach) * part_stride + (k % kEach) * 8, bl + k * (2048 >> 4), idesc, accumulate || k > 0);
+  for (int part = 0; part < kParts; ++part)
+#pragma unroll
+    for (int k = kFrom; k < kTo; ++k)
+      mma_ts(d, a + part * part_stride + k * 8, bl + (part * kEach + k) * (2048 >> 4), idesc,
+             accumulate || part > 0 || k > kFrom);
 }
 
 // ---------------------------------------------------------------------------

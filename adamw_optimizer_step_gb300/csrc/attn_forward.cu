@@ -10,14 +10,16 @@
 // Per tile of rows and of keys: S = Q K^T (TMEM), P = 2^(S c - m) with c =
 // scale log2(e) by the eight warps of the row tile, half a row to a thread, back
 // into TMEM in bf16 over S, O += P V (TMEM).  While the softmax of one row tile
-// runs, the tensor cores work for the other: PV0(j-1) S0(j) PV1(j-1) S1(j).
+// runs, the tensor cores work for the other: PV0(j-1) S0(j) PV1(j-1) S1(j).  What
+// bounds that turn is the time from S to P, so P V starts with the first half of each
+// warp's P while the second is formed (2 x 8192 tokens: 380 -> 344 us).
 // m is a running maximum that is moved, and O rescaled, only when a row's
 // maximum grows by more than 2^8: until then P is at most 2^8 and its rounding
 // is relative, so nothing is lost; sums are fp32.  P is rounded to bf16 once
 // (2^-8 of it at most, as the operand of the product); the sum takes it unrounded.
-// Measured, causal, 16 query and 4 key heads of 128: 2 x 8192 tokens 379 us, 1.45
-// PFLOP/s of the products that count (76% of a library product's rate); 512 new tokens
-// over a cache of 32768 (keys split, parts joined) 117 us, 1.17.  Bound: the turn of the two row
+// Measured, causal, 16 query and 4 key heads of 128: 2 x 8192 tokens 344 us, 1.60
+// PFLOP/s of the products that count (84% of a library product's rate); 512 new tokens
+// over a cache of 32768 (keys split, parts joined) 108 us, 1.27.  Bound: the turn of the two row
 // tiles, S to softmax to P V; the warps issue 39% of the time, mostly waiting for
 // products.  Short sequences (documents, 777 tokens) are bound by a CTA's start and
 // end, some 9000 clocks: 65 us at 2.4 to 3.7 TB/s.  A CTA that walks over several
@@ -39,8 +41,9 @@ struct Fwd {
   static constexpr int kKStages = kKb == 1 ? 5 : kKb == 2 ? 3 : 2, kVStages = kKb == 1 ? 5 : kKb == 2 ? 2 : 1;
   static constexpr int kKRing = 2 * kQTile, kVRing = kKRing + kKStages * kQTile;
   static constexpr int kUsed = kVRing + kVStages * kVTile;
-  // queries (two), keys and values full/empty, raw, S, P, O (two each), pairs of warps, drained (two), turns (two)
-  static constexpr int kBars = 2 + 2 * kKStages + 2 * kVStages + 1 + 6 + 8 + 2 + 2;
+  // queries (two), keys and values full/empty, raw, S, P, P's second half, O (two each), pairs of warps, drained (two),
+  // turns (two)
+  static constexpr int kBars = 2 + 2 * kKStages + 2 * kVStages + 1 + 8 + 8 + 2 + 2;
   static constexpr int kHalves = 2 * 2 * kAttnTile * 4;  // half of the keys, row tile, row: a float
   static constexpr int kSmem = kUsed + kHalves + kBars * 8 + 16;
   static constexpr uint32_t kO = 256;  // TMEM: S0, S1 of 128 columns, O0, O1 of kVb * 64
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
   const uint32_t qfull0 = smem_u32(bars), kfull0 = qfull0 + 16, kempty0 = kfull0 + 8 * C::kKStages;
   const uint32_t vfull0 = kempty0 + 8 * C::kKStages, vempty0 = vfull0 + 8 * C::kVStages, raw = vempty0 + 8 * C::kVStages;
-  const uint32_t sfull0 = raw + 8, pready0 = sfull0 + 16, odone0 = pready0 + 16, pair0 = odone0 + 16;
+  const uint32_t sfull0 = raw + 8, pready0 = sfull0 + 16, prest0 = pready0 + 16, odone0 = prest0 + 16, pair0 = odone0 + 16;
   const uint32_t drain0 = pair0 + 64, turn0 = drain0 + 16;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -90,6 +93,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
     for (int t = 0; t < 2; ++t) {
       mbar_init(sfull0 + 8 * t, 1);
       mbar_init(pready0 + 8 * t, 8);
+      mbar_init(prest0 + 8 * t, 8);
       mbar_init(odone0 + 8 * t, 1);
     }
     for (int t = 0; t < 8; ++t) mbar_init(pair0 + 8 * t, 2);
@@ -198,9 +202,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
       if (!guard.wait_warp(turn0 + 8 * t, turn)) break;
       turn ^= 1;
       tc_fence_after();
+      if (pv) {
+        const uint32_t v = vring + V.stage * C::kVTile;
+        if (elect_one()) product_ts<8, 2, 0, 2>(O, S, 64, v, kAttnBlock, A.v_cols, np > 0);
+        __syncwarp();
+        if (!guard.wait_warp(prest0 + 8 * t, np & 1)) break;
+        tc_fence_after();
+      }
       if (elect_one()) {
         if (pv) {
-          product_ts<8, 2>(O, S, 64, vring + V.stage * C::kVTile, kAttnBlock, A.v_cols, np > 0);
+          product_ts<8, 2, 2, 4>(O, S, 64, vring + V.stage * C::kVTile, kAttnBlock, A.v_cols, true);
           mma_commit_one(odone0 + 8 * t);
           mma_commit_one(vempty0 + 8 * V.stage);
         } else if (j > J0) {
@@ -306,13 +317,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
           p[c] = pack_bf16(x.x, x.y);
         }
         tmem_put16(S + 16 * h, p);
+        if (h == 0) {  // the product starts with this half
+          tmem_put_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pready0 + 8 * t);
+        }
       }
       const float2 both = f2_add(sum[0], sum[1]);
       l += both.x + both.y;
       tmem_put_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pready0 + 8 * t);
+      if (lane == 0) mbar_arrive(prest0 + 8 * t);
     }
     if (ok && n > 0) {
       float theirs = 0.f;
