@@ -248,12 +248,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
     int n = 0;
     float *const my_slot = halves + (half * 2 + t) * kAttnTile + row;
     const float *const their_slot = halves + ((half ^ 1) * 2 + t) * kAttnTile + row;
-    // This row's value of the other warp.  A slot is written again only after
-    // products that waited for both warps' P, and so for their reads.
-    auto exchange = [&](float v, int turn, float &other) {
+    // This row's value of the other warp, from share() to theirs().  A slot is written
+    // again only after products that waited for both warps' P, and so for their reads.
+    auto share = [&](float v) {
       *my_slot = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(pair);
+    };
+    auto theirs = [&](int turn, float &other) {
       if (!guard.wait_warp(pair, turn & 1)) return false;
       other = *their_slot;
       return true;
@@ -263,8 +265,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
       tc_fence_after();
       const bool masked = tk[t].masked(j);
       const int lo = keys.lo - j * kAttnTile - half * 64, hi = keys.hi - j * kAttnTile - half * 64;
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      const float2 c2 = make_float2(A.scale2, A.scale2);
+      float2 sum[2];
+      uint32_t p[16];
+      // P of 32 scores, and their sums
+      auto exponentials = [&](const uint32_t *r) {
+        const float at = m == -INFINITY ? 0.f : -m;
+        const float2 at2 = make_float2(at, at);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float2 x = f2_fma(make_float2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), c2, at2);
+          x.x = ex2(x.x), x.y = ex2(x.y);
+          sum[c & 1] = f2_add(sum[c & 1], x);
+          p[c] = pack_bf16(x.x, x.y);
+        }
+      };
+      auto half_of_row = [&](int h) {
+        uint32_t r[32];
+        tmem_read<32>(S + 32 * h, r);
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (32 * h + c < lo || 32 * h + c >= hi) r[c] = 0xff800000u;
+        }
+        exponentials(r);
+      };
+      sum[0] = sum[1] = make_float2(0.f, 0.f);
+      float mine, other;
       {
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         uint32_t r[64];
         tmem_read<64>(S, r);
         if (masked) {
@@ -276,10 +305,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
         for (int c = 0; c < 64; c += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(r[c + e]), __uint_as_float(r[c + e + 4]));
+        mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        share(mine);
+        // the first half beside the exchange, from the maximum so far: it mostly stays
+        exponentials(r);
       }
-      float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), theirs;
-      if (!(ok = exchange(mine, n, theirs))) break;
-      const float mn = fmaxf(m, fmaxf(mine, theirs) * A.scale2);
+      if (!(ok = theirs(n, other))) break;
+      const float mn = fmaxf(m, fmaxf(mine, other) * A.scale2);
       if (__any_sync(0xffffffffu, mn > m + kRescale)) {
         const float a = ex2(m - (mn == -INFINITY ? 0.f : mn));  // (m = -inf: 0)
         l *= a;
@@ -296,34 +328,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
             tmem_put(O + c, o);
           }
         }
+        sum[0] = sum[1] = make_float2(0.f, 0.f);
+        half_of_row(0);
       }
-      const float at = m == -INFINITY ? 0.f : -m;
-      const float2 c2 = make_float2(A.scale2, A.scale2), at2 = make_float2(at, at);
-      float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t r[32], p[16];
-        tmem_read<32>(S + 32 * h, r);
-        if (masked) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (32 * h + c < lo || 32 * h + c >= hi) r[c] = 0xff800000u;
-        }
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float2 x = f2_fma(make_float2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), c2, at2);
-          x.x = ex2(x.x), x.y = ex2(x.y);
-          sum[c & 1] = f2_add(sum[c & 1], x);
-          p[c] = pack_bf16(x.x, x.y);
-        }
-        tmem_put16(S + 16 * h, p);
-        if (h == 0) {  // the product starts with this half
-          tmem_put_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pready0 + 8 * t);
-        }
-      }
+      tmem_put16(S, p);
+      tmem_put_wait();  // (the product starts with this half)
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pready0 + 8 * t);
+      half_of_row(1);
+      tmem_put16(S + 16, p);
       const float2 both = f2_add(sum[0], sum[1]);
       l += both.x + both.y;
       tmem_put_wait();
@@ -332,9 +346,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
       if (lane == 0) mbar_arrive(prest0 + 8 * t);
     }
     if (ok && n > 0) {
-      float theirs = 0.f;
-      ok = guard.wait_warp(odone0 + 8 * t, (n - 1) & 1) && exchange(l, n, theirs);
-      l += theirs;
+      float other = 0.f;
+      ok = guard.wait_warp(odone0 + 8 * t, (n - 1) & 1);
+      share(l);
+      ok = ok && theirs(n, other);
+      l += other;
     }
     tc_fence_after();
     if (ok && t0 + t * tokens < P.mask.sq) {
