@@ -12,14 +12,16 @@
 // into TMEM in bf16 over S, O += P V (TMEM).  While the softmax of one row tile
 // runs, the tensor cores work for the other: PV0(j-1) S0(j) PV1(j-1) S1(j).  What
 // bounds that turn is the time from S to P, so P V starts with the first half of each
-// warp's P while the second is formed (2 x 8192 tokens: 380 -> 344 us).
+// warp's P while the second is formed (2 x 8192 tokens: 380 -> 344 us), and that
+// first half is formed from the maximum so far while the row's two warps exchange
+// theirs (344 -> 339), again where the maximum moves.
 // m is a running maximum that is moved, and O rescaled, only when a row's
 // maximum grows by more than 2^8: until then P is at most 2^8 and its rounding
 // is relative, so nothing is lost; sums are fp32.  P is rounded to bf16 once
 // (2^-8 of it at most, as the operand of the product); the sum takes it unrounded.
-// Measured, causal, 16 query and 4 key heads of 128: 2 x 8192 tokens 344 us, 1.60
-// PFLOP/s of the products that count (84% of a library product's rate); 512 new tokens
-// over a cache of 32768 (keys split, parts joined) 108 us, 1.27.  Bound: the turn of the two row
+// Measured, causal, 16 query and 4 key heads of 128: 2 x 8192 tokens 339 us, 1.62
+// PFLOP/s of the products that count (85% of a library product's rate); 512 new tokens
+// over a cache of 32768 (keys split, parts joined) 107 us, 1.28.  Bound: the turn of the two row
 // tiles, S to softmax to P V; the warps issue 39% of the time, mostly waiting for
 // products.  Short sequences (documents, 777 tokens) are bound by a CTA's start and
 // end, some 9000 clocks: 65 us at 2.4 to 3.7 TB/s.  A CTA that walks over several
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
     // over S, and one thread's products run in order.  Each tile has a warp of its
     // own, whose waits lie beside the other's products, and the two take turns: with
     // products of both at once the tiles fall in step, and the tensor cores rest while
-    // both wait for their softmax (474 us instead of 381 at 2 x 8192 tokens x 16 heads of 128).
+    // both wait for their softmax (474 us instead of 381 at 2 x 8192 tokens x 16 heads of 128, before P came in halves).
     const int t = warp - kFwdSoftWarps;
     const uint32_t S = tmem + t * 128, O = tmem + C::kO + t * kVb * 64, q = q0 + t * C::kQTile;
     bool started = false;
