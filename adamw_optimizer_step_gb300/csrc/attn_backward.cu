@@ -3,7 +3,7 @@
 //   dV = P^T dY,  dS = scale P (dY V^T - D),  dQ = dS K,  dK = dS^T Q.
 // P is formed again from the forward's lse: P = 2^(S c - lse log2(e)).
 //
-//   attn_delta_kernel     per row: -lse log2(e) and D
+//   attn_delta_kernel     per row: -lse log2(e) and D (from P and V for rows of few keys)
 //   attn_backward_kernel  attn_dkv: a CTA holds 128 keys and walks over the rows that see them;
 //                         attn_dq: a CTA holds 128 rows and walks over the keys that they see
 //
@@ -11,9 +11,9 @@
 // sum crosses CTAs: no atomics, results that repeat bit for bit, no fp32 dQ in
 // memory.  Every sum stays in TMEM for a CTA's whole walk, the query heads that
 // share a key head among them.  P and dS are rounded to bf16 once, as operands of
-// products (by 2^-8 of them at most); sums are fp32.  With D from the rounded y, that
-// makes dQ's and dK's error 2.5e-3 of them against 1.7e-3 of the outputs' rounding
-// alone; dS as two bf16 numbers would take two products more.
+// products (by 2^-8 of them at most); sums are fp32.  That makes dQ's and dK's error
+// 2.4e-3 of them against 1.7e-3 of the outputs' rounding alone (D from the rounded y adds
+// up to 0.1e-3); dS as two bf16 numbers would take two products more.
 //
 // Measured, causal, 2 x 8192 tokens, 16 query and 4 key heads of 128: 1110 us, the
 // keys' walk alone 670 (1.64 PFLOP/s of the four products it forms), the queries'
@@ -36,41 +36,139 @@ constexpr float kLog2ePlain = 1.4426950408889634f;
 // ---------------------------------------------------------------------------
 // -lse log2(e) and D of each row: 16 lanes to a row.  A row that sees nothing
 // (lse = -inf) gets -inf and 0, whatever stands in it: its P and dS are 0.  Bound by
-// HBM (dy and y once); 10 us for 4096 x 16 heads of 128, from HBM.
+// HBM (dy and y once).
+// D = dy . y takes over the rounding of y, an error that every dS of the row gets times
+// its P: beside dS's own rounding it counts 1 / sqrt(n) over n keys.  Rows that see 8
+// keys or fewer form D = sum p (dy . v) instead (dQ's and dK's error at 48 tokens 2.9e-3
+// -> 2.6e-3 of them, at a handful of tokens 4.4e-3 -> 2.8e-3; with one key dS is 0 and
+// not D's error).  They are looked for among the first 8 tokens of each sequence or
+// document (no later one of a causal sequence sees so few), or among all tokens where a
+// narrow window or few keys may leave any row so few, by the first CTAs, beside the
+// others' stream: 2 to 4 us where sequences are short (up to 16 keys: 5 to 15 us, and
+// 1% less error), nothing at 2 x 8192.  15 us for 6 x 777 x 32 rows of 128 elements.
+
+constexpr int kFewKeys = 8;     // (a power of two)
+constexpr int kDeltaRows = 32;  // of a CTA, two to each 16 lanes: their loads are under way together
 
 struct DeltaParams {
-  const __nv_bfloat16 *dy, *y;
+  const __nv_bfloat16 *dy, *y, *q, *k, *v;
   const float *lse;
   float2 *stats;
-  int64_t ds[3], ys[3], rows;
-  int32_t sq, heads, dv;
+  AttnMask mask;
+  int64_t ds[3], ys[3], qs[3], ks[3], vs[3], rows;
+  float scale2;
+  int32_t sq, heads, group, dk, dv;
+  FastDiv by_heads, by_sq;  // of row numbers that fit 32 bits
+  int32_t places, every;    // of rows of few keys: tokens looked at (of all heads); 1: every token
+  uint32_t few_ctas;
 };
 
-__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ DeltaParams P) {
+// Sum of the products of eight pairs of bf16.
+__device__ __forceinline__ float dot8(const uint4 &u, const uint4 &v, float d) {
+  const uint32_t a[4] = {u.x, u.y, u.z, u.w}, c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    d = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(c[e] << 16), d);
+    d = fmaf(__uint_as_float(a[e] & 0xffff0000u), __uint_as_float(c[e] & 0xffff0000u), d);
+  }
+  return d;
+}
+
+// The first CTAs: rows that see few keys, a warp to a row, a key to each half of it.
+__device__ __forceinline__ void few_keys_delta(const DeltaParams &P) {
+  const int half = threadIdx.x >> 4 & 1, lane = threadIdx.x & 15;
+  int at = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (at >= P.places * P.heads) return;
+  const int h = P.by_heads.split(at);
+  int b = 0, t;
+  if (P.every) {
+    t = P.by_sq.split(at), b = at;
+  } else {
+    const int unit = at / kFewKeys;
+    if (!P.mask.docs) b = unit;
+    t = (P.mask.docs ? clamp_to(P.mask.docs[unit], P.mask.sq) : attn_seq(P.mask, b).q_lo) + at % kFewKeys;
+  }
+  const AttnSeq seq = attn_seq(P.mask, b);
+  const Span keys = keys_of(P.mask, seq, doc_window(P.mask, t), t);
+  const int n = t >= seq.q_lo && t < seq.q_hi ? keys.hi - keys.lo : 0;
+  if (n <= 0 || n > kFewKeys) return;
+  const int64_t row = ((int64_t)b * P.sq + t) * P.heads + h, kh = h / P.group;
+  const __nv_bfloat16 *k = P.k + b * P.ks[0] + keys.lo * P.ks[1] + kh * P.ks[2] + lane * 8;
+  const __nv_bfloat16 *v = P.v + b * P.vs[0] + keys.lo * P.vs[1] + kh * P.vs[2] + lane * 8;
+  const __nv_bfloat16 *const q_row = P.q + b * P.qs[0] + t * P.qs[1] + h * P.qs[2] + lane * 8;
+  const bool k0 = lane * 8 < P.dk, k1 = lane * 8 + 128 < P.dk, v0 = lane * 8 < P.dv;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  const uint4 q = k0 ? *reinterpret_cast<const uint4 *>(q_row) : none, r = k1 ? *reinterpret_cast<const uint4 *>(q_row + 128) : none;
+  const uint4 g = v0 ? *reinterpret_cast<const uint4 *>(P.dy + b * P.ds[0] + t * P.ds[1] + h * P.ds[2] + lane * 8) : none;
+  const float lse2 = P.lse[row] * kLog2ePlain;
+  float sum = 0.f;
+#pragma unroll 2
+  for (int i0 = 0; i0 < n; i0 += 2) {
+    const int i = i0 + half;
+    float s = 0.f, dp = 0.f;
+    if (i < n) {
+      if (k0) s = dot8(q, *reinterpret_cast<const uint4 *>(k + i * P.ks[1]), s);
+      if (k1) s = dot8(r, *reinterpret_cast<const uint4 *>(k + i * P.ks[1] + 128), s);
+      if (v0) dp = dot8(g, *reinterpret_cast<const uint4 *>(v + i * P.vs[1]), dp);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      dp += __shfl_xor_sync(0xffffffffu, dp, o);
+    }
+    if (i < n) sum = fmaf(ex2(fmaf(s, P.scale2, -lse2)), dp, sum);
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+  if ((threadIdx.x & 31) == 0) P.stats[row] = lse2 == -INFINITY ? make_float2(-INFINITY, 0.f) : make_float2(-lse2, sum);
+}
+
+__global__ void __launch_bounds__(256, 5) attn_delta_kernel(const __grid_constant__ DeltaParams P) {
   pdl_launch();
   pdl_wait();
-  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (blockIdx.x < P.few_ctas) {
+    few_keys_delta(P);
+    return;
+  }
+  const int64_t row0 = (int64_t)(blockIdx.x - P.few_ctas) * kDeltaRows + (threadIdx.x >> 4);
   const int lane = threadIdx.x & 15;
-  const bool in = row < P.rows;
-  float d = 0.f, lse = -INFINITY;
-  if (in) {
-    lse = P.lse[row];
-    const int64_t bt = row / P.heads, b = bt / P.sq;
-    const int64_t h = row - bt * P.heads, t = bt - b * P.sq;
-    if (lane * 8 < P.dv) {
-      const uint4 u = *reinterpret_cast<const uint4 *>(P.dy + b * P.ds[0] + t * P.ds[1] + h * P.ds[2] + lane * 8);
-      const uint4 v = *reinterpret_cast<const uint4 *>(P.y + b * P.ys[0] + t * P.ys[1] + h * P.ys[2] + lane * 8);
-      const uint32_t a[4] = {u.x, u.y, u.z, u.w}, c[4] = {v.x, v.y, v.z, v.w};
+  constexpr int kEach = kDeltaRows / 16;
+  int b[kEach], t[kEach];
+  float lse[kEach];
+  uint4 g[kEach], y[kEach];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        d = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(c[e] << 16), d);
-        d = fmaf(__uint_as_float(a[e] & 0xffff0000u), __uint_as_float(c[e] & 0xffff0000u), d);
-      }
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t row = row0 + 16 * i;
+    const bool in = row < P.rows;
+    int h = 0;
+    b[i] = t[i] = 0;
+    if (P.rows <= INT32_MAX) {
+      int at = in ? (int)row : 0;
+      h = P.by_heads.split(at), t[i] = P.by_sq.split(at), b[i] = at;
+    } else if (in) {
+      const int64_t bt = row / P.heads;
+      b[i] = (int)(bt / P.sq), h = (int)(row - bt * P.heads), t[i] = (int)(bt - (int64_t)b[i] * P.sq);
+    }
+    lse[i] = in ? P.lse[row] : -INFINITY;
+    g[i] = y[i] = make_uint4(0, 0, 0, 0);
+    if (in && lane * 8 < P.dv) {
+      g[i] = *reinterpret_cast<const uint4 *>(P.dy + b[i] * P.ds[0] + t[i] * P.ds[1] + h * P.ds[2] + lane * 8);
+      y[i] = *reinterpret_cast<const uint4 *>(P.y + b[i] * P.ys[0] + t[i] * P.ys[1] + h * P.ys[2] + lane * 8);
     }
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if (in && lane == 0) P.stats[row] = lse == -INFINITY ? make_float2(-INFINITY, 0.f) : make_float2(-lse * kLog2ePlain, d);
+  for (int i = 0; i < kEach; ++i) {
+    bool few = false;
+    if (P.few_ctas) {
+      const AttnSeq seq = attn_seq(P.mask, b[i]);
+      const Span keys = keys_of(P.mask, seq, doc_window(P.mask, __shfl_sync(0xffffffffu, t[i], 0)), t[i]);
+      few = t[i] >= seq.q_lo && t[i] < seq.q_hi && keys.hi > keys.lo && keys.hi - keys.lo <= kFewKeys;
+    }
+    float d = dot8(g[i], y[i], 0.f);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (row0 + 16 * i < P.rows && !few && lane == 0)
+      P.stats[row0 + 16 * i] = lse[i] == -INFINITY ? make_float2(-INFINITY, 0.f) : make_float2(-lse[i] * kLog2ePlain, d);
+  }
 }
 
 struct BwdParams {
@@ -718,8 +816,21 @@ extern "C" int gbo_attn_backward(const gbo_attn_args *a, const gbo_attn_grads *g
     D.dy = static_cast<const __nv_bfloat16 *>(g->dy), D.y = static_cast<const __nv_bfloat16 *>(g->y);
     D.lse = g->lse, D.stats = static_cast<float2 *>(workspace);
     const int64_t extent[3] = {a->batch, a->sq, a->q_heads};
-    for (int i = 0; i < 3; ++i) D.ds[i] = extent[i] > 1 ? g->dy_stride[i] : 0, D.ys[i] = extent[i] > 1 ? g->y_stride[i] : 0;
-    D.rows = rows, D.sq = (int32_t)a->sq, D.heads = a->q_heads, D.dv = a->dv;
+    const int64_t k_extent[3] = {a->batch, a->sk, a->k_heads};
+    for (int i = 0; i < 3; ++i) {
+      D.ds[i] = extent[i] > 1 ? g->dy_stride[i] : 0, D.ys[i] = extent[i] > 1 ? g->y_stride[i] : 0;
+      D.qs[i] = extent[i] > 1 ? a->q_stride[i] : 0;
+      D.ks[i] = k_extent[i] > 1 ? a->k_stride[i] : 0, D.vs[i] = k_extent[i] > 1 ? a->v_stride[i] : 0;
+    }
+    D.q = static_cast<const __nv_bfloat16 *>(a->q), D.k = static_cast<const __nv_bfloat16 *>(a->k);
+    D.v = static_cast<const __nv_bfloat16 *>(a->v);
+    D.rows = rows, D.sq = (int32_t)a->sq, D.heads = a->q_heads, D.dk = a->dk, D.dv = a->dv;
+    D.by_heads = fast_div(a->q_heads), D.by_sq = fast_div(a->sq);
+    D.mask = M, D.scale2 = S.scale2, D.group = S.group;
+    D.every = a->sk <= kFewKeys || (a->window > 0 && a->window <= kFewKeys) || (!a->causal && a->k_lengths);
+    int64_t few = D.every ? a->batch * a->sq : a->documents ? (int64_t)a->n_documents * kFewKeys : a->causal ? a->batch * kFewKeys : 0;
+    if (few * a->q_heads > INT32_MAX) few = 0;  // (D = dy . y throughout)
+    D.places = (int32_t)few, D.few_ctas = (uint32_t)((few * a->q_heads + 7) / 8);
     maps = heads_map(&P.k, a->k, a->dk, a->k_heads, a->sk, a->batch, a->k_stride, 1, kAttnTile) &&
            heads_map(&P.v, a->v, a->dv, a->k_heads, a->sk, a->batch, a->v_stride, 1, kAttnTile) &&
            heads_map(&P.q, a->q, a->dk, a->q_heads, a->sq, a->batch, a->q_stride, heads, qt >> S.pack) &&
@@ -737,7 +848,7 @@ extern "C" int gbo_attn_backward(const gbo_attn_args *a, const gbo_attn_grads *g
   Q.tiles = (int32_t)q_tiles;
   if (queries && keys && (dkv_grid || dq_grid)) {
     count_launches(1);
-    e = launch_kernel_as(pdl_allowed(), attn_delta_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, st, 1, D);
+    e = launch_kernel_as(pdl_allowed(), attn_delta_kernel, dim3((unsigned)((rows + kDeltaRows - 1) / kDeltaRows + D.few_ctas)), dim3(256), 0, st, 1, D);
   }
   both.key_tiles = (int32_t)dkv_grid;
   const int64_t grid = dkv_grid + dq_grid;

@@ -492,3 +492,40 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     for call in (lambda: layers.attention(q, k, v), lambda: layers.attention_backward(y, q, k, v, y, lse)):
         with pytest.raises(ValueError, match="on the current device"):
             call()
+
+
+@pytest.mark.parametrize("dims", [(8, 8, 4, 4), (16, 8, 2, 1), (24, 16, 6, 2)])
+@pytest.mark.parametrize("window", [1, 0])
+def test_rows_of_one_key_take_no_error_from_the_rounded_output(dims, window):
+    """A query that sees one key: P is 1, dS = P (dy . v - D) is 0.  Sums of dk and dv products are off by at most
+    2^-23 a product of |q| |k| and |dy| |v| (truncated sums), P by as much of the exponent s = scale log2(e) q . k and
+    16 more steps, so |dS| <= 2^-23 (dk + dv + 16) (1 + |s|) |dy| |v|.  D from y in bf16 would be off by some
+    2^-10 |dy| |v| / sqrt(dv)."""
+    dk, dv, hq, hk = dims
+    q, k, v, dy = inputs(3, 200, 200, hq, hk, dk, dv, seed=dk)
+    y, lse = layers.attention(q, k, v, return_lse=True, window=window)
+    dq, dk_, _ = layers.attention_backward(dy, q, k, v, y, lse, window=window)
+    rows = 200 if window else 1  # without a window the first query alone sees one key
+    norm = lambda t: t.double().norm(dim=-1)  # noqa: E731
+    shared = lambda t: norm(t).repeat_interleave(hq // hk, 2)  # noqa: E731
+    ds = 2.0 ** -23 * (dk + dv + 16) * (1 + 1.4427 * dk ** -0.5 * norm(q) * shared(k)) * norm(dy) * shared(v) * dk ** -0.5
+    assert (norm(dq)[:, :rows] <= (1 + 2.0 ** -8) * (ds * shared(k))[:, :rows]).all()
+    if window:
+        tol = (ds * norm(q)).view(3, 200, hk, hq // hk).sum(-1)
+        assert (norm(dk_) <= (1 + 2.0 ** -7) * tol).all()
+
+
+@pytest.mark.parametrize("shape", [(2, 16, 16), (1, 40, 17), (3, 5, 300), (2, 33, 33)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_on_either_side_of_few_keys(shape, causal):
+    """Rows that see a handful of keys, and more, of ragged sequences and documents, in heads of every kind."""
+    b, sq, sk = shape
+    for dk, dv, hq, hk in ((64, 64, 4, 2), (192, 128, 3, 3), (136, 72, 6, 1)):
+        q, k, v, dy = inputs(b, sq, sk, hq, hk, dk, dv, seed=sq)
+        lengths = dict(q_lengths=ints(*[max(0, sq - 7 * i) for i in range(b)]), k_lengths=ints(*[max(1, sk - 9 * i) for i in range(b)]))
+        check(q, k, v, dy, causal=causal, **lengths)
+        if b == 1:
+            continue
+        check(q, k, v, dy, causal=True, window=11)
+    q, k, v, dy = inputs(1, 90, 90, 4, 2, 64, 64, seed=3)
+    check(q, k, v, dy, causal=causal, documents=ints(2, 3, 3, 19, 36, 80))
