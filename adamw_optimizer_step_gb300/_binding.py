@@ -788,6 +788,8 @@ def attn_args(q, k, v, *, causal=True, window=0, scale=None, q_lengths=None, k_l
     _here(q, k, v, q_lengths, k_lengths, documents)
     docs = _attn_index(documents, None, "documents")
     n_docs = documents.shape[0] - 1 if documents is not None else 0
+    if documents is not None and n_docs < 1:
+        raise ValueError("documents must be the first tokens of one document or more, and the end of the last")
     return _PACK_ATTN_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), _attn_index(q_lengths, batch, "q_lengths"),
                            _attn_index(k_lengths, batch, "k_lengths"), docs, batch, sq, sk, *qs, *ks, *vs, int(window),
                            hq, hk, dk, dv, n_docs, 1 if causal else 0, GBO_BF16,

@@ -608,7 +608,7 @@ int check_heads(const void *p, const int64_t stride[3], int64_t batch, int64_t t
   return GBO_OK;
 }
 
-// (no pointer is looked at: sizes are asked for before memory is there)
+// (no pointer is followed: sizes are asked for before memory is there)
 int check_attn_sizes(const gbo_attn_args *a) {
   if (!a) return attn_fail(GBO_ERR_INVALID_ARG, "args is NULL");
   if (a->dtype != GBO_BF16) return attn_fail(GBO_ERR_DTYPE, "queries, keys and values must be GBO_BF16");
@@ -623,6 +623,13 @@ int check_attn_sizes(const gbo_attn_args *a) {
   if (a->causal != 0 && a->causal != 1) return attn_fail(GBO_ERR_INVALID_ARG, "causal must be 0 or 1");
   if (a->window < 0 || (a->window > 0 && !a->causal))
     return attn_fail(GBO_ERR_INVALID_ARG, "window must be >= 0, and needs causal = 1");
+  if (a->documents) {
+    if (a->n_documents < 1) return attn_fail(GBO_ERR_INVALID_ARG, "documents without a number of documents");
+    if (a->batch > 1 || a->sq != a->sk || a->q_lengths || a->k_lengths)
+      return attn_fail(GBO_ERR_INVALID_ARG, "documents need one row of as many queries as keys, without lengths");
+  } else if (a->n_documents != 0) {
+    return attn_fail(GBO_ERR_INVALID_ARG, "n_documents without documents");
+  }
   return GBO_OK;
 }
 
@@ -632,13 +639,6 @@ int check_attn(const gbo_attn_args *a) {
   if ((reinterpret_cast<uintptr_t>(a->q_lengths) | reinterpret_cast<uintptr_t>(a->k_lengths) |
        reinterpret_cast<uintptr_t>(a->documents)) & 3)
     return attn_fail(GBO_ERR_INVALID_ARG, "misaligned lengths or documents");
-  if (a->documents) {
-    if (a->n_documents < 1) return attn_fail(GBO_ERR_INVALID_ARG, "documents without a number of documents");
-    if (a->batch > 1 || a->sq != a->sk || a->q_lengths || a->k_lengths)
-      return attn_fail(GBO_ERR_INVALID_ARG, "documents need one row of as many queries as keys, without lengths");
-  } else if (a->n_documents != 0) {
-    return attn_fail(GBO_ERR_INVALID_ARG, "n_documents without documents");
-  }
   if (a->batch == 0 || a->sq == 0) return GBO_OK;
   rc = check_heads(a->q, a->q_stride, a->batch, a->sq, a->q_heads);
   if (rc == GBO_OK && a->sk > 0) rc = check_heads(a->k, a->k_stride, a->batch, a->sk, a->k_heads);

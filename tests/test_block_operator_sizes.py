@@ -1,0 +1,65 @@
+"""Host-side sizes and checks of attention, the residual update and dropout where there
+is nothing, or little, to work on.  No GPU needed: nothing is launched, and the fake
+addresses are never dereferenced."""
+
+import ctypes
+
+import pytest
+import torch
+
+from adamw_optimizer_step_gb300 import _binding as B
+from adamw_optimizer_step_gb300 import build as build_mod
+
+FAKE = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def L():
+    build_mod.build()
+    return B.lib()
+
+
+def attn_args(**kw):
+    a = B.AttnArgs()
+    o = dict(q=FAKE, k=2 * FAKE, v=3 * FAKE, batch=1, sq=64, sk=64, q_heads=4, k_heads=2, dk=64, dv=64, causal=1,
+             dtype=B.GBO_BF16, scale=0.125)
+    o.update(kw)
+    for k, v in o.items():
+        setattr(a, k, v)
+    a.q_stride[:], a.k_stride[:], a.v_stride[:] = (64 * 256, 256, 64), (64 * 128, 128, 64), (64 * 128, 128, 64)
+    return a
+
+
+@pytest.mark.parametrize("args", [dict(documents=FAKE), dict(documents=FAKE, n_documents=-1), dict(n_documents=2),
+                                  dict(documents=FAKE, n_documents=3, batch=2), dict(documents=FAKE, n_documents=3, sk=65),
+                                  dict(documents=FAKE, n_documents=3, k_lengths=FAKE)], ids=str)
+def test_attention_sizes_refuse_what_the_calls_refuse(L, args):
+    """Documents without a number of them among others: keys are divided among the documents
+    to see how a call is cut, so this has to be refused before."""
+    a = attn_args(**args)
+    for size in (L.gbo_attn_forward_workspace_bytes, L.gbo_attn_backward_workspace_bytes):
+        assert size(ctypes.byref(a)) == 0 and b"documents" in L.gbo_last_error()
+    assert L.gbo_attn_forward(ctypes.byref(a), 4 * FAKE, a.q_stride, None, None, 0, None, None) == -1
+
+
+def test_documents_are_two_values_or_more(monkeypatch):
+    """One value is the end of no document."""
+    class Here:
+        """Stands for a CUDA tensor: what the binding asks of one before it packs."""
+
+        def __init__(self, *shape, dtype=torch.bfloat16):
+            self.t = torch.zeros(*shape, dtype=dtype)
+            self.is_cuda = True
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
+            return 0
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    q = Here(1, 5, 2, 8)
+    for count in (0, 1):
+        with pytest.raises(ValueError, match="documents must be"):
+            B.attn_args(q, q, q, documents=Here(count, dtype=torch.int32))
+    assert len(B.attn_args(q, q, q, documents=Here(2, dtype=torch.int32))) == ctypes.sizeof(B.AttnArgs)
