@@ -591,10 +591,12 @@ constexpr int kSmemMost = 220 * 1024;  // of an SM's shared memory, for rings an
 // as much then); 512 threads an SM.  Gradients of single elements, two chunks a thread,
 // spill (8194 x 8190: 1303 us, the wide form 651): those rows take the wide form, shorter
 // ones the ring (65600 x 1023: 752 us, wide 2544).
-// `row_bytes`: of a row's inputs, in their places.
+// `row_bytes`: of a row's inputs, in their places (0 where there are no rows: their
+// pointers may be NULL).
 ResCut cut_of(int64_t n, int64_t d, int sm, bool back, bool vec, int64_t row_bytes) {
   ResCut c;
   memset(&c, 0, sizeof c);
+  row_bytes = std::max<int64_t>(row_bytes, 16);
   const int64_t chunks = (d + 7) / 8;
   auto blocks = [&](int per_sm, int64_t rows) {
     c.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm * per_sm, (n + rows - 1) / rows));

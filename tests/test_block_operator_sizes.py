@@ -3,6 +3,7 @@ is nothing, or little, to work on.  No GPU needed: nothing is launched, and the 
 addresses are never dereferenced."""
 
 import ctypes
+import subprocess
 
 import pytest
 import torch
@@ -63,3 +64,49 @@ def test_documents_are_two_values_or_more(monkeypatch):
         with pytest.raises(ValueError, match="documents must be"):
             B.attn_args(q, q, q, documents=Here(count, dtype=torch.int32))
     assert len(B.attn_args(q, q, q, documents=Here(2, dtype=torch.int32))) == ctypes.sizeof(B.AttnArgs)
+
+
+# how the residual kernels are cut, by a small host program over their header
+CUTS = r"""
+#include "residual.cuh"
+
+namespace gbo {
+int report_error(int code, const char *) { return code; }
+int report_ok() { return 0; }
+int require_device(int *, int *) { return -1; }
+int32_t pdl_allowed() { return 0; }
+void count_launches(uint64_t) {}
+}  // namespace gbo
+
+int main() {
+  using namespace gbo;
+  for (int64_t d : {1, 64, 504, 505, 1024, 1031, 4104, 8192, 8199, 16384})
+    for (bool back : {false, true})
+      for (bool vec : {false, true}) {
+        if (vec && d % 8) continue;
+        // no rows: no tensors either
+        const ResCut c = cut_of(0, d, 152, back, vec, 0);
+        if (c.blocks != 1 || c.threads < 32 || c.smem < 0 || c.smem > kSmemMost) return 1;
+        if (c.form == kFormRing && (c.stages < 1 || c.stages > kMaxStages)) return 2;
+        if (parts_of(c) > most_parts(0, d, 152)) return 3;
+        // one row and many, of inputs of any size
+        for (int64_t n : {int64_t(1), int64_t(37), int64_t(1) << 40})
+          for (int64_t bytes : {16, 1024, 16384, 65536, 163840}) {
+            const ResCut r = cut_of(n, d, 152, back, vec, bytes);
+            if (r.blocks < 1 || r.blocks > n || r.smem > kSmemMost) return 4;
+            if (back && parts_of(r) > most_parts(n, d, 152)) return 5;
+            if (r.form == kFormRing && (r.stages < 2 || r.stages > kMaxStages)) return 6;
+          }
+      }
+  return 0;
+}
+"""
+
+
+def test_cuts_of_no_rows_and_of_many(tmp_path):
+    """A ring's stages are what fits divided by a row's bytes, which are none where there is no row."""
+    src, exe = tmp_path / "cuts.cu", tmp_path / "cuts"
+    src.write_text(CUTS)
+    subprocess.run([build_mod.nvcc(), *build_mod.ARCH, "-std=c++17", "-O1", "--expt-relaxed-constexpr", "-I", build_mod.INCLUDE,
+                    "-I", build_mod.CSRC, str(src), "-o", str(exe)], check=True, capture_output=True)
+    assert subprocess.run([str(exe)], timeout=60).returncode == 0

@@ -1,0 +1,30 @@
+"""Attention, the residual update and dropout at the edges of what their arguments allow:
+no rows.  Values are compared as in
+tests/test_gpu_residual.py, whose tolerances hold here."""
+
+import pytest
+import torch
+
+from adamw_optimizer_step_gb300 import _binding as B
+from adamw_optimizer_step_gb300 import layers
+from tests.test_gpu_residual import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from adamw_optimizer_step_gb300 import build
+    build.build()
+    B.lib()
+
+
+@pytest.mark.parametrize("d", [64, 505, 1024, 8192, 8200])
+@pytest.mark.parametrize("scale", [None, "one", "vector"])
+def test_gradients_of_no_rows(d, scale):
+    """Tensors of no rows, without a norm behind the update: sums of nothing are 0."""
+    c = Case(0, d, pre=False, gate="element", scale=scale)
+    x, h = layers.residual_norm(c.x, c.block, **c.kw())
+    g = layers.residual_norm_backward(c.dx_out, None, x, c.block, **c.kw())
+    assert h is None and x.shape == g["dx"].shape == g["dblock"].shape == g["dgate"].shape == (0, d)
+    assert not g["dpost_gain"].any() and (scale is None or not g["dscale"].any())
