@@ -65,7 +65,9 @@ __global__ void __launch_bounds__(kGroupThreads, 4) residual_backward_kernel(con
       }
     }
     if (P.pre || P.post) group_sum(sum, group, in_group, red[g], turn, 1 + g);
-    const float ro = P.post ? rsqrtf(fmaf(sum[2], P.inv_d, P.eps)) : 1.f;
+    // (a row that is not there has sums of 0, and with eps = 0 a norm's factor of it would
+    // be infinite: 0 times that, NaN, would stand in the sums over rows)
+    const float ro = P.post ? dr ? rsqrtf(fmaf(sum[2], P.inv_d, P.eps)) : 0.f : 1.f;
     float dx[N];
     if (P.dxo) {
       load_part<XT, kVec>(in.dxo, dr, 0, in_group, group, dx);
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kGroupThreads, 4) residual_backward_kernel(con
       float x[N], w[N];
       load_part<XT, kVec>(in.x, dr, 0, in_group, group, x);
       load_part<BT, kVec>(in.dh, dr, 0, in_group, group, w);
-      const float r = rsqrtf(fmaf(sum[0], P.inv_d, P.eps)), c = sum[1] * P.inv_d * r * r;
+      const float r = dr ? rsqrtf(fmaf(sum[0], P.inv_d, P.eps)) : 0.f, c = sum[1] * P.inv_d * r * r;
 #pragma unroll
       for (int e = 0; e < N; ++e) a_pre[e] = fmaf(w[e], x[e] * r, a_pre[e]);
       times_table<kVec>(P.pre_gain, d, 0, in_group, group, w);

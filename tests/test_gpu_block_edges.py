@@ -1,5 +1,5 @@
 """Attention, the residual update and dropout at the edges of what their arguments allow:
-no rows.  Values are compared as in
+no rows, an eps of zero.  Values are compared as in
 tests/test_gpu_residual.py, whose tolerances hold here."""
 
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 from adamw_optimizer_step_gb300 import _binding as B
 from adamw_optimizer_step_gb300 import layers
-from tests.test_gpu_residual import Case
+from tests.test_gpu_residual import BF16, F32, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +28,13 @@ def test_gradients_of_no_rows(d, scale):
     g = layers.residual_norm_backward(c.dx_out, None, x, c.block, **c.kw())
     assert h is None and x.shape == g["dx"].shape == g["dblock"].shape == g["dgate"].shape == (0, d)
     assert not g["dpost_gain"].any() and (scale is None or not g["dscale"].any())
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (F32, BF16), (F32, F32)], ids=lambda t: "-".join(str(x)[6:] for x in t))
+@pytest.mark.parametrize("n", [1, 3, 37])
+@pytest.mark.parametrize("d", [5, 64, 128, 200, 2048, 8200])
+def test_eps_of_zero(d, n, types):
+    """Rows of numbers that are not 0 have a norm without an eps; the rows that a warp of
+    several does not have (32 / threads of them, widths up to 128) reach no sum."""
+    for gate in (None, "row", "element"):
+        Case(n, d, *types, gate=gate, eps=0.0, seed=d + n).check()
