@@ -216,6 +216,8 @@ def lib():
         "gbo_dropout": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64, c_int32, ctypes.c_double,
                                   ctypes.c_uint64, ctypes.c_uint64, c_void_p, c_void_p]),
         "gbo_testing_wait_timeout": (c_int32, [c_void_p, ctypes.c_uint32, c_void_p]),
+        "gbo_testing_ring_give_up": (c_int32, [c_void_p, c_int32, c_int32, c_void_p, c_void_p, ctypes.c_uint32,
+                                               c_void_p]),
         "gbo_testing_set_small_chain": (c_int32, [c_int32]),
         "gbo_testing_set_fused_gram": (c_int32, [c_int32]),
         "gbo_testing_set_fused_momentum": (c_int32, [c_int32]),
@@ -1020,6 +1022,16 @@ def gbo_testing_set_pdl(mode):
 def gbo_testing_wait_timeout(dev_status, limit_us, stream=None):
     """Test hook: the GEMM's bounded wait on a barrier nothing arrives on."""
     _check(lib().gbo_testing_wait_timeout(_dev_ptr(dev_status, "dev_status"), int(limit_us), _stream(stream)))
+
+
+def gbo_testing_ring_give_up(rows, lost, found, dev_status, limit_us, stream=None):
+    """Test hook: ``rows`` (n, 256 int32) through the residual kernels' ring, the copy of row
+    ``lost`` never started; ``found``: n + 2 int32."""
+    n = rows.shape[0]
+    if rows.dtype != torch.int32 or rows.shape != (n, 256) or found.dtype != torch.int32 or found.shape != (n + 2,):
+        raise ValueError("rows must be (n, 256) int32, found n + 2 int32 values")
+    _check(lib().gbo_testing_ring_give_up(_dev_ptr(rows, "rows"), n, int(lost), _dev_ptr(found, "found"),
+                                          _dev_ptr(dev_status, "dev_status"), int(limit_us), _stream(stream)))
 
 
 def gbo_launch_count():

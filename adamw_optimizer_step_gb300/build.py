@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(LIB_DIR, "libgbo.so")
 
 SOURCES = ["plan.cpp", "muon_elementwise.cu", "ns_gemm_tc.cu", "ns_gemm_tf32.cu", "adamw.cu",
            "clip_noalloc.cu", "ns_chain_tc.cu", "h2d.cu", "rotary.cu", "xent_tc.cu",
-           "attn_forward.cu", "attn_backward.cu", "residual_forward.cu", "residual_backward.cu"]
+           "attn_forward.cu", "attn_backward.cu", "residual_forward.cu", "residual_backward.cu",
+           "testing_waits.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
           "--expt-relaxed-constexpr"]

@@ -253,10 +253,12 @@ enum { kInX = 0, kInBlock = 1, kInGate = 2, kInDxo = 3, kInDh = 4, kInputs = 5 }
 struct RowRing {
   uint32_t base, full0, stage_bytes;
   int stages;
-  volatile int32_t *late;
+  volatile int32_t *late;  // some thread's wait has run out
   int32_t *status;
+  uint64_t limit = kWaitNs;
   int stage = 0, to_fill = 0;
   uint32_t phase = 0;
+  bool gave_up = false;  // this thread took a row that had not arrived
 
   static __device__ __forceinline__ void copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
@@ -265,16 +267,26 @@ struct RowRing {
   }
   // All threads: the stage of the next row has arrived.  A wait that runs out is
   // flagged, and every later one passes at once: the outputs are invalid.
-  __device__ __forceinline__ uint32_t take() const {
+  __device__ __forceinline__ uint32_t take() {
     const uint32_t bar = full0 + 8 * stage;
-    if (!mbar_try(bar, phase) && !*late && !mbar_wait(bar, phase)) {
-      *late = 1;
-      flag_status(status, GBO_STATUS_TIMEOUT);
+    if (!mbar_try(bar, phase) && (*late || !mbar_wait_ns(bar, phase, limit))) {
+      gave_up = true;
+      if (!*late) {
+        *late = 1;
+        flag_status(status, GBO_STATUS_TIMEOUT);
+      }
     }
     return base + (uint32_t)stage * stage_bytes;
   }
   __device__ __forceinline__ void next() {
     if (++stage == stages) stage = 0, phase ^= 1;
+  }
+  // Thread 0, at the end, where it gave up (else it has waited for every row that it
+  // asked for): the copies under way, of `filled` that were started, land (or run out of
+  // time, too) before shared memory goes away.
+  __device__ __forceinline__ void settle(int64_t filled) const {
+    for (int64_t k = max((int64_t)0, filled - stages); k < filled; ++k)
+      (void)mbar_wait_ns(full0 + 8 * (uint32_t)(k % stages), (uint32_t)(k / stages) & 1, limit);
   }
 };
 
@@ -296,8 +308,10 @@ struct RowFeed {
     for (uint32_t b = 0; b < bytes; b += 2)
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + b), "h"(*reinterpret_cast<const uint16_t *>(p + b)) : "memory");
   }
+  // Nothing more where this thread gave up: the stage's barrier and place may still be a
+  // copy's.  (Where others alone did, the rows that this one has taken have landed.)
   __device__ __forceinline__ void fill(RowRing &r) {
-    if (row >= n) return;
+    if (row >= n || r.gave_up) return;
     const uint32_t bar = r.full0 + 8 * r.to_fill;
     uint32_t dst = r.base + (uint32_t)r.to_fill * r.stage_bytes;
     if constexpr (kOdd) {

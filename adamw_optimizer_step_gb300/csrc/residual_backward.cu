@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_backward_ring_kernel(const
     sums = make_float4(0.f, 0.f, 0.f, j0.x + j0.y);
     if (row + step < P.n) first_sums(at = ring.take(), row + step, sums);
   }
+  if (tid == 0 && ring.gave_up) ring.settle((feed.row - row0) / step);
   const int64_t rows = (int64_t)gridDim.x * P.d;
 #pragma unroll
   for (int it = 0; it < kIter; ++it) {

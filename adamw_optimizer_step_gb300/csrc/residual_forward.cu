@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kMaxGroup) residual_forward_ring_kernel(const 
     }
     ring.next();
   }
+  if (tid == 0 && ring.gave_up) ring.settle((feed.row - row0) / step);
 }
 
 // ---------------------------------------------------------------------------

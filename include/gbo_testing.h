@@ -24,6 +24,22 @@ extern "C" {
 int gbo_testing_wait_timeout(int32_t *dev_status, uint32_t limit_us, gbo_stream_t stream);
 
 /*
+ * Launch one CTA that takes `n` rows of 1024 bytes (1..64; device, 16-byte
+ * aligned) through the ring of gbo_residual_*'s kernels, three stages, with a
+ * limit of `limit_us` microseconds a wait instead of 2 s.  The copy of row
+ * `lost` (-1: of none) is asked for and never starts.  The wait for it gives up
+ * and ORs GBO_STATUS_TIMEOUT into *dev_status, no further copy is started, and
+ * those under way land before the CTA ends.
+ *   found  device int32, n + 2: of each row its first int32, or -1 where a wait
+ *          had run out; the number of rows asked for; a bit for each stage whose
+ *          last copy had landed at the end
+ * Asynchronous on `stream`.
+ * Errors: INVALID_ARG (limit outside 1..10^6 us among others), UNSUPPORTED, CUDA.
+ */
+int gbo_testing_ring_give_up(const void *rows, int32_t n, int32_t lost, int32_t *found, int32_t *dev_status,
+                             uint32_t limit_us, gbo_stream_t stream);
+
+/*
  * Whether Muon plans created from now on (any thread) run the Gram route's
  * p x p iterations of matrices with p <= 192 in bf16 mode as one on-chip
  * chain launch (enable != 0, the default) or as one tensor-core launch per
