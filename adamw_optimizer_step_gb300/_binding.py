@@ -216,6 +216,7 @@ def lib():
         "gbo_dropout": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64, c_int32, ctypes.c_double,
                                   ctypes.c_uint64, ctypes.c_uint64, c_void_p, c_void_p]),
         "gbo_testing_wait_timeout": (c_int32, [c_void_p, ctypes.c_uint32, c_void_p]),
+        "gbo_testing_attn_give_up": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, ctypes.c_uint32, c_void_p]),
         "gbo_testing_ring_give_up": (c_int32, [c_void_p, c_int32, c_int32, c_void_p, c_void_p, ctypes.c_uint32,
                                                c_void_p]),
         "gbo_testing_set_small_chain": (c_int32, [c_int32]),
@@ -1031,6 +1032,15 @@ def gbo_testing_ring_give_up(rows, lost, found, dev_status, limit_us, stream=Non
     if rows.dtype != torch.int32 or rows.shape != (n, 256) or found.dtype != torch.int32 or found.shape != (n + 2,):
         raise ValueError("rows must be (n, 256) int32, found n + 2 int32 values")
     _check(lib().gbo_testing_ring_give_up(_dev_ptr(rows, "rows"), n, int(lost), _dev_ptr(found, "found"),
+                                          _dev_ptr(dev_status, "dev_status"), int(limit_us), _stream(stream)))
+
+
+def gbo_testing_attn_give_up(tokens, first, found, dev_status, limit_us, stream=None):
+    """Test hook: the attention kernels' waits on what never comes, that of warp ``first`` with
+    the short limit.  ``tokens``: (64, 64) bfloat16; ``found``: 10 int32."""
+    if tokens.dtype != torch.bfloat16 or tokens.shape != (64, 64) or found.dtype != torch.int32 or found.shape != (10,):
+        raise ValueError("tokens must be (64, 64) bfloat16, found 10 int32 values")
+    _check(lib().gbo_testing_attn_give_up(_dev_ptr(tokens, "tokens"), int(first), _dev_ptr(found, "found"),
                                           _dev_ptr(dev_status, "dev_status"), int(limit_us), _stream(stream)))
 
 

@@ -201,7 +201,7 @@ struct Dkv {
   static constexpr int kUsed = kStatAt + kStats * kQt * 8;
   // kv, q full/empty, dy full/empty, stats full/empty, S, P, dP, dS, drained (two), raw, turns (two)
   static constexpr int kBars = 1 + 2 * kQStages + 2 * kDStages + 2 * kStats + 4 + 2 + 1 + 2;
-  static constexpr int kSmem = kUsed + kBars * 8 + 16;
+  static constexpr int kSmem = kUsed + kBars * 8 + kNotes;
   static constexpr uint32_t kDp = kQt, kDv = 2 * kQt, kDk = 2 * kQt + kVb * 64;  // TMEM columns
   static_assert(kDk + kKb * 64 <= 512, "TMEM columns");
   static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -282,11 +282,11 @@ __device__ __forceinline__ void attn_dkv(const BwdParams &P, uint8_t *smem, int 
   const uint32_t dring = qring + C::kQStages * C::kQStage;
   float *const stats = reinterpret_cast<float *>(smem + C::kStatAt);
   const AttnGuard guard = {abort_flag, P.status};
+  const Started started = {abort_flag + 1};
 
   if (warp == kBwdWarps + 2) {
     uint32_t raw_phase = 0;
     TileRing Q(qfull0, qempty0, qring, C::kQStage, C::kQStages), D(dfull0, dempty0, dring, C::kDStage, C::kDStages);
-    Armed kv;
     if (steps > 0) {
       if (elect_one()) {
         mbar_expect_tx(kvfull, (uint32_t)(A.kb + A.vb) * kAttnBlock);
@@ -294,7 +294,6 @@ __device__ __forceinline__ void attn_dkv(const BwdParams &P, uint8_t *smem, int 
         for (int c = 0; c < A.vb; ++c) tma_load_4d(vt + c * kAttnBlock, &P.v, kvfull, 64 * c, kh, k0, b);
       }
       __syncwarp();
-      kv.set(0, 0);
     }
     int tt = 0, hb = 0;
     for (int i = 0; i < steps; ++i) {
@@ -305,7 +304,7 @@ __device__ __forceinline__ void attn_dkv(const BwdParams &P, uint8_t *smem, int 
       if (!D.load(guard, &P.dy, A.vb, C::kQBlock, h0, t0, b, dirty, raw, raw_phase, kQt, lo, hi, lane)) break;
       if (++tt == n_tok) tt = 0, ++hb;
     }
-    if (guard.aborted()) kv.settle(kvfull), Q.armed.settle(qfull0), D.armed.settle(dfull0);
+    if (lane == 0) started.note(1, Q.loads, D.loads);
   } else if (warp == kBwdWarps + 3) {
     // the rows' statistics, a stage ahead of the elementwise warps
     int s = 0, tt = 0, hb = 0;
@@ -497,6 +496,11 @@ __device__ __forceinline__ void attn_dkv(const BwdParams &P, uint8_t *smem, int 
   __syncthreads();
   tc_fence_after();
   if (warp == kBwdWarps) tmem_free(tmem, 512);
+  if (warp == kBwdWarps + 2 && guard.aborted()) {
+    started.settle_single(guard, kvfull);
+    started.settle_ring(guard, 1, qfull0, C::kQStages);
+    started.settle_ring(guard, 2, dfull0, C::kDStages);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -515,7 +519,7 @@ struct Dq {
   static constexpr int kUsed = kVRing + kVStages * kDTile;
   // rows, K full/empty, V full/empty, S (two), dP, dP read, dS (two), drained (two), raw
   static constexpr int kBars = 1 + 2 * kKStages + 2 * kVStages + 6 + 2 + 1;
-  static constexpr int kSmem = kUsed + kBars * 8 + 16;
+  static constexpr int kSmem = kUsed + kBars * 8 + kNotes;
   static constexpr uint32_t kDp = kBufs * 128, kDq = kDp + 128;  // TMEM columns
   static_assert(kDq + kKb * 64 <= 512, "TMEM columns");
   static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -575,11 +579,11 @@ __device__ __forceinline__ void attn_dq(const BwdParams &P, uint8_t *smem, int i
   const uint32_t tmem = *tmem_slot;
   const uint32_t qt = smem_u32(smem), dt = qt + C::kQTile, kring = qt + C::kKRing, vring = qt + C::kVRing;
   const AttnGuard guard = {abort_flag, P.status};
+  const Started started = {abort_flag + 1};
 
   if (warp == kBwdWarps + 2) {
     uint32_t raw_phase = 0;
     TileRing K(kfull0, kempty0, kring, C::kQTile, C::kKStages), V(vfull0, vempty0, vring, C::kDTile, C::kVStages);
-    Armed rows;
     if (steps > 0) {
       if (elect_one()) {
         mbar_expect_tx(rfull, (uint32_t)(A.kb + A.vb) * kAttnBlock);
@@ -587,7 +591,6 @@ __device__ __forceinline__ void attn_dq(const BwdParams &P, uint8_t *smem, int i
         for (int c = 0; c < A.vb; ++c) tma_load_4d(dt + c * kAttnBlock, &P.dy, rfull, 64 * c, h0, t0, b);
       }
       __syncwarp();
-      rows.set(0, 0);
     }
     for (int i = 0; i < steps; ++i) {
       const int k0 = (tk.j0 + i) * kAttnTile;
@@ -596,7 +599,7 @@ __device__ __forceinline__ void attn_dq(const BwdParams &P, uint8_t *smem, int i
         break;
       if (!V.load(guard, &P.v, A.vb, kAttnBlock, kh, k0, b, false, raw, raw_phase, 0, 0, 0, lane)) break;
     }
-    if (guard.aborted()) rows.settle(rfull), K.armed.settle(kfull0), V.armed.settle(vfull0);
+    if (lane == 0) started.note(1, K.loads, V.loads);
   } else if (warp == kBwdWarps) {
     // S ahead of dQ where there are two places for S, else behind it
     RingAt K, behind;  // S's and dQ's tile of keys
@@ -721,6 +724,11 @@ __device__ __forceinline__ void attn_dq(const BwdParams &P, uint8_t *smem, int i
   __syncthreads();
   tc_fence_after();
   if (warp == kBwdWarps) tmem_free(tmem, 512);
+  if (warp == kBwdWarps + 2 && guard.aborted()) {
+    started.settle_single(guard, rfull);
+    started.settle_ring(guard, 1, kfull0, C::kKStages);
+    started.settle_ring(guard, 2, vfull0, C::kVStages);
+  }
 }
 
 // Both walks in one launch, the keys' tiles first: the queries' tiles start as the last

@@ -408,6 +408,7 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t part
 struct AttnGuard {
   volatile int32_t *abort_flag;
   int32_t *status;
+  uint64_t limit = kWaitNs;
 
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
     if (mbar_try(bar, parity)) return true;
@@ -416,7 +417,7 @@ struct AttnGuard {
       if (mbar_try(bar, parity)) return true;
       if ((spin & 63u) == 0) {
         if (*abort_flag) return false;
-        if (global_ns() - t0 > kWaitNs) {
+        if (global_ns() - t0 > limit) {
           *abort_flag = 1;
           flag_status(status, GBO_STATUS_TIMEOUT);
           return false;
@@ -431,7 +432,7 @@ struct AttnGuard {
     for (uint32_t spin = 1;; ++spin) {
       if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
       if ((spin & 63u) == 0) {
-        const bool late = global_ns() - t0 > kWaitNs;
+        const bool late = global_ns() - t0 > limit;
         if (__any_sync(0xffffffffu, late || *abort_flag)) {
           if (!*abort_flag) {
             *abort_flag = 1;
@@ -445,19 +446,27 @@ struct AttnGuard {
   __device__ __forceinline__ bool aborted() const { return *abort_flag != 0; }
 };
 
-// Stages of a ring whose copies were started: after a wait that ran out, they
-// land (or run out of time, too) before shared memory goes away.
-struct Armed {
-  uint32_t mask = 0, parity = 0;
-  __device__ __forceinline__ void set(int stage, uint32_t phase) {
-    mask |= 1u << stage;
-    parity = (parity & ~(1u << stage)) | (phase << stage);
+// The copies that a CTA's loading warp has started, noted in shared memory when it is
+// done.  Where a wait of any warp ran out, they land (or run out of time, too) behind the
+// CTA's last barrier, before the CTA ends and with it its shared memory: not sooner,
+// because until there another warp's wait may run out.
+struct Started {
+  volatile int32_t *at;  // a bit for each barrier that takes one copy; numbers of copies into two rings
+
+  __device__ __forceinline__ void note(int32_t single, int32_t first, int32_t second) const {
+    at[0] = single, at[1] = first, at[2] = second;
   }
-  __device__ __forceinline__ void settle(uint32_t bars) const {
-    for (int s = 0; s < 32; ++s)
-      if (mask >> s & 1u) (void)mbar_wait(bars + 8 * s, parity >> s & 1u);
+  __device__ __forceinline__ void settle_single(const AttnGuard &guard, uint32_t bars) const {
+    for (int s = 0; s < 2; ++s)
+      if (at[0] >> s & 1) (void)mbar_wait_ns(bars + 8 * s, 0, guard.limit);
+  }
+  // ring: 1 or 2
+  __device__ __forceinline__ void settle_ring(const AttnGuard &guard, int ring, uint32_t bars, int stages) const {
+    const int n = at[ring];
+    for (int k = max(0, n - stages); k < n; ++k) (void)mbar_wait_ns(bars + 8 * (k % stages), (k / stages) & 1, guard.limit);
   }
 };
+constexpr int kNotes = 32;  // bytes: where TMEM starts, the flag, these
 
 // Wait until every product this warp's elected lane has issued is done: nothing
 // reads shared memory or writes TMEM when the CTA goes on to give them up.
@@ -476,9 +485,8 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int blocks, int rows, u
 // the tile counts as loaded.
 struct TileRing {
   uint32_t full, empty, base, bytes;  // barriers, first tile, bytes from tile to tile
-  int stages, stage = 0;
+  int stages, stage = 0, loads = 0;
   uint32_t phase = 0;
-  Armed armed;
 
   __device__ __forceinline__ TileRing(uint32_t full_, uint32_t empty_, uint32_t base_, uint32_t bytes_, int stages_)
       : full(full_), empty(empty_), base(base_), bytes(bytes_), stages(stages_) {}
@@ -496,16 +504,15 @@ struct TileRing {
     __syncwarp();
     if (dirty) {
       if (!guard.wait_warp(raw, raw_phase)) {
-        (void)mbar_wait(raw, raw_phase);
+        (void)mbar_wait_ns(raw, raw_phase, guard.limit);
         return false;
       }
       raw_phase ^= 1;
       zero_rows(tile, blocks, rows, block_bytes, lo, hi, lane);
       if (elect_one()) mbar_arrive(full + 8 * stage);
       __syncwarp();
-    } else {
-      armed.set(stage, phase);
     }
+    ++loads;
     if (++stage == stages) stage = 0, phase ^= 1;
     return true;
   }

@@ -47,7 +47,7 @@ struct Fwd {
   // turns (two)
   static constexpr int kBars = 2 + 2 * kKStages + 2 * kVStages + 1 + 8 + 8 + 2 + 2;
   static constexpr int kHalves = 2 * 2 * kAttnTile * 4;  // half of the keys, row tile, row: a float
-  static constexpr int kSmem = kUsed + kHalves + kBars * 8 + 16;
+  static constexpr int kSmem = kUsed + kHalves + kBars * 8 + kNotes;
   static constexpr uint32_t kO = 256;  // TMEM: S0, S1 of 128 columns, O0, O1 of kVb * 64
   static constexpr uint32_t kCols = 512;
   static_assert(kVb * kAttnBlock <= kQTile, "the output leaves through the queries' place");
@@ -160,11 +160,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
   const uint32_t q0 = smem_u32(smem), kring = q0 + C::kKRing, vring = q0 + C::kVRing;
   const AttnGuard guard = {abort_flag, P.status};
+  const Started started = {abort_flag + 1};
 
   if (warp == kFwdSoftWarps + 2) {
     uint32_t raw_phase = 0;
     TileRing K(kfull0, kempty0, kring, C::kQTile, C::kKStages), V(vfull0, vempty0, vring, C::kVTile, C::kVStages);
-    Armed q;
+    int32_t queries = 0;
     for (int t = 0; t < 2; ++t)
       if (tk[t].j1 > tk[t].j0) {
         if (elect_one()) {
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
             tma_load_4d(q0 + t * C::kQTile + c * kAttnBlock, &P.q, qfull0 + 8 * t, 64 * c, h0, t0 + t * tokens, b);
         }
         __syncwarp();
-        q.set(t, 0);
+        queries |= 1 << t;
       }
     for (int j = J0; j < J1; ++j) {
       const int k0 = j * kAttnTile;
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
       if (!V.load(guard, &P.v, A.vb, kAttnBlock, kh, k0, b, dirty, raw, raw_phase, kAttnTile, seq.k_lo - k0, seq.k_hi - k0, lane))
         break;
     }
-    if (guard.aborted()) q.settle(qfull0), K.armed.settle(kfull0), V.armed.settle(vfull0);
+    if (lane == 0) started.note(queries, K.loads, V.loads);
   } else if (warp >= kFwdSoftWarps) {
     // The tensor cores' work for row tile t: steps of PV(j - 1) and S(j); P stands
     // over S, and one thread's products run in order.  Each tile has a warp of its
@@ -407,6 +408,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   if (warp == kFwdSoftWarps) tmem_free(tmem, C::kCols);
+  if (warp == kFwdSoftWarps + 2 && guard.aborted()) {
+    started.settle_single(guard, qfull0);
+    started.settle_ring(guard, 1, kfull0, C::kKStages);
+    started.settle_ring(guard, 2, vfull0, C::kVStages);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -429,7 +435,7 @@ struct Tok {
   static constexpr int kStages = kKb == 1 ? 6 : kKb == 2 ? 3 : 2;
   static constexpr int kJoin = kTokWarps * 16 * (kVb * 64 + 4) * 4;  // outputs, maxima and sums of the warps
   static constexpr int kUsed = kStages * kStage > kJoin ? kStages * kStage : kJoin;
-  static constexpr int kSmem = kUsed + (2 * kStages) * 8 + 16;
+  static constexpr int kSmem = kUsed + (2 * kStages) * 8 + kNotes;
   static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
 };
 
@@ -507,6 +513,7 @@ __global__ void __launch_bounds__(kTokThreads, 2) attn_token_kernel(const __grid
   J0 += split * each;
   J1 = min(J1, J0 + each);
   const AttnGuard guard = {abort_flag, P.status};
+  const Started started = {abort_flag + 1};
   const int blocks = A.kb + A.vb;
   const int rows = P.group * P.mask.sq;  // row r: token r / group, head r % group
   bool ok = true;
@@ -519,22 +526,18 @@ __global__ void __launch_bounds__(kTokThreads, 2) attn_token_kernel(const __grid
 
   if (warp == kTokWarps) {
     if (lane == 0) {
-      uint32_t armed = 0, parity = 0, phase = 0;
-      int s = 0;
-      for (int j = J0; j < J1; ++j) {
+      uint32_t phase = 0;
+      int s = 0, j = J0;
+      for (; j < J1; ++j) {
         if (!guard.wait(empty0 + 8 * s, phase ^ 1)) break;
         mbar_expect_tx(full0 + 8 * s, (uint32_t)(blocks * kTokBlock));
         const uint32_t st = ring0 + s * C::kStage;
         for (int c = 0; c < A.kb; ++c) tma_load_4d(st + c * kTokBlock, &P.k, full0 + 8 * s, 64 * c, kh, j * kTokKeys, b);
         for (int c = 0; c < A.vb; ++c)
           tma_load_4d(st + (kKb + c) * kTokBlock, &P.v, full0 + 8 * s, 64 * c, kh, j * kTokKeys, b);
-        armed |= 1u << s;
-        parity = (parity & ~(1u << s)) | (phase << s);
         if (++s == C::kStages) s = 0, phase ^= 1;
       }
-      if (guard.aborted())
-        for (int i = 0; i < C::kStages; ++i)
-          if (armed >> i & 1u) (void)mbar_wait(full0 + 8 * i, parity >> i & 1u);
+      started.note(0, j - J0, 0);
     }
   } else if (J1 > J0) {
     // the two rows of this lane, and the queries as the A operand
@@ -634,7 +637,10 @@ __global__ void __launch_bounds__(kTokThreads, 2) attn_token_kernel(const __grid
     }
   }
   __syncthreads();  // every stage has been read
-  if (guard.aborted()) return;
+  if (guard.aborted()) {
+    if (threadIdx.x == kTokWarps * 32) started.settle_ring(guard, 1, full0, C::kStages);
+    return;
+  }
   float *const jo = reinterpret_cast<float *>(smem), *const js = jo + kTokWarps * 16 * kVb * 64;
   if (warp < kTokWarps) {
 #pragma unroll

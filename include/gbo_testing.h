@@ -40,6 +40,23 @@ int gbo_testing_ring_give_up(const void *rows, int32_t n, int32_t lost, int32_t 
                              uint32_t limit_us, gbo_stream_t stream);
 
 /*
+ * Launch one CTA of the attention kernels' waits on what never comes: warp 0 of
+ * the ring of tiles on a place for a third tile of two, one thread of warp 1 and
+ * all lanes of warp 2 on a barrier nothing arrives on.  Warp `first` (0..2) has a
+ * limit of `limit_us` microseconds, the others one a hundred times as long: its
+ * wait gives up and ORs GBO_STATUS_TIMEOUT into *dev_status, and theirs follow.
+ *   tokens  device, 64 x 64 bf16, 16-byte aligned
+ *   found   device int32, 10: of each warp whether what it waited for came; of
+ *           each the microseconds that it took; a bit for each stage that had
+ *           landed at the end; the first word of the first tile, of row 8
+ *           of the second (whose rows 8 to 23 are kept) and of its row 0 (zeroed)
+ * Asynchronous on `stream`.
+ * Errors: INVALID_ARG (limit outside 1..50000 us among others), UNSUPPORTED, CUDA.
+ */
+int gbo_testing_attn_give_up(const void *tokens, int32_t first, int32_t *found, int32_t *dev_status, uint32_t limit_us,
+                             gbo_stream_t stream);
+
+/*
  * Whether Muon plans created from now on (any thread) run the Gram route's
  * p x p iterations of matrices with p <= 192 in bf16 mode as one on-chip
  * chain launch (enable != 0, the default) or as one tensor-core launch per

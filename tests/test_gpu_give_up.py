@@ -54,9 +54,31 @@ def test_a_rows_copy_that_does_not_land(n, lost):
     still_works()
 
 
+@pytest.mark.parametrize("first", [0, 1, 2])
+def test_attentions_waits_give_up_together(first):
+    """The one with the short limit raises the flag, the others (two seconds) see it; the ring's
+    tiles have landed, the cleaned one among them, when the kernel ends."""
+    gen = torch.Generator().manual_seed(first)
+    tokens = torch.randn(64, 64, generator=gen).to(torch.bfloat16).cuda()
+    words = tokens.view(torch.int32)
+    found = torch.full((10,), -7, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.gbo_testing_attn_give_up(tokens, first, found, status, LIMIT_US)
+    got = found.tolist()
+    assert int(status) == B.GBO_STATUS_TIMEOUT
+    assert got[:3] == [0, 0, 0]
+    assert all(0.9 * LIMIT_US < t < 50 * LIMIT_US for t in got[3:6]), got  # (half of their own)
+    assert got[6] == 3 and got[7] == int(words[0, 0]) and got[8] == int(words[32 + 8, 0]) and got[9] == 0
+    still_works()
+
+
 def test_refused():
     rows = torch.zeros(2, 256, dtype=torch.int32, device="cuda")
     found, status = (torch.zeros(k, dtype=torch.int32, device="cuda") for k in (4, 1))
     for lost, limit in ((2, 10), (-2, 10), (0, 0), (0, 10 ** 7)):
         with pytest.raises(B.GboError):
             B.gbo_testing_ring_give_up(rows, lost, found, status, limit)
+    tokens, found = torch.zeros(64, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(10, dtype=torch.int32, device="cuda")
+    for first, limit in ((3, 10), (-1, 10), (0, 0), (0, 50001)):
+        with pytest.raises(B.GboError):
+            B.gbo_testing_attn_give_up(tokens, first, found, status, limit)
