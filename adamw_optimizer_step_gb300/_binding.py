@@ -906,9 +906,25 @@ def _rows_or_null(t, what, shape, dtype):
     return t.data_ptr(), _rows_of(t, what, shape)
 
 
+_residual_sizes = functools.partial(struct.Struct("@2q").unpack_from, offset=ResidualArgs.n.offset)
+_residual_modes = functools.partial(struct.Struct("@8i").unpack_from, offset=ResidualArgs.x_dtype.offset)
+
+
+def _residual_of(args, shape, x_dtype, block_dtype):
+    """Shapes that ``args`` asks of dgate, and values of dscale; refuses other sizes and types than
+    theirs, because outputs are checked against the ones and written by the others."""
+    n, d = _residual_sizes(args)
+    xt, bt, _, _, _, gate, _, scale = _residual_modes(args)
+    if tuple(shape) != (n, d) or _ELEMENT.get(x_dtype) != xt or _ELEMENT.get(block_dtype) != bt:
+        raise ValueError("args are of %s rows, and of other types or sizes than %s in %s and %s" %
+                         ((n, d), tuple(shape), x_dtype, block_dtype))
+    return (n, 1 if gate == GBO_GATE_ROW else d), 1 if scale == GBO_SCALE_ONE else d
+
+
 def gbo_residual_forward(args, x_out, h, shape, x_dtype, block_dtype, dev_status=None, stream=None):
     """Residual update of ``args`` (of :func:`residual_args`) into ``x_out`` and ``h``
     (each may be None where there is nothing to write), ``shape`` (n, d) both."""
+    _residual_of(args, shape, x_dtype, block_dtype)
     xp, xs = _rows_or_null(x_out, "x_out", shape, x_dtype)
     hp, hs = _rows_or_null(h, "h", shape, block_dtype)
     _here(x_out, h, dev_status)
@@ -927,18 +943,19 @@ def gbo_residual_workspace_bytes(n, d, sums):
 
 def gbo_residual_backward(args, workspace, shape, x_dtype, block_dtype, *, dx_out=None, dh=None, dx=None, dblock=None,
                           dgate=None, dscale=None, dpost_gain=None, dpre_gain=None, dev_status=None, stream=None):
-    """Gradients of the residual update, whichever are given to be written."""
-    n, d = shape
+    """Gradients of the residual update, whichever are given to be written: ``dgate`` and
+    ``dscale`` of the gate's and the scale's own sizes."""
+    d = shape[1]
+    gate_shape, scales = _residual_of(args, shape, x_dtype, block_dtype)
+    ds = _out_f32(dscale, scales, "dscale") or 0
+    gp, gs = _rows_or_null(dgate, "dgate", gate_shape, block_dtype)
     _here(dx_out, dh, dx, dblock, dgate, dscale, dpost_gain, dpre_gain, workspace, dev_status)
     oxp, oxs = _rows_or_null(dx_out, "dx_out", shape, x_dtype)
     ohp, ohs = _rows_or_null(dh, "dh", shape, block_dtype)
     xp, xs = _rows_or_null(dx, "dx", shape, x_dtype)
     bp, bs = _rows_or_null(dblock, "dblock", shape, block_dtype)
-    gp, gs = _rows_or_null(dgate, "dgate", None if dgate is None else (n, dgate.shape[1]), block_dtype)
-    grads = _PACK_RESIDUAL_GRADS(oxp, ohp, xp, bp, gp,
-                                 (_out_f32(dscale, 1 if dscale.numel() == 1 else d, "dscale") if dscale is not None else 0),
-                                 _out_f32(dpost_gain, d, "dpost_gain") or 0, _out_f32(dpre_gain, d, "dpre_gain") or 0, oxs,
-                                 ohs, xs, bs, gs)
+    grads = _PACK_RESIDUAL_GRADS(oxp, ohp, xp, bp, gp, ds, _out_f32(dpost_gain, d, "dpost_gain") or 0,
+                                 _out_f32(dpre_gain, d, "dpre_gain") or 0, oxs, ohs, xs, bs, gs)
     ws, nbytes = _workspace(workspace)
     _check(lib().gbo_residual_backward(args, grads, ws, nbytes, _dev_ptr(dev_status, "dev_status"), _stream(stream)))
 

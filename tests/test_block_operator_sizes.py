@@ -110,3 +110,32 @@ def test_cuts_of_no_rows_and_of_many(tmp_path):
     subprocess.run([build_mod.nvcc(), *build_mod.ARCH, "-std=c++17", "-O1", "--expt-relaxed-constexpr", "-I", build_mod.INCLUDE,
                     "-I", build_mod.CSRC, str(src), "-o", str(exe)], check=True, capture_output=True)
     assert subprocess.run([str(exe)], timeout=60).returncode == 0
+
+
+# outputs against the arguments that the kernels write them by
+
+def residual_bytes(n, d, gate=B.GBO_GATE_ELEMENT, scale=B.GBO_SCALE_VECTOR, xt=B.GBO_BF16, bt=B.GBO_BF16):
+    return bytes(B.ResidualArgs(n=n, d=d, gate_mode=gate, scale_mode=scale, x_dtype=xt, block_dtype=bt, has_block=1))
+
+
+@pytest.mark.parametrize("modes,what,shape", [
+    (dict(scale=B.GBO_SCALE_VECTOR), "dscale", (1,)), (dict(scale=B.GBO_SCALE_ONE), "dscale", (64,)),
+    (dict(gate=B.GBO_GATE_ELEMENT), "dgate", (1, 1)), (dict(gate=B.GBO_GATE_ROW), "dgate", (1, 64)),
+    (dict(gate=B.GBO_GATE_ROW), "dgate", (2, 1)), (dict(), "dpost_gain", (1,)), (dict(), "dpre_gain", (63,)),
+], ids=str)
+def test_residual_gradients_have_the_sizes_of_what_they_are_of(monkeypatch, modes, what, shape):
+    """A scale of d values has d gradients, not one, whatever the output's own size says."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)  # (where these tensors are)
+    out = torch.zeros(shape, dtype=torch.bfloat16 if what == "dgate" else torch.float32)
+    with pytest.raises(ValueError, match=what + " must be (1|64|two-dim)"):
+        B.gbo_residual_backward(residual_bytes(1, 64, **modes), None, (1, 64), torch.bfloat16, torch.bfloat16, **{what: out})
+
+
+@pytest.mark.parametrize("shape,xt,bt", [((4, 63), 1, 1), ((5, 64), 1, 1), ((4, 64), 0, 1), ((4, 64), 0, 0)])
+def test_residual_outputs_are_of_the_arguments_rows(shape, xt, bt):
+    types = [{1: torch.bfloat16, 0: torch.float32}[t] for t in (xt, bt)]
+    args = residual_bytes(4, 64)
+    with pytest.raises(ValueError, match="args are of"):
+        B.gbo_residual_forward(args, None, None, shape, *types)
+    with pytest.raises(ValueError, match="args are of"):
+        B.gbo_residual_backward(args, None, shape, *types)
