@@ -812,11 +812,27 @@ def _workspace(t):
     return _dev_ptr(t, "workspace"), 0 if t is None else t.numel() * t.element_size()
 
 
+_attn_lengths = functools.partial(struct.Struct("@3q").unpack_from, offset=AttnArgs.batch.offset)
+_attn_dims = functools.partial(struct.Struct("@4i").unpack_from, offset=AttnArgs.q_heads.offset)
+
+
+def _attn_of(args, q, k, v):
+    """Shapes of q, k (not looked at if None) and v, from ``args``; refuses tensors of others, because
+    outputs are checked against the ones and written by the others."""
+    b, sq, sk = _attn_lengths(args)
+    hq, hk, dk, dv = _attn_dims(args)
+    shapes = (b, sq, hq, dk), (b, sk, hk, dk), (b, sk, hk, dv)
+    for what, t, shape in zip("qkv", (q, k, v), shapes):
+        if t is not None and t.shape != shape:
+            raise ValueError("args are of %s %s, not of %s" % (what, shape, tuple(t.shape)))
+    return shapes
+
+
 def gbo_attn_forward(args, q, v, y, workspace=None, *, lse=None, dev_status=None, stream=None):
     """Attention of ``args`` (of :func:`attn_args`, from ``q`` and ``v`` among others)
     into ``y`` (batch, seq, heads, dv) and ``lse`` (batch, seq, heads float32)."""
-    b, sq, hq, _ = q.shape
-    ys = _PACK_STRIDE(*_attn_heads(y, "y", (b, sq, hq, v.shape[3])))
+    (b, sq, hq, _), _, v_shape = _attn_of(args, q, None, v)
+    ys = _PACK_STRIDE(*_attn_heads(y, "y", (b, sq, hq, v_shape[3])))
     if not y.is_cuda:
         raise ValueError("y must be a CUDA tensor")
     _here(y, lse, workspace, dev_status)
@@ -828,11 +844,11 @@ def gbo_attn_forward(args, q, v, y, workspace=None, *, lse=None, dev_status=None
 def gbo_attn_backward(args, q, k, v, dy, y, lse, workspace, *, dq=None, dk=None, dv=None, dev_status=None, stream=None):
     """Gradients into ``dq``, ``dk`` and ``dv``, whichever are given, from the
     forward's ``y`` and ``lse``."""
-    q_shape, v_shape = q.shape, v.shape
+    q_shape, k_shape, v_shape = _attn_of(args, q, k, v)
     b, sq, hq, _ = q_shape
     y_shape = (b, sq, hq, v_shape[3])
     ptrs, strides = [], ()
-    for what, t, shape in (("dy", dy, y_shape), ("y", y, y_shape), ("dq", dq, q_shape), ("dk", dk, k.shape), ("dv", dv, v_shape)):
+    for what, t, shape in (("dy", dy, y_shape), ("y", y, y_shape), ("dq", dq, q_shape), ("dk", dk, k_shape), ("dv", dv, v_shape)):
         if t is None:
             ptrs.append(0)
             strides += _ZERO3

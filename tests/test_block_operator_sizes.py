@@ -139,3 +139,18 @@ def test_residual_outputs_are_of_the_arguments_rows(shape, xt, bt):
         B.gbo_residual_forward(args, None, None, shape, *types)
     with pytest.raises(ValueError, match="args are of"):
         B.gbo_residual_backward(args, None, shape, *types)
+
+
+@pytest.mark.parametrize("what,shape", [("q", (2, 5, 4, 64)), ("q", (1, 4, 4, 64)), ("k", (1, 7, 1, 64)), ("v", (1, 7, 2, 32)),
+                                        ("v", (1, 9, 2, 64))], ids=str)
+def test_attention_outputs_are_of_the_arguments_tensors(what, shape):
+    """Outputs are checked against the tensors beside the arguments: those have to be the arguments' own."""
+    args = bytes(B.AttnArgs(batch=1, sq=5, sk=7, q_heads=4, k_heads=2, dk=64, dv=64))
+    shapes = dict(dict(q=(1, 5, 4, 64), k=(1, 7, 2, 64), v=(1, 7, 2, 64)), **{what: shape})
+    q, k, v = (torch.zeros(shapes[n], dtype=torch.bfloat16) for n in "qkv")
+    dy = torch.zeros(*q.shape[:3], v.shape[3], dtype=torch.bfloat16)
+    if what != "k":
+        with pytest.raises(ValueError, match="args are of " + what):
+            B.gbo_attn_forward(args, q, v, torch.zeros_like(dy))
+    with pytest.raises(ValueError, match="args are of " + what):
+        B.gbo_attn_backward(args, q, k, v, dy, dy, None, None)
