@@ -231,7 +231,9 @@ def residual_norm(x, block=None, *, post_norm=False, pre_norm=True, post_gain=No
     that is read when the kernel runs) and ``offset``, see ``gbo_residual_args``.
     ``block=None``: the norm alone, and x' is ``x``.  ``x`` and ``block`` are bfloat16 or
     float32, ``block`` bfloat16 where ``x`` is; ``h`` has the dtype of ``block``.
-    ``x_out`` may be ``x``.  Without ``pre_norm`` h is None."""
+    ``x_out`` (with a block's output) may be ``x``.  Without ``pre_norm`` h is None."""
+    if block is None and x_out is not None:
+        raise ValueError("x_out without a block's output: the stream stays as it is")
     flat = x.dim() == 2
     x2, b2, g2 = (x, block, gate) if flat else (_flat(x), _flat(block), _flat(gate))
     bt = x.dtype if block is None else block.dtype

@@ -10,6 +10,7 @@ import torch
 
 from adamw_optimizer_step_gb300 import _binding as B
 from adamw_optimizer_step_gb300 import build as build_mod
+from adamw_optimizer_step_gb300 import layers
 
 FAKE = 1 << 20
 
@@ -154,3 +155,11 @@ def test_attention_outputs_are_of_the_arguments_tensors(what, shape):
             B.gbo_attn_forward(args, q, v, torch.zeros_like(dy))
     with pytest.raises(ValueError, match="args are of " + what):
         B.gbo_attn_backward(args, q, k, v, dy, dy, None, None)
+
+
+def test_a_stream_without_a_block_is_not_written():
+    """The norm alone leaves the stream as it is: a place for the updated one is refused, not ignored."""
+    x = torch.zeros(2, 8)
+    for t in (x, x.view(1, 2, 8)):
+        with pytest.raises(ValueError, match="x_out without"):
+            layers.residual_norm(t, x_out=torch.empty_like(t))
