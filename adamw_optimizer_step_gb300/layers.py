@@ -282,13 +282,18 @@ def dropout(x, p, seed, *, offset=0, out=None):
     """``x`` with elements dropped with probability ``p`` (a multiple of 2^-16) and the
     others divided by the share kept.  Which ones follows from ``seed`` (an int, or a
     CUDA int64 tensor that is read when the kernel runs), ``offset`` and an element's
-    place alone: no mask is kept, and the same call on a gradient is the gradient."""
-    if x.dim() == 2:
-        y = _like(x) if out is None else out
-        B.gbo_dropout(x, y, p, seed, offset)
+    place alone: no mask is kept, and the same call on a gradient is the gradient.  Rows
+    of a two-dimensional ``x`` may lie apart; other strides are copied together first."""
+    flat = x.dim() == 2
+    rows = x if flat else x.reshape(1, -1)  # (a view where it can be, with any stride)
+    if (rows.stride(1) != 1 and rows.shape[1] > 1) or (rows.stride(0) < rows.shape[1] and rows.shape[0] > 1):
+        rows = rows.contiguous()
+    if flat:
+        y = _like(rows) if out is None else out
+        B.gbo_dropout(rows, y, p, seed, offset)
         return y
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    B.gbo_dropout(x.reshape(1, -1), y.view(1, -1), p, seed, offset)
+    B.gbo_dropout(rows, y.view(1, -1), p, seed, offset)
     return y
 
 

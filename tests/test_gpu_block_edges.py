@@ -1,5 +1,5 @@
 """Attention, the residual update and dropout at the edges of what their arguments allow:
-no rows, an eps of zero.  Values are compared as in
+no rows, an eps of zero, strides of any kind.  Values are compared as in
 tests/test_gpu_residual.py, whose tolerances hold here."""
 
 import pytest
@@ -38,3 +38,19 @@ def test_eps_of_zero(d, n, types):
     several does not have (32 / threads of them, widths up to 128) reach no sum."""
     for gate in (None, "row", "element"):
         Case(n, d, *types, gate=gate, eps=0.0, seed=d + n).check()
+
+
+def test_dropout_of_any_strides():
+    """Transposed and expanded tensors, of two axes as of three: the bits of their copies."""
+    base = torch.randn(24, 40, device="cuda")
+    for t in (base.T, base[:, ::2], base[:1].expand(24, 40), base[:, :1].expand(24, 40), base[:, 3:4], base[:, :1].T):
+        want = layers.dropout(t.contiguous(), 0.4, 5)
+        assert torch.equal(layers.dropout(t, 0.4, 5), want)
+        assert torch.equal(layers.dropout(t[None], 0.4, 5), want[None])
+        out = torch.full((t.shape[0], t.shape[1] + 3), 7.0, device="cuda")
+        layers.dropout(t, 0.4, 5, out=out[:, :t.shape[1]])
+        assert torch.equal(out[:, :t.shape[1]], want) and (out[:, t.shape[1]:] == 7).all()
+    x = base.T.requires_grad_()
+    y = layers.dropout_autograd(x, 0.4, 5)
+    y.backward(torch.ones_like(y))
+    assert torch.equal(x.grad, layers.dropout(torch.ones_like(y), 0.4, 5))
