@@ -580,11 +580,22 @@ int attn_cuda(cudaError_t e) {
   return report_error(GBO_ERR_CUDA, msg);
 }
 
-// The current device, made current in the driver too: on a thread that has made no
-// runtime call yet (autograd's, say) the driver has no context to encode maps in.
+// The current device.  On a thread that has made no runtime call yet (autograd's, say)
+// the driver has no context to encode maps in: there the device's own is made current.
+// One that is current stays, the device's own or not.
 int attn_device(int *dev, int *sm) {
   const int rc = require_device(dev, sm);
   if (rc != GBO_OK) return rc;
+  using GetCurrentFn = CUresult (*)(CUcontext *);
+  static const GetCurrentFn current = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 4000, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<GetCurrentFn>(p) : nullptr;
+  }();
+  CUcontext ctx = nullptr;
+  if (current && current(&ctx) == CUDA_SUCCESS && ctx) return GBO_OK;
   const cudaError_t e = cudaSetDevice(*dev);
   return e == cudaSuccess ? GBO_OK : attn_cuda(e);
 }

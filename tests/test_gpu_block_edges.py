@@ -1,6 +1,9 @@
 """Attention, the residual update and dropout at the edges of what their arguments allow:
-no rows, an eps of zero, strides of any kind.  Values are compared as in
+no rows, an eps of zero, strides of any kind, a caller's context.  Values are compared as in
 tests/test_gpu_residual.py, whose tolerances hold here."""
+
+import ctypes
+import threading
 
 import pytest
 import torch
@@ -54,3 +57,27 @@ def test_dropout_of_any_strides():
     y = layers.dropout_autograd(x, 0.4, 5)
     y.backward(torch.ones_like(y))
     assert torch.equal(x.grad, layers.dropout(torch.ones_like(y), 0.4, 5))
+
+
+def test_a_callers_context_stays_current():
+    """A thread with a driver context of its own: a call of attention (of no sequences, so nothing
+    runs in it) leaves it current."""
+    driver = ctypes.CDLL("libcuda.so.1")
+    torch.zeros(1, device="cuda")
+    args = B.AttnArgs(batch=0, sq=4, sk=4, q_heads=1, k_heads=1, dk=64, dv=64, causal=1, dtype=B.GBO_BF16, scale=1.0)
+    seen = []
+
+    def call():
+        mine, now, device = ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_int()
+        seen.append(driver.cuDeviceGet(ctypes.byref(device), 0))
+        seen.append(driver.cuCtxCreate_v2(ctypes.byref(mine), 0, device))
+        seen.append(B.lib().gbo_attn_forward(ctypes.byref(args), None, None, None, None, 0, None, None))
+        seen.append(driver.cuCtxGetCurrent(ctypes.byref(now)))
+        seen.append(now.value == mine.value)
+        seen.append(driver.cuCtxDestroy_v2(mine))
+
+    t = threading.Thread(target=call)
+    t.start()
+    t.join()
+    assert seen == [0, 0, 0, 0, True, 0]
+    assert torch.equal(layers.dropout(torch.ones(8, device="cuda"), 0.0, 1), torch.ones(8, device="cuda"))
