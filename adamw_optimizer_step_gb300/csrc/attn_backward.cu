@@ -3,7 +3,8 @@
 //   dV = P^T dY,  dS = scale P (dY V^T - D),  dQ = dS K,  dK = dS^T Q.
 // P is formed again from the forward's lse: P = 2^(S c - lse log2(e)).
 //
-//   attn_delta_kernel     per row: -lse log2(e) and D (from P and V for rows of few keys)
+//   attn_delta_kernel     per row: -lse log2(e) and D
+//   attn_few_kernel       the same of rows that see few keys, D from P and V
 //   attn_backward_kernel  attn_dkv: a CTA holds 128 keys and walks over the rows that see them;
 //                         attn_dq: a CTA holds 128 rows and walks over the keys that they see
 //
@@ -12,8 +13,8 @@
 // memory.  Every sum stays in TMEM for a CTA's whole walk, the query heads that
 // share a key head among them.  P and dS are rounded to bf16 once, as operands of
 // products (by 2^-8 of them at most); sums are fp32.  That makes dQ's and dK's error
-// 2.4e-3 of them against 1.7e-3 of the outputs' rounding alone (D from the rounded y adds
-// up to 0.1e-3); dS as two bf16 numbers would take two products more.
+// 2.4e-3 of them against 1.7e-3 of the outputs' rounding alone; dS as two bf16 numbers
+// would take two products more.
 //
 // Measured, causal, 2 x 8192 tokens, 16 query and 4 key heads of 128: 1110 us, the
 // keys' walk alone 670 (1.64 PFLOP/s of the four products it forms), the queries'
@@ -37,17 +38,19 @@ constexpr float kLog2ePlain = 1.4426950408889634f;
 // -lse log2(e) and D of each row: 16 lanes to a row.  A row that sees nothing
 // (lse = -inf) gets -inf and 0, whatever stands in it: its P and dS are 0.  Bound by
 // HBM (dy and y once).
+//
 // D = dy . y takes over the rounding of y, an error that every dS of the row gets times
-// its P: beside dS's own rounding it counts 1 / sqrt(n) over n keys.  Rows that see 8
-// keys or fewer form D = sum p (dy . v) instead (dQ's and dK's error at 48 tokens 2.9e-3
-// -> 2.6e-3 of them, at a handful of tokens 4.4e-3 -> 2.8e-3; with one key dS is 0 and
-// not D's error).  They are looked for among the first 8 tokens of each sequence or
-// document (no later one of a causal sequence sees so few), or among all tokens where a
-// narrow window or few keys may leave any row so few, by the first CTAs, beside the
-// others' stream: 2 to 4 us where sequences are short (up to 16 keys: 5 to 15 us, and
-// 1% less error), nothing at 2 x 8192.  15 us for 6 x 777 x 32 rows of 128 elements.
-
-constexpr int kFewKeys = 8;     // (a power of two)
+// its P: beside dS's own rounding it counts 1 / sqrt(n) over n keys of like weight.  Rows
+// that see 64 keys or fewer form D = sum p (dy . v) instead: dQ's and dK's error is 2.4e-3
+// of them, not 2.6e-3 (16 x 48 tokens, heads of 32) to 3.0e-3 (a handful of tokens), as it
+// is with D from y for rows of more than 8 keys, and over values that lie close together,
+// where D is a difference, it is smaller by orders.  Such rows are looked for among the
+// first 64 tokens of each sequence or document (no later one of a causal sequence sees so
+// few), or among all tokens where a narrow window or few keys may leave any row so few;
+// where no row sees more, attn_delta_kernel does not run.
+constexpr int kFewKeys = 64;
+constexpr int kFewWarps = 4;    // of a CTA, 16 rows each
+constexpr int kFewChunk = 80;   // keys in shared memory at a time: 64 and those of 16 tokens more
 constexpr int kDeltaRows = 32;  // of a CTA, two to each 16 lanes: their loads are under way together
 
 struct DeltaParams {
@@ -59,8 +62,11 @@ struct DeltaParams {
   float scale2;
   int32_t sq, heads, group, dk, dv;
   FastDiv by_heads, by_sq;  // of row numbers that fit 32 bits
-  int32_t places, every;    // of rows of few keys: tokens looked at (of all heads); 1: every token
-  uint32_t few_ctas;
+  // rows of few keys: 2^pack heads that share a key head and 16 / 2^pack tokens to a warp,
+  // `sets` of them to a key head of a sequence or document, chunks of four to a CTA
+  FastDiv by_chunks, by_k_heads, by_blocks;
+  int32_t pack, sets, every;  // every: all tokens are looked at
+  int32_t all;                // no row sees more: those that see nothing are written, too
 };
 
 // Sum of the products of eight pairs of bf16.
@@ -74,62 +80,151 @@ __device__ __forceinline__ float dot8(const uint4 &u, const uint4 &v, float d) {
   return d;
 }
 
-// The first CTAs: rows that see few keys, a warp to a row, a key to each half of it.
-__device__ __forceinline__ void few_keys_delta(const DeltaParams &P) {
-  const int half = threadIdx.x >> 4 & 1, lane = threadIdx.x & 15;
-  int at = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (at >= P.places * P.heads) return;
-  const int h = P.by_heads.split(at);
-  int b = 0, t;
-  if (P.every) {
-    t = P.by_sq.split(at), b = at;
-  } else {
-    const int unit = at / kFewKeys;
-    if (!P.mask.docs) b = unit;
-    t = (P.mask.docs ? clamp_to(P.mask.docs[unit], P.mask.sq) : attn_seq(P.mask, b).q_lo) + at % kFewKeys;
+// acc (16 rows x 8 columns) += A B^T over 32 elements of each row, of which a lane holds
+// eight that follow one another, of A's rows lane / 4 and lane / 4 + 8 and of B's row
+// lane / 4.  (In a sum of products any order of the elements will do, the same in both.)
+__device__ __forceinline__ void mma_rows32(float (&acc)[4], const uint4 &a0, const uint4 &a1, const uint4 &b) {
+  const uint32_t x[4] = {a0.x, a0.y, a0.z, a0.w}, y[4] = {a1.x, a1.y, a1.z, a1.w}, z[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int s = 0; s < 4; s += 2)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+        : "r"(x[s]), "r"(y[s]), "r"(x[s + 1]), "r"(y[s + 1]), "r"(z[s]), "r"(z[s + 1]));
+}
+
+// Keys and values of a chunk, a row 64 bytes longer than whole lines: two rows' 64 bytes
+// that eight lanes read meet in no bank.
+template <int kKb, int kVb>
+struct Few {
+  static constexpr int kKPitch = kKb * 128 + 64, kVPitch = kVb * 128 + 64;
+  static constexpr int kVAt = kFewChunk * kKPitch, kSmem = kVAt + kFewChunk * kVPitch;
+};
+
+// Rows that see few keys.  A warp takes 16 rows of a key head, heads of a token side by
+// side, held in registers; the CTA's warps go over the keys that any of their rows sees,
+// a chunk in shared memory at a time.  Bound by the wait for rows and keys where the first
+// tokens alone are looked at (5 us of a call), by mma.sync where all are (a window of 64
+// over 2 x 8192 tokens of 16 heads: 60 us).  Fragments straight from global memory: 103.
+template <int kKb, int kVb>
+__global__ void __launch_bounds__(32 * kFewWarps, 4) attn_few_kernel(const __grid_constant__ DeltaParams P) {
+  pdl_launch();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  using C = Few<kKb, kVb>;
+  __shared__ int32_t range[2][kFewWarps];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c0 = (lane & 3) * 8;
+  int unit = (int)blockIdx.x;
+  int set = P.by_chunks.split(unit) * kFewWarps + warp;
+  const int kh = P.by_k_heads.split(unit);
+  const bool mine = set < P.sets;
+  const int h0 = kh * P.group + (P.by_blocks.split(set) << P.pack);
+  int first = set * (16 >> P.pack), end = P.sq, b = unit;  // this warp's tokens
+  if (!P.every) {
+    int from;
+    if (P.mask.docs) {
+      b = 0, from = clamp_to(P.mask.docs[unit], P.mask.sq), end = clamp_to(P.mask.docs[unit + 1], P.mask.sq);
+    } else {
+      const AttnSeq seq = attn_seq(P.mask, b);
+      from = seq.q_lo, end = seq.q_hi;
+    }
+    end = min(end, from + kFewKeys), first += from;
   }
   const AttnSeq seq = attn_seq(P.mask, b);
-  const Span keys = keys_of(P.mask, seq, doc_window(P.mask, t), t);
-  const int n = t >= seq.q_lo && t < seq.q_hi ? keys.hi - keys.lo : 0;
-  if (n <= 0 || n > kFewKeys) return;
-  const int64_t row = ((int64_t)b * P.sq + t) * P.heads + h, kh = h / P.group;
-  const __nv_bfloat16 *k = P.k + b * P.ks[0] + keys.lo * P.ks[1] + kh * P.ks[2] + lane * 8;
-  const __nv_bfloat16 *v = P.v + b * P.vs[0] + keys.lo * P.vs[1] + kh * P.vs[2] + lane * 8;
-  const __nv_bfloat16 *const q_row = P.q + b * P.qs[0] + t * P.qs[1] + h * P.qs[2] + lane * 8;
-  const bool k0 = lane * 8 < P.dk, k1 = lane * 8 + 128 < P.dk, v0 = lane * 8 < P.dv;
-  const uint4 none = make_uint4(0, 0, 0, 0);
-  const uint4 q = k0 ? *reinterpret_cast<const uint4 *>(q_row) : none, r = k1 ? *reinterpret_cast<const uint4 *>(q_row + 128) : none;
-  const uint4 g = v0 ? *reinterpret_cast<const uint4 *>(P.dy + b * P.ds[0] + t * P.ds[1] + h * P.ds[2] + lane * 8) : none;
-  const float lse2 = P.lse[row] * kLog2ePlain;
-  float sum = 0.f;
-#pragma unroll 2
-  for (int i0 = 0; i0 < n; i0 += 2) {
-    const int i = i0 + half;
-    float s = 0.f, dp = 0.f;
-    if (i < n) {
-      if (k0) s = dot8(q, *reinterpret_cast<const uint4 *>(k + i * P.ks[1]), s);
-      if (k1) s = dot8(r, *reinterpret_cast<const uint4 *>(k + i * P.ks[1] + 128), s);
-      if (v0) dp = dot8(g, *reinterpret_cast<const uint4 *>(v + i * P.vs[1]), dp);
+  const DocWindow docs = doc_window(P.mask, first);
+  Span keys[2];
+  int64_t row[2];
+  float lse2[2];
+  bool in[2];
+  uint4 q[2][2 * kKb], dy[2][2 * kVb];
+  int lo = INT32_MAX, hi = 0;  // (of no row: no chunk starts there)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = g + 8 * i, t = first + (r >> P.pack), h = h0 + (r & ((1 << P.pack) - 1));
+    keys[i] = keys_of(P.mask, seq, docs, t);
+    in[i] = mine && t < end && t >= seq.q_lo && t < seq.q_hi && !keys[i].empty() && keys[i].hi - keys[i].lo <= kFewKeys;
+    if (!in[i]) keys[i] = {0, 0};
+    if (in[i]) lo = min(lo, keys[i].lo), hi = max(hi, keys[i].hi);
+    row[i] = ((int64_t)b * P.sq + t) * P.heads + h;
+    lse2[i] = in[i] ? P.lse[row[i]] * kLog2ePlain : 0.f;
+    const __nv_bfloat16 *const q_row = P.q + b * P.qs[0] + t * P.qs[1] + h * P.qs[2];
+    const __nv_bfloat16 *const dy_row = P.dy + b * P.ds[0] + t * P.ds[1] + h * P.ds[2];
+#pragma unroll
+    for (int c = 0; c < 2 * kKb; ++c) {
+      q[i][c] = make_uint4(0, 0, 0, 0);
+      if (in[i] && c * 32 + c0 < P.dk) q[i][c] = *reinterpret_cast<const uint4 *>(q_row + c * 32 + c0);
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      dp += __shfl_xor_sync(0xffffffffu, dp, o);
+    for (int c = 0; c < 2 * kVb; ++c) {
+      dy[i][c] = make_uint4(0, 0, 0, 0);
+      if (in[i] && c * 32 + c0 < P.dv) dy[i][c] = *reinterpret_cast<const uint4 *>(dy_row + c * 32 + c0);
     }
-    if (i < n) sum = fmaf(ex2(fmaf(s, P.scale2, -lse2)), dp, sum);
   }
-  sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-  if ((threadIdx.x & 31) == 0) P.stats[row] = lse2 == -INFINITY ? make_float2(-INFINITY, 0.f) : make_float2(-lse2, sum);
+  lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) range[0][warp] = lo, range[1][warp] = hi;
+  __syncthreads();
+  int from = INT32_MAX, to = 0;
+#pragma unroll
+  for (int w = 0; w < kFewWarps; ++w) from = min(from, range[0][w]), to = max(to, range[1][w]);
+  const __nv_bfloat16 *const k = P.k + b * P.ks[0] + kh * P.ks[2], *const v = P.v + b * P.vs[0] + kh * P.vs[2];
+  const uint32_t ktile = smem_u32(smem), vtile = ktile + C::kVAt;
+  float sum[2] = {0.f, 0.f};
+  for (int j0 = from; j0 < to; j0 += kFewChunk) {
+    // rows of eight elements a thread; behind the last key and a row's last element zeros
+    auto copy = [&](uint32_t tile, int pitch, int pieces, int dim, const __nv_bfloat16 *src, int64_t stride) {
+      for (int i = threadIdx.x; i < kFewChunk * pieces; i += 32 * kFewWarps) {
+        const int j = i / pieces, c = i - j * pieces;
+        const bool here = j0 + j < to && c * 8 < dim;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + j * pitch + c * 16),
+                     "l"(src + (here ? (j0 + j) * stride + c * 8 : 0)), "r"(here ? 16 : 0)
+                     : "memory");
+      }
+    };
+    copy(ktile, C::kKPitch, 8 * kKb, P.dk, k, P.ks[1]);
+    copy(vtile, C::kVPitch, 8 * kVb, P.dv, v, P.vs[1]);
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    for (int m = 0; m < kFewChunk; m += 16) {
+      if (j0 + m >= hi || j0 + m + 16 <= lo) continue;
+      float s[2][4] = {}, dp[2][4] = {};
+      auto eight = [&](uint32_t at) {
+        uint4 x;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+        return x;
+      };
+      const uint32_t kr = ktile + (m + g) * C::kKPitch + c0 * 2, vr = vtile + (m + g) * C::kVPitch + c0 * 2;
+#pragma unroll
+      for (int c = 0; c < 2 * std::max(kKb, kVb); ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // (four chains of products, one beside the other)
+          if (c < 2 * kKb) mma_rows32(s[i], q[0][c], q[1][c], eight(kr + 8 * i * C::kKPitch + c * 64));
+          if (c < 2 * kVb) mma_rows32(dp[i], dy[0][c], dy[1][c], eight(vr + 8 * i * C::kVPitch + c * 64));
+        }
+      // (keys that a row does not see may hold anything)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = j0 + m + 8 * i + (lane & 3) * 2 + (e & 1);
+          if (key >= keys[e >> 1].lo && key < keys[e >> 1].hi)
+            sum[e >> 1] = fmaf(ex2(fmaf(s[i][e], P.scale2, -lse2[e >> 1])), dp[i][e], sum[e >> 1]);
+        }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    if ((lane & 3) == 0 && in[i]) P.stats[row[i]] = lse2[i] == -INFINITY ? make_float2(-INFINITY, 0.f) : make_float2(-lse2[i], sum[i]);
+    if ((lane & 3) == 0 && P.all && !in[i] && mine && first + ((g + 8 * i) >> P.pack) < end)
+      P.stats[row[i]] = make_float2(-INFINITY, 0.f);
+  }
 }
 
 __global__ void __launch_bounds__(256, 5) attn_delta_kernel(const __grid_constant__ DeltaParams P) {
-  pdl_launch();
   pdl_wait();
-  if (blockIdx.x < P.few_ctas) {
-    few_keys_delta(P);
-    return;
-  }
-  const int64_t row0 = (int64_t)(blockIdx.x - P.few_ctas) * kDeltaRows + (threadIdx.x >> 4);
+  const int64_t row0 = (int64_t)blockIdx.x * kDeltaRows + (threadIdx.x >> 4);
   const int lane = threadIdx.x & 15;
   constexpr int kEach = kDeltaRows / 16;
   int b[kEach], t[kEach];
@@ -157,18 +252,13 @@ __global__ void __launch_bounds__(256, 5) attn_delta_kernel(const __grid_constan
   }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    bool few = false;
-    if (P.few_ctas) {
-      const AttnSeq seq = attn_seq(P.mask, b[i]);
-      const Span keys = keys_of(P.mask, seq, doc_window(P.mask, __shfl_sync(0xffffffffu, t[i], 0)), t[i]);
-      few = t[i] >= seq.q_lo && t[i] < seq.q_hi && keys.hi > keys.lo && keys.hi - keys.lo <= kFewKeys;
-    }
     float d = dot8(g[i], y[i], 0.f);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (row0 + 16 * i < P.rows && !few && lane == 0)
+    if (row0 + 16 * i < P.rows && lane == 0)
       P.stats[row0 + 16 * i] = lse[i] == -INFINITY ? make_float2(-INFINITY, 0.f) : make_float2(-lse[i] * kLog2ePlain, d);
   }
+  pdl_launch();
 }
 
 struct BwdParams {
@@ -752,6 +842,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_backward_kernel(const __g
 // ---------------------------------------------------------------------------
 // host
 
+template <int kKb, int kVb>
+cudaError_t launch_few(const DeltaParams &D, int64_t grid, int dev, cudaStream_t st) {
+  static PerDevice<cudaError_t> limit;
+  const cudaError_t *err = limit.of(dev, [](cudaError_t &e) {
+    e = cudaFuncSetAttribute(attn_few_kernel<kKb, kVb>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<kKb, kVb>::kSmem);
+  });
+  if (!err || *err != cudaSuccess) return err ? *err : cudaErrorInvalidDevice;
+  count_launches(1);
+  return launch_kernel_as(pdl_allowed(), attn_few_kernel<kKb, kVb>, dim3((unsigned)grid), dim3(32 * kFewWarps), Few<kKb, kVb>::kSmem,
+                          st, 1, D);
+}
+
 template <int kKb, int kVb, int kQt>
 cudaError_t launch_walks(const BothParams &P, int64_t grid, int dev, cudaStream_t st) {
   constexpr int kSmem = std::max(Dkv<kKb, kVb, kQt>::kSmem, Dq<kKb, kVb>::kSmem);
@@ -819,6 +921,7 @@ extern "C" int gbo_attn_backward(const gbo_attn_args *a, const gbo_attn_grads *g
   Q.mask = M, Q.shape = S, Q.stats = P.stats, Q.status = dev_status;
   DeltaParams D;
   memset(&D, 0, sizeof D);
+  int64_t few_grid = 0;
   bool maps = true;
   if (queries && keys) {
     D.dy = static_cast<const __nv_bfloat16 *>(g->dy), D.y = static_cast<const __nv_bfloat16 *>(g->y);
@@ -835,10 +938,17 @@ extern "C" int gbo_attn_backward(const gbo_attn_args *a, const gbo_attn_grads *g
     D.rows = rows, D.sq = (int32_t)a->sq, D.heads = a->q_heads, D.dk = a->dk, D.dv = a->dv;
     D.by_heads = fast_div(a->q_heads), D.by_sq = fast_div(a->sq);
     D.mask = M, D.scale2 = S.scale2, D.group = S.group;
-    D.every = a->sk <= kFewKeys || (a->window > 0 && a->window <= kFewKeys) || (!a->causal && a->k_lengths);
-    int64_t few = D.every ? a->batch * a->sq : a->documents ? (int64_t)a->n_documents * kFewKeys : a->causal ? a->batch * kFewKeys : 0;
-    if (few * a->q_heads > INT32_MAX) few = 0;  // (D = dy . y throughout)
-    D.places = (int32_t)few, D.few_ctas = (uint32_t)((few * a->q_heads + 7) / 8);
+    // (documents so short that looking at the first tokens of each is looking at more than all)
+    D.all = a->sk <= kFewKeys || (a->window > 0 && a->window <= kFewKeys);
+    D.every = D.all || (!a->causal && a->k_lengths) || (a->documents && (int64_t)a->n_documents * kFewKeys >= a->sq);
+    D.pack = std::min(S.pack, 4);
+    const int64_t units = D.every ? a->batch : a->documents ? a->n_documents : a->causal ? a->batch : 0;
+    const int64_t tokens = 16 >> D.pack, blocks = S.group >> D.pack;
+    const int64_t sets = ((D.every ? a->sq : kFewKeys) + tokens - 1) / tokens * blocks, chunks = (sets + kFewWarps - 1) / kFewWarps;
+    // (where they are more than a launch takes: D = dy . y throughout)
+    few_grid = sets <= INT32_MAX - kFewWarps && units * a->k_heads * chunks <= INT32_MAX ? units * a->k_heads * chunks : 0;
+    D.all = D.all && few_grid;
+    D.sets = (int32_t)sets, D.by_chunks = fast_div(chunks), D.by_k_heads = S.by_k_heads, D.by_blocks = fast_div(blocks);
     maps = heads_map(&P.k, a->k, a->dk, a->k_heads, a->sk, a->batch, a->k_stride, 1, kAttnTile) &&
            heads_map(&P.v, a->v, a->dv, a->k_heads, a->sk, a->batch, a->v_stride, 1, kAttnTile) &&
            heads_map(&P.q, a->q, a->dk, a->q_heads, a->sq, a->batch, a->q_stride, heads, qt >> S.pack) &&
@@ -855,8 +965,13 @@ extern "C" int gbo_attn_backward(const gbo_attn_args *a, const gbo_attn_grads *g
   P.has1 = g->dk != nullptr, P.has2 = g->dv != nullptr;
   Q.tiles = (int32_t)q_tiles;
   if (queries && keys && (dkv_grid || dq_grid)) {
-    count_launches(1);
-    e = launch_kernel_as(pdl_allowed(), attn_delta_kernel, dim3((unsigned)((rows + kDeltaRows - 1) / kDeltaRows + D.few_ctas)), dim3(256), 0, st, 1, D);
+    if (!D.all) {
+      count_launches(1);
+      e = launch_kernel_as(pdl_allowed(), attn_delta_kernel, dim3((unsigned)((rows + kDeltaRows - 1) / kDeltaRows)), dim3(256), 0, st, 1, D);
+    }
+    if (e == cudaSuccess && few_grid)
+      e = cfg == 0 ? launch_few<1, 1>(D, few_grid, dev, st)
+                   : cfg == 1 ? launch_few<2, 2>(D, few_grid, dev, st) : launch_few<3, 2>(D, few_grid, dev, st);
   }
   both.key_tiles = (int32_t)dkv_grid;
   const int64_t grid = dkv_grid + dq_grid;
