@@ -812,19 +812,19 @@ def _workspace(t):
     return _dev_ptr(t, "workspace"), 0 if t is None else t.numel() * t.element_size()
 
 
-_attn_lengths = functools.partial(struct.Struct("@3q").unpack_from, offset=AttnArgs.batch.offset)
-_attn_dims = functools.partial(struct.Struct("@4i").unpack_from, offset=AttnArgs.q_heads.offset)
+_attn_sizes = struct.Struct("@3q%dx4i" % (AttnArgs.q_heads.offset - AttnArgs.sk.offset - 8)).unpack_from
+_ATTN_AT = AttnArgs.batch.offset
 
 
 def _attn_of(args, q, k, v):
     """Shapes of q, k (not looked at if None) and v, from ``args``; refuses tensors of others, because
     outputs are checked against the ones and written by the others."""
-    b, sq, sk = _attn_lengths(args)
-    hq, hk, dk, dv = _attn_dims(args)
-    shapes = (b, sq, hq, dk), (b, sk, hk, dk), (b, sk, hk, dv)
-    for what, t, shape in zip("qkv", (q, k, v), shapes):
-        if t is not None and t.shape != shape:
-            raise ValueError("args are of %s %s, not of %s" % (what, shape, tuple(t.shape)))
+    b, sq, sk, hq, hk, dk, dv = _attn_sizes(args, _ATTN_AT)
+    shapes = qs, ks, vs = (b, sq, hq, dk), (b, sk, hk, dk), (b, sk, hk, dv)
+    if q.shape != qs or v.shape != vs or (k is not None and k.shape != ks):
+        for what, t, shape in zip("qkv", (q, k, v), shapes):
+            if t is not None and t.shape != shape:
+                raise ValueError("args are of %s %s, not of %s" % (what, shape, tuple(t.shape)))
     return shapes
 
 
@@ -922,16 +922,15 @@ def _rows_or_null(t, what, shape, dtype):
     return t.data_ptr(), _rows_of(t, what, shape)
 
 
-_residual_sizes = functools.partial(struct.Struct("@2q").unpack_from, offset=ResidualArgs.n.offset)
-_residual_modes = functools.partial(struct.Struct("@8i").unpack_from, offset=ResidualArgs.x_dtype.offset)
+_residual_sizes = struct.Struct("@2q%dx8i" % (ResidualArgs.x_dtype.offset - ResidualArgs.d.offset - 8)).unpack_from
+_RESIDUAL_AT = ResidualArgs.n.offset
 
 
 def _residual_of(args, shape, x_dtype, block_dtype):
     """Shapes that ``args`` asks of dgate, and values of dscale; refuses other sizes and types than
     theirs, because outputs are checked against the ones and written by the others."""
-    n, d = _residual_sizes(args)
-    xt, bt, _, _, _, gate, _, scale = _residual_modes(args)
-    if tuple(shape) != (n, d) or _ELEMENT.get(x_dtype) != xt or _ELEMENT.get(block_dtype) != bt:
+    n, d, xt, bt, _, _, _, gate, _, scale = _residual_sizes(args, _RESIDUAL_AT)
+    if shape != (n, d) or _ELEMENT.get(x_dtype) != xt or _ELEMENT.get(block_dtype) != bt:
         raise ValueError("args are of %s rows, and of other types or sizes than %s in %s and %s" %
                          ((n, d), tuple(shape), x_dtype, block_dtype))
     return (n, 1 if gate == GBO_GATE_ROW else d), 1 if scale == GBO_SCALE_ONE else d

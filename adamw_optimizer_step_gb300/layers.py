@@ -286,7 +286,8 @@ def dropout(x, p, seed, *, offset=0, out=None):
     of a two-dimensional ``x`` may lie apart; other strides are copied together first."""
     flat = x.dim() == 2
     rows = x if flat else x.reshape(1, -1)  # (a view where it can be, with any stride)
-    if (rows.stride(1) != 1 and rows.shape[1] > 1) or (rows.stride(0) < rows.shape[1] and rows.shape[0] > 1):
+    (n, d), (by, apart) = rows.shape, rows.stride()
+    if (apart != 1 and d > 1) or (by < d and n > 1):
         rows = rows.contiguous()
     if flat:
         y = _like(rows) if out is None else out
