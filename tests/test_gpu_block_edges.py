@@ -81,3 +81,64 @@ def test_a_callers_context_stays_current():
     t.join()
     assert seen == [0, 0, 0, 0, True, 0]
     assert torch.equal(layers.dropout(torch.ones(8, device="cuda"), 0.0, 1), torch.ones(8, device="cuda"))
+
+
+def test_a_training_pass_captured():
+    """Both passes of a block in autograd, captured into a graph with the seed on the device: replays have
+    the bits of the eager pass, on the values and with the seed that they find."""
+    gen = torch.Generator().manual_seed(3)
+    made = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    b, s, hq, hk, d = 2, 150, 4, 2, 64
+    x, block, qkv = (made(b, s, hq * d).to(BF16).cuda(), made(b, s, hq * d).to(BF16).cuda(),
+                     made(b, s, hq + 2 * hk, d).to(BF16).cuda())
+    gain = (1 + 0.3 * made(hq * d)).cuda()
+    leaves = [t.requires_grad_() for t in (x, block, qkv, gain)]
+    seed, lengths = torch.tensor([5], device="cuda"), torch.tensor([150, 90], dtype=torch.int32, device="cuda")
+
+    def both():
+        y = layers.attention_autograd(*qkv.split((hq, hk, hk), dim=2), q_lengths=lengths, k_lengths=lengths)
+        z, h = layers.residual_norm_autograd(x, block + y.flatten(2), post_norm=True, post_gain=gain, pre_gain=gain, dropout=0.25, seed=seed)
+        out = layers.dropout_autograd(h, 0.5, seed, offset=1)
+        return (out, *torch.autograd.grad((z.float() + out.float().square()).sum(), leaves))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        first = [t.clone() for t in both()]
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, w) for a, w in zip(got, first))
+    with torch.no_grad():
+        seed += 1
+        qkv.copy_(qkv.flip(1))
+        lengths.copy_(lengths.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    replayed = [t.clone() for t in got]
+    assert all(torch.equal(a, w) for a, w in zip(replayed, both())) and not torch.equal(replayed[0], first[0])
+
+
+def test_two_residual_calls_at_once():
+    """Two streams at the same time, each with partial sums of its own: the bits of the calls alone."""
+    cases = [Case(3000, d, gate="element", seed=d) for d in (72, 1024)]
+    alone = []
+    for c in cases:
+        x, h = layers.residual_norm(c.x, c.block, **c.kw())
+        alone.append((x, h, layers.residual_norm_backward(c.dx_out, c.dh, x, c.block, **c.kw())))
+    streams = [torch.cuda.Stream() for _ in cases]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for n, (c, st) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(st):
+                x, h = layers.residual_norm(c.x, c.block, **c.kw())
+                got[n].append((x, h, layers.residual_norm_backward(c.dx_out, c.dh, x, c.block, **c.kw())))
+    torch.cuda.synchronize()
+    for n, (x, h, g) in enumerate(alone):
+        for x1, h1, g1 in got[n]:
+            assert torch.equal(x1, x) and torch.equal(h1, h) and all(torch.equal(g1[k], g[k]) for k in g)
