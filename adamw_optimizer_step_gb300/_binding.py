@@ -884,8 +884,9 @@ def _seed_of(seed):
 def residual_args(x, block, *, post_norm=False, pre_norm=True, post_gain=None, pre_gain=None, gate=None,
                   gate_kind="sigmoid", scale=None, dropout=0.0, seed=0, offset=0, eps=1e-6, block_dtype=None):
     """The packed arguments of the residual calls (``gbo_residual_args``): ``x``
-    (the updated stream, backward; None there without ``pre_norm``), ``block`` (or
-    None) and ``gate`` two-dimensional, gains and scale float32."""
+    (backward: the updated stream, or any tensor of its rows and type without
+    ``pre_norm``), ``block`` (or None) and ``gate`` two-dimensional, gains and scale
+    float32."""
     if gate_kind not in ("sigmoid", "linear"):
         raise ValueError("gate_kind must be sigmoid or linear")
     n, d = x.shape

@@ -16,12 +16,15 @@
 // 2.4e-3 of them against 1.7e-3 of the outputs' rounding alone; dS as two bf16 numbers
 // would take two products more.
 //
-// Measured, causal, 2 x 8192 tokens, 16 query and 4 key heads of 128: 1110 us, the
-// keys' walk alone 670 (1.64 PFLOP/s of the four products it forms), the queries'
-// alone 490 with the delta kernel (1.69 of three): 86% of a library product's rate.
+// Measured, causal, 2 x 8192 tokens, 16 query and 4 key heads of 128: 1104 us at best, 1190
+// over a second of calls (the power limit holds the clock at 1.78 GHz); the keys' walk alone
+// 676 and 717 (1.63 and 1.53 PFLOP/s of the four products it forms), the queries' alone 493
+// and 526 (1.67 and 1.57 of three), delta and few kernels with each: 86 and 91% of a library
+// product's burst and sustained rates.  Heads of 192 and 128: 1863 us, 1.33 PFLOP/s of all
+// seven at 1.95 GHz.
 // Bound: tensor cores (active 72% at 4096 tokens, where the tail counts), then the
-// elementwise warps between S and dS.  13 documents in 8192 tokens 139 us, 6 x 777
-// tokens of 32 heads of 192 and 128 187 us: a CTA's start and end (9000 clocks).
+// elementwise warps between S and dS.  13 documents in 8192 tokens 141 us, 6 x 777
+// tokens of 32 heads of 192 and 128 180 us: a CTA's start and end (9000 clocks).
 // Resident CTAs with several tiles each, the next one looked up ahead: 488 us in place
 // of 493 for the queries' walk, but 93 in place of 83 for the documents, whose tiles
 // are uneven.  Not kept.
@@ -103,9 +106,10 @@ struct Few {
 
 // Rows that see few keys.  A warp takes 16 rows of a key head, heads of a token side by
 // side, held in registers; the CTA's warps go over the keys that any of their rows sees,
-// a chunk in shared memory at a time.  Bound by the wait for rows and keys where the first
-// tokens alone are looked at (5 us of a call), by mma.sync where all are (a window of 64
-// over 2 x 8192 tokens of 16 heads: 60 us).  Fragments straight from global memory: 103.
+// a chunk in shared memory at a time.  Bound by the wait for rows and keys, at 16 warps an
+// SM: some 5 us of a call where the first tokens alone are looked at; a window of 64 over
+// 2 x 8192 tokens of 16 heads 60 us (issue slots 35%), 103 with fragments straight from
+// global memory.
 template <int kKb, int kVb>
 __global__ void __launch_bounds__(32 * kFewWarps, 4) attn_few_kernel(const __grid_constant__ DeltaParams P) {
   pdl_launch();

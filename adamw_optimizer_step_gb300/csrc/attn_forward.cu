@@ -19,13 +19,15 @@
 // maximum grows by more than 2^8: until then P is at most 2^8 and its rounding
 // is relative, so nothing is lost; sums are fp32.  P is rounded to bf16 once
 // (2^-8 of it at most, as the operand of the product); the sum takes it unrounded.
-// Measured, causal, 16 query and 4 key heads of 128: 2 x 8192 tokens 339 us, 1.62
-// PFLOP/s of the products that count (85% of a library product's rate); 512 new tokens
-// over a cache of 32768 (keys split, parts joined) 107 us, 1.28.  Bound: the turn of the two row
-// tiles, S to softmax to P V; the warps issue 39% of the time, mostly waiting for
-// products.  Short sequences (documents, 777 tokens) are bound by a CTA's start and
-// end, some 9000 clocks: 65 us at 2.4 to 3.7 TB/s.  A CTA that walks over several
-// tiles instead (one launch of resident CTAs) lost at every length.
+// Measured, causal, 16 query and 4 key heads of 128: 2 x 8192 tokens 330 us at best, 356 over
+// a second of calls (the power limit holds the clock at 1.88 GHz), 1.67 and 1.55 PFLOP/s of the
+// products that count: 87% of a library product's burst, 91% of its sustained rate.  Heads of
+// 192 and 128, V's ring of one stage: 540 us, 1.27 PFLOP/s at 2.0 GHz.  512 new tokens over a
+// cache of 32768 (keys split, parts joined) 103 us, 1.33; four equal parts are 128 CTAs on
+// 152 SMs.  Bound: the turn of the two row tiles, S to softmax to P V; the warps issue 39% of
+// the time, mostly waiting for products.  Short sequences (documents, 777 tokens) are bound by
+// a CTA's start and end, some 9000 clocks: 57 us at 1.5 to 2.0 TB/s.  A CTA that walks over
+// several tiles instead (one launch of resident CTAs) lost at every length.
 #include "attn_common.cuh"
 
 namespace gbo {
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_forward_kernel(const __gr
 // takes 16 of the keys, with a running maximum, sum and output of its own, and
 // the four are joined at the end.  Two CTAs an SM, so that one's start and end
 // lie beside the other's stream.  Eight sequences' caches of 32768 to 65536 tokens, 4 key
-// heads of 128: 134 us, 6.0 TB/s (89% of a copy's rate).
+// heads of 128: 133 us, 6.1 TB/s (89% of a copy's rate).
 constexpr int kTokKeys = 64, kTokWarps = 4;
 constexpr int kTokThreads = (kTokWarps + 1) * 32;
 constexpr int kTokBlock = kTokKeys * 128;  // bytes of 64 rows of 64 elements
@@ -796,7 +798,8 @@ FwdPlan plan_forward(const gbo_attn_args *a, const AttnShape &S, int sm) {
   int64_t seen = a->window > 0 ? std::min<int64_t>(tiles, a->window / (p.token ? kTokKeys : kAttnTile) + 2) : tiles;
   if (a->documents) seen = std::min<int64_t>(seen, tiles / a->n_documents + 1);
   // The split that ends first, in microseconds: a step of a CTA takes 1.4 (128 keys
-  // for two row tiles; 64 keys of a cache, two CTAs an SM), its start and end as
+  // for two row tiles; 64 keys of a cache, two CTAs an SM; both of heads of 128 elements,
+  // and taken for narrower and wider ones too), its start and end as
   // much as `fixed` steps, and the parts are written and read once, 4 bytes an
   // element, with a launch of 5.  Without the parts' bytes in the account, 8192 tokens
   // of 13 documents were split in two: 183 us instead of 68.

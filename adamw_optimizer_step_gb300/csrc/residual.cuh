@@ -23,9 +23,9 @@
 // for all (a group of threads that loads straight into registers, the row in
 // registers between its sums), us of the gradients and of the forward pass:
 //   32768 x 2048, gate and dropout    556 -> 231     (no gate or dropout) 84
-//   65600 x 1023, the same           2748 -> 752     903 -> 398
-//   8192 x 8192 (wide), the same     1652 -> 705     (ring) 163 -> 141
-//   4096 x 16384 (wide), the same    1020 -> 608     244 -> 198
+//   65600 x 1023, the same           2748 -> 764     903 -> 395
+//   8192 x 8192 (wide), the same     1652 -> 703     (ring) 163 -> 140
+//   4096 x 16384 (wide), the same    1020 -> 612     244 -> 198
 // The sums over rows stay with the thread that has the columns (registers; wide: shared
 // memory), one partial row a group is left at the end, and a second kernel adds them in
 // a fixed order.
@@ -604,7 +604,7 @@ constexpr int kSmemMost = 220 * 1024;  // of an SM's shared memory, for rings an
 // to half as many in the forward pass (what a row costs beside its elements is half
 // as much then); 512 threads an SM.  Gradients of single elements, two chunks a thread,
 // spill (8194 x 8190: 1303 us, the wide form 651): those rows take the wide form, shorter
-// ones the ring (65600 x 1023: 752 us, wide 2544).
+// ones the ring (65600 x 1023: 764 us, wide 2544).
 // `row_bytes`: of a row's inputs, in their places (0 where there are no rows: their
 // pointers may be NULL).
 ResCut cut_of(int64_t n, int64_t d, int sm, bool back, bool vec, int64_t row_bytes) {

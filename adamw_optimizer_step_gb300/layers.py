@@ -14,7 +14,9 @@ a label outside the vocabulary leaves its row out and a wait that ran out
 ``qk_norm_rotary_autograd``, ``attention_autograd``, ``residual_norm_autograd``,
 ``dropout_autograd`` and ``linear_cross_entropy_loss`` are the same operators inside
 autograd, so that ``loss.backward()`` leaves the gradients that
-:class:`~.routing.HybridOptimizer` steps.
+:class:`~.routing.HybridOptimizer` steps.  A captured backward pass must find no graph of an
+eager one alive that accumulates into the same leaves (torch would leave the capture for
+that one's stream).
 
 Heads are (batch, seq, heads, dim) tensors whose last axis is contiguous; any
 other strides are taken as they are (slices of a fused projection, or a
