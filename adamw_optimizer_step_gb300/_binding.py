@@ -858,7 +858,7 @@ def gbo_attn_backward(args, q, k, v, dy, y, lse, workspace, *, dq=None, dk=None,
             raise ValueError("%s must be a CUDA tensor" % what)
         ptrs.append(t.data_ptr())
     _here(dy, y, lse, dq, dk, dv, workspace, dev_status)
-    grads = _PACK_ATTN_GRADS(ptrs[0], ptrs[1], _out_f32(lse, b * sq * hq, "lse"), *ptrs[2:], *strides)
+    grads = _PACK_ATTN_GRADS(ptrs[0], ptrs[1], _out_f32(lse, b * sq * hq, "lse") or 0, *ptrs[2:], *strides)
     ws, nbytes = _workspace(workspace)
     _check(lib().gbo_attn_backward(args, grads, ws, nbytes, _dev_ptr(dev_status, "dev_status"), _stream(stream)))
 

@@ -142,3 +142,12 @@ def test_two_residual_calls_at_once():
     for n, (x, h, g) in enumerate(alone):
         for x1, h1, g1 in got[n]:
             assert torch.equal(x1, x) and torch.equal(h1, h) and all(torch.equal(g1[k], g[k]) for k in g)
+
+
+def test_what_the_gradients_need_is_asked_for():
+    """Without the forward's lse, its output or the gradient of that: the library's refusal."""
+    q = torch.zeros(1, 4, 2, 64, dtype=BF16, device="cuda")
+    y, lse = layers.attention(q, q, q, return_lse=True)
+    for dy, out, sums, what in ((y, y, None, "lse"), (None, y, lse, "NULL"), (y, None, lse, "NULL")):
+        with pytest.raises(B.GboError, match=what):
+            layers.attention_backward(dy, q, q, q, out, sums)
