@@ -543,6 +543,8 @@ typedef struct {
  *   dq_i = sum_j ds_ij k_j,  dk_j = sum_i ds_ij q_i,
  * the sums over i over all query heads that read key head j's.  p is formed
  * again from lse; no sum crosses thread blocks, so results repeat bit for bit.
+ * dy_i y_i is of y as it was rounded, but for queries that see 64 keys or
+ * fewer, which take sum_j p_ij dy_i v_j.
  */
 int gbo_attn_backward(const gbo_attn_args *args, const gbo_attn_grads *grads, void *workspace, size_t ws_bytes,
                       int32_t *dev_status, gbo_stream_t stream);
